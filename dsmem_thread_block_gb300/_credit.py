@@ -68,6 +68,12 @@ class Candidate(ctypes.Structure):
                 ("tail_staged_elems", ctypes.c_int64)]
 
 
+class DropoutFields(ctypes.Structure):
+    """Mirror of credit_dropout_t."""
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("device_offset", ctypes.c_void_p)]
+
+
 class DeviceKey(ctypes.Structure):
     """Mirror of credit_device_key_t."""
     _fields_ = [("gpu_name", ctypes.c_char * 96), ("sms", ctypes.c_int32),
@@ -131,6 +137,15 @@ SIGNATURES = {
                                    ctypes.POINTER(Plan), _vp, _sz, _vp]),
     "credit_pearson": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i32, _f32, ctypes.POINTER(Plan),
                               _vp, _sz, _vp]),
+    "credit_dropout": (_i32, [_vp, _vp, _vp, _i64, _i64, _i32, ctypes.POINTER(DropoutFields),
+                              _vp]),
+    "credit_norm_workspace": (_i32, [_i32, _i32, _i64, _i64, _i32, _i32,
+                                     ctypes.POINTER(ctypes.c_size_t)]),
+    "credit_norm_forward": (_i32, [_i32, _vp, _vp, ctypes.POINTER(DropoutFields), _vp, _vp, _vp,
+                                   _vp, _i64, _i64, _i32, _vp, _vp, _i32, _f32, _vp, _sz, _vp]),
+    "credit_norm_backward": (_i32, [_i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32,
+                                    ctypes.POINTER(DropoutFields), _vp, _vp, _vp, _vp, _i64, _i64,
+                                    _i32, _vp, _sz, _vp]),
     "credit_two_pass_noalloc": (_i32, [_i32, _vp, _vp, _i64, _i64, _i32, _vp, _vp, _i32, _f32,
                                        _vp]),
     "credit_bench_dsmem": (_i32, [_i32, _i32, _i32, _i32, _i32, ctypes.POINTER(BenchResult)]),
@@ -312,6 +327,49 @@ def credit_pearson(x: int, u: int, y: int, r: int, rows: int, cols: int, dtype: 
     return load().credit_pearson(x or None, u or None, y or None, r or None, rows, cols, dtype,
                                  eps, _plan_ptr(plan), workspace or None, workspace_bytes,
                                  stream or None)
+
+
+def dropout_fields(p: float, seed: int = 0, offset: int = 0, device_offset: int = 0):
+    return DropoutFields(p=p, seed=seed, offset=offset, device_offset=device_offset or None)
+
+
+def _drop_ptr(drop):
+    return None if drop is None else ctypes.byref(drop)
+
+
+def credit_dropout(x: int, residual: int, y: int, rows: int, cols: int, dtype: int, drop=None,
+                   stream: int = 0) -> int:
+    return load().credit_dropout(x or None, residual or None, y or None, rows, cols, dtype,
+                                 _drop_ptr(drop), stream or None)
+
+
+def credit_norm_workspace(op: int, backward: bool, rows: int, cols: int, dtype: int,
+                          device: int = 0) -> int:
+    n = ctypes.c_size_t()
+    _check(load().credit_norm_workspace(op, int(backward), rows, cols, dtype, device,
+                                        ctypes.byref(n)), "credit_norm_workspace")
+    return n.value
+
+
+def credit_norm_forward(op: int, x: int, residual: int, drop, y: int, h: int, mean: int, rstd: int,
+                        rows: int, cols: int, dtype: int, gamma: int, beta: int, param_dtype: int,
+                        eps: float, workspace: int = 0, workspace_bytes: int = 0,
+                        stream: int = 0) -> int:
+    return load().credit_norm_forward(op, x or None, residual or None, _drop_ptr(drop), y or None,
+                                      h or None, mean or None, rstd or None, rows, cols, dtype,
+                                      gamma or None, beta or None, param_dtype, eps,
+                                      workspace or None, workspace_bytes, stream or None)
+
+
+def credit_norm_backward(op: int, dy: int, dh: int, h: int, mean: int, rstd: int, gamma: int,
+                         param_dtype: int, drop, dx: int, dresidual: int, dgamma: int, dbeta: int,
+                         rows: int, cols: int, dtype: int, workspace: int = 0,
+                         workspace_bytes: int = 0, stream: int = 0) -> int:
+    return load().credit_norm_backward(op, dy or None, dh or None, h or None, mean or None,
+                                       rstd or None, gamma or None, param_dtype, _drop_ptr(drop),
+                                       dx or None, dresidual or None, dgamma or None,
+                                       dbeta or None, rows, cols, dtype, workspace or None,
+                                       workspace_bytes, stream or None)
 
 
 def credit_two_pass_noalloc(op: int, x: int, y: int, rows: int, cols: int, dtype: int,

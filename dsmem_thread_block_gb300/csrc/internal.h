@@ -103,6 +103,76 @@ struct WarpRowsArgs {
 constexpr int kWarpRowNV = 8;          // 16-byte vectors per lane: rows up to 4 KiB
 constexpr int kWarpRowThreads = 256;
 
+// ------------------------------------------------- the training operators
+// A dropout stream (train.cuh): off when `on` is 0.
+struct DropArgs {
+    int32_t on;
+    uint32_t threshold;               // keep where the random word >= threshold
+    uint32_t k0, k1;                  // the seed
+    uint64_t offset;
+    const uint64_t* device_offset;    // added to offset when the kernel runs (or null)
+    float scale;                      // 1 / (1 - p)
+};
+
+struct DropoutArgs {
+    const void* x;
+    const void* residual;  // or null
+    void* y;
+    int64_t rows;
+    int64_t cols;
+    DropArgs drop;
+};
+
+struct NormFwdArgs {
+    const void* x;
+    const void* residual;  // or null
+    void* y;
+    void* h;               // or null
+    float* mean;           // or null
+    float* rstd;           // or null
+    const void* gamma;     // or null
+    const void* beta;      // or null
+    int64_t rows;
+    int64_t cols;
+    float eps;
+    DropArgs drop;
+    float* ws;             // per (row, chunk): count, mean, M2 (RMSNorm: 0, 0, sum of squares)
+    int32_t nch;           // chunks per row
+};
+
+struct NormBwdArgs {
+    const void* dy;
+    const void* dh;        // or null
+    const void* h;
+    const float* mean;     // null for RMSNorm
+    const float* rstd;
+    const void* gamma;     // or null
+    void* dx;
+    void* dres;            // or null
+    void* dgamma;          // or null
+    void* dbeta;           // or null
+    int64_t rows;
+    int64_t cols;
+    DropArgs drop;
+    float* ws;             // per (row, chunk): the sums of dy gamma xh and dy gamma
+    float* pws;            // per row group: dgamma [cols], then dbeta [cols]
+    int32_t nch;           // chunks per row
+    int32_t groups;        // row groups of the parameter sums
+    int64_t group_rows;    // rows of one group
+};
+
+// Kernel selector of the training operators (types as in KernelKey).
+struct TrainKey {
+    int op, dtype, pdtype;
+    bool vec;
+};
+
+int train_chunks(int dtype, int64_t cols);
+int train_groups(int dtype, int64_t rows, int64_t cols, int sms, int64_t* group_rows);
+cudaError_t launch_dropout(int dtype, bool vec, const DropoutArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_norm_fwd(TrainKey k, const NormFwdArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_norm_bwd(TrainKey k, const NormBwdArgs& a, int sms, cudaStream_t s);
+
 // Kernel selector: op 0..2, dtype 0 = fp32 / 1 = bf16, pdtype likewise,
 // vec = aligned 16-byte path, rows = rows per cluster (1, 2 or 4; the
 // element path has 1).

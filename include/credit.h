@@ -266,6 +266,110 @@ credit_status_t credit_rmsnorm(const void *x, void *y, int64_t rows,
                                void *stream);
 
 /*
+ * ---- Training operators: a block's residual step and its gradient ----
+ *
+ *     h = residual + dropout(x),   y = norm(h)      norm: LayerNorm or RMSNorm
+ *
+ * forward, backward (with the parameters' gradients) and dropout alone.
+ * Matrices are rows x cols of one `dtype` as above; unlike the operators
+ * above, rows == 0 is a legal empty batch.  Arithmetic, row sums and the sums
+ * over rows are fp32; every output is rounded once.  Results repeat bit for
+ * bit: every sum has a fixed order.  Each call works entirely on `stream`
+ * and may be captured; a workspace is used by one call at a time (two
+ * captured graphs that may run side by side need one each).
+ */
+
+/*
+ * Dropout with a mask that is never stored.  Element (r, c) of a call draws
+ * word c % 4 of Philox4x32-10 (Salmon et al., SC 2011) with counter
+ * (c / 4, r, offset low 32 bits, offset high 32 bits) and key `seed` (low,
+ * high), and is kept, scaled by 1 / (1 - p), when that word is at least
+ * floor(p 2^32); a dropped element is 0 whatever x holds there (NaN and
+ * infinity included).  The backward pass passes the forward pass's fields.
+ *   p              0 <= p < 1; 0 keeps everything
+ *   device_offset  NULL, or an 8-byte aligned device word added to `offset`
+ *                  (modulo 2^64) when the kernel runs: a captured graph draws
+ *                  a new mask at each replay when the word has moved on
+ * Calls that must not share a mask differ in seed or offset.  rows <= 2^32
+ * and cols <= 2^34 where p > 0.
+ */
+typedef struct {
+    double p;
+    uint64_t seed;
+    uint64_t offset;
+    const uint64_t *device_offset;
+} credit_dropout_t;
+
+/*
+ * y = residual + dropout(x).  residual may be NULL; drop may be NULL (no
+ * dropout).  y may equal x or residual; other overlap is rejected.  On the
+ * incoming gradient (residual NULL) the call is its own backward pass.
+ */
+credit_status_t credit_dropout(const void *x, const void *residual, void *y,
+                               int64_t rows, int64_t cols, credit_dtype_t dtype,
+                               const credit_dropout_t *drop, void *stream);
+
+/*
+ * Device workspace a credit_norm_forward (backward = 0) or
+ * credit_norm_backward (backward = 1) call of this shape needs, in bytes (may
+ * be 0).  Host only.  op is CREDIT_LAYERNORM or CREDIT_RMSNORM.
+ */
+credit_status_t credit_norm_workspace(credit_op_t op, int backward, int64_t rows,
+                                      int64_t cols, credit_dtype_t dtype, int device,
+                                      size_t *bytes);
+
+/*
+ * Forward: h = residual + dropout(x), y = norm(h) as credit_layernorm /
+ * credit_rmsnorm define it.  The statistics and y come from h before it is
+ * rounded to `dtype`.
+ *   residual, drop   NULL: none
+ *   h                rows x cols out, or NULL (not wanted; without residual
+ *                    and dropout h is x)
+ *   mean, rstd       fp32, one per row, out: the row mean (NULL for RMSNorm)
+ *                    and 1 / sqrt(variance or mean square + eps); NULL: not
+ *                    wanted
+ *   gamma, beta      device vectors of cols elements of param_dtype, or NULL
+ *                    (1 and 0); beta is NULL for RMSNorm
+ *   workspace        16-byte aligned, credit_norm_workspace bytes
+ * y and h may each equal x or residual (not one another); other overlap is
+ * rejected.
+ */
+credit_status_t credit_norm_forward(credit_op_t op, const void *x, const void *residual,
+                                    const credit_dropout_t *drop, void *y, void *h,
+                                    float *mean, float *rstd, int64_t rows, int64_t cols,
+                                    credit_dtype_t dtype, const void *gamma,
+                                    const void *beta, credit_dtype_t param_dtype,
+                                    float eps, void *workspace, size_t workspace_bytes,
+                                    void *stream);
+
+/*
+ * Backward of credit_norm_forward: with xh = (h - mean) rstd and w = dy gamma
+ * (RMSNorm: mean = 0),
+ *     dtot   = rstd (w - mean_j(w) - xh mean_j(w xh)) + dh
+ *              (RMSNorm: without mean_j(w))
+ *     dresidual = dtot,    dx = dtot through the same dropout,
+ *     dgamma = sum_r dy xh,    dbeta = sum_r dy.
+ *   dh               NULL, or the gradient that reaches h past the norm
+ *   h, mean, rstd    of the forward pass (mean NULL for RMSNorm)
+ *   drop             the forward pass's fields, or NULL
+ *   dx               rows x cols out
+ *   dresidual        rows x cols out, or NULL (without dropout it equals dx)
+ *   dgamma, dbeta    cols elements of param_dtype, out; NULL: not wanted;
+ *                    dbeta is NULL for RMSNorm; zeros for an empty batch
+ *   workspace        16-byte aligned, credit_norm_workspace bytes
+ * dx and dresidual may each equal dy, dh or h (not one another); other
+ * overlap is rejected.
+ */
+credit_status_t credit_norm_backward(credit_op_t op, const void *dy, const void *dh,
+                                     const void *h, const float *mean, const float *rstd,
+                                     const void *gamma, credit_dtype_t param_dtype,
+                                     const credit_dropout_t *drop, void *dx,
+                                     void *dresidual, void *dgamma, void *dbeta,
+                                     int64_t rows, int64_t cols, credit_dtype_t dtype,
+                                     void *workspace, size_t workspace_bytes,
+                                     void *stream);
+
+/*
  * Two-pass call that needs no workspace and allocates no device memory.
  * The CREDIT paper has no counterpart to this entry point; it exists for
  * callers that cannot allocate: programs that gave all device memory to their
