@@ -108,7 +108,7 @@ constexpr int kWarpRowThreads = 256;
 struct DropArgs {
     int32_t on;
     uint32_t threshold;               // keep where the random word >= threshold
-    uint32_t k0, k1;                  // the seed
+    uint32_t key[20];                 // the generator's round keys, from the seed
     uint64_t offset;
     const uint64_t* device_offset;    // added to offset when the kernel runs (or null)
     float scale;                      // 1 / (1 - p)
@@ -133,7 +133,9 @@ struct NormFwdArgs {
     const void* gamma;     // or null
     const void* beta;      // or null
     int64_t rows;
-    int64_t cols;
+    int32_t cols;
+    float inv_cols;        // 1 / cols
+    bool half;             // gamma, beta are bf16
     float eps;
     DropArgs drop;
     float* ws;             // per (row, chunk): count, mean, M2 (RMSNorm: 0, 0, sum of squares)
@@ -152,10 +154,13 @@ struct NormBwdArgs {
     void* dgamma;          // or null
     void* dbeta;           // or null
     int64_t rows;
-    int64_t cols;
+    int32_t cols;
+    float inv_cols;        // 1 / cols
+    bool half;             // gamma and the parameters' gradients are bf16
     DropArgs drop;
     float* ws;             // per (row, chunk): the sums of dy gamma xh and dy gamma
-    float* pws;            // per row group: dgamma [cols], then dbeta [cols]
+    float* pws;            // per row group: dgamma [pitch], then dbeta [pitch]
+    int32_t pitch;         // cols rounded up to whole tiles
     int32_t nch;           // chunks per row
     int32_t groups;        // row groups of the parameter sums
     int64_t group_rows;    // rows of one group
@@ -163,15 +168,25 @@ struct NormBwdArgs {
 
 // Kernel selector of the training operators (types as in KernelKey).
 struct TrainKey {
-    int op, dtype, pdtype;
+    int op, dtype;
     bool vec;
 };
 
-int train_chunks(int dtype, int64_t cols);
-int train_groups(int dtype, int64_t rows, int64_t cols, int sms, int64_t* group_rows);
+// Workspace of a backward call: `partials` bytes of row sums, then
+// room_groups groups' sums; groups and group_rows are the general form's (and
+// the one-warp form's groups).
+struct TrainLayout {
+    int64_t partials;
+    int32_t nch, groups, room_groups, pitch;
+    int64_t group_rows;
+};
+
+int train_chunks(int64_t cols);
+int64_t norm_fwd_partials(int dtype, int64_t rows, int64_t cols, int sms);  // bytes
+TrainLayout norm_bwd_layout(int dtype, int64_t rows, int64_t cols, int sms);
 cudaError_t launch_dropout(int dtype, bool vec, const DropoutArgs& a, int sms, cudaStream_t s);
 cudaError_t launch_norm_fwd(TrainKey k, const NormFwdArgs& a, int sms, cudaStream_t s);
-cudaError_t launch_norm_bwd(TrainKey k, const NormBwdArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_norm_bwd(TrainKey k, NormBwdArgs a, int sms, cudaStream_t s);
 
 // Kernel selector: op 0..2, dtype 0 = fp32 / 1 = bf16, pdtype likewise,
 // vec = aligned 16-byte path, rows = rows per cluster (1, 2 or 4; the

@@ -4,11 +4,20 @@
 //   dres   = dtot,   dx = keep ? dtot / (1 - p) : 0
 //   dgamma = sum_rows dy xh,   dbeta = sum_rows dy
 //
-// General form, rows of any width: one kernel writes the two row sums per
-// row and chunk, the next owns a strip of columns of a group of rows, writes
-// dx and sums the parameters' gradients over the group in registers, the last
-// adds the groups.  Every sum has a fixed order: results repeat bit for bit.
-#include "train.cuh"
+// Three forms, chosen by the row's width alone, as the forward pass's:
+//   bwd_warp   one warp per row
+//   bwd_ring   a CTA, or a cluster, per row; the next rows' dy, h and dh
+//              arrive in a ring of shared-memory stages
+//   bwd_stats, bwd_apply   wider rows: the two row sums per chunk, then a
+//              second read by CTAs that own a strip of columns
+// In each a thread keeps the same columns for all its rows and sums their
+// dgamma and dbeta in registers; the row groups' sums go to the workspace and
+// bwd_params adds them.  Every sum has a fixed order: results repeat bit for
+// bit.
+#include <algorithm>
+
+#include "planner.h"
+#include "ring.cuh"
 
 namespace credit {
 
@@ -20,40 +29,331 @@ constexpr int kTilesPerWarp = 4;
 constexpr int kChunkTiles = kWarps * kTilesPerWarp;
 constexpr int kRowBlock = 32;  // rows whose sums a CTA merges at a time
 
+struct RowStats { float mean, rstd; };
+
+template <int OP>
+__device__ __forceinline__ RowStats row_stats(const NormBwdArgs& a, int64_t row) {
+    RowStats r{0.f, 0.f};
+    if (row < a.rows) {
+        if constexpr (OP == kLayerNorm) r.mean = a.mean[row];
+        r.rstd = a.rstd[row];
+    }
+    return r;
+}
+
+// Sums of a tile: s1 += w xh, s2 += w; and the columns' gradients.
+template <int OP, int NP>
+__device__ __forceinline__ void tile_sums(const F2* dy, const F2* h, const F2* g, RowStats r,
+                                          F2& s1, F2& s2, F2* ag, F2* ab) {
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+        const F2 xh = mul2(OP == kLayerNorm ? add2(h[k], f2(-r.mean)) : h[k], f2(r.rstd));
+        const F2 w = mul2(dy[k], g[k]);
+        s1 = fma2(w, xh, s1);
+        ag[k] = fma2(dy[k], xh, ag[k]);
+        if constexpr (OP == kLayerNorm) {
+            s2 = add2(s2, w);
+            ab[k] = add2(ab[k], dy[k]);
+        }
+    }
+}
+
+// dtot of a tile from its row's two means, then the outputs; dx and dres point
+// at the lane's first column, the tile lies `off` further, at column `base`.
+// `on`: draw the mask (all 32 lanes call).
+template <int OP, typename T, typename IO, bool FULL>
+__device__ __forceinline__ void tile_out(const DropStream& d, const F2* dy, const F2* h,
+                                         const F2* g, const F2* dh, RowStats r, float c1, float c2,
+                                         int64_t row, int base, int off, int left, int lane,
+                                         bool on, T* dx, T* dres) {
+    F2 v[IO::NP];
+#pragma unroll
+    for (int k = 0; k < IO::NP; ++k) {
+        const F2 xh = mul2(OP == kLayerNorm ? add2(h[k], f2(-r.mean)) : h[k], f2(r.rstd));
+        F2 t = fma2(xh, f2(-c1), mul2(dy[k], g[k]));
+        if constexpr (OP == kLayerNorm) t = add2(t, f2(-c2));
+        v[k] = dh ? fma2(t, f2(r.rstd), dh[k]) : mul2(t, f2(r.rstd));
+    }
+    if (dres) IO::template store<FULL>(dres, off, left, v);
+    if (on) {
+        IO::drop(d, base, lane, (uint32_t)row, v);
+#pragma unroll
+        for (int k = 0; k < IO::NP; ++k) v[k] = mul2(v[k], f2(d.a.scale));
+    }
+    IO::template store<FULL>(dx, off, left, v);
+}
+
+// The group's sums of a thread's columns, to its workspace row; j0 is the
+// lane's first column.
+template <int OP, typename IO>
+__device__ __forceinline__ void tile_params(const NormBwdArgs& a, int64_t group, int j0, int off,
+                                            int left, const F2* ag, const F2* ab) {
+    float* p = a.pws + group * 2 * a.pitch + j0;
+    if (a.dgamma) IO::template store_sums<false>(p, off, left, ag);
+    if (OP == kLayerNorm && a.dbeta) IO::template store_sums<false>(p + a.pitch, off, left, ab);
+}
+
+// ------------------------------------------------------------- one warp a row
+template <int OP, typename T, typename IO, typename PT, int V>
+__global__ void __launch_bounds__(kThreads) bwd_warp(NormBwdArgs a) {
+    constexpr int kCols = V * IO::kTile;
+    __shared__ float sums[2][kCols];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int l0 = IO::first(lane), left = a.cols - l0;
+    const DropStream d(a.drop);
+    const T* const dyp = static_cast<const T*>(a.dy) + l0;
+    const T* const hp = static_cast<const T*>(a.h) + l0;
+    const T* const dhp = moved(static_cast<const T*>(a.dh), l0);
+    const PT* const gp = moved(static_cast<const PT*>(a.gamma), l0);
+    const int64_t step = (int64_t)gridDim.x * kWarps;
+    int64_t row = (int64_t)blockIdx.x * kWarps + warp;
+    F2 g[V][IO::NP], ag[V][IO::NP], ab[V][IO::NP];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        IO::template params<false>(gp, i * IO::kTile, left, g[i], 1.f);
+#pragma unroll
+        for (int k = 0; k < IO::NP; ++k) ag[i][k] = ab[i][k] = f2(0.f);
+    }
+    typename IO::R yv[V], hv[V], rv[V];
+    auto fetch = [&](int64_t at) {
+        if (at >= a.rows) return;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            yv[i] = IO::template load<false>(dyp + at * a.cols, i * IO::kTile, left);
+            hv[i] = IO::template load<false>(hp + at * a.cols, i * IO::kTile, left);
+            if (dhp) rv[i] = IO::template load<false>(dhp + at * a.cols, i * IO::kTile, left);
+        }
+    };
+    fetch(row);
+    RowStats next = row_stats<OP>(a, row);
+    while (row < a.rows) {
+        const RowStats r = next;
+        F2 u[V][IO::NP], h[V][IO::NP], dh[V][IO::NP], s1 = f2(0.f), s2 = f2(0.f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            unpack<T, IO::NP>(yv[i], u[i]);
+            unpack<T, IO::NP>(hv[i], h[i]);
+            if (dhp) unpack<T, IO::NP>(rv[i], dh[i]);
+        }
+        const int64_t now = row;
+        row += step;
+        fetch(row);  // in flight while this row is reduced and written
+        next = row_stats<OP>(a, row);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            tile_sums<OP, IO::NP>(u[i], h[i], g[i], r, s1, s2, ag[i], ab[i]);
+        const float c1 = warp_allreduce(s1.x + s1.y, SumOp()) * a.inv_cols;
+        const float c2 =
+            OP == kLayerNorm ? warp_allreduce(s2.x + s2.y, SumOp()) * a.inv_cols : 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            tile_out<OP, T, IO, false>(d, u[i], h[i], g[i], dhp ? dh[i] : nullptr, r, c1, c2, now,
+                                       i * IO::kTile, i * IO::kTile, left, lane,
+                                       a.drop.on && i * IO::kTile < a.cols,
+                                       static_cast<T*>(a.dx) + now * a.cols + l0,
+                                       moved(static_cast<T*>(a.dres), now * a.cols + l0));
+    }
+    // the CTA's warps add their sums in warp order
+    for (int j = threadIdx.x; j < kCols; j += kThreads) sums[0][j] = sums[1][j] = 0.f;
+    for (int w = 0; w < kWarps; ++w) {
+        __syncthreads();
+        if (w != warp) continue;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int k = 0; k < IO::N; ++k) {
+                const int j = i * IO::kTile + l0 + IO::at(k);
+                sums[0][j] += k & 1 ? ag[i][k / 2].y : ag[i][k / 2].x;
+                if constexpr (OP == kLayerNorm) sums[1][j] += k & 1 ? ab[i][k / 2].y : ab[i][k / 2].x;
+            }
+    }
+    __syncthreads();
+    float* p = a.pws + (int64_t)blockIdx.x * 2 * a.pitch;
+    for (int j = threadIdx.x; j < a.cols; j += kThreads) {
+        if (a.dgamma) p[j] = sums[0][j];
+        if (OP == kLayerNorm && a.dbeta) p[a.pitch + j] = sums[1][j];
+    }
+}
+
+// Both sums over the lanes of each half warp.
+template <int OP> __device__ __forceinline__ void sum16(float& a, float& b) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        if constexpr (OP == kLayerNorm) b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+}
+
+// ------------------------------------------------- a CTA or a cluster per row
+template <int OP, typename T, typename IO, typename PT, int V>
+__global__ void __launch_bounds__(kRingThreads) bwd_ring(NormBwdArgs a, RingShape q) {
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ __align__(8) uint64_t full[kRingStages];
+    __shared__ float2 wred[2][kRingWarps];
+    __shared__ RingExchange ex;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
+    const uint32_t P = cluster_nctarank(), rank = cluster_ctarank();
+    const int64_t first = blockIdx.x / P;
+    const int c0 = (int)rank * q.tiles * IO::kTile;
+    const int c1 = min(a.cols, c0 + q.tiles * IO::kTile);
+    const int bytes = (c1 - c0) * (int)sizeof(T);
+    const void* const src[3] = {a.dy, a.h, a.dh};
+    const int ns = a.dh ? 3 : 2;
+    const int64_t total = a.rows * a.cols * (int64_t)sizeof(T);
+    auto offset = [&](int64_t row) { return (row * a.cols + c0) * (int64_t)sizeof(T); };
+    auto stage = [&](int s) { return ring + s * ns * q.room; };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < q.stages; ++s) mbar_init(smem_u32(&full[s]), 1);
+        if (P > 1) ex.init(P);
+        fence_mbar_init();
+        fence_proxy_async_smem();
+    }
+    __syncthreads();
+    if (P > 1) {
+        cluster_arrive_release();
+        cluster_wait_acquire();
+    }
+    if (threadIdx.x == 0)
+        for (int s = 0; s < q.stages; ++s) {
+            const int64_t row = first + (int64_t)s * q.clusters;
+            if (row < a.rows)
+                ring_issue<3, T, IO>(src, ns, offset(row), bytes, total, stage(s), q.room,
+                                     smem_u32(&full[s]));
+        }
+
+    const DropStream d(a.drop);
+    const int base0 = c0 + warp * V * IO::kTile, j0 = base0 + IO::first(lane), left = c1 - j0;
+    const bool whole = base0 + V * IO::kTile <= c1;
+    const PT* const gp = moved(static_cast<const PT*>(a.gamma), j0);
+    F2 ag[V][IO::NP], ab[V][IO::NP];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int k = 0; k < IO::NP; ++k) ag[i][k] = ab[i][k] = f2(0.f);
+    RowStats next = row_stats<OP>(a, first);
+    int s = 0;
+    uint32_t phase = 0;
+    int64_t k = 0;
+    for (int64_t row = first; row < a.rows; row += q.clusters, ++k) {
+        const RowStats r = next;
+        next = row_stats<OP>(a, row + q.clusters);
+        mbar_wait_bounded(smem_u32(&full[s]), phase, q.err);
+        const int64_t off = offset(row);
+        const T* const ys = reinterpret_cast<const T*>(stage(s) + ring_shift<IO>(a.dy, off)) + (j0 - c0);
+        const T* const hs = reinterpret_cast<const T*>(stage(s) + q.room + ring_shift<IO>(a.h, off)) +
+                            (j0 - c0);
+        const T* const ds = reinterpret_cast<const T*>(stage(s) + 2 * q.room +
+                                                       ring_shift<IO>(a.dh, off)) + (j0 - c0);
+        F2 s1 = f2(0.f), s2 = f2(0.f);
+        auto take = [&](auto f) {
+            constexpr bool FULL = decltype(f)::value;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                F2 u[IO::NP], h[IO::NP], g[IO::NP];
+                unpack<T, IO::NP>(IO::template staged<FULL>(ys, i * IO::kTile, left), u);
+                unpack<T, IO::NP>(IO::template staged<FULL>(hs, i * IO::kTile, left), h);
+                IO::template params<FULL>(gp, i * IO::kTile, left, g, 1.f);
+                tile_sums<OP, IO::NP>(u, h, g, r, s1, s2, ag[i], ab[i]);
+            }
+        };
+        if (whole) take(std::true_type()); else take(std::false_type());
+        float t1 = warp_allreduce(s1.x + s1.y, SumOp());
+        float t2 = OP == kLayerNorm ? warp_allreduce(s2.x + s2.y, SumOp()) : 0.f;
+        if (lane == 0) wred[k & 1][warp] = make_float2(t1, t2);
+        __syncthreads();
+        // every thread has left the previous row: refill its stage
+        if (threadIdx.x == 0 && k > 0 && q.stages > 1) {
+            const int64_t fill = row + (int64_t)(q.stages - 1) * q.clusters;
+            const int sp = s == 0 ? q.stages - 1 : s - 1;
+            if (fill < a.rows)
+                ring_issue<3, T, IO>(src, ns, offset(fill), bytes, total, stage(sp), q.room,
+                                     smem_u32(&full[sp]));
+        }
+        const int l16 = lane & 15;
+        t1 = l16 < W ? wred[k & 1][l16].x : 0.f;
+        t2 = l16 < W ? wred[k & 1][l16].y : 0.f;
+        sum16<OP>(t1, t2);
+        if (P > 1) {
+            const float4* parts = ex.all(k, make_float4(t1, t2, 0.f, 0.f), P, rank, q.err);
+            t1 = l16 < (int)P ? parts[l16].x : 0.f;
+            t2 = l16 < (int)P ? parts[l16].y : 0.f;
+            sum16<OP>(t1, t2);
+        }
+        t1 *= a.inv_cols;
+        t2 *= a.inv_cols;
+        T* const dx = static_cast<T*>(a.dx) + row * a.cols + j0;
+        T* const dres = moved(static_cast<T*>(a.dres), row * a.cols + j0);
+        auto give = [&](auto f) {
+            constexpr bool FULL = decltype(f)::value;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                F2 u[IO::NP], h[IO::NP], g[IO::NP], dh[IO::NP];
+                unpack<T, IO::NP>(IO::template staged<FULL>(ys, i * IO::kTile, left), u);
+                unpack<T, IO::NP>(IO::template staged<FULL>(hs, i * IO::kTile, left), h);
+                if (ns > 2) unpack<T, IO::NP>(IO::template staged<FULL>(ds, i * IO::kTile, left), dh);
+                IO::template params<FULL>(gp, i * IO::kTile, left, g, 1.f);
+                tile_out<OP, T, IO, FULL>(d, u, h, g, ns > 2 ? dh : nullptr, r, t1, t2, row,
+                                          base0 + i * IO::kTile, i * IO::kTile, left, lane,
+                                          a.drop.on && (FULL || base0 + i * IO::kTile < c1), dx,
+                                          dres);
+            }
+        };
+        if (whole) give(std::true_type()); else give(std::false_type());
+        if (q.stages == 1) {  // nowhere to fetch ahead: the next row comes now
+            __syncthreads();
+            if (threadIdx.x == 0 && row + q.clusters < a.rows)
+                ring_issue<3, T, IO>(src, ns, offset(row + q.clusters), bytes, total, stage(0),
+                                     q.room, smem_u32(&full[0]));
+        }
+        if (++s == q.stages) {
+            s = 0;
+            phase ^= 1u;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        tile_params<OP, IO>(a, first, j0, i * IO::kTile, left, ag[i], ab[i]);
+    if (P > 1) {  // no CTA leaves while a peer's deposit to it may be in flight
+        cluster_arrive_release();
+        cluster_wait_acquire();
+    }
+}
+
+// ------------------------------------------------------------- general form
 template <int OP, typename T, typename IO, typename PT>
 __global__ void __launch_bounds__(kThreads) bwd_stats(NormBwdArgs a) {
     __shared__ float red[2][2 * kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const PT* gp = static_cast<const PT*>(a.gamma);
     const int64_t items = a.rows * a.nch;
     int turn = 0;
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x, turn ^= 1) {
         const int64_t row = it / a.nch;
-        const int64_t c0 = (it - row * a.nch) * (int64_t)(kChunkTiles * IO::kTile);
-        const T* dy = static_cast<const T*>(a.dy) + row * a.cols;
-        const T* h = static_cast<const T*>(a.h) + row * a.cols;
-        const float rstd = a.rstd[row], mean = OP == kLayerNorm ? a.mean[row] : 0.f;
-        float s1 = 0.f, s2 = 0.f;
+        const int c0 = (int)(it - row * a.nch) * (kChunkTiles * IO::kTile);
+        const int j0 = c0 + warp * kTilesPerWarp * IO::kTile + IO::first(lane), left = a.cols - j0;
+        const T* dy = static_cast<const T*>(a.dy) + row * a.cols + j0;
+        const T* hp = static_cast<const T*>(a.h) + row * a.cols + j0;
+        const PT* gp = moved(static_cast<const PT*>(a.gamma), j0);
+        const RowStats r = row_stats<OP>(a, row);
+        F2 s1 = f2(0.f), s2 = f2(0.f);
 #pragma unroll
         for (int i = 0; i < kTilesPerWarp; ++i) {
-            const int64_t base = c0 + (int64_t)(warp + kWarps * i) * IO::kTile;
-            if (base < a.cols) {
-                float u[IO::N], v[IO::N], g[IO::N];
-                Elem<T>::unpack(IO::load(dy, base, lane, a.cols), u);
-                Elem<T>::unpack(IO::load(h, base, lane, a.cols), v);
-                IO::template params<PT>(gp, base, lane, a.cols, g, 1.f);
+            F2 u[IO::NP], h[IO::NP], g[IO::NP];
+            unpack<T, IO::NP>(IO::template load<false>(dy, i * IO::kTile, left), u);
+            unpack<T, IO::NP>(IO::template load<false>(hp, i * IO::kTile, left), h);
+            IO::template params<false>(gp, i * IO::kTile, left, g, 1.f);
 #pragma unroll
-                for (int k = 0; k < IO::N; ++k) {
-                    const float w = u[k] * g[k];  // 0 past the row
-                    s1 = fmaf(w, (v[k] - mean) * rstd, s1);
-                    s2 += w;
-                }
+            for (int k = 0; k < IO::NP; ++k) {
+                const F2 w = mul2(u[k], g[k]);  // 0 past the row
+                s1 = fma2(w, mul2(add2(h[k], f2(-r.mean)), f2(r.rstd)), s1);
+                s2 = add2(s2, w);
             }
         }
-        block_sum2(s1, s2, red[turn], kWarps, kThreads);
+        float t1 = s1.x + s1.y, t2 = s2.x + s2.y;
+        block_sum2(t1, t2, red[turn], kWarps, kThreads);
         if (threadIdx.x == 0) {
-            a.ws[2 * it] = s1;
-            a.ws[2 * it + 1] = s2;
+            a.ws[2 * it] = t1;
+            a.ws[2 * it + 1] = t2;
         }
     }
 }
@@ -63,12 +363,14 @@ __global__ void __launch_bounds__(kThreads) bwd_apply(NormBwdArgs a) {
     __shared__ float4 rowc[kRowBlock];  // mean, rstd, mean_j(w xh), mean_j(w)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const DropStream d(a.drop);
-    const int64_t base = ((int64_t)blockIdx.x * kWarps + warp) * IO::kTile;
+    const int base = ((int)blockIdx.x * kWarps + warp) * IO::kTile;
+    const int j0 = base + IO::first(lane), left = a.cols - j0;
     const bool mine = base < a.cols;
-    float g[IO::N], ag[IO::N], ab[IO::N];
+    F2 g[IO::NP], ag[IO::NP], ab[IO::NP];
 #pragma unroll
-    for (int k = 0; k < IO::N; ++k) ag[k] = ab[k] = 0.f;
-    if (mine) IO::template params<PT>(static_cast<const PT*>(a.gamma), base, lane, a.cols, g, 1.f);
+    for (int k = 0; k < IO::NP; ++k) ag[k] = ab[k] = f2(0.f);
+    if (mine)
+        IO::template params<false>(moved(static_cast<const PT*>(a.gamma), j0), 0, left, g, 1.f);
     const int64_t r1 = min(a.rows, (int64_t)(blockIdx.y + 1) * a.group_rows);
     for (int64_t r0 = (int64_t)blockIdx.y * a.group_rows; r0 < r1; r0 += kRowBlock) {
         const int nr = (int)min((int64_t)kRowBlock, r1 - r0);
@@ -82,117 +384,168 @@ __global__ void __launch_bounds__(kThreads) bwd_apply(NormBwdArgs a) {
             }
             s1 = warp_allreduce(s1, SumOp());
             s2 = warp_allreduce(s2, SumOp());
+            const RowStats r = row_stats<OP>(a, r0 + i);
             if (lane == 0)
-                rowc[i] = make_float4(OP == kLayerNorm ? a.mean[r0 + i] : 0.f, a.rstd[r0 + i],
-                                      s1 / (float)a.cols,
-                                      OP == kLayerNorm ? s2 / (float)a.cols : 0.f);
+                rowc[i] = make_float4(r.mean, r.rstd, s1 * a.inv_cols, s2 * a.inv_cols);
         }
         __syncthreads();
         if (!mine) continue;
 #pragma unroll 2
         for (int i = 0; i < nr; ++i) {
-            const int64_t o = (r0 + i) * a.cols;
+            const int64_t o = (r0 + i) * a.cols + j0;
             const float4 c = rowc[i];
-            float u[IO::N], v[IO::N];
-            Elem<T>::unpack(IO::load(static_cast<const T*>(a.dy) + o, base, lane, a.cols), u);
-            Elem<T>::unpack(IO::load(static_cast<const T*>(a.h) + o, base, lane, a.cols), v);
-#pragma unroll
-            for (int k = 0; k < IO::N; ++k) {
-                const float xh = (v[k] - c.x) * c.y;
-                ag[k] = fmaf(u[k], xh, ag[k]);
-                ab[k] += u[k];
-                v[k] = (fmaf(-xh, c.z, u[k] * g[k]) - c.w) * c.y;
-            }
-            if (a.dh) {
-                Elem<T>::unpack(IO::load(static_cast<const T*>(a.dh) + o, base, lane, a.cols), u);
-#pragma unroll
-                for (int k = 0; k < IO::N; ++k) v[k] += u[k];
-            }
-            if (a.dres) IO::store(static_cast<T*>(a.dres) + o, base, lane, a.cols, Elem<T>::pack(v));
-            if (a.drop.on) {
-                const uint32_t m = IO::keep(d, base, lane, (uint32_t)(r0 + i));
-#pragma unroll
-                for (int k = 0; k < IO::N; ++k) v[k] = (m >> k) & 1u ? v[k] * d.scale : 0.f;
-            }
-            IO::store(static_cast<T*>(a.dx) + o, base, lane, a.cols, Elem<T>::pack(v));
+            F2 u[IO::NP], h[IO::NP], dh[IO::NP], s1, s2;
+            unpack<T, IO::NP>(IO::template load<false>(static_cast<const T*>(a.dy) + o, 0, left), u);
+            unpack<T, IO::NP>(IO::template load<false>(static_cast<const T*>(a.h) + o, 0, left), h);
+            if (a.dh)
+                unpack<T, IO::NP>(IO::template load<false>(static_cast<const T*>(a.dh) + o, 0, left),
+                                  dh);
+            s1 = s2 = f2(0.f);
+            tile_sums<OP, IO::NP>(u, h, g, {c.x, c.y}, s1, s2, ag, ab);
+            tile_out<OP, T, IO, false>(d, u, h, g, a.dh ? dh : nullptr, {c.x, c.y}, c.z, c.w, r0 + i,
+                                       base, 0, left, lane, a.drop.on, static_cast<T*>(a.dx) + o,
+                                       moved(static_cast<T*>(a.dres), o));
         }
     }
-    if (mine) {
-        float* p = a.pws + (int64_t)blockIdx.y * 2 * a.cols;
-        if (a.dgamma) {
-#pragma unroll
-            for (int k = 0; k < IO::N; ++k)
-                if (IO::valid(base, lane, k, a.cols)) p[IO::col(base, lane, k)] = ag[k];
-        }
-        if (a.dbeta) {
-#pragma unroll
-            for (int k = 0; k < IO::N; ++k)
-                if (IO::valid(base, lane, k, a.cols)) p[a.cols + IO::col(base, lane, k)] = ab[k];
-        }
-    }
+    if (mine) tile_params<OP, IO>(a, blockIdx.y, j0, 0, left, ag, ab);
 }
 
-// dgamma and dbeta: the groups' sums added in group order.
-template <typename PT>
+__device__ __forceinline__ void store_param(void* p, bool half, int64_t j, float v) {
+    if (half) static_cast<bf16*>(p)[j] = Elem<bf16>::from_f(v);
+    else static_cast<float*>(p)[j] = v;
+}
+
+// dgamma (blockIdx.y 0) and dbeta (1): the groups' sums.  A warp adds groups
+// w, w + kWarps, ... of 128 columns, the CTA's warps are added in order.
 __global__ void __launch_bounds__(kThreads) bwd_params(NormBwdArgs a) {
-    for (int64_t j = (int64_t)blockIdx.x * kThreads + threadIdx.x; j < a.cols;
-         j += (int64_t)gridDim.x * kThreads) {
-        float sg = 0.f, sb = 0.f;
-        for (int q = 0; q < a.groups; ++q) {
-            const float* p = a.pws + (int64_t)q * 2 * a.cols;
-            if (a.dgamma) sg += p[j];
-            if (a.dbeta) sb += p[a.cols + j];
-        }
-        if (a.dgamma) static_cast<PT*>(a.dgamma)[j] = Elem<PT>::from_f(sg);
-        if (a.dbeta) static_cast<PT*>(a.dbeta)[j] = Elem<PT>::from_f(sb);
+    __shared__ float4 part[kWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    void* const out = blockIdx.y ? a.dbeta : a.dgamma;
+    if (!out) return;
+    const int j = (int)blockIdx.x * 128 + 4 * lane;  // below the pitch, a multiple of 128
+    const float* p = a.pws + (blockIdx.y ? a.pitch : 0) + j;
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int q = warp; q < a.groups; q += kWarps) {
+        const float4 v = *reinterpret_cast<const float4*>(p + (int64_t)q * 2 * a.pitch);
+        t.x += v.x; t.y += v.y; t.z += v.z; t.w += v.w;
+    }
+    part[warp][lane] = t;
+    __syncthreads();
+    if (threadIdx.x < 128) {
+        const int c = (int)blockIdx.x * 128 + threadIdx.x;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+            v += reinterpret_cast<const float*>(part[w])[threadIdx.x];
+        if (c < a.cols) store_param(out, a.half, c, v);
     }
 }
 
 template <int OP, typename T, typename IO, typename PT>
-cudaError_t run_bwd(const NormBwdArgs& a, int sms, cudaStream_t s) {
-    if (a.rows > 0) {
-        const int64_t items = a.rows * a.nch;
-        const unsigned grid = (unsigned)(items < (int64_t)sms * 32 ? items : (int64_t)sms * 32);
-        bwd_stats<OP, T, IO, PT><<<grid, kThreads, 0, s>>>(a);
-        const int64_t strip = (int64_t)kWarps * IO::kTile;
-        bwd_apply<OP, T, IO, PT><<<dim3((unsigned)((a.cols + strip - 1) / strip), (unsigned)a.groups),
-                                   kThreads, 0, s>>>(a);
-    }
-    if (a.dgamma || a.dbeta) {
-        const int64_t blocks = (a.cols + kThreads - 1) / kThreads;
-        bwd_params<PT><<<(unsigned)(blocks < sms * 8 ? blocks : sms * 8), kThreads, 0, s>>>(a);
-    }
+cudaError_t run_general(const NormBwdArgs& a, int sms, cudaStream_t s) {
+    const int64_t items = a.rows * a.nch;
+    const unsigned grid = (unsigned)(items < (int64_t)sms * 32 ? items : (int64_t)sms * 32);
+    bwd_stats<OP, T, IO, PT><<<grid, kThreads, 0, s>>>(a);
+    const int strip = kWarps * IO::kTile;
+    bwd_apply<OP, T, IO, PT><<<dim3((unsigned)((a.cols + strip - 1) / strip), (unsigned)a.groups),
+                           kThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
-template <int OP, typename T>
-cudaError_t pick_bwd(TrainKey k, const NormBwdArgs& a, int sms, cudaStream_t s) {
-    if (k.vec)
-        return k.pdtype == 0 ? run_bwd<OP, T, VecIO<T>, float>(a, sms, s)
-                             : run_bwd<OP, T, VecIO<T>, bf16>(a, sms, s);
-    return k.pdtype == 0 ? run_bwd<OP, T, ElemIO<T>, float>(a, sms, s)
-                         : run_bwd<OP, T, ElemIO<T>, bf16>(a, sms, s);
+template <int OP, typename T, typename IO, typename PT, int V>
+cudaError_t run_warp(const NormBwdArgs& a, cudaStream_t s) {
+    bwd_warp<OP, T, IO, PT, V><<<(unsigned)a.groups, kThreads, 0, s>>>(a);
+    return cudaGetLastError();
 }
+
+template <int OP, typename T, typename IO, typename PT, int V>
+cudaError_t run_ring(NormBwdArgs& a, const RingPlan& p, cudaStream_t s) {
+    const void* fn = (const void*)bwd_ring<OP, T, IO, PT, V>;
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    unsigned* err = device_error_word();
+    a.groups = ring_clusters(dev, fn, p, a.rows);  // at most the layout's
+    if (!err || a.groups < 1) return cudaErrorInvalidConfiguration;
+    return launch_ring(fn, a, p, a.groups, err, s);
+}
+
+template <int OP, typename T, typename IO, typename PT>
+cudaError_t run_bwd(NormBwdArgs& a, int sms, cudaStream_t s) {
+    const int tiles = (a.cols + IO::kTile - 1) / IO::kTile;
+    if (tiles <= 1) return run_warp<OP, T, IO, PT, 1>(a, s);
+    if (tiles <= 2) return run_warp<OP, T, IO, PT, 2>(a, s);
+    if (tiles <= 4) return run_warp<OP, T, IO, PT, 4>(a, s);
+    RingPlan p;
+    if (!plan_ring(tiles, sizeof(T), a.dh ? 3 : 2, a.rows, sms, &p))
+        return run_general<OP, T, IO, PT>(a, sms, s);
+    return p.V == 4 ? run_ring<OP, T, IO, PT, 4>(a, p, s) : run_ring<OP, T, IO, PT, 8>(a, p, s);
+}
+
+template <int OP, typename T, typename IO>
+cudaError_t pick_param(NormBwdArgs& a, int sms, cudaStream_t s) {
+    return a.half ? run_bwd<OP, T, IO, bf16>(a, sms, s) : run_bwd<OP, T, IO, float>(a, sms, s);
+}
+
+template <int OP, typename T>
+cudaError_t pick_bwd(TrainKey k, NormBwdArgs& a, int sms, cudaStream_t s) {
+    return k.vec ? pick_param<OP, T, VecIO<T, 4>>(a, sms, s)
+                 : pick_param<OP, T, ElemIO<T, 4>>(a, sms, s);
+}
+
+constexpr int kTileCols = VecIO<float, 4>::kTile;
 
 }  // namespace
 
-int train_groups(int dtype, int64_t rows, int64_t cols, int sms, int64_t* group_rows) {
-    const int64_t strip = (int64_t)kWarps * (dtype == 0 ? VecIO<float>::kTile : VecIO<bf16>::kTile);
-    const int64_t strips = (cols + strip - 1) / strip;
-    int64_t g = (4 * (int64_t)sms + strips - 1) / strips;
-    g = g < (rows + 7) / 8 ? g : (rows + 7) / 8;
-    if (g < 1) g = 1;
-    *group_rows = (rows + g - 1) / g;
-    if (*group_rows < 1) *group_rows = 1;
-    return (int)((rows + *group_rows - 1) / *group_rows);
+TrainLayout norm_bwd_layout(int dtype, int64_t rows, int64_t cols, int sms) {
+    TrainLayout l{};
+    l.pitch = (int)((cols + kTileCols - 1) / kTileCols * kTileCols);
+    l.nch = train_chunks(cols);
+    l.group_rows = 1;
+    if (rows == 0) return l;
+    const int tiles = l.pitch / kTileCols;
+    if (tiles <= 4) {  // one warp per row
+        const int64_t want = (rows + kWarps - 1) / kWarps;
+        l.groups = (int)(want < sms * 2 ? want : sms * 2);
+    } else {
+        // the ring's grid and the general form's groups, whichever is larger:
+        // which of them runs depends on the call's streams too
+        const int64_t strips = (tiles + kWarps - 1) / kWarps;
+        int64_t g = (4 * (int64_t)sms + strips - 1) / strips;
+        g = std::max<int64_t>(1, std::min<int64_t>(g, (rows + 7) / 8));
+        l.group_rows = (rows + g - 1) / g;
+        l.groups = (int)((rows + l.group_rows - 1) / l.group_rows);
+        l.room_groups = l.groups;
+        for (int streams = 2; streams <= 3; ++streams) {
+            RingPlan p;
+            if (plan_ring(tiles, dtype == 0 ? 4 : 2, streams, rows, sms, &p))
+                l.room_groups = (int)std::max<int64_t>(l.room_groups, std::min<int64_t>(p.most, rows));
+        }
+        // the general form's partials, where it may run
+        RingPlan p;
+        if (!plan_ring(tiles, dtype == 0 ? 4 : 2, 3, rows, sms, &p)) l.partials = rows * l.nch * 8;
+    }
+    l.room_groups = std::max(l.room_groups, l.groups);
+    return l;
 }
 
-cudaError_t launch_norm_bwd(TrainKey k, const NormBwdArgs& a, int sms, cudaStream_t s) {
-    if (k.op == kLayerNorm)
-        return k.dtype == 0 ? pick_bwd<kLayerNorm, float>(k, a, sms, s)
-                            : pick_bwd<kLayerNorm, bf16>(k, a, sms, s);
-    return k.dtype == 0 ? pick_bwd<kRMSNorm, float>(k, a, sms, s)
-                        : pick_bwd<kRMSNorm, bf16>(k, a, sms, s);
+cudaError_t launch_norm_bwd(TrainKey k, NormBwdArgs a, int sms, cudaStream_t s) {
+    if (a.rows > 0) {
+        cudaError_t e;
+        if (k.op == kLayerNorm)
+            e = k.dtype == 0 ? pick_bwd<kLayerNorm, float>(k, a, sms, s)
+                             : pick_bwd<kLayerNorm, bf16>(k, a, sms, s);
+        else
+            e = k.dtype == 0 ? pick_bwd<kRMSNorm, float>(k, a, sms, s)
+                             : pick_bwd<kRMSNorm, bf16>(k, a, sms, s);
+        if (e != cudaSuccess) return e;
+    }
+    if (a.dgamma || a.dbeta) {
+        bwd_params<<<dim3((unsigned)(a.pitch / kTileCols), a.dbeta ? 2u : 1u), kThreads, 0, s>>>(a);
+        return cudaGetLastError();
+    }
+    return cudaSuccess;
 }
 
 }  // namespace credit

@@ -1,11 +1,18 @@
 // norm_fwd.cu -- h = residual + dropout(x), y = norm(h) and the row statistics
 // (mean, 1/sqrt(var + eps)) that the backward pass needs.
 //
-// General form, rows of any width: one kernel writes a partial (count, mean,
-// M2 about that mean) per row and chunk of 32 warp tiles, the next merges a
-// row's partials (the parallel-axis form of Chan et al.'s merge) and writes.
-// Two reads of x and residual, the second from L2 where they fit it.
-#include "train.cuh"
+// Three forms, chosen by the row's width alone:
+//   fwd_warp   one warp holds a row's h in registers
+//   fwd_ring   a CTA, or a cluster, holds it; the next rows' x and residual
+//              arrive in a ring of shared-memory stages meanwhile
+//   fwd_stats, fwd_apply   wider rows: partial statistics per chunk, then a
+//              second read (from L2 where the rows fit it)
+// The first two read x and residual once and write h and y once.
+//
+// Statistics: sum and M2 about the piece's own mean (of a warp, a CTA or a
+// chunk), merged with the parallel-axis form of Chan et al.'s update.
+#include "planner.h"
+#include "ring.cuh"
 
 namespace credit {
 
@@ -16,6 +23,248 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kTilesPerWarp = 4;
 constexpr int kChunkTiles = kWarps * kTilesPerWarp;
 
+// (h - mean) rstd gamma + beta; rstd is CUDA's rsqrtf (2 ulp).
+template <int OP>
+__device__ __forceinline__ F2 normed(F2 h, float mu, float rstd, F2 g, F2 b) {
+    const F2 z = OP == kLayerNorm ? mul2(add2(h, f2(-mu)), f2(rstd)) : mul2(h, f2(rstd));
+    return fma2(z, g, b);
+}
+
+// Merge `count` <= 16 parts (n, sum, mean, M2 about that mean) of a row's
+// pieces, the same in every lane; `part`: the pieces are not the whole row,
+// whose mean is sum / n (else sum inv_cols).
+template <int OP>
+__device__ __forceinline__ void merge_parts(const float4* parts, int count, int lane, bool part,
+                                            float inv_cols, float& n, float& s, float& mu,
+                                            float& m2) {
+    const int at = lane & 15;
+    const float4 q = at < count ? parts[at] : make_float4(0.f, 0.f, 0.f, 0.f);
+    m2 = q.w;
+    if constexpr (OP == kLayerNorm) {
+        s = q.y;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        mu = s * inv_cols;
+        if (part) {
+            n = q.x;
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+            mu = __fdividef(s, n);
+        }
+        m2 = fmaf(q.x * (q.z - mu), q.z - mu, m2);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
+}
+
+// A warp's part of a row from its V tiles' h (zeros past the end): the sum,
+// the mean sum inv_n, and M2 about it.
+template <int OP, typename IO, int V, bool FULL>
+__device__ __forceinline__ void warp_part(const F2 (&h)[V][IO::NP], int left, float inv_n, float& s,
+                                          float& mu, float& m2) {
+    F2 m = f2(0.f);
+    if constexpr (OP == kLayerNorm) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int k = 0; k < IO::NP; ++k) m = add2(m, h[i][k]);
+        s = warp_allreduce(m.x + m.y, SumOp());
+        mu = s * inv_n;
+        m = f2(0.f);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int k = 0; k < IO::NP; ++k) {
+                F2 e = add2(h[i][k], f2(-mu));
+                if constexpr (!FULL) e = inside<FULL, IO>(e, i * IO::kTile, k, left);
+                m = fma2(e, e, m);
+            }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int k = 0; k < IO::NP; ++k) m = fma2(h[i][k], h[i][k], m);
+    }
+    m2 = warp_allreduce(m.x + m.y, SumOp());
+}
+
+// y of a warp's tiles; g, b, y point at the lane's first column.
+template <int OP, typename T, typename IO, int V, bool FULL, typename PT>
+__device__ __forceinline__ void write_tiles(F2 (&h)[V][IO::NP], const PT* gp, const PT* bp, T* y,
+                                            int left, float mu, float rstd) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        F2 g[IO::NP], b[IO::NP];
+        IO::template params<FULL>(gp, i * IO::kTile, left, g, 1.f);
+        IO::template params<FULL>(bp, i * IO::kTile, left, b, 0.f);
+#pragma unroll
+        for (int k = 0; k < IO::NP; ++k) h[i][k] = normed<OP>(h[i][k], mu, rstd, g[k], b[k]);
+        IO::template store<FULL>(y, i * IO::kTile, left, h[i]);
+    }
+}
+
+__device__ __forceinline__ float finish(const NormFwdArgs& a, int64_t row, bool stats, float mu,
+                                        float m2) {
+    const float rstd = rsqrtf(fmaf(m2, a.inv_cols, a.eps));
+    if (stats) {
+        if (a.mean) a.mean[row] = mu;
+        if (a.rstd) a.rstd[row] = rstd;
+    }
+    return rstd;
+}
+
+// ------------------------------------------------------------- one warp a row
+template <int OP, typename T, typename IO, typename PT, int V>
+__global__ void __launch_bounds__(kThreads) fwd_warp(NormFwdArgs a) {
+    const int lane = threadIdx.x & 31, l0 = IO::first(lane), left = a.cols - l0;
+    const DropStream d(a.drop);
+    const T* const x = static_cast<const T*>(a.x) + l0;
+    const T* const r = moved(static_cast<const T*>(a.residual), l0);
+    const PT* const gp = moved(static_cast<const PT*>(a.gamma), l0);
+    const PT* const bp = moved(static_cast<const PT*>(a.beta), l0);
+    const int64_t step = (int64_t)gridDim.x * kWarps;
+    int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (row >= a.rows) return;
+    typename IO::R xv[V], rv[V];
+    auto fetch = [&](int64_t at) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            xv[i] = IO::template load<false>(x + at * a.cols, i * IO::kTile, left);
+        if (r) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                rv[i] = IO::template load<false>(r + at * a.cols, i * IO::kTile, left);
+        }
+    };
+    fetch(row);
+    while (row < a.rows) {
+        F2 h[V][IO::NP];
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            tile_h<T, IO>(xv[i], rv[i], r != nullptr, a.drop.on && i * IO::kTile < a.cols, d,
+                          i * IO::kTile, lane, (uint32_t)row, h[i]);
+        const int64_t now = row;
+        row += step;
+        if (row < a.rows) fetch(row);  // in flight while this row is reduced and written
+        if (a.h) {
+            T* const ho = static_cast<T*>(a.h) + now * a.cols + l0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) IO::template store<false>(ho, i * IO::kTile, left, h[i]);
+        }
+        float s, mu = 0.f, m2;
+        warp_part<OP, IO, V, false>(h, left, a.inv_cols, s, mu, m2);
+        const float rstd = finish(a, now, lane == 0, mu, m2);
+        write_tiles<OP, T, IO, V, false>(h, gp, bp, static_cast<T*>(a.y) + now * a.cols + l0, left,
+                                         mu, rstd);
+    }
+}
+
+// ------------------------------------------------- a CTA or a cluster per row
+// Warp w of a CTA holds the V tiles from column c0 + 128 V w on: every address
+// of a row is one register plus a constant.
+template <int OP, typename T, typename IO, typename PT, int V>
+__global__ void __launch_bounds__(kRingThreads) fwd_ring(NormFwdArgs a, RingShape q) {
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ __align__(8) uint64_t full[kRingStages];
+    __shared__ float4 wred[2][kRingWarps];
+    __shared__ RingExchange ex;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
+    const uint32_t P = cluster_nctarank(), rank = cluster_ctarank();
+    const int64_t first = blockIdx.x / P;
+    const int c0 = (int)rank * q.tiles * IO::kTile;               // the slice's columns
+    const int c1 = min(a.cols, c0 + q.tiles * IO::kTile);
+    const int bytes = (c1 - c0) * (int)sizeof(T);
+    const void* const src[2] = {a.x, a.residual};
+    const int ns = a.residual ? 2 : 1;
+    const int64_t total = a.rows * a.cols * (int64_t)sizeof(T);
+    auto offset = [&](int64_t row) { return (row * a.cols + c0) * (int64_t)sizeof(T); };
+    auto stage = [&](int s) { return ring + s * ns * q.room; };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < q.stages; ++s) mbar_init(smem_u32(&full[s]), 1);
+        if (P > 1) ex.init(P);
+        fence_mbar_init();
+        fence_proxy_async_smem();
+    }
+    __syncthreads();
+    if (P > 1) {  // every CTA's slots and mbarriers exist before any deposit
+        cluster_arrive_release();
+        cluster_wait_acquire();
+    }
+    if (threadIdx.x == 0)
+        for (int s = 0; s < q.stages; ++s) {
+            const int64_t row = first + (int64_t)s * q.clusters;
+            if (row < a.rows)
+                ring_issue<2, T, IO>(src, ns, offset(row), bytes, total, stage(s), q.room,
+                                     smem_u32(&full[s]));
+        }
+
+    const DropStream d(a.drop);
+    const int base0 = c0 + warp * V * IO::kTile, j0 = base0 + IO::first(lane), left = c1 - j0;
+    const bool whole = base0 + V * IO::kTile <= c1;
+    const float n = (float)max(0, min(c1 - base0, V * IO::kTile));
+    const float inv_n = 1.f / fmaxf(n, 1.f);
+    const PT* const gp = moved(static_cast<const PT*>(a.gamma), j0);
+    const PT* const bp = moved(static_cast<const PT*>(a.beta), j0);
+    int s = 0;
+    uint32_t phase = 0;
+    int64_t k = 0;
+    for (int64_t row = first; row < a.rows; row += q.clusters, ++k) {
+        const int64_t off = offset(row), out = row * a.cols + j0;
+        F2 h[V][IO::NP];
+        float sum = 0.f, mu = 0.f, m2, cn;
+        mbar_wait_bounded(smem_u32(&full[s]), phase, q.err);
+        auto take = [&](auto f) {
+            constexpr bool FULL = decltype(f)::value;
+            const T* xs = reinterpret_cast<const T*>(stage(s) + ring_shift<IO>(a.x, off)) + (j0 - c0);
+            const T* rs = reinterpret_cast<const T*>(stage(s) + q.room +
+                                                     ring_shift<IO>(a.residual, off)) + (j0 - c0);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                typename IO::R rv = {};
+                if (ns > 1) rv = IO::template staged<FULL>(rs, i * IO::kTile, left);
+                tile_h<T, IO>(IO::template staged<FULL>(xs, i * IO::kTile, left), rv, ns > 1,
+                              a.drop.on && (FULL || base0 + i * IO::kTile < c1), d,
+                              base0 + i * IO::kTile, lane, (uint32_t)row, h[i]);
+            }
+            if (a.h) {
+                T* const ho = static_cast<T*>(a.h) + out;
+#pragma unroll
+                for (int i = 0; i < V; ++i) IO::template store<FULL>(ho, i * IO::kTile, left, h[i]);
+            }
+            warp_part<OP, IO, V, FULL>(h, left, inv_n, sum, mu, m2);
+        };
+        if (whole) take(std::true_type()); else take(std::false_type());
+        if (lane == 0) wred[k & 1][warp] = make_float4(n, sum, mu, m2);
+        __syncthreads();
+        // every thread has read the stage: bring the row that comes next in it
+        if (threadIdx.x == 0) {
+            const int64_t next = row + (int64_t)q.stages * q.clusters;
+            if (next < a.rows)
+                ring_issue<2, T, IO>(src, ns, offset(next), bytes, total, stage(s), q.room,
+                                     smem_u32(&full[s]));
+        }
+        merge_parts<OP>(wred[k & 1], W, lane, P > 1, a.inv_cols, cn, sum, mu, m2);
+        if (P > 1) {
+            const float4* parts = ex.all(k, make_float4(cn, sum, mu, m2), P, rank, q.err);
+            merge_parts<OP>(parts, (int)P, lane, false, a.inv_cols, cn, sum, mu, m2);
+        }
+        const float rstd = finish(a, row, rank == 0 && threadIdx.x == 0, mu, m2);
+        T* const y = static_cast<T*>(a.y) + out;
+        if (whole) write_tiles<OP, T, IO, V, true>(h, gp, bp, y, left, mu, rstd);
+        else write_tiles<OP, T, IO, V, false>(h, gp, bp, y, left, mu, rstd);
+        if (++s == q.stages) {
+            s = 0;
+            phase ^= 1u;
+        }
+    }
+    if (P > 1) {  // no CTA leaves while a peer's deposit to it may be in flight
+        cluster_arrive_release();
+        cluster_wait_acquire();
+    }
+}
+
+// ------------------------------------------------------------- general form
 // Merge a row's nch partials; every lane of the calling warp returns the same.
 template <int OP>
 __device__ __forceinline__ NormPart merge_row(const float* ws, int nch, int lane) {
@@ -49,39 +298,38 @@ __global__ void __launch_bounds__(kThreads) fwd_stats(NormFwdArgs a) {
     const int64_t items = a.rows * a.nch;
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
         const int64_t row = it / a.nch;
-        const int64_t c0 = (it - row * a.nch) * (int64_t)(kChunkTiles * IO::kTile);
-        const T* x = static_cast<const T*>(a.x) + row * a.cols;
-        const T* r = a.residual ? static_cast<const T*>(a.residual) + row * a.cols : nullptr;
-        float h[kTilesPerWarp][IO::N];
-        float s = 0.f;
+        const int c0 = (int)(it - row * a.nch) * (kChunkTiles * IO::kTile);
+        const int base0 = c0 + warp * kTilesPerWarp * IO::kTile;
+        const int j0 = base0 + IO::first(lane), left = a.cols - j0;
+        const T* x = static_cast<const T*>(a.x) + row * a.cols + j0;
+        const T* r = moved(static_cast<const T*>(a.residual), row * a.cols + j0);
+        F2 h[kTilesPerWarp][IO::NP], s2 = f2(0.f);
 #pragma unroll
         for (int i = 0; i < kTilesPerWarp; ++i) {
-            const int64_t base = c0 + (int64_t)(warp + kWarps * i) * IO::kTile;
-            if (base < a.cols) {
-                tile_h<T, IO>(x, r, a.drop.on, d, base, lane, (uint32_t)row, a.cols, h[i]);
-            } else {
+            typename IO::R rv = {};
+            if (r) rv = IO::template load<false>(r, i * IO::kTile, left);
+            tile_h<T, IO>(IO::template load<false>(x, i * IO::kTile, left), rv, r != nullptr,
+                          a.drop.on && base0 + i * IO::kTile < a.cols, d, base0 + i * IO::kTile,
+                          lane, (uint32_t)row, h[i]);
 #pragma unroll
-                for (int k = 0; k < IO::N; ++k) h[i][k] = 0.f;
-            }
-#pragma unroll
-            for (int k = 0; k < IO::N; ++k) s += OP == kLayerNorm ? h[i][k] : h[i][k] * h[i][k];
+            for (int k = 0; k < IO::NP; ++k)
+                s2 = OP == kLayerNorm ? add2(s2, h[i][k]) : fma2(h[i][k], h[i][k], s2);
         }
-        s = block_allreduce(s, red[0], SumOp(), 0.f);
-        const float n = (float)min(a.cols - c0, (int64_t)(kChunkTiles * IO::kTile));
-        float mu = 0.f, m2 = s;
+        float m2 = block_allreduce(s2.x + s2.y, red[0], SumOp(), 0.f), mu = 0.f;
+        const float n = (float)min(a.cols - c0, kChunkTiles * IO::kTile);
         if constexpr (OP == kLayerNorm) {
-            mu = s / n;
-            m2 = 0.f;
+            mu = m2 / n;
+            s2 = f2(0.f);
 #pragma unroll
             for (int i = 0; i < kTilesPerWarp; ++i) {
-                const int64_t base = c0 + (int64_t)(warp + kWarps * i) * IO::kTile;
 #pragma unroll
-                for (int k = 0; k < IO::N; ++k) {
-                    const float e = IO::valid(base, lane, k, a.cols) ? h[i][k] - mu : 0.f;
-                    m2 = fmaf(e, e, m2);
+                for (int k = 0; k < IO::NP; ++k) {
+                    const F2 e =
+                        inside<false, IO>(add2(h[i][k], f2(-mu)), i * IO::kTile, k, left);
+                    s2 = fma2(e, e, s2);
                 }
             }
-            m2 = block_allreduce(m2, red[1], SumOp(), 0.f);
+            m2 = block_allreduce(s2.x + s2.y, red[1], SumOp(), 0.f);
         } else {
             __syncthreads();  // red[0] is rewritten by the next item
         }
@@ -98,61 +346,100 @@ template <int OP, typename T, typename IO, typename PT>
 __global__ void __launch_bounds__(kThreads) fwd_apply(NormFwdArgs a) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const DropStream d(a.drop);
-    const PT* gp = static_cast<const PT*>(a.gamma);
-    const PT* bp = static_cast<const PT*>(a.beta);
     const int64_t items = a.rows * a.nch;
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
         const int64_t row = it / a.nch;
-        const int64_t c0 = (it - row * a.nch) * (int64_t)(kChunkTiles * IO::kTile);
+        const int c0 = (int)(it - row * a.nch) * (kChunkTiles * IO::kTile);
         const NormPart st = merge_row<OP>(a.ws + row * a.nch * 4, a.nch, lane);
-        const float rstd = 1.f / sqrtf(st.m2 / (float)a.cols + a.eps);
-        if (c0 == 0 && threadIdx.x == 0) {
-            if (a.mean) a.mean[row] = st.mu;
-            if (a.rstd) a.rstd[row] = rstd;
-        }
-        const T* x = static_cast<const T*>(a.x) + row * a.cols;
-        const T* r = a.residual ? static_cast<const T*>(a.residual) + row * a.cols : nullptr;
-        T* y = static_cast<T*>(a.y) + row * a.cols;
-        T* ho = a.h ? static_cast<T*>(a.h) + row * a.cols : nullptr;
+        const int base0 = c0 + warp * kTilesPerWarp * IO::kTile;
+        const int j0 = base0 + IO::first(lane), left = a.cols - j0;
+        const int64_t at = row * a.cols + j0;
+        const T* x = static_cast<const T*>(a.x) + at;
+        const T* r = moved(static_cast<const T*>(a.residual), at);
+        F2 h[kTilesPerWarp][IO::NP];
 #pragma unroll
         for (int i = 0; i < kTilesPerWarp; ++i) {
-            const int64_t base = c0 + (int64_t)(warp + kWarps * i) * IO::kTile;
-            if (base >= a.cols) break;
-            float h[IO::N], g[IO::N], b[IO::N];
-            tile_h<T, IO>(x, r, a.drop.on, d, base, lane, (uint32_t)row, a.cols, h);
-            if (ho) IO::store(ho, base, lane, a.cols, Elem<T>::pack(h));
-            IO::template params<PT>(gp, base, lane, a.cols, g, 1.f);
-            IO::template params<PT>(bp, base, lane, a.cols, b, 0.f);
-#pragma unroll
-            for (int k = 0; k < IO::N; ++k) {
-                const float z = OP == kLayerNorm ? (h[k] - st.mu) * rstd : h[k] * rstd;
-                h[k] = fmaf(z, g[k], b[k]);
-            }
-            IO::store(y, base, lane, a.cols, Elem<T>::pack(h));
+            typename IO::R rv = {};
+            if (r) rv = IO::template load<false>(r, i * IO::kTile, left);
+            tile_h<T, IO>(IO::template load<false>(x, i * IO::kTile, left), rv, r != nullptr,
+                          a.drop.on && base0 + i * IO::kTile < a.cols, d, base0 + i * IO::kTile,
+                          lane, (uint32_t)row, h[i]);
+            if (a.h)
+                IO::template store<false>(static_cast<T*>(a.h) + at, i * IO::kTile, left, h[i]);
         }
+        const float rstd = finish(a, row, c0 == 0 && threadIdx.x == 0, st.mu, st.m2);
+        write_tiles<OP, T, IO, kTilesPerWarp, false>(
+            h, moved(static_cast<const PT*>(a.gamma), j0), moved(static_cast<const PT*>(a.beta), j0),
+            static_cast<T*>(a.y) + at, left, st.mu, rstd);
     }
 }
 
-template <int OP, typename T, typename IO>
-cudaError_t run_fwd(TrainKey k, const NormFwdArgs& a, int sms, cudaStream_t s) {
+template <int OP, typename T, typename IO, typename PT>
+cudaError_t run_general(const NormFwdArgs& a, int sms, cudaStream_t s) {
     const int64_t items = a.rows * a.nch;
     const unsigned grid = (unsigned)(items < (int64_t)sms * 32 ? items : (int64_t)sms * 32);
     fwd_stats<OP, T, IO><<<grid, kThreads, 0, s>>>(a);
-    if (k.pdtype == 0) fwd_apply<OP, T, IO, float><<<grid, kThreads, 0, s>>>(a);
-    else fwd_apply<OP, T, IO, bf16><<<grid, kThreads, 0, s>>>(a);
+    fwd_apply<OP, T, IO, PT><<<grid, kThreads, 0, s>>>(a);
     return cudaGetLastError();
+}
+
+template <int OP, typename T, typename IO, typename PT, int V>
+cudaError_t run_warp(const NormFwdArgs& a, int sms, cudaStream_t s) {
+    const int64_t want = (a.rows + kWarps - 1) / kWarps;
+    fwd_warp<OP, T, IO, PT, V>
+        <<<(unsigned)(want < sms * 8 ? want : sms * 8), kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <int OP, typename T, typename IO, typename PT, int V>
+cudaError_t run_ring(const NormFwdArgs& a, const RingPlan& p, cudaStream_t s) {
+    const void* fn = (const void*)fwd_ring<OP, T, IO, PT, V>;
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    unsigned* err = device_error_word();
+    const int clusters = ring_clusters(dev, fn, p, a.rows);
+    if (!err || clusters < 1) return cudaErrorInvalidConfiguration;
+    return launch_ring(fn, a, p, clusters, err, s);
+}
+
+template <int OP, typename T, typename IO, typename PT>
+cudaError_t run_fwd(const NormFwdArgs& a, int sms, cudaStream_t s) {
+    const int tiles = (a.cols + IO::kTile - 1) / IO::kTile;
+    if (tiles <= 1) return run_warp<OP, T, IO, PT, 1>(a, sms, s);
+    if (tiles <= 2) return run_warp<OP, T, IO, PT, 2>(a, sms, s);
+    if (tiles <= 4) return run_warp<OP, T, IO, PT, 4>(a, sms, s);
+    RingPlan p;
+    if (!plan_ring(tiles, sizeof(T), a.residual ? 2 : 1, a.rows, sms, &p))
+        return run_general<OP, T, IO, PT>(a, sms, s);
+    return p.V == 4 ? run_ring<OP, T, IO, PT, 4>(a, p, s) : run_ring<OP, T, IO, PT, 8>(a, p, s);
+}
+
+template <int OP, typename T, typename IO>
+cudaError_t pick_param(const NormFwdArgs& a, int sms, cudaStream_t s) {
+    return a.half ? run_fwd<OP, T, IO, bf16>(a, sms, s) : run_fwd<OP, T, IO, float>(a, sms, s);
 }
 
 template <int OP, typename T>
 cudaError_t pick_fwd(TrainKey k, const NormFwdArgs& a, int sms, cudaStream_t s) {
-    return k.vec ? run_fwd<OP, T, VecIO<T>>(k, a, sms, s) : run_fwd<OP, T, ElemIO<T>>(k, a, sms, s);
+    return k.vec ? pick_param<OP, T, VecIO<T, 4>>(a, sms, s)
+                 : pick_param<OP, T, ElemIO<T, 4>>(a, sms, s);
 }
 
 }  // namespace
 
-int train_chunks(int dtype, int64_t cols) {
-    const int64_t chunk = (int64_t)kChunkTiles * (dtype == 0 ? VecIO<float>::kTile : VecIO<bf16>::kTile);
+int train_chunks(int64_t cols) {
+    const int64_t chunk = (int64_t)kChunkTiles * VecIO<float, 4>::kTile;
     return (int)((cols + chunk - 1) / chunk);
+}
+
+int64_t norm_fwd_partials(int dtype, int64_t rows, int64_t cols, int sms) {
+    // the general form runs where the ring does not hold x and residual; a
+    // call without residual then has room it does not need
+    RingPlan p;
+    const int tiles = (int)((cols + VecIO<float, 4>::kTile - 1) / VecIO<float, 4>::kTile);
+    if (tiles <= 4 || plan_ring(tiles, dtype == 0 ? 4 : 2, 2, rows, sms, &p)) return 0;
+    return rows * train_chunks(cols) * 16;
 }
 
 cudaError_t launch_norm_fwd(TrainKey k, const NormFwdArgs& a, int sms, cudaStream_t s) {

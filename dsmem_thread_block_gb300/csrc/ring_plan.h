@@ -1,0 +1,51 @@
+// ring_plan.h -- launch shapes of the ring kernels (ring.cuh).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <cstddef>
+#include <cstdint>
+
+namespace credit {
+
+constexpr int kRingStages = 8;    // most stages
+constexpr int kRingWarps = 16;    // most warps of a CTA
+constexpr int kRingThreads = 32 * kRingWarps;
+
+struct RingShape {
+    int32_t tiles;      // warp tiles of a CTA's slice
+    int32_t stages;
+    int32_t room;       // bytes of one stream's slice in a stage
+    int32_t clusters;   // of the grid
+    unsigned* err;
+};
+
+struct RingPlan {
+    int V, W, P;        // tiles per warp, warps per CTA, CTAs per row
+    int most;           // most clusters of the grid
+    size_t smem;
+    RingShape shape;    // `clusters` and `err` are set by the launch
+};
+
+// A shape for rows of `tiles` warp tiles in `streams` streams of `es`-byte
+// elements; false where the rows are too wide.
+bool plan_ring(int tiles, int es, int streams, int64_t rows, int sms, RingPlan* out);
+
+// The clusters a launch of `fn` runs: as many as are resident, no more than
+// rows or plan.most, evened out so that none has a row more than it must.
+int ring_clusters(int dev, const void* fn, const RingPlan& p, int64_t rows);
+
+cudaError_t launch_ring_args(const void* fn, void** args, const RingPlan& p, int clusters,
+                             cudaStream_t s);
+
+// `clusters` CTA clusters of a ring kernel with arguments (Args, RingShape).
+template <typename Args>
+cudaError_t launch_ring(const void* fn, Args a, const RingPlan& p, int clusters, unsigned* err,
+                        cudaStream_t s) {
+    RingShape q = p.shape;
+    q.clusters = clusters;
+    q.err = err;
+    void* args[] = {&a, &q};
+    return launch_ring_args(fn, args, p, clusters, s);
+}
+
+}  // namespace credit

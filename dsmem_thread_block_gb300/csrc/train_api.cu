@@ -50,26 +50,28 @@ credit_status_t matrix_ok(int64_t rows, int64_t cols, credit_dtype_t dtype, uint
     const int64_t es = (int64_t)esize(dtype);
     if (rows > 0 && (rows > INT64_MAX / cols || rows * cols > INT64_MAX / es))
         return CREDIT_ERR_INVALID_ARG;
-    // chunks of a row are counted in 32 bits, and a launch grid covers its strips
-    if (cols > ((int64_t)1 << 40)) return CREDIT_ERR_INVALID_ARG;
+    if (cols > ((int64_t)1 << 30)) return CREDIT_ERR_INVALID_ARG;  // counted in 32 bits
     *bytes = (uint64_t)(rows * cols * es);
     return CREDIT_OK;
 }
 
 // A call's dropout: null or p = 0 is none.  The mask's counter holds the row
-// and a quarter of the column in 32 bits each.
-credit_status_t drop_args(const credit_dropout_t* d, int64_t rows, int64_t cols, DropArgs* a) {
+// in 32 bits.
+credit_status_t drop_args(const credit_dropout_t* d, int64_t rows, DropArgs* a) {
     *a = DropArgs{};
     a->scale = 1.f;
     if (!d) return CREDIT_OK;
     if (!(d->p >= 0.0 && d->p < 1.0)) return CREDIT_ERR_INVALID_ARG;
     if (!aligned(d->device_offset, 8)) return CREDIT_ERR_INVALID_ARG;
     if (d->p == 0.0) return CREDIT_OK;
-    if (rows > ((int64_t)1 << 32) || cols > ((int64_t)1 << 34)) return CREDIT_ERR_INVALID_ARG;
+    if (rows > ((int64_t)1 << 32)) return CREDIT_ERR_INVALID_ARG;
     a->on = 1;
     a->threshold = (uint32_t)(uint64_t)std::floor(d->p * 4294967296.0);
-    a->k0 = (uint32_t)d->seed;
-    a->k1 = (uint32_t)(d->seed >> 32);
+    // the key of a round is the last one's plus two constants
+    for (uint32_t i = 0; i < 10; ++i) {
+        a->key[2 * i] = (uint32_t)d->seed + i * 0x9E3779B9u;
+        a->key[2 * i + 1] = (uint32_t)(d->seed >> 32) + i * 0xBB67AE85u;
+    }
     a->offset = d->offset;
     a->device_offset = d->device_offset;
     a->scale = (float)(1.0 / (1.0 - d->p));
@@ -84,25 +86,10 @@ credit_status_t device(int* dev, const DevInfo** info) {
 
 credit_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? CREDIT_OK : CREDIT_ERR_CUDA; }
 
-// Workspace of a call: the row partials, then (backward) the groups' sums.
-struct Layout {
-    uint64_t partials, bytes;
-    int nch, groups;
-    int64_t group_rows;
-};
-
-Layout layout(bool backward, int64_t rows, int64_t cols, credit_dtype_t dtype, int sms) {
-    Layout l{};
-    l.nch = train_chunks((int)dtype, cols);
-    const uint64_t part = (uint64_t)rows * (uint64_t)l.nch * (backward ? 8 : 16);
-    l.partials = (part + 15) / 16 * 16;
-    l.bytes = l.partials;
-    l.group_rows = 1;
-    if (backward && rows > 0) {
-        l.groups = train_groups((int)dtype, rows, cols, sms, &l.group_rows);
-        l.bytes += (uint64_t)l.groups * 2 * (uint64_t)cols * 4;
-    }
-    return l;
+// Workspace bytes of a backward call with this layout: the row sums, then the
+// groups' sums.
+uint64_t bwd_bytes(const TrainLayout& l) {
+    return (uint64_t)(l.partials + 15) / 16 * 16 + (uint64_t)l.room_groups * 2 * (uint64_t)l.pitch * 4;
 }
 
 }  // namespace
@@ -118,7 +105,8 @@ credit_status_t credit_norm_workspace(credit_op_t op, int backward, int64_t rows
     if (st != CREDIT_OK) return st;
     const DevInfo* d = device_info(device);
     if (!d) return CREDIT_ERR_CUDA;
-    *bytes = (size_t)layout(backward != 0, rows, cols, dtype, d->sms).bytes;
+    *bytes = backward ? (size_t)bwd_bytes(norm_bwd_layout((int)dtype, rows, cols, d->sms))
+                      : (size_t)norm_fwd_partials((int)dtype, rows, cols, d->sms);
     return CREDIT_OK;
 }
 
@@ -129,7 +117,7 @@ credit_status_t credit_dropout(const void* x, const void* residual, void* y, int
     credit_status_t st = matrix_ok(rows, cols, dtype, &mb);
     if (st != CREDIT_OK) return st;
     DropoutArgs a{};
-    st = drop_args(drop, rows, cols, &a.drop);
+    st = drop_args(drop, rows, &a.drop);
     if (st != CREDIT_OK) return st;
     if (rows == 0) return CREDIT_OK;
     if (!x || !y) return CREDIT_ERR_INVALID_ARG;
@@ -165,7 +153,7 @@ credit_status_t credit_norm_forward(credit_op_t op, const void* x, const void* r
     if (!(eps >= 0.f)) return CREDIT_ERR_INVALID_ARG;
     if (op == CREDIT_RMSNORM && (beta || mean)) return CREDIT_ERR_INVALID_ARG;
     NormFwdArgs a{};
-    st = drop_args(drop, rows, cols, &a.drop);
+    st = drop_args(drop, rows, &a.drop);
     if (st != CREDIT_OK) return st;
     if (rows == 0) return CREDIT_OK;
     if (!x || !y) return CREDIT_ERR_INVALID_ARG;
@@ -182,17 +170,18 @@ credit_status_t credit_norm_forward(credit_op_t op, const void* x, const void* r
     const DevInfo* d;
     st = device(&dev, &d);
     if (st != CREDIT_OK) return st;
-    const Layout l = layout(false, rows, cols, dtype, d->sms);
-    if (l.bytes && (!workspace || workspace_bytes < l.bytes || !aligned(workspace, 16)))
+    const uint64_t need = (uint64_t)norm_fwd_partials((int)dtype, rows, cols, d->sms);
+    if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
         return CREDIT_ERR_INVALID_ARG;
     a.x = x; a.residual = residual; a.y = y; a.h = h;
     a.mean = mean; a.rstd = rstd; a.gamma = gamma; a.beta = beta;
-    a.rows = rows; a.cols = cols; a.eps = eps;
+    a.rows = rows; a.cols = (int32_t)cols; a.inv_cols = 1.f / (float)cols; a.eps = eps;
+    a.half = (gamma || beta) && param_dtype == CREDIT_BF16;
     a.ws = static_cast<float*>(workspace);
-    a.nch = l.nch;
+    a.nch = train_chunks(cols);
     const bool vec = aligned(x, 16) && aligned(y, 16) && aligned(residual, 16) && aligned(h, 16) &&
                      aligned(gamma, 16) && aligned(beta, 16) && (uint64_t)cols * es % 16 == 0;
-    const TrainKey k{(int)op, (int)dtype, (gamma || beta) ? (int)param_dtype : 0, vec};
+    const TrainKey k{(int)op, (int)dtype, vec};
     return from_cuda(launch_norm_fwd(k, a, d->sms, (cudaStream_t)stream));
 }
 
@@ -210,7 +199,7 @@ credit_status_t credit_norm_backward(credit_op_t op, const void* dy, const void*
     if (params && !dtype_ok(param_dtype)) return CREDIT_ERR_UNSUPPORTED;
     if (op == CREDIT_RMSNORM && (dbeta || mean)) return CREDIT_ERR_INVALID_ARG;
     NormBwdArgs a{};
-    st = drop_args(drop, rows, cols, &a.drop);
+    st = drop_args(drop, rows, &a.drop);
     if (st != CREDIT_OK) return st;
     if (rows == 0 && !dgamma && !dbeta) return CREDIT_OK;
     if (rows > 0 && (!dy || !h || !rstd || !dx || (op == CREDIT_LAYERNORM && !mean)))
@@ -230,20 +219,23 @@ credit_status_t credit_norm_backward(credit_op_t op, const void* dy, const void*
     const DevInfo* d;
     st = device(&dev, &d);
     if (st != CREDIT_OK) return st;
-    const Layout l = layout(true, rows, cols, dtype, d->sms);
-    if (l.bytes && (!workspace || workspace_bytes < l.bytes || !aligned(workspace, 16)))
+    const TrainLayout l = norm_bwd_layout((int)dtype, rows, cols, d->sms);
+    const uint64_t need = bwd_bytes(l);
+    if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
         return CREDIT_ERR_INVALID_ARG;
     a.dy = dy; a.dh = dh; a.h = h; a.mean = mean; a.rstd = rstd; a.gamma = gamma;
     a.dx = dx; a.dres = dresidual; a.dgamma = dgamma; a.dbeta = dbeta;
-    a.rows = rows; a.cols = cols;
+    a.rows = rows; a.cols = (int32_t)cols; a.inv_cols = 1.f / (float)cols;
+    a.half = params && param_dtype == CREDIT_BF16;
     a.ws = static_cast<float*>(workspace);
-    a.pws = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.partials);
+    a.pws = reinterpret_cast<float*>(static_cast<char*>(workspace) + (l.partials + 15) / 16 * 16);
+    a.pitch = l.pitch;
     a.nch = l.nch;
     a.groups = l.groups;
     a.group_rows = l.group_rows;
     const bool vec = aligned(dy, 16) && aligned(dh, 16) && aligned(h, 16) && aligned(dx, 16) &&
                      aligned(dresidual, 16) && aligned(gamma, 16) && (uint64_t)cols * es % 16 == 0;
-    const TrainKey k{(int)op, (int)dtype, params ? (int)param_dtype : 0, vec};
+    const TrainKey k{(int)op, (int)dtype, vec};
     return from_cuda(launch_norm_bwd(k, a, d->sms, (cudaStream_t)stream));
 }
 

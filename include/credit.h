@@ -272,7 +272,7 @@ credit_status_t credit_rmsnorm(const void *x, void *y, int64_t rows,
  *
  * forward, backward (with the parameters' gradients) and dropout alone.
  * Matrices are rows x cols of one `dtype` as above; unlike the operators
- * above, rows == 0 is a legal empty batch.  Arithmetic, row sums and the sums
+ * above, rows == 0 is a legal empty batch, and cols <= 2^30.  Arithmetic, row sums and the sums
  * over rows are fp32; every output is rounded once.  Results repeat bit for
  * bit: every sum has a fixed order.  Each call works entirely on `stream`
  * and may be captured; a workspace is used by one call at a time (two
@@ -291,7 +291,7 @@ credit_status_t credit_rmsnorm(const void *x, void *y, int64_t rows,
  *                  (modulo 2^64) when the kernel runs: a captured graph draws
  *                  a new mask at each replay when the word has moved on
  * Calls that must not share a mask differ in seed or offset.  rows <= 2^32
- * and cols <= 2^34 where p > 0.
+ * where p > 0.
  */
 typedef struct {
     double p;

@@ -120,6 +120,7 @@ def test_dropout_refusals():
     assert call(d=drop(device_offset=Y + 8)) == BAD       # inside the output
     assert call(x=X + 2) == BAD and call(y=Y + 1) == BAD and call(res=RES + 2) == BAD
     assert call(y=X + 4) == BAD and call(y=RES + 16) == BAD   # partial overlap
+    assert call(cols=(1 << 30) + 1, rows=1) == BAD
     assert call(rows=(1 << 32) + 1, cols=1) == BAD        # the mask's row counter
     assert call(x=0, res=0, y=0, rows=0) == C.OK          # an empty batch
 
