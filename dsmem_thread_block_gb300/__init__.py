@@ -17,9 +17,6 @@ raises instead of falling back to anything else.
 """
 from __future__ import annotations
 
-import contextlib
-import dataclasses
-
 from . import _credit as C
 from ._credit import CreditError, Plan  # noqa: F401
 
@@ -216,220 +213,19 @@ def pearson(x, u, eps: float = 0.0, out=None, r=None, plan: Plan | None = None, 
     return out, r
 
 
-# ------------------------------------------------------- training operators
-@dataclasses.dataclass(frozen=True)
-class Dropout:
-    """A dropout stream: drop probability 0 <= p < 1, a 64-bit seed and a
-    64-bit offset (calls that must not share a mask differ in one of them).
-    `device_offset`, an int64 CUDA tensor of one element, is added to the
-    offset when the kernel runs, so a captured graph draws a new mask at each
-    replay once the tensor has changed.  The backward call takes the forward
-    call's object."""
-    p: float
-    seed: int
-    offset: int = 0
-    device_offset: object = None
-
-    def __post_init__(self):
-        import torch
-        if not 0.0 <= self.p < 1.0:
-            raise ValueError("credit: dropout needs 0 <= p < 1")
-        for v in (self.seed, self.offset):
-            if not 0 <= v < 1 << 64:
-                raise ValueError("credit: dropout seed and offset are unsigned 64-bit integers")
-        d = self.device_offset
-        if d is not None and (d.dtype != torch.int64 or d.numel() != 1 or not d.is_cuda):
-            raise ValueError("credit: device_offset must be an int64 CUDA tensor of one element")
-        object.__setattr__(self, "_fields", C.dropout_fields(
-            self.p, self.seed, self.offset, d.data_ptr() if d is not None else 0))
+# The training operators live in train.py, loaded at first use (this module
+# imports torch only inside its calls).
+_TRAIN = ("Dropout", "dropout", "layernorm_forward", "layernorm_backward", "rmsnorm_forward",
+          "rmsnorm_backward")
 
 
-_ws_cache: dict = {}
-
-
-def _on(x):
-    """Launch on x's device, whatever the current one is."""
-    import torch
-    if torch.cuda.current_device() == x.device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(x.device)
-
-
-def _matrix(t, x, name):
-    if t is None:
-        return 0
-    if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device or not t.is_contiguous():
-        raise ValueError(f"credit: {name} must be a contiguous tensor shaped like the input, "
-                         "of its dtype and on its device")
-    return t.data_ptr()
-
-
-def _rowvec(t, x, rows, name):
-    import torch
-    if t is None:
-        raise ValueError(f"credit: {name} is required")
-    if t.dtype != torch.float32 or t.numel() != rows or t.device != x.device or \
-            not t.is_contiguous():
-        raise ValueError(f"credit: {name} must be a contiguous fp32 tensor on the input's device, "
-                         "one element per row")
-    return t.data_ptr()
-
-
-def _colvec(t, x, cols, name):
-    if t is None:
-        return 0
-    if t.numel() != cols or t.device != x.device:
-        raise ValueError(f"credit: {name} must have cols elements on the input's device")
-    return t.data_ptr()
-
-
-def _shape(x):
-    if not x.is_cuda or not x.is_contiguous():
-        raise ValueError("credit: inputs must be contiguous CUDA tensors")
-    if x.dim() < 1 or x.shape[-1] < 1:
-        raise ValueError("credit: the last dimension must hold at least one element")
-    cols = x.shape[-1]
-    return x.numel() // cols, cols
-
-
-def _drop(d, x):
-    if d is None:
-        return None
-    if d.device_offset is not None and d.device_offset.device != x.device:
-        raise ValueError("credit: device_offset must be on the input's device")
-    return d._fields
-
-
-def _norm_ws(op, backward, rows, cols, x, workspace):
-    import torch
-    key = (op, backward, rows, cols, x.dtype, x.device.index)
-    need = _ws_cache.get(key)
-    if need is None:
-        need = C.credit_norm_workspace(op, backward, rows, cols, _dtype(x.dtype), x.device.index)
-        if len(_ws_cache) >= 4096:
-            _ws_cache.clear()
-        _ws_cache[key] = need
-    if workspace is None:
-        if not need:
-            return None, 0, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    elif workspace.device != x.device or not workspace.is_contiguous():
-        raise ValueError("credit: workspace must be a contiguous tensor on the input's device")
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
-
-def dropout(x, drop: Dropout, residual=None, out=None):
-    """residual + dropout(x) with a mask drawn from the counter-based
-    generator and never stored.  On the incoming gradient, without residual,
-    it is its own backward pass."""
-    import torch
-    rows, cols = _shape(x)
-    rp = _matrix(residual, x, "residual")
-    if out is None:
-        out = torch.empty_like(x)
-    op = _matrix(out, x, "out")
-    with _on(x):
-        st = C.credit_dropout(x.data_ptr(), rp, op, rows, cols, _dtype(x.dtype), _drop(drop, x),
-                              _stream(x))
-    if st != C.OK:
-        raise CreditError(st, "credit_dropout")
-    return out
-
-
-def _norm_forward(op, x, gamma, beta, eps, residual, drop, out, h_out, workspace):
-    import torch
-    rows, cols = _shape(x)
-    gp, bp = _colvec(gamma, x, cols, "gamma"), _colvec(beta, x, cols, "beta")
-    rp = _matrix(residual, x, "residual")
-    pdtype = _pdtype(gamma, beta)
-    fields = _drop(drop, x)
-    if out is None:
-        out = torch.empty_like(x)
-    same = residual is None and (drop is None or drop.p == 0.0)
-    if h_out is None and not same:
-        h_out = torch.empty_like(x)
-    hp = _matrix(h_out, x, "h_out")
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) \
-        if op == C.LAYERNORM else None
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    ws, wp, wb = _norm_ws(op, False, rows, cols, x, workspace)
-    with _on(x):
-        st = C.credit_norm_forward(op, x.data_ptr(), rp, fields, _matrix(out, x, "out"), hp,
-                                   _ptr(mean), rstd.data_ptr(), rows, cols, _dtype(x.dtype), gp,
-                                   bp, pdtype, float(eps), wp, wb, _stream(x))
-    if st != C.OK:
-        raise CreditError(st, "credit_norm_forward")
-    return out, h_out if h_out is not None else x, mean, rstd
-
-
-def layernorm_forward(x, gamma=None, beta=None, eps: float = 1e-5, residual=None,
-                      dropout: Dropout | None = None, out=None, h_out=None, workspace=None):
-    """h = residual + dropout(x), y = LayerNorm(h) over the last dimension;
-    returns (y, h, mean, rstd): what layernorm_backward needs, mean and rstd
-    fp32, one per row.  Without residual and dropout h is x itself.  `out` and
-    `h_out` may each be x or residual (in place)."""
-    return _norm_forward(C.LAYERNORM, x, gamma, beta, eps, residual, dropout, out, h_out,
-                         workspace)
-
-
-def rmsnorm_forward(x, weight=None, eps: float = 1e-6, residual=None,
-                    dropout: Dropout | None = None, out=None, h_out=None, workspace=None):
-    """As layernorm_forward for RMSNorm; returns (y, h, rstd)."""
-    y, h, _, rstd = _norm_forward(C.RMSNORM, x, weight, None, eps, residual, dropout, out, h_out,
-                                  workspace)
-    return y, h, rstd
-
-
-def _norm_backward(op, dy, h, mean, rstd, gamma, dh, drop, need_dresidual, dx, dresidual,
-                   workspace):
-    import torch
-    rows, cols = _shape(dy)
-    hp, dhp = _matrix(h, dy, "h"), _matrix(dh, dy, "dh")
-    if h is None:
-        raise ValueError("credit: h is required")
-    mp = _rowvec(mean, dy, rows, "mean") if op == C.LAYERNORM else 0
-    sp = _rowvec(rstd, dy, rows, "rstd")
-    gp = _colvec(gamma, dy, cols, "gamma")
-    pdtype = _pdtype(gamma)
-    fields = _drop(drop, dy)
-    drops = drop is not None and drop.p > 0.0
-    if dx is None:
-        dx = torch.empty_like(dy)
-    if dresidual is None and need_dresidual and drops:
-        dresidual = torch.empty_like(dy)
-    dgamma = torch.empty_like(gamma) if gamma is not None else None
-    dbeta = torch.empty_like(gamma) if gamma is not None and op == C.LAYERNORM else None
-    ws, wp, wb = _norm_ws(op, True, rows, cols, dy, workspace)
-    with _on(dy):
-        st = C.credit_norm_backward(op, dy.data_ptr(), dhp, hp, mp, sp, gp, pdtype, fields,
-                                    _matrix(dx, dy, "dx"), _matrix(dresidual, dy, "dresidual"),
-                                    _ptr(dgamma), _ptr(dbeta), rows, cols, _dtype(dy.dtype), wp,
-                                    wb, _stream(dy))
-    if st != C.OK:
-        raise CreditError(st, "credit_norm_backward")
-    if dresidual is None and need_dresidual:
-        dresidual = dx  # without dropout the two gradients are one
-    return dx, dresidual, dgamma, dbeta
-
-
-def layernorm_backward(dy, h, mean, rstd, gamma=None, dh=None, dropout: Dropout | None = None,
-                       need_dresidual: bool = False, dx=None, dresidual=None, workspace=None):
-    """The gradient of layernorm_forward: from dy (of y) and dh (the gradient
-    that reaches h past the norm, or None), returns (dx, dresidual, dgamma,
-    dbeta).  dresidual is None unless asked for, and dx itself where there is
-    no dropout; dgamma and dbeta are None without gamma.  `dx` and `dresidual`
-    may each be dy, dh or h (in place)."""
-    return _norm_backward(C.LAYERNORM, dy, h, mean, rstd, gamma, dh, dropout, need_dresidual, dx,
-                          dresidual, workspace)
-
-
-def rmsnorm_backward(dy, h, rstd, weight=None, dh=None, dropout: Dropout | None = None,
-                     need_dresidual: bool = False, dx=None, dresidual=None, workspace=None):
-    """As layernorm_backward for rmsnorm_forward; returns (dx, dresidual,
-    dweight)."""
-    dx, dresidual, dweight, _ = _norm_backward(C.RMSNORM, dy, h, None, rstd, weight, dh, dropout,
-                                               need_dresidual, dx, dresidual, workspace)
-    return dx, dresidual, dweight
+def __getattr__(name):
+    if name in _TRAIN:
+        from . import train
+        for n in _TRAIN:
+            globals()[n] = getattr(train, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def device_error(device: int = 0) -> int:

@@ -339,8 +339,8 @@ def _drop_ptr(drop):
 
 def credit_dropout(x: int, residual: int, y: int, rows: int, cols: int, dtype: int, drop=None,
                    stream: int = 0) -> int:
-    return load().credit_dropout(x or None, residual or None, y or None, rows, cols, dtype,
-                                 _drop_ptr(drop), stream or None)
+    # (a zero passed for a void* is a null pointer)
+    return load().credit_dropout(x, residual, y, rows, cols, dtype, _drop_ptr(drop), stream)
 
 
 def credit_norm_workspace(op: int, backward: bool, rows: int, cols: int, dtype: int,
@@ -355,21 +355,18 @@ def credit_norm_forward(op: int, x: int, residual: int, drop, y: int, h: int, me
                         rows: int, cols: int, dtype: int, gamma: int, beta: int, param_dtype: int,
                         eps: float, workspace: int = 0, workspace_bytes: int = 0,
                         stream: int = 0) -> int:
-    return load().credit_norm_forward(op, x or None, residual or None, _drop_ptr(drop), y or None,
-                                      h or None, mean or None, rstd or None, rows, cols, dtype,
-                                      gamma or None, beta or None, param_dtype, eps,
-                                      workspace or None, workspace_bytes, stream or None)
+    return load().credit_norm_forward(op, x, residual, _drop_ptr(drop), y, h, mean, rstd, rows,
+                                      cols, dtype, gamma, beta, param_dtype, eps, workspace,
+                                      workspace_bytes, stream)
 
 
 def credit_norm_backward(op: int, dy: int, dh: int, h: int, mean: int, rstd: int, gamma: int,
                          param_dtype: int, drop, dx: int, dresidual: int, dgamma: int, dbeta: int,
                          rows: int, cols: int, dtype: int, workspace: int = 0,
                          workspace_bytes: int = 0, stream: int = 0) -> int:
-    return load().credit_norm_backward(op, dy or None, dh or None, h or None, mean or None,
-                                       rstd or None, gamma or None, param_dtype, _drop_ptr(drop),
-                                       dx or None, dresidual or None, dgamma or None,
-                                       dbeta or None, rows, cols, dtype, workspace or None,
-                                       workspace_bytes, stream or None)
+    return load().credit_norm_backward(op, dy, dh, h, mean, rstd, gamma, param_dtype,
+                                       _drop_ptr(drop), dx, dresidual, dgamma, dbeta, rows, cols,
+                                       dtype, workspace, workspace_bytes, stream)
 
 
 def credit_two_pass_noalloc(op: int, x: int, y: int, rows: int, cols: int, dtype: int,

@@ -175,33 +175,87 @@ __global__ void __launch_bounds__(kThreads) bwd_warp(NormBwdArgs a) {
     }
 }
 
-// Both sums over the lanes of each half warp.
-template <int OP> __device__ __forceinline__ void sum16(float& a, float& b) {
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        if constexpr (OP == kLayerNorm) b += __shfl_xor_sync(0xffffffffu, b, o);
+// Two row sums of R rows over the warp, value (row j, sum i) in the lanes of
+// group 2 j + i (of 8 lanes; R = 1: of 16, j = 0): the lanes halve the values
+// they carry before the last steps add over their group.
+template <int R>
+__device__ __forceinline__ float sums_over_warp(const float (&t)[R][2], int lane) {
+    float v;
+    if constexpr (R == 2) {
+        const bool up = lane & 16;
+        const float a = (up ? t[1][0] : t[0][0]) + __shfl_xor_sync(0xffffffffu, up ? t[0][0] : t[1][0], 16);
+        const float b = (up ? t[1][1] : t[0][1]) + __shfl_xor_sync(0xffffffffu, up ? t[0][1] : t[1][1], 16);
+        const bool hi = lane & 8;
+        v = (hi ? b : a) + __shfl_xor_sync(0xffffffffu, hi ? a : b, 8);
+    } else {
+        const bool up = lane & 16;
+        v = (up ? t[0][1] : t[0][0]) + __shfl_xor_sync(0xffffffffu, up ? t[0][0] : t[0][1], 16);
+        v += __shfl_xor_sync(0xffffffffu, v, 8);
     }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// The totals of up to 16 parts of R rows' two sums (`parts`: value-major,
+// kRingWarps apart), in every lane.
+template <int R>
+__device__ __forceinline__ void merge_sums(const float* parts, int count, int lane,
+                                           float (&t)[R][2]) {
+    const int g = R == 2 ? lane >> 3 : lane >> 4, at = lane & (R == 2 ? 7 : 15);
+    float v = at < count ? parts[g * kRingWarps + at] : 0.f;
+    if constexpr (R == 2) {
+        if (at + 8 < count) v += parts[g * kRingWarps + at + 8];
+    } else {
+        v += __shfl_xor_sync(0xffffffffu, v, 8);
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            t[j][i] = __shfl_sync(0xffffffffu, v, (2 * j + i) * (R == 2 ? 8 : 16));
+}
+
+// The same over the CTAs' deposits (one float4 a CTA: its rows' sums in turn).
+template <int R>
+__device__ __forceinline__ void merge_sums_cluster(const float4* parts, int count, int lane,
+                                                   float (&t)[R][2]) {
+    const int g = R == 2 ? lane >> 3 : lane >> 4, at = lane & (R == 2 ? 7 : 15);
+    const float* p = reinterpret_cast<const float*>(parts) + g;
+    float v = at < count ? p[4 * at] : 0.f;
+    if constexpr (R == 2) {
+        if (at + 8 < count) v += p[4 * (at + 8)];
+    } else {
+        v += __shfl_xor_sync(0xffffffffu, v, 8);
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            t[j][i] = __shfl_sync(0xffffffffu, v, (2 * j + i) * (R == 2 ? 8 : 16));
 }
 
 // ------------------------------------------------- a CTA or a cluster per row
-template <int OP, typename T, typename IO, typename PT, int V>
+// Warp w of a CTA owns the V tiles from column c0 + 128 V w on, of R rows at a
+// time.  A stage is read twice, before and after its rows' sums are known.
+template <int OP, typename T, typename IO, typename PT, int V, int R>
 __global__ void __launch_bounds__(kRingThreads) bwd_ring(NormBwdArgs a, RingShape q) {
     extern __shared__ __align__(128) unsigned char ring[];
     __shared__ __align__(8) uint64_t full[kRingStages];
-    __shared__ float2 wred[2][kRingWarps];
+    __shared__ float wred[2][2 * R][kRingWarps];
     __shared__ RingExchange ex;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
     const uint32_t P = cluster_nctarank(), rank = cluster_ctarank();
-    const int64_t first = blockIdx.x / P;
+    const int64_t first = (int64_t)(blockIdx.x / P) * R, stride = (int64_t)q.clusters * R;
     const int c0 = (int)rank * q.tiles * IO::kTile;
     const int c1 = min(a.cols, c0 + q.tiles * IO::kTile);
     const int bytes = (c1 - c0) * (int)sizeof(T);
     const void* const src[3] = {a.dy, a.h, a.dh};
-    const int ns = a.dh ? 3 : 2;
-    const int64_t total = a.rows * a.cols * (int64_t)sizeof(T);
-    auto offset = [&](int64_t row) { return (row * a.cols + c0) * (int64_t)sizeof(T); };
-    auto stage = [&](int s) { return ring + s * ns * q.room; };
+    const int ns = a.dh ? 3 : 2, stage_bytes = ns * R * q.room;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < q.stages; ++s) mbar_init(smem_u32(&full[s]), 1);
@@ -214,97 +268,125 @@ __global__ void __launch_bounds__(kRingThreads) bwd_ring(NormBwdArgs a, RingShap
         cluster_arrive_release();
         cluster_wait_acquire();
     }
+    auto issue = [&](int64_t row, int s) {
+        if (row < a.rows)
+            ring_issue<3, R, T, IO>(src, ns, row, a.rows, a.cols, c0, bytes, ring + s * stage_bytes,
+                                    q.room, smem_u32(&full[s]));
+    };
     if (threadIdx.x == 0)
-        for (int s = 0; s < q.stages; ++s) {
-            const int64_t row = first + (int64_t)s * q.clusters;
-            if (row < a.rows)
-                ring_issue<3, T, IO>(src, ns, offset(row), bytes, total, stage(s), q.room,
-                                     smem_u32(&full[s]));
-        }
+        for (int s = 0; s < q.stages; ++s) issue(first + s * stride, s);
 
     const DropStream d(a.drop);
     const int base0 = c0 + warp * V * IO::kTile, j0 = base0 + IO::first(lane), left = c1 - j0;
     const bool whole = base0 + V * IO::kTile <= c1;
     const PT* const gp = moved(static_cast<const PT*>(a.gamma), j0);
+    T* dx = static_cast<T*>(a.dx) + first * a.cols + j0;
+    T* dres = moved(static_cast<T*>(a.dres), first * a.cols + j0);
     F2 ag[V][IO::NP], ab[V][IO::NP];
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int k = 0; k < IO::NP; ++k) ag[i][k] = ab[i][k] = f2(0.f);
-    RowStats next = row_stats<OP>(a, first);
+        for (int e = 0; e < IO::NP; ++e) ag[i][e] = ab[i][e] = f2(0.f);
+    RowStats next[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) next[j] = row_stats<OP>(a, first + j);
     int s = 0;
-    uint32_t phase = 0;
-    int64_t k = 0;
-    for (int64_t row = first; row < a.rows; row += q.clusters, ++k) {
-        const RowStats r = next;
-        next = row_stats<OP>(a, row + q.clusters);
+    uint32_t phase = 0, k = 0;
+    for (int64_t row = first; row < a.rows; row += stride, ++k) {
+        RowStats r[R];
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            r[j] = next[j];
+            next[j] = row_stats<OP>(a, row + stride + j);
+        }
+        const bool both = R > 1 && row + 1 < a.rows;
+        const unsigned char* const stage = ring + s * stage_bytes;
         mbar_wait_bounded(smem_u32(&full[s]), phase, q.err);
-        const int64_t off = offset(row);
-        const T* const ys = reinterpret_cast<const T*>(stage(s) + ring_shift<IO>(a.dy, off)) + (j0 - c0);
-        const T* const hs = reinterpret_cast<const T*>(stage(s) + q.room + ring_shift<IO>(a.h, off)) +
-                            (j0 - c0);
-        const T* const ds = reinterpret_cast<const T*>(stage(s) + 2 * q.room +
-                                                       ring_shift<IO>(a.dh, off)) + (j0 - c0);
-        F2 s1 = f2(0.f), s2 = f2(0.f);
+        // row j's slice of stream i, at the lane's first column
+        auto slice = [&](int i, int j, const void* p) {
+            const int64_t off = ((row + j) * a.cols + c0) * (int64_t)sizeof(T);
+            return reinterpret_cast<const T*>(stage + (i * R + j) * q.room + ring_shift<IO>(p, off)) +
+                   (j0 - c0);
+        };
+        const T *ys[R], *hs[R], *ds[R];
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            ys[j] = slice(0, j, a.dy);
+            hs[j] = slice(1, j, a.h);
+            ds[j] = slice(2, j, a.dh);
+        }
+        F2 s1[R], s2[R];
+#pragma unroll
+        for (int j = 0; j < R; ++j) s1[j] = s2[j] = f2(0.f);
         auto take = [&](auto f) {
             constexpr bool FULL = decltype(f)::value;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                F2 u[IO::NP], h[IO::NP], g[IO::NP];
-                unpack<T, IO::NP>(IO::template staged<FULL>(ys, i * IO::kTile, left), u);
-                unpack<T, IO::NP>(IO::template staged<FULL>(hs, i * IO::kTile, left), h);
+                F2 g[IO::NP];
                 IO::template params<FULL>(gp, i * IO::kTile, left, g, 1.f);
-                tile_sums<OP, IO::NP>(u, h, g, r, s1, s2, ag[i], ab[i]);
+#pragma unroll
+                for (int j = 0; j < R; ++j) {
+                    if (j > 0 && !both) break;
+                    F2 u[IO::NP], h[IO::NP];
+                    unpack<T, IO::NP>(IO::template staged<FULL>(ys[j], i * IO::kTile, left), u);
+                    unpack<T, IO::NP>(IO::template staged<FULL>(hs[j], i * IO::kTile, left), h);
+                    tile_sums<OP, IO::NP>(u, h, g, r[j], s1[j], s2[j], ag[i], ab[i]);
+                }
             }
         };
         if (whole) take(std::true_type()); else take(std::false_type());
-        float t1 = warp_allreduce(s1.x + s1.y, SumOp());
-        float t2 = OP == kLayerNorm ? warp_allreduce(s2.x + s2.y, SumOp()) : 0.f;
-        if (lane == 0) wred[k & 1][warp] = make_float2(t1, t2);
+        float t[R][2];
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            t[j][0] = s1[j].x + s1[j].y;
+            t[j][1] = s2[j].x + s2[j].y;
+        }
+        const float v = sums_over_warp<R>(t, lane);
+        constexpr int G = R == 2 ? 8 : 16;  // lanes of a value's group
+        if (lane % G == 0) wred[k & 1][lane / G][warp] = v;
         __syncthreads();
-        // every thread has left the previous row: refill its stage
-        if (threadIdx.x == 0 && k > 0 && q.stages > 1) {
-            const int64_t fill = row + (int64_t)(q.stages - 1) * q.clusters;
-            const int sp = s == 0 ? q.stages - 1 : s - 1;
-            if (fill < a.rows)
-                ring_issue<3, T, IO>(src, ns, offset(fill), bytes, total, stage(sp), q.room,
-                                     smem_u32(&full[sp]));
-        }
-        const int l16 = lane & 15;
-        t1 = l16 < W ? wred[k & 1][l16].x : 0.f;
-        t2 = l16 < W ? wred[k & 1][l16].y : 0.f;
-        sum16<OP>(t1, t2);
+        // every thread has left the previous turn: refill its stage
+        if (threadIdx.x == 0 && k > 0 && q.stages > 1)
+            issue(row + (q.stages - 1) * stride, s == 0 ? q.stages - 1 : s - 1);
+        merge_sums<R>(&wred[k & 1][0][0], W, lane, t);
         if (P > 1) {
-            const float4* parts = ex.all(k, make_float4(t1, t2, 0.f, 0.f), P, rank, q.err);
-            t1 = l16 < (int)P ? parts[l16].x : 0.f;
-            t2 = l16 < (int)P ? parts[l16].y : 0.f;
-            sum16<OP>(t1, t2);
+            const float4* parts =
+                ex.all(k, make_float4(t[0][0], t[0][1], t[R - 1][0], t[R - 1][1]), P, rank, q.err);
+            merge_sums_cluster<R>(parts, (int)P, lane, t);
         }
-        t1 *= a.inv_cols;
-        t2 *= a.inv_cols;
-        T* const dx = static_cast<T*>(a.dx) + row * a.cols + j0;
-        T* const dres = moved(static_cast<T*>(a.dres), row * a.cols + j0);
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            t[j][0] *= a.inv_cols;
+            t[j][1] *= a.inv_cols;
+        }
         auto give = [&](auto f) {
             constexpr bool FULL = decltype(f)::value;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                F2 u[IO::NP], h[IO::NP], g[IO::NP], dh[IO::NP];
-                unpack<T, IO::NP>(IO::template staged<FULL>(ys, i * IO::kTile, left), u);
-                unpack<T, IO::NP>(IO::template staged<FULL>(hs, i * IO::kTile, left), h);
-                if (ns > 2) unpack<T, IO::NP>(IO::template staged<FULL>(ds, i * IO::kTile, left), dh);
+                F2 g[IO::NP];
                 IO::template params<FULL>(gp, i * IO::kTile, left, g, 1.f);
-                tile_out<OP, T, IO, FULL>(d, u, h, g, ns > 2 ? dh : nullptr, r, t1, t2, row,
-                                          base0 + i * IO::kTile, i * IO::kTile, left, lane,
-                                          a.drop.on && (FULL || base0 + i * IO::kTile < c1), dx,
-                                          dres);
+#pragma unroll
+                for (int j = 0; j < R; ++j) {
+                    if (j > 0 && !both) break;
+                    F2 u[IO::NP], h[IO::NP], dh[IO::NP];
+                    unpack<T, IO::NP>(IO::template staged<FULL>(ys[j], i * IO::kTile, left), u);
+                    unpack<T, IO::NP>(IO::template staged<FULL>(hs[j], i * IO::kTile, left), h);
+                    if (ns > 2)
+                        unpack<T, IO::NP>(IO::template staged<FULL>(ds[j], i * IO::kTile, left), dh);
+                    tile_out<OP, T, IO, FULL>(d, u, h, g, ns > 2 ? dh : nullptr, r[j], t[j][0],
+                                              t[j][1], row + j, base0 + i * IO::kTile, i * IO::kTile,
+                                              left, lane,
+                                              a.drop.on && (FULL || base0 + i * IO::kTile < c1),
+                                              dx + j * a.cols, moved(dres, j * a.cols));
+                }
             }
         };
         if (whole) give(std::true_type()); else give(std::false_type());
-        if (q.stages == 1) {  // nowhere to fetch ahead: the next row comes now
+        dx += stride * a.cols;
+        if (dres) dres += stride * a.cols;
+        if (q.stages == 1) {  // nowhere to fetch ahead: the next turn comes now
             __syncthreads();
-            if (threadIdx.x == 0 && row + q.clusters < a.rows)
-                ring_issue<3, T, IO>(src, ns, offset(row + q.clusters), bytes, total, stage(0),
-                                     q.room, smem_u32(&full[0]));
+            if (threadIdx.x == 0) issue(row + stride, 0);
         }
         if (++s == q.stages) {
             s = 0;
@@ -313,7 +395,7 @@ __global__ void __launch_bounds__(kRingThreads) bwd_ring(NormBwdArgs a, RingShap
     }
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        tile_params<OP, IO>(a, first, j0, i * IO::kTile, left, ag[i], ab[i]);
+        tile_params<OP, IO>(a, blockIdx.x / P, j0, i * IO::kTile, left, ag[i], ab[i]);
     if (P > 1) {  // no CTA leaves while a peer's deposit to it may be in flight
         cluster_arrive_release();
         cluster_wait_acquire();
@@ -459,15 +541,13 @@ cudaError_t run_warp(const NormBwdArgs& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-template <int OP, typename T, typename IO, typename PT, int V>
+template <int OP, typename T, typename IO, typename PT, int V, int R>
 cudaError_t run_ring(NormBwdArgs& a, const RingPlan& p, cudaStream_t s) {
-    const void* fn = (const void*)bwd_ring<OP, T, IO, PT, V>;
-    int dev = 0;
-    const cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    unsigned* err = device_error_word();
-    a.groups = ring_clusters(dev, fn, p, a.rows);  // at most the layout's
-    if (!err || a.groups < 1) return cudaErrorInvalidConfiguration;
+    const void* fn = (const void*)bwd_ring<OP, T, IO, PT, V, R>;
+    int resident;
+    unsigned* err;
+    if (!ring_resident(fn, p, &resident, &err)) return cudaErrorInvalidConfiguration;
+    a.groups = ring_grid(p, resident, a.rows);  // at most the layout's
     return launch_ring(fn, a, p, a.groups, err, s);
 }
 
@@ -480,7 +560,8 @@ cudaError_t run_bwd(NormBwdArgs& a, int sms, cudaStream_t s) {
     RingPlan p;
     if (!plan_ring(tiles, sizeof(T), a.dh ? 3 : 2, a.rows, sms, &p))
         return run_general<OP, T, IO, PT>(a, sms, s);
-    return p.V == 4 ? run_ring<OP, T, IO, PT, 4>(a, p, s) : run_ring<OP, T, IO, PT, 8>(a, p, s);
+    if (p.V == 8) return run_ring<OP, T, IO, PT, 8, 1>(a, p, s);
+    return p.R == 2 ? run_ring<OP, T, IO, PT, 4, 2>(a, p, s) : run_ring<OP, T, IO, PT, 4, 1>(a, p, s);
 }
 
 template <int OP, typename T, typename IO>

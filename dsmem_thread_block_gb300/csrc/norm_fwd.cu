@@ -30,33 +30,6 @@ __device__ __forceinline__ F2 normed(F2 h, float mu, float rstd, F2 g, F2 b) {
     return fma2(z, g, b);
 }
 
-// Merge `count` <= 16 parts (n, sum, mean, M2 about that mean) of a row's
-// pieces, the same in every lane; `part`: the pieces are not the whole row,
-// whose mean is sum / n (else sum inv_cols).
-template <int OP>
-__device__ __forceinline__ void merge_parts(const float4* parts, int count, int lane, bool part,
-                                            float inv_cols, float& n, float& s, float& mu,
-                                            float& m2) {
-    const int at = lane & 15;
-    const float4 q = at < count ? parts[at] : make_float4(0.f, 0.f, 0.f, 0.f);
-    m2 = q.w;
-    if constexpr (OP == kLayerNorm) {
-        s = q.y;
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        mu = s * inv_cols;
-        if (part) {
-            n = q.x;
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-            mu = __fdividef(s, n);
-        }
-        m2 = fmaf(q.x * (q.z - mu), q.z - mu, m2);
-    }
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
-}
-
 // A warp's part of a row from its V tiles' h (zeros past the end): the sum,
 // the mean sum inv_n, and M2 about it.
 template <int OP, typename IO, int V, bool FULL>
@@ -160,25 +133,22 @@ __global__ void __launch_bounds__(kThreads) fwd_warp(NormFwdArgs a) {
 }
 
 // ------------------------------------------------- a CTA or a cluster per row
-// Warp w of a CTA holds the V tiles from column c0 + 128 V w on: every address
-// of a row is one register plus a constant.
-template <int OP, typename T, typename IO, typename PT, int V>
+// Warp w of a CTA holds the V tiles from column c0 + 128 V w on, of R rows at
+// a time: every address of a turn is one register plus a constant.
+template <int OP, typename T, typename IO, typename PT, int V, int R>
 __global__ void __launch_bounds__(kRingThreads) fwd_ring(NormFwdArgs a, RingShape q) {
     extern __shared__ __align__(128) unsigned char ring[];
     __shared__ __align__(8) uint64_t full[kRingStages];
-    __shared__ float4 wred[2][kRingWarps];
+    __shared__ float2 wred[2][R][kRingWarps];
     __shared__ RingExchange ex;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
     const uint32_t P = cluster_nctarank(), rank = cluster_ctarank();
-    const int64_t first = blockIdx.x / P;
-    const int c0 = (int)rank * q.tiles * IO::kTile;               // the slice's columns
-    const int c1 = min(a.cols, c0 + q.tiles * IO::kTile);
+    const int64_t first = (int64_t)(blockIdx.x / P) * R, stride = (int64_t)q.clusters * R;
+    const int slice = q.tiles * IO::kTile;
+    const int c0 = (int)rank * slice, c1 = min(a.cols, c0 + slice);  // the slice's columns
     const int bytes = (c1 - c0) * (int)sizeof(T);
     const void* const src[2] = {a.x, a.residual};
-    const int ns = a.residual ? 2 : 1;
-    const int64_t total = a.rows * a.cols * (int64_t)sizeof(T);
-    auto offset = [&](int64_t row) { return (row * a.cols + c0) * (int64_t)sizeof(T); };
-    auto stage = [&](int s) { return ring + s * ns * q.room; };
+    const int ns = a.residual ? 2 : 1, stage_bytes = ns * R * q.room;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < q.stages; ++s) mbar_init(smem_u32(&full[s]), 1);
@@ -192,67 +162,148 @@ __global__ void __launch_bounds__(kRingThreads) fwd_ring(NormFwdArgs a, RingShap
         cluster_wait_acquire();
     }
     if (threadIdx.x == 0)
-        for (int s = 0; s < q.stages; ++s) {
-            const int64_t row = first + (int64_t)s * q.clusters;
-            if (row < a.rows)
-                ring_issue<2, T, IO>(src, ns, offset(row), bytes, total, stage(s), q.room,
-                                     smem_u32(&full[s]));
-        }
+        for (int s = 0; s < q.stages; ++s)
+            if (first + s * stride < a.rows)
+                ring_issue<2, R, T, IO>(src, ns, first + s * stride, a.rows, a.cols, c0, bytes,
+                                        ring + s * stage_bytes, q.room, smem_u32(&full[s]));
 
     const DropStream d(a.drop);
     const int base0 = c0 + warp * V * IO::kTile, j0 = base0 + IO::first(lane), left = c1 - j0;
     const bool whole = base0 + V * IO::kTile <= c1;
-    const float n = (float)max(0, min(c1 - base0, V * IO::kTile));
-    const float inv_n = 1.f / fmaxf(n, 1.f);
     const PT* const gp = moved(static_cast<const PT*>(a.gamma), j0);
     const PT* const bp = moved(static_cast<const PT*>(a.beta), j0);
+    // columns of this warp, of the warp and of the CTA that this lane merges
+    const int part = lane & 15;
+    const float inv_warp = 1.f / (float)max(1, min(c1 - base0, V * IO::kTile));
+    const float wn = (float)max(0, min(c1 - (c0 + part * V * IO::kTile), V * IO::kTile));
+    const float cn = (float)max(0, min(a.cols - part * slice, slice));
+    const float inv_wn = 1.f / fmaxf(wn, 1.f), inv_cn = 1.f / fmaxf(cn, 1.f);
+    const float inv_cta = P > 1 ? 1.f / (float)(c1 - c0) : a.inv_cols;
+    T* ho = moved(static_cast<T*>(a.h), first * a.cols + j0);
+    T* yo = static_cast<T*>(a.y) + first * a.cols + j0;
     int s = 0;
-    uint32_t phase = 0;
-    int64_t k = 0;
-    for (int64_t row = first; row < a.rows; row += q.clusters, ++k) {
-        const int64_t off = offset(row), out = row * a.cols + j0;
-        F2 h[V][IO::NP];
-        float sum = 0.f, mu = 0.f, m2, cn;
+    uint32_t phase = 0, k = 0;
+    for (int64_t row = first; row < a.rows; row += stride, ++k) {
+        F2 h[R][V][IO::NP];
+        float v[R];
+        const bool both = R > 1 && row + 1 < a.rows;
+        unsigned char* const stage = ring + s * stage_bytes;
         mbar_wait_bounded(smem_u32(&full[s]), phase, q.err);
+        float mean[R], m2;
         auto take = [&](auto f) {
             constexpr bool FULL = decltype(f)::value;
-            const T* xs = reinterpret_cast<const T*>(stage(s) + ring_shift<IO>(a.x, off)) + (j0 - c0);
-            const T* rs = reinterpret_cast<const T*>(stage(s) + q.room +
-                                                     ring_shift<IO>(a.residual, off)) + (j0 - c0);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                typename IO::R rv = {};
-                if (ns > 1) rv = IO::template staged<FULL>(rs, i * IO::kTile, left);
-                tile_h<T, IO>(IO::template staged<FULL>(xs, i * IO::kTile, left), rv, ns > 1,
-                              a.drop.on && (FULL || base0 + i * IO::kTile < c1), d,
-                              base0 + i * IO::kTile, lane, (uint32_t)row, h[i]);
-            }
-            if (a.h) {
-                T* const ho = static_cast<T*>(a.h) + out;
+            for (int j = 0; j < R; ++j) {
+                const int64_t off = ((row + j) * a.cols + c0) * (int64_t)sizeof(T);
+                const T* xs = reinterpret_cast<const T*>(stage + j * q.room +
+                                                         ring_shift<IO>(a.x, off)) + (j0 - c0);
+                const T* rs = reinterpret_cast<const T*>(stage + (R + j) * q.room +
+                                                         ring_shift<IO>(a.residual, off)) + (j0 - c0);
+                F2 t = f2(0.f);
 #pragma unroll
-                for (int i = 0; i < V; ++i) IO::template store<FULL>(ho, i * IO::kTile, left, h[i]);
+                for (int i = 0; i < V; ++i) {
+                    typename IO::R rv = {};
+                    if (ns > 1) rv = IO::template staged<FULL>(rs, i * IO::kTile, left);
+                    tile_h<T, IO>(IO::template staged<FULL>(xs, i * IO::kTile, left), rv, ns > 1,
+                                  a.drop.on && (FULL || base0 + i * IO::kTile < c1), d,
+                                  base0 + i * IO::kTile, lane, (uint32_t)(row + j), h[j][i]);
+#pragma unroll
+                    for (int e = 0; e < IO::NP; ++e)
+                        t = OP == kLayerNorm ? add2(t, h[j][i][e]) : fma2(h[j][i][e], h[j][i][e], t);
+                }
+                if (ho && (j == 0 || both)) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        IO::template store<FULL>(ho + j * a.cols, i * IO::kTile, left, h[j][i]);
+                }
+                v[j] = t.x + t.y;
             }
-            warp_part<OP, IO, V, FULL>(h, left, inv_n, sum, mu, m2);
+            m2 = row_sum<R>(v, lane);  // LayerNorm: the sum; RMSNorm: the sum of squares
+            if constexpr (OP == kLayerNorm) {
+                spread<R>(m2 * inv_warp, lane, mean);
+#pragma unroll
+                for (int j = 0; j < R; ++j) {
+                    F2 t = f2(0.f);
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+#pragma unroll
+                        for (int e = 0; e < IO::NP; ++e) {
+                            F2 z = add2(h[j][i][e], f2(-mean[j]));
+                            if constexpr (!FULL) z = inside<FULL, IO>(z, i * IO::kTile, e, left);
+                            t = fma2(z, z, t);
+                        }
+                    v[j] = t.x + t.y;
+                }
+            }
         };
         if (whole) take(std::true_type()); else take(std::false_type());
-        if (lane == 0) wred[k & 1][warp] = make_float4(n, sum, mu, m2);
+        {   // the warp's (sum, M2 about its mean) of each row
+            const float sum = m2;
+            if constexpr (OP == kLayerNorm) m2 = row_sum<R>(v, lane);
+            if ((lane & 15) == 0 && (R > 1 || lane == 0))
+                wred[k & 1][R > 1 ? lane >> 4 : 0][warp] = make_float2(sum, m2);
+        }
         __syncthreads();
-        // every thread has read the stage: bring the row that comes next in it
+        // every thread has read the stage: bring the turn that comes next in it
         if (threadIdx.x == 0) {
-            const int64_t next = row + (int64_t)q.stages * q.clusters;
+            const int64_t next = row + q.stages * stride;
             if (next < a.rows)
-                ring_issue<2, T, IO>(src, ns, offset(next), bytes, total, stage(s), q.room,
-                                     smem_u32(&full[s]));
+                ring_issue<2, R, T, IO>(src, ns, next, a.rows, a.cols, c0, bytes, stage, q.room,
+                                        smem_u32(&full[s]));
         }
-        merge_parts<OP>(wred[k & 1], W, lane, P > 1, a.inv_cols, cn, sum, mu, m2);
+        const int mine = R > 1 ? lane >> 4 : 0;  // the row this half warp merges
+        float2 w = part < W ? wred[k & 1][mine][part] : make_float2(0.f, 0.f);
+        float sum = 0.f, mu = 0.f;
+        if constexpr (OP == kLayerNorm) {
+            sum = half_sum(w.x);
+            mu = sum * inv_cta;
+            const float e = fmaf(w.x, inv_wn, -mu);
+            w.y = fmaf(wn * e, e, w.y);
+        }
+        m2 = half_sum(w.y);
         if (P > 1) {
-            const float4* parts = ex.all(k, make_float4(cn, sum, mu, m2), P, rank, q.err);
-            merge_parts<OP>(parts, (int)P, lane, false, a.inv_cols, cn, sum, mu, m2);
+            float t0[R], t1[R];
+            spread<R>(sum, lane, t0);
+            spread<R>(m2, lane, t1);
+            const float4* parts = ex.all(k, make_float4(t0[0], t1[0], t0[R - 1], t1[R - 1]), P, rank,
+                                         q.err);
+            const float4 c = part < (int)P ? parts[part] : make_float4(0.f, 0.f, 0.f, 0.f);
+            w = mine ? make_float2(c.z, c.w) : make_float2(c.x, c.y);
+            if constexpr (OP == kLayerNorm) {
+                mu = half_sum(w.x) * a.inv_cols;
+                const float e = fmaf(w.x, inv_cn, -mu);
+                w.y = fmaf(cn * e, e, w.y);
+            }
+            m2 = half_sum(w.y);
         }
-        const float rstd = finish(a, row, rank == 0 && threadIdx.x == 0, mu, m2);
-        T* const y = static_cast<T*>(a.y) + out;
-        if (whole) write_tiles<OP, T, IO, V, true>(h, gp, bp, y, left, mu, rstd);
-        else write_tiles<OP, T, IO, V, false>(h, gp, bp, y, left, mu, rstd);
+        const float own = rsqrtf(fmaf(m2, a.inv_cols, a.eps));
+        if (rank == 0 && warp == 0 && (lane & 15) == 0 && (lane == 0 || both)) {
+            if (a.mean) a.mean[row + (lane >> 4)] = mu;
+            if (a.rstd) a.rstd[row + (lane >> 4)] = own;
+        }
+        float rstd[R];
+        spread<R>(own, lane, rstd);
+        if constexpr (OP == kLayerNorm) spread<R>(mu, lane, mean);
+        auto give = [&](auto f) {
+            constexpr bool FULL = decltype(f)::value;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                F2 g[IO::NP], b[IO::NP];
+                IO::template params<FULL>(gp, i * IO::kTile, left, g, 1.f);
+                IO::template params<FULL>(bp, i * IO::kTile, left, b, 0.f);
+#pragma unroll
+                for (int j = 0; j < R; ++j) {
+#pragma unroll
+                    for (int e = 0; e < IO::NP; ++e)
+                        h[j][i][e] = normed<OP>(h[j][i][e], mean[j], rstd[j], g[e], b[e]);
+                    if (j == 0 || both)
+                        IO::template store<FULL>(yo + j * a.cols, i * IO::kTile, left, h[j][i]);
+                }
+            }
+        };
+        if (whole) give(std::true_type()); else give(std::false_type());
+        yo += stride * a.cols;
+        if (ho) ho += stride * a.cols;
         if (++s == q.stages) {
             s = 0;
             phase ^= 1u;
@@ -391,16 +442,13 @@ cudaError_t run_warp(const NormFwdArgs& a, int sms, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-template <int OP, typename T, typename IO, typename PT, int V>
+template <int OP, typename T, typename IO, typename PT, int V, int R>
 cudaError_t run_ring(const NormFwdArgs& a, const RingPlan& p, cudaStream_t s) {
-    const void* fn = (const void*)fwd_ring<OP, T, IO, PT, V>;
-    int dev = 0;
-    const cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    unsigned* err = device_error_word();
-    const int clusters = ring_clusters(dev, fn, p, a.rows);
-    if (!err || clusters < 1) return cudaErrorInvalidConfiguration;
-    return launch_ring(fn, a, p, clusters, err, s);
+    const void* fn = (const void*)fwd_ring<OP, T, IO, PT, V, R>;
+    int resident;
+    unsigned* err;
+    if (!ring_resident(fn, p, &resident, &err)) return cudaErrorInvalidConfiguration;
+    return launch_ring(fn, a, p, ring_grid(p, resident, a.rows), err, s);
 }
 
 template <int OP, typename T, typename IO, typename PT>
@@ -412,7 +460,8 @@ cudaError_t run_fwd(const NormFwdArgs& a, int sms, cudaStream_t s) {
     RingPlan p;
     if (!plan_ring(tiles, sizeof(T), a.residual ? 2 : 1, a.rows, sms, &p))
         return run_general<OP, T, IO, PT>(a, sms, s);
-    return p.V == 4 ? run_ring<OP, T, IO, PT, 4>(a, p, s) : run_ring<OP, T, IO, PT, 8>(a, p, s);
+    if (p.V == 8) return run_ring<OP, T, IO, PT, 8, 1>(a, p, s);
+    return p.R == 2 ? run_ring<OP, T, IO, PT, 4, 2>(a, p, s) : run_ring<OP, T, IO, PT, 4, 1>(a, p, s);
 }
 
 template <int OP, typename T, typename IO>

@@ -1,7 +1,9 @@
 // ring.cuh -- a stream of rows through shared memory: one CTA, or a cluster
-// of P CTAs each owning a slice of every row's columns, walks the rows
-// c, c + clusters, ... ; bulk copies bring the slices of the next rows into a
-// ring of stages while the present one is reduced and written.
+// of P CTAs each owning a slice of every row's columns, walks turns of R rows
+// c, c + clusters, ... ; bulk copies bring the slices of the next turns into a
+// ring of stages while the present one is reduced and written.  Two rows a
+// turn share the parameters' loads, a barrier and the shuffles of a reduction
+// (each half warp finishes one row's sums).
 #pragma once
 
 #include "ring_plan.h"
@@ -33,29 +35,35 @@ struct Lines {
     __device__ bool cut() const { return begin < lo || hi < end; }
 };
 
-// One thread brings the row's slices of NS streams into a stage; waiters see
-// them when the stage's mbarrier completes its phase.
-template <int NS, typename T, typename IO>
-__device__ __forceinline__ void ring_issue(const void* const (&src)[NS], int ns, int64_t off,
-                                           int bytes, int64_t total, unsigned char* stage, int room,
-                                           uint32_t bar) {
+// One thread brings the slices of R rows (those below `rows`) of NS streams
+// into a stage; waiters see them when the stage's mbarrier completes its
+// phase.  Slice (stream i, row j) has room i R + j.
+template <int NS, int R, typename T, typename IO>
+__device__ __forceinline__ void ring_issue(const void* const (&src)[NS], int ns, int64_t row,
+                                           int64_t rows, int cols, int c0, int bytes,
+                                           unsigned char* stage, int room, uint32_t bar) {
     const uint64_t pol = l2_policy_evict_first();
+    const int64_t pitch = (int64_t)cols * (int)sizeof(T);
+    const int64_t off = row * pitch + c0 * (int)sizeof(T);
+    const int n = R > 1 && row + 1 < rows ? 2 : 1;
     if constexpr (IO::kAligned) {
-        mbar_arrive_expect_tx(bar, (uint32_t)(ns * bytes));
+        mbar_arrive_expect_tx(bar, (uint32_t)(ns * n * bytes));
 #pragma unroll
-        for (int s = 0; s < NS; ++s)
-            if (s < ns)
-                bulk_g2s(smem_u32(stage) + s * room, static_cast<const char*>(src[s]) + off,
-                         (uint32_t)bytes, bar, pol);
+        for (int i = 0; i < NS; ++i)
+            if (i < ns) {
+                const char* p = static_cast<const char*>(src[i]) + off;
+                const uint32_t d = smem_u32(stage) + i * R * room;
+                bulk_g2s(d, p, (uint32_t)bytes, bar, pol);
+                if (n > 1) bulk_g2s(d + room, p + pitch, (uint32_t)bytes, bar, pol);
+            }
     } else {
         uint32_t tx = 0;
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-            if (s >= ns) continue;
-            const Lines l(static_cast<const char*>(src[s]), off, bytes, total);
+        for (int e = 0; e < ns * n; ++e) {
+            const int i = e / n, j = e - i * n;
+            const Lines l(static_cast<const char*>(src[i]), off + j * pitch, bytes, rows * pitch);
             tx += l.bulk();
             if (l.cut()) {
-                unsigned char* d = stage + s * room;
+                unsigned char* d = stage + (i * R + j) * room;
                 const char* const head = l.lo < l.end ? l.lo : l.end;
                 for (const char* p = l.begin; p < head; p += sizeof(T))
                     *reinterpret_cast<T*>(d + (p - l.first)) = *reinterpret_cast<const T*>(p);
@@ -64,13 +72,12 @@ __device__ __forceinline__ void ring_issue(const void* const (&src)[NS], int ns,
             }
         }
         mbar_arrive_expect_tx(bar, tx);  // releases the plain stores too
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-            if (s >= ns) continue;
-            const Lines l(static_cast<const char*>(src[s]), off, bytes, total);
+        for (int e = 0; e < ns * n; ++e) {
+            const int i = e / n, j = e - i * n;
+            const Lines l(static_cast<const char*>(src[i]), off + j * pitch, bytes, rows * pitch);
             if (l.bulk())
-                bulk_g2s(smem_u32(stage) + s * room + (uint32_t)(l.lo - l.first), l.lo, l.bulk(),
-                         bar, pol);
+                bulk_g2s(smem_u32(stage) + (i * R + j) * room + (uint32_t)(l.lo - l.first), l.lo,
+                         l.bulk(), bar, pol);
         }
     }
 }
@@ -82,12 +89,12 @@ __device__ __forceinline__ int ring_shift(const void* src, int64_t off) {
     return (int)(((uintptr_t)src + (uintptr_t)off) & 15);
 }
 
-// The clusters' exchange of one 16-byte part per row: each CTA deposits its
+// The clusters' exchange of one 16-byte part per turn: each CTA deposits its
 // part in every peer's slot with st.async and waits on its own mbarrier for
 // the P - 1 deposits and its own arrival.  Slots and mbarriers alternate by
-// row parity: a peer's deposit for row k + 2 comes after its wait for row
-// k + 1, which needs this CTA's deposit for row k + 1, made after it read the
-// slots of row k.
+// turn parity: a peer's deposit for turn k + 2 comes after its wait for turn
+// k + 1, which needs this CTA's deposit for turn k + 1, made after it read the
+// slots of turn k.
 struct RingExchange {
     float4 slots[2][kMaxCluster];
     uint64_t bar[2];
@@ -115,5 +122,35 @@ struct RingExchange {
         return slots[b];
     }
 };
+
+// Sums over the warp of one value (R = 1) or of two rows' values (R = 2, lanes
+// 0-15 return row 0's, lanes 16-31 row 1's).
+template <int R> __device__ __forceinline__ float row_sum(const float (&v)[R], int lane) {
+    float s;
+    if constexpr (R == 1) {
+        s = v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
+    } else {
+        const bool up = lane & 16;
+        s = (up ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[1], 16);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+__device__ __forceinline__ float half_sum(float s) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+// Every lane's copy of the value that the lanes of row j's half hold.
+template <int R> __device__ __forceinline__ void spread(float s, int lane, float (&v)[R]) {
+    if constexpr (R == 1) {
+        v[0] = s;
+    } else {
+        const float o = __shfl_xor_sync(0xffffffffu, s, 16);
+        v[0] = lane & 16 ? o : s;
+        v[1] = lane & 16 ? s : o;
+    }
+}
 
 }  // namespace credit

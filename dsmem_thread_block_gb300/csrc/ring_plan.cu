@@ -2,9 +2,9 @@
 #include "ring_plan.h"
 
 #include <algorithm>
-#include <map>
+#include <cstdlib>
 #include <mutex>
-#include <tuple>
+#include <vector>
 
 #include "common.cuh"
 #include "planner.h"
@@ -20,10 +20,9 @@ constexpr int kMostStage = 220 * 1024;  // shared memory a CTA may spend on its 
 
 bool plan_ring(int tiles, int es, int streams, int64_t rows, int sms, RingPlan* out) {
     RingPlan p{};
-    if (tiles <= 4 * kRingWarps) {
-        p.V = 4;
-        p.P = 1;
-    } else {
+    p.V = 4;
+    p.P = (tiles + 4 * kRingWarps - 1) / (4 * kRingWarps);
+    if (getenv("PV8") || p.P > kMaxCluster) {
         p.V = 8;
         p.P = (tiles + 8 * kRingWarps - 1) / (8 * kRingWarps);
     }
@@ -33,14 +32,16 @@ bool plan_ring(int tiles, int es, int streams, int64_t rows, int sms, RingPlan* 
     p.W = (p.shape.tiles + p.V - 1) / p.V;
     // a slice that starts inside a 16-byte line takes one line more
     p.shape.room = (p.shape.tiles * kTileCols * es + 16 + 127) / 128 * 128;
-    const int stage = p.shape.room * streams;
-    int ctas = std::max(1, std::min(8, 1024 / (32 * p.W)));  // per SM
-    const int budget = (p.P == 1 ? 144 : 200) * 1024;
+    const int ctas_most = std::max(1, std::min(8, 1024 / (32 * p.W)));  // per SM
+    p.most = std::max(1, sms * ctas_most / p.P);
+    p.R = p.V == 4 && rows >= (getenv("RM") ? atof(getenv("RM")) : 2) * p.most ? 2 : 1;
+    const int stage = p.shape.room * streams * p.R;
+    int ctas = ctas_most;
+    const int budget = (getenv("BUD") ? atoi(getenv("BUD")) : 144) * 1024;
     while (ctas > 1 && budget / ctas < 2 * stage) --ctas;
     int stages = budget / ctas / stage;
     if (stages < 2) stages = kMostStage / stage;
     if (stages < 1) return false;
-    p.most = (int)std::max<int64_t>(1, (int64_t)sms * std::max(1, std::min(8, 1024 / (32 * p.W))) / p.P);
     if (rows * p.P * 2 <= sms) stages = 1;  // every cluster has one row
     p.shape.stages = std::min(stages, kRingStages);
     p.smem = (size_t)p.shape.stages * stage;
@@ -48,34 +49,61 @@ bool plan_ring(int tiles, int es, int streams, int64_t rows, int sms, RingPlan* 
     return true;
 }
 
-int ring_clusters(int dev, const void* fn, const RingPlan& p, int64_t rows) {
+namespace {
+
+// What a launch of (kernel, shape) needs from the device, looked up once.
+struct Resident {
+    const void* fn;
+    int dev, W, P, clusters;
+    size_t smem;
+    unsigned* err;
+};
+
+}  // namespace
+
+bool ring_resident(const void* fn, const RingPlan& p, int* clusters, unsigned** err) {
     static std::mutex mu;
-    static std::map<std::tuple<int, const void*, int, int, size_t>, int> resident;
-    const auto key = std::make_tuple(dev, fn, p.W, p.P, p.smem);
-    int most = 0;
+    static std::vector<Resident> known;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
     {
         std::lock_guard<std::mutex> lk(mu);
-        const auto it = resident.find(key);
-        if (it != resident.end()) most = it->second;
+        for (const Resident& r : known)
+            if (r.fn == fn && r.dev == dev && r.W == p.W && r.P == p.P && r.smem == p.smem) {
+                *clusters = r.clusters;
+                *err = r.err;
+                return true;
+            }
     }
-    if (most == 0) {
-        if (!kernel_info(dev, fn, true)) return 0;
-        most = occupancy_clusters(dev, fn, p.P, 32 * p.W, p.smem, 1 << 20);
-        if (most < 1) return 0;
-        std::lock_guard<std::mutex> lk(mu);
-        if (resident.size() >= 4096) resident.clear();
-        resident[key] = most;
-    }
-    const int64_t c = std::min<int64_t>(std::min(most, p.most), rows);
-    const int64_t turns = (rows + c - 1) / c;
-    return (int)((rows + turns - 1) / turns);
+    if (!kernel_info(dev, fn, true)) return false;
+    Resident r{fn, dev, p.W, p.P, occupancy_clusters(dev, fn, p.P, 32 * p.W, p.smem, 1 << 20),
+               p.smem, device_error_word()};
+    if (r.clusters < 1 || !r.err) return false;
+    std::lock_guard<std::mutex> lk(mu);
+    if (known.size() >= 256) known.clear();  // shapes come and go
+    known.push_back(r);
+    *clusters = r.clusters;
+    *err = r.err;
+    return true;
+}
+
+int ring_grid(const RingPlan& p, int resident, int64_t rows) {
+    const int64_t units = (rows + p.R - 1) / p.R;  // turns of all clusters
+    const int64_t c = std::min<int64_t>(std::min(resident, p.most), units);
+    const int64_t turns = (units + c - 1) / c;
+    return (int)((units + turns - 1) / turns);
 }
 
 cudaError_t launch_ring_args(const void* fn, void** args, const RingPlan& p, int clusters,
                              cudaStream_t s) {
+    const dim3 grid((unsigned)(clusters * p.P)), block((unsigned)(32 * p.W));
+    if (p.P == 1) return cudaLaunchKernel(fn, grid, block, args, p.smem, s);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(clusters * p.P));
-    cfg.blockDim = dim3((unsigned)(32 * p.W));
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
     cfg.dynamicSmemBytes = p.smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

@@ -20,7 +20,7 @@ struct RingShape {
 };
 
 struct RingPlan {
-    int V, W, P;        // tiles per warp, warps per CTA, CTAs per row
+    int V, W, P, R;     // tiles per warp, warps per CTA, CTAs per row, rows per turn
     int most;           // most clusters of the grid
     size_t smem;
     RingShape shape;    // `clusters` and `err` are set by the launch
@@ -30,9 +30,13 @@ struct RingPlan {
 // elements; false where the rows are too wide.
 bool plan_ring(int tiles, int es, int streams, int64_t rows, int sms, RingPlan* out);
 
-// The clusters a launch of `fn` runs: as many as are resident, no more than
-// rows or plan.most, evened out so that none has a row more than it must.
-int ring_clusters(int dev, const void* fn, const RingPlan& p, int64_t rows);
+// The clusters of `fn` in this shape that the current device holds at once,
+// and its error word; false on a CUDA error.
+bool ring_resident(const void* fn, const RingPlan& p, int* clusters, unsigned** err);
+
+// The clusters of a launch: as many as are resident, no more than rows or
+// plan.most, evened out so that none has a row more than it must.
+int ring_grid(const RingPlan& p, int resident, int64_t rows);
 
 cudaError_t launch_ring_args(const void* fn, void** args, const RingPlan& p, int clusters,
                              cudaStream_t s);
