@@ -41,38 +41,50 @@ __device__ __forceinline__ RowStats row_stats(const NormBwdArgs& a, int64_t row)
     return r;
 }
 
+// xh of a pair.  The mean is subtracted before the product: where a row's
+// deviation is far below its mean, h rstd - mean rstd would keep the product's
+// rounding.
+template <int OP> __device__ __forceinline__ F2 normalised(F2 h, RowStats r) {
+    return mul2(OP == kLayerNorm ? add2(h, f2(-r.mean)) : h, f2(r.rstd));
+}
+
 // Sums of a tile: s1 += w xh, s2 += w; and the columns' gradients.
 template <int OP, int NP>
 __device__ __forceinline__ void tile_sums(const F2* dy, const F2* h, const F2* g, RowStats r,
                                           F2& s1, F2& s2, F2* ag, F2* ab) {
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
-        const F2 xh = mul2(OP == kLayerNorm ? add2(h[k], f2(-r.mean)) : h[k], f2(r.rstd));
-        const F2 w = mul2(dy[k], g[k]);
-        s1 = fma2(w, xh, s1);
-        ag[k] = fma2(dy[k], xh, ag[k]);
+        const F2 t = mul2(dy[k], normalised<OP>(h[k], r));
+        ag[k] = add2(ag[k], t);
+        s1 = fma2(t, g[k], s1);
         if constexpr (OP == kLayerNorm) {
-            s2 = add2(s2, w);
+            s2 = fma2(dy[k], g[k], s2);
             ab[k] = add2(ab[k], dy[k]);
         }
     }
 }
+
+// A row's dtot = w rstd + (c - xh b): what the two means make of it.
+struct RowBack {
+    float rstd, b, c;  // b = rstd mean_j(w xh), c = -rstd mean_j(w)
+    __device__ RowBack(RowStats r, float m1, float m2) : rstd(r.rstd), b(r.rstd * m1), c(-r.rstd * m2) {}
+};
 
 // dtot of a tile from its row's two means, then the outputs; dx and dres point
 // at the lane's first column, the tile lies `off` further, at column `base`.
 // `on`: draw the mask (all 32 lanes call).
 template <int OP, typename T, typename IO, bool FULL>
 __device__ __forceinline__ void tile_out(const DropStream& d, const F2* dy, const F2* h,
-                                         const F2* g, const F2* dh, RowStats r, float c1, float c2,
-                                         int64_t row, int base, int off, int left, int lane,
-                                         bool on, T* dx, T* dres) {
+                                         const F2* g, bool has_dh, const F2* dh, RowStats r,
+                                         RowBack q, int64_t row, int base, int off, int left,
+                                         int lane, bool on, T* dx, T* dres) {
     F2 v[IO::NP];
 #pragma unroll
     for (int k = 0; k < IO::NP; ++k) {
-        const F2 xh = mul2(OP == kLayerNorm ? add2(h[k], f2(-r.mean)) : h[k], f2(r.rstd));
-        F2 t = fma2(xh, f2(-c1), mul2(dy[k], g[k]));
-        if constexpr (OP == kLayerNorm) t = add2(t, f2(-c2));
-        v[k] = dh ? fma2(t, f2(r.rstd), dh[k]) : mul2(t, f2(r.rstd));
+        const F2 xh = normalised<OP>(h[k], r);
+        F2 t = OP == kLayerNorm ? fma2(xh, f2(-q.b), f2(q.c)) : mul2(xh, f2(-q.b));
+        if (has_dh) t = add2(t, dh[k]);
+        v[k] = fma2(mul2(dy[k], g[k]), f2(q.rstd), t);
     }
     if (dres) IO::template store<FULL>(dres, off, left, v);
     if (on) {
@@ -147,7 +159,7 @@ __global__ void __launch_bounds__(kThreads) bwd_warp(NormBwdArgs a) {
             OP == kLayerNorm ? warp_allreduce(s2.x + s2.y, SumOp()) * a.inv_cols : 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            tile_out<OP, T, IO, false>(d, u[i], h[i], g[i], dhp ? dh[i] : nullptr, r, c1, c2, now,
+            tile_out<OP, T, IO, false>(d, u[i], h[i], g[i], dhp != nullptr, dh[i], r, RowBack(r, c1, c2), now,
                                        i * IO::kTile, i * IO::kTile, left, lane,
                                        a.drop.on && i * IO::kTile < a.cols,
                                        static_cast<T*>(a.dx) + now * a.cols + l0,
@@ -175,87 +187,34 @@ __global__ void __launch_bounds__(kThreads) bwd_warp(NormBwdArgs a) {
     }
 }
 
-// Two row sums of R rows over the warp, value (row j, sum i) in the lanes of
-// group 2 j + i (of 8 lanes; R = 1: of 16, j = 0): the lanes halve the values
-// they carry before the last steps add over their group.
-template <int R>
-__device__ __forceinline__ float sums_over_warp(const float (&t)[R][2], int lane) {
-    float v;
-    if constexpr (R == 2) {
-        const bool up = lane & 16;
-        const float a = (up ? t[1][0] : t[0][0]) + __shfl_xor_sync(0xffffffffu, up ? t[0][0] : t[1][0], 16);
-        const float b = (up ? t[1][1] : t[0][1]) + __shfl_xor_sync(0xffffffffu, up ? t[0][1] : t[1][1], 16);
-        const bool hi = lane & 8;
-        v = (hi ? b : a) + __shfl_xor_sync(0xffffffffu, hi ? a : b, 8);
-    } else {
-        const bool up = lane & 16;
-        v = (up ? t[0][1] : t[0][0]) + __shfl_xor_sync(0xffffffffu, up ? t[0][0] : t[0][1], 16);
-        v += __shfl_xor_sync(0xffffffffu, v, 8);
-    }
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
-// The totals of up to 16 parts of R rows' two sums (`parts`: value-major,
-// kRingWarps apart), in every lane.
-template <int R>
-__device__ __forceinline__ void merge_sums(const float* parts, int count, int lane,
-                                           float (&t)[R][2]) {
-    const int g = R == 2 ? lane >> 3 : lane >> 4, at = lane & (R == 2 ? 7 : 15);
-    float v = at < count ? parts[g * kRingWarps + at] : 0.f;
-    if constexpr (R == 2) {
-        if (at + 8 < count) v += parts[g * kRingWarps + at + 8];
-    } else {
-        v += __shfl_xor_sync(0xffffffffu, v, 8);
-    }
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-#pragma unroll
-    for (int j = 0; j < R; ++j)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            t[j][i] = __shfl_sync(0xffffffffu, v, (2 * j + i) * (R == 2 ? 8 : 16));
-}
-
-// The same over the CTAs' deposits (one float4 a CTA: its rows' sums in turn).
-template <int R>
-__device__ __forceinline__ void merge_sums_cluster(const float4* parts, int count, int lane,
-                                                   float (&t)[R][2]) {
-    const int g = R == 2 ? lane >> 3 : lane >> 4, at = lane & (R == 2 ? 7 : 15);
-    const float* p = reinterpret_cast<const float*>(parts) + g;
-    float v = at < count ? p[4 * at] : 0.f;
-    if constexpr (R == 2) {
-        if (at + 8 < count) v += p[4 * (at + 8)];
-    } else {
-        v += __shfl_xor_sync(0xffffffffu, v, 8);
-    }
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-#pragma unroll
-    for (int j = 0; j < R; ++j)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            t[j][i] = __shfl_sync(0xffffffffu, v, (2 * j + i) * (R == 2 ? 8 : 16));
+// Two sums over the warp: lanes 0-15 return the first, lanes 16-31 the second.
+__device__ __forceinline__ float two_sums(float a, float b, int lane) {
+    const float t[2] = {a, b};
+    return row_sum<2>(t, lane);
 }
 
 // ------------------------------------------------- a CTA or a cluster per row
-// Warp w of a CTA owns the V tiles from column c0 + 128 V w on, of R rows at a
-// time.  A stage is read twice, before and after its rows' sums are known.
-template <int OP, typename T, typename IO, typename PT, int V, int R>
+// Warp w of a CTA owns the V tiles from column c0 + 128 V w on.  The rows are
+// pipelined: an iteration sums row k and writes row k - 1, whose sums were
+// merged (and exchanged with the cluster) meanwhile, with one barrier between
+// iterations; so a stage is read in two iterations and its row's sums are
+// never waited for at once.
+template <int OP, typename T, typename IO, typename PT, int V>
 __global__ void __launch_bounds__(kRingThreads) bwd_ring(NormBwdArgs a, RingShape q) {
+    constexpr bool kHeld = V == 4;  // gamma stays in registers
     extern __shared__ __align__(128) unsigned char ring[];
     __shared__ __align__(8) uint64_t full[kRingStages];
-    __shared__ float wred[2][2 * R][kRingWarps];
+    __shared__ float wred[2][2][kRingWarps];
     __shared__ RingExchange ex;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
+    const int part = lane & 15, which = lane >> 4;
     const uint32_t P = cluster_nctarank(), rank = cluster_ctarank();
-    const int64_t first = (int64_t)(blockIdx.x / P) * R, stride = (int64_t)q.clusters * R;
+    const int64_t first = blockIdx.x / P;
     const int c0 = (int)rank * q.tiles * IO::kTile;
     const int c1 = min(a.cols, c0 + q.tiles * IO::kTile);
     const int bytes = (c1 - c0) * (int)sizeof(T);
     const void* const src[3] = {a.dy, a.h, a.dh};
-    const int ns = a.dh ? 3 : 2, stage_bytes = ns * R * q.room;
+    const int ns = a.dh ? 3 : 2, stage_bytes = ns * q.room;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < q.stages; ++s) mbar_init(smem_u32(&full[s]), 1);
@@ -270,124 +229,133 @@ __global__ void __launch_bounds__(kRingThreads) bwd_ring(NormBwdArgs a, RingShap
     }
     auto issue = [&](int64_t row, int s) {
         if (row < a.rows)
-            ring_issue<3, R, T, IO>(src, ns, row, a.rows, a.cols, c0, bytes, ring + s * stage_bytes,
+            ring_issue<3, 1, T, IO>(src, ns, row, a.rows, a.cols, c0, bytes, ring + s * stage_bytes,
                                     q.room, smem_u32(&full[s]));
     };
     if (threadIdx.x == 0)
-        for (int s = 0; s < q.stages; ++s) issue(first + s * stride, s);
+        for (int s = 0; s < q.stages; ++s) issue(first + (int64_t)s * q.clusters, s);
 
     const DropStream d(a.drop);
     const int base0 = c0 + warp * V * IO::kTile, j0 = base0 + IO::first(lane), left = c1 - j0;
     const bool whole = base0 + V * IO::kTile <= c1;
+    const bool simple = !a.drop.on && !a.dres;  // dx is the only matrix written
     const PT* const gp = moved(static_cast<const PT*>(a.gamma), j0);
     T* dx = static_cast<T*>(a.dx) + first * a.cols + j0;
     T* dres = moved(static_cast<T*>(a.dres), first * a.cols + j0);
-    F2 ag[V][IO::NP], ab[V][IO::NP];
+    F2 held[kHeld ? V : 1][IO::NP], ag[V][IO::NP], ab[V][IO::NP];
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+    for (int i = 0; i < V; ++i) {
+        if (kHeld) IO::template params<false>(gp, i * IO::kTile, left, held[kHeld ? i : 0], 1.f);
 #pragma unroll
         for (int e = 0; e < IO::NP; ++e) ag[i][e] = ab[i][e] = f2(0.f);
-    RowStats next[R];
+    }
+    // gamma of tile i
+    auto weight = [&](auto f, int i, F2 (&g)[IO::NP]) {
+        if constexpr (kHeld) {
 #pragma unroll
-    for (int j = 0; j < R; ++j) next[j] = row_stats<OP>(a, first + j);
-    int s = 0;
-    uint32_t phase = 0, k = 0;
-    for (int64_t row = first; row < a.rows; row += stride, ++k) {
-        RowStats r[R];
-#pragma unroll
-        for (int j = 0; j < R; ++j) {
-            r[j] = next[j];
-            next[j] = row_stats<OP>(a, row + stride + j);
+            for (int e = 0; e < IO::NP; ++e) g[e] = held[i][e];
+        } else {
+            IO::template params<decltype(f)::value>(gp, i * IO::kTile, left, g, 1.f);
         }
-        const bool both = R > 1 && row + 1 < a.rows;
-        const unsigned char* const stage = ring + s * stage_bytes;
-        mbar_wait_bounded(smem_u32(&full[s]), phase, q.err);
-        // row j's slice of stream i, at the lane's first column
-        auto slice = [&](int i, int j, const void* p) {
-            const int64_t off = ((row + j) * a.cols + c0) * (int64_t)sizeof(T);
-            return reinterpret_cast<const T*>(stage + (i * R + j) * q.room + ring_shift<IO>(p, off)) +
-                   (j0 - c0);
-        };
-        const T *ys[R], *hs[R], *ds[R];
-#pragma unroll
-        for (int j = 0; j < R; ++j) {
-            ys[j] = slice(0, j, a.dy);
-            hs[j] = slice(1, j, a.h);
-            ds[j] = slice(2, j, a.dh);
-        }
-        F2 s1[R], s2[R];
-#pragma unroll
-        for (int j = 0; j < R; ++j) s1[j] = s2[j] = f2(0.f);
-        auto take = [&](auto f) {
-            constexpr bool FULL = decltype(f)::value;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                F2 g[IO::NP];
-                IO::template params<FULL>(gp, i * IO::kTile, left, g, 1.f);
-#pragma unroll
-                for (int j = 0; j < R; ++j) {
-                    if (j > 0 && !both) break;
-                    F2 u[IO::NP], h[IO::NP];
-                    unpack<T, IO::NP>(IO::template staged<FULL>(ys[j], i * IO::kTile, left), u);
-                    unpack<T, IO::NP>(IO::template staged<FULL>(hs[j], i * IO::kTile, left), h);
-                    tile_sums<OP, IO::NP>(u, h, g, r[j], s1[j], s2[j], ag[i], ab[i]);
+    };
+    // stream i's slice of a row in a stage, at the lane's first column
+    auto slice = [&](const unsigned char* stage, int i, const void* p, int64_t row) {
+        const int64_t off = (row * a.cols + c0) * (int64_t)sizeof(T);
+        return reinterpret_cast<const T*>(stage + i * q.room + ring_shift<IO>(p, off)) + (j0 - c0);
+    };
+    const uint32_t turns = (uint32_t)((a.rows - first + q.clusters - 1) / q.clusters);
+    const int64_t stride = (int64_t)q.clusters * a.cols;
+    RowStats next = row_stats<OP>(a, first), prev{0.f, 0.f};
+    const float* mp = OP == kLayerNorm ? a.mean + first : nullptr;
+    const float* rp = a.rstd + first;
+    int64_t row = first;  // of turn k
+    int s = 0, sp = 0;
+    uint32_t phase = 0;
+    const std::true_type yes;
+    const std::false_type no;
+    for (uint32_t k = 0;; ++k) {
+        const RowStats r = next;
+        if (k < turns) {
+            if (k + 1 < turns) {
+                rp += q.clusters;
+                next.rstd = *rp;
+                if constexpr (OP == kLayerNorm) {
+                    mp += q.clusters;
+                    next.mean = *mp;
                 }
             }
-        };
-        if (whole) take(std::true_type()); else take(std::false_type());
-        float t[R][2];
+            const unsigned char* const stage = ring + s * stage_bytes;
+            mbar_wait_bounded(smem_u32(&full[s]), phase, q.err);
+            const T* const ys = slice(stage, 0, a.dy, row);
+            const T* const hs = slice(stage, 1, a.h, row);
+            F2 s1 = f2(0.f), s2 = f2(0.f);
+            auto take = [&](auto f) {
+                constexpr bool FULL = decltype(f)::value;
 #pragma unroll
-        for (int j = 0; j < R; ++j) {
-            t[j][0] = s1[j].x + s1[j].y;
-            t[j][1] = s2[j].x + s2[j].y;
+                for (int i = 0; i < V; ++i) {
+                    F2 u[IO::NP], h[IO::NP], g[IO::NP];
+                    unpack<T, IO::NP>(IO::template staged<FULL>(ys, i * IO::kTile, left), u);
+                    unpack<T, IO::NP>(IO::template staged<FULL>(hs, i * IO::kTile, left), h);
+                    weight(f, i, g);
+                    tile_sums<OP, IO::NP>(u, h, g, r, s1, s2, ag[i], ab[i]);
+                }
+            };
+            if (whole) take(yes); else take(no);
+            const float v = two_sums(s1.x + s1.y, s2.x + s2.y, lane);
+            if (part == 0) wred[k & 1][which][warp] = v;
         }
-        const float v = sums_over_warp<R>(t, lane);
-        constexpr int G = R == 2 ? 8 : 16;  // lanes of a value's group
-        if (lane % G == 0) wred[k & 1][lane / G][warp] = v;
+        if (k > 0) {  // the row before
+            float v;
+            if (P > 1) {
+                const float4* parts = ex.wait(k - 1, P, rank, q.err);
+                v = part < (int)P ? (which ? parts[part].y : parts[part].x) : 0.f;
+            } else {
+                v = part < W ? wred[(k - 1) & 1][which][part] : 0.f;
+            }
+            float t[2];
+            spread<2>(half_sum(v) * a.inv_cols, lane, t);
+            const RowBack back(prev, t[0], t[1]);
+            const int64_t at = row - q.clusters;
+            const unsigned char* const stage = ring + sp * stage_bytes;
+            const T* const ys = slice(stage, 0, a.dy, at);
+            const T* const hs = slice(stage, 1, a.h, at);
+            const T* const ds = slice(stage, 2, a.dh, at);
+            // (the conditions that hold for the whole call are constants of the
+            // tiles' code: as predicates they cost as much as the work)
+            auto give = [&](auto f, auto has_dh, auto plain) {
+                constexpr bool FULL = decltype(f)::value;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    F2 u[IO::NP], h[IO::NP], g[IO::NP], dh[IO::NP];
+                    unpack<T, IO::NP>(IO::template staged<FULL>(ys, i * IO::kTile, left), u);
+                    unpack<T, IO::NP>(IO::template staged<FULL>(hs, i * IO::kTile, left), h);
+                    if (has_dh)
+                        unpack<T, IO::NP>(IO::template staged<FULL>(ds, i * IO::kTile, left), dh);
+                    weight(f, i, g);
+                    tile_out<OP, T, IO, FULL>(
+                        d, u, h, g, has_dh, dh, prev, back, at, base0 + i * IO::kTile, i * IO::kTile,
+                        left, lane, !plain && a.drop.on && (FULL || base0 + i * IO::kTile < c1), dx,
+                        plain ? nullptr : dres);
+                }
+            };
+            if (!whole) give(no, ns > 2, no);
+            else if (ns > 2) simple ? give(yes, yes, yes) : give(yes, yes, no);
+            else simple ? give(yes, no, yes) : give(yes, no, no);
+            dx += stride;
+            if (dres) dres += stride;
+        }
+        if (k == turns) break;
         __syncthreads();
-        // every thread has left the previous turn: refill its stage
-        if (threadIdx.x == 0 && k > 0 && q.stages > 1)
-            issue(row + (q.stages - 1) * stride, s == 0 ? q.stages - 1 : s - 1);
-        merge_sums<R>(&wred[k & 1][0][0], W, lane, t);
-        if (P > 1) {
-            const float4* parts =
-                ex.all(k, make_float4(t[0][0], t[0][1], t[R - 1][0], t[R - 1][1]), P, rank, q.err);
-            merge_sums_cluster<R>(parts, (int)P, lane, t);
+        // every thread has left row k - 1: refill its stage
+        if (threadIdx.x == 0 && k > 0) issue(row + (int64_t)(q.stages - 1) * q.clusters, sp);
+        if (P > 1 && warp == 0) {
+            float t[2];
+            spread<2>(half_sum(part < W ? wred[k & 1][which][part] : 0.f), lane, t);
+            ex.deposit(k, make_float4(t[0], t[1], 0.f, 0.f), P, rank);
         }
-#pragma unroll
-        for (int j = 0; j < R; ++j) {
-            t[j][0] *= a.inv_cols;
-            t[j][1] *= a.inv_cols;
-        }
-        auto give = [&](auto f) {
-            constexpr bool FULL = decltype(f)::value;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                F2 g[IO::NP];
-                IO::template params<FULL>(gp, i * IO::kTile, left, g, 1.f);
-#pragma unroll
-                for (int j = 0; j < R; ++j) {
-                    if (j > 0 && !both) break;
-                    F2 u[IO::NP], h[IO::NP], dh[IO::NP];
-                    unpack<T, IO::NP>(IO::template staged<FULL>(ys[j], i * IO::kTile, left), u);
-                    unpack<T, IO::NP>(IO::template staged<FULL>(hs[j], i * IO::kTile, left), h);
-                    if (ns > 2)
-                        unpack<T, IO::NP>(IO::template staged<FULL>(ds[j], i * IO::kTile, left), dh);
-                    tile_out<OP, T, IO, FULL>(d, u, h, g, ns > 2 ? dh : nullptr, r[j], t[j][0],
-                                              t[j][1], row + j, base0 + i * IO::kTile, i * IO::kTile,
-                                              left, lane,
-                                              a.drop.on && (FULL || base0 + i * IO::kTile < c1),
-                                              dx + j * a.cols, moved(dres, j * a.cols));
-                }
-            }
-        };
-        if (whole) give(std::true_type()); else give(std::false_type());
-        dx += stride * a.cols;
-        if (dres) dres += stride * a.cols;
-        if (q.stages == 1) {  // nowhere to fetch ahead: the next turn comes now
-            __syncthreads();
-            if (threadIdx.x == 0) issue(row + stride, 0);
-        }
+        prev = r;
+        row += q.clusters;
+        sp = s;
         if (++s == q.stages) {
             s = 0;
             phase ^= 1u;
@@ -395,7 +363,7 @@ __global__ void __launch_bounds__(kRingThreads) bwd_ring(NormBwdArgs a, RingShap
     }
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        tile_params<OP, IO>(a, blockIdx.x / P, j0, i * IO::kTile, left, ag[i], ab[i]);
+        tile_params<OP, IO>(a, first, j0, i * IO::kTile, left, ag[i], ab[i]);
     if (P > 1) {  // no CTA leaves while a peer's deposit to it may be in flight
         cluster_arrive_release();
         cluster_wait_acquire();
@@ -427,7 +395,7 @@ __global__ void __launch_bounds__(kThreads) bwd_stats(NormBwdArgs a) {
 #pragma unroll
             for (int k = 0; k < IO::NP; ++k) {
                 const F2 w = mul2(u[k], g[k]);  // 0 past the row
-                s1 = fma2(w, mul2(add2(h[k], f2(-r.mean)), f2(r.rstd)), s1);
+                s1 = fma2(w, normalised<OP>(h[k], r), s1);
                 s2 = add2(s2, w);
             }
         }
@@ -484,8 +452,8 @@ __global__ void __launch_bounds__(kThreads) bwd_apply(NormBwdArgs a) {
                                   dh);
             s1 = s2 = f2(0.f);
             tile_sums<OP, IO::NP>(u, h, g, {c.x, c.y}, s1, s2, ag, ab);
-            tile_out<OP, T, IO, false>(d, u, h, g, a.dh ? dh : nullptr, {c.x, c.y}, c.z, c.w, r0 + i,
-                                       base, 0, left, lane, a.drop.on, static_cast<T*>(a.dx) + o,
+            tile_out<OP, T, IO, false>(d, u, h, g, a.dh != nullptr, dh, {c.x, c.y},
+                                       RowBack({c.x, c.y}, c.z, c.w), r0 + i, base, 0, left, lane, a.drop.on, static_cast<T*>(a.dx) + o,
                                        moved(static_cast<T*>(a.dres), o));
         }
     }
@@ -541,9 +509,9 @@ cudaError_t run_warp(const NormBwdArgs& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-template <int OP, typename T, typename IO, typename PT, int V, int R>
+template <int OP, typename T, typename IO, typename PT, int V>
 cudaError_t run_ring(NormBwdArgs& a, const RingPlan& p, cudaStream_t s) {
-    const void* fn = (const void*)bwd_ring<OP, T, IO, PT, V, R>;
+    const void* fn = (const void*)bwd_ring<OP, T, IO, PT, V>;
     int resident;
     unsigned* err;
     if (!ring_resident(fn, p, &resident, &err)) return cudaErrorInvalidConfiguration;
@@ -558,10 +526,9 @@ cudaError_t run_bwd(NormBwdArgs& a, int sms, cudaStream_t s) {
     if (tiles <= 2) return run_warp<OP, T, IO, PT, 2>(a, s);
     if (tiles <= 4) return run_warp<OP, T, IO, PT, 4>(a, s);
     RingPlan p;
-    if (!plan_ring(tiles, sizeof(T), a.dh ? 3 : 2, a.rows, sms, &p))
+    if (!plan_ring(tiles, sizeof(T), a.dh ? 3 : 2, 1, a.rows, sms, &p))
         return run_general<OP, T, IO, PT>(a, sms, s);
-    if (p.V == 8) return run_ring<OP, T, IO, PT, 8, 1>(a, p, s);
-    return p.R == 2 ? run_ring<OP, T, IO, PT, 4, 2>(a, p, s) : run_ring<OP, T, IO, PT, 4, 1>(a, p, s);
+    return p.V == 4 ? run_ring<OP, T, IO, PT, 4>(a, p, s) : run_ring<OP, T, IO, PT, 8>(a, p, s);
 }
 
 template <int OP, typename T, typename IO>
@@ -600,12 +567,12 @@ TrainLayout norm_bwd_layout(int dtype, int64_t rows, int64_t cols, int sms) {
         l.room_groups = l.groups;
         for (int streams = 2; streams <= 3; ++streams) {
             RingPlan p;
-            if (plan_ring(tiles, dtype == 0 ? 4 : 2, streams, rows, sms, &p))
+            if (plan_ring(tiles, dtype == 0 ? 4 : 2, streams, 1, rows, sms, &p))
                 l.room_groups = (int)std::max<int64_t>(l.room_groups, std::min<int64_t>(p.most, rows));
         }
         // the general form's partials, where it may run
         RingPlan p;
-        if (!plan_ring(tiles, dtype == 0 ? 4 : 2, 3, rows, sms, &p)) l.partials = rows * l.nch * 8;
+        if (!plan_ring(tiles, dtype == 0 ? 4 : 2, 3, 1, rows, sms, &p)) l.partials = rows * l.nch * 8;
     }
     l.room_groups = std::max(l.room_groups, l.groups);
     return l;

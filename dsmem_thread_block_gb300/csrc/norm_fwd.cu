@@ -23,10 +23,11 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kTilesPerWarp = 4;
 constexpr int kChunkTiles = kWarps * kTilesPerWarp;
 
-// (h - mean) rstd gamma + beta; rstd is CUDA's rsqrtf (2 ulp).
+// (h - mean) rstd gamma + beta; rstd is CUDA's rsqrtf (2 ulp).  The mean is
+// subtracted first, so that a mean far above the deviation costs nothing.
 template <int OP>
 __device__ __forceinline__ F2 normed(F2 h, float mu, float rstd, F2 g, F2 b) {
-    const F2 z = OP == kLayerNorm ? mul2(add2(h, f2(-mu)), f2(rstd)) : mul2(h, f2(rstd));
+    const F2 z = mul2(OP == kLayerNorm ? add2(h, f2(-mu)) : h, f2(rstd));
     return fma2(z, g, b);
 }
 
@@ -172,6 +173,7 @@ __global__ void __launch_bounds__(kRingThreads) fwd_ring(NormFwdArgs a, RingShap
     const bool whole = base0 + V * IO::kTile <= c1;
     const PT* const gp = moved(static_cast<const PT*>(a.gamma), j0);
     const PT* const bp = moved(static_cast<const PT*>(a.beta), j0);
+    const bool affine = whole && gp && (OP != kLayerNorm || bp);
     // columns of this warp, of the warp and of the CTA that this lane merges
     const int part = lane & 15;
     const float inv_warp = 1.f / (float)max(1, min(c1 - base0, V * IO::kTile));
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(kRingThreads) fwd_ring(NormFwdArgs a, RingShap
         unsigned char* const stage = ring + s * stage_bytes;
         mbar_wait_bounded(smem_u32(&full[s]), phase, q.err);
         float mean[R], m2;
-        auto take = [&](auto f) {
+        auto take = [&](auto f, auto res, auto on) {
             constexpr bool FULL = decltype(f)::value;
 #pragma unroll
             for (int j = 0; j < R; ++j) {
@@ -203,15 +205,15 @@ __global__ void __launch_bounds__(kRingThreads) fwd_ring(NormFwdArgs a, RingShap
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     typename IO::R rv = {};
-                    if (ns > 1) rv = IO::template staged<FULL>(rs, i * IO::kTile, left);
-                    tile_h<T, IO>(IO::template staged<FULL>(xs, i * IO::kTile, left), rv, ns > 1,
-                                  a.drop.on && (FULL || base0 + i * IO::kTile < c1), d,
+                    if (res) rv = IO::template staged<FULL>(rs, i * IO::kTile, left);
+                    tile_h<T, IO>(IO::template staged<FULL>(xs, i * IO::kTile, left), rv, res,
+                                  on && (FULL || base0 + i * IO::kTile < c1), d,
                                   base0 + i * IO::kTile, lane, (uint32_t)(row + j), h[j][i]);
 #pragma unroll
                     for (int e = 0; e < IO::NP; ++e)
                         t = OP == kLayerNorm ? add2(t, h[j][i][e]) : fma2(h[j][i][e], h[j][i][e], t);
                 }
-                if (ho && (j == 0 || both)) {
+                if ((res || on) && ho && (j == 0 || both)) {
 #pragma unroll
                     for (int i = 0; i < V; ++i)
                         IO::template store<FULL>(ho + j * a.cols, i * IO::kTile, left, h[j][i]);
@@ -236,7 +238,11 @@ __global__ void __launch_bounds__(kRingThreads) fwd_ring(NormFwdArgs a, RingShap
                 }
             }
         };
-        if (whole) take(std::true_type()); else take(std::false_type());
+        const std::true_type yes;
+        const std::false_type no;
+        if (!whole) take(no, ns > 1, a.drop.on != 0);
+        else if (ns > 1) a.drop.on ? take(yes, yes, yes) : take(yes, yes, no);
+        else a.drop.on ? take(yes, no, yes) : take(yes, no, no);
         {   // the warp's (sum, M2 about its mean) of each row
             const float sum = m2;
             if constexpr (OP == kLayerNorm) m2 = row_sum<R>(v, lane);
@@ -265,8 +271,9 @@ __global__ void __launch_bounds__(kRingThreads) fwd_ring(NormFwdArgs a, RingShap
             float t0[R], t1[R];
             spread<R>(sum, lane, t0);
             spread<R>(m2, lane, t1);
-            const float4* parts = ex.all(k, make_float4(t0[0], t1[0], t0[R - 1], t1[R - 1]), P, rank,
-                                         q.err);
+            if (warp == 0)
+                ex.deposit(k, make_float4(t0[0], t1[0], t0[R - 1], t1[R - 1]), P, rank);
+            const float4* parts = ex.wait(k, P, rank, q.err);
             const float4 c = part < (int)P ? parts[part] : make_float4(0.f, 0.f, 0.f, 0.f);
             w = mine ? make_float2(c.z, c.w) : make_float2(c.x, c.y);
             if constexpr (OP == kLayerNorm) {
@@ -284,13 +291,14 @@ __global__ void __launch_bounds__(kRingThreads) fwd_ring(NormFwdArgs a, RingShap
         float rstd[R];
         spread<R>(own, lane, rstd);
         if constexpr (OP == kLayerNorm) spread<R>(mu, lane, mean);
-        auto give = [&](auto f) {
+        auto give = [&](auto f) {  // FULL: gamma, and LayerNorm's beta, are there too
             constexpr bool FULL = decltype(f)::value;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 F2 g[IO::NP], b[IO::NP];
-                IO::template params<FULL>(gp, i * IO::kTile, left, g, 1.f);
-                IO::template params<FULL>(bp, i * IO::kTile, left, b, 0.f);
+                IO::template params<FULL>(gp, i * IO::kTile, left, g, 1.f, FULL);
+                if (OP == kLayerNorm) IO::template params<FULL>(bp, i * IO::kTile, left, b, 0.f, FULL);
+                else for (int e = 0; e < IO::NP; ++e) b[e] = f2(0.f);
 #pragma unroll
                 for (int j = 0; j < R; ++j) {
 #pragma unroll
@@ -301,7 +309,7 @@ __global__ void __launch_bounds__(kRingThreads) fwd_ring(NormFwdArgs a, RingShap
                 }
             }
         };
-        if (whole) give(std::true_type()); else give(std::false_type());
+        if (affine) give(yes); else give(no);
         yo += stride * a.cols;
         if (ho) ho += stride * a.cols;
         if (++s == q.stages) {
@@ -458,7 +466,7 @@ cudaError_t run_fwd(const NormFwdArgs& a, int sms, cudaStream_t s) {
     if (tiles <= 2) return run_warp<OP, T, IO, PT, 2>(a, sms, s);
     if (tiles <= 4) return run_warp<OP, T, IO, PT, 4>(a, sms, s);
     RingPlan p;
-    if (!plan_ring(tiles, sizeof(T), a.residual ? 2 : 1, a.rows, sms, &p))
+    if (!plan_ring(tiles, sizeof(T), a.residual ? 2 : 1, 2, a.rows, sms, &p))
         return run_general<OP, T, IO, PT>(a, sms, s);
     if (p.V == 8) return run_ring<OP, T, IO, PT, 8, 1>(a, p, s);
     return p.R == 2 ? run_ring<OP, T, IO, PT, 4, 2>(a, p, s) : run_ring<OP, T, IO, PT, 4, 1>(a, p, s);
@@ -487,7 +495,7 @@ int64_t norm_fwd_partials(int dtype, int64_t rows, int64_t cols, int sms) {
     // call without residual then has room it does not need
     RingPlan p;
     const int tiles = (int)((cols + VecIO<float, 4>::kTile - 1) / VecIO<float, 4>::kTile);
-    if (tiles <= 4 || plan_ring(tiles, dtype == 0 ? 4 : 2, 2, rows, sms, &p)) return 0;
+    if (tiles <= 4 || plan_ring(tiles, dtype == 0 ? 4 : 2, 2, 2, rows, sms, &p)) return 0;
     return rows * train_chunks(cols) * 16;
 }
 

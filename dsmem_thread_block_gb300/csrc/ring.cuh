@@ -93,8 +93,8 @@ __device__ __forceinline__ int ring_shift(const void* src, int64_t off) {
 // part in every peer's slot with st.async and waits on its own mbarrier for
 // the P - 1 deposits and its own arrival.  Slots and mbarriers alternate by
 // turn parity: a peer's deposit for turn k + 2 comes after its wait for turn
-// k + 1, which needs this CTA's deposit for turn k + 1, made after it read the
-// slots of turn k.
+// k + 1, which needs this CTA's deposit for turn k + 1, made after a barrier
+// that follows every thread's reads of the slots of turn k.
 struct RingExchange {
     float4 slots[2][kMaxCluster];
     uint64_t bar[2];
@@ -105,10 +105,9 @@ struct RingExchange {
             mbar_arrive_expect_tx(smem_u32(&bar[b]), (P - 1) * 16u);
         }
     }
-    // All threads of the CTA call, after the barrier that made `v` the same in
-    // all of them.  Returns the P parts of row k.
-    __device__ const float4* all(int64_t k, float4 v, uint32_t P, uint32_t rank, unsigned* err) {
-        const int b = (int)(k & 1);
+    // Warp 0 calls, every lane with the CTA's part of turn k.
+    __device__ void deposit(uint32_t k, float4 v, uint32_t P, uint32_t rank) {
+        const int b = k & 1;
         const uint32_t bb = smem_u32(&bar[b]);
         if (threadIdx.x == rank) {
             slots[b][rank] = v;
@@ -117,9 +116,13 @@ struct RingExchange {
             st_async_v4f32(mapa_shared(smem_u32(&slots[b][rank]), threadIdx.x), v.x, v.y, v.z, v.w,
                            mapa_shared(bb, threadIdx.x));
         }
-        mbar_wait_bounded(bb, (uint32_t)(k >> 1) & 1u, err);
+    }
+    // All threads call: the P parts of turn k, once they are here.
+    __device__ const float4* wait(uint32_t k, uint32_t P, uint32_t rank, unsigned* err) {
+        const uint32_t bb = smem_u32(&bar[k & 1]);
+        mbar_wait_bounded(bb, (k >> 1) & 1u, err);
         if (threadIdx.x == rank) mbar_arrive_expect_tx(bb, (P - 1) * 16u);
-        return slots[b];
+        return slots[k & 1];
     }
 };
 

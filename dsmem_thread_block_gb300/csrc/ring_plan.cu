@@ -18,35 +18,38 @@ constexpr int kMostStage = 220 * 1024;  // shared memory a CTA may spend on its 
 
 }  // namespace
 
-bool plan_ring(int tiles, int es, int streams, int64_t rows, int sms, RingPlan* out) {
-    RingPlan p{};
-    p.V = 4;
-    p.P = (tiles + 4 * kRingWarps - 1) / (4 * kRingWarps);
-    if (getenv("PV8") || p.P > kMaxCluster) {
-        p.V = 8;
-        p.P = (tiles + 8 * kRingWarps - 1) / (8 * kRingWarps);
+bool plan_ring(int tiles, int es, int streams, int turn, int64_t rows, int sms, RingPlan* out) {
+    const int fewest = turn == 1 ? 2 : 1, want = turn == 1 ? 4 : 2;  // stages
+    for (int least : {turn == 1 ? 3 : 1, fewest}) {
+        for (int V : {4, 8}) {
+            if (getenv("PV8") && V == 4) continue;
+            for (int P = (tiles + V * kRingWarps - 1) / (V * kRingWarps); P <= kMaxCluster; ++P) {
+                RingPlan p{};
+                p.V = V;
+                p.shape.tiles = (tiles + P - 1) / P;
+                p.P = (tiles + p.shape.tiles - 1) / p.shape.tiles;  // no CTA without columns
+                p.W = (p.shape.tiles + V - 1) / V;
+                // a slice that starts inside a 16-byte line takes one line more
+                p.shape.room = (p.shape.tiles * kTileCols * es + 16 + 127) / 128 * 128;
+                const int ctas_most = std::max(1, std::min(8, 1024 / (32 * p.W)));  // per SM
+                p.most = std::max(1, sms * ctas_most / p.P);
+                p.R = turn == 2 && V == 4 && rows >= 2 * (int64_t)p.most ? 2 : 1;
+                const int stage = p.shape.room * streams * p.R;
+                const int budget = (getenv("BUD") ? atoi(getenv("BUD")) : turn == 1 ? 200 : 144) * 1024;
+                int ctas = ctas_most;
+                while (ctas > 1 && budget / ctas < want * stage) --ctas;
+                int stages = budget / ctas / stage;
+                if (stages < want) stages = std::min(want, kMostStage / stage);
+                if (stages < least) continue;
+                if (rows * p.P * 2 <= sms) stages = fewest;  // every cluster has one row
+                p.shape.stages = std::min(stages, kRingStages);
+                p.smem = (size_t)p.shape.stages * stage;
+                *out = p;
+                return true;
+            }
+        }
     }
-    if (p.P > kMaxCluster) return false;
-    p.shape.tiles = (tiles + p.P - 1) / p.P;
-    p.P = (tiles + p.shape.tiles - 1) / p.shape.tiles;  // no CTA without columns
-    p.W = (p.shape.tiles + p.V - 1) / p.V;
-    // a slice that starts inside a 16-byte line takes one line more
-    p.shape.room = (p.shape.tiles * kTileCols * es + 16 + 127) / 128 * 128;
-    const int ctas_most = std::max(1, std::min(8, 1024 / (32 * p.W)));  // per SM
-    p.most = std::max(1, sms * ctas_most / p.P);
-    p.R = p.V == 4 && rows >= (getenv("RM") ? atof(getenv("RM")) : 2) * p.most ? 2 : 1;
-    const int stage = p.shape.room * streams * p.R;
-    int ctas = ctas_most;
-    const int budget = (getenv("BUD") ? atoi(getenv("BUD")) : 144) * 1024;
-    while (ctas > 1 && budget / ctas < 2 * stage) --ctas;
-    int stages = budget / ctas / stage;
-    if (stages < 2) stages = kMostStage / stage;
-    if (stages < 1) return false;
-    if (rows * p.P * 2 <= sms) stages = 1;  // every cluster has one row
-    p.shape.stages = std::min(stages, kRingStages);
-    p.smem = (size_t)p.shape.stages * stage;
-    *out = p;
-    return true;
+    return false;
 }
 
 namespace {

@@ -27,8 +27,10 @@ struct RingPlan {
 };
 
 // A shape for rows of `tiles` warp tiles in `streams` streams of `es`-byte
-// elements; false where the rows are too wide.
-bool plan_ring(int tiles, int es, int streams, int64_t rows, int sms, RingPlan* out);
+// elements; `turn`: most rows per turn (2: the forward kernel; 1: the
+// backward kernel, which holds two turns' stages at once).  False where the
+// rows are too wide.
+bool plan_ring(int tiles, int es, int streams, int turn, int64_t rows, int sms, RingPlan* out);
 
 // The clusters of `fn` in this shape that the current device holds at once,
 // and its error word; false on a CUDA error.

@@ -147,9 +147,17 @@ template <typename T, int ELEMS> struct VecIO {
                     make_float4(f[k].x, f[k].y, f[k + 1].x, f[k + 1].y);
         }
     }
+    // `there`: the caller knows that p is not null
     template <bool FULL, typename PT>
     __device__ static __forceinline__ void params(const PT* p, int off, int left, F2* f,
-                                                  float absent) {
+                                                  float absent, bool there = false) {
+        if (FULL && there) {
+            float v[N];
+            load_params<PT, N>(p, off, v);
+#pragma unroll
+            for (int k = 0; k < NP; ++k) f[k] = {v[2 * k], v[2 * k + 1]};
+            return;
+        }
 #pragma unroll
         for (int k = 0; k < NP; ++k) f[k] = f2(absent);
         if (p && in<FULL>(off, 0, left)) load_param_pairs<PT, NP>(p, off, f, absent);
@@ -216,16 +224,16 @@ template <typename T, int ELEMS> struct ElemIO {
     }
     template <bool FULL, typename PT>
     __device__ static __forceinline__ float param1(const PT* p, int off, int k, int left,
-                                                   float absent) {
-        return p && in<FULL>(off, k, left) ? load_param1<PT>(p, off + 32 * k) : absent;
+                                                   float absent, bool there) {
+        return (there || p) && in<FULL>(off, k, left) ? load_param1<PT>(p, off + 32 * k) : absent;
     }
     template <bool FULL, typename PT>
     __device__ static __forceinline__ void params(const PT* p, int off, int left, F2* f,
-                                                  float absent) {
+                                                  float absent, bool there = false) {
 #pragma unroll
         for (int k = 0; k < NP; ++k)
-            f[k] = {param1<FULL>(p, off, 2 * k, left, absent),
-                    param1<FULL>(p, off, 2 * k + 1, left, absent)};
+            f[k] = {param1<FULL>(p, off, 2 * k, left, absent, there),
+                    param1<FULL>(p, off, 2 * k + 1, left, absent, there)};
     }
     // Every lane draws the block of columns 4 lane .. 4 lane + 3 of each 128
     // columns; a ballot per word hands each lane the bits of its own columns
