@@ -138,8 +138,9 @@ struct NormFwdArgs {
     bool half;             // gamma, beta are bf16
     float eps;
     DropArgs drop;
-    float* ws;             // per (row, chunk): count, mean, M2 (RMSNorm: 0, 0, sum of squares)
+    float* ws;             // the sweep's, per (row, chunk): sum, M2 (RMSNorm: sum of squares twice)
     int32_t nch;           // chunks per row
+    int32_t l2_bytes;      // of the device
 };
 
 struct NormBwdArgs {
@@ -158,12 +159,12 @@ struct NormBwdArgs {
     float inv_cols;        // 1 / cols
     bool half;             // gamma and the parameters' gradients are bf16
     DropArgs drop;
-    float* ws;             // per (row, chunk): the sums of dy gamma xh and dy gamma
+    float* ws;             // the sweep's, per (row, chunk): sums of dy gamma xh and dy gamma
     float* pws;            // per row group: dgamma [pitch], then dbeta [pitch]
     int32_t pitch;         // cols rounded up to whole tiles
     int32_t nch;           // chunks per row
     int32_t groups;        // row groups of the parameter sums
-    int64_t group_rows;    // rows of one group
+    int64_t batch;         // rows of one batch of the sweep
 };
 
 // Kernel selector of the training operators (types as in KernelKey).
@@ -173,17 +174,16 @@ struct TrainKey {
 };
 
 // Workspace of a backward call: `partials` bytes of row sums, then
-// room_groups groups' sums; groups and group_rows are the general form's (and
-// the one-warp form's groups).
+// room_groups groups' sums.  groups: of the one-warp form or the sweep (the
+// ring's are its grid's).
 struct TrainLayout {
-    int64_t partials;
+    int64_t partials, batch;
     int32_t nch, groups, room_groups, pitch;
-    int64_t group_rows;
 };
 
-int train_chunks(int64_t cols);
+int train_chunks(int dtype, int64_t cols);
 int64_t norm_fwd_partials(int dtype, int64_t rows, int64_t cols, int sms);  // bytes
-TrainLayout norm_bwd_layout(int dtype, int64_t rows, int64_t cols, int sms);
+TrainLayout norm_bwd_layout(int dtype, int64_t rows, int64_t cols, int sms, int l2_bytes);
 cudaError_t launch_dropout(int dtype, bool vec, const DropoutArgs& a, int sms, cudaStream_t s);
 cudaError_t launch_norm_fwd(TrainKey k, const NormFwdArgs& a, int sms, cudaStream_t s);
 cudaError_t launch_norm_bwd(TrainKey k, NormBwdArgs a, int sms, cudaStream_t s);

@@ -8,8 +8,8 @@
 //   bwd_warp   one warp per row
 //   bwd_ring   a CTA, or a cluster, per row; the next rows' dy, h and dh
 //              arrive in a ring of shared-memory stages
-//   bwd_stats, bwd_apply   wider rows: the two row sums per chunk, then a
-//              second read by CTAs that own a strip of columns
+//   bwd_sweep  wider rows: the two row sums per chunk, then a second read, from
+//              L2 (sweep.cuh)
 // In each a thread keeps the same columns for all its rows and sums their
 // dgamma and dbeta in registers; the row groups' sums go to the workspace and
 // bwd_params adds them.  Every sum has a fixed order: results repeat bit for
@@ -18,6 +18,7 @@
 
 #include "planner.h"
 #include "ring.cuh"
+#include "sweep.cuh"
 
 namespace credit {
 
@@ -25,9 +26,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTilesPerWarp = 4;
-constexpr int kChunkTiles = kWarps * kTilesPerWarp;
-constexpr int kRowBlock = 32;  // rows whose sums a CTA merges at a time
 
 struct RowStats { float mean, rstd; };
 
@@ -370,94 +368,139 @@ __global__ void __launch_bounds__(kRingThreads) bwd_ring(NormBwdArgs a, RingShap
     }
 }
 
-// ------------------------------------------------------------- general form
+// ------------------------------------------------------------- wider rows
+// One launch of sweep.cuh: the two row sums of one batch, outputs of the batch
+// before and its rows' part of the parameters' gradients, which the blocks of
+// one (strip, group) add up from batch to batch.
 template <int OP, typename T, typename IO, typename PT>
-__global__ void __launch_bounds__(kThreads) bwd_stats(NormBwdArgs a) {
-    __shared__ float red[2][2 * kWarps];
+__global__ void __launch_bounds__(kSweepThreads, kSweepCtas) bwd_sweep(NormBwdArgs a, Sweep q) {
+    constexpr int kChunk = sweep_chunk(IO::N), kStrip = sweep_strip(IO::N);
+    __shared__ float part[2][2 * kSweepRows][kSweepWarps];
+    __shared__ float4 rowc[kSweepGroup];  // mean, rstd, mean_j(w xh), mean_j(w)
+    wait_for_previous_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t items = a.rows * a.nch;
-    int turn = 0;
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x, turn ^= 1) {
-        const int64_t row = it / a.nch;
-        const int c0 = (int)(it - row * a.nch) * (kChunkTiles * IO::kTile);
-        const int j0 = c0 + warp * kTilesPerWarp * IO::kTile + IO::first(lane), left = a.cols - j0;
-        const T* dy = static_cast<const T*>(a.dy) + row * a.cols + j0;
-        const T* hp = static_cast<const T*>(a.h) + row * a.cols + j0;
-        const PT* gp = moved(static_cast<const PT*>(a.gamma), j0);
-        const RowStats r = row_stats<OP>(a, row);
-        F2 s1 = f2(0.f), s2 = f2(0.f);
+    float2* const ws = reinterpret_cast<float2*>(a.ws);
+    uint32_t index;
+    if (sweep_sums(q, blockIdx.x, &index)) {
+        const int chunk = (int)(index % (uint32_t)a.nch);
+        const int64_t r0 = q.s0 + (int64_t)(index / (uint32_t)a.nch) * kSweepGroup;
+        const int64_t r1 = min(q.s1, r0 + kSweepGroup);
+        const int j0 = chunk * kChunk + warp * kSweepTiles * IO::kTile + IO::first(lane);
+        const int left = a.cols - j0;
+        const T* const dyp = static_cast<const T*>(a.dy) + j0;
+        const T* const hp = static_cast<const T*>(a.h) + j0;
+        F2 g[kSweepTiles][IO::NP];
 #pragma unroll
-        for (int i = 0; i < kTilesPerWarp; ++i) {
-            F2 u[IO::NP], h[IO::NP], g[IO::NP];
-            unpack<T, IO::NP>(IO::template load<false>(dy, i * IO::kTile, left), u);
-            unpack<T, IO::NP>(IO::template load<false>(hp, i * IO::kTile, left), h);
-            IO::template params<false>(gp, i * IO::kTile, left, g, 1.f);
+        for (int i = 0; i < kSweepTiles; ++i)
+            IO::template params<false>(moved(static_cast<const PT*>(a.gamma), j0), i * IO::kTile,
+                                       left, g[i], 1.f);
+        int turn = 0;
+        for (int64_t r = r0; r < r1; r += kSweepRows, turn ^= 1) {
+            typename IO::R yv[kSweepRows][kSweepTiles], hv[kSweepRows][kSweepTiles];
+            RowStats st[kSweepRows];
+            float v[2 * kSweepRows];
 #pragma unroll
-            for (int k = 0; k < IO::NP; ++k) {
-                const F2 w = mul2(u[k], g[k]);  // 0 past the row
-                s1 = fma2(w, normalised<OP>(h[k], r), s1);
-                s2 = add2(s2, w);
+            for (int j = 0; j < kSweepRows; ++j) {
+                const int64_t row = min(r + j, r1 - 1);  // past the group: its last row
+                st[j] = row_stats<OP>(a, row);
+#pragma unroll
+                for (int i = 0; i < kSweepTiles; ++i) {
+                    yv[j][i] = IO::template load<false>(dyp + row * a.cols, i * IO::kTile, left);
+                    hv[j][i] = IO::template load<false>(hp + row * a.cols, i * IO::kTile, left);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kSweepRows; ++j) {
+                F2 s1 = f2(0.f), s2 = f2(0.f);
+#pragma unroll
+                for (int i = 0; i < kSweepTiles; ++i) {
+                    F2 u[IO::NP], h[IO::NP];
+                    unpack<T, IO::NP>(yv[j][i], u);
+                    unpack<T, IO::NP>(hv[j][i], h);
+#pragma unroll
+                    for (int e = 0; e < IO::NP; ++e) {
+                        const F2 w = mul2(u[e], g[i][e]);  // 0 past the row
+                        s1 = fma2(w, normalised<OP>(h[e], st[j]), s1);
+                        s2 = add2(s2, w);
+                    }
+                }
+                v[2 * j] = s1.x + s1.y;
+                v[2 * j + 1] = s2.x + s2.y;
+            }
+            constexpr int G = 32 / (2 * kSweepRows);
+            const float sum = sums_over_warp<2 * kSweepRows>(v, lane);
+            if (lane % G == 0) part[turn][lane / G][warp] = sum;
+            __syncthreads();
+            if (threadIdx.x < kSweepRows && r + threadIdx.x < r1) {
+                float2 t = make_float2(0.f, 0.f);
+                for (int k = 0; k < kSweepWarps; ++k) {
+                    t.x += part[turn][2 * threadIdx.x][k];
+                    t.y += part[turn][2 * threadIdx.x + 1][k];
+                }
+                ws[(r + threadIdx.x) * a.nch + chunk] = t;
             }
         }
-        float t1 = s1.x + s1.y, t2 = s2.x + s2.y;
-        block_sum2(t1, t2, red[turn], kWarps, kThreads);
-        if (threadIdx.x == 0) {
-            a.ws[2 * it] = t1;
-            a.ws[2 * it + 1] = t2;
-        }
+        return;
     }
-}
-
-template <int OP, typename T, typename IO, typename PT>
-__global__ void __launch_bounds__(kThreads) bwd_apply(NormBwdArgs a) {
-    __shared__ float4 rowc[kRowBlock];  // mean, rstd, mean_j(w xh), mean_j(w)
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const DropStream d(a.drop);
-    const int base = ((int)blockIdx.x * kWarps + warp) * IO::kTile;
-    const int j0 = base + IO::first(lane), left = a.cols - j0;
-    const bool mine = base < a.cols;
-    F2 g[IO::NP], ag[IO::NP], ab[IO::NP];
-#pragma unroll
-    for (int k = 0; k < IO::NP; ++k) ag[k] = ab[k] = f2(0.f);
-    if (mine)
-        IO::template params<false>(moved(static_cast<const PT*>(a.gamma), j0), 0, left, g, 1.f);
-    const int64_t r1 = min(a.rows, (int64_t)(blockIdx.y + 1) * a.group_rows);
-    for (int64_t r0 = (int64_t)blockIdx.y * a.group_rows; r0 < r1; r0 += kRowBlock) {
-        const int nr = (int)min((int64_t)kRowBlock, r1 - r0);
-        __syncthreads();
-        for (int i = warp; i < nr; i += kWarps) {
-            const float* w = a.ws + (r0 + i) * a.nch * 2;
-            float s1 = 0.f, s2 = 0.f;
-            for (int c = lane; c < a.nch; c += 32) {
-                s1 += w[2 * c];
-                s2 += w[2 * c + 1];
-            }
-            s1 = warp_allreduce(s1, SumOp());
-            s2 = warp_allreduce(s2, SumOp());
-            const RowStats r = row_stats<OP>(a, r0 + i);
-            if (lane == 0)
-                rowc[i] = make_float4(r.mean, r.rstd, s1 * a.inv_cols, s2 * a.inv_cols);
+    const int strips = (a.cols + kStrip - 1) / kStrip, strip = (int)(index % (uint32_t)strips);
+    const int group = (int)(index / (uint32_t)strips);
+    const int64_t r0 = q.b0 + (int64_t)group * kSweepGroup;
+    const int nr = (int)(min(q.b1, r0 + kSweepGroup) - r0);
+    for (int i = warp; i < nr; i += kSweepWarps) {
+        const float2* w = ws + (r0 + i) * a.nch;
+        float s1 = 0.f, s2 = 0.f;
+        for (int c = lane; c < a.nch; c += 32) {
+            const float2 t = __ldcg(w + c);
+            s1 += t.x;
+            s2 += t.y;
         }
-        __syncthreads();
-        if (!mine) continue;
-#pragma unroll 2
-        for (int i = 0; i < nr; ++i) {
-            const int64_t o = (r0 + i) * a.cols + j0;
-            const float4 c = rowc[i];
-            F2 u[IO::NP], h[IO::NP], dh[IO::NP], s1, s2;
-            unpack<T, IO::NP>(IO::template load<false>(static_cast<const T*>(a.dy) + o, 0, left), u);
-            unpack<T, IO::NP>(IO::template load<false>(static_cast<const T*>(a.h) + o, 0, left), h);
-            if (a.dh)
-                unpack<T, IO::NP>(IO::template load<false>(static_cast<const T*>(a.dh) + o, 0, left),
-                                  dh);
-            s1 = s2 = f2(0.f);
-            tile_sums<OP, IO::NP>(u, h, g, {c.x, c.y}, s1, s2, ag, ab);
-            tile_out<OP, T, IO, false>(d, u, h, g, a.dh != nullptr, dh, {c.x, c.y},
-                                       RowBack({c.x, c.y}, c.z, c.w), r0 + i, base, 0, left, lane, a.drop.on, static_cast<T*>(a.dx) + o,
-                                       moved(static_cast<T*>(a.dres), o));
+        s1 = warp_allreduce(s1, SumOp());
+        s2 = warp_allreduce(s2, SumOp());
+        const RowStats st = row_stats<OP>(a, r0 + i);
+        if (lane == 0) rowc[i] = make_float4(st.mean, st.rstd, s1 * a.inv_cols, s2 * a.inv_cols);
+    }
+    __syncthreads();
+    const int base = strip * kStrip + warp * IO::kTile;
+    if (base >= a.cols) return;
+    const int j0 = base + IO::first(lane), left = a.cols - j0;
+    F2 g[IO::NP], ag[IO::NP], ab[IO::NP];
+    IO::template params<false>(moved(static_cast<const PT*>(a.gamma), j0), 0, left, g, 1.f);
+#pragma unroll
+    for (int e = 0; e < IO::NP; ++e) ag[e] = ab[e] = f2(0.f);
+    for (int i = 0; i < nr; i += kSweepRows) {
+        typename IO::R yv[kSweepRows], hv[kSweepRows], dv[kSweepRows];
+#pragma unroll
+        for (int j = 0; j < kSweepRows; ++j) {
+            const int64_t at = (r0 + min(i + j, nr - 1)) * a.cols + j0;
+            yv[j] = IO::template load<false>(static_cast<const T*>(a.dy) + at, 0, left);
+            hv[j] = IO::template load<false>(static_cast<const T*>(a.h) + at, 0, left);
+            if (a.dh) dv[j] = IO::template load<false>(static_cast<const T*>(a.dh) + at, 0, left);
+        }
+#pragma unroll
+        for (int j = 0; j < kSweepRows; ++j) {
+            if (i + j >= nr) break;
+            const int64_t at = (r0 + i + j) * a.cols + j0;
+            const float4 c = rowc[i + j];
+            const RowStats st{c.x, c.y};
+            F2 u[IO::NP], h[IO::NP], dh[IO::NP], s1 = f2(0.f), s2 = f2(0.f);
+            unpack<T, IO::NP>(yv[j], u);
+            unpack<T, IO::NP>(hv[j], h);
+            if (a.dh) unpack<T, IO::NP>(dv[j], dh);
+            tile_sums<OP, IO::NP>(u, h, g, st, s1, s2, ag, ab);
+            tile_out<OP, T, IO, false>(d, u, h, g, a.dh != nullptr, dh, st, RowBack(st, c.z, c.w),
+                                       r0 + i + j, base, 0, left, lane, a.drop.on,
+                                       static_cast<T*>(a.dx) + at,
+                                       moved(static_cast<T*>(a.dres), at));
         }
     }
-    if (mine) tile_params<OP, IO>(a, blockIdx.y, j0, 0, left, ag, ab);
+    // the earlier batches' sums of these columns, then this one's
+    float* const p = a.pws + (int64_t)group * 2 * a.pitch + j0;
+    if (!q.first) {
+        if (a.dgamma) IO::add_sums(p, left, ag);
+        if (OP == kLayerNorm && a.dbeta) IO::add_sums(p + a.pitch, left, ab);
+    }
+    tile_params<OP, IO>(a, group, j0, 0, left, ag, ab);
 }
 
 __device__ __forceinline__ void store_param(void* p, bool half, int64_t j, float v) {
@@ -492,90 +535,90 @@ __global__ void __launch_bounds__(kThreads) bwd_params(NormBwdArgs a) {
     }
 }
 
-template <int OP, typename T, typename IO, typename PT>
-cudaError_t run_general(const NormBwdArgs& a, int sms, cudaStream_t s) {
-    const int64_t items = a.rows * a.nch;
-    const unsigned grid = (unsigned)(items < (int64_t)sms * 32 ? items : (int64_t)sms * 32);
-    bwd_stats<OP, T, IO, PT><<<grid, kThreads, 0, s>>>(a);
-    const int strip = kWarps * IO::kTile;
-    bwd_apply<OP, T, IO, PT><<<dim3((unsigned)((a.cols + strip - 1) / strip), (unsigned)a.groups),
-                           kThreads, 0, s>>>(a);
-    return cudaGetLastError();
-}
-
 template <int OP, typename T, typename IO, typename PT, int V>
 cudaError_t run_warp(const NormBwdArgs& a, cudaStream_t s) {
     bwd_warp<OP, T, IO, PT, V><<<(unsigned)a.groups, kThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
-template <int OP, typename T, typename IO, typename PT, int V>
-cudaError_t run_ring(NormBwdArgs& a, const RingPlan& p, cudaStream_t s) {
-    const void* fn = (const void*)bwd_ring<OP, T, IO, PT, V>;
-    int resident;
-    unsigned* err;
-    if (!ring_resident(fn, p, &resident, &err)) return cudaErrorInvalidConfiguration;
-    a.groups = ring_grid(p, resident, a.rows);  // at most the layout's
-    return launch_ring(fn, a, p, a.groups, err, s);
-}
-
-template <int OP, typename T, typename IO, typename PT>
+// IO and WIO: the access forms of the ring and warp kernels and of the sweep.
+template <int OP, typename T, typename IO, typename WIO, typename PT>
 cudaError_t run_bwd(NormBwdArgs& a, int sms, cudaStream_t s) {
     const int tiles = (a.cols + IO::kTile - 1) / IO::kTile;
     if (tiles <= 1) return run_warp<OP, T, IO, PT, 1>(a, s);
     if (tiles <= 2) return run_warp<OP, T, IO, PT, 2>(a, s);
     if (tiles <= 4) return run_warp<OP, T, IO, PT, 4>(a, s);
+    const int streams = a.dh ? 3 : 2;
+    if (!ring_fits(tiles, sizeof(T), streams, 1, a.rows, sms))
+        return run_sweep((const void*)bwd_sweep<OP, T, WIO, PT>, a, a.batch, WIO::N, s);
+    const RingKernels fn{(const void*)bwd_ring<OP, T, IO, PT, 4>, nullptr,
+                         (const void*)bwd_ring<OP, T, IO, PT, 8>};
     RingPlan p;
-    if (!plan_ring(tiles, sizeof(T), a.dh ? 3 : 2, 1, a.rows, sms, &p))
-        return run_general<OP, T, IO, PT>(a, sms, s);
-    return p.V == 4 ? run_ring<OP, T, IO, PT, 4>(a, p, s) : run_ring<OP, T, IO, PT, 8>(a, p, s);
+    int resident;
+    unsigned* err;
+    if (!plan_ring(tiles, sizeof(T), streams, 1, a.rows, sms, fn, &p, &resident, &err))
+        return cudaErrorInvalidConfiguration;
+    a.groups = ring_grid(p, resident, a.rows);  // at most the layout's
+    return launch_ring(fn.of(p), a, p, a.groups, err, s);
 }
 
-template <int OP, typename T, typename IO>
+template <int OP, typename T, typename IO, typename WIO>
 cudaError_t pick_param(NormBwdArgs& a, int sms, cudaStream_t s) {
-    return a.half ? run_bwd<OP, T, IO, bf16>(a, sms, s) : run_bwd<OP, T, IO, float>(a, sms, s);
+    return a.half ? run_bwd<OP, T, IO, WIO, bf16>(a, sms, s)
+                  : run_bwd<OP, T, IO, WIO, float>(a, sms, s);
 }
 
 template <int OP, typename T>
 cudaError_t pick_bwd(TrainKey k, NormBwdArgs& a, int sms, cudaStream_t s) {
-    return k.vec ? pick_param<OP, T, VecIO<T, 4>>(a, sms, s)
-                 : pick_param<OP, T, ElemIO<T, 4>>(a, sms, s);
+    constexpr int N = 16 / (int)sizeof(T);
+    return k.vec ? pick_param<OP, T, VecIO<T, 4>, VecIO<T, N>>(a, sms, s)
+                 : pick_param<OP, T, ElemIO<T, 4>, ElemIO<T, N>>(a, sms, s);
 }
 
 constexpr int kTileCols = VecIO<float, 4>::kTile;
 
 }  // namespace
 
-TrainLayout norm_bwd_layout(int dtype, int64_t rows, int64_t cols, int sms) {
+namespace {
+
+TrainLayout bwd_layout(int dtype, int64_t rows, int64_t cols, int sms, int l2_bytes) {
     TrainLayout l{};
+    const int es = dtype == 0 ? 4 : 2;
     l.pitch = (int)((cols + kTileCols - 1) / kTileCols * kTileCols);
-    l.nch = train_chunks(cols);
-    l.group_rows = 1;
+    l.nch = train_chunks(dtype, cols);
     if (rows == 0) return l;
     const int tiles = l.pitch / kTileCols;
     if (tiles <= 4) {  // one warp per row
         const int64_t want = (rows + kWarps - 1) / kWarps;
-        l.groups = (int)(want < sms * 2 ? want : sms * 2);
-    } else {
-        // the ring's grid and the general form's groups, whichever is larger:
-        // which of them runs depends on the call's streams too
-        const int64_t strips = (tiles + kWarps - 1) / kWarps;
-        int64_t g = (4 * (int64_t)sms + strips - 1) / strips;
-        g = std::max<int64_t>(1, std::min<int64_t>(g, (rows + 7) / 8));
-        l.group_rows = (rows + g - 1) / g;
-        l.groups = (int)((rows + l.group_rows - 1) / l.group_rows);
-        l.room_groups = l.groups;
-        for (int streams = 2; streams <= 3; ++streams) {
-            RingPlan p;
-            if (plan_ring(tiles, dtype == 0 ? 4 : 2, streams, 1, rows, sms, &p))
-                l.room_groups = (int)std::max<int64_t>(l.room_groups, std::min<int64_t>(p.most, rows));
-        }
-        // the general form's partials, where it may run
-        RingPlan p;
-        if (!plan_ring(tiles, dtype == 0 ? 4 : 2, 3, 1, rows, sms, &p)) l.partials = rows * l.nch * 8;
+        l.groups = l.room_groups = (int)(want < sms * 2 ? want : sms * 2);
+        return l;
     }
-    l.room_groups = std::max(l.room_groups, l.groups);
+    // the ring's grid and the sweep's groups, whichever is larger: which of
+    // them runs depends on the call's streams too
+    l.batch = sweep_batch(rows, cols * 2 * es, l2_bytes);
+    l.groups = (int)((std::min(rows, l.batch) + kSweepGroup - 1) / kSweepGroup);
+    for (int streams = 2; streams <= 3; ++streams) {
+        if (ring_fits(tiles, es, streams, 1, rows, sms)) {
+            l.room_groups = (int)std::max<int64_t>(
+                l.room_groups, ring_groups_bound(tiles, es, streams, rows, sms));
+        } else {
+            l.room_groups = std::max(l.room_groups, l.groups);
+            l.partials = rows * l.nch * 8;
+        }
+    }
     return l;
+}
+
+}  // namespace
+
+TrainLayout norm_bwd_layout(int dtype, int64_t rows, int64_t cols, int sms, int l2_bytes) {
+    // the last shape's answer, as a training step asks for few shapes in turn
+    struct Known { int dtype, sms, l2; int64_t rows, cols; TrainLayout l; };
+    static thread_local Known known[8] = {};
+    Known& k = known[(uint64_t)(rows * 31 + cols * 7 + dtype) % 8];
+    if (k.sms == sms && k.l2 == l2_bytes && k.dtype == dtype && k.rows == rows && k.cols == cols) return k.l;
+    k = Known{dtype, sms, l2_bytes, rows, cols, bwd_layout(dtype, rows, cols, sms, l2_bytes)};
+    return k.l;
 }
 
 cudaError_t launch_norm_bwd(TrainKey k, NormBwdArgs a, int sms, cudaStream_t s) {

@@ -5,14 +5,15 @@
 //   fwd_warp   one warp holds a row's h in registers
 //   fwd_ring   a CTA, or a cluster, holds it; the next rows' x and residual
 //              arrive in a ring of shared-memory stages meanwhile
-//   fwd_stats, fwd_apply   wider rows: partial statistics per chunk, then a
-//              second read (from L2 where the rows fit it)
-// The first two read x and residual once and write h and y once.
+//   fwd_sweep  wider rows: partial statistics per chunk, then a second read,
+//              from L2 (sweep.cuh)
+// Each reads x and residual from HBM once and writes h and y once.
 //
 // Statistics: sum and M2 about the piece's own mean (of a warp, a CTA or a
 // chunk), merged with the parallel-axis form of Chan et al.'s update.
 #include "planner.h"
 #include "ring.cuh"
+#include "sweep.cuh"
 
 namespace credit {
 
@@ -20,8 +21,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTilesPerWarp = 4;
-constexpr int kChunkTiles = kWarps * kTilesPerWarp;
 
 // (h - mean) rstd gamma + beta; rstd is CUDA's rsqrtf (2 ulp).  The mean is
 // subtracted first, so that a mean far above the deviation costs nothing.
@@ -323,123 +322,159 @@ __global__ void __launch_bounds__(kRingThreads) fwd_ring(NormFwdArgs a, RingShap
     }
 }
 
-// ------------------------------------------------------------- general form
-// Merge a row's nch partials; every lane of the calling warp returns the same.
-template <int OP>
-__device__ __forceinline__ NormPart merge_row(const float* ws, int nch, int lane) {
-    NormPart r{0.f, 0.f, 0.f};
-    if constexpr (OP == kLayerNorm) {
-        float n = 0.f, nm = 0.f;
-        for (int c = lane; c < nch; c += 32) {
-            n += ws[4 * c];
-            nm = fmaf(ws[4 * c], ws[4 * c + 1], nm);
-        }
-        n = warp_allreduce(n, SumOp());
-        nm = warp_allreduce(nm, SumOp());
-        r.n = n;
-        r.mu = nm / n;
-        for (int c = lane; c < nch; c += 32) {
-            const float d = ws[4 * c + 1] - r.mu;
-            r.m2 += fmaf(ws[4 * c] * d, d, ws[4 * c + 2]);
-        }
-    } else {
-        for (int c = lane; c < nch; c += 32) r.m2 += ws[4 * c + 2];
-    }
-    r.m2 = warp_allreduce(r.m2, SumOp());
-    return r;
-}
-
-template <int OP, typename T, typename IO>
-__global__ void __launch_bounds__(kThreads) fwd_stats(NormFwdArgs a) {
-    __shared__ float red[2][kWarps];
+// ------------------------------------------------------------- wider rows
+// One launch of sweep.cuh: row sums of one batch, outputs of the batch before.
+// The sums of a row and chunk are (sum, M2 about the chunk's mean).
+template <int OP, typename T, typename IO, typename PT>
+__global__ void __launch_bounds__(kSweepThreads, kSweepCtas) fwd_sweep(NormFwdArgs a, Sweep q) {
+    constexpr int kChunk = sweep_chunk(IO::N), kStrip = sweep_strip(IO::N);
+    __shared__ float2 part[2][kSweepRows][kSweepWarps];
+    __shared__ float2 rowc[kSweepGroup];  // mean, rstd
+    wait_for_previous_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const DropStream d(a.drop);
-    const int64_t items = a.rows * a.nch;
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-        const int64_t row = it / a.nch;
-        const int c0 = (int)(it - row * a.nch) * (kChunkTiles * IO::kTile);
-        const int base0 = c0 + warp * kTilesPerWarp * IO::kTile;
+    float2* const ws = reinterpret_cast<float2*>(a.ws);
+    uint32_t index;
+    if (sweep_sums(q, blockIdx.x, &index)) {
+        const int chunk = (int)(index % (uint32_t)a.nch);
+        const int64_t r0 = q.s0 + (int64_t)(index / (uint32_t)a.nch) * kSweepGroup;
+        const int64_t r1 = min(q.s1, r0 + kSweepGroup);
+        const int base0 = chunk * kChunk + warp * kSweepTiles * IO::kTile;
         const int j0 = base0 + IO::first(lane), left = a.cols - j0;
-        const T* x = static_cast<const T*>(a.x) + row * a.cols + j0;
-        const T* r = moved(static_cast<const T*>(a.residual), row * a.cols + j0);
-        F2 h[kTilesPerWarp][IO::NP], s2 = f2(0.f);
+        const T* const x = static_cast<const T*>(a.x) + j0;
+        const T* const res = moved(static_cast<const T*>(a.residual), j0);
+        const float n = (float)max(0, min(a.cols - base0, kSweepTiles * IO::kTile));
+        const float inv_n = 1.f / fmaxf(n, 1.f);
+        int turn = 0;
+        for (int64_t r = r0; r < r1; r += kSweepRows, turn ^= 1) {
+            typename IO::R xv[kSweepRows][kSweepTiles], rv[kSweepRows][kSweepTiles];
+            F2 h[kSweepRows][kSweepTiles][IO::NP];
+            float v[kSweepRows];
 #pragma unroll
-        for (int i = 0; i < kTilesPerWarp; ++i) {
-            typename IO::R rv = {};
-            if (r) rv = IO::template load<false>(r, i * IO::kTile, left);
-            tile_h<T, IO>(IO::template load<false>(x, i * IO::kTile, left), rv, r != nullptr,
-                          a.drop.on && base0 + i * IO::kTile < a.cols, d, base0 + i * IO::kTile,
-                          lane, (uint32_t)row, h[i]);
+            for (int j = 0; j < kSweepRows; ++j) {
+                const int64_t at = min(r + j, r1 - 1) * a.cols;  // past the group: its last row
 #pragma unroll
-            for (int k = 0; k < IO::NP; ++k)
-                s2 = OP == kLayerNorm ? add2(s2, h[i][k]) : fma2(h[i][k], h[i][k], s2);
-        }
-        float m2 = block_allreduce(s2.x + s2.y, red[0], SumOp(), 0.f), mu = 0.f;
-        const float n = (float)min(a.cols - c0, kChunkTiles * IO::kTile);
-        if constexpr (OP == kLayerNorm) {
-            mu = m2 / n;
-            s2 = f2(0.f);
-#pragma unroll
-            for (int i = 0; i < kTilesPerWarp; ++i) {
-#pragma unroll
-                for (int k = 0; k < IO::NP; ++k) {
-                    const F2 e =
-                        inside<false, IO>(add2(h[i][k], f2(-mu)), i * IO::kTile, k, left);
-                    s2 = fma2(e, e, s2);
+                for (int i = 0; i < kSweepTiles; ++i) {
+                    xv[j][i] = IO::template load<false>(x + at, i * IO::kTile, left);
+                    if (res) rv[j][i] = IO::template load<false>(res + at, i * IO::kTile, left);
                 }
             }
-            m2 = block_allreduce(s2.x + s2.y, red[1], SumOp(), 0.f);
-        } else {
-            __syncthreads();  // red[0] is rewritten by the next item
-        }
-        if (threadIdx.x == 0) {
-            float* w = a.ws + it * 4;
-            w[0] = n;
-            w[1] = mu;
-            w[2] = m2;
-        }
-    }
-}
-
-template <int OP, typename T, typename IO, typename PT>
-__global__ void __launch_bounds__(kThreads) fwd_apply(NormFwdArgs a) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const DropStream d(a.drop);
-    const int64_t items = a.rows * a.nch;
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-        const int64_t row = it / a.nch;
-        const int c0 = (int)(it - row * a.nch) * (kChunkTiles * IO::kTile);
-        const NormPart st = merge_row<OP>(a.ws + row * a.nch * 4, a.nch, lane);
-        const int base0 = c0 + warp * kTilesPerWarp * IO::kTile;
-        const int j0 = base0 + IO::first(lane), left = a.cols - j0;
-        const int64_t at = row * a.cols + j0;
-        const T* x = static_cast<const T*>(a.x) + at;
-        const T* r = moved(static_cast<const T*>(a.residual), at);
-        F2 h[kTilesPerWarp][IO::NP];
 #pragma unroll
-        for (int i = 0; i < kTilesPerWarp; ++i) {
-            typename IO::R rv = {};
-            if (r) rv = IO::template load<false>(r, i * IO::kTile, left);
-            tile_h<T, IO>(IO::template load<false>(x, i * IO::kTile, left), rv, r != nullptr,
-                          a.drop.on && base0 + i * IO::kTile < a.cols, d, base0 + i * IO::kTile,
-                          lane, (uint32_t)row, h[i]);
-            if (a.h)
-                IO::template store<false>(static_cast<T*>(a.h) + at, i * IO::kTile, left, h[i]);
+            for (int j = 0; j < kSweepRows; ++j) {
+                F2 t = f2(0.f);
+#pragma unroll
+                for (int i = 0; i < kSweepTiles; ++i) {
+                    const int base = base0 + i * IO::kTile;
+                    tile_h<T, IO>(xv[j][i], rv[j][i], res != nullptr, a.drop.on && base < a.cols, d,
+                                  base, lane, (uint32_t)min(r + j, r1 - 1), h[j][i]);
+#pragma unroll
+                    for (int e = 0; e < IO::NP; ++e)
+                        t = OP == kLayerNorm ? add2(t, h[j][i][e]) : fma2(h[j][i][e], h[j][i][e], t);
+                }
+                v[j] = t.x + t.y;
+            }
+            constexpr int G = 32 / kSweepRows;
+            const float sum = sums_over_warp<kSweepRows>(v, lane);
+            float m2 = sum;
+            if constexpr (OP == kLayerNorm) {
+#pragma unroll
+                for (int j = 0; j < kSweepRows; ++j) {
+                    const float mu = __shfl_sync(0xffffffffu, sum, j * G) * inv_n;
+                    F2 t = f2(0.f);
+#pragma unroll
+                    for (int i = 0; i < kSweepTiles; ++i)
+#pragma unroll
+                        for (int e = 0; e < IO::NP; ++e) {
+                            const F2 z = inside<false, IO>(add2(h[j][i][e], f2(-mu)), i * IO::kTile,
+                                                           e, left);
+                            t = fma2(z, z, t);
+                        }
+                    v[j] = t.x + t.y;
+                }
+                m2 = sums_over_warp<kSweepRows>(v, lane);
+            }
+            if (lane % G == 0) part[turn][lane / G][warp] = make_float2(sum, m2);
+            __syncthreads();
+            if (threadIdx.x < kSweepRows && r + threadIdx.x < r1) {
+                // the warps' parts of the chunk, merged about the chunk's mean
+                const float2* w = part[turn][threadIdx.x];
+                float total = 0.f, dev = 0.f;
+                for (int k = 0; k < kSweepWarps; ++k) total += w[k].x;
+                const int c0 = chunk * kChunk;
+                const float mu = total / (float)min(a.cols - c0, kChunk);
+                for (int k = 0; k < kSweepWarps; ++k) {
+                    dev += w[k].y;
+                    if constexpr (OP == kLayerNorm) {
+                        const float wn = (float)max(0, min(a.cols - c0 - k * kSweepTiles * IO::kTile,
+                                                           kSweepTiles * IO::kTile));
+                        const float e = wn > 0.f ? w[k].x / wn - mu : 0.f;
+                        dev = fmaf(wn * e, e, dev);
+                    }
+                }
+                ws[(r + threadIdx.x) * a.nch + chunk] = make_float2(total, dev);
+            }
         }
-        const float rstd = finish(a, row, c0 == 0 && threadIdx.x == 0, st.mu, st.m2);
-        write_tiles<OP, T, IO, kTilesPerWarp, false>(
-            h, moved(static_cast<const PT*>(a.gamma), j0), moved(static_cast<const PT*>(a.beta), j0),
-            static_cast<T*>(a.y) + at, left, st.mu, rstd);
+        return;
     }
-}
-
-template <int OP, typename T, typename IO, typename PT>
-cudaError_t run_general(const NormFwdArgs& a, int sms, cudaStream_t s) {
-    const int64_t items = a.rows * a.nch;
-    const unsigned grid = (unsigned)(items < (int64_t)sms * 32 ? items : (int64_t)sms * 32);
-    fwd_stats<OP, T, IO><<<grid, kThreads, 0, s>>>(a);
-    fwd_apply<OP, T, IO, PT><<<grid, kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    const int strips = (a.cols + kStrip - 1) / kStrip, strip = (int)(index % (uint32_t)strips);
+    const int64_t r0 = q.b0 + (int64_t)(index / (uint32_t)strips) * kSweepGroup;
+    const int nr = (int)(min(q.b1, r0 + kSweepGroup) - r0);
+    for (int i = warp; i < nr; i += kSweepWarps) {
+        const float2* w = ws + (r0 + i) * a.nch;
+        float sum = 0.f, m2 = 0.f, mu = 0.f;
+        if constexpr (OP == kLayerNorm) {
+            for (int c = lane; c < a.nch; c += 32) sum += __ldcg(w + c).x;
+            mu = warp_allreduce(sum, SumOp()) * a.inv_cols;
+        }
+        for (int c = lane; c < a.nch; c += 32) {
+            const float2 p = __ldcg(w + c);
+            m2 += p.y;
+            if constexpr (OP == kLayerNorm) {
+                const float n = (float)min(a.cols - c * kChunk, kChunk);
+                const float e = p.x / n - mu;
+                m2 = fmaf(n * e, e, m2);
+            }
+        }
+        m2 = warp_allreduce(m2, SumOp());
+        const float rstd = rsqrtf(fmaf(m2, a.inv_cols, a.eps));
+        if (lane == 0) {
+            rowc[i] = make_float2(mu, rstd);
+            if (strip == 0) {
+                if (a.mean) a.mean[r0 + i] = mu;
+                if (a.rstd) a.rstd[r0 + i] = rstd;
+            }
+        }
+    }
+    __syncthreads();
+    const int base = strip * kStrip + warp * IO::kTile;
+    if (base >= a.cols) return;
+    const int j0 = base + IO::first(lane), left = a.cols - j0;
+    F2 g[IO::NP], b[IO::NP];
+    IO::template params<false>(moved(static_cast<const PT*>(a.gamma), j0), 0, left, g, 1.f);
+    IO::template params<false>(moved(static_cast<const PT*>(a.beta), j0), 0, left, b, 0.f);
+    for (int i = 0; i < nr; i += kSweepRows) {
+        typename IO::R xv[kSweepRows], rv[kSweepRows];
+#pragma unroll
+        for (int j = 0; j < kSweepRows; ++j) {
+            const int64_t at = (r0 + min(i + j, nr - 1)) * a.cols + j0;
+            xv[j] = IO::template load<false>(static_cast<const T*>(a.x) + at, 0, left);
+            if (a.residual)
+                rv[j] = IO::template load<false>(static_cast<const T*>(a.residual) + at, 0, left);
+        }
+#pragma unroll
+        for (int j = 0; j < kSweepRows; ++j) {
+            if (i + j >= nr) break;
+            const int64_t at = (r0 + i + j) * a.cols + j0;
+            const float2 c = rowc[i + j];
+            F2 h[IO::NP];
+            tile_h<T, IO>(xv[j], rv[j], a.residual != nullptr, a.drop.on, d, base, lane,
+                          (uint32_t)(r0 + i + j), h);
+            if (a.h) IO::template store<false>(static_cast<T*>(a.h) + at, 0, left, h);
+#pragma unroll
+            for (int e = 0; e < IO::NP; ++e) h[e] = normed<OP>(h[e], c.x, c.y, g[e], b[e]);
+            IO::template store<false>(static_cast<T*>(a.y) + at, 0, left, h);
+        }
+    }
 }
 
 template <int OP, typename T, typename IO, typename PT, int V>
@@ -450,53 +485,55 @@ cudaError_t run_warp(const NormFwdArgs& a, int sms, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-template <int OP, typename T, typename IO, typename PT, int V, int R>
-cudaError_t run_ring(const NormFwdArgs& a, const RingPlan& p, cudaStream_t s) {
-    const void* fn = (const void*)fwd_ring<OP, T, IO, PT, V, R>;
-    int resident;
-    unsigned* err;
-    if (!ring_resident(fn, p, &resident, &err)) return cudaErrorInvalidConfiguration;
-    return launch_ring(fn, a, p, ring_grid(p, resident, a.rows), err, s);
-}
-
-template <int OP, typename T, typename IO, typename PT>
+// IO and WIO: the access forms of the ring and warp kernels and of the sweep.
+template <int OP, typename T, typename IO, typename WIO, typename PT>
 cudaError_t run_fwd(const NormFwdArgs& a, int sms, cudaStream_t s) {
     const int tiles = (a.cols + IO::kTile - 1) / IO::kTile;
     if (tiles <= 1) return run_warp<OP, T, IO, PT, 1>(a, sms, s);
     if (tiles <= 2) return run_warp<OP, T, IO, PT, 2>(a, sms, s);
     if (tiles <= 4) return run_warp<OP, T, IO, PT, 4>(a, sms, s);
+    const int streams = a.residual ? 2 : 1;
+    if (!ring_fits(tiles, sizeof(T), streams, 2, a.rows, sms))
+        return run_sweep((const void*)fwd_sweep<OP, T, WIO, PT>, a,
+                         sweep_batch(a.rows, (int64_t)a.cols * streams * sizeof(T), a.l2_bytes),
+                         WIO::N, s);
+    const RingKernels fn{(const void*)fwd_ring<OP, T, IO, PT, 4, 1>,
+                         (const void*)fwd_ring<OP, T, IO, PT, 4, 2>,
+                         (const void*)fwd_ring<OP, T, IO, PT, 8, 1>};
     RingPlan p;
-    if (!plan_ring(tiles, sizeof(T), a.residual ? 2 : 1, 2, a.rows, sms, &p))
-        return run_general<OP, T, IO, PT>(a, sms, s);
-    if (p.V == 8) return run_ring<OP, T, IO, PT, 8, 1>(a, p, s);
-    return p.R == 2 ? run_ring<OP, T, IO, PT, 4, 2>(a, p, s) : run_ring<OP, T, IO, PT, 4, 1>(a, p, s);
+    int resident;
+    unsigned* err;
+    if (!plan_ring(tiles, sizeof(T), streams, 2, a.rows, sms, fn, &p, &resident, &err))
+        return cudaErrorInvalidConfiguration;
+    return launch_ring(fn.of(p), a, p, ring_grid(p, resident, a.rows), err, s);
 }
 
-template <int OP, typename T, typename IO>
+template <int OP, typename T, typename IO, typename WIO>
 cudaError_t pick_param(const NormFwdArgs& a, int sms, cudaStream_t s) {
-    return a.half ? run_fwd<OP, T, IO, bf16>(a, sms, s) : run_fwd<OP, T, IO, float>(a, sms, s);
+    return a.half ? run_fwd<OP, T, IO, WIO, bf16>(a, sms, s)
+                  : run_fwd<OP, T, IO, WIO, float>(a, sms, s);
 }
 
 template <int OP, typename T>
 cudaError_t pick_fwd(TrainKey k, const NormFwdArgs& a, int sms, cudaStream_t s) {
-    return k.vec ? pick_param<OP, T, VecIO<T, 4>>(a, sms, s)
-                 : pick_param<OP, T, ElemIO<T, 4>>(a, sms, s);
+    constexpr int N = 16 / (int)sizeof(T);
+    return k.vec ? pick_param<OP, T, VecIO<T, 4>, VecIO<T, N>>(a, sms, s)
+                 : pick_param<OP, T, ElemIO<T, 4>, ElemIO<T, N>>(a, sms, s);
 }
 
 }  // namespace
 
-int train_chunks(int64_t cols) {
-    const int64_t chunk = (int64_t)kChunkTiles * VecIO<float, 4>::kTile;
+int train_chunks(int dtype, int64_t cols) {
+    const int chunk = sweep_chunk(dtype == 0 ? 4 : 8);
     return (int)((cols + chunk - 1) / chunk);
 }
 
 int64_t norm_fwd_partials(int dtype, int64_t rows, int64_t cols, int sms) {
-    // the general form runs where the ring does not hold x and residual; a
+    // the sweep runs where the ring does not hold x and residual; a
     // call without residual then has room it does not need
-    RingPlan p;
     const int tiles = (int)((cols + VecIO<float, 4>::kTile - 1) / VecIO<float, 4>::kTile);
-    if (tiles <= 4 || plan_ring(tiles, dtype == 0 ? 4 : 2, 2, 2, rows, sms, &p)) return 0;
-    return rows * train_chunks(cols) * 16;
+    if (tiles <= 4 || ring_fits(tiles, dtype == 0 ? 4 : 2, 2, 2, rows, sms)) return 0;
+    return rows * train_chunks(dtype, cols) * 8;
 }
 
 cudaError_t launch_norm_fwd(TrainKey k, const NormFwdArgs& a, int sms, cudaStream_t s) {

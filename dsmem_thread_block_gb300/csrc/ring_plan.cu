@@ -2,7 +2,6 @@
 #include "ring_plan.h"
 
 #include <algorithm>
-#include <cstdlib>
 #include <mutex>
 #include <vector>
 
@@ -18,40 +17,6 @@ constexpr int kMostStage = 220 * 1024;  // shared memory a CTA may spend on its 
 
 }  // namespace
 
-bool plan_ring(int tiles, int es, int streams, int turn, int64_t rows, int sms, RingPlan* out) {
-    const int fewest = turn == 1 ? 2 : 1, want = turn == 1 ? 4 : 2;  // stages
-    for (int least : {turn == 1 ? 3 : 1, fewest}) {
-        for (int V : {4, 8}) {
-            if (getenv("PV8") && V == 4) continue;
-            for (int P = (tiles + V * kRingWarps - 1) / (V * kRingWarps); P <= kMaxCluster; ++P) {
-                RingPlan p{};
-                p.V = V;
-                p.shape.tiles = (tiles + P - 1) / P;
-                p.P = (tiles + p.shape.tiles - 1) / p.shape.tiles;  // no CTA without columns
-                p.W = (p.shape.tiles + V - 1) / V;
-                // a slice that starts inside a 16-byte line takes one line more
-                p.shape.room = (p.shape.tiles * kTileCols * es + 16 + 127) / 128 * 128;
-                const int ctas_most = std::max(1, std::min(8, 1024 / (32 * p.W)));  // per SM
-                p.most = std::max(1, sms * ctas_most / p.P);
-                p.R = turn == 2 && V == 4 && rows >= 2 * (int64_t)p.most ? 2 : 1;
-                const int stage = p.shape.room * streams * p.R;
-                const int budget = (getenv("BUD") ? atoi(getenv("BUD")) : turn == 1 ? 200 : 144) * 1024;
-                int ctas = ctas_most;
-                while (ctas > 1 && budget / ctas < want * stage) --ctas;
-                int stages = budget / ctas / stage;
-                if (stages < want) stages = std::min(want, kMostStage / stage);
-                if (stages < least) continue;
-                if (rows * p.P * 2 <= sms) stages = fewest;  // every cluster has one row
-                p.shape.stages = std::min(stages, kRingStages);
-                p.smem = (size_t)p.shape.stages * stage;
-                *out = p;
-                return true;
-            }
-        }
-    }
-    return false;
-}
-
 namespace {
 
 // What a launch of (kernel, shape) needs from the device, looked up once.
@@ -62,8 +27,8 @@ struct Resident {
     unsigned* err;
 };
 
-}  // namespace
-
+// The clusters of `fn` in this shape that the current device holds at once,
+// and its error word; false on a CUDA error.
 bool ring_resident(const void* fn, const RingPlan& p, int* clusters, unsigned** err) {
     static std::mutex mu;
     static std::vector<Resident> known;
@@ -90,6 +55,141 @@ bool ring_resident(const void* fn, const RingPlan& p, int* clusters, unsigned** 
     known.push_back(r);
     *clusters = r.clusters;
     *err = r.err;
+    return true;
+}
+
+// The shape of `tiles` tiles over P CTAs of warps that hold V each; false where
+// the stages do not fit.
+bool shape(int tiles, int es, int streams, int turn, int64_t rows, int sms, int V, int P,
+           RingPlan* out) {
+    RingPlan p{};
+    p.V = V;
+    p.shape.tiles = (tiles + P - 1) / P;
+    p.P = (tiles + p.shape.tiles - 1) / p.shape.tiles;  // no CTA without columns
+    p.W = (p.shape.tiles + V - 1) / V;
+    if (p.P != P || p.W > kRingWarps) return false;
+    // a slice that starts inside a 16-byte line takes one line more
+    p.shape.room = (p.shape.tiles * kTileCols * es + 16 + 127) / 128 * 128;
+    p.most = ring_most(p, sms);
+    p.R = turn == 2 && V == 4 && rows >= 2 * (int64_t)p.most ? 2 : 1;
+    const int stage = p.shape.room * streams * p.R;
+    // the backward kernel keeps two rows' stages busy, and wants two to come
+    const int fewest = turn == 1 ? 2 : 1, want = turn == 1 ? 4 : 2;
+    const int budget = (turn == 1 ? 200 : 144) * 1024;
+    int ctas = std::max(1, kRingWarps / p.W);  // per SM, by registers
+    while (ctas > 1 && budget / ctas < want * stage) --ctas;
+    int stages = budget / ctas / stage;
+    if (stages < want) stages = std::min(want, kMostStage / stage);
+    if (stages < fewest) return false;
+    if (rows * p.P * 2 <= sms) stages = fewest;  // every cluster has one row
+    p.shape.stages = std::min(stages, kRingStages);
+    p.smem = (size_t)p.shape.stages * stage;
+    *out = p;
+    return true;
+}
+
+}  // namespace
+
+int ring_most(const RingPlan& p, int sms) {
+    return std::max(1, sms * std::max(1, std::min(8, 1024 / (32 * p.W))) / p.P);
+}
+
+bool ring_fits(int tiles, int es, int streams, int turn, int64_t rows, int sms) {
+    RingPlan p;
+    for (int P = kMaxCluster; P >= 1; --P)
+        for (int V : {8, 4})
+            if (shape(tiles, es, streams, turn, rows, sms, V, P, &p)) return true;
+    return false;
+}
+
+int64_t ring_groups_bound(int tiles, int es, int streams, int64_t rows, int sms) {
+    int64_t most = 0;
+    RingPlan p;
+    for (int P = 1; P <= kMaxCluster; ++P)
+        for (int V : {4, 8})
+            if (shape(tiles, es, streams, 1, rows, sms, V, P, &p))
+                most = std::max<int64_t>(most, std::min<int64_t>(p.most, rows));
+    return most;
+}
+
+namespace {
+
+struct Choice {
+    int dev, tiles, streams;
+    int64_t rows;
+    const void* fn;
+    RingPlan plan;
+    int resident;
+    unsigned* err;
+};
+
+// Calls of one shape come again and again: the last shapes' choices, each in
+// the slot its key hashes to.
+constexpr int kChoices = 256;
+std::mutex g_choice_mu;
+Choice g_choice[kChoices];
+
+}  // namespace
+
+// The kernels are bound by how many warps an SM holds to hide the latencies of
+// a row's reduction, so the shape is the one with the most resident warps per
+// SM (occupancy counts what clusters leave empty in a GPC) whose lanes all have
+// columns, weighted by what was measured besides (copy rate = 1):
+//   a cluster's exchange costs: 16384 bf16 columns, forward, V 8 P 1 0.66,
+//     P 2 0.62; and more where one CTA fills an SM (65536 columns with dropout:
+//     V 4 P 8, 16 warps a CTA, 0.57; V 8 P 8, two CTAs of 8, 0.65)
+//   two rows a turn (V = 4) share more: 8192 columns, V 4 0.79, V 8 0.74; the
+//     backward kernel spills at V = 8 (8192 columns, LayerNorm: 0.63, 0.35)
+//   two stages leave the backward kernel without a row to come: 20000 fp32
+//     columns, P 3 with two stages 0.46, P 4 with three 0.62
+// The rule's choices against the best of all shapes at 20 widths: within 8 %.
+bool plan_ring(int tiles, int es, int streams, int turn, int64_t rows, int sms,
+               const RingKernels& fn, RingPlan* out, int* resident, unsigned** err) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    const uint64_t key = ((uint64_t)(uintptr_t)fn.v4 ^ ((uint64_t)rows << 20) ^
+                          ((uint64_t)tiles << 8) ^ (uint64_t)(streams * 16 + dev)) *
+                         0x9E3779B97F4A7C15ull;
+    Choice& slot = g_choice[key >> 56];
+    {
+        std::lock_guard<std::mutex> lk(g_choice_mu);
+        if (slot.fn == fn.v4 && slot.dev == dev && slot.tiles == tiles && slot.streams == streams &&
+            slot.rows == rows) {
+            *out = slot.plan;
+            *resident = slot.resident;
+            *err = slot.err;
+            return true;
+        }
+    }
+    float best = 0.f;
+    for (int P = 1; P <= kMaxCluster; ++P) {
+        for (int V : {4, 8}) {
+            RingPlan p;
+            if (!shape(tiles, es, streams, turn, rows, sms, V, P, &p)) continue;
+            int clusters;
+            unsigned* word;
+            if (!ring_resident(fn.of(p), p, &clusters, &word)) continue;
+            const float warps = std::min(16.f, (float)std::min(clusters, p.most) * p.P * p.W / sms);
+            const float full = (float)tiles / (p.P * p.W * p.V);
+            float score = warps * full * full * (1.f - 0.004f * P);
+            if (V == 8) score *= turn == 1 ? 0.8f : P == 1 ? 0.97f : 0.93f;
+            if (P > 1) score *= 0.93f;
+            if (P > 1 && turn == 2 && p.W > 8) score *= 0.85f;
+            if (turn == 1 && p.shape.stages < 3 && rows * P * 2 > sms) score *= 0.7f;
+            if (score > best) {
+                best = score;
+                *out = p;
+                *resident = clusters;
+                *err = word;
+            }
+        }
+    }
+    if (best <= 0.f) return false;
+    std::lock_guard<std::mutex> lk(g_choice_mu);
+    slot = Choice{dev, tiles, streams, rows, fn.v4, *out, *resident, *err};
     return true;
 }
 

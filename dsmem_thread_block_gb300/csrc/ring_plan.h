@@ -26,15 +26,28 @@ struct RingPlan {
     RingShape shape;    // `clusters` and `err` are set by the launch
 };
 
-// A shape for rows of `tiles` warp tiles in `streams` streams of `es`-byte
-// elements; `turn`: most rows per turn (2: the forward kernel; 1: the
-// backward kernel, which holds two turns' stages at once).  False where the
-// rows are too wide.
-bool plan_ring(int tiles, int es, int streams, int turn, int64_t rows, int sms, RingPlan* out);
+// The instantiations a plan may choose: one and two rows of four tiles a warp,
+// one row of eight.
+struct RingKernels {
+    const void* v4;
+    const void* v4r2;
+    const void* v8;
+    const void* of(const RingPlan& p) const { return p.V == 8 ? v8 : p.R == 2 ? v4r2 : v4; }
+};
 
-// The clusters of `fn` in this shape that the current device holds at once,
-// and its error word; false on a CUDA error.
-bool ring_resident(const void* fn, const RingPlan& p, int* clusters, unsigned** err);
+// The shape for rows of `tiles` warp tiles in `streams` streams of `es`-byte
+// elements; `turn`: most rows per turn (2: the forward kernel; 1: the backward
+// kernel, which holds two turns' stages at once).  False where the rows are
+// too wide (ring_fits, which needs no device) or on a CUDA error.  Also the
+// clusters the device holds at once and its error word.
+bool plan_ring(int tiles, int es, int streams, int turn, int64_t rows, int sms,
+               const RingKernels& fn, RingPlan* out, int* resident, unsigned** err);
+bool ring_fits(int tiles, int es, int streams, int turn, int64_t rows, int sms);
+
+// Most clusters of a grid in this shape; and over every shape the backward
+// kernel may be given (the row groups a workspace has room for).
+int ring_most(const RingPlan& p, int sms);
+int64_t ring_groups_bound(int tiles, int es, int streams, int64_t rows, int sms);
 
 // The clusters of a launch: as many as are resident, no more than rows or
 // plan.most, evened out so that none has a row more than it must.

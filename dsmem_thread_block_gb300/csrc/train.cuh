@@ -147,6 +147,17 @@ template <typename T, int ELEMS> struct VecIO {
                     make_float4(f[k].x, f[k].y, f[k + 1].x, f[k + 1].y);
         }
     }
+    // f += the sums at p, which an earlier launch of the call's chain wrote: read
+    // from L2, where L1 could hold a line from before
+    __device__ static __forceinline__ void add_sums(const float* p, int left, F2* f) {
+        if (!in<false>(0, 0, left)) return;
+#pragma unroll
+        for (int k = 0; k < NP; k += 2) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(p + 2 * k));
+            f[k] = add2(F2{v.x, v.y}, f[k]);
+            f[k + 1] = add2(F2{v.z, v.w}, f[k + 1]);
+        }
+    }
     // `there`: the caller knows that p is not null
     template <bool FULL, typename PT>
     __device__ static __forceinline__ void params(const PT* p, int off, int left, F2* f,
@@ -221,6 +232,12 @@ template <typename T, int ELEMS> struct ElemIO {
 #pragma unroll
         for (int k = 0; k < N; ++k)
             if (in<FULL>(off, k, left)) p[off + 32 * k] = k & 1 ? f[k / 2].y : f[k / 2].x;
+    }
+    __device__ static __forceinline__ void add_sums(const float* p, int left, F2* f) {
+#pragma unroll
+        for (int k = 0; k < NP; ++k)
+            f[k] = add2(F2{in<false>(0, 2 * k, left) ? __ldcg(p + 64 * k) : 0.f,
+                           in<false>(0, 2 * k + 1, left) ? __ldcg(p + 64 * k + 32) : 0.f}, f[k]);
     }
     template <bool FULL, typename PT>
     __device__ static __forceinline__ float param1(const PT* p, int off, int k, int left,

@@ -105,7 +105,7 @@ credit_status_t credit_norm_workspace(credit_op_t op, int backward, int64_t rows
     if (st != CREDIT_OK) return st;
     const DevInfo* d = device_info(device);
     if (!d) return CREDIT_ERR_CUDA;
-    *bytes = backward ? (size_t)bwd_bytes(norm_bwd_layout((int)dtype, rows, cols, d->sms))
+    *bytes = backward ? (size_t)bwd_bytes(norm_bwd_layout((int)dtype, rows, cols, d->sms, d->l2_bytes))
                       : (size_t)norm_fwd_partials((int)dtype, rows, cols, d->sms);
     return CREDIT_OK;
 }
@@ -178,7 +178,8 @@ credit_status_t credit_norm_forward(credit_op_t op, const void* x, const void* r
     a.rows = rows; a.cols = (int32_t)cols; a.inv_cols = 1.f / (float)cols; a.eps = eps;
     a.half = (gamma || beta) && param_dtype == CREDIT_BF16;
     a.ws = static_cast<float*>(workspace);
-    a.nch = train_chunks(cols);
+    a.nch = train_chunks((int)dtype, cols);
+    a.l2_bytes = d->l2_bytes;
     const bool vec = aligned(x, 16) && aligned(y, 16) && aligned(residual, 16) && aligned(h, 16) &&
                      aligned(gamma, 16) && aligned(beta, 16) && (uint64_t)cols * es % 16 == 0;
     const TrainKey k{(int)op, (int)dtype, vec};
@@ -219,7 +220,7 @@ credit_status_t credit_norm_backward(credit_op_t op, const void* dy, const void*
     const DevInfo* d;
     st = device(&dev, &d);
     if (st != CREDIT_OK) return st;
-    const TrainLayout l = norm_bwd_layout((int)dtype, rows, cols, d->sms);
+    const TrainLayout l = norm_bwd_layout((int)dtype, rows, cols, d->sms, d->l2_bytes);
     const uint64_t need = bwd_bytes(l);
     if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
         return CREDIT_ERR_INVALID_ARG;
@@ -232,7 +233,7 @@ credit_status_t credit_norm_backward(credit_op_t op, const void* dy, const void*
     a.pitch = l.pitch;
     a.nch = l.nch;
     a.groups = l.groups;
-    a.group_rows = l.group_rows;
+    a.batch = l.batch;
     const bool vec = aligned(dy, 16) && aligned(dh, 16) && aligned(h, 16) && aligned(dx, 16) &&
                      aligned(dresidual, 16) && aligned(gamma, 16) && (uint64_t)cols * es % 16 == 0;
     const TrainKey k{(int)op, (int)dtype, vec};
