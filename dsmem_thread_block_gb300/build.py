@@ -18,6 +18,8 @@ LIB = os.path.join(BUILD, "libcredit.so")
 # the checked build: the same sources with -DCREDIT_DEBUG (index checks and the
 # phase trace), in its own object directory
 CHECKED_LIB = os.path.join(BUILD, "libcredit_checked.so")
+# the torch layer of the training operators, a Python extension
+TORCH_LIB = os.path.join(BUILD, "credit_train_torch.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -87,11 +89,47 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     return lib
 
 
+def _torch_root() -> str:
+    """The directory of the installed torch, without importing it."""
+    import importlib.util
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("torch not found: its headers are required to build the torch layer")
+    return spec.submodule_search_locations[0]
+
+
+def build_torch(force: bool = False) -> str:
+    """Compile and link the training operators' torch layer
+    (csrc/train_torch.cpp) against the installed torch, if out of date."""
+    import sysconfig
+    src = os.path.join(CSRC, "train_torch.cpp")
+    deps = [src, os.path.join(INCLUDE, "credit.h"), __file__]
+    if not force and os.path.exists(TORCH_LIB) and \
+            os.path.getmtime(TORCH_LIB) >= max(os.path.getmtime(p) for p in deps):
+        return TORCH_LIB
+    os.makedirs(BUILD, exist_ok=True)
+    root = _torch_root()
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    tmp = TORCH_LIB + f".{os.getpid()}.tmp"
+    r = subprocess.run(
+        [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-shared", "-fPIC", "-I", INCLUDE,
+         "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+         "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+         "-isystem", cuda, src, "-o", tmp, "-L", os.path.join(root, "lib"), "-ltorch_python",
+         "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TORCH_LIB)
+    return TORCH_LIB
+
+
 def build_all(force: bool = False) -> tuple[str, str]:
-    """Both libraries, compiled side by side: (regular, checked)."""
-    with cf.ThreadPoolExecutor(max_workers=2) as ex:
+    """Both libraries and the torch layer, compiled side by side: (regular,
+    checked)."""
+    with cf.ThreadPoolExecutor(max_workers=3) as ex:
         reg = ex.submit(build, force)
         chk = ex.submit(build, force, False, None, True)
+        ex.submit(build_torch, force).result()
         return reg.result(), chk.result()
 
 
