@@ -8,6 +8,7 @@
 //   bwd_warp   one warp per row
 //   bwd_ring   a CTA, or a cluster, per row; the next rows' dy, h and dh
 //              arrive in a ring of shared-memory stages
+//   bwd_team   a team of CTAs across the GPU per row (team.cuh)
 //   bwd_sweep  wider rows: the two row sums per chunk, then a second read, from
 //              L2 (sweep.cuh)
 // In each a thread keeps the same columns for all its rows and sums their
@@ -19,6 +20,7 @@
 #include "planner.h"
 #include "ring.cuh"
 #include "sweep.cuh"
+#include "team.cuh"
 
 namespace credit {
 
@@ -26,6 +28,25 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+
+constexpr int kTileCols = VecIO<float, 4>::kTile;
+
+// The form of a call, by its shape.  A team hides the exchange that a cluster
+// waits for, and is not bound to a GPC, but clears its exchange and launches
+// cooperatively, some microseconds on the host: it takes large calls of rows
+// that clusters would share.  Measured, cluster and team (copy rate = 1): 4096
+// rows of 16384 bf16 columns, RMSNorm 0.81 and 0.72; 3355 of 20000, 0.61 and
+// 0.68; 1024 of 65536, LayerNorm, 0.49 and 0.60; 64 rows of 20000 columns 9.3
+// and 10.8 us, of 65536 columns 16.0 and 15.2 us.
+enum class Form { kWarp, kRing, kTeam, kSweep };
+
+Form form_of(int tiles, int es, int streams, int64_t rows, int64_t cols, int sms, TeamPlan* team) {
+    if (tiles <= 4) return Form::kWarp;
+    const bool ring = ring_fits(tiles, es, streams, 1, rows, sms);
+    if (ring && (cols <= 16384 || rows * cols < (1 << 22))) return Form::kRing;
+    if (plan_team(tiles, es, streams, rows, sms, team)) return Form::kTeam;
+    return ring ? Form::kRing : Form::kSweep;
+}
 
 struct RowStats { float mean, rstd; };
 
@@ -368,6 +389,173 @@ __global__ void __launch_bounds__(kRingThreads) bwd_ring(NormBwdArgs a, RingShap
     }
 }
 
+// ------------------------------------------------------------- a team per row
+// team.cuh's pipeline: a summing and a writing warp own four tiles of the
+// slice each, gamma (and the columns' sums) in registers.
+template <int OP, typename T, typename IO, typename PT>
+__global__ void __launch_bounds__(kTeamThreads) bwd_team(NormBwdArgs a, TeamShape q) {
+    constexpr int V = 4;
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ __align__(8) uint64_t full[kRingStages];
+    __shared__ float wred[2][2][kRingWarps];
+    __shared__ float2 tot[2];  // mean_j(w xh), mean_j(w) of the row to write
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = (blockDim.x >> 6) - 1;
+    const int team = (int)blockIdx.x / q.size, rank = (int)blockIdx.x - team * q.size;
+    const int c0 = rank * q.tiles * IO::kTile, c1 = min(a.cols, c0 + q.tiles * IO::kTile);
+    const int bytes = (c1 - c0) * (int)sizeof(T);
+    const void* const src[3] = {a.dy, a.h, a.dh};
+    const int ns = a.dh ? 3 : 2, stage_bytes = ns * q.room;
+    const int turns = (int)((a.rows - team + q.teams - 1) / q.teams);
+    auto row_of = [&](int k) { return team + (int64_t)k * q.teams; };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < q.stages; ++s) mbar_init(smem_u32(&full[s]), 1);
+        fence_mbar_init();
+        fence_proxy_async_smem();
+    }
+    __syncthreads();
+
+    if (warp == 2 * W) {  // collects
+        TeamExchange(q, team, rank, lane)
+            .collect_all(turns, q.lag, [&](int j, int, const float* x, const float* y) {
+                float t1 = 0.f, t2 = 0.f;
+#pragma unroll
+                for (int i = 0; i < kTeamParts; ++i) {
+                    t1 += x[i];
+                    t2 += y[i];
+                }
+                t1 = warp_allreduce(t1, SumOp()) * a.inv_cols;
+                t2 = warp_allreduce(t2, SumOp()) * a.inv_cols;
+                if (lane == 0) tot[(j + 1) & 1] = make_float2(t1, t2);
+            });
+        return;
+    }
+    if (warp == 2 * W + 1) {  // feeds
+        const TeamExchange ex(q, team, rank, lane);
+        auto issue = [&](int k) {
+            if (lane == 0 && k < turns)
+                ring_issue<3, 1, T, IO>(src, ns, row_of(k), a.rows, a.cols, c0, bytes,
+                                        ring + (k % q.stages) * stage_bytes, q.room,
+                                        smem_u32(&full[k % q.stages]));
+            __syncwarp();
+        };
+        for (int k = 0; k < q.stages; ++k) issue(k);
+        const int part = lane & 15, which = lane >> 4;
+        for (int j = 0; j < turns + q.lag; ++j) {
+            __syncthreads();
+            if (j < turns) {
+                float t[2];
+                spread<2>(half_sum(part < W ? wred[j & 1][which][part] : 0.f), lane, t);
+                ex.deposit((uint32_t)j, lane ? t[1] : t[0]);
+            }
+            if (j >= q.lag) issue(j - q.lag + q.stages);
+        }
+        return;
+    }
+
+    const bool summing = warp < W;
+    const int base0 = c0 + (summing ? warp : warp - W) * V * IO::kTile;
+    const int j0 = base0 + IO::first(lane), left = c1 - j0;
+    const bool whole = base0 + V * IO::kTile <= c1;
+    const PT* const gp = moved(static_cast<const PT*>(a.gamma), j0);
+    F2 g[V][IO::NP];
+#pragma unroll
+    for (int i = 0; i < V; ++i) IO::template params<false>(gp, i * IO::kTile, left, g[i], 1.f);
+    auto slice = [&](int s, int i, const void* p, int64_t row) {
+        const int64_t off = (row * a.cols + c0) * (int64_t)sizeof(T);
+        return reinterpret_cast<const T*>(ring + s * stage_bytes + i * q.room +
+                                          ring_shift<IO>(p, off)) + (j0 - c0);
+    };
+    RowStats next = row_stats<OP>(a, row_of(0));
+    int s = 0;
+    uint32_t phase = 0;
+    const std::true_type yes;
+    const std::false_type no;
+    // row k's stage is here; the next row's statistics are on their way
+    auto enter = [&](int k) {
+        const RowStats r = next;
+        if (k + 1 < turns) next = row_stats<OP>(a, row_of(k + 1));
+        mbar_wait_bounded(smem_u32(&full[s]), phase, q.err);
+        return r;
+    };
+    auto leave = [&] {
+        if (++s == q.stages) {
+            s = 0;
+            phase ^= 1u;
+        }
+    };
+    if (summing) {
+        F2 ag[V][IO::NP], ab[V][IO::NP];
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int e = 0; e < IO::NP; ++e) ag[i][e] = ab[i][e] = f2(0.f);
+        for (int j = 0; j < turns + q.lag; ++j) {
+            if (j < turns) {
+                const RowStats r = enter(j);
+                const T* const ys = slice(s, 0, a.dy, row_of(j));
+                const T* const hs = slice(s, 1, a.h, row_of(j));
+                F2 s1 = f2(0.f), s2 = f2(0.f);
+                auto take = [&](auto f) {
+                    constexpr bool FULL = decltype(f)::value;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        F2 u[IO::NP], h[IO::NP];
+                        unpack<T, IO::NP>(IO::template staged<FULL>(ys, i * IO::kTile, left), u);
+                        unpack<T, IO::NP>(IO::template staged<FULL>(hs, i * IO::kTile, left), h);
+                        tile_sums<OP, IO::NP>(u, h, g[i], r, s1, s2, ag[i], ab[i]);
+                    }
+                };
+                if (whole) take(yes); else take(no);
+                const float t[2] = {s1.x + s1.y, s2.x + s2.y};
+                const float v = row_sum<2>(t, lane);
+                if ((lane & 15) == 0) wred[j & 1][lane >> 4][warp] = v;
+                leave();
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            tile_params<OP, IO>(a, team, j0, i * IO::kTile, left, ag[i], ab[i]);
+        return;
+    }
+    const DropStream d(a.drop);
+    const bool simple = !a.drop.on && !a.dres;  // dx is the only matrix written
+    for (int j = 0; j < turns + q.lag; ++j) {
+        if (j >= q.lag) {
+            const int64_t at = row_of(j - q.lag);
+            const RowStats r = enter(j - q.lag);
+            const float2 m = tot[j & 1];
+            const RowBack back(r, m.x, m.y);
+            const T* const ys = slice(s, 0, a.dy, at);
+            const T* const hs = slice(s, 1, a.h, at);
+            const T* const ds = slice(s, 2, a.dh, at);
+            T* const dx = static_cast<T*>(a.dx) + at * a.cols + j0;
+            T* const dres = moved(static_cast<T*>(a.dres), at * a.cols + j0);
+            auto give = [&](auto f, auto has_dh, auto plain) {
+                constexpr bool FULL = decltype(f)::value;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    F2 u[IO::NP], h[IO::NP], dh[IO::NP];
+                    unpack<T, IO::NP>(IO::template staged<FULL>(ys, i * IO::kTile, left), u);
+                    unpack<T, IO::NP>(IO::template staged<FULL>(hs, i * IO::kTile, left), h);
+                    if (has_dh)
+                        unpack<T, IO::NP>(IO::template staged<FULL>(ds, i * IO::kTile, left), dh);
+                    tile_out<OP, T, IO, FULL>(
+                        d, u, h, g[i], has_dh, dh, r, back, at, base0 + i * IO::kTile, i * IO::kTile,
+                        left, lane, !plain && a.drop.on && (FULL || base0 + i * IO::kTile < c1), dx,
+                        plain ? nullptr : dres);
+                }
+            };
+            if (!whole) give(no, ns > 2, no);
+            else if (ns > 2) simple ? give(yes, yes, yes) : give(yes, yes, no);
+            else simple ? give(yes, no, yes) : give(yes, no, no);
+            leave();
+        }
+        __syncthreads();
+    }
+}
+
 // ------------------------------------------------------------- wider rows
 // One launch of sweep.cuh: the two row sums of one batch, outputs of the batch
 // before and its rows' part of the parameters' gradients, which the blocks of
@@ -549,8 +737,15 @@ cudaError_t run_bwd(NormBwdArgs& a, int sms, cudaStream_t s) {
     if (tiles <= 2) return run_warp<OP, T, IO, PT, 2>(a, s);
     if (tiles <= 4) return run_warp<OP, T, IO, PT, 4>(a, s);
     const int streams = a.dh ? 3 : 2;
-    if (!ring_fits(tiles, sizeof(T), streams, 1, a.rows, sms))
-        return run_sweep((const void*)bwd_sweep<OP, T, WIO, PT>, a, a.batch, WIO::N, s);
+    TeamPlan team;
+    switch (form_of(tiles, sizeof(T), streams, a.rows, a.cols, sms, &team)) {
+        case Form::kTeam:
+            a.groups = team.teams;  // at most the layout's
+            return launch_team((const void*)bwd_team<OP, T, IO, PT>, a, team, a.ws, s);
+        case Form::kSweep:
+            return run_sweep((const void*)bwd_sweep<OP, T, WIO, PT>, a, a.batch, WIO::N, s);
+        default: break;
+    }
     const RingKernels fn{(const void*)bwd_ring<OP, T, IO, PT, 4>, nullptr,
                          (const void*)bwd_ring<OP, T, IO, PT, 8>};
     RingPlan p;
@@ -575,7 +770,6 @@ cudaError_t pick_bwd(TrainKey k, NormBwdArgs& a, int sms, cudaStream_t s) {
                  : pick_param<OP, T, ElemIO<T, 4>, ElemIO<T, N>>(a, sms, s);
 }
 
-constexpr int kTileCols = VecIO<float, 4>::kTile;
 
 }  // namespace
 
@@ -593,17 +787,23 @@ TrainLayout bwd_layout(int dtype, int64_t rows, int64_t cols, int sms, int l2_by
         l.groups = l.room_groups = (int)(want < sms * 2 ? want : sms * 2);
         return l;
     }
-    // the ring's grid and the sweep's groups, whichever is larger: which of
-    // them runs depends on the call's streams too
+    // which form runs depends on the call's streams too: room for either
     l.batch = sweep_batch(rows, cols * 2 * es, l2_bytes);
     l.groups = (int)((std::min(rows, l.batch) + kSweepGroup - 1) / kSweepGroup);
     for (int streams = 2; streams <= 3; ++streams) {
-        if (ring_fits(tiles, es, streams, 1, rows, sms)) {
-            l.room_groups = (int)std::max<int64_t>(
-                l.room_groups, ring_groups_bound(tiles, es, streams, rows, sms));
-        } else {
-            l.room_groups = std::max(l.room_groups, l.groups);
-            l.partials = rows * l.nch * 8;
+        TeamPlan team;
+        switch (form_of(tiles, es, streams, rows, cols, sms, &team)) {
+            case Form::kTeam:
+                l.room_groups = std::max(l.room_groups, team.teams);
+                l.partials = std::max(l.partials, team.exchange_bytes);
+                break;
+            case Form::kSweep:
+                l.room_groups = std::max(l.room_groups, l.groups);
+                l.partials = std::max(l.partials, rows * l.nch * 8);
+                break;
+            default:
+                l.room_groups = (int)std::max<int64_t>(
+                    l.room_groups, ring_groups_bound(tiles, es, streams, rows, sms));
         }
     }
     return l;

@@ -5,15 +5,19 @@
 //   fwd_warp   one warp holds a row's h in registers
 //   fwd_ring   a CTA, or a cluster, holds it; the next rows' x and residual
 //              arrive in a ring of shared-memory stages meanwhile
+//   fwd_team   a team of CTAs across the GPU holds it (team.cuh)
 //   fwd_sweep  wider rows: partial statistics per chunk, then a second read,
 //              from L2 (sweep.cuh)
 // Each reads x and residual from HBM once and writes h and y once.
 //
 // Statistics: sum and M2 about the piece's own mean (of a warp, a CTA or a
 // chunk), merged with the parallel-axis form of Chan et al.'s update.
+#include <algorithm>
+
 #include "planner.h"
 #include "ring.cuh"
 #include "sweep.cuh"
+#include "team.cuh"
 
 namespace credit {
 
@@ -322,6 +326,207 @@ __global__ void __launch_bounds__(kRingThreads) fwd_ring(NormFwdArgs a, RingShap
     }
 }
 
+// ------------------------------------------------------------- a team per row
+// team.cuh's pipeline: a summing and a writing warp own four tiles of the
+// slice each; h is formed from the stage by both.
+template <int OP, typename T, typename IO, typename PT>
+__global__ void __launch_bounds__(kTeamThreads) fwd_team(NormFwdArgs a, TeamShape q) {
+    constexpr int V = 4;
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ __align__(8) uint64_t full[kRingStages];
+    __shared__ float2 wred[2][kRingWarps];
+    __shared__ float2 tot[2];  // mean, rstd of the row to write
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = (blockDim.x >> 6) - 1;
+    const int team = (int)blockIdx.x / q.size, rank = (int)blockIdx.x - team * q.size;
+    const int slice = q.tiles * IO::kTile;
+    const int c0 = rank * slice, c1 = min(a.cols, c0 + slice);
+    const int bytes = (c1 - c0) * (int)sizeof(T);
+    const void* const src[2] = {a.x, a.residual};
+    const int ns = a.residual ? 2 : 1, stage_bytes = ns * q.room;
+    const int turns = (int)((a.rows - team + q.teams - 1) / q.teams);
+    auto row_of = [&](int k) { return team + (int64_t)k * q.teams; };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < q.stages; ++s) mbar_init(smem_u32(&full[s]), 1);
+        fence_mbar_init();
+        fence_proxy_async_smem();
+    }
+    __syncthreads();
+
+    if (warp == 2 * W) {  // collects: sums, M2 about each CTA's mean
+        float n[kTeamParts], inv_n[kTeamParts];  // columns of the CTAs this lane merges
+#pragma unroll
+        for (int i = 0; i < kTeamParts; ++i) {
+            n[i] = (float)max(0, min(a.cols - (lane + 32 * i) * slice, slice));
+            inv_n[i] = 1.f / fmaxf(n[i], 1.f);
+        }
+        TeamExchange(q, team, rank, lane)
+            .collect_all(turns, q.lag, [&](int j, int due, const float* x, const float* y) {
+                float mu = 0.f, m2 = 0.f;
+                if constexpr (OP == kLayerNorm) {
+#pragma unroll
+                    for (int i = 0; i < kTeamParts; ++i) mu += x[i];
+                    mu = warp_allreduce(mu, SumOp()) * a.inv_cols;
+                }
+#pragma unroll
+                for (int i = 0; i < kTeamParts; ++i) {
+                    m2 += y[i];
+                    if constexpr (OP == kLayerNorm) {
+                        const float e = fmaf(x[i], inv_n[i], -mu);
+                        m2 = fmaf(n[i] * e, e, m2);
+                    }
+                }
+                m2 = warp_allreduce(m2, SumOp());
+                const float rstd = rsqrtf(fmaf(m2, a.inv_cols, a.eps));
+                if (lane == 0) {
+                    tot[(j + 1) & 1] = make_float2(mu, rstd);
+                    if (rank == 0) {
+                        if (a.mean) a.mean[row_of(due)] = mu;
+                        if (a.rstd) a.rstd[row_of(due)] = rstd;
+                    }
+                }
+            });
+        return;
+    }
+    if (warp == 2 * W + 1) {  // feeds
+        const TeamExchange ex(q, team, rank, lane);
+        auto issue = [&](int k) {
+            if (lane == 0 && k < turns)
+                ring_issue<2, 1, T, IO>(src, ns, row_of(k), a.rows, a.cols, c0, bytes,
+                                        ring + (k % q.stages) * stage_bytes, q.room,
+                                        smem_u32(&full[k % q.stages]));
+            __syncwarp();
+        };
+        for (int k = 0; k < q.stages; ++k) issue(k);
+        const int part = lane & 15;
+        const float wn = (float)max(0, min(c1 - (c0 + part * V * IO::kTile), V * IO::kTile));
+        const float inv_wn = 1.f / fmaxf(wn, 1.f), inv_cta = 1.f / (float)(c1 - c0);
+        for (int j = 0; j < turns + q.lag; ++j) {
+            __syncthreads();
+            if (j < turns) {
+                const float2 w = part < W ? wred[j & 1][part] : make_float2(0.f, 0.f);
+                float sum = 0.f, m2 = w.y;
+                if constexpr (OP == kLayerNorm) {
+                    sum = half_sum(w.x);
+                    const float e = fmaf(w.x, inv_wn, -sum * inv_cta);
+                    m2 = fmaf(wn * e, e, m2);
+                }
+                m2 = half_sum(m2);
+                ex.deposit((uint32_t)j, lane ? m2 : sum);
+            }
+            if (j >= q.lag) issue(j - q.lag + q.stages);
+        }
+        return;
+    }
+
+    const DropStream d(a.drop);
+    const bool summing = warp < W;
+    const int base0 = c0 + (summing ? warp : warp - W) * V * IO::kTile;
+    const int j0 = base0 + IO::first(lane), left = c1 - j0;
+    const bool whole = base0 + V * IO::kTile <= c1;
+    int s = 0;
+    uint32_t phase = 0;
+    const std::true_type yes;
+    const std::false_type no;
+    // h of a tile of the row in stage s
+    auto tile = [&](auto f, auto res, auto on, int64_t row, int i, F2 (&h)[IO::NP]) {
+        constexpr bool FULL = decltype(f)::value;
+        const int64_t off = (row * a.cols + c0) * (int64_t)sizeof(T);
+        const unsigned char* const p = ring + s * stage_bytes;
+        const T* xs = reinterpret_cast<const T*>(p + ring_shift<IO>(a.x, off)) + (j0 - c0);
+        const T* rs = reinterpret_cast<const T*>(p + q.room + ring_shift<IO>(a.residual, off)) +
+                      (j0 - c0);
+        typename IO::R rv = {};
+        if (res) rv = IO::template staged<FULL>(rs, i * IO::kTile, left);
+        tile_h<T, IO>(IO::template staged<FULL>(xs, i * IO::kTile, left), rv, res,
+                      on && (FULL || base0 + i * IO::kTile < c1), d, base0 + i * IO::kTile, lane,
+                      (uint32_t)row, h);
+    };
+    // f(whole, residual, dropout) with what holds for the whole call as constants
+    auto pick = [&](auto f) {
+        if (!whole) f(no, ns > 1, a.drop.on != 0);
+        else if (ns > 1) a.drop.on ? f(yes, yes, yes) : f(yes, yes, no);
+        else a.drop.on ? f(yes, no, yes) : f(yes, no, no);
+    };
+    auto leave = [&] {
+        if (++s == q.stages) {
+            s = 0;
+            phase ^= 1u;
+        }
+    };
+    if (summing) {
+        const float inv_warp = 1.f / (float)max(1, min(c1 - base0, V * IO::kTile));
+        for (int j = 0; j < turns + q.lag; ++j) {
+            if (j < turns) {
+                mbar_wait_bounded(smem_u32(&full[s]), phase, q.err);
+                pick([&](auto f, auto res, auto on) {
+                    constexpr bool FULL = decltype(f)::value;
+                    F2 h[V][IO::NP], t = f2(0.f);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        tile(f, res, on, row_of(j), i, h[i]);
+#pragma unroll
+                        for (int e = 0; e < IO::NP; ++e)
+                            t = OP == kLayerNorm ? add2(t, h[i][e]) : fma2(h[i][e], h[i][e], t);
+                    }
+                    const float sum = warp_allreduce(t.x + t.y, SumOp());
+                    float m2 = sum;
+                    if constexpr (OP == kLayerNorm) {
+                        const float mu = sum * inv_warp;
+                        t = f2(0.f);
+#pragma unroll
+                        for (int i = 0; i < V; ++i)
+#pragma unroll
+                            for (int e = 0; e < IO::NP; ++e) {
+                                F2 z = add2(h[i][e], f2(-mu));
+                                if constexpr (!FULL)
+                                    z = inside<FULL, IO>(z, i * IO::kTile, e, left);
+                                t = fma2(z, z, t);
+                            }
+                        m2 = warp_allreduce(t.x + t.y, SumOp());
+                    }
+                    if (lane == 0) wred[j & 1][warp] = make_float2(sum, m2);
+                });
+                leave();
+            }
+            __syncthreads();
+        }
+        return;
+    }
+    const PT* const gp = moved(static_cast<const PT*>(a.gamma), j0);
+    const PT* const bp = moved(static_cast<const PT*>(a.beta), j0);
+    F2 g[V][IO::NP], b[V][IO::NP];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        IO::template params<false>(gp, i * IO::kTile, left, g[i], 1.f);
+        IO::template params<false>(bp, i * IO::kTile, left, b[i], 0.f);
+    }
+    for (int j = 0; j < turns + q.lag; ++j) {
+        if (j >= q.lag) {
+            const int64_t at = row_of(j - q.lag);
+            mbar_wait_bounded(smem_u32(&full[s]), phase, q.err);
+            const float2 m = tot[j & 1];
+            T* const y = static_cast<T*>(a.y) + at * a.cols + j0;
+            T* const ho = moved(static_cast<T*>(a.h), at * a.cols + j0);
+            pick([&](auto f, auto res, auto on) {
+                constexpr bool FULL = decltype(f)::value;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    F2 h[IO::NP];
+                    tile(f, res, on, at, i, h);
+                    if ((res || on) && ho) IO::template store<FULL>(ho, i * IO::kTile, left, h);
+#pragma unroll
+                    for (int e = 0; e < IO::NP; ++e)
+                        h[e] = normed<OP>(h[e], m.x, m.y, g[i][e], b[i][e]);
+                    IO::template store<FULL>(y, i * IO::kTile, left, h);
+                }
+            });
+            leave();
+        }
+        __syncthreads();
+    }
+}
+
 // ------------------------------------------------------------- wider rows
 // One launch of sweep.cuh: row sums of one batch, outputs of the batch before.
 // The sums of a row and chunk are (sum, M2 about the chunk's mean).
@@ -493,10 +698,14 @@ cudaError_t run_fwd(const NormFwdArgs& a, int sms, cudaStream_t s) {
     if (tiles <= 2) return run_warp<OP, T, IO, PT, 2>(a, sms, s);
     if (tiles <= 4) return run_warp<OP, T, IO, PT, 4>(a, sms, s);
     const int streams = a.residual ? 2 : 1;
-    if (!ring_fits(tiles, sizeof(T), streams, 2, a.rows, sms))
+    if (!ring_fits(tiles, sizeof(T), streams, 2, a.rows, sms)) {
+        TeamPlan team;
+        if (plan_team(tiles, sizeof(T), streams, a.rows, sms, &team))
+            return launch_team((const void*)fwd_team<OP, T, IO, PT>, a, team, a.ws, s);
         return run_sweep((const void*)fwd_sweep<OP, T, WIO, PT>, a,
                          sweep_batch(a.rows, (int64_t)a.cols * streams * sizeof(T), a.l2_bytes),
                          WIO::N, s);
+    }
     const RingKernels fn{(const void*)fwd_ring<OP, T, IO, PT, 4, 1>,
                          (const void*)fwd_ring<OP, T, IO, PT, 4, 2>,
                          (const void*)fwd_ring<OP, T, IO, PT, 8, 1>};
@@ -529,11 +738,19 @@ int train_chunks(int dtype, int64_t cols) {
 }
 
 int64_t norm_fwd_partials(int dtype, int64_t rows, int64_t cols, int sms) {
-    // the sweep runs where the ring does not hold x and residual; a
-    // call without residual then has room it does not need
+    const int es = dtype == 0 ? 4 : 2;
     const int tiles = (int)((cols + VecIO<float, 4>::kTile - 1) / VecIO<float, 4>::kTile);
-    if (tiles <= 4 || ring_fits(tiles, dtype == 0 ? 4 : 2, 2, 2, rows, sms)) return 0;
-    return rows * train_chunks(dtype, cols) * 8;
+    if (tiles <= 4 || rows == 0) return 0;
+    int64_t most = 0;
+    for (int streams = 1; streams <= 2; ++streams) {  // without and with a residual
+        if (ring_fits(tiles, es, streams, 2, rows, sms)) continue;
+        TeamPlan team;
+        if (plan_team(tiles, es, streams, rows, sms, &team))
+            most = std::max(most, team.exchange_bytes);
+        else
+            most = std::max(most, rows * train_chunks(dtype, cols) * 8);
+    }
+    return most;
 }
 
 cudaError_t launch_norm_fwd(TrainKey k, const NormFwdArgs& a, int sms, cudaStream_t s) {

@@ -2,10 +2,11 @@
 #include "ring_plan.h"
 
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 #include <vector>
 
-#include "common.cuh"
+#include "team.cuh"
 #include "planner.h"
 
 namespace credit {
@@ -214,6 +215,58 @@ cudaError_t launch_ring_args(const void* fn, void** args, const RingPlan& p, int
     attr[0].val.clusterDim.x = (unsigned)p.P;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+// From teams of a few CTAs to one of all SMs: the size whose CTAs have the least
+// to do, rows of a team times the tiles of a slice and a fixed part a row.
+bool plan_team(int tiles, int es, int streams, int64_t rows, int sms, TeamPlan* out) {
+    struct Known { int tiles, es, streams, sms; int64_t rows; bool found; TeamPlan plan; };
+    static thread_local Known known[8] = {};  // the last shapes' answers
+    Known& k = known[(uint64_t)(rows * 5 + tiles + streams) % 8];
+    if (k.tiles == tiles && k.es == es && k.streams == streams && k.sms == sms && k.rows == rows) {
+        *out = k.plan;
+        return k.found;
+    }
+    float best = INFINITY;
+    for (int T = std::max(2, (tiles + 4 * kTeamWarps - 1) / (4 * kTeamWarps));
+         T <= std::min(sms, kTeamMost); ++T) {
+        TeamPlan p{};
+        p.tiles = (tiles + T - 1) / T;
+        p.size = (tiles + p.tiles - 1) / p.tiles;  // no CTA without columns
+        if (p.size != T) continue;
+        p.W = (p.tiles + 3) / 4;
+        p.room = (p.tiles * kTileCols * es + 16 + 127) / 128 * 128;
+        p.stages = std::min(kRingStages, kMostStage / (p.room * streams));
+        if (p.stages < 3) continue;
+        p.lag = std::min(kTeamLag, std::max(2, p.stages - 2));
+        p.teams = (int)std::min<int64_t>(sms / T, rows);
+        p.smem = (size_t)p.stages * p.room * streams;
+        p.exchange_bytes = (int64_t)p.teams * kTeamSlots * T * 16;
+        const float cost = (float)((rows + p.teams - 1) / p.teams) * (p.tiles + 8);
+        if (cost < best) {
+            best = cost;
+            *out = p;
+        }
+    }
+    k = Known{tiles, es, streams, sms, rows, best < INFINITY, *out};
+    return k.found;
+}
+
+cudaError_t launch_team_args(const void* fn, void** args, const TeamPlan& p, void* words,
+                             cudaStream_t s) {
+    const cudaError_t e = cudaMemsetAsync(words, 0, (size_t)p.exchange_bytes, s);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.size * p.teams));
+    cfg.blockDim = dim3((unsigned)(32 * (2 * p.W + 2)));
+    cfg.dynamicSmemBytes = p.smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;  // the CTAs wait for one another
+    attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelExC(&cfg, fn, args);

@@ -7,7 +7,7 @@
 
 namespace credit {
 
-constexpr int kRingStages = 8;    // most stages
+constexpr int kRingStages = 12;   // most stages
 constexpr int kRingWarps = 16;    // most warps of a CTA
 constexpr int kRingThreads = 32 * kRingWarps;
 
@@ -66,5 +66,22 @@ cudaError_t launch_ring(const void* fn, Args a, const RingPlan& p, int clusters,
     void* args[] = {&a, &q};
     return launch_ring_args(fn, args, p, clusters, s);
 }
+
+constexpr int kTeamWarps = 11;    // most summing (and as many writing) warps of a team's CTA
+
+// A team launch (team.cuh).
+struct TeamPlan {
+    int tiles, stages, room, size, teams, lag, W;
+    size_t smem;
+    int64_t exchange_bytes;  // of the words, which the launch clears
+};
+
+// The team shape for rows of `tiles` tiles in `streams` streams; false where a
+// slice does not fit.  Host only: one CTA per SM.
+bool plan_team(int tiles, int es, int streams, int64_t rows, int sms, TeamPlan* out);
+
+// Clears the words and launches `fn` of (Args, TeamShape).
+cudaError_t launch_team_args(const void* fn, void** args, const TeamPlan& p, void* words,
+                             cudaStream_t s);
 
 }  // namespace credit
