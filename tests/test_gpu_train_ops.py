@@ -140,6 +140,55 @@ def test_many_rows(rows, cols, dtype, norm):
                    backward(norm, q, dy, h, mean, rstd, dh, need_dresidual=True))
 
 
+# rows shared by CTAs across the GPU (more rows than a team has in flight, odd
+# counts, more teams than one), and rows beyond them, swept in two passes
+WIDE = [(13, 300008, "bf16"), (27, 300001, "bf16"), (41, 300000, "f32"), (6, 600008, "f32"),
+        (40, 131080, "bf16"), (90, 60000, "f32"), (75, 70001, "bf16"), (3, 1300000, "bf16"),
+        (2, 1200001, "f32")]
+
+
+@pytest.mark.parametrize("norm", ["layernorm", "rmsnorm"])
+@pytest.mark.parametrize("rows, cols, dtype", WIDE)
+def test_wide_rows(rows, cols, dtype, norm):
+    for residual, p in ((True, 0.1), (False, 0.0)):
+        q = problem(rows, cols, dtype, norm, residual, p, "f32", seed=17)
+        out = forward(norm, q)
+        check_forward(norm, q, out)
+        _, h, mean, rstd = out
+        dy, dh = grads(rows, cols, dtype)
+        dh = dh if residual else None
+        back = backward(norm, q, dy, h, mean, rstd, dh, need_dresidual=residual)
+        check_backward(norm, q, dy, h, mean, rstd, dh, back)
+        again = backward(norm, q, dy, h, mean, rstd, dh, need_dresidual=residual)
+        assert all(a is b is None or torch.equal(a, b) for a, b in zip(back, again))
+    assert credit.device_error() == 0
+
+
+def test_wide_rows_on_two_streams_at_once():
+    # both calls want every SM: one runs after the other, neither waits in vain
+    qs = [problem(20, 300008 + 8 * i, "bf16", "layernorm", False, 0.0, "f32", seed=80 + i)
+          for i in range(2)]
+    dys = [grads(20, 300008 + 8 * i, "bf16")[0] for i in range(2)]
+
+    def step(q, dy):
+        f = forward("layernorm", q)
+        return f, backward("layernorm", q, dy, *f[1:], None)
+
+    want = [step(q, dy) for q, dy in zip(qs, dys)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    for _ in range(4):
+        got = []
+        for s, q, dy in zip(streams, qs, dys):
+            with torch.cuda.stream(s):
+                got.append(step(q, dy))
+        torch.cuda.synchronize()
+        for (f, b), (wf, wb) in zip(got, want):
+            assert all(torch.equal(u, v) for u, v in zip(f, wf))
+            assert all(u is v is None or torch.equal(u, v) for u, v in zip(b, wb))
+    assert credit.device_error() == 0
+
+
 def test_a_training_step_of_two_blocks():
     # two residual steps forward and back; the second's input gradient is the
     # first's incoming one, and every gradient is autograd's in 64 bits on the
