@@ -14,6 +14,7 @@ raises instead of falling back to anything else.
     y = credit.layernorm(x, gamma, beta, eps=1e-5)       # plans automatically
     p = credit.plan("softmax", rows, cols, torch.float32, cluster_size=4)
     y = credit.softmax(x, plan=p)                         # forced cluster size
+    y, h, mean, rstd = credit.layernorm_forward(x, gamma, beta, residual=r)  # for training
 """
 from __future__ import annotations
 

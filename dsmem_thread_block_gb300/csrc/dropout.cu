@@ -1,6 +1,11 @@
 // dropout.cu -- y = residual + keep ? x / (1 - p) : 0, the mask drawn on the
 // way (train.cuh) and never stored.  The same call on the incoming gradient
 // is the backward pass.
+//
+// Measured: 16384 x 8192 bf16 with residual 135 us, 0.88 of the copy rate;
+// 64 x 4096 1.9 us.  Bound by HBM: a mask costs nine instructions an element
+// (36 for a block of four) of the 22 that the SMs issue in an element's time.
+// Two tiles of 16 bytes a lane in flight; one measured 147 us.
 #include "train.cuh"
 
 namespace credit {

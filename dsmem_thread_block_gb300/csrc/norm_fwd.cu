@@ -1,7 +1,7 @@
 // norm_fwd.cu -- h = residual + dropout(x), y = norm(h) and the row statistics
 // (mean, 1/sqrt(var + eps)) that the backward pass needs.
 //
-// Three forms, chosen by the row's width alone:
+// Four forms, chosen by the row's width:
 //   fwd_warp   one warp holds a row's h in registers
 //   fwd_ring   a CTA, or a cluster, holds it; the next rows' x and residual
 //              arrive in a ring of shared-memory stages meanwhile
@@ -9,6 +9,19 @@
 //   fwd_sweep  wider rows: partial statistics per chunk, then a second read,
 //              from L2 (sweep.cuh)
 // Each reads x and residual from HBM once and writes h and y once.
+//
+// Measured (GB300, share of the 6782 GB/s copy rate; bf16, fp32 parameters):
+//   16384 x 4096, LayerNorm, residual, dropout    89 us  0.88   (ring)
+//   8192 x 8192, LayerNorm                         50 us  0.79   (ring)
+//   2048 x 10001, LayerNorm, residual, dropout    64 us  0.38   (ring, odd rows)
+//   1024 x 262144, LayerNorm                      371 us  0.43   (ring, clusters of 16)
+//   1024 x 262144, RMSNorm                        253 us  0.63
+//   one row of 4096, RMSNorm, residual            2.1 us
+// What bounds them: instructions and the latency of a row's reduction, then
+// HBM.  13 instructions an element for LayerNorm (16 with a residual, 27 with
+// dropout too), at 16 warps an SM; odd rows are read, written and masked an
+// element at a time; the widest LayerNorm rows read their parameters from L2
+// for every row, and clusters of 16 leave 40 SMs empty.
 //
 // Statistics: sum and M2 about the piece's own mean (of a warp, a CTA or a
 // chunk), merged with the parallel-axis form of Chan et al.'s update.
@@ -154,6 +167,7 @@ __global__ void __launch_bounds__(kRingThreads) fwd_ring(NormFwdArgs a, RingShap
     const void* const src[2] = {a.x, a.residual};
     const int ns = a.residual ? 2 : 1, stage_bytes = ns * R * q.room;
 
+    layout_fits((uint64_t)q.stages * stage_bytes, q.stages, kRingStages, q.err);
     if (threadIdx.x == 0) {
         for (int s = 0; s < q.stages; ++s) mbar_init(smem_u32(&full[s]), 1);
         if (P > 1) ex.init(P);
@@ -346,6 +360,7 @@ __global__ void __launch_bounds__(kTeamThreads) fwd_team(NormFwdArgs a, TeamShap
     const int turns = (int)((a.rows - team + q.teams - 1) / q.teams);
     auto row_of = [&](int k) { return team + (int64_t)k * q.teams; };
 
+    layout_fits((uint64_t)q.stages * stage_bytes, q.stages, kRingStages, q.err);
     if (threadIdx.x == 0) {
         for (int s = 0; s < q.stages; ++s) mbar_init(smem_u32(&full[s]), 1);
         fence_mbar_init();

@@ -2,7 +2,8 @@
  * credit.h -- C ABI of libcredit: CREDIT's DSMEM reduction-reuse
  * transformation for wide-row reduce-then-reuse operators (row softmax,
  * LayerNorm, RMSNorm, int8 quantization, weighted standardization, Pearson
- * correlation) on GB300 (sm_103a).
+ * correlation) on GB300 (sm_103a); and the training operators of its norms:
+ * forward with residual, dropout and saved statistics, backward, dropout.
  *
  * Operation (CREDIT summary page, arXiv 2609.01864v1, "B. Reduction-Reuse
  * Transformation" and "C. Cluster Reduction and Reuse Protocol"): each row is
@@ -21,7 +22,8 @@
  *
  * Conventions for every entry point:
  *  - Pointers named x, u, y, q, scales, r, gamma, beta, weight(s), workspace
- *    are DEVICE pointers on the current CUDA device; the caller owns them.
+ *    (and the training operators' matrices and vectors) are DEVICE pointers on
+ *    the current CUDA device; the caller owns them.
  *    Nothing on the call path allocates memory.  (credit_run_host takes host
  *    buffers; the calibration and microbenchmark calls allocate scratch.)
  *  - Matrices are row-major with row stride == cols (contiguous rows).
@@ -276,7 +278,10 @@ credit_status_t credit_rmsnorm(const void *x, void *y, int64_t rows,
  * over rows are fp32; every output is rounded once.  Results repeat bit for
  * bit: every sum has a fixed order.  Each call works entirely on `stream`
  * and may be captured; a workspace is used by one call at a time (two
- * captured graphs that may run side by side need one each).
+ * captured graphs that may run side by side need one each).  Large calls on
+ * rows that CTAs all over the GPU share launch cooperatively and use every SM:
+ * such a call waits for SMs that other work holds.  A device wait that gives
+ * up after a second records CREDIT_ERR_DEVICE_TIMEOUT, as above.
  */
 
 /*

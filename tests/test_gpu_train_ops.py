@@ -431,6 +431,30 @@ def test_captured_step_draws_new_masks(rows, cols):
         assert all(torch.equal(a, b) for a, b in zip(got, eager))
 
 
+def test_checked_build_runs_every_form():
+    # the checked build's kernels, reached through the same calls: no index
+    # check fires, and the results are the regular build's
+    cases = [(5, 300, "bf16"), (40, 4096, "bf16"), (7, 10001, "f32"), (6, 40000, "bf16"),
+             (64, 70000, "bf16"), (9, 300008, "f32"), (2, 1300000, "bf16")]
+    for rows, cols, dtype in cases:
+        q = problem(rows, cols, dtype, "layernorm", True, 0.1, "f32", seed=90)
+        dy, dh = grads(rows, cols, dtype)
+
+        def step():
+            f = forward("layernorm", q)
+            return (*f, *backward("layernorm", q, dy, *f[1:], dh, need_dresidual=True),
+                    credit.dropout(q["x"], q["drop"]))
+
+        want = step()
+        torch.cuda.synchronize()
+        with C.use_checked_build():
+            got = step()
+            assert C.credit_get_device_error(torch.cuda.current_device()) == C.OK
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    credit.dropout(q["x"], q["drop"])  # back on the regular build
+    assert credit.device_error() == 0
+
+
 def test_torch_layer_rejects_bad_tensors():
     q = problem(4, 64, "f32", "layernorm", True, 0.2, "f32")
     x, res, g, b = q["x"], q["residual"], q["gamma"], q["beta"]
