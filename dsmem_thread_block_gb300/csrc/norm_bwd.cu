@@ -264,7 +264,8 @@ __global__ void __launch_bounds__(kRingThreads) bwd_ring(NormBwdArgs a, RingShap
             ring_issue<3, 1, T, IO>(src, ns, row, a.rows, a.cols, c0, bytes, ring + s * stage_bytes,
                                     q.room, smem_u32(&full[s]));
     };
-    if (threadIdx.x == 0)
+    const int feeder = W > 1;  // not the warp whose deposit a cluster waits for
+    if (warp == feeder)
         for (int s = 0; s < q.stages; ++s) issue(first + (int64_t)s * q.clusters, s);
 
     const DropStream d(a.drop);
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(kRingThreads) bwd_ring(NormBwdArgs a, RingShap
         if (k == turns) break;
         __syncthreads();
         // every thread has left row k - 1: refill its stage
-        if (threadIdx.x == 0 && k > 0) issue(row + (int64_t)(q.stages - 1) * q.clusters, sp);
+        if (warp == feeder && k > 0) issue(row + (int64_t)(q.stages - 1) * q.clusters, sp);
         if (P > 1 && warp == 0) {
             float t[2];
             spread<2>(half_sum(part < W ? wred[k & 1][which][part] : 0.f), lane, t);
@@ -447,7 +448,7 @@ __global__ void __launch_bounds__(kTeamThreads) bwd_team(NormBwdArgs a, TeamShap
     if (warp == 2 * W + 1) {  // feeds
         const TeamExchange ex(q, team, rank, lane);
         auto issue = [&](int k) {
-            if (lane == 0 && k < turns)
+            if (k < turns)
                 ring_issue<3, 1, T, IO>(src, ns, row_of(k), a.rows, a.cols, c0, bytes,
                                         ring + (k % q.stages) * stage_bytes, q.room,
                                         smem_u32(&full[k % q.stages]));

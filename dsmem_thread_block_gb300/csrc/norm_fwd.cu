@@ -179,7 +179,8 @@ __global__ void __launch_bounds__(kRingThreads) fwd_ring(NormFwdArgs a, RingShap
         cluster_arrive_release();
         cluster_wait_acquire();
     }
-    if (threadIdx.x == 0)
+    const int feeder = W > 1;  // not the warp whose deposit a cluster waits for
+    if (warp == feeder)
         for (int s = 0; s < q.stages; ++s)
             if (first + s * stride < a.rows)
                 ring_issue<2, R, T, IO>(src, ns, first + s * stride, a.rows, a.cols, c0, bytes,
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(kRingThreads) fwd_ring(NormFwdArgs a, RingShap
                 F2 t = f2(0.f);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    typename IO::R rv = {};
+                    typename IO::S rv = {};
                     if (res) rv = IO::template staged<FULL>(rs, i * IO::kTile, left);
                     tile_h<T, IO>(IO::template staged<FULL>(xs, i * IO::kTile, left), rv, res,
                                   on && (FULL || base0 + i * IO::kTile < c1), d,
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(kRingThreads) fwd_ring(NormFwdArgs a, RingShap
         }
         __syncthreads();
         // every thread has read the stage: bring the turn that comes next in it
-        if (threadIdx.x == 0) {
+        if (warp == feeder) {
             const int64_t next = row + q.stages * stride;
             if (next < a.rows)
                 ring_issue<2, R, T, IO>(src, ns, next, a.rows, a.cols, c0, bytes, stage, q.room,
@@ -406,7 +407,7 @@ __global__ void __launch_bounds__(kTeamThreads) fwd_team(NormFwdArgs a, TeamShap
     if (warp == 2 * W + 1) {  // feeds
         const TeamExchange ex(q, team, rank, lane);
         auto issue = [&](int k) {
-            if (lane == 0 && k < turns)
+            if (k < turns)
                 ring_issue<2, 1, T, IO>(src, ns, row_of(k), a.rows, a.cols, c0, bytes,
                                         ring + (k % q.stages) * stage_bytes, q.room,
                                         smem_u32(&full[k % q.stages]));
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(kTeamThreads) fwd_team(NormFwdArgs a, TeamShap
         const T* xs = reinterpret_cast<const T*>(p + ring_shift<IO>(a.x, off)) + (j0 - c0);
         const T* rs = reinterpret_cast<const T*>(p + q.room + ring_shift<IO>(a.residual, off)) +
                       (j0 - c0);
-        typename IO::R rv = {};
+        typename IO::S rv = {};
         if (res) rv = IO::template staged<FULL>(rs, i * IO::kTile, left);
         tile_h<T, IO>(IO::template staged<FULL>(xs, i * IO::kTile, left), rv, res,
                       on && (FULL || base0 + i * IO::kTile < c1), d, base0 + i * IO::kTile, lane,

@@ -36,50 +36,53 @@ struct Lines {
     __device__ bool cut() const { return begin < lo || hi < end; }
 };
 
-// One thread brings the slices of R rows (those below `rows`) of NS streams
-// into a stage; waiters see them when the stage's mbarrier completes its
-// phase.  Slice (stream i, row j) has room i R + j.
+// One warp brings the slices of R rows (those below `rows`) of NS streams into
+// a stage, all lanes calling; waiters see them when the stage's mbarrier
+// completes its phase.  Slice (stream i, row j) has room i R + j.  Rows that
+// are not whole lines take a lane a slice: their addresses, worked out by one
+// thread, were what a turn of 10001 bf16 columns waited for.
 template <int NS, int R, typename T, typename IO>
 __device__ __forceinline__ void ring_issue(const void* const (&src)[NS], int ns, int64_t row,
                                            int64_t rows, int cols, int c0, int bytes,
                                            unsigned char* stage, int room, uint32_t bar) {
     const uint64_t pol = l2_policy_evict_first();
+    const int lane = threadIdx.x & 31;
     const int64_t pitch = (int64_t)cols * (int)sizeof(T);
     const int64_t off = row * pitch + c0 * (int)sizeof(T);
-    const int n = R > 1 && row + 1 < rows ? 2 : 1;
+    const bool two = R > 1 && row + 1 < rows;
     if constexpr (IO::kAligned) {
-        mbar_arrive_expect_tx(bar, (uint32_t)(ns * n * bytes));
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bar, (uint32_t)((two ? 2 * ns : ns) * bytes));
 #pragma unroll
-        for (int i = 0; i < NS; ++i)
-            if (i < ns) {
-                const char* p = static_cast<const char*>(src[i]) + off;
-                const uint32_t d = smem_u32(stage) + i * R * room;
-                bulk_g2s(d, p, (uint32_t)bytes, bar, pol);
-                if (n > 1) bulk_g2s(d + room, p + pitch, (uint32_t)bytes, bar, pol);
-            }
+            for (int i = 0; i < NS; ++i)
+                if (i < ns) {
+                    const char* p = static_cast<const char*>(src[i]) + off;
+                    const uint32_t d = smem_u32(stage) + i * R * room;
+                    bulk_g2s(d, p, (uint32_t)bytes, bar, pol);
+                    if (two) bulk_g2s(d + room, p + pitch, (uint32_t)bytes, bar, pol);
+                }
+        }
     } else {
-        uint32_t tx = 0;
-        for (int e = 0; e < ns * n; ++e) {
-            const int i = e / n, j = e - i * n;
-            const Lines l(static_cast<const char*>(src[i]), off + j * pitch, bytes, rows * pitch);
-            tx += l.bulk();
-            if (l.cut()) {
-                unsigned char* d = stage + (i * R + j) * room;
-                const char* const head = l.lo < l.end ? l.lo : l.end;
-                for (const char* p = l.begin; p < head; p += sizeof(T))
-                    *reinterpret_cast<T*>(d + (p - l.first)) = *reinterpret_cast<const T*>(p);
-                for (const char* p = l.hi > l.begin ? l.hi : l.begin; p < l.end; p += sizeof(T))
-                    *reinterpret_cast<T*>(d + (p - l.first)) = *reinterpret_cast<const T*>(p);
-            }
+        const int i = lane / R, j = lane % R;
+        const char* p = static_cast<const char*>(src[0]);
+#pragma unroll
+        for (int t = 1; t < NS; ++t) p = i == t ? static_cast<const char*>(src[t]) : p;
+        const bool mine = i < ns && (j == 0 || two);
+        const Lines l(p, off + j * pitch, bytes, rows * pitch);
+        unsigned char* const d = stage + lane * room;
+        if (mine && l.cut()) {
+            const char* const head = l.lo < l.end ? l.lo : l.end;
+            for (const char* c = l.begin; c < head; c += sizeof(T))
+                *reinterpret_cast<T*>(d + (c - l.first)) = *reinterpret_cast<const T*>(c);
+            for (const char* c = l.hi > l.begin ? l.hi : l.begin; c < l.end; c += sizeof(T))
+                *reinterpret_cast<T*>(d + (c - l.first)) = *reinterpret_cast<const T*>(c);
         }
-        mbar_arrive_expect_tx(bar, tx);  // releases the plain stores too
-        for (int e = 0; e < ns * n; ++e) {
-            const int i = e / n, j = e - i * n;
-            const Lines l(static_cast<const char*>(src[i]), off + j * pitch, bytes, rows * pitch);
-            if (l.bulk())
-                bulk_g2s(smem_u32(stage) + (i * R + j) * room + (uint32_t)(l.lo - l.first), l.lo,
-                         l.bulk(), bar, pol);
-        }
+        const uint32_t tx = __reduce_add_sync(0xffffffffu, mine ? l.bulk() : 0u);
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(bar, tx);  // releases the plain stores too
+        __syncwarp();
+        if (mine && l.bulk())
+            bulk_g2s(smem_u32(d) + (uint32_t)(l.lo - l.first), l.lo, l.bulk(), bar, pol);
     }
 }
 

@@ -92,6 +92,13 @@ __device__ __forceinline__ void unpack(const Raw<NP * 2 * (int)sizeof(T)>& v, F2
             f[k] = Pairs<bf16>::one(v.w[k]);
     }
 }
+// (bf16 elements already in the upper halves of words)
+template <typename T, int NP, typename = std::enable_if_t<sizeof(T) == 2>>
+__device__ __forceinline__ void unpack(const Raw<NP * 8>& v, F2* f) {
+#pragma unroll
+    for (int k = 0; k < NP; ++k)
+        f[k] = {__uint_as_float(v.w[2 * k]), __uint_as_float(v.w[2 * k + 1])};
+}
 template <typename T, int NP>
 __device__ __forceinline__ Raw<NP * 2 * (int)sizeof(T)> pack(const F2* f) {
     Raw<NP * 2 * (int)sizeof(T)> v;
@@ -118,6 +125,7 @@ template <typename T, int ELEMS> struct VecIO {
     static constexpr int NP = N / 2;  // a lane's elements as pairs (element k: pair k / 2)
     static constexpr int kTile = 32 * N;
     using R = Raw<N * (int)sizeof(T)>;
+    using S = R;
     __device__ static __forceinline__ int first(int lane) { return lane * N; }
     __device__ static __forceinline__ int at(int k) { return k; }  // element k, from the first
     // a lane's vector lies whole inside the row or whole outside
@@ -195,6 +203,7 @@ template <typename T, int ELEMS> struct ElemIO {
     static constexpr int NP = N / 2;
     static constexpr int kTile = 32 * N;
     using R = Raw<N * (int)sizeof(T)>;
+    using S = Raw<N * 4>;  // staged elements: bf16 ones in the upper halves of words
     using Word = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
     __device__ static __forceinline__ int first(int lane) { return lane; }
     __device__ static __forceinline__ int at(int k) { return 32 * k; }
@@ -215,8 +224,13 @@ template <typename T, int ELEMS> struct ElemIO {
         return v;
     }
     template <bool FULL>
-    __device__ static __forceinline__ R staged(const T* p, int off, int left) {
-        return load<FULL>(p, off, left);
+    __device__ static __forceinline__ S staged(const T* p, int off, int left) {
+        const Word* r = reinterpret_cast<const Word*>(p) + off;
+        S v;
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            v.w[k] = in<FULL>(off, k, left) ? (uint32_t)r[32 * k] << (32 - 8 * sizeof(T)) : 0u;
+        return v;
     }
     template <bool FULL>
     __device__ static __forceinline__ void store(T* p, int off, int left, const F2* f) {
@@ -279,10 +293,10 @@ template <typename T, int ELEMS> struct ElemIO {
 
 // h of one tile from its raw values: residual + dropout(x), in fp32 (one
 // fused multiply-add; `has_r` false: no residual).  All 32 lanes call.
-template <typename T, typename IO>
-__device__ __forceinline__ void tile_h(const typename IO::R& xv, const typename IO::R& rv,
-                                       bool has_r, bool on, const DropStream& d, int base,
-                                       int lane, uint32_t row, F2* h) {
+template <typename T, typename IO, typename V>
+__device__ __forceinline__ void tile_h(const V& xv, const V& rv, bool has_r, bool on,
+                                       const DropStream& d, int base, int lane, uint32_t row,
+                                       F2* h) {
     unpack<T, IO::NP>(xv, h);
     if (on) IO::drop(d, base, lane, row, h);
     if (has_r) {
