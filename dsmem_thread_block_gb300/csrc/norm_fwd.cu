@@ -191,7 +191,17 @@ __global__ void __launch_bounds__(kRingThreads) fwd_ring(NormFwdArgs a, RingShap
     const bool whole = base0 + V * IO::kTile <= c1;
     const PT* const gp = moved(static_cast<const PT*>(a.gamma), j0);
     const PT* const bp = moved(static_cast<const PT*>(a.beta), j0);
-    const bool affine = whole && gp && (OP != kLayerNorm || bp);
+    constexpr bool kHeld = V == 4;  // the parameters stay in registers
+    const bool affine = whole && (kHeld || (gp && (OP != kLayerNorm || bp)));
+    F2 hg[kHeld ? V : 1][IO::NP], hb[kHeld ? V : 1][IO::NP];
+    if constexpr (kHeld) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            IO::template params<false>(gp, i * IO::kTile, left, hg[i], 1.f);
+            if (OP == kLayerNorm) IO::template params<false>(bp, i * IO::kTile, left, hb[i], 0.f);
+            else for (int e = 0; e < IO::NP; ++e) hb[i][e] = f2(0.f);
+        }
+    }
     // columns of this warp, of the warp and of the CTA that this lane merges
     const int part = lane & 15;
     const float inv_warp = 1.f / (float)max(1, min(c1 - base0, V * IO::kTile));
@@ -314,9 +324,13 @@ __global__ void __launch_bounds__(kRingThreads) fwd_ring(NormFwdArgs a, RingShap
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 F2 g[IO::NP], b[IO::NP];
-                IO::template params<FULL>(gp, i * IO::kTile, left, g, 1.f, FULL);
-                if (OP == kLayerNorm) IO::template params<FULL>(bp, i * IO::kTile, left, b, 0.f, FULL);
-                else for (int e = 0; e < IO::NP; ++e) b[e] = f2(0.f);
+                if constexpr (kHeld) {
+                    for (int e = 0; e < IO::NP; ++e) g[e] = hg[i][e], b[e] = hb[i][e];
+                } else {
+                    IO::template params<FULL>(gp, i * IO::kTile, left, g, 1.f, FULL);
+                    if (OP == kLayerNorm) IO::template params<FULL>(bp, i * IO::kTile, left, b, 0.f, FULL);
+                    else for (int e = 0; e < IO::NP; ++e) b[e] = f2(0.f);
+                }
 #pragma unroll
                 for (int j = 0; j < R; ++j) {
 #pragma unroll
