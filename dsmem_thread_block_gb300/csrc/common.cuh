@@ -266,6 +266,17 @@ __device__ __forceinline__ int quant_code(float x, float s, float inv) {
     return max(-127, min(127, __float2int_rn(c)));
 }
 
+// Whether the phase of this parity has completed; never suspends the thread.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+
 // Bounded mbarrier wait: spins on try_wait; after kWaitLimitNs sets the
 // device error word and returns false (the caller carries on so that every
 // cluster barrier is still reached).

@@ -410,9 +410,9 @@ template <int OP, typename T, typename IO, typename PT>
 __global__ void __launch_bounds__(kTeamThreads) bwd_team(NormBwdArgs a, TeamShape q) {
     constexpr int V = 4;
     extern __shared__ __align__(128) unsigned char ring[];
-    __shared__ __align__(8) uint64_t full[kRingStages];
-    __shared__ float wred[2][2][kRingWarps];
-    __shared__ float2 tot[2];  // mean_j(w xh), mean_j(w) of the row to write
+    __shared__ __align__(8) TeamBars bars;
+    __shared__ float wred[kTeamStages][2][kTeamWarps];
+    __shared__ float2 tot[kTeamStages];  // mean_j(w xh), mean_j(w)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = (blockDim.x >> 6) - 1;
     const int team = (int)blockIdx.x / q.size, rank = (int)blockIdx.x - team * q.size;
     const int c0 = rank * q.tiles * IO::kTile, c1 = min(a.cols, c0 + q.tiles * IO::kTile);
@@ -422,17 +422,12 @@ __global__ void __launch_bounds__(kTeamThreads) bwd_team(NormBwdArgs a, TeamShap
     const int turns = (int)((a.rows - team + q.teams - 1) / q.teams);
     auto row_of = [&](int k) { return team + (int64_t)k * q.teams; };
 
-    layout_fits((uint64_t)q.stages * stage_bytes, q.stages, kRingStages, q.err);
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < q.stages; ++s) mbar_init(smem_u32(&full[s]), 1);
-        fence_mbar_init();
-        fence_proxy_async_smem();
-    }
-    __syncthreads();
+    layout_fits((uint64_t)q.stages * stage_bytes, q.stages, kTeamStages, q.err);
+    bars.init(q.stages, W);
 
     if (warp == 2 * W) {  // collects
         TeamExchange(q, team, rank, lane)
-            .collect_all(turns, q.lag, [&](int j, int, const float* x, const float* y) {
+            .collect_all(turns, q.stages, bars, [&](int, int st, const float* x, const float* y) {
                 float t1 = 0.f, t2 = 0.f;
 #pragma unroll
                 for (int i = 0; i < kTeamParts; ++i) {
@@ -441,33 +436,29 @@ __global__ void __launch_bounds__(kTeamThreads) bwd_team(NormBwdArgs a, TeamShap
                 }
                 t1 = warp_allreduce(t1, SumOp()) * a.inv_cols;
                 t2 = warp_allreduce(t2, SumOp()) * a.inv_cols;
-                if (lane == 0) tot[(j + 1) & 1] = make_float2(t1, t2);
+                if (lane == 0) tot[st] = make_float2(t1, t2);
             });
         return;
     }
-    if (warp == 2 * W + 1) {  // feeds
+    if (warp == 2 * W + 1) {  // serves
         const TeamExchange ex(q, team, rank, lane);
-        auto issue = [&](int k) {
-            if (k < turns)
-                ring_issue<3, 1, T, IO>(src, ns, row_of(k), a.rows, a.cols, c0, bytes,
-                                        ring + (k % q.stages) * stage_bytes, q.room,
-                                        smem_u32(&full[k % q.stages]));
-            __syncwarp();
-        };
-        for (int k = 0; k < q.stages; ++k) issue(k);
         const int part = lane & 15, which = lane >> 4;
-        for (int j = 0; j < turns + q.lag; ++j) {
-            __syncthreads();
-            if (j < turns) {
-                float t[2];
-                spread<2>(half_sum(part < W ? wred[j & 1][which][part] : 0.f), lane, t);
-                ex.deposit((uint32_t)j, lane ? t[1] : t[0]);
-            }
-            if (j >= q.lag) issue(j - q.lag + q.stages);
-        }
+        bars.serve(
+            turns, q.stages, q.err,
+            [&](int k, int st) {
+                ring_issue<3, 1, T, IO>(src, ns, row_of(k), a.rows, a.cols, c0, bytes,
+                                        ring + st * stage_bytes, q.room, smem_u32(&bars.fed[st]));
+                __syncwarp();
+            },
+            [&](int k, int st) {
+                float v[2];
+                spread<2>(half_sum(part < W ? wred[st][which][part] : 0.f), lane, v);
+                ex.deposit((uint32_t)k, lane ? v[1] : v[0]);
+            });
         return;
     }
 
+    TeamTurn t;
     const bool summing = warp < W;
     const int base0 = c0 + (summing ? warp : warp - W) * V * IO::kTile;
     const int j0 = base0 + IO::first(lane), left = c1 - j0;
@@ -482,22 +473,14 @@ __global__ void __launch_bounds__(kTeamThreads) bwd_team(NormBwdArgs a, TeamShap
                                           ring_shift<IO>(p, off)) + (j0 - c0);
     };
     RowStats next = row_stats<OP>(a, row_of(0));
-    int s = 0;
-    uint32_t phase = 0;
     const std::true_type yes;
     const std::false_type no;
     // row k's stage is here; the next row's statistics are on their way
     auto enter = [&](int k) {
         const RowStats r = next;
         if (k + 1 < turns) next = row_stats<OP>(a, row_of(k + 1));
-        mbar_wait_bounded(smem_u32(&full[s]), phase, q.err);
+        TeamBars::wait(bars.fed[t.s], t, q.err);
         return r;
-    };
-    auto leave = [&] {
-        if (++s == q.stages) {
-            s = 0;
-            phase ^= 1u;
-        }
     };
     if (summing) {
         F2 ag[V][IO::NP], ab[V][IO::NP];
@@ -505,29 +488,26 @@ __global__ void __launch_bounds__(kTeamThreads) bwd_team(NormBwdArgs a, TeamShap
         for (int i = 0; i < V; ++i)
 #pragma unroll
             for (int e = 0; e < IO::NP; ++e) ag[i][e] = ab[i][e] = f2(0.f);
-        for (int j = 0; j < turns + q.lag; ++j) {
-            if (j < turns) {
-                const RowStats r = enter(j);
-                const T* const ys = slice(s, 0, a.dy, row_of(j));
-                const T* const hs = slice(s, 1, a.h, row_of(j));
-                F2 s1 = f2(0.f), s2 = f2(0.f);
-                auto take = [&](auto f) {
-                    constexpr bool FULL = decltype(f)::value;
+        for (int k = 0; k < turns; ++k, t.next(q.stages)) {
+            const RowStats r = enter(k);
+            const T* const ys = slice(t.s, 0, a.dy, row_of(k));
+            const T* const hs = slice(t.s, 1, a.h, row_of(k));
+            F2 s1 = f2(0.f), s2 = f2(0.f);
+            auto take = [&](auto f) {
+                constexpr bool FULL = decltype(f)::value;
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        F2 u[IO::NP], h[IO::NP];
-                        unpack<T, IO::NP>(IO::template staged<FULL>(ys, i * IO::kTile, left), u);
-                        unpack<T, IO::NP>(IO::template staged<FULL>(hs, i * IO::kTile, left), h);
-                        tile_sums<OP, IO::NP>(u, h, g[i], r, s1, s2, ag[i], ab[i]);
-                    }
-                };
-                if (whole) take(yes); else take(no);
-                const float t[2] = {s1.x + s1.y, s2.x + s2.y};
-                const float v = row_sum<2>(t, lane);
-                if ((lane & 15) == 0) wred[j & 1][lane >> 4][warp] = v;
-                leave();
-            }
-            __syncthreads();
+                for (int i = 0; i < V; ++i) {
+                    F2 u[IO::NP], h[IO::NP];
+                    unpack<T, IO::NP>(IO::template staged<FULL>(ys, i * IO::kTile, left), u);
+                    unpack<T, IO::NP>(IO::template staged<FULL>(hs, i * IO::kTile, left), h);
+                    tile_sums<OP, IO::NP>(u, h, g[i], r, s1, s2, ag[i], ab[i]);
+                }
+            };
+            if (whole) take(yes); else take(no);
+            const float v[2] = {s1.x + s1.y, s2.x + s2.y};
+            const float sum = row_sum<2>(v, lane);
+            if ((lane & 15) == 0) wred[t.s][lane >> 4][warp] = sum;
+            TeamBars::done(bars.summed[t.s]);
         }
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -536,38 +516,36 @@ __global__ void __launch_bounds__(kTeamThreads) bwd_team(NormBwdArgs a, TeamShap
     }
     const DropStream d(a.drop);
     const bool simple = !a.drop.on && !a.dres;  // dx is the only matrix written
-    for (int j = 0; j < turns + q.lag; ++j) {
-        if (j >= q.lag) {
-            const int64_t at = row_of(j - q.lag);
-            const RowStats r = enter(j - q.lag);
-            const float2 m = tot[j & 1];
-            const RowBack back(r, m.x, m.y);
-            const T* const ys = slice(s, 0, a.dy, at);
-            const T* const hs = slice(s, 1, a.h, at);
-            const T* const ds = slice(s, 2, a.dh, at);
-            T* const dx = static_cast<T*>(a.dx) + at * a.cols + j0;
-            T* const dres = moved(static_cast<T*>(a.dres), at * a.cols + j0);
-            auto give = [&](auto f, auto has_dh, auto plain) {
-                constexpr bool FULL = decltype(f)::value;
+    for (int k = 0; k < turns; ++k, t.next(q.stages)) {
+        const int64_t at = row_of(k);
+        const RowStats r = enter(k);
+        TeamBars::wait(bars.known[t.s], t, q.err);
+        const float2 m = tot[t.s];
+        const RowBack back(r, m.x, m.y);
+        const T* const ys = slice(t.s, 0, a.dy, at);
+        const T* const hs = slice(t.s, 1, a.h, at);
+        const T* const ds = slice(t.s, 2, a.dh, at);
+        T* const dx = static_cast<T*>(a.dx) + at * a.cols + j0;
+        T* const dres = moved(static_cast<T*>(a.dres), at * a.cols + j0);
+        auto give = [&](auto f, auto has_dh, auto plain) {
+            constexpr bool FULL = decltype(f)::value;
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    F2 u[IO::NP], h[IO::NP], dh[IO::NP];
-                    unpack<T, IO::NP>(IO::template staged<FULL>(ys, i * IO::kTile, left), u);
-                    unpack<T, IO::NP>(IO::template staged<FULL>(hs, i * IO::kTile, left), h);
-                    if (has_dh)
-                        unpack<T, IO::NP>(IO::template staged<FULL>(ds, i * IO::kTile, left), dh);
-                    tile_out<OP, T, IO, FULL>(
-                        d, u, h, g[i], has_dh, dh, r, back, at, base0 + i * IO::kTile, i * IO::kTile,
-                        left, lane, !plain && a.drop.on && (FULL || base0 + i * IO::kTile < c1), dx,
-                        plain ? nullptr : dres);
-                }
-            };
-            if (!whole) give(no, ns > 2, no);
-            else if (ns > 2) simple ? give(yes, yes, yes) : give(yes, yes, no);
-            else simple ? give(yes, no, yes) : give(yes, no, no);
-            leave();
-        }
-        __syncthreads();
+            for (int i = 0; i < V; ++i) {
+                F2 u[IO::NP], h[IO::NP], dh[IO::NP];
+                unpack<T, IO::NP>(IO::template staged<FULL>(ys, i * IO::kTile, left), u);
+                unpack<T, IO::NP>(IO::template staged<FULL>(hs, i * IO::kTile, left), h);
+                if (has_dh)
+                    unpack<T, IO::NP>(IO::template staged<FULL>(ds, i * IO::kTile, left), dh);
+                tile_out<OP, T, IO, FULL>(
+                    d, u, h, g[i], has_dh, dh, r, back, at, base0 + i * IO::kTile, i * IO::kTile,
+                    left, lane, !plain && a.drop.on && (FULL || base0 + i * IO::kTile < c1), dx,
+                    plain ? nullptr : dres);
+            }
+        };
+        if (!whole) give(no, ns > 2, no);
+        else if (ns > 2) simple ? give(yes, yes, yes) : give(yes, yes, no);
+        else simple ? give(yes, no, yes) : give(yes, no, no);
+        TeamBars::done(bars.written[t.s]);
     }
 }
 

@@ -362,9 +362,9 @@ template <int OP, typename T, typename IO, typename PT>
 __global__ void __launch_bounds__(kTeamThreads) fwd_team(NormFwdArgs a, TeamShape q) {
     constexpr int V = 4;
     extern __shared__ __align__(128) unsigned char ring[];
-    __shared__ __align__(8) uint64_t full[kRingStages];
-    __shared__ float2 wred[2][kRingWarps];
-    __shared__ float2 tot[2];  // mean, rstd of the row to write
+    __shared__ __align__(8) TeamBars bars;
+    __shared__ float2 wred[kTeamStages][kTeamWarps];
+    __shared__ float2 tot[kTeamStages];  // mean, rstd
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = (blockDim.x >> 6) - 1;
     const int team = (int)blockIdx.x / q.size, rank = (int)blockIdx.x - team * q.size;
     const int slice = q.tiles * IO::kTile;
@@ -375,13 +375,8 @@ __global__ void __launch_bounds__(kTeamThreads) fwd_team(NormFwdArgs a, TeamShap
     const int turns = (int)((a.rows - team + q.teams - 1) / q.teams);
     auto row_of = [&](int k) { return team + (int64_t)k * q.teams; };
 
-    layout_fits((uint64_t)q.stages * stage_bytes, q.stages, kRingStages, q.err);
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < q.stages; ++s) mbar_init(smem_u32(&full[s]), 1);
-        fence_mbar_init();
-        fence_proxy_async_smem();
-    }
-    __syncthreads();
+    layout_fits((uint64_t)q.stages * stage_bytes, q.stages, kTeamStages, q.err);
+    bars.init(q.stages, W);
 
     if (warp == 2 * W) {  // collects: sums, M2 about each CTA's mean
         float n[kTeamParts], inv_n[kTeamParts];  // columns of the CTAs this lane merges
@@ -391,7 +386,7 @@ __global__ void __launch_bounds__(kTeamThreads) fwd_team(NormFwdArgs a, TeamShap
             inv_n[i] = 1.f / fmaxf(n[i], 1.f);
         }
         TeamExchange(q, team, rank, lane)
-            .collect_all(turns, q.lag, [&](int j, int due, const float* x, const float* y) {
+            .collect_all(turns, q.stages, bars, [&](int k, int st, const float* x, const float* y) {
                 float mu = 0.f, m2 = 0.f;
                 if constexpr (OP == kLayerNorm) {
 #pragma unroll
@@ -409,32 +404,29 @@ __global__ void __launch_bounds__(kTeamThreads) fwd_team(NormFwdArgs a, TeamShap
                 m2 = warp_allreduce(m2, SumOp());
                 const float rstd = rsqrtf(fmaf(m2, a.inv_cols, a.eps));
                 if (lane == 0) {
-                    tot[(j + 1) & 1] = make_float2(mu, rstd);
+                    tot[st] = make_float2(mu, rstd);
                     if (rank == 0) {
-                        if (a.mean) a.mean[row_of(due)] = mu;
-                        if (a.rstd) a.rstd[row_of(due)] = rstd;
+                        if (a.mean) a.mean[row_of(k)] = mu;
+                        if (a.rstd) a.rstd[row_of(k)] = rstd;
                     }
                 }
             });
         return;
     }
-    if (warp == 2 * W + 1) {  // feeds
+    if (warp == 2 * W + 1) {  // serves
         const TeamExchange ex(q, team, rank, lane);
-        auto issue = [&](int k) {
-            if (k < turns)
-                ring_issue<2, 1, T, IO>(src, ns, row_of(k), a.rows, a.cols, c0, bytes,
-                                        ring + (k % q.stages) * stage_bytes, q.room,
-                                        smem_u32(&full[k % q.stages]));
-            __syncwarp();
-        };
-        for (int k = 0; k < q.stages; ++k) issue(k);
         const int part = lane & 15;
         const float wn = (float)max(0, min(c1 - (c0 + part * V * IO::kTile), V * IO::kTile));
         const float inv_wn = 1.f / fmaxf(wn, 1.f), inv_cta = 1.f / (float)(c1 - c0);
-        for (int j = 0; j < turns + q.lag; ++j) {
-            __syncthreads();
-            if (j < turns) {
-                const float2 w = part < W ? wred[j & 1][part] : make_float2(0.f, 0.f);
+        bars.serve(
+            turns, q.stages, q.err,
+            [&](int k, int st) {
+                ring_issue<2, 1, T, IO>(src, ns, row_of(k), a.rows, a.cols, c0, bytes,
+                                        ring + st * stage_bytes, q.room, smem_u32(&bars.fed[st]));
+                __syncwarp();
+            },
+            [&](int k, int st) {
+                const float2 w = part < W ? wred[st][part] : make_float2(0.f, 0.f);
                 float sum = 0.f, m2 = w.y;
                 if constexpr (OP == kLayerNorm) {
                     sum = half_sum(w.x);
@@ -442,27 +434,24 @@ __global__ void __launch_bounds__(kTeamThreads) fwd_team(NormFwdArgs a, TeamShap
                     m2 = fmaf(wn * e, e, m2);
                 }
                 m2 = half_sum(m2);
-                ex.deposit((uint32_t)j, lane ? m2 : sum);
-            }
-            if (j >= q.lag) issue(j - q.lag + q.stages);
-        }
+                ex.deposit((uint32_t)k, lane ? m2 : sum);
+            });
         return;
     }
 
+    TeamTurn t;
     const DropStream d(a.drop);
     const bool summing = warp < W;
     const int base0 = c0 + (summing ? warp : warp - W) * V * IO::kTile;
     const int j0 = base0 + IO::first(lane), left = c1 - j0;
     const bool whole = base0 + V * IO::kTile <= c1;
-    int s = 0;
-    uint32_t phase = 0;
     const std::true_type yes;
     const std::false_type no;
-    // h of a tile of the row in stage s
+    // h of a tile of the row in the stage
     auto tile = [&](auto f, auto res, auto on, int64_t row, int i, F2 (&h)[IO::NP]) {
         constexpr bool FULL = decltype(f)::value;
         const int64_t off = (row * a.cols + c0) * (int64_t)sizeof(T);
-        const unsigned char* const p = ring + s * stage_bytes;
+        const unsigned char* const p = ring + t.s * stage_bytes;
         const T* xs = reinterpret_cast<const T*>(p + ring_shift<IO>(a.x, off)) + (j0 - c0);
         const T* rs = reinterpret_cast<const T*>(p + q.room + ring_shift<IO>(a.residual, off)) +
                       (j0 - c0);
@@ -478,48 +467,39 @@ __global__ void __launch_bounds__(kTeamThreads) fwd_team(NormFwdArgs a, TeamShap
         else if (ns > 1) a.drop.on ? f(yes, yes, yes) : f(yes, yes, no);
         else a.drop.on ? f(yes, no, yes) : f(yes, no, no);
     };
-    auto leave = [&] {
-        if (++s == q.stages) {
-            s = 0;
-            phase ^= 1u;
-        }
-    };
     if (summing) {
         const float inv_warp = 1.f / (float)max(1, min(c1 - base0, V * IO::kTile));
-        for (int j = 0; j < turns + q.lag; ++j) {
-            if (j < turns) {
-                mbar_wait_bounded(smem_u32(&full[s]), phase, q.err);
-                pick([&](auto f, auto res, auto on) {
-                    constexpr bool FULL = decltype(f)::value;
-                    F2 h[V][IO::NP], t = f2(0.f);
+        for (int k = 0; k < turns; ++k, t.next(q.stages)) {
+            TeamBars::wait(bars.fed[t.s], t, q.err);
+            pick([&](auto f, auto res, auto on) {
+                constexpr bool FULL = decltype(f)::value;
+                F2 h[V][IO::NP], v = f2(0.f);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        tile(f, res, on, row_of(j), i, h[i]);
+                for (int i = 0; i < V; ++i) {
+                    tile(f, res, on, row_of(k), i, h[i]);
 #pragma unroll
-                        for (int e = 0; e < IO::NP; ++e)
-                            t = OP == kLayerNorm ? add2(t, h[i][e]) : fma2(h[i][e], h[i][e], t);
-                    }
-                    const float sum = warp_allreduce(t.x + t.y, SumOp());
-                    float m2 = sum;
-                    if constexpr (OP == kLayerNorm) {
-                        const float mu = sum * inv_warp;
-                        t = f2(0.f);
+                    for (int e = 0; e < IO::NP; ++e)
+                        v = OP == kLayerNorm ? add2(v, h[i][e]) : fma2(h[i][e], h[i][e], v);
+                }
+                const float sum = warp_allreduce(v.x + v.y, SumOp());
+                float m2 = sum;
+                if constexpr (OP == kLayerNorm) {
+                    const float mu = sum * inv_warp;
+                    v = f2(0.f);
 #pragma unroll
-                        for (int i = 0; i < V; ++i)
+                    for (int i = 0; i < V; ++i)
 #pragma unroll
-                            for (int e = 0; e < IO::NP; ++e) {
-                                F2 z = add2(h[i][e], f2(-mu));
-                                if constexpr (!FULL)
-                                    z = inside<FULL, IO>(z, i * IO::kTile, e, left);
-                                t = fma2(z, z, t);
-                            }
-                        m2 = warp_allreduce(t.x + t.y, SumOp());
-                    }
-                    if (lane == 0) wred[j & 1][warp] = make_float2(sum, m2);
-                });
-                leave();
-            }
-            __syncthreads();
+                        for (int e = 0; e < IO::NP; ++e) {
+                            F2 z = add2(h[i][e], f2(-mu));
+                            if constexpr (!FULL)
+                                z = inside<FULL, IO>(z, i * IO::kTile, e, left);
+                            v = fma2(z, z, v);
+                        }
+                    m2 = warp_allreduce(v.x + v.y, SumOp());
+                }
+                if (lane == 0) wred[t.s][warp] = make_float2(sum, m2);
+            });
+            TeamBars::done(bars.summed[t.s]);
         }
         return;
     }
@@ -531,29 +511,27 @@ __global__ void __launch_bounds__(kTeamThreads) fwd_team(NormFwdArgs a, TeamShap
         IO::template params<false>(gp, i * IO::kTile, left, g[i], 1.f);
         IO::template params<false>(bp, i * IO::kTile, left, b[i], 0.f);
     }
-    for (int j = 0; j < turns + q.lag; ++j) {
-        if (j >= q.lag) {
-            const int64_t at = row_of(j - q.lag);
-            mbar_wait_bounded(smem_u32(&full[s]), phase, q.err);
-            const float2 m = tot[j & 1];
-            T* const y = static_cast<T*>(a.y) + at * a.cols + j0;
-            T* const ho = moved(static_cast<T*>(a.h), at * a.cols + j0);
-            pick([&](auto f, auto res, auto on) {
-                constexpr bool FULL = decltype(f)::value;
+    for (int k = 0; k < turns; ++k, t.next(q.stages)) {
+        const int64_t at = row_of(k);
+        TeamBars::wait(bars.fed[t.s], t, q.err);
+        TeamBars::wait(bars.known[t.s], t, q.err);
+        const float2 m = tot[t.s];
+        T* const y = static_cast<T*>(a.y) + at * a.cols + j0;
+        T* const ho = moved(static_cast<T*>(a.h), at * a.cols + j0);
+        pick([&](auto f, auto res, auto on) {
+            constexpr bool FULL = decltype(f)::value;
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    F2 h[IO::NP];
-                    tile(f, res, on, at, i, h);
-                    if ((res || on) && ho) IO::template store<FULL>(ho, i * IO::kTile, left, h);
+            for (int i = 0; i < V; ++i) {
+                F2 h[IO::NP];
+                tile(f, res, on, at, i, h);
+                if ((res || on) && ho) IO::template store<FULL>(ho, i * IO::kTile, left, h);
 #pragma unroll
-                    for (int e = 0; e < IO::NP; ++e)
-                        h[e] = normed<OP>(h[e], m.x, m.y, g[i][e], b[i][e]);
-                    IO::template store<FULL>(y, i * IO::kTile, left, h);
-                }
-            });
-            leave();
-        }
-        __syncthreads();
+                for (int e = 0; e < IO::NP; ++e)
+                    h[e] = normed<OP>(h[e], m.x, m.y, g[i][e], b[i][e]);
+                IO::template store<FULL>(y, i * IO::kTile, left, h);
+            }
+        });
+        TeamBars::done(bars.written[t.s]);
     }
 }
 

@@ -239,9 +239,8 @@ bool plan_team(int tiles, int es, int streams, int64_t rows, int sms, TeamPlan* 
         if (p.size != T) continue;
         p.W = (p.tiles + 3) / 4;
         p.room = (p.tiles * kTileCols * es + 16 + 127) / 128 * 128;
-        p.stages = std::min(kRingStages, kMostStage / (p.room * streams));
+        p.stages = std::min(kTeamStages, kMostStage / (p.room * streams));
         if (p.stages < 3) continue;
-        p.lag = std::min(kTeamLag, std::max(2, p.stages - 2));
         p.teams = (int)std::min<int64_t>(sms / T, rows);
         p.smem = (size_t)p.stages * p.room * streams;
         p.exchange_bytes = (int64_t)p.teams * kTeamSlots * T * 16;

@@ -71,7 +71,7 @@ constexpr int kTeamWarps = 11;    // most summing (and as many writing) warps of
 
 // A team launch (team.cuh).
 struct TeamPlan {
-    int tiles, stages, room, size, teams, lag, W;
+    int tiles, stages, room, size, teams, W;
     size_t smem;
     int64_t exchange_bytes;  // of the words, which the launch clears
 };
