@@ -20,9 +20,9 @@
 // said otherwise):
 //   16384 x 4096 bf16, LayerNorm, dh, dropout    142 us  0.70   (ring)
 //   8192 x 8192 bf16, RMSNorm, dh, bf16 weight    88 us  0.90   (ring)
-//   2048 x 10001 fp32, LayerNorm                  51 us  0.71   (ring, clusters of 5)
-//   1024 x 262144 bf16, LayerNorm                347 us  0.69   (team)
-//   256 x 786432 bf16, RMSNorm, bf16 weight      275 us  0.65   (team)
+//   2048 x 10001 fp32, LayerNorm                  48 us  0.76   (ring, clusters of 5)
+//   1024 x 262144 bf16, LayerNorm                331 us  0.72   (team)
+//   256 x 786432 bf16, RMSNorm, bf16 weight      225 us  0.79   (team)
 //   32 x 1024 fp32, LayerNorm                    5.1 us (two launches)
 // What bounds them: instructions (21 an element for RMSNorm, 26 for LayerNorm,
 // half as much again with dropout) at the 16 warps an SM that the parameter
@@ -426,8 +426,9 @@ __global__ void __launch_bounds__(kTeamThreads) bwd_team(NormBwdArgs a, TeamShap
     bars.init(q.stages, W);
 
     if (warp == 2 * W) {  // collects
-        TeamExchange(q, team, rank, lane)
-            .collect_all(turns, q.stages, bars, [&](int, int st, const float* x, const float* y) {
+        TeamExchange(q, team, rank, lane).collect(
+            turns, q.stages, bars,
+            [&](const float* x, const float* y) {
                 float t1 = 0.f, t2 = 0.f;
 #pragma unroll
                 for (int i = 0; i < kTeamParts; ++i) {
@@ -435,8 +436,10 @@ __global__ void __launch_bounds__(kTeamThreads) bwd_team(NormBwdArgs a, TeamShap
                     t2 += y[i];
                 }
                 t1 = warp_allreduce(t1, SumOp()) * a.inv_cols;
-                t2 = warp_allreduce(t2, SumOp()) * a.inv_cols;
-                if (lane == 0) tot[st] = make_float2(t1, t2);
+                return make_float2(t1, warp_allreduce(t2, SumOp()) * a.inv_cols);
+            },
+            [&](int, int st, float2 m) {
+                if (lane == 0) tot[st] = m;
             });
         return;
     }
@@ -453,7 +456,7 @@ __global__ void __launch_bounds__(kTeamThreads) bwd_team(NormBwdArgs a, TeamShap
             [&](int k, int st) {
                 float v[2];
                 spread<2>(half_sum(part < W ? wred[st][which][part] : 0.f), lane, v);
-                ex.deposit((uint32_t)k, lane ? v[1] : v[0]);
+                ex.deposit(k, v[0], v[1]);
             });
         return;
     }

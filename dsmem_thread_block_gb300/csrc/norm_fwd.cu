@@ -11,17 +11,19 @@
 // Each reads x and residual from HBM once and writes h and y once.
 //
 // Measured (GB300, share of the 6782 GB/s copy rate; bf16, fp32 parameters):
-//   16384 x 4096, LayerNorm, residual, dropout    89 us  0.88   (ring)
-//   8192 x 8192, LayerNorm                         50 us  0.79   (ring)
-//   2048 x 10001, LayerNorm, residual, dropout    64 us  0.38   (ring, odd rows)
-//   1024 x 262144, LayerNorm                      371 us  0.43   (ring, clusters of 16)
-//   1024 x 262144, RMSNorm                        253 us  0.63
+//   16384 x 4096, LayerNorm, residual, dropout    88 us  0.90   (ring)
+//   8192 x 8192, LayerNorm                         49 us  0.81   (ring)
+//   2048 x 10001, LayerNorm, residual, dropout    53 us  0.46   (ring, odd rows)
+//   1024 x 262144, LayerNorm                      359 us  0.44   (ring, clusters of 16)
+//   1024 x 262144, RMSNorm                        239 us  0.66
+//   300 x 850000, LayerNorm                       267 us  0.57   (team)
 //   one row of 4096, RMSNorm, residual            2.1 us
 // What bounds them: instructions and the latency of a row's reduction, then
 // HBM.  13 instructions an element for LayerNorm (16 with a residual, 27 with
 // dropout too), at 16 warps an SM; odd rows are read, written and masked an
 // element at a time; the widest LayerNorm rows read their parameters from L2
-// for every row, and clusters of 16 leave 40 SMs empty.
+// for every row, and clusters of 16 leave 40 SMs empty (teams use them all, but
+// took 355 us for LayerNorm and 302 for RMSNorm on 1024 x 262144).
 //
 // Statistics: sum and M2 about the piece's own mean (of a warp, a CTA or a
 // chunk), merged with the parallel-axis form of Chan et al.'s update.
@@ -385,8 +387,9 @@ __global__ void __launch_bounds__(kTeamThreads) fwd_team(NormFwdArgs a, TeamShap
             n[i] = (float)max(0, min(a.cols - (lane + 32 * i) * slice, slice));
             inv_n[i] = 1.f / fmaxf(n[i], 1.f);
         }
-        TeamExchange(q, team, rank, lane)
-            .collect_all(turns, q.stages, bars, [&](int k, int st, const float* x, const float* y) {
+        TeamExchange(q, team, rank, lane).collect(
+            turns, q.stages, bars,
+            [&](const float* x, const float* y) {
                 float mu = 0.f, m2 = 0.f;
                 if constexpr (OP == kLayerNorm) {
 #pragma unroll
@@ -402,12 +405,14 @@ __global__ void __launch_bounds__(kTeamThreads) fwd_team(NormFwdArgs a, TeamShap
                     }
                 }
                 m2 = warp_allreduce(m2, SumOp());
-                const float rstd = rsqrtf(fmaf(m2, a.inv_cols, a.eps));
+                return make_float2(mu, rsqrtf(fmaf(m2, a.inv_cols, a.eps)));
+            },
+            [&](int k, int st, float2 m) {
                 if (lane == 0) {
-                    tot[st] = make_float2(mu, rstd);
+                    tot[st] = m;
                     if (rank == 0) {
-                        if (a.mean) a.mean[row_of(k)] = mu;
-                        if (a.rstd) a.rstd[row_of(k)] = rstd;
+                        if (a.mean) a.mean[row_of(k)] = m.x;
+                        if (a.rstd) a.rstd[row_of(k)] = m.y;
                     }
                 }
             });
@@ -434,7 +439,7 @@ __global__ void __launch_bounds__(kTeamThreads) fwd_team(NormFwdArgs a, TeamShap
                     m2 = fmaf(wn * e, e, m2);
                 }
                 m2 = half_sum(m2);
-                ex.deposit((uint32_t)k, lane ? m2 : sum);
+                ex.deposit(k, sum, m2);
             });
         return;
     }

@@ -243,7 +243,7 @@ bool plan_team(int tiles, int es, int streams, int64_t rows, int sms, TeamPlan* 
         if (p.stages < 3) continue;
         p.teams = (int)std::min<int64_t>(sms / T, rows);
         p.smem = (size_t)p.stages * p.room * streams;
-        p.exchange_bytes = (int64_t)p.teams * kTeamSlots * T * 16;
+        p.exchange_bytes = (int64_t)p.teams * kTeamSlots * (T + 1) * 16;
         const float cost = (float)((rows + p.teams - 1) / p.teams) * (p.tiles + 8);
         if (cost < best) {
             best = cost;

@@ -12,12 +12,16 @@
 //     fed      the serving warp issues the copies of a turn into a free stage
 //     summed   W warps sum it, a part each; the serving warp merges the parts
 //              and deposits the CTA's in L2
-//     known    the collecting warp merges the team's parts: the row's statistics
+//     known    the collecting warp has the row's statistics from the exchange
 //     written  W warps write the row's outputs; the stage is free
-// No barrier joins them, so each kind runs as far ahead as the stages allow and
-// the exchange's latency falls on no one: with one barrier a row for all of
-// them the GPU took @ us for 256 rows of 786432 bf16 columns (RMSNorm
-// backward), now @.
+// No barrier joins them, so each kind runs as far ahead as the stages allow.
+//
+// Measured on 256 rows of 786432 bf16 columns, RMSNorm backward: warps that sum
+// and write, 366 us; the kinds apart with a barrier a row, 314 and later 272;
+// mbarriers 269; statistics from one CTA a turn instead of every CTA merging
+// all parts, 225 (0.79 of the copy rate).  What bounds it now is a turn's
+// passage through the slowest CTA, 0.7 to 1.0 us however few columns it has:
+// 1024 rows of 262144 columns take 331 us with 50 CTAs a row, 740 with 140.
 #pragma once
 
 #include "planner.h"
@@ -38,7 +42,7 @@ struct TeamShape {
     int32_t room;       // bytes of one stream's slice in a stage
     int32_t size;       // CTAs of a team
     int32_t teams;
-    unsigned long long* words;  // [team][slot][CTA][2], zero before the launch
+    ulonglong2* words;  // a team: [slot][CTA] parts, [slot] statistics; zero before the launch
     unsigned* err;
 };
 
@@ -123,91 +127,110 @@ struct TeamBars {
     }
 };
 
-// A part is two words of (value, turn + 1): each word arrives whole, so a word
-// that carries the turn carries its value, and no fence orders two words.  A
-// slot is used again kTeamSlots turns later: a CTA that deposits turn k has
-// collected turn k - stages (its stage was free again), so every CTA has
-// deposited that one and has collected turn k - 2 stages; with 2 stages <=
-// kTeamSlots nobody still reads the slot.
+// The exchange: every CTA deposits its part of a turn, turn k's leader (the CTA
+// of rank k % T) merges the T parts and publishes the row's statistics, which
+// every CTA reads.  So a CTA merges one turn in T, and one load (a lane a turn)
+// brings it all the turns that have been published since the last.
+//
+// Parts and statistics are two words of (value, turn + 1): each word arrives
+// whole, so a word that carries the turn carries its value, and no fence orders
+// two words.  A slot is used again kTeamSlots turns later: a CTA that deposits
+// turn k has the statistics of the turns up to k - stages (its stage was free
+// again), so those turns' leaders have read all parts, and every CTA had the
+// statistics of the turns up to k - 2 stages when it deposited that part; with
+// 2 stages <= kTeamSlots nobody still reads the slot.
 struct TeamExchange {
-    unsigned long long* words;
+    using Pair = ulonglong2;
+    Pair* parts;  // [slot][CTA]
+    Pair* stats;  // [slot]
     int size, rank, lane;
     unsigned* err;
-    bool dead = false;  // a wait gave up: the next ones do not wait again
 
     __device__ TeamExchange(const TeamShape& q, int team, int r, int l)
-        : words(q.words + (size_t)team * kTeamSlots * q.size * 2), size(q.size), rank(r), lane(l),
-          err(q.err) {}
-    __device__ unsigned long long* slot(uint32_t turn) const {
-        return words + (size_t)(turn % kTeamSlots) * size * 2;
+        : parts(q.words + (size_t)team * kTeamSlots * (q.size + 1)),
+          stats(parts + (size_t)kTeamSlots * q.size), size(q.size), rank(r), lane(l), err(q.err) {}
+    __device__ static void put(Pair* p, int turn, float a, float b) {
+        const unsigned long long tag = (unsigned long long)(uint32_t)(turn + 1) << 32;
+        asm volatile("st.relaxed.gpu.global.v2.u64 [%0], {%1, %2};"
+                     :: "l"(p), "l"(tag | __float_as_uint(a)), "l"(tag | __float_as_uint(b))
+                     : "memory");
     }
-    // lanes 0 and 1: the CTA's two values
-    __device__ void deposit(uint32_t turn, float v) const {
-        if (lane < 2) {
-            const unsigned long long w =
-                (unsigned long long)__float_as_uint(v) | ((unsigned long long)(turn + 1) << 32);
-            asm volatile("st.relaxed.gpu.global.u64 [%0], %1;"
-                         :: "l"(slot(turn) + 2 * rank + lane), "l"(w) : "memory");
-        }
+    __device__ static Pair get(const Pair* p) {
+        Pair v;
+        asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];"
+                     : "=l"(v.x), "=l"(v.y) : "l"(p) : "memory");
+        return v;
     }
-    // Lane l holds the words of CTAs l, l + 32, ... of a turn.  `fetch` only
-    // issues the loads, so that they travel while the warp works on another
-    // turn; `collect` loads again until every word carries the turn.
-    struct Words { unsigned long long w[kTeamParts][2]; };
-    __device__ void fetch(uint32_t turn, Words& f) const {
-        const unsigned long long* const p = slot(turn);
-#pragma unroll
-        for (int i = 0; i < kTeamParts; ++i) {
-            const int c = lane + 32 * i;
-            if (c < size) {
-                asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(f.w[i][0]) : "l"(p + 2 * c));
-                asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];"
-                             : "=l"(f.w[i][1]) : "l"(p + 2 * c + 1));
-            }
-        }
+    __device__ static bool of(const Pair& v, int turn) {
+        return (uint32_t)(v.x >> 32) == (uint32_t)(turn + 1) &&
+               (uint32_t)(v.y >> 32) == (uint32_t)(turn + 1);
     }
-    __device__ bool arrived(uint32_t turn, const Words& f) const {
-        bool all = true;
-#pragma unroll
-        for (int i = 0; i < kTeamParts; ++i)
-            if (lane + 32 * i < size)
-                all = all && (uint32_t)(f.w[i][0] >> 32) == turn + 1 &&
-                      (uint32_t)(f.w[i][1] >> 32) == turn + 1;
-        return __all_sync(0xffffffffu, all);
+    __device__ void deposit(int turn, float a, float b) const {
+        if (lane == 0) put(parts + (size_t)(turn % kTeamSlots) * size + rank, turn, a, b);
     }
-    // After a fetch of this turn: the parts, zeros past the team.
-    __device__ void collect(uint32_t turn, Words& f, float (&a)[kTeamParts],
-                            float (&b)[kTeamParts]) {
+    // The collecting warp: merge(parts of CTAs lane, lane + 32, ...; zeros past
+    // the team) gives a turn's statistics, done(turn, stage, statistics) hands
+    // them to the writing warps.
+    template <typename M, typename F>
+    __device__ void collect(int turns, int stages, TeamBars& bars, M merge, F done) const {
+        TeamTurn t;
+        int k = 0, lead = rank;  // the turn to be known next, the turn to be merged next
         uint64_t t0 = 0;
-        for (uint32_t tries = 0; !arrived(turn, f) && !dead; ++tries) {
-            fetch(turn, f);
+        while (k < turns || lead < turns) {
+            const bool leads = lead < turns && lead < k + stages;  // (no part of later turns)
+            Pair f[kTeamParts], r = {};
+            if (leads) {
+#pragma unroll
+                for (int i = 0; i < kTeamParts; ++i)
+                    if (lane + 32 * i < size)
+                        f[i] = get(parts + (size_t)(lead % kTeamSlots) * size + lane + 32 * i);
+            }
+            if (lane < stages && k + lane < turns) r = get(stats + (k + lane) % kTeamSlots);
+            bool moved = false;
+            if (leads) {
+                bool all = true;
+#pragma unroll
+                for (int i = 0; i < kTeamParts; ++i)
+                    if (lane + 32 * i < size) all = all && of(f[i], lead);
+                if (__all_sync(0xffffffffu, all)) {
+                    float x[kTeamParts], y[kTeamParts];
+#pragma unroll
+                    for (int i = 0; i < kTeamParts; ++i) {
+                        const bool in = lane + 32 * i < size;
+                        x[i] = in ? __uint_as_float((uint32_t)f[i].x) : 0.f;
+                        y[i] = in ? __uint_as_float((uint32_t)f[i].y) : 0.f;
+                    }
+                    const float2 m = merge(x, y);
+                    if (lane == 0) put(stats + lead % kTeamSlots, lead, m.x, m.y);
+                    lead += size;
+                    moved = true;
+                }
+            }
+            const unsigned here = __ballot_sync(0xffffffffu, of(r, k + lane));
+            const int n = min(__ffs((int)~here) - 1, turns - k);  // published without a gap
+            for (int i = 0; i < n; ++i) {
+                const float a = __shfl_sync(0xffffffffu, __uint_as_float((uint32_t)r.x), i);
+                const float b = __shfl_sync(0xffffffffu, __uint_as_float((uint32_t)r.y), i);
+                done(k++, t.s, make_float2(a, b));
+                TeamBars::done(bars.known[t.s]);
+                t.next(stages);
+                moved = true;
+            }
+            if (moved) {
+                t0 = 0;
+                continue;
+            }
             const uint64_t now = globaltimer_ns();
-            if (tries == 0) t0 = now;
+            if (t0 == 0) t0 = now;
             if (__any_sync(0xffffffffu, now - t0 > kWaitLimitNs)) {
                 if (lane == 0) atomicOr(err, kErrTimeout);
-                dead = true;
+                break;
             }
         }
-#pragma unroll
-        for (int i = 0; i < kTeamParts; ++i) {
-            const bool in = lane + 32 * i < size;
-            a[i] = in ? __uint_as_float((uint32_t)f.w[i][0]) : 0.f;
-            b[i] = in ? __uint_as_float((uint32_t)f.w[i][1]) : 0.f;
-        }
-    }
-    // The collecting warp: done(turn, stage, parts...) writes a turn's statistics.
-    // The next turn's words are fetched while this one's are merged.
-    template <typename F> __device__ void collect_all(int turns, int stages, TeamBars& bars, F done) {
-        Words now = {}, then = {};
-        TeamTurn t;
-        for (int k = 0; k < turns; ++k) {
-            if (k + 1 < turns) fetch((uint32_t)(k + 1), then);
-            float x[kTeamParts], y[kTeamParts];
-            collect((uint32_t)k, now, x, y);
-            done(k, t.s, x, y);
+        for (; k < turns; ++k, t.next(stages)) {  // gave up: the other warps still end
+            TeamBars::wait(bars.fed[t.s], t, err);
+            done(k, t.s, make_float2(0.f, 0.f));
             TeamBars::done(bars.known[t.s]);
-            t.next(stages);
-            now = then;
         }
     }
 };
@@ -221,7 +244,7 @@ cudaError_t launch_team(const void* fn, Args a, const TeamPlan& p, void* words, 
     unsigned* err = device_error_word();
     if (!err || !kernel_info(dev, fn, false)) return cudaErrorInvalidConfiguration;
     TeamShape q{p.tiles, p.stages, p.room, p.size, p.teams,
-                static_cast<unsigned long long*>(words), err};
+                static_cast<ulonglong2*>(words), err};
     void* args[] = {&a, &q};
     return launch_team_args(fn, args, p, words, s);
 }
