@@ -164,6 +164,28 @@ def test_wide_rows(rows, cols, dtype, norm):
     assert credit.device_error() == 0
 
 
+@pytest.mark.parametrize("norm", ["layernorm", "rmsnorm"])
+@pytest.mark.parametrize("rows, cols, dtype", [(250, 300008, "bf16"), (150, 300001, "f32")])
+def test_wide_rows_again_and_again(rows, cols, dtype, norm):
+    # two teams of 54 CTAs or more: 125 and 75 turns, so every stage and every
+    # slot of the exchange is used again and every CTA leads more than one turn
+    q = problem(rows, cols, dtype, norm, True, 0.0, "f32", seed=19)
+    out = forward(norm, q)
+    check_forward(norm, q, out)
+    _, h, mean, rstd = out
+    dy, dh = grads(rows, cols, dtype)
+    back = backward(norm, q, dy, h, mean, rstd, dh)
+    check_backward(norm, q, dy, h, mean, rstd, dh, back)
+    # in place, with rows still to come in flight
+    x, res = q["x"].clone(), q["residual"].clone()
+    again = forward(norm, dict(q, x=x, residual=res), out=x, h_out=res)
+    assert again[0] is x and all(a is b is None or torch.equal(a, b) for a, b in zip(again, out))
+    dy2 = dy.clone()
+    again = backward(norm, q, dy2, h, mean, rstd, dh, dx=dy2)
+    assert again[0] is dy2 and all(a is b is None or torch.equal(a, b) for a, b in zip(again, back))
+    assert credit.device_error() == 0
+
+
 def test_wide_rows_on_two_streams_at_once():
     # both calls want every SM: one runs after the other, neither waits in vain
     qs = [problem(20, 300008 + 8 * i, "bf16", "layernorm", False, 0.0, "f32", seed=80 + i)
