@@ -21,6 +21,7 @@
 //   16384 x 4096 bf16, LayerNorm, dh, dropout    142 us  0.70   (ring)
 //   8192 x 8192 bf16, RMSNorm, dh, bf16 weight    88 us  0.90   (ring)
 //   2048 x 10001 fp32, LayerNorm                  48 us  0.76   (ring, clusters of 5)
+//   4096 x 8192 fp32, LayerNorm                   69 us  0.86   (ring)
 //   1024 x 262144 bf16, LayerNorm                331 us  0.72   (team)
 //   256 x 786432 bf16, RMSNorm, bf16 weight      225 us  0.79   (team)
 //   32 x 1024 fp32, LayerNorm                    5.1 us (two launches)
@@ -725,13 +726,14 @@ cudaError_t run_warp(const NormBwdArgs& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// IO and WIO: the access forms of the ring and warp kernels and of the sweep.
-template <int OP, typename T, typename IO, typename WIO, typename PT>
+// WarpIO, IO and WIO: the access forms of the warp kernels, of the ring and team
+// kernels and of the sweep.
+template <int OP, typename T, typename WarpIO, typename IO, typename WIO, typename PT>
 cudaError_t run_bwd(NormBwdArgs& a, int sms, cudaStream_t s) {
     const int tiles = (a.cols + IO::kTile - 1) / IO::kTile;
-    if (tiles <= 1) return run_warp<OP, T, IO, PT, 1>(a, s);
-    if (tiles <= 2) return run_warp<OP, T, IO, PT, 2>(a, s);
-    if (tiles <= 4) return run_warp<OP, T, IO, PT, 4>(a, s);
+    if (tiles <= 1) return run_warp<OP, T, WarpIO, PT, 1>(a, s);
+    if (tiles <= 2) return run_warp<OP, T, WarpIO, PT, 2>(a, s);
+    if (tiles <= 4) return run_warp<OP, T, WarpIO, PT, 4>(a, s);
     const int streams = a.dh ? 3 : 2;
     TeamPlan team;
     switch (form_of(tiles, sizeof(T), streams, a.rows, a.cols, sms, &team)) {
@@ -753,17 +755,22 @@ cudaError_t run_bwd(NormBwdArgs& a, int sms, cudaStream_t s) {
     return launch_ring(fn.of(p), a, p, a.groups, err, s);
 }
 
-template <int OP, typename T, typename IO, typename WIO>
+template <int OP, typename T, typename WarpIO, typename IO, typename WIO>
 cudaError_t pick_param(NormBwdArgs& a, int sms, cudaStream_t s) {
-    return a.half ? run_bwd<OP, T, IO, WIO, bf16>(a, sms, s)
-                  : run_bwd<OP, T, IO, WIO, float>(a, sms, s);
+    return a.half ? run_bwd<OP, T, WarpIO, IO, WIO, bf16>(a, sms, s)
+                  : run_bwd<OP, T, WarpIO, IO, WIO, float>(a, sms, s);
 }
 
 template <int OP, typename T>
 cudaError_t pick_bwd(TrainKey k, NormBwdArgs& a, int sms, cudaStream_t s) {
     constexpr int N = 16 / (int)sizeof(T);
-    return k.vec ? pick_param<OP, T, VecIO<T, 4>, VecIO<T, N>>(a, sms, s)
-                 : pick_param<OP, T, ElemIO<T, 4>, ElemIO<T, N>>(a, sms, s);
+    // fp32 slices in shared memory are read an element a lane even where the rows
+    // are whole lines: 2048 x 10000 LayerNorm 60 us with four columns a lane, 47
+    // with one; 4096 x 8192 92 and 69, 1024 x 32768 89 and 79, 512 x 262144 335
+    // and 289 (bf16 rows the other way round: 2048 x 10000 39 and 45)
+    using RingIO = std::conditional_t<sizeof(T) == 4, ElemIO<T, 4>, VecIO<T, 4>>;
+    return k.vec ? pick_param<OP, T, VecIO<T, 4>, RingIO, VecIO<T, N>>(a, sms, s)
+                 : pick_param<OP, T, ElemIO<T, 4>, ElemIO<T, 4>, ElemIO<T, N>>(a, sms, s);
 }
 
 
