@@ -222,7 +222,8 @@ __global__ void __launch_bounds__(kRingThreads) fwd_ring(NormFwdArgs a, RingShap
         unsigned char* const stage = ring + s * stage_bytes;
         mbar_wait_bounded(smem_u32(&full[s]), phase, q.err);
         float mean[R], m2;
-        auto take = [&](auto f, auto res, auto on) {
+        // (`keep`: h may be wanted; a constant where it is not)
+        auto take = [&](auto f, auto res, auto on, auto keep) {
             constexpr bool FULL = decltype(f)::value;
 #pragma unroll
             for (int j = 0; j < R; ++j) {
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(kRingThreads) fwd_ring(NormFwdArgs a, RingShap
                     for (int e = 0; e < IO::NP; ++e)
                         t = OP == kLayerNorm ? add2(t, h[j][i][e]) : fma2(h[j][i][e], h[j][i][e], t);
                 }
-                if ((res || on) && ho && (j == 0 || both)) {
+                if (keep && ho && (j == 0 || both)) {
 #pragma unroll
                     for (int i = 0; i < V; ++i)
                         IO::template store<FULL>(ho + j * a.cols, i * IO::kTile, left, h[j][i]);
@@ -270,9 +271,10 @@ __global__ void __launch_bounds__(kRingThreads) fwd_ring(NormFwdArgs a, RingShap
         };
         const std::true_type yes;
         const std::false_type no;
-        if (!whole) take(no, ns > 1, a.drop.on != 0);
-        else if (ns > 1) a.drop.on ? take(yes, yes, yes) : take(yes, yes, no);
-        else a.drop.on ? take(yes, no, yes) : take(yes, no, no);
+        if (!whole) take(no, ns > 1, a.drop.on != 0, yes);
+        else if (ns > 1) a.drop.on ? take(yes, yes, yes, yes) : take(yes, yes, no, yes);
+        else if (a.drop.on) take(yes, no, yes, yes);
+        else ho ? take(yes, no, no, yes) : take(yes, no, no, no);
         {   // the warp's (sum, M2 about its mean) of each row
             const float sum = m2;
             if constexpr (OP == kLayerNorm) m2 = row_sum<R>(v, lane);
@@ -529,7 +531,7 @@ __global__ void __launch_bounds__(kTeamThreads) fwd_team(NormFwdArgs a, TeamShap
             for (int i = 0; i < V; ++i) {
                 F2 h[IO::NP];
                 tile(f, res, on, at, i, h);
-                if ((res || on) && ho) IO::template store<FULL>(ho, i * IO::kTile, left, h);
+                if (ho) IO::template store<FULL>(ho, i * IO::kTile, left, h);
 #pragma unroll
                 for (int e = 0; e < IO::NP; ++e)
                     h[e] = normed<OP>(h[e], m.x, m.y, g[i][e], b[i][e]);

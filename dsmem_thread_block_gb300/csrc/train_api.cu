@@ -173,7 +173,9 @@ credit_status_t credit_norm_forward(credit_op_t op, const void* x, const void* r
     const uint64_t need = (uint64_t)norm_fwd_partials((int)dtype, rows, cols, d->sms);
     if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
         return CREDIT_ERR_INVALID_ARG;
-    a.x = x; a.residual = residual; a.y = y; a.h = h;
+    a.x = x; a.residual = residual; a.y = y;
+    // a copy of x that is x itself is not written
+    a.h = h == x && !residual && !a.drop.on ? nullptr : h;
     a.mean = mean; a.rstd = rstd; a.gamma = gamma; a.beta = beta;
     a.rows = rows; a.cols = (int32_t)cols; a.inv_cols = 1.f / (float)cols; a.eps = eps;
     a.half = (gamma || beta) && param_dtype == CREDIT_BF16;

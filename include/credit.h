@@ -328,8 +328,8 @@ credit_status_t credit_norm_workspace(credit_op_t op, int backward, int64_t rows
  * credit_rmsnorm define it.  The statistics and y come from h before it is
  * rounded to `dtype`.
  *   residual, drop   NULL: none
- *   h                rows x cols out, or NULL (not wanted; without residual
- *                    and dropout h is x)
+ *   h                rows x cols out, or NULL (not wanted); without residual
+ *                    and dropout it is a copy of x
  *   mean, rstd       fp32, one per row, out: the row mean (NULL for RMSNorm)
  *                    and 1 / sqrt(variance or mean square + eps); NULL: not
  *                    wanted

@@ -1,0 +1,38 @@
+"""What the training operators hand back beside y: h where a caller asks for
+it, and gradients formed from what the forward pass returned, in every form
+(a warp, a ring, a team, a sweep a row), aligned and odd."""
+import pytest
+import torch
+
+import dsmem_thread_block_gb300 as credit
+
+import test_gpu_train_ops as T
+
+pytestmark = pytest.mark.gpu
+
+# a warp a row; rings of one CTA (two rows a turn where there are many) and of
+# several; a team; a sweep
+FORMS = [(5, 512), (700, 4096), (9, 5000), (6, 10001), (3, 40000), (5, 300008), (4, 300001),
+         (2, 1300000), (2, 1200001)]
+
+
+def same(got, want):
+    return all(a is b is None or torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("norm", ["layernorm", "rmsnorm"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows, cols", FORMS)
+def test_h_out_without_residual_and_dropout(rows, cols, dtype, norm):
+    # h is x then, and a buffer given for it holds a copy
+    q = T.problem(rows, cols, dtype, norm, False, 0.0, "f32", seed=23)
+    want = T.forward(norm, q)
+    T.check_forward(norm, q, want)
+    for drop in (None, credit.Dropout(0.0, 1)):
+        buf = torch.full_like(q["x"], 7.0)
+        got = T.forward(norm, dict(q, drop=drop), h_out=buf)
+        assert got[1] is buf and same(got, want)
+    x = q["x"].clone()  # x itself as h's buffer
+    got = T.forward(norm, dict(q, x=x), h_out=x)
+    assert got[1] is x and same(got, want)
+    assert credit.device_error() == 0
