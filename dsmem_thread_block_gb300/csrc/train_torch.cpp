@@ -208,8 +208,9 @@ PyObject* py_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor ws = workspace(x, op, 0, tensor(a[9]), &wb, &st);
         if (st != CREDIT_OK) return result(st);
         const at::Tensor y = out.defined() ? out : x.like();
-        // without residual and dropout h is x itself, and is not written
-        const bool same = !residual.defined() && (!drop || drop->p == 0.0);
+        // without residual and dropout h is x itself, and is not written, unless y
+        // takes x's place
+        const bool same = !residual.defined() && (!drop || drop->p == 0.0) && ptr(y) != ptr(x.t);
         const at::Tensor h = h_out.defined() ? h_out : same ? x.t : x.like();
         const at::IntArrayRef per_row = x.t.sizes().slice(0, x.t.dim() - 1);
         const at::Tensor rstd = x.empty(per_row, at::kFloat);

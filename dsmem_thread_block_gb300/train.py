@@ -108,8 +108,9 @@ def layernorm_forward(x, gamma=None, beta=None, eps: float = 1e-5, residual=None
                       dropout: Dropout | None = None, out=None, h_out=None, workspace=None):
     """h = residual + dropout(x), y = LayerNorm(h) over the last dimension;
     returns (y, h, mean, rstd): what layernorm_backward needs, mean and rstd
-    fp32, one per row.  Without residual and dropout h is x itself.  `out` and
-    `h_out` may each be x or residual (in place)."""
+    fp32, one per row.  Without residual and dropout h is x itself, or a copy
+    of it in `h_out` or where `out` is x.  `out` and `h_out` may each be x or
+    residual (in place)."""
     return _norm_forward(C.LAYERNORM, x, gamma, beta, eps, residual, dropout, out, h_out,
                          workspace)
 

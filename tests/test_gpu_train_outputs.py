@@ -36,3 +36,28 @@ def test_h_out_without_residual_and_dropout(rows, cols, dtype, norm):
     got = T.forward(norm, dict(q, x=x), h_out=x)
     assert got[1] is x and same(got, want)
     assert credit.device_error() == 0
+
+
+@pytest.mark.parametrize("norm", ["layernorm", "rmsnorm"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows, cols", FORMS)
+def test_y_in_place_of_x_leaves_h(rows, cols, dtype, norm):
+    # y overwrites x: the h handed back is what x held, and a backward pass on
+    # it is the one on untouched buffers
+    q = T.problem(rows, cols, dtype, norm, False, 0.0, "f32", seed=29)
+    want = T.forward(norm, q)
+    dy, _ = T.grads(rows, cols, dtype)
+    back = T.backward(norm, q, dy, *want[1:], None)
+    for drop, given in ((None, False), (credit.Dropout(0.0, 1), False), (None, True)):
+        x = q["x"].clone()
+        kw = {"h_out": torch.full_like(x, 7.0)} if given else {}
+        got = T.forward(norm, dict(q, x=x, drop=drop), out=x, **kw)
+        assert got[0] is x and got[1] is not x and same(got, want)
+        assert same(T.backward(norm, q, dy, *got[1:], None), back)
+    assert credit.device_error() == 0
+
+
+def test_y_in_place_of_an_empty_x():
+    x = torch.empty(0, 64, device="cuda")
+    y, h, mean, rstd = credit.layernorm_forward(x, out=x)
+    assert y is x and h.shape == (0, 64) and mean.numel() == rstd.numel() == 0
