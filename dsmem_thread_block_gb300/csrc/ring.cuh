@@ -77,6 +77,8 @@ __device__ __forceinline__ void ring_issue(const void* const (&src)[NS], int ns,
                 *reinterpret_cast<T*>(d + (c - l.first)) = *reinterpret_cast<const T*>(c);
             for (const char* c = l.hi > l.begin ? l.hi : l.begin; c < l.end; c += sizeof(T))
                 *reinterpret_cast<T*>(d + (c - l.first)) = *reinterpret_cast<const T*>(c);
+            // a later turn's bulk copy overwrites these bytes: order it behind them
+            fence_proxy_async_smem();
         }
         const uint32_t tx = __reduce_add_sync(0xffffffffu, mine ? l.bulk() : 0u);
         __syncwarp();

@@ -61,3 +61,25 @@ def test_y_in_place_of_an_empty_x():
     x = torch.empty(0, 64, device="cuda")
     y, h, mean, rstd = credit.layernorm_forward(x, out=x)
     assert y is x and h.shape == (0, 64) and mean.numel() == rstd.numel() == 0
+
+
+@pytest.mark.parametrize("rows, cols, dtype", [(16000, 1024, "bf16"), (2500, 4096, "f32"),
+                                               (420, 20000, "bf16"), (180, 70001, "f32"),
+                                               (70, 300008, "bf16")])
+def test_stages_filled_again_after_a_cut_line(rows, cols, dtype):
+    # matrices that start inside a 16-byte line: the first row's stage holds
+    # elements that were copied one by one, and whole lines of later rows after
+    # that; every output repeats and is the definition's
+    for norm in ("layernorm", "rmsnorm"):
+        q = T.problem(rows, cols, dtype, norm, True, 0.0, "f32", seed=37)
+        for n in (1, 3):
+            q2 = dict(q, x=T.offset_by(q["x"], n), residual=T.offset_by(q["residual"], n + 1))
+            out = T.forward(norm, q2)
+            T.check_forward(norm, q2, out)
+            assert same(T.forward(norm, q2), out)
+            dy, dh = T.grads(rows, cols, dtype)
+            dy, dh, h = T.offset_by(dy, n), T.offset_by(dh, n + 1), T.offset_by(out[1], n)
+            back = T.backward(norm, q2, dy, h, *out[2:], dh)
+            T.check_backward(norm, q2, dy, h, *out[2:], dh, back)
+            assert same(T.backward(norm, q2, dy, h, *out[2:], dh), back)
+    assert credit.device_error() == 0
