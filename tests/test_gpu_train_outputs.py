@@ -83,3 +83,55 @@ def test_stages_filled_again_after_a_cut_line(rows, cols, dtype):
             T.check_backward(norm, q2, dy, h, *out[2:], dh, back)
             assert same(T.backward(norm, q2, dy, h, *out[2:], dh), back)
     assert credit.device_error() == 0
+
+
+@pytest.mark.parametrize("norm", ["layernorm", "rmsnorm"])
+@pytest.mark.parametrize("rows, cols, dtype", [(37, 1300000, "bf16"), (45, 900000, "bf16"),
+                                               (43, 900001, "bf16"), (23, 1300000, "f32"),
+                                               (21, 1000003, "f32")])
+def test_sweep_of_several_batches(rows, cols, dtype, norm):
+    # rows beyond the teams', in several batches with an uneven last one: a
+    # launch sums one batch while it writes the one before, and the parameters'
+    # sums go on from batch to batch
+    for residual, p in ((True, 0.1), (False, 0.0)):
+        q = T.problem(rows, cols, dtype, norm, residual, p, "f32", seed=43)
+        out = T.forward(norm, q)
+        T.check_forward(norm, q, out)
+        dy, dh = T.grads(rows, cols, dtype)
+        dh = dh if residual else None
+        back = T.backward(norm, q, dy, *out[1:], dh, need_dresidual=residual)
+        T.check_backward(norm, q, dy, *out[1:], dh, back)
+        # in place: a batch is written while the next one's rows are summed
+        x = q["x"].clone()
+        res = q["residual"].clone() if residual else None
+        got = T.forward(norm, dict(q, x=x, residual=res), out=x, h_out=res)
+        assert got[0] is x and same(got, out)
+        dy2, h2 = dy.clone(), out[1].clone()
+        got = T.backward(norm, q, dy2, h2, *out[2:], dh, need_dresidual=residual, dx=dy2,
+                         dresidual=h2 if p else None)
+        assert got[0] is dy2 and same(got, back)
+    assert credit.device_error() == 0
+
+
+def test_sweep_of_several_batches_captured():
+    rows, cols = 21, 1300000
+    q = T.problem(rows, cols, "bf16", "layernorm", True, 0.1, "f32", seed=47)
+    dy, dh = T.grads(rows, cols, "bf16")
+
+    def step():
+        f = T.forward("layernorm", q)
+        return (*f, *T.backward("layernorm", q, dy, *f[1:], dh, need_dresidual=True))
+
+    want = step()
+    T.check_forward("layernorm", q, want[:4])
+    T.check_backward("layernorm", q, dy, *want[1:4], dh, want[4:])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step()
+    for _ in range(3):
+        for t in out:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert same(out, want)
+    assert credit.device_error() == 0
