@@ -4,7 +4,8 @@ with residual add, dropout and saved statistics, and its gradient.
 The functions here carry the arguments' meaning; a small extension
 (csrc/train_torch.cpp) checks the tensors, allocates outputs and workspace from
 torch's allocator, and calls the C ABI on the input's device and its current
-stream.  A missing extension raises, as a missing library does.
+stream.  The extension is loaded by the first call; a missing one raises there,
+as a missing library does.
 """
 from __future__ import annotations
 
@@ -14,14 +15,13 @@ import importlib.machinery
 import importlib.util
 import os
 
-import torch
-
 from . import _credit as C
 from . import build as _build
 from ._credit import CreditError
 
 
 def _load():
+    import torch  # noqa: F401  (the extension's libraries)
     path = _build.TORCH_LIB
     if not os.path.exists(path):
         raise RuntimeError(f"the training operators' torch layer is not built ({path}); run "
@@ -33,15 +33,17 @@ def _load():
     return module
 
 
-_ext = _load()
-_bound = None  # the library whose functions the extension calls
+_ext = None    # the extension
+_bound = None  # the library whose functions it calls
 
 
 def _bind():
     """Hand the extension the current library's functions (the regular build's,
     or the checked build's inside `use_checked_build`)."""
-    global _bound
+    global _ext, _bound
     lib = C.load()
+    if _ext is None:
+        _ext = _load()
     _ext.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
                 for f in ("credit_dropout", "credit_norm_workspace", "credit_norm_forward",
                           "credit_norm_backward")))
@@ -67,8 +69,10 @@ class Dropout:
         if not (0 <= self.seed < 1 << 64 and 0 <= self.offset < 1 << 64):
             raise ValueError("credit: dropout seed and offset are unsigned 64-bit integers")
         d = self.device_offset
-        if d is not None and (d.dtype != torch.int64 or d.numel() != 1 or not d.is_cuda):
-            raise ValueError("credit: device_offset must be an int64 CUDA tensor of one element")
+        if d is not None:
+            import torch
+            if d.dtype != torch.int64 or d.numel() != 1 or not d.is_cuda:
+                raise ValueError("credit: device_offset must be an int64 CUDA tensor of one element")
         fields = C.dropout_fields(self.p, self.seed, self.offset,
                                   d.data_ptr() if d is not None else 0)
         object.__setattr__(self, "_fields", fields)
