@@ -78,6 +78,10 @@ class Dropout:
         object.__setattr__(self, "_fields", fields)
         object.__setattr__(self, "_address", ctypes.addressof(fields))
 
+    def __reduce__(self):
+        # a copy has a C struct of its own
+        return type(self), (self.p, self.seed, self.offset, self.device_offset)
+
 
 def _drop(d, x):
     if d is None:

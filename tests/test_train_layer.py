@@ -1,6 +1,9 @@
 """The training operators' Python layer without a GPU: importing the package,
 `Dropout` objects, the build of the torch layer, and refusals on the host."""
+import copy
+import dataclasses
 import os
+import pickle
 import subprocess
 import sys
 
@@ -49,3 +52,32 @@ except RuntimeError as e:
     print("refused:", e)
 """)
     assert r.returncode == 0 and "torch layer is not built" in r.stdout, r.stderr
+
+
+class Word:
+    """Stands for a one-element int64 CUDA tensor."""
+    dtype, is_cuda, device = torch.int64, True, "cuda:0"
+
+    def __init__(self, address):
+        self.address = address
+
+    def numel(self):
+        return 1
+
+    def data_ptr(self):
+        return self.address
+
+
+@pytest.mark.parametrize("again", [copy.copy, copy.deepcopy, dataclasses.replace,
+                                   lambda d: pickle.loads(pickle.dumps(d))])
+def test_dropout_objects_are_copied_and_pickled(again):
+    for word in (None, Word(4096)):
+        d = credit.Dropout(0.25, (1 << 63) + 5, (1 << 40) + 3, word)
+        e = again(d)
+        assert (e.p, e.seed, e.offset) == (d.p, d.seed, d.offset)
+        # the C struct is the copy's own and says the same
+        assert e._fields is not d._fields and e._address != d._address
+        assert (e._fields.p, e._fields.seed, e._fields.offset, e._fields.device_offset) == \
+            (0.25, (1 << 63) + 5, (1 << 40) + 3, 4096 if word else None)
+        if word is None:
+            assert e == d and hash(e) == hash(d)
