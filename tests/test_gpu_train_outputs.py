@@ -135,3 +135,53 @@ def test_sweep_of_several_batches_captured():
         torch.cuda.synchronize()
         assert same(out, want)
     assert credit.device_error() == 0
+
+
+@pytest.mark.parametrize("cols", [256, 1001, 4096, 40000, 300008])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_infinity_in_a_kept_element(cols, dtype):
+    q = T.problem(5, cols, dtype, "layernorm", True, 0.5, "f32", seed=53)
+    j = int(q["mask"][2].nonzero()[-1])  # the row's last kept column
+    x = q["x"].clone()
+    x[2, j] = float("inf")
+    rows = [0, 1, 3, 4]
+    clean = T.forward("layernorm", q)
+    y, h, mean, rstd = T.forward("layernorm", dict(q, x=x))
+    # h - mean is -inf, and NaN at the infinity: so is the variance
+    assert bool(y[2].isnan().all()) and bool(rstd[2].isnan()) and float(mean[2]) == float("inf")
+    assert float(h[2, j]) == float("inf") and bool(h[2].isinf().sum() == 1)
+    assert all(torch.equal(a[rows], b[rows]) for a, b in zip((y, h, mean, rstd), clean))
+    # the mean square is infinite, 1 / sqrt of it zero
+    clean = T.forward("rmsnorm", q)
+    y, h, _, rstd = T.forward("rmsnorm", dict(q, x=x))
+    assert float(rstd[2]) == 0.0 and bool(y[2, j].isnan()) and int((y[2] != 0).sum()) == 1
+    assert all(torch.equal(a[rows], b[rows]) for a, b in zip((y, h, rstd), (clean[0], clean[1],
+                                                                           clean[3])))
+
+
+@pytest.mark.parametrize("cols", [256, 512, 4096, 8192])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_zero_variance_without_eps(cols, dtype):
+    # widths whose reciprocal is exact, so that the mean is: 0 / 0 in the
+    # definition, NaN, and the statistics as they are (1 / sqrt within 2 units
+    # in the last place, 4 u)
+    x = torch.full((3, cols), 2.0, device="cuda", dtype=T.R.DT[dtype])
+    y, h, mean, rstd = credit.layernorm_forward(x, eps=0.0)
+    assert bool(y.isnan().all()) and bool((mean == 2.0).all()) and bool(rstd.isposinf().all())
+    y, _, rstd = credit.rmsnorm_forward(x, eps=0.0)
+    assert bool(((rstd - 0.5).abs() <= 4 * T.R.U * 0.5).all())
+    assert bool(((y.double() - 1.0).abs() <= 6 * T.R.U + T.R.U_OUT[x.dtype]).all())
+    y, _, rstd = credit.rmsnorm_forward(torch.zeros_like(x), eps=0.0)
+    assert bool(y.isnan().all()) and bool(rstd.isposinf().all())
+
+
+def test_dropout_overflow_and_signed_zero():
+    big = torch.finfo(torch.float32).max
+    for cols in (64, 1001):
+        x = torch.full((2, cols), big, device="cuda")
+        x[1] = -0.0
+        drop = credit.Dropout(0.5, 9, 4)
+        keep = T.R.keep_mask(2, cols, 0.5, 9, 4).cuda()
+        y = credit.dropout(x, drop)
+        assert bool(y[0][keep[0]].isposinf().all()) and bool((y[0][~keep[0]] == 0).all())
+        assert torch.equal(y[1].signbit(), keep[1]) and bool((y[1] == 0).all())
