@@ -50,6 +50,16 @@ def _bind():
     _bound = lib
 
 
+def _word(d):
+    """The address of a device_offset tensor (0: none)."""
+    if d is None:
+        return 0
+    import torch
+    if d.dtype != torch.int64 or d.numel() != 1 or not d.is_cuda:
+        raise ValueError("credit: device_offset must be an int64 CUDA tensor of one element")
+    return d.data_ptr()
+
+
 @dataclasses.dataclass(frozen=True)
 class Dropout:
     """A dropout stream: drop probability 0 <= p < 1, a 64-bit seed and a
@@ -68,13 +78,7 @@ class Dropout:
             raise ValueError("credit: dropout needs 0 <= p < 1")
         if not (0 <= self.seed < 1 << 64 and 0 <= self.offset < 1 << 64):
             raise ValueError("credit: dropout seed and offset are unsigned 64-bit integers")
-        d = self.device_offset
-        if d is not None:
-            import torch
-            if d.dtype != torch.int64 or d.numel() != 1 or not d.is_cuda:
-                raise ValueError("credit: device_offset must be an int64 CUDA tensor of one element")
-        fields = C.dropout_fields(self.p, self.seed, self.offset,
-                                  d.data_ptr() if d is not None else 0)
+        fields = C.dropout_fields(self.p, self.seed, self.offset, _word(self.device_offset))
         object.__setattr__(self, "_fields", fields)
         object.__setattr__(self, "_address", ctypes.addressof(fields))
 
@@ -86,8 +90,11 @@ class Dropout:
 def _drop(d, x):
     if d is None:
         return None
-    if d.device_offset is not None and d.device_offset.device != x.device:
-        raise ValueError("credit: device_offset must be on the input's device")
+    if d.device_offset is not None:
+        if d.device_offset.device != x.device:
+            raise ValueError("credit: device_offset must be on the input's device")
+        # the tensor may have been given other storage since the last call
+        d._fields.device_offset = _word(d.device_offset)
     return d._address
 
 

@@ -185,3 +185,12 @@ def test_dropout_overflow_and_signed_zero():
         y = credit.dropout(x, drop)
         assert bool(y[0][keep[0]].isposinf().all()) and bool((y[0][~keep[0]] == 0).all())
         assert torch.equal(y[1].signbit(), keep[1]) and bool((y[1] == 0).all())
+
+
+def test_device_word_with_new_storage():
+    x = T.make((4, 4096), torch.float32, 5)
+    word = torch.zeros(1, dtype=torch.int64, device="cuda")
+    drop = credit.Dropout(0.5, 21, 3, word)
+    assert torch.equal(credit.dropout(x, drop), credit.dropout(x, credit.Dropout(0.5, 21, 3)))
+    word.data = torch.full((1,), 6, dtype=torch.int64, device="cuda")
+    assert torch.equal(credit.dropout(x, drop), credit.dropout(x, credit.Dropout(0.5, 21, 9)))

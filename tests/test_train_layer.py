@@ -81,3 +81,14 @@ def test_dropout_objects_are_copied_and_pickled(again):
             (0.25, (1 << 63) + 5, (1 << 40) + 3, 4096 if word else None)
         if word is None:
             assert e == d and hash(e) == hash(d)
+
+
+def test_the_device_word_is_found_at_every_call():
+    # the tensor may be given other storage between two calls (`t.data = u`)
+    word = Word(4096)
+    d = credit.Dropout(0.25, 1, 2, word)
+    word.address = 8192
+    assert train._drop(d, word) == d._address and d._fields.device_offset == 8192
+    word.dtype = torch.int32
+    with pytest.raises(ValueError):
+        train._drop(d, word)
