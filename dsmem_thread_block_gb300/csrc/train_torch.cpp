@@ -223,18 +223,18 @@ PyObject* py_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // norm_backward(op, dy, h, mean, rstd, gamma, dh, drop address, need dresidual, dx, dresidual,
-//               workspace)
+//               workspace, beta)
 PyObject* py_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded(n, 12, [&]() -> PyObject* {
+    return guarded(n, 13, [&]() -> PyObject* {
         const credit_op_t op = (credit_op_t)PyLong_AsLong(a[0]);
         const Input dy(a[1]);
         const at::Tensor &h = tensor(a[2]), &gamma = tensor(a[5]), &dh = tensor(a[6]);
-        const at::Tensor &dx_given = tensor(a[9]), &dr_given = tensor(a[10]);
+        const at::Tensor &dx_given = tensor(a[9]), &dr_given = tensor(a[10]), &beta = tensor(a[12]);
         if (!h.defined()) bad("credit: h is required");
         const void *hp = dy.matrix(h), *dhp = dy.matrix(dh);
         const float* mp = op == CREDIT_LAYERNORM ? dy.per_row(tensor(a[3])) : nullptr;
         const float* sp = dy.per_row(tensor(a[4]));
-        const credit_dtype_t pcode = params(dy, gamma, at::Tensor());
+        const credit_dtype_t pcode = params(dy, gamma, beta);
         const credit_dropout_t* drop = drop_of(a[7]);
         const int want = PyObject_IsTrue(a[8]);
         if (want < 0 || PyErr_Occurred()) return nullptr;
@@ -249,10 +249,11 @@ PyObject* py_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         at::Tensor dr = dr_given;
         if (!dr.defined() && want && drop && drop->p > 0.0) dr = dy.like();
         at::Tensor dgamma, dbeta;
-        if (gamma.defined()) {
-            dgamma = dy.empty(gamma.sizes(), gamma.scalar_type());
-            if (op == CREDIT_LAYERNORM) dbeta = dy.empty(gamma.sizes(), gamma.scalar_type());
-        }
+        if (gamma.defined()) dgamma = dy.empty(gamma.sizes(), gamma.scalar_type());
+        // beta's gradient is shaped like beta, or like gamma where only that is given
+        const at::Tensor& like_beta = beta.defined() ? beta : gamma;
+        if (op == CREDIT_LAYERNORM && like_beta.defined())
+            dbeta = dy.empty(like_beta.sizes(), like_beta.scalar_type());
         st = g_backward(op, ptr(dy.t), dhp, hp, mp, sp, ptr(gamma), pcode, drop, ptr(dx), ptr(dr),
                         ptr(dgamma), ptr(dbeta), dy.rows, dy.cols, dy.code, ptr(ws), wb, stream(dy));
         // without dropout the two gradients are one

@@ -139,25 +139,28 @@ def rmsnorm_forward(x, weight=None, eps: float = 1e-6, residual=None,
 
 
 def _norm_backward(op, dy, h, mean, rstd, gamma, dh, drop, need_dresidual, dx, dresidual,
-                   workspace):
+                   workspace, beta=None):
     if C._lib is not _bound or _bound is None:
         _bind()
     r = _ext.norm_backward(op, dy, h, mean, rstd, gamma, dh, _drop(drop, dy), need_dresidual, dx,
-                           dresidual, workspace)
+                           dresidual, workspace, beta)
     if type(r) is int:
         raise CreditError(r, "credit_norm_backward")
     return r
 
 
 def layernorm_backward(dy, h, mean, rstd, gamma=None, dh=None, dropout: Dropout | None = None,
-                       need_dresidual: bool = False, dx=None, dresidual=None, workspace=None):
+                       need_dresidual: bool = False, dx=None, dresidual=None, workspace=None,
+                       beta=None):
     """The gradient of layernorm_forward: from dy (of y) and dh (the gradient
     that reaches h past the norm, or None), returns (dx, dresidual, dgamma,
     dbeta).  dresidual is None unless asked for, and dx itself where there is
-    no dropout; dgamma and dbeta are None without gamma.  `dx` and `dresidual`
-    may each be dy, dh or h (in place)."""
+    no dropout.  dgamma is None without gamma; dbeta is None without gamma
+    and without `beta`, of which only the shape and type count (those of
+    gamma where it is not given).  `dx` and `dresidual` may each be dy, dh or h
+    (in place)."""
     return _norm_backward(C.LAYERNORM, dy, h, mean, rstd, gamma, dh, dropout, need_dresidual, dx,
-                          dresidual, workspace)
+                          dresidual, workspace, beta)
 
 
 def rmsnorm_backward(dy, h, rstd, weight=None, dh=None, dropout: Dropout | None = None,

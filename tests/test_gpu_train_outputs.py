@@ -194,3 +194,32 @@ def test_device_word_with_new_storage():
     assert torch.equal(credit.dropout(x, drop), credit.dropout(x, credit.Dropout(0.5, 21, 3)))
     word.data = torch.full((1,), 6, dtype=torch.int64, device="cuda")
     assert torch.equal(credit.dropout(x, drop), credit.dropout(x, credit.Dropout(0.5, 21, 9)))
+
+
+@pytest.mark.parametrize("rows, cols, dtype, pdtype", [
+    (40, 512, "bf16", "bf16"), (9, 5000, "f32", "f32"), (64, 8192, "bf16", "f32"),
+    (5, 300008, "bf16", "bf16"), (9, 1300000, "bf16", "f32")])
+def test_gradient_of_beta_without_gamma(rows, cols, dtype, pdtype):
+    # the forward pass takes beta alone, so the backward pass gives its gradient
+    q = T.problem(rows, cols, dtype, "layernorm", False, 0.0, pdtype, seed=59)
+    beta, q["gamma"] = q["beta"].view(1, cols), None
+    out = T.forward("layernorm", dict(q, beta=beta))
+    T.check_forward("layernorm", q, out)
+    dy, _ = T.grads(rows, cols, dtype)
+    back = T.backward("layernorm", q, dy, *out[1:], None, beta=beta)
+    assert back[2] is None and back[3].shape == beta.shape and back[3].dtype == beta.dtype
+    _, rx, _, rb, _, ex, _, eb = T.R.ref_backward("layernorm", dy, None, *out[1:], None, 0.0, None)
+    T.R.assert_close(back[0], rx, T.R.U_OUT[dy.dtype] * rx.abs() + T.R.U * ex, "dx")
+    T.R.assert_close(back[3].view(-1), rb, T.R.U_OUT[beta.dtype] * rb.abs() + T.R.U * eb, "dbeta")
+    # beside gamma the same call takes beta's shape, and without either gives none
+    gamma = torch.ones_like(beta).view(-1)
+    both = credit.layernorm_backward(dy, *out[1:], gamma, beta=beta)
+    assert both[2].shape == gamma.shape and both[3].shape == beta.shape
+    assert torch.equal(both[3], back[3]) and torch.equal(both[0], back[0])
+    assert T.backward("layernorm", q, dy, *out[1:], None)[2:] == (None, None)
+    with pytest.raises(ValueError):
+        credit.layernorm_backward(dy, *out[1:], beta=beta[:, :-1].contiguous())
+    with pytest.raises(ValueError):
+        credit.layernorm_backward(dy, *out[1:], gamma, beta=beta.to(
+            torch.float32 if pdtype == "bf16" else torch.bfloat16))
+    assert credit.device_error() == 0
