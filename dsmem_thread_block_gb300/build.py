@@ -89,12 +89,16 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     return lib
 
 
-def _torch_root() -> str:
-    """The directory of the installed torch, without importing it."""
+def _torch_root() -> str | None:
+    """The directory of the installed torch (None: there is none), without
+    importing it."""
     import importlib.util
-    spec = importlib.util.find_spec("torch")
+    try:
+        spec = importlib.util.find_spec("torch")
+    except ValueError:  # (a module that stands in sys.modules without a spec)
+        spec = None
     if spec is None or not spec.submodule_search_locations:
-        raise RuntimeError("torch not found: its headers are required to build the torch layer")
+        return None
     return spec.submodule_search_locations[0]
 
 
@@ -109,6 +113,8 @@ def build_torch(force: bool = False) -> str:
         return TORCH_LIB
     os.makedirs(BUILD, exist_ok=True)
     root = _torch_root()
+    if root is None:
+        raise RuntimeError("torch not found: its headers are required to build the torch layer")
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
     tmp = TORCH_LIB + f".{os.getpid()}.tmp"
     r = subprocess.run(
@@ -124,13 +130,17 @@ def build_torch(force: bool = False) -> str:
 
 
 def build_all(force: bool = False) -> tuple[str, str]:
-    """Both libraries and the torch layer, compiled side by side: (regular,
-    checked)."""
+    """Both libraries and, where torch is installed, the torch layer, compiled
+    side by side: (regular, checked).  The libraries need no torch; a torch
+    layer that does not compile raises after both are there."""
     with cf.ThreadPoolExecutor(max_workers=3) as ex:
         reg = ex.submit(build, force)
         chk = ex.submit(build, force, False, None, True)
-        ex.submit(build_torch, force).result()
-        return reg.result(), chk.result()
+        layer = ex.submit(build_torch, force) if _torch_root() else None
+        libs = reg.result(), chk.result()
+        if layer:
+            layer.result()
+        return libs
 
 
 if __name__ == "__main__":

@@ -92,3 +92,31 @@ def test_the_device_word_is_found_at_every_call():
     word.dtype = torch.int32
     with pytest.raises(ValueError):
         train._drop(d, word)
+
+
+@pytest.fixture
+def built(monkeypatch):
+    """What build_all builds, recorded instead of compiled."""
+    calls = []
+    monkeypatch.setattr(B, "build", lambda force=False, verbose=False, extra=None, checked=False:
+                        calls.append("checked" if checked else "regular") or calls[-1])
+    monkeypatch.setattr(B, "build_torch", lambda force=False: calls.append("torch"))
+    return calls
+
+
+def test_the_libraries_build_without_torch(built, monkeypatch):
+    assert B.build_all() == ("regular", "checked") and sorted(built) == ["checked", "regular",
+                                                                        "torch"]
+    built.clear()
+    monkeypatch.setitem(sys.modules, "torch", None)  # not installed
+    assert B.build_all() == ("regular", "checked") and sorted(built) == ["checked", "regular"]
+
+
+def test_a_torch_layer_that_does_not_compile_raises(built, monkeypatch):
+    def fails(force=False):
+        raise RuntimeError("g++ failed")
+
+    monkeypatch.setattr(B, "build_torch", fails)
+    with pytest.raises(RuntimeError, match="g\\+\\+ failed"):
+        B.build_all()
+    assert sorted(built) == ["checked", "regular"]
