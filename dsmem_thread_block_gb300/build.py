@@ -102,19 +102,30 @@ def _torch_root() -> str | None:
     return spec.submodule_search_locations[0]
 
 
+def _torch_stamp(root: str) -> str:
+    """What the torch layer is compiled against: the interpreter and the torch."""
+    with open(os.path.join(root, "version.py")) as f:
+        return f"{sys.version}\n{root}\n{f.read()}"
+
+
 def build_torch(force: bool = False) -> str:
     """Compile and link the training operators' torch layer
-    (csrc/train_torch.cpp) against the installed torch, if out of date."""
+    (csrc/train_torch.cpp) against the installed torch, if out of date: its
+    sources, or the torch it was compiled against."""
     import sysconfig
     src = os.path.join(CSRC, "train_torch.cpp")
     deps = [src, os.path.join(INCLUDE, "credit.h"), __file__]
-    if not force and os.path.exists(TORCH_LIB) and \
-            os.path.getmtime(TORCH_LIB) >= max(os.path.getmtime(p) for p in deps):
-        return TORCH_LIB
-    os.makedirs(BUILD, exist_ok=True)
     root = _torch_root()
     if root is None:
         raise RuntimeError("torch not found: its headers are required to build the torch layer")
+    stamp, stamp_file, old = _torch_stamp(root), TORCH_LIB + ".stamp", None
+    if os.path.exists(stamp_file):
+        with open(stamp_file) as f:
+            old = f.read()
+    if not force and old == stamp and os.path.exists(TORCH_LIB) and \
+            os.path.getmtime(TORCH_LIB) >= max(os.path.getmtime(p) for p in deps):
+        return TORCH_LIB
+    os.makedirs(BUILD, exist_ok=True)
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
     tmp = TORCH_LIB + f".{os.getpid()}.tmp"
     r = subprocess.run(
@@ -125,7 +136,11 @@ def build_torch(force: bool = False) -> str:
          "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
+    if os.path.exists(stamp_file):
+        os.remove(stamp_file)  # none stands beside a library it does not describe
     os.replace(tmp, TORCH_LIB)
+    with open(stamp_file, "w") as f:
+        f.write(stamp)
     return TORCH_LIB
 
 

@@ -120,3 +120,33 @@ def test_a_torch_layer_that_does_not_compile_raises(built, monkeypatch):
     with pytest.raises(RuntimeError, match="g\\+\\+ failed"):
         B.build_all()
     assert sorted(built) == ["checked", "regular"]
+
+
+def test_the_torch_layer_follows_the_installed_torch(tmp_path, monkeypatch):
+    import types
+    runs, version = [], tmp_path / "torch" / "version.py"
+    version.parent.mkdir()
+    version.write_text("1.0")
+
+    def run(cmd, **kw):
+        runs.append(cmd)
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write(version.read_text())
+        return types.SimpleNamespace(returncode=0, stdout="", stderr="")
+
+    monkeypatch.setattr(B, "BUILD", str(tmp_path))
+    monkeypatch.setattr(B, "TORCH_LIB", str(tmp_path / "credit_train_torch.so"))
+    monkeypatch.setattr(B, "_torch_root", lambda: str(version.parent))
+    monkeypatch.setattr(B.subprocess, "run", run)
+    B.build_torch()
+    B.build_torch()
+    assert len(runs) == 1  # up to date
+    version.write_text("2.0")
+    B.build_torch()
+    B.build_torch()
+    assert len(runs) == 2
+    with open(B.TORCH_LIB) as f:
+        assert f.read() == "2.0"
+    os.remove(B.TORCH_LIB)
+    B.build_torch()
+    assert len(runs) == 3
