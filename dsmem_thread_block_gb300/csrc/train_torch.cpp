@@ -10,12 +10,14 @@
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
+#include <initializer_list>
 #include <stdexcept>
 
 #include "credit.h"
@@ -46,6 +48,18 @@ const at::Tensor& tensor(PyObject* o) {
     if (o == Py_None) return none;
     if (!THPVariable_Check(o)) throw Refused{PyExc_TypeError, "credit: a tensor was expected"};
     return THPVariable_Unpack(o);
+}
+
+// The calls record no graph: under grad mode a tensor that requires a gradient
+// would lose it without a word.
+void no_graph(PyObject* const* a, std::initializer_list<int> tensors) {
+    if (!c10::GradMode::is_enabled()) return;
+    for (const int i : tensors)
+        if (THPVariable_Check(a[i]) && THPVariable_Unpack(a[i]).requires_grad())
+            throw Refused{PyExc_RuntimeError,
+                          "credit: the training operators record no autograd graph, and a tensor "
+                          "that requires a gradient was given: call the forward and backward pair "
+                          "under torch.no_grad(), or inside a torch.autograd.Function"};
 }
 
 void* ptr(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
@@ -177,6 +191,7 @@ template <typename F> PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
 // dropout(x, drop address, residual, out)
 PyObject* py_dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 4, [&]() -> PyObject* {
+        no_graph(a, {0, 2, 3});
         const Input x(a[0]);
         const at::Tensor &residual = tensor(a[2]), &given = tensor(a[3]);
         const void* rp = x.matrix(residual);
@@ -191,6 +206,7 @@ PyObject* py_dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // norm_forward(op, x, gamma, beta, eps, residual, drop address, out, h out, workspace)
 PyObject* py_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 10, [&]() -> PyObject* {
+        no_graph(a, {1, 2, 3, 5, 7, 8});
         const credit_op_t op = (credit_op_t)PyLong_AsLong(a[0]);
         const Input x(a[1]);
         const at::Tensor &gamma = tensor(a[2]), &beta = tensor(a[3]), &residual = tensor(a[5]);
@@ -226,6 +242,7 @@ PyObject* py_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 //               workspace, beta)
 PyObject* py_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 13, [&]() -> PyObject* {
+        no_graph(a, {1, 2, 3, 4, 5, 6, 9, 10, 12});
         const credit_op_t op = (credit_op_t)PyLong_AsLong(a[0]);
         const Input dy(a[1]);
         const at::Tensor &h = tensor(a[2]), &gamma = tensor(a[5]), &dh = tensor(a[6]);

@@ -6,6 +6,10 @@ The functions here carry the arguments' meaning; a small extension
 torch's allocator, and calls the C ABI on the input's device and its current
 stream.  The extension is loaded by the first call; a missing one raises there,
 as a missing library does.
+
+The calls record no autograd graph: they are the two halves of a
+torch.autograd.Function, or of a step written out by hand.  Under grad mode they
+refuse tensors that require a gradient, whose gradient would be lost.
 """
 from __future__ import annotations
 

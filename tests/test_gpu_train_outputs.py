@@ -223,3 +223,31 @@ def test_gradient_of_beta_without_gamma(rows, cols, dtype, pdtype):
         credit.layernorm_backward(dy, *out[1:], gamma, beta=beta.to(
             torch.float32 if pdtype == "bf16" else torch.bfloat16))
     assert credit.device_error() == 0
+
+
+class LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, gamma, beta):
+        y, h, mean, rstd = credit.layernorm_forward(x, gamma, beta)
+        ctx.save_for_backward(h, mean, rstd, gamma)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        dx, _, dgamma, dbeta = credit.layernorm_backward(dy.contiguous(), *ctx.saved_tensors)
+        return dx, dgamma, dbeta
+
+
+def test_the_pair_inside_an_autograd_function():
+    q = T.problem(33, 1500, "f32", "layernorm", False, 0.0, "f32", seed=61)
+    leaves = [q[k].clone().requires_grad_() for k in ("x", "gamma", "beta")]
+    with pytest.raises(RuntimeError, match="record no autograd graph"):
+        credit.layernorm_forward(*leaves)
+    y = LayerNorm.apply(*leaves)
+    dy, _ = T.grads(33, 1500, "f32")
+    y.backward(dy)
+    with torch.no_grad():
+        out = credit.layernorm_forward(*leaves)  # a step written out by hand
+        assert torch.equal(y, out[0])
+        T.check_backward("layernorm", q, dy, *out[1:], None,
+                         (leaves[0].grad, None, leaves[1].grad, leaves[2].grad))

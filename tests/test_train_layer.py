@@ -150,3 +150,35 @@ def test_the_torch_layer_follows_the_installed_torch(tmp_path, monkeypatch):
     os.remove(B.TORCH_LIB)
     B.build_torch()
     assert len(runs) == 3
+
+
+def test_tensors_that_require_a_gradient_are_refused_under_grad_mode():
+    # every tensor argument of every call; the refusal comes before any look at
+    # the tensors themselves, which is all that a machine without a GPU can see
+    x, v = torch.zeros(4, 8), torch.zeros(8)
+    m = torch.zeros(4)
+    calls = [(lambda x, r, o: credit.dropout(x, None, residual=r, out=o), (x, x, x)),
+             (lambda x, g, b, r, o, h: credit.layernorm_forward(x, g, b, residual=r, out=o, h_out=h),
+              (x, v, v, x, x, x)),
+             (lambda x, w, r: credit.rmsnorm_forward(x, w, residual=r), (x, v, x)),
+             (lambda dy, h, mu, s, g, dh, dx, dr, b: credit.layernorm_backward(
+                 dy, h, mu, s, g, dh=dh, dx=dx, dresidual=dr, beta=b), (x, x, m, m, v, x, x, x, v)),
+             (lambda dy, h, s, w, dh: credit.rmsnorm_backward(dy, h, s, w, dh=dh), (x, x, m, v, x))]
+    for call, args in calls:
+        for i in range(len(args)):
+            bad = [a.clone() for a in args]
+            bad[i].requires_grad_()
+            with pytest.raises(RuntimeError, match="record no autograd graph"):
+                call(*bad)
+            with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+                call(*bad)
+        with pytest.raises(ValueError, match="CUDA"):
+            call(*args)
+
+    class Norm(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            return credit.rmsnorm_forward(x)[0]
+
+    with pytest.raises(ValueError, match="CUDA"):  # not refused for its gradient
+        Norm.apply(x.clone().requires_grad_())
