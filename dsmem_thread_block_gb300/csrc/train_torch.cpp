@@ -62,6 +62,12 @@ void no_graph(PyObject* const* a, std::initializer_list<int> tensors) {
                           "under torch.no_grad(), or inside a torch.autograd.Function"};
 }
 
+// A caller's output has been written: autograd refuses to use what it saved of it.
+void written(std::initializer_list<const at::Tensor*> outs) {
+    for (const at::Tensor* t : outs)
+        if (t->defined() && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 void* ptr(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 
 // The first matrix of a call.
@@ -198,8 +204,10 @@ PyObject* py_dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
         void* given_p = x.matrix(given);
         const c10::cuda::CUDAGuard guard(x.t.device());
         const at::Tensor out = given.defined() ? given : x.like();
-        return result(g_dropout(ptr(x.t), rp, given_p ? given_p : ptr(out), x.rows, x.cols, x.code,
-                                drop_of(a[1]), stream(x)), out);
+        const credit_status_t st = g_dropout(ptr(x.t), rp, given_p ? given_p : ptr(out), x.rows,
+                                             x.cols, x.code, drop_of(a[1]), stream(x));
+        if (st == CREDIT_OK) written({&given});
+        return result(st, out);
     });
 }
 
@@ -234,6 +242,7 @@ PyObject* py_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         st = g_forward(op, ptr(x.t), rp, drop, ptr(y), h_out.defined() || !same ? ptr(h) : nullptr,
                        static_cast<float*>(ptr(mean)), static_cast<float*>(ptr(rstd)), x.rows, x.cols,
                        x.code, ptr(gamma), ptr(beta), pcode, (float)eps, ptr(ws), wb, stream(x));
+        if (st == CREDIT_OK) written({&out, &h_out});
         return result(st, y, h, mean, rstd);
     });
 }
@@ -273,6 +282,7 @@ PyObject* py_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
             dbeta = dy.empty(like_beta.sizes(), like_beta.scalar_type());
         st = g_backward(op, ptr(dy.t), dhp, hp, mp, sp, ptr(gamma), pcode, drop, ptr(dx), ptr(dr),
                         ptr(dgamma), ptr(dbeta), dy.rows, dy.cols, dy.code, ptr(ws), wb, stream(dy));
+        if (st == CREDIT_OK) written({&dx_given, &dr_given});
         // without dropout the two gradients are one
         return result(st, dx, dr.defined() || !want ? dr : dx, dgamma, dbeta);
     });

@@ -251,3 +251,33 @@ def test_the_pair_inside_an_autograd_function():
         assert torch.equal(y, out[0])
         T.check_backward("layernorm", q, dy, *out[1:], None,
                          (leaves[0].grad, None, leaves[1].grad, leaves[2].grad))
+
+
+def test_tensors_written_in_place_are_known_to_autograd():
+    # a tensor that an earlier product saved is overwritten: its backward pass
+    # is refused, as after torch's own in-place operators
+    def saved():
+        x = T.make((4, 512), torch.float32, 5)
+        w = torch.ones(512, device="cuda", requires_grad=True)
+        return x, (x * w).sum()
+
+    dy, _ = T.grads(4, 512, "f32")
+    h = T.make((4, 512), torch.float32, 6)
+    s = torch.ones(4, device="cuda")
+    drop = credit.Dropout(0.5, 3)
+    writes = [lambda x: credit.dropout(x, drop, out=x),
+              lambda x: credit.layernorm_forward(x, out=x),
+              lambda x: credit.rmsnorm_forward(h, residual=x, h_out=x),
+              lambda x: credit.layernorm_backward(x, h, s, s, dx=x),
+              lambda x: credit.rmsnorm_backward(dy, x, s, dropout=drop, dresidual=x)]
+    for write in writes:
+        x, loss = saved()
+        write(x)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    x, loss = saved()
+    credit.layernorm_forward(x)  # reading leaves it as it is
+    loss.backward()
+    with torch.inference_mode():
+        x = T.make((4, 512), torch.float32, 5)
+    credit.layernorm_forward(x, out=x)  # a tensor without a version
