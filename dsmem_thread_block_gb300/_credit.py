@@ -169,6 +169,7 @@ SIGNATURES = {
                                _vp]),
     "credit_get_device_error": (_i32, [_i32]),
     "credit_selftest_wait_timeout": (_i32, [_i32, _i64]),
+    "credit_selftest_team_timeout": (_i32, [_i32]),
     "credit_debug_build": (_i32, []),
     "credit_selftest_bounds": (_i32, [_i32]),
     "credit_debug_trace": (_i32, [_vp, _i64]),
@@ -510,6 +511,10 @@ def credit_selftest_wait_timeout(device: int = 0, limit_ns: int = 2_000_000) -> 
 
 def credit_debug_build() -> int:
     return load().credit_debug_build()
+
+
+def credit_selftest_team_timeout(device: int = 0) -> int:
+    return load().credit_selftest_team_timeout(device)
 
 
 def credit_selftest_bounds(device: int = 0) -> int:

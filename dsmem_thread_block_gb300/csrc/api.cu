@@ -605,6 +605,16 @@ credit_status_t credit_selftest_wait_timeout(int device, int64_t limit_ns) {
     return credit_get_device_error(device);
 }
 
+credit_status_t credit_selftest_team_timeout(int device) {
+    DeviceGuard g(device);
+    if (!g.ok) return CREDIT_ERR_INVALID_ARG;
+    if (run_team_alone(device) != cudaSuccess) {
+        cudaGetLastError();
+        return CREDIT_ERR_CUDA;
+    }
+    return credit_get_device_error(device);
+}
+
 const char* credit_version(void) { return "0.5.0"; }
 
 }  // extern "C"

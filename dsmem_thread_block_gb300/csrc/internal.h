@@ -187,6 +187,9 @@ TrainLayout norm_bwd_layout(int dtype, int64_t rows, int64_t cols, int sms, int 
 cudaError_t launch_dropout(int dtype, bool vec, const DropoutArgs& a, int sms, cudaStream_t s);
 cudaError_t launch_norm_fwd(TrainKey k, const NormFwdArgs& a, int sms, cudaStream_t s);
 cudaError_t launch_norm_bwd(TrainKey k, NormBwdArgs a, int sms, cudaStream_t s);
+// The forward team kernel as the first CTA of a team whose second is not there;
+// allocates its scratch and waits for it.
+cudaError_t run_team_alone(int dev);
 
 // Kernel selector: op 0..2, dtype 0 = fp32 / 1 = bf16, pdtype likewise,
 // vec = aligned 16-byte path, rows = rows per cluster (1, 2 or 4; the

@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kTeamThreads) bwd_team(NormBwdArgs a, TeamShap
     auto enter = [&](int k) {
         const RowStats r = next;
         if (k + 1 < turns) next = row_stats<OP>(a, row_of(k + 1));
-        TeamBars::wait(bars.fed[t.s], t, q.err);
+        bars.wait(bars.fed[t.s], t, q.err);
         return r;
     };
     if (summing) {
@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(kTeamThreads) bwd_team(NormBwdArgs a, TeamShap
     for (int k = 0; k < turns; ++k, t.next(q.stages)) {
         const int64_t at = row_of(k);
         const RowStats r = enter(k);
-        TeamBars::wait(bars.known[t.s], t, q.err);
+        bars.wait(bars.known[t.s], t, q.err);
         const float2 m = tot[t.s];
         const RowBack back(r, m.x, m.y);
         const T* const ys = slice(t.s, 0, a.dy, at);

@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(kTeamThreads) fwd_team(NormFwdArgs a, TeamShap
     if (summing) {
         const float inv_warp = 1.f / (float)max(1, min(c1 - base0, V * IO::kTile));
         for (int k = 0; k < turns; ++k, t.next(q.stages)) {
-            TeamBars::wait(bars.fed[t.s], t, q.err);
+            bars.wait(bars.fed[t.s], t, q.err);
             pick([&](auto f, auto res, auto on) {
                 constexpr bool FULL = decltype(f)::value;
                 F2 h[V][IO::NP], v = f2(0.f);
@@ -520,8 +520,8 @@ __global__ void __launch_bounds__(kTeamThreads) fwd_team(NormFwdArgs a, TeamShap
     }
     for (int k = 0; k < turns; ++k, t.next(q.stages)) {
         const int64_t at = row_of(k);
-        TeamBars::wait(bars.fed[t.s], t, q.err);
-        TeamBars::wait(bars.known[t.s], t, q.err);
+        bars.wait(bars.fed[t.s], t, q.err);
+        bars.wait(bars.known[t.s], t, q.err);
         const float2 m = tot[t.s];
         T* const y = static_cast<T*>(a.y) + at * a.cols + j0;
         T* const ho = moved(static_cast<T*>(a.h), at * a.cols + j0);
@@ -774,6 +774,38 @@ cudaError_t launch_norm_fwd(TrainKey k, const NormFwdArgs& a, int sms, cudaStrea
                             : pick_fwd<kLayerNorm, bf16>(k, a, sms, s);
     return k.dtype == 0 ? pick_fwd<kRMSNorm, float>(k, a, sms, s)
                         : pick_fwd<kRMSNorm, bf16>(k, a, sms, s);
+}
+
+cudaError_t run_team_alone(int dev) {
+    // 40 turns of 8 tiles through 4 stages, for a rank that the grid does not hold
+    constexpr int kTiles = 8, kStages = 4, kRows = 40, kSize = 2, kWarps = 2;
+    constexpr int kCols = kSize * kTiles * VecIO<float, 4>::kTile;
+    constexpr int kRoom = (kCols / kSize * 4 + 16 + 127) / 128 * 128;
+    constexpr size_t kMatrix = (size_t)kRows * kCols * 4;
+    constexpr size_t kWords = (size_t)kTeamSlots * (kSize + 1) * 16;
+    const void* fn = (const void*)fwd_team<kLayerNorm, float, VecIO<float, 4>, float>;
+    unsigned* err = device_error_word();
+    if (!err || !kernel_info(dev, fn, false)) return cudaErrorInvalidConfiguration;
+    char* buf = nullptr;
+    cudaError_t e = cudaMalloc(&buf, 2 * kMatrix + kWords);
+    if (e != cudaSuccess) return e;
+    e = cudaMemset(buf, 0, 2 * kMatrix + kWords);
+    NormFwdArgs a{};
+    a.x = buf;
+    a.y = buf + kMatrix;
+    a.rows = kRows;
+    a.cols = kCols;
+    a.inv_cols = 1.f / kCols;
+    a.eps = 1.f;
+    a.drop.scale = 1.f;
+    TeamShape q{kTiles, kStages, kRoom, kSize, 1,
+                reinterpret_cast<ulonglong2*>(buf + 2 * kMatrix), err};
+    void* args[] = {&a, &q};
+    if (e == cudaSuccess)
+        e = cudaLaunchKernel(fn, dim3(1), dim3(32 * (2 * kWarps + 2)), args, kStages * kRoom, nullptr);
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
+    const cudaError_t f = cudaFree(buf);
+    return e != cudaSuccess ? e : f;
 }
 
 }  // namespace credit

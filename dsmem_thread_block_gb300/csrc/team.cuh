@@ -63,11 +63,18 @@ struct TeamTurn {
 // after it was deposited (every CTA of the team deposits first), and that after
 // it was summed; so values a stage's warps pass in shared memory (their parts,
 // the row's statistics) stand until they have been read.
+//
+// A wait that gives up ends the waiting of the whole CTA: its other warps go
+// through their turns without any (the call has failed, as the error word
+// says), no copy is issued any more, and the serving warp leaves when those in
+// flight have arrived.  A CTA ends one time limit after its team fell silent.
 struct TeamBars {
     uint64_t fed[kTeamStages], summed[kTeamStages], known[kTeamStages], written[kTeamStages];
+    int gave_up;
     // All threads call.
     __device__ void init(int stages, int W) {
         if (threadIdx.x == 0) {
+            gave_up = 0;
             for (int s = 0; s < stages; ++s) {
                 mbar_init(smem_u32(&fed[s]), 1);
                 mbar_init(smem_u32(&summed[s]), (uint32_t)W);
@@ -79,8 +86,20 @@ struct TeamBars {
         }
         __syncthreads();
     }
-    __device__ static void wait(uint64_t& bar, const TeamTurn& t, unsigned* err) {
-        mbar_wait_bounded(smem_u32(&bar), t.phase, err);
+    __device__ bool over() const { return *static_cast<const volatile int*>(&gave_up) != 0; }
+    __device__ void give_up(unsigned* err) {
+        atomicOr(err, kErrTimeout);
+        *static_cast<volatile int*>(&gave_up) = 1;
+    }
+    __device__ void wait(uint64_t& bar, const TeamTurn& t, unsigned* err) {
+        const uint32_t b = smem_u32(&bar);
+        for (int i = 0; i < 256; ++i)
+            if (mbar_try_wait(b, t.phase)) return;
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(b, t.phase)) {
+            if (over()) return;
+            if (globaltimer_ns() - t0 > kWaitLimitNs) return give_up(err);
+        }
     }
     // Whether the turn of a stage is complete, for every lane of the warp.
     __device__ static bool ready(uint64_t& bar, const TeamTurn& t) {
@@ -94,16 +113,17 @@ struct TeamBars {
         int fed = 0, given = 0;
         for (; fed < min(turns, stages); ++fed) feed(fed, fed);
         TeamTurn sum, out;
-        bool dead = false;  // a wait gave up: carry on without, so that all warps end
         uint64_t t0 = 0;
         while (given < turns || fed < turns) {
             bool moved = false;
-            if (given < turns && (dead || ready(summed[sum.s], sum))) {
+            if (given < turns && ready(summed[sum.s], sum)) {
                 deposit(given++, sum.s);
                 sum.next(stages);
                 moved = true;
             }
-            if (fed < turns && fed < given + stages && (dead || ready(written[out.s], out))) {
+            // (a warp that no longer waits may have passed the stage on too early)
+            if (fed < turns && fed < given + stages && ready(written[out.s], out) &&
+                !__any_sync(0xffffffffu, over())) {
                 feed(fed++, out.s);
                 out.next(stages);
                 moved = true;
@@ -114,9 +134,12 @@ struct TeamBars {
             }
             const uint64_t now = globaltimer_ns();
             if (t0 == 0) t0 = now;
-            if (__any_sync(0xffffffffu, now - t0 > kWaitLimitNs)) {
-                if ((threadIdx.x & 31) == 0) atomicOr(err, kErrTimeout);
-                dead = true;
+            if (__any_sync(0xffffffffu, over() || now - t0 > kWaitLimitNs)) {
+                if ((threadIdx.x & 31) == 0) give_up(err);
+                // the copies in flight: each stage's last
+                for (int f = max(0, fed - stages); f < fed; ++f)
+                    mbar_wait_bounded(smem_u32(&this->fed[f % stages]), (f / stages) & 1, err);
+                return;
             }
         }
     }
@@ -222,15 +245,10 @@ struct TeamExchange {
             }
             const uint64_t now = globaltimer_ns();
             if (t0 == 0) t0 = now;
-            if (__any_sync(0xffffffffu, now - t0 > kWaitLimitNs)) {
-                if (lane == 0) atomicOr(err, kErrTimeout);
-                break;
+            if (__any_sync(0xffffffffu, bars.over() || now - t0 > kWaitLimitNs)) {
+                if (lane == 0) bars.give_up(err);
+                return;
             }
-        }
-        for (; k < turns; ++k, t.next(stages)) {  // gave up: the other warps still end
-            TeamBars::wait(bars.fed[t.s], t, err);
-            done(k, t.s, make_float2(0.f, 0.f));
-            TeamBars::done(bars.known[t.s]);
         }
     }
 };

@@ -785,6 +785,15 @@ credit_status_t credit_get_device_error(int device);
 credit_status_t credit_selftest_wait_timeout(int device, int64_t limit_ns);
 
 /*
+ * The same for the training operators' teams of CTAs: one CTA runs 40 rows as
+ * the first of a team whose second CTA does not exist.  Its wait for the other's
+ * sums gives up after a second, which ends every other wait of the CTA; its
+ * copies in flight are waited for, and CREDIT_ERR_DEVICE_TIMEOUT is returned.
+ * Allocates scratch and synchronises the device.
+ */
+credit_status_t credit_selftest_team_timeout(int device);
+
+/*
  * The checked build (libcredit_checked.so, compiled with -DCREDIT_DEBUG) runs
  * the same kernels with index checks on the staged-slice, ring-slot, chunk
  * mbarrier and exchange-slot accesses: a failed check records

@@ -1,10 +1,13 @@
 """What the training operators hand back beside y: h where a caller asks for
 it, and gradients formed from what the forward pass returned, in every form
 (a warp, a ring, a team, a sweep a row), aligned and odd."""
+import time
+
 import pytest
 import torch
 
 import dsmem_thread_block_gb300 as credit
+from dsmem_thread_block_gb300 import _credit as C
 
 import test_gpu_train_ops as T
 
@@ -281,3 +284,22 @@ def test_tensors_written_in_place_are_known_to_autograd():
     with torch.inference_mode():
         x = T.make((4, 512), torch.float32, 5)
     credit.layernorm_forward(x, out=x)  # a tensor without a version
+
+
+def test_a_team_whose_wait_gives_up_ends():
+    # a CTA whose peer never deposits: it gives up after a second, and its other
+    # 39 turns and the waits of its other warps cost no second each
+    dev = torch.cuda.current_device()
+    assert credit.device_error(dev) == 0
+    for load in (C.load(), None):
+        t0 = time.monotonic()
+        if load is not None:
+            assert C.credit_selftest_team_timeout(dev) == C.ERR_DEVICE_TIMEOUT
+        else:
+            with C.use_checked_build():
+                assert C.credit_selftest_team_timeout(dev) == C.ERR_DEVICE_TIMEOUT
+        assert time.monotonic() - t0 < 5.0
+    assert credit.device_error(dev) == 0  # read and cleared
+    q = T.problem(13, 300008, "bf16", "layernorm", True, 0.1, "f32", seed=67)
+    T.check_forward("layernorm", q, T.forward("layernorm", q))
+    assert credit.device_error(dev) == 0
