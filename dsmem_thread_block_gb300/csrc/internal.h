@@ -185,7 +185,7 @@ int train_chunks(int dtype, int64_t cols);
 int64_t norm_fwd_partials(int dtype, int64_t rows, int64_t cols, int sms);  // bytes
 TrainLayout norm_bwd_layout(int dtype, int64_t rows, int64_t cols, int sms, int l2_bytes);
 cudaError_t launch_dropout(int dtype, bool vec, const DropoutArgs& a, int sms, cudaStream_t s);
-cudaError_t launch_norm_fwd(TrainKey k, const NormFwdArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_norm_fwd(TrainKey k, NormFwdArgs a, int sms, cudaStream_t s);
 cudaError_t launch_norm_bwd(TrainKey k, NormBwdArgs a, int sms, cudaStream_t s);
 // The forward team kernel as the first CTA of a team whose second is not there;
 // allocates its scratch and waits for it.

@@ -222,8 +222,7 @@ __global__ void __launch_bounds__(kRingThreads) fwd_ring(NormFwdArgs a, RingShap
         unsigned char* const stage = ring + s * stage_bytes;
         mbar_wait_bounded(smem_u32(&full[s]), phase, q.err);
         float mean[R], m2;
-        // (`keep`: h may be wanted; a constant where it is not)
-        auto take = [&](auto f, auto res, auto on, auto keep) {
+        auto take = [&](auto f, auto res, auto on) {
             constexpr bool FULL = decltype(f)::value;
 #pragma unroll
             for (int j = 0; j < R; ++j) {
@@ -244,7 +243,7 @@ __global__ void __launch_bounds__(kRingThreads) fwd_ring(NormFwdArgs a, RingShap
                     for (int e = 0; e < IO::NP; ++e)
                         t = OP == kLayerNorm ? add2(t, h[j][i][e]) : fma2(h[j][i][e], h[j][i][e], t);
                 }
-                if (keep && ho && (j == 0 || both)) {
+                if ((res || on) && ho && (j == 0 || both)) {
 #pragma unroll
                     for (int i = 0; i < V; ++i)
                         IO::template store<FULL>(ho + j * a.cols, i * IO::kTile, left, h[j][i]);
@@ -271,10 +270,9 @@ __global__ void __launch_bounds__(kRingThreads) fwd_ring(NormFwdArgs a, RingShap
         };
         const std::true_type yes;
         const std::false_type no;
-        if (!whole) take(no, ns > 1, a.drop.on != 0, yes);
-        else if (ns > 1) a.drop.on ? take(yes, yes, yes, yes) : take(yes, yes, no, yes);
-        else if (a.drop.on) take(yes, no, yes, yes);
-        else ho ? take(yes, no, no, yes) : take(yes, no, no, no);
+        if (!whole) take(no, ns > 1, a.drop.on != 0);
+        else if (ns > 1) a.drop.on ? take(yes, yes, yes) : take(yes, yes, no);
+        else a.drop.on ? take(yes, no, yes) : take(yes, no, no);
         {   // the warp's (sum, M2 about its mean) of each row
             const float sum = m2;
             if constexpr (OP == kLayerNorm) m2 = row_sum<R>(v, lane);
@@ -469,8 +467,10 @@ __global__ void __launch_bounds__(kTeamThreads) fwd_team(NormFwdArgs a, TeamShap
                       (uint32_t)row, h);
     };
     // f(whole, residual, dropout) with what holds for the whole call as constants
+    // (a copy of x as h, without residual and dropout, takes the general code)
+    const bool plain = whole && (summing || ns > 1 || a.drop.on || !a.h);
     auto pick = [&](auto f) {
-        if (!whole) f(no, ns > 1, a.drop.on != 0);
+        if (!plain) f(no, ns > 1, a.drop.on != 0);
         else if (ns > 1) a.drop.on ? f(yes, yes, yes) : f(yes, yes, no);
         else a.drop.on ? f(yes, no, yes) : f(yes, no, no);
     };
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(kTeamThreads) fwd_team(NormFwdArgs a, TeamShap
             for (int i = 0; i < V; ++i) {
                 F2 h[IO::NP];
                 tile(f, res, on, at, i, h);
-                if (ho) IO::template store<FULL>(ho, i * IO::kTile, left, h);
+                if ((res || on || !FULL) && ho) IO::template store<FULL>(ho, i * IO::kTile, left, h);
 #pragma unroll
                 for (int e = 0; e < IO::NP; ++e)
                     h[e] = normed<OP>(h[e], m.x, m.y, g[i][e], b[i][e]);
@@ -707,7 +707,7 @@ cudaError_t run_warp(const NormFwdArgs& a, int sms, cudaStream_t s) {
 
 // IO and WIO: the access forms of the ring and warp kernels and of the sweep.
 template <int OP, typename T, typename IO, typename WIO, typename PT>
-cudaError_t run_fwd(const NormFwdArgs& a, int sms, cudaStream_t s) {
+cudaError_t run_fwd(NormFwdArgs& a, int sms, cudaStream_t s) {
     const int tiles = (a.cols + IO::kTile - 1) / IO::kTile;
     if (tiles <= 1) return run_warp<OP, T, IO, PT, 1>(a, sms, s);
     if (tiles <= 2) return run_warp<OP, T, IO, PT, 2>(a, sms, s);
@@ -721,6 +721,16 @@ cudaError_t run_fwd(const NormFwdArgs& a, int sms, cudaStream_t s) {
                          sweep_batch(a.rows, (int64_t)a.cols * streams * sizeof(T), a.l2_bytes),
                          WIO::N, s);
     }
+    // The ring kernel stores h where it forms it from x and something else.  A copy
+    // of x is formed by a mask that keeps all (any word is at least 0, and x 1 is
+    // x): a store in its code without residual and dropout, written in three
+    // ways, cost the calls that want none up to 6 % (1024 x 262144 bf16 LayerNorm
+    // 358 -> 379 us, 4096 x 8192 fp32 with residual and dropout 114 -> 121).
+    if (a.h && !a.residual && !a.drop.on) {
+        a.drop.on = 1;
+        a.drop.threshold = 0;
+        a.drop.scale = 1.f;
+    }
     const RingKernels fn{(const void*)fwd_ring<OP, T, IO, PT, 4, 1>,
                          (const void*)fwd_ring<OP, T, IO, PT, 4, 2>,
                          (const void*)fwd_ring<OP, T, IO, PT, 8, 1>};
@@ -733,13 +743,13 @@ cudaError_t run_fwd(const NormFwdArgs& a, int sms, cudaStream_t s) {
 }
 
 template <int OP, typename T, typename IO, typename WIO>
-cudaError_t pick_param(const NormFwdArgs& a, int sms, cudaStream_t s) {
+cudaError_t pick_param(NormFwdArgs& a, int sms, cudaStream_t s) {
     return a.half ? run_fwd<OP, T, IO, WIO, bf16>(a, sms, s)
                   : run_fwd<OP, T, IO, WIO, float>(a, sms, s);
 }
 
 template <int OP, typename T>
-cudaError_t pick_fwd(TrainKey k, const NormFwdArgs& a, int sms, cudaStream_t s) {
+cudaError_t pick_fwd(TrainKey k, NormFwdArgs& a, int sms, cudaStream_t s) {
     constexpr int N = 16 / (int)sizeof(T);
     return k.vec ? pick_param<OP, T, VecIO<T, 4>, VecIO<T, N>>(a, sms, s)
                  : pick_param<OP, T, ElemIO<T, 4>, ElemIO<T, N>>(a, sms, s);
@@ -768,7 +778,7 @@ int64_t norm_fwd_partials(int dtype, int64_t rows, int64_t cols, int sms) {
     return most;
 }
 
-cudaError_t launch_norm_fwd(TrainKey k, const NormFwdArgs& a, int sms, cudaStream_t s) {
+cudaError_t launch_norm_fwd(TrainKey k, NormFwdArgs a, int sms, cudaStream_t s) {
     if (k.op == kLayerNorm)
         return k.dtype == 0 ? pick_fwd<kLayerNorm, float>(k, a, sms, s)
                             : pick_fwd<kLayerNorm, bf16>(k, a, sms, s);
