@@ -16,18 +16,34 @@
 // bwd_params adds them.  Every sum has a fixed order: results repeat bit for
 // bit.
 //
-// Measured (GB300, share of the 6782 GB/s copy rate; fp32 parameters unless
-// said otherwise):
+// Measured (GB300, both launches in a replayed graph, share of the 6782 GB/s copy
+// rate; fp32 parameters unless said otherwise):
 //   16384 x 4096 bf16, LayerNorm, dh, dropout    142 us  0.70   (ring)
-//   8192 x 8192 bf16, RMSNorm, dh, bf16 weight    88 us  0.90   (ring)
-//   2048 x 10001 fp32, LayerNorm                  48 us  0.76   (ring, clusters of 5)
+//   8192 x 8192 bf16, RMSNorm, dh, bf16 weight    89 us  0.89   (ring)
+//   2048 x 10001 fp32, LayerNorm                  47 us  0.77   (ring, clusters of 5)
+//   2048 x 10001 bf16, LayerNorm                  46 us  0.40   (ring)
 //   4096 x 8192 fp32, LayerNorm                   69 us  0.86   (ring)
-//   1024 x 262144 bf16, LayerNorm                331 us  0.72   (team)
-//   256 x 786432 bf16, RMSNorm, bf16 weight      225 us  0.79   (team)
-//   32 x 1024 fp32, LayerNorm                    5.1 us (two launches)
-// What bounds them: instructions (21 an element for RMSNorm, 26 for LayerNorm,
-// half as much again with dropout) at the 16 warps an SM that the parameter
-// sums' registers leave, then HBM.
+//   the same with dh and dropout                 136 us  0.73
+//   16384 x 2048 bf16, LayerNorm                  55 us  0.54   (ring)
+//   8192 x 1024 fp32, LayerNorm                   32 us  0.46   (ring)
+//   512 x 70001 bf16, LayerNorm                   77 us  0.41   (team)
+//   1024 x 262144 bf16, LayerNorm                328 us  0.72   (team)
+//   256 x 786432 bf16, RMSNorm, bf16 weight      226 us  0.79   (team)
+//   64 x 1000000 bf16, LayerNorm                 161 us  0.36   (sweep)
+//   524288 x 128 bf16, LayerNorm                 158 us  0.38   (warp)
+//   262144 x 64 bf16, LayerNorm                   75 us  0.20   (warp)
+//   65536 x 512 bf16, LayerNorm                   56 us  0.53   (warp)
+//   32 x 1024 fp32, LayerNorm                    5.5 us (two launches, one behind
+//                                                 the other)
+// What bounds them.  Training block: 45 instructions an element fill 57 % of the
+// issue slots; the rest is their latency, which the 15 warps an SM that the
+// parameter sums' registers leave do not hide (the mask is drawn between a row's
+// sums and its stores).  Up to 2048 columns: CTAs of few warps leave some 900
+// groups' sums, which bwd_params adds on a CTA for each 128 columns.  Odd bf16
+// rows: staged and stored two bytes at a time.  Short rows: 8 to 16 warps an SM
+// (153 to 221 registers above 256 columns), one row each in flight.  Spills:
+// odd bf16 LayerNorm rings 60 to 76 bytes, sweeps of bf16 rows 32 to 120, odd ones
+// 212 to 364.
 #include <algorithm>
 
 #include "planner.h"

@@ -10,20 +10,31 @@
 //              from L2 (sweep.cuh)
 // Each reads x and residual from HBM once and writes h and y once.
 //
-// Measured (GB300, share of the 6782 GB/s copy rate; bf16, fp32 parameters):
-//   16384 x 4096, LayerNorm, residual, dropout    88 us  0.90   (ring)
-//   8192 x 8192, LayerNorm                         49 us  0.81   (ring)
-//   2048 x 10001, LayerNorm, residual, dropout    53 us  0.46   (ring, odd rows)
-//   1024 x 262144, LayerNorm                      359 us  0.44   (ring, clusters of 16)
-//   1024 x 262144, RMSNorm                        239 us  0.66
-//   300 x 850000, LayerNorm                       267 us  0.57   (team)
-//   one row of 4096, RMSNorm, residual            2.1 us
-// What bounds them: instructions and the latency of a row's reduction, then
-// HBM.  13 instructions an element for LayerNorm (16 with a residual, 27 with
-// dropout too), at 16 warps an SM; odd rows are read, written and masked an
-// element at a time; the widest LayerNorm rows read their parameters from L2
-// for every row, and clusters of 16 leave 40 SMs empty (teams use them all, but
-// took 355 us for LayerNorm and 302 for RMSNorm on 1024 x 262144).
+// Measured (GB300, in a replayed graph, share of the 6782 GB/s copy rate; bf16,
+// fp32 parameters):
+//   16384 x 4096, LayerNorm, residual, dropout    89 us  0.89   (ring)
+//   8192 x 8192, LayerNorm                        50 us  0.80   (ring)
+//   16384 x 2048, LayerNorm                       24 us  0.81   (ring)
+//   2048 x 10001, LayerNorm, residual, dropout    52 us  0.46   (ring, odd rows)
+//   4096 x 8192 fp32, LayerNorm                   45 us  0.88   (ring)
+//   the same with residual and dropout           113 us  0.70
+//   1024 x 262144, LayerNorm                     358 us  0.44   (ring, clusters of 16)
+//   1024 x 262144, RMSNorm                       239 us  0.66
+//   300 x 850000, LayerNorm                      247 us  0.61   (team)
+//   64 x 1000000, LayerNorm                      122 us  0.32   (sweep)
+//   524288 x 128, LayerNorm                       78 us  0.51   (warp)
+//   262144 x 64, LayerNorm                        38 us  0.26   (warp)
+//   65536 x 512, LayerNorm                        30 us  0.66   (warp)
+//   one row of 4096, RMSNorm, residual           2.2 us
+// What bounds them: HBM up to some 8192 columns.  Odd rows: 44 instructions an
+// element with residual and dropout (read, written and masked one at a time)
+// fill 47 % of the issue slots; 15 warps an SM do not hide their loads from
+// global and local memory (the two-row LayerNorm form spills 40 to 44 bytes).
+// The widest LayerNorm rows read their parameters from L2 for every row and wait
+// a row's exchange out, and clusters of 16 leave 40 SMs empty (teams use them all,
+// but took 355 us for LayerNorm and 302 for RMSNorm on 1024 x 262144).  Short
+// rows: a warp has one row's few hundred bytes in flight.  Teams at odd widths
+// spill 48 to 112 bytes, sweeps of odd bf16 rows 116 to 168.
 //
 // Statistics: sum and M2 about the piece's own mean (of a warp, a CTA or a
 // chunk), merged with the parallel-axis form of Chan et al.'s update.

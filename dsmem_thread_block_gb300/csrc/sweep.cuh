@@ -6,7 +6,7 @@
 // columns, whose parameters stay in registers, of a group of rows.
 //
 // Measured on rows that the team kernels (team.cuh) take: 256 x 786432 bf16,
-// RMSNorm backward, 376 us against a team's 225 us; so only rows that no team
+// RMSNorm backward, 376 us against a team's 226 us; so only rows that no team
 // holds come here (above 856064 columns, 44 tiles for each of 152 CTAs).
 // Bound by the latency of a block's first loads: two rows in flight, eight a
 // block and four blocks an SM measured best of nine settings (349 to 581 us).

@@ -19,9 +19,9 @@
 // Measured on 256 rows of 786432 bf16 columns, RMSNorm backward: warps that sum
 // and write, 366 us; the kinds apart with a barrier a row, 314 and later 272;
 // mbarriers 269; statistics from one CTA a turn instead of every CTA merging
-// all parts, 225 (0.79 of the copy rate).  What bounds it now is a turn's
+// all parts, 226 (0.79 of the copy rate).  What bounds it now is a turn's
 // passage through the slowest CTA, 0.7 to 1.0 us however few columns it has:
-// 1024 rows of 262144 columns take 331 us with 50 CTAs a row, 740 with 140.
+// 1024 rows of 262144 columns take 328 us with 50 CTAs a row, 740 with 140.
 #pragma once
 
 #include "planner.h"
