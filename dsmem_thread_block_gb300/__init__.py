@@ -2,7 +2,8 @@
 
 Clustered DSMEM row softmax, LayerNorm, RMSNorm, int8 quantization, weighted
 standardization and Pearson correlation, and the row norms' training step
-(dropout, residual add and norm with saved statistics, and its gradient),
+(dropout, residual add and norm with saved statistics, and its gradient), the
+linear head's cross entropy with its gradient, and the clipping of gradients,
 behind a C ABI
 (``libcredit.so``, declared in ``include/credit.h``), with this thin torch
 binding on top.  The binding only marshals arguments (device pointers, sizes,
@@ -23,7 +24,8 @@ from ._credit import CreditError, Plan  # noqa: F401
 
 __all__ = ["softmax", "layernorm", "rmsnorm", "quantize", "weighted_std", "pearson", "plan",
            "Dropout", "dropout", "layernorm_forward", "layernorm_backward", "rmsnorm_forward",
-           "rmsnorm_backward", "CreditError", "Plan", "device_error", "load_library"]
+           "rmsnorm_backward", "linear_cross_entropy_forward", "linear_cross_entropy_backward",
+           "gradient_norm", "clip_gradients", "CreditError", "Plan", "device_error", "load_library"]
 
 _OPS = {"softmax": C.SOFTMAX, "layernorm": C.LAYERNORM, "rmsnorm": C.RMSNORM,
         "quantize": C.QUANTIZE, "weighted_std": C.WEIGHTED_STD, "pearson": C.PEARSON}
@@ -217,7 +219,8 @@ def pearson(x, u, eps: float = 0.0, out=None, r=None, plan: Plan | None = None, 
 # The training operators live in train.py, loaded at first use (this module
 # imports torch only inside its calls).
 _TRAIN = ("Dropout", "dropout", "layernorm_forward", "layernorm_backward", "rmsnorm_forward",
-          "rmsnorm_backward")
+          "rmsnorm_backward", "linear_cross_entropy_forward", "linear_cross_entropy_backward",
+          "gradient_norm", "clip_gradients")
 
 
 def __getattr__(name):

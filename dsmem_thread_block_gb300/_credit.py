@@ -74,6 +74,12 @@ class DropoutFields(ctypes.Structure):
                 ("device_offset", ctypes.c_void_p)]
 
 
+class Tensor(ctypes.Structure):
+    """Mirror of credit_tensor_t."""
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("count", ctypes.c_int64),
+                ("dtype", ctypes.c_int32)]
+
+
 class DeviceKey(ctypes.Structure):
     """Mirror of credit_device_key_t."""
     _fields_ = [("gpu_name", ctypes.c_char * 96), ("sms", ctypes.c_int32),
@@ -146,6 +152,16 @@ SIGNATURES = {
     "credit_norm_backward": (_i32, [_i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32,
                                     ctypes.POINTER(DropoutFields), _vp, _vp, _vp, _vp, _i64, _i64,
                                     _i32, _vp, _sz, _vp]),
+    "credit_linear_ce_workspace": (_i32, [_i32, _vp, _vp, _i64, _i64, _i64, _i32, _i32,
+                                          ctypes.POINTER(ctypes.c_size_t)]),
+    "credit_linear_ce_forward": (_i32, [_vp, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _i32,
+                                        _vp, _sz, _vp]),
+    "credit_linear_ce_backward": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64,
+                                         _i64, _i64, _i32, _vp, _sz, _vp]),
+    "credit_grad_workspace": (_i32, [ctypes.POINTER(Tensor), _i64, _i32,
+                                     ctypes.POINTER(ctypes.c_size_t)]),
+    "credit_grad_norm": (_i32, [ctypes.POINTER(Tensor), _i64, _vp, _vp, _sz, _vp]),
+    "credit_grad_clip": (_i32, [ctypes.POINTER(Tensor), _i64, _f32, _f32, _vp, _vp, _sz, _vp]),
     "credit_two_pass_noalloc": (_i32, [_i32, _vp, _vp, _i64, _i64, _i32, _vp, _vp, _i32, _f32,
                                        _vp]),
     "credit_bench_dsmem": (_i32, [_i32, _i32, _i32, _i32, _i32, ctypes.POINTER(BenchResult)]),
@@ -368,6 +384,55 @@ def credit_norm_backward(op: int, dy: int, dh: int, h: int, mean: int, rstd: int
     return load().credit_norm_backward(op, dy, dh, h, mean, rstd, gamma, param_dtype,
                                        _drop_ptr(drop), dx, dresidual, dgamma, dbeta, rows, cols,
                                        dtype, workspace, workspace_bytes, stream)
+
+
+def credit_linear_ce_workspace(backward: bool, hidden: int, weight: int, tokens: int,
+                               hidden_size: int, vocab: int, dtype: int, device: int = 0) -> int:
+    n = ctypes.c_size_t()
+    _check(load().credit_linear_ce_workspace(int(backward), hidden, weight, tokens, hidden_size,
+                                             vocab, dtype, device, ctypes.byref(n)),
+           "credit_linear_ce_workspace")
+    return n.value
+
+
+def credit_linear_ce_forward(hidden: int, weight: int, target: int, ignore_index: int, loss: int,
+                             lse: int, tokens: int, hidden_size: int, vocab: int, dtype: int,
+                             workspace: int = 0, workspace_bytes: int = 0, stream: int = 0) -> int:
+    return load().credit_linear_ce_forward(hidden, weight, target, ignore_index, loss, lse, tokens,
+                                           hidden_size, vocab, dtype, workspace, workspace_bytes,
+                                           stream)
+
+
+def credit_linear_ce_backward(dloss: int, dlse: int, hidden: int, weight: int, target: int,
+                              ignore_index: int, lse: int, dhidden: int, dweight: int, tokens: int,
+                              hidden_size: int, vocab: int, dtype: int, workspace: int = 0,
+                              workspace_bytes: int = 0, stream: int = 0) -> int:
+    return load().credit_linear_ce_backward(dloss, dlse, hidden, weight, target, ignore_index, lse,
+                                            dhidden, dweight, tokens, hidden_size, vocab, dtype,
+                                            workspace, workspace_bytes, stream)
+
+
+def tensors(entries):
+    """An array of credit_tensor_t from (data, out, count, dtype) tuples."""
+    return (Tensor * len(entries))(*(Tensor(d, o, n, t) for d, o, n, t in entries))
+
+
+def credit_grad_workspace(array, device: int = 0) -> int:
+    n = ctypes.c_size_t()
+    _check(load().credit_grad_workspace(array, len(array), device, ctypes.byref(n)),
+           "credit_grad_workspace")
+    return n.value
+
+
+def credit_grad_norm(array, norm: int, workspace: int = 0, workspace_bytes: int = 0,
+                     stream: int = 0) -> int:
+    return load().credit_grad_norm(array, len(array), norm, workspace, workspace_bytes, stream)
+
+
+def credit_grad_clip(array, max_norm: float, eps: float, norm: int, workspace: int = 0,
+                     workspace_bytes: int = 0, stream: int = 0) -> int:
+    return load().credit_grad_clip(array, len(array), max_norm, eps, norm, workspace,
+                                   workspace_bytes, stream)
 
 
 def credit_two_pass_noalloc(op: int, x: int, y: int, rows: int, cols: int, dtype: int,

@@ -19,6 +19,7 @@
 #include <cstdint>
 #include <initializer_list>
 #include <stdexcept>
+#include <vector>
 
 #include "credit.h"
 
@@ -28,6 +29,12 @@ decltype(&credit_dropout) g_dropout;
 decltype(&credit_norm_workspace) g_workspace;
 decltype(&credit_norm_forward) g_forward;
 decltype(&credit_norm_backward) g_backward;
+decltype(&credit_linear_ce_workspace) g_ce_workspace;
+decltype(&credit_linear_ce_forward) g_ce_forward;
+decltype(&credit_linear_ce_backward) g_ce_backward;
+decltype(&credit_grad_workspace) g_grad_workspace;
+decltype(&credit_grad_norm) g_grad_norm;
+decltype(&credit_grad_clip) g_grad_clip;
 
 // A refusal: the Python exception type and its message.
 struct Refused {
@@ -288,17 +295,197 @@ PyObject* py_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// ---------------------------------------------------- the head's cross entropy
+// hidden, weight and target of a call.
+struct Head {
+    const Input h;
+    const at::Tensor &w, &target;
+    int64_t vocab, ignore;
+    Head(PyObject* hidden, PyObject* weight, PyObject* targets, PyObject* ignore_index)
+        : h(hidden), w(tensor(weight)), target(tensor(targets)) {
+        if (!w.defined() || w.dim() != 2 || w.size(1) != h.cols || w.size(0) < 1 ||
+            w.scalar_type() != h.t.scalar_type() || w.device() != h.t.device() || !w.is_contiguous())
+            bad("credit: weight must be a contiguous (vocabulary, hidden size) tensor of the hidden "
+                "states' dtype and on their device");
+        vocab = w.size(0);
+        if (!target.defined() || target.scalar_type() != at::kLong || target.device() != h.t.device() ||
+            target.sizes() != h.t.sizes().slice(0, h.t.dim() - 1) || !target.is_contiguous())
+            bad("credit: target must be a contiguous int64 tensor on the hidden states' device, one "
+                "element per token");
+        ignore = PyLong_AsLongLong(ignore_index);
+    }
+    // one fp32 value per token
+    const float* per_token(const at::Tensor& v) const {
+        if (v.scalar_type() != at::kFloat || v.numel() != h.rows || v.device() != h.t.device() ||
+            !v.is_contiguous())
+            bad("credit: dloss, dlse and lse must be contiguous fp32 tensors on the hidden states' "
+                "device, one element per token");
+        return static_cast<const float*>(v.data_ptr());
+    }
+    const int64_t* targets() const { return static_cast<const int64_t*>(target.data_ptr()); }
+    at::Tensor workspace(int backward, const at::Tensor& given, size_t* bytes,
+                         credit_status_t* status) const {
+        size_t need = 0;
+        *status = g_ce_workspace(backward, ptr(h.t), ptr(w), h.rows, h.cols, vocab, h.code,
+                                 h.t.get_device(), &need);
+        if (given.defined()) {
+            if (given.device() != h.t.device() || !given.is_contiguous())
+                bad("credit: workspace must be a contiguous tensor on the input's device");
+            *bytes = given.nbytes();
+            return given;
+        }
+        *bytes = need;
+        if (*status != CREDIT_OK || need == 0) return at::Tensor();
+        return h.empty({(int64_t)need}, at::kByte);
+    }
+};
+
+// linear_ce_forward(hidden, weight, target, ignore index, workspace)
+PyObject* py_ce_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 5, [&]() -> PyObject* {
+        no_graph(a, {0, 1});
+        const Head head(a[0], a[1], a[2], a[3]);
+        if (PyErr_Occurred()) return nullptr;
+        const Input& h = head.h;
+        const c10::cuda::CUDAGuard guard(h.t.device());
+        size_t wb = 0;
+        credit_status_t st;
+        const at::Tensor ws = head.workspace(0, tensor(a[4]), &wb, &st);
+        if (st != CREDIT_OK) return result(st);
+        const at::Tensor loss = h.empty(head.target.sizes(), at::kFloat);
+        const at::Tensor lse = h.empty(head.target.sizes(), at::kFloat);
+        st = g_ce_forward(ptr(h.t), ptr(head.w), head.targets(), head.ignore,
+                          static_cast<float*>(ptr(loss)), static_cast<float*>(ptr(lse)), h.rows, h.cols,
+                          head.vocab, h.code, ptr(ws), wb, stream(h));
+        return result(st, loss, lse);
+    });
+}
+
+// linear_ce_backward(dloss, hidden, weight, target, lse, dlse, ignore index, need dhidden,
+//                    need dweight, dhidden, dweight, workspace)
+PyObject* py_ce_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 12, [&]() -> PyObject* {
+        no_graph(a, {0, 1, 2, 4, 5, 9, 10});
+        const Head head(a[1], a[2], a[3], a[6]);
+        if (PyErr_Occurred()) return nullptr;
+        const Input& h = head.h;
+        const at::Tensor &dloss = tensor(a[0]), &lse = tensor(a[4]), &dlse = tensor(a[5]);
+        const at::Tensor &dh_given = tensor(a[9]), &dw_given = tensor(a[10]);
+        if (!dloss.defined() || !lse.defined()) bad("credit: dloss and the forward pass's lse are required");
+        const float *dp = head.per_token(dloss), *lp = head.per_token(lse);
+        const float* ep = dlse.defined() ? head.per_token(dlse) : nullptr;
+        const int want_h = PyObject_IsTrue(a[7]), want_w = PyObject_IsTrue(a[8]);
+        if (want_h < 0 || want_w < 0) return nullptr;
+        h.matrix(dh_given);
+        if (dw_given.defined() &&
+            (dw_given.sizes() != head.w.sizes() || dw_given.scalar_type() != head.w.scalar_type() ||
+             dw_given.device() != head.w.device() || !dw_given.is_contiguous()))
+            bad("credit: dweight must be a contiguous tensor like weight");
+        const c10::cuda::CUDAGuard guard(h.t.device());
+        size_t wb = 0;
+        credit_status_t st;
+        const at::Tensor ws = head.workspace(1, tensor(a[11]), &wb, &st);
+        if (st != CREDIT_OK) return result(st);
+        at::Tensor dh = dh_given, dw = dw_given;
+        if (!dh.defined() && want_h) dh = h.like();
+        if (!dw.defined() && want_w) dw = h.empty(head.w.sizes(), head.w.scalar_type());
+        st = g_ce_backward(dp, ep, ptr(h.t), ptr(head.w), head.targets(), head.ignore, lp, ptr(dh),
+                           ptr(dw), h.rows, h.cols, head.vocab, h.code, ptr(ws), wb, stream(h));
+        if (st == CREDIT_OK) written({&dh_given, &dw_given});
+        return result(st, dh, dw);
+    });
+}
+
+// ------------------------------------------------ the gradients' norm and clipping
+// The elements of a list or tuple (a new reference, released with it).
+struct Items {
+    PyObject* seq;
+    explicit Items(PyObject* o) : seq(PySequence_Fast(o, "credit: a list of tensors was expected")) {
+        if (!seq) throw python_error();
+    }
+    ~Items() { Py_XDECREF(seq); }
+    Items(const Items&) = delete;
+    Items& operator=(const Items&) = delete;
+    Py_ssize_t size() const { return PySequence_Fast_GET_SIZE(seq); }
+    PyObject* operator[](Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(seq, i); }
+};
+
+// gradients(tensors, outputs, clip, max norm, eps, workspace): the norm; outputs
+// None: in place (clip) or none
+PyObject* py_gradients(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 6, [&]() -> PyObject* {
+        const int clip = PyObject_IsTrue(a[2]);
+        const double max_norm = PyFloat_AsDouble(a[3]), eps = PyFloat_AsDouble(a[4]);
+        if (clip < 0 || PyErr_Occurred()) return nullptr;
+        const Items in(a[0]);
+        const bool apart = clip && a[1] != Py_None;
+        const Items out(apart ? a[1] : a[0]);
+        if (in.size() == 0) bad("credit: at least one gradient is required");
+        if (in.size() != out.size()) bad("credit: one output per gradient is required");
+        std::vector<credit_tensor_t> t((size_t)in.size());
+        const bool graph = c10::GradMode::is_enabled();
+        at::Device device(at::kCPU);
+        for (Py_ssize_t i = 0; i < in.size(); ++i) {
+            const at::Tensor &g = tensor(in[i]), &o = tensor(out[i]);
+            if (!g.defined() || !g.is_cuda() || !g.is_non_overlapping_and_dense())
+                bad("credit: gradients must be dense CUDA tensors");
+            if (i == 0) device = g.device();
+            if (g.device() != device) bad("credit: gradients must be on one device");
+            if (apart && (!o.defined() || o.sizes() != g.sizes() || o.strides() != g.strides() ||
+                          o.scalar_type() != g.scalar_type() || o.device() != device))
+                bad("credit: outputs must be tensors like the gradients, of their strides");
+            if (graph && (g.requires_grad() || (apart && o.requires_grad())))
+                throw Refused{PyExc_RuntimeError,
+                              "credit: the training operators record no autograd graph, and a tensor "
+                              "that requires a gradient was given: call under torch.no_grad()"};
+            t[i].data = ptr(g);
+            t[i].out = clip ? ptr(o) : nullptr;
+            t[i].count = g.numel();
+            t[i].dtype = code_of(g);
+        }
+        const c10::cuda::CUDAGuard guard(device);
+        const at::Tensor& given = tensor(a[5]);
+        size_t bytes = 0;
+        credit_status_t st = g_grad_workspace(t.data(), (int64_t)t.size(), device.index(), &bytes);
+        if (st != CREDIT_OK) return result(st);
+        at::Tensor ws = given;
+        if (given.defined()) {
+            if (given.device() != device || !given.is_contiguous())
+                bad("credit: workspace must be a contiguous tensor on the gradients' device");
+            bytes = given.nbytes();
+        } else if (bytes) {
+            ws = at::detail::empty_cuda({(int64_t)bytes}, at::kByte, device, c10::nullopt);
+        }
+        const at::Tensor norm = at::detail::empty_cuda({}, at::kFloat, device, c10::nullopt);
+        float* const np = static_cast<float*>(ptr(norm));
+        void* const s = c10::cuda::getCurrentCUDAStream(device.index()).stream();
+        st = clip ? g_grad_clip(t.data(), (int64_t)t.size(), (float)max_norm, (float)eps, np, ptr(ws),
+                                bytes, s)
+                  : g_grad_norm(t.data(), (int64_t)t.size(), np, ptr(ws), bytes, s);
+        if (st == CREDIT_OK && clip)
+            for (Py_ssize_t i = 0; i < out.size(); ++i) written({&tensor(out[i])});
+        return result(st, norm);
+    });
+}
+
 // bind(addresses of credit_dropout, credit_norm_workspace, credit_norm_forward,
-//      credit_norm_backward)
+//      credit_norm_backward, credit_linear_ce_workspace, credit_linear_ce_forward,
+//      credit_linear_ce_backward, credit_grad_workspace, credit_grad_norm, credit_grad_clip)
 PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (n != 4) {
-        PyErr_SetString(PyExc_TypeError, "bind takes four addresses");
+    if (n != 10) {
+        PyErr_SetString(PyExc_TypeError, "bind takes ten addresses");
         return nullptr;
     }
     g_dropout = reinterpret_cast<decltype(g_dropout)>(PyLong_AsVoidPtr(a[0]));
     g_workspace = reinterpret_cast<decltype(g_workspace)>(PyLong_AsVoidPtr(a[1]));
     g_forward = reinterpret_cast<decltype(g_forward)>(PyLong_AsVoidPtr(a[2]));
     g_backward = reinterpret_cast<decltype(g_backward)>(PyLong_AsVoidPtr(a[3]));
+    g_ce_workspace = reinterpret_cast<decltype(g_ce_workspace)>(PyLong_AsVoidPtr(a[4]));
+    g_ce_forward = reinterpret_cast<decltype(g_ce_forward)>(PyLong_AsVoidPtr(a[5]));
+    g_ce_backward = reinterpret_cast<decltype(g_ce_backward)>(PyLong_AsVoidPtr(a[6]));
+    g_grad_workspace = reinterpret_cast<decltype(g_grad_workspace)>(PyLong_AsVoidPtr(a[7]));
+    g_grad_norm = reinterpret_cast<decltype(g_grad_norm)>(PyLong_AsVoidPtr(a[8]));
+    g_grad_clip = reinterpret_cast<decltype(g_grad_clip)>(PyLong_AsVoidPtr(a[9]));
     if (PyErr_Occurred()) return nullptr;
     Py_RETURN_NONE;
 }
@@ -308,6 +495,9 @@ PyMethodDef g_methods[] = {{"bind", CREDIT_FAST(py_bind), nullptr},
                            {"dropout", CREDIT_FAST(py_dropout), nullptr},
                            {"norm_forward", CREDIT_FAST(py_forward), nullptr},
                            {"norm_backward", CREDIT_FAST(py_backward), nullptr},
+                           {"linear_ce_forward", CREDIT_FAST(py_ce_forward), nullptr},
+                           {"linear_ce_backward", CREDIT_FAST(py_ce_backward), nullptr},
+                           {"gradients", CREDIT_FAST(py_gradients), nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "credit_train_torch", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,82 @@
+// vocab.h -- the linear head's cross entropy: launch arguments and launchers.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+namespace credit {
+
+constexpr int kTileM = 128;   // rows of an output tile
+constexpr int kTileN = 256;   // columns
+constexpr int kTileK = 64;    // k of a stage
+
+// A matrix of bf16 terms: `terms` planes of rows x cols, rows `pitch` bytes and
+// planes `plane` bytes apart, all 16-byte aligned.
+struct TermMatrix {
+    const void* p;
+    int64_t rows, cols, pitch, plane;
+    int terms;
+};
+
+// The tiles of one matrix product, C = A B summed over k.
+struct TileWork {
+    int32_t mt, nt;        // tiles of C
+    int32_t splits;        // parts of k, each summed apart
+    int32_t kb, per;       // stages of k in all, and in a part
+    int32_t group;         // tile rows that are walked together
+    int32_t a_mn, b_mn;    // operand lies with M (N) innermost
+    int32_t b_y0;          // first row of B's matrix
+};
+
+// Where a product goes: rows x cols at `out` (of the call's type), or the
+// fp32 sums of its splits, rows x pitch each.
+struct ProductOut {
+    void* out;
+    float* sums;
+    int64_t pitch;         // elements
+    int32_t rows, cols;
+    int32_t add;           // to what the sums hold
+    int32_t vec;           // rows of `out` are whole 16-byte lines
+};
+
+struct VocabArgs {
+    TileWork work[2];
+    int32_t jobs, pairs;   // products, and pairs of terms of each
+    int32_t rows, cols;    // tokens, vocabulary rows of this piece
+    int32_t v0;            // the piece's first vocabulary row
+    int64_t vocab;
+    const int64_t* target;
+    int64_t ignore;
+    // statistics: per (tile column, token) maximum and sum of exponentials, and
+    // the target's logit per token
+    float2* parts;
+    float* picked;
+    // gradient of the logits
+    const float* lse;
+    const float* dloss;
+    const float* dlse;     // or null
+    void* grad;            // terms planes, tokens x grad_pitch
+    int64_t grad_pitch, grad_plane;  // elements
+    ProductOut out[2];
+    unsigned* err;
+};
+
+enum VocabOut : int { kVocabStats, kVocabGrad, kVocabProduct };
+
+// `boxed`: rows of a box (K innermost: the tile's rows; else the stage's k).
+bool term_map(const TermMatrix& m, int box_rows, CUtensorMap* map);
+
+cudaError_t launch_vocab(VocabOut out, int dtype, const CUtensorMap (&maps)[4], const VocabArgs& a,
+                         int sms, cudaStream_t s);
+// loss and lse from the tiles' parts
+cudaError_t launch_vocab_merge(const VocabArgs& a, int tiles, float* loss, float* lse,
+                               cudaStream_t s);
+// rows x cols of the call's type as bf16 terms
+cudaError_t launch_vocab_pack(int dtype, const void* src, int64_t rows, int64_t cols, void* dst,
+                              int64_t pitch, int64_t plane, int sms, cudaStream_t s);
+// out = the splits' sums added in order
+cudaError_t launch_vocab_sum(int dtype, const float* sums, int splits, int64_t rows, int64_t cols,
+                             int64_t pitch, void* out, int sms, cudaStream_t s);
+
+}  // namespace credit

@@ -1,0 +1,344 @@
+// vocab_api.cu -- the C ABI of the linear head's cross entropy (see
+// include/credit.h): argument checks, the pieces of the vocabulary and their
+// workspace, and the launches.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "credit.h"
+#include "internal.h"
+#include "planner.h"
+#include "vocab.h"
+
+using namespace credit;
+
+namespace {
+
+bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+
+// Bytes of the logits' gradient that a piece of the vocabulary may take.
+constexpr int64_t kPieceBytes = (int64_t)256 << 20;
+// Most parts of a sum over the vocabulary.
+constexpr int kMaxSplits = 64;
+
+struct Shape {
+    int64_t tokens, hidden, vocab;
+    int dtype, es, terms;
+    bool pack_h, pack_w;   // the operand is copied as bf16 terms first
+};
+
+credit_status_t shape_of(const void* h, const void* w, int64_t tokens, int64_t hidden, int64_t vocab,
+                         credit_dtype_t dtype, Shape* s) {
+    if (tokens < 0 || hidden < 1 || vocab < 1) return CREDIT_ERR_INVALID_ARG;
+    if (dtype != CREDIT_F32 && dtype != CREDIT_BF16) return CREDIT_ERR_UNSUPPORTED;
+    // rows and columns are counted in 32 bits, tiles of 128 past them too
+    const int64_t most = ((int64_t)1 << 31) - 1024;
+    if (tokens > most || vocab > most || hidden > ((int64_t)1 << 24)) return CREDIT_ERR_INVALID_ARG;
+    const int64_t tiles = ceil_div(tokens, kTileM) * ceil_div(vocab, kTileN);
+    if (tiles > ((int64_t)1 << 30)) return CREDIT_ERR_INVALID_ARG;
+    s->tokens = tokens;
+    s->hidden = hidden;
+    s->vocab = vocab;
+    s->dtype = (int)dtype;
+    s->es = dtype == CREDIT_F32 ? 4 : 2;
+    s->terms = dtype == CREDIT_F32 ? 3 : 1;
+    if (!aligned(h, s->es) || !aligned(w, s->es)) return CREDIT_ERR_INVALID_ARG;
+    const bool lines = hidden * s->es % 16 == 0;
+    s->pack_h = s->terms > 1 || !lines || !aligned(h, 16);
+    s->pack_w = s->terms > 1 || !lines || !aligned(w, 16);
+    return CREDIT_OK;
+}
+
+// An operand of the call as the tensor maps see it, packed to `at` or not.
+TermMatrix operand(const Shape& s, const void* p, int64_t rows, bool pack, char* at) {
+    const int64_t pitch = pack ? round_up(s.hidden, 8) * 2 : s.hidden * 2;
+    return {pack ? at : p, rows, s.hidden, pitch, pitch * rows, s.terms};
+}
+int64_t operand_bytes(const Shape& s, int64_t rows, bool pack) {
+    return pack ? round_up(s.hidden, 8) * 2 * rows * s.terms : 0;
+}
+
+// The workspace of a call, in the order of its parts.
+struct Layout {
+    int64_t h, w, parts, picked, grad, sums, bytes;  // offsets
+    int64_t piece;      // vocabulary rows at a time
+    int32_t pieces, splits, per;
+    int64_t sums_pitch;
+    void place(int64_t* at, int64_t n) {
+        *at = bytes;
+        bytes += round_up(n, 256);
+    }
+};
+
+Layout forward_layout(const Shape& s) {
+    Layout l{};
+    l.place(&l.h, operand_bytes(s, s.tokens, s.pack_h));
+    l.place(&l.w, operand_bytes(s, s.vocab, s.pack_w));
+    l.place(&l.parts, ceil_div(s.vocab, kTileN) * s.tokens * 8);
+    l.place(&l.picked, s.tokens * 4);
+    return l;
+}
+
+// The vocabulary is walked in equal pieces whose logits' gradient fits
+// kPieceBytes; the sum over a piece that dhidden takes is split where its
+// tiles alone would not fill the SMs.
+Layout backward_layout(const Shape& s, bool dh, bool dw, int sms) {
+    Layout l{};
+    l.place(&l.h, operand_bytes(s, s.tokens, s.pack_h));
+    l.place(&l.w, operand_bytes(s, s.vocab, s.pack_w));
+    const int64_t most = std::max<int64_t>(kTileN, kPieceBytes / (s.tokens * 2 * s.terms) / kTileN * kTileN);
+    l.pieces = (int32_t)ceil_div(s.vocab, most);
+    l.piece = round_up(ceil_div(s.vocab, l.pieces), kTileN);
+    l.pieces = (int32_t)ceil_div(s.vocab, l.piece);
+    l.place(&l.grad, s.tokens * l.piece * 2 * s.terms);
+    l.splits = 1;
+    const int64_t kb = ceil_div(std::min(l.piece, s.vocab), kTileK);
+    l.per = (int32_t)kb;
+    if (dh) {
+        const int64_t nt = ceil_div(s.hidden, kTileN), tiles = ceil_div(s.tokens, kTileM) * nt;
+        // stages of all products over the SMs: a part of k is at most half of that
+        int64_t all = tiles * kb;
+        if (dw) all += ceil_div(l.piece, kTileM) * nt * ceil_div(s.tokens, kTileK);
+        const int64_t share = std::max<int64_t>(16, ceil_div(all, 2 * sms));
+        const int64_t want = std::min<int64_t>({ceil_div(kb, share), kMaxSplits, kb});
+        if (want > 1) {
+            l.per = (int32_t)ceil_div(kb, want);
+            l.splits = (int32_t)ceil_div(kb, l.per);
+        }
+        l.sums_pitch = round_up(s.hidden, 4);
+        if (l.splits > 1 || l.pieces > 1) l.place(&l.sums, l.splits * s.tokens * l.sums_pitch * 4);
+    }
+    return l;
+}
+
+credit_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? CREDIT_OK : CREDIT_ERR_CUDA; }
+
+credit_status_t device(const DevInfo** info) {
+    int dev;
+    if (cudaGetDevice(&dev) != cudaSuccess) { cudaGetLastError(); return CREDIT_ERR_CUDA; }
+    *info = device_info(dev);
+    return *info ? CREDIT_OK : CREDIT_ERR_CUDA;
+}
+
+struct Span {
+    const void* p;
+    uint64_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    return a.p && b.p && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+}
+// Every output is disjoint from every input and every other output.
+bool disjoint(const Span* in, int nin, const Span* out, int nout) {
+    for (int i = 0; i < nout; ++i) {
+        for (int j = 0; j < nin; ++j)
+            if (overlap(out[i], in[j])) return false;
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return false;
+    }
+    return true;
+}
+
+// Tile rows walked together: their operand rows stay in L2 while the other
+// operand's pass by.
+int32_t group_of(int64_t mt) { return (int32_t)std::min<int64_t>(mt, 16); }
+
+TileWork work_of(int64_t m, int64_t n, int64_t k, bool a_mn, bool b_mn) {
+    TileWork w{};
+    w.mt = (int32_t)ceil_div(m, kTileM);
+    w.nt = (int32_t)ceil_div(n, kTileN);
+    w.splits = 1;
+    w.kb = w.per = (int32_t)ceil_div(k, kTileK);
+    w.group = group_of(w.mt);
+    w.a_mn = a_mn;
+    w.b_mn = b_mn;
+    return w;
+}
+
+cudaError_t pack(const Shape& s, const void* src, const TermMatrix& m, int sms, cudaStream_t stream) {
+    return launch_vocab_pack(s.dtype, src, m.rows, m.cols, const_cast<void*>(m.p), m.pitch / 2,
+                             m.plane / 2, sms, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+credit_status_t credit_linear_ce_workspace(int backward, const void* hidden, const void* weight,
+                                           int64_t tokens, int64_t hidden_size, int64_t vocab,
+                                           credit_dtype_t dtype, int device, size_t* bytes) {
+    if (!bytes) return CREDIT_ERR_INVALID_ARG;
+    Shape s;
+    const credit_status_t st = shape_of(hidden, weight, tokens, hidden_size, vocab, dtype, &s);
+    if (st != CREDIT_OK) return st;
+    *bytes = 0;
+    if (tokens == 0) return CREDIT_OK;
+    if (!backward) {
+        *bytes = (size_t)forward_layout(s).bytes;
+        return CREDIT_OK;
+    }
+    const DevInfo* d = device_info(device);
+    if (!d) return CREDIT_ERR_CUDA;
+    // (whichever gradients are asked for)
+    *bytes = (size_t)std::max(backward_layout(s, true, true, d->sms).bytes,
+                              backward_layout(s, true, false, d->sms).bytes);
+    return CREDIT_OK;
+}
+
+credit_status_t credit_linear_ce_forward(const void* hidden, const void* weight,
+                                         const int64_t* target, int64_t ignore_index, float* loss,
+                                         float* lse, int64_t tokens, int64_t hidden_size,
+                                         int64_t vocab, credit_dtype_t dtype, void* workspace,
+                                         size_t workspace_bytes, void* stream) {
+    Shape s;
+    credit_status_t st = shape_of(hidden, weight, tokens, hidden_size, vocab, dtype, &s);
+    if (st != CREDIT_OK) return st;
+    if (tokens == 0) return CREDIT_OK;
+    if (!hidden || !weight || !target || !loss || !lse) return CREDIT_ERR_INVALID_ARG;
+    if (!aligned(target, 8) || !aligned(loss, 4) || !aligned(lse, 4)) return CREDIT_ERR_INVALID_ARG;
+    const uint64_t hb = (uint64_t)(tokens * hidden_size) * s.es, wb = (uint64_t)(vocab * hidden_size) * s.es;
+    const Span in[] = {{hidden, hb}, {weight, wb}, {target, (uint64_t)tokens * 8}};
+    const Span out[] = {{loss, (uint64_t)tokens * 4}, {lse, (uint64_t)tokens * 4},
+                        {workspace, workspace ? workspace_bytes : 0}};
+    if (!disjoint(in, 3, out, 3)) return CREDIT_ERR_INVALID_ARG;
+    const Layout l = forward_layout(s);
+    if (!workspace || workspace_bytes < (uint64_t)l.bytes || !aligned(workspace, 16))
+        return CREDIT_ERR_INVALID_ARG;
+    const DevInfo* d;
+    st = device(&d);
+    if (st != CREDIT_OK) return st;
+    unsigned* err = device_error_word();
+    if (!err) return CREDIT_ERR_CUDA;
+    cudaStream_t q = (cudaStream_t)stream;
+    char* const ws = static_cast<char*>(workspace);
+    const TermMatrix h = operand(s, hidden, tokens, s.pack_h, ws + l.h);
+    const TermMatrix w = operand(s, weight, vocab, s.pack_w, ws + l.w);
+    CUtensorMap maps[4] = {};
+    if (!term_map(h, kTileM, &maps[0]) || !term_map(w, kTileN, &maps[1])) return CREDIT_ERR_CUDA;
+    if (s.pack_h && (st = from_cuda(pack(s, hidden, h, d->sms, q))) != CREDIT_OK) return st;
+    if (s.pack_w && (st = from_cuda(pack(s, weight, w, d->sms, q))) != CREDIT_OK) return st;
+    VocabArgs a{};
+    a.jobs = 1;
+    a.pairs = s.terms == 1 ? 1 : 6;
+    a.work[0] = work_of(tokens, vocab, hidden_size, false, false);
+    a.rows = (int32_t)tokens;
+    a.cols = (int32_t)vocab;
+    a.vocab = vocab;
+    a.target = target;
+    a.ignore = ignore_index;
+    a.parts = reinterpret_cast<float2*>(ws + l.parts);
+    a.picked = reinterpret_cast<float*>(ws + l.picked);
+    a.err = err;
+    if ((st = from_cuda(launch_vocab(kVocabStats, s.dtype, maps, a, d->sms, q))) != CREDIT_OK) return st;
+    return from_cuda(launch_vocab_merge(a, a.work[0].nt, loss, lse, q));
+}
+
+credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse, const void* hidden,
+                                          const void* weight, const int64_t* target,
+                                          int64_t ignore_index, const float* lse, void* dhidden,
+                                          void* dweight, int64_t tokens, int64_t hidden_size,
+                                          int64_t vocab, credit_dtype_t dtype, void* workspace,
+                                          size_t workspace_bytes, void* stream) {
+    Shape s;
+    credit_status_t st = shape_of(hidden, weight, tokens, hidden_size, vocab, dtype, &s);
+    if (st != CREDIT_OK) return st;
+    cudaStream_t q = (cudaStream_t)stream;
+    const uint64_t hb = (uint64_t)(tokens * hidden_size) * s.es, wb = (uint64_t)(vocab * hidden_size) * s.es;
+    if (!aligned(dhidden, s.es) || !aligned(dweight, s.es)) return CREDIT_ERR_INVALID_ARG;
+    if (!dhidden && !dweight) return CREDIT_OK;
+    if (tokens == 0) return dweight ? from_cuda(cudaMemsetAsync(dweight, 0, wb, q)) : CREDIT_OK;
+    if (!dloss || !hidden || !weight || !target || !lse) return CREDIT_ERR_INVALID_ARG;
+    if (!aligned(dloss, 4) || !aligned(dlse, 4) || !aligned(target, 8) || !aligned(lse, 4))
+        return CREDIT_ERR_INVALID_ARG;
+    const uint64_t tb = (uint64_t)tokens * 4;
+    const Span in[] = {{hidden, hb}, {weight, wb}, {target, 2 * tb}, {dloss, tb}, {dlse, tb}, {lse, tb}};
+    const Span out[] = {{dhidden, hb}, {dweight, wb}, {workspace, workspace ? workspace_bytes : 0}};
+    if (!disjoint(in, 6, out, 3)) return CREDIT_ERR_INVALID_ARG;
+    const DevInfo* d;
+    st = device(&d);
+    if (st != CREDIT_OK) return st;
+    const Layout l = backward_layout(s, dhidden != nullptr, dweight != nullptr, d->sms);
+    if (!workspace || workspace_bytes < (uint64_t)l.bytes || !aligned(workspace, 16))
+        return CREDIT_ERR_INVALID_ARG;
+    unsigned* err = device_error_word();
+    if (!err) return CREDIT_ERR_CUDA;
+    char* const ws = static_cast<char*>(workspace);
+    const TermMatrix h = operand(s, hidden, tokens, s.pack_h, ws + l.h);
+    const TermMatrix w = operand(s, weight, vocab, s.pack_w, ws + l.w);
+    if (s.pack_h && (st = from_cuda(pack(s, hidden, h, d->sms, q))) != CREDIT_OK) return st;
+    if (s.pack_w && (st = from_cuda(pack(s, weight, w, d->sms, q))) != CREDIT_OK) return st;
+
+    // the logits' products, and what their gradient is multiplied with
+    CUtensorMap logits[4] = {}, products[4] = {};
+    if (!term_map(h, kTileM, &logits[0]) || !term_map(w, kTileN, &logits[1])) return CREDIT_ERR_CUDA;
+    const bool sums = l.splits > 1 || l.pieces > 1;
+    for (int p = 0; p < l.pieces; ++p) {
+        const int64_t v0 = p * l.piece, pv = std::min(l.piece, vocab - v0);
+        VocabArgs a{};
+        a.jobs = 1;
+        a.pairs = s.terms == 1 ? 1 : 6;
+        a.work[0] = work_of(tokens, pv, hidden_size, false, false);
+        a.work[0].b_y0 = (int32_t)v0;
+        a.rows = (int32_t)tokens;
+        a.cols = (int32_t)pv;
+        a.v0 = (int32_t)v0;
+        a.vocab = vocab;
+        a.target = target;
+        a.ignore = ignore_index;
+        a.lse = lse;
+        a.dloss = dloss;
+        a.dlse = dlse;
+        a.grad = ws + l.grad;
+        a.grad_pitch = l.piece;
+        a.grad_plane = l.piece * tokens;
+        a.err = err;
+        if ((st = from_cuda(launch_vocab(kVocabGrad, s.dtype, logits, a, d->sms, q))) != CREDIT_OK)
+            return st;
+        const TermMatrix g{ws + l.grad, tokens, pv, l.piece * 2, l.piece * tokens * 2, s.terms};
+        a.jobs = 0;
+        if (dhidden) {
+            // (a piece starts at a whole stage of k, and past its end g is zero)
+            TileWork& k = a.work[0] = work_of(tokens, hidden_size, pv, false, true);
+            k.b_y0 = (int32_t)v0;
+            k.per = std::min(l.per, k.kb);
+            k.splits = l.splits;
+            // a shorter last piece may leave parts without a stage: they add nothing
+            k.splits = (int32_t)ceil_div(k.kb, k.per);
+            ProductOut& o = a.out[0];
+            o.out = dhidden;
+            o.sums = sums ? reinterpret_cast<float*>(ws + l.sums) : nullptr;
+            o.pitch = sums ? l.sums_pitch : hidden_size;
+            o.rows = (int32_t)tokens;
+            o.cols = (int32_t)hidden_size;
+            o.add = p > 0;
+            o.vec = aligned(dhidden, 16) && hidden_size * s.es % 16 == 0;
+            if (!term_map(g, kTileM, &products[0]) || !term_map(w, kTileK, &products[1]))
+                return CREDIT_ERR_CUDA;
+            a.jobs = 1;
+        }
+        if (dweight) {
+            const int j = a.jobs++;
+            a.work[j] = work_of(pv, hidden_size, tokens, true, true);
+            ProductOut& o = a.out[j];
+            o = ProductOut{};
+            o.out = static_cast<char*>(dweight) + v0 * hidden_size * s.es;
+            o.pitch = hidden_size;
+            o.rows = (int32_t)pv;
+            o.cols = (int32_t)hidden_size;
+            o.vec = aligned(dweight, 16) && hidden_size * s.es % 16 == 0;
+            if (!term_map(g, kTileK, &products[2 * j]) || !term_map(h, kTileK, &products[2 * j + 1]))
+                return CREDIT_ERR_CUDA;
+        }
+        if ((st = from_cuda(launch_vocab(kVocabProduct, s.dtype, products, a, d->sms, q))) != CREDIT_OK)
+            return st;
+    }
+    if (dhidden && sums)
+        return from_cuda(launch_vocab_sum(s.dtype, reinterpret_cast<float*>(ws + l.sums), l.splits,
+                                          tokens, hidden_size, l.sums_pitch, dhidden, d->sms, q));
+    return CREDIT_OK;
+}
+
+}  // extern "C"

@@ -1,5 +1,6 @@
 """The training operators on torch tensors: dropout, the norms' forward pass
-with residual add, dropout and saved statistics, and its gradient.
+with residual add, dropout and saved statistics, and its gradient; the linear
+head's cross entropy, and its gradient; the norm of all gradients, and clipping.
 
 The functions here carry the arguments' meaning; a small extension
 (csrc/train_torch.cpp) checks the tensors, allocates outputs and workspace from
@@ -50,7 +51,9 @@ def _bind():
         _ext = _load()
     _ext.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
                 for f in ("credit_dropout", "credit_norm_workspace", "credit_norm_forward",
-                          "credit_norm_backward")))
+                          "credit_norm_backward", "credit_linear_ce_workspace",
+                          "credit_linear_ce_forward", "credit_linear_ce_backward",
+                          "credit_grad_workspace", "credit_grad_norm", "credit_grad_clip")))
     _bound = lib
 
 
@@ -173,3 +176,60 @@ def rmsnorm_backward(dy, h, rstd, weight=None, dh=None, dropout: Dropout | None 
     dweight)."""
     return _norm_backward(C.RMSNORM, dy, h, None, rstd, weight, dh, dropout, need_dresidual, dx,
                           dresidual, workspace)[:3]
+
+
+def linear_cross_entropy_forward(hidden, weight, target, ignore_index: int = -100, workspace=None):
+    """Softmax cross entropy of the logits hidden @ weight.T, which are never
+    stored: returns (loss, lse), fp32, one per token.  lse is the logarithm of the
+    sum of the logits' exponentials, loss is lse less the target's logit, and 0
+    where the target is `ignore_index`.  hidden is (..., hidden size), weight
+    (vocabulary, hidden size), target int64 (...); the caller takes the mean, or a
+    sum of its own weights.  A target outside the vocabulary that is not
+    ignore_index gives NaN."""
+    if C._lib is not _bound or _bound is None:
+        _bind()
+    r = _ext.linear_ce_forward(hidden, weight, target, ignore_index, workspace)
+    if type(r) is int:
+        raise CreditError(r, "credit_linear_ce_forward")
+    return r
+
+
+def linear_cross_entropy_backward(dloss, hidden, weight, target, lse, dlse=None,
+                                  ignore_index: int = -100, need_dhidden: bool = True,
+                                  need_dweight: bool = True, dhidden=None, dweight=None,
+                                  workspace=None):
+    """The gradient of linear_cross_entropy_forward: from dloss (of each token's
+    loss; of an ignored one it does not count) and dlse (of its lse, or None),
+    returns (dhidden, dweight).  One that is not needed is None, unless a tensor
+    for it is given in `dhidden` or `dweight`."""
+    if C._lib is not _bound or _bound is None:
+        _bind()
+    r = _ext.linear_ce_backward(dloss, hidden, weight, target, lse, dlse, ignore_index,
+                                need_dhidden, need_dweight, dhidden, dweight, workspace)
+    if type(r) is int:
+        raise CreditError(r, "credit_linear_ce_backward")
+    return r
+
+
+def gradient_norm(gradients, workspace=None):
+    """The 2-norm of all elements of a list of tensors (fp32 and bf16, any dense
+    strides, one device), a fp32 tensor of no dimensions on their device."""
+    if C._lib is not _bound or _bound is None:
+        _bind()
+    r = _ext.gradients(gradients, None, False, 0.0, 0.0, workspace)
+    if type(r) is int:
+        raise CreditError(r, "credit_grad_norm")
+    return r[0]
+
+
+def clip_gradients(gradients, max_norm: float, eps: float = 1e-6, out=None, workspace=None):
+    """Scale a list of tensors by min(1, max_norm / (norm + eps)), in place or into
+    the tensors of `out`, and return their norm before that, as gradient_norm does.
+    Nothing waits for the GPU.  A norm that is not finite is the caller's to look
+    at: an infinite one makes the factor 0, a NaN makes it NaN."""
+    if C._lib is not _bound or _bound is None:
+        _bind()
+    r = _ext.gradients(gradients, out, True, max_norm, eps, workspace)
+    if type(r) is int:
+        raise CreditError(r, "credit_grad_clip")
+    return r[0]

@@ -375,6 +375,109 @@ credit_status_t credit_norm_backward(credit_op_t op, const void *dy, const void 
                                      void *stream);
 
 /*
+ * ---- The linear head's cross entropy, without the logits, and its gradient ----
+ *
+ *     z = hidden weight^T,   lse_t = log sum_v exp(z_tv),
+ *     loss_t = lse_t - z_t,target(t)        (0 where target(t) is ignore_index)
+ *
+ *     g_tv = (dloss_t + dlse_t) exp(z_tv - lse_t) - dloss_t [v = target(t)]
+ *     dhidden = g weight,   dweight = g^T hidden
+ *
+ * (dloss_t counts as 0 where the target is ignored, dlse_t does not).  hidden is
+ * tokens x hidden_size, weight vocab x hidden_size, both of `dtype` and
+ * contiguous; tokens == 0 is a legal empty batch.  The tokens x vocab logits are
+ * formed a tile at a time by the tensor cores and reduced there: the forward
+ * pass keeps a maximum and a sum per token and tile of 256 columns, the backward
+ * pass the gradient of one piece of the vocabulary at a time (bf16 operands:
+ * rounded to bf16).  fp32 operands are taken apart into three bf16 terms each
+ * and multiplied in six products, which keeps 24 bits; an infinite fp32 value
+ * gives NaN.  Sums are fp32, every output is rounded once, and results repeat
+ * bit for bit.
+ *
+ * Operands whose rows are not whole 16-byte lines at 16-byte addresses, and fp32
+ * ones, are copied into the workspace first.  A target outside [0, vocab) that
+ * is not ignore_index gives its token a NaN loss and gradient.  Each call works
+ * entirely on `stream` and may be captured; a workspace is used by one call at a
+ * time.
+ */
+
+/*
+ * Device workspace of a forward (backward = 0) or backward (1) call, in bytes.
+ * Of the pointers only the alignment counts.  Host only.
+ */
+credit_status_t credit_linear_ce_workspace(int backward, const void *hidden,
+                                           const void *weight, int64_t tokens,
+                                           int64_t hidden_size, int64_t vocab,
+                                           credit_dtype_t dtype, int device,
+                                           size_t *bytes);
+
+/*
+ *   target      device, one int64 per token
+ *   loss, lse   device, fp32 out, one per token
+ *   workspace   16-byte aligned, credit_linear_ce_workspace bytes
+ * No output overlaps another buffer.
+ */
+credit_status_t credit_linear_ce_forward(const void *hidden, const void *weight,
+                                         const int64_t *target, int64_t ignore_index,
+                                         float *loss, float *lse, int64_t tokens,
+                                         int64_t hidden_size, int64_t vocab,
+                                         credit_dtype_t dtype, void *workspace,
+                                         size_t workspace_bytes, void *stream);
+
+/*
+ *   dloss       device, fp32, the gradient of each token's loss
+ *   dlse        the same of lse, or NULL (none)
+ *   lse         the forward pass's
+ *   dhidden     out, like hidden; dweight  out, like weight; NULL: not wanted
+ * No output overlaps another buffer.
+ */
+credit_status_t credit_linear_ce_backward(const float *dloss, const float *dlse,
+                                          const void *hidden, const void *weight,
+                                          const int64_t *target, int64_t ignore_index,
+                                          const float *lse, void *dhidden, void *dweight,
+                                          int64_t tokens, int64_t hidden_size,
+                                          int64_t vocab, credit_dtype_t dtype,
+                                          void *workspace, size_t workspace_bytes,
+                                          void *stream);
+
+/*
+ * ---- The norm of all gradients together, and clipping ----
+ *
+ *     norm = sqrt(sum over tensors and elements of g^2)
+ *     out  = g min(1, max_norm / (norm + eps))
+ *
+ * A tensor is `count` elements of `dtype` at `data` (any order: nothing depends
+ * on a shape), fp32 and bf16 in one call.  `out` may be `data` (in place) or
+ * hold no byte of any other buffer of the call; the norm alone does not look at it.  The norm is right for
+ * every magnitude of finite elements, up to fp32's own range.  Where it is not
+ * finite the formula holds: an infinite norm gives 0 (NaN for the infinite
+ * elements), a NaN gives NaN.  In place a factor of 1 writes nothing.  Results
+ * repeat bit for bit.  The tensors' addresses are part of the launches: the
+ * array may be freed after the call, and a captured call works on the same
+ * tensors at each replay.
+ */
+typedef struct {
+    const void *data;
+    void *out;
+    int64_t count;
+    credit_dtype_t dtype;
+} credit_tensor_t;
+
+/* Device workspace of a call on these tensors, in bytes (0 without elements). */
+credit_status_t credit_grad_workspace(const credit_tensor_t *tensors, int64_t n,
+                                      int device, size_t *bytes);
+
+/*   norm        device, one fp32 value out
+ *   workspace   16-byte aligned, credit_grad_workspace bytes */
+credit_status_t credit_grad_norm(const credit_tensor_t *tensors, int64_t n, float *norm,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+
+/*   max_norm, eps  >= 0 */
+credit_status_t credit_grad_clip(const credit_tensor_t *tensors, int64_t n, float max_norm,
+                                 float eps, float *norm, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/*
  * Two-pass call that needs no workspace and allocates no device memory.
  * The CREDIT paper has no counterpart to this entry point; it exists for
  * callers that cannot allocate: programs that gave all device memory to their
