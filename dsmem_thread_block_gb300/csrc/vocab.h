@@ -7,9 +7,18 @@
 
 namespace credit {
 
-constexpr int kTileM = 128;   // rows of an output tile
-constexpr int kTileN = 256;   // columns
+constexpr int kTileM = 128;   // rows of a CTA's output tile
 constexpr int kTileK = 64;    // k of a stage
+
+// The output tile of a CTA or pair of CTAs: rows x columns.
+enum VocabTile : int {
+    kPair256,   // 256 x 256, a pair
+    kOne128,    // 128 x 128
+    kOne64,     // 128 x 64
+};
+constexpr int vocab_tile_rows(VocabTile t) { return t == kPair256 ? 2 * kTileM : kTileM; }
+constexpr int vocab_tile_cols(VocabTile t) { return t == kPair256 ? 256 : t == kOne128 ? 128 : 64; }
+constexpr int vocab_tile_ctas(VocabTile t) { return t == kPair256 ? 2 : 1; }
 
 // A matrix of bf16 terms: `terms` planes of rows x cols, rows `pitch` bytes and
 // planes `plane` bytes apart, all 16-byte aligned.
@@ -27,6 +36,7 @@ struct TileWork {
     int32_t group;         // tile rows that are walked together
     int32_t a_mn, b_mn;    // operand lies with M (N) innermost
     int32_t b_y0;          // first row of B's matrix
+    int32_t a_bytes;       // of A that a CTA's stage receives
 };
 
 // Where a product goes: rows x cols at `out` (of the call's type), or the
@@ -43,12 +53,14 @@ struct ProductOut {
 struct VocabArgs {
     TileWork work[2];
     int32_t jobs, pairs;   // products, and pairs of terms of each
+    int32_t lead;          // rounds of the second product that some units start early
+    int32_t a_room;        // of A in a stage: a_bytes at least, a multiple of 1024
     int32_t rows, cols;    // tokens, vocabulary rows of this piece
     int32_t v0;            // the piece's first vocabulary row
     int64_t vocab;
     const int64_t* target;
     int64_t ignore;
-    // statistics: per (tile column, token) maximum and sum of exponentials, and
+    // statistics: per (half a tile's columns, token) maximum and sum of exponentials, and
     // the target's logit per token
     float2* parts;
     float* picked;
@@ -67,10 +79,14 @@ enum VocabOut : int { kVocabStats, kVocabGrad, kVocabProduct };
 // `boxed`: rows of a box (K innermost: the tile's rows; else the stage's k).
 bool term_map(const TermMatrix& m, int box_rows, CUtensorMap* map);
 
-cudaError_t launch_vocab(VocabOut out, int dtype, const CUtensorMap (&maps)[4], const VocabArgs& a,
-                         int sms, cudaStream_t s);
+const void* vocab_stats_kernel(VocabTile t);
+const void* vocab_grad_kernel(int dtype, VocabTile t);
+const void* vocab_product_kernel(int dtype, VocabTile t);
+
+cudaError_t launch_vocab(VocabOut out, int dtype, VocabTile tile, const CUtensorMap (&maps)[4],
+                         const VocabArgs& a, int sms, cudaStream_t s);
 // loss and lse from the tiles' parts
-cudaError_t launch_vocab_merge(const VocabArgs& a, int tiles, float* loss, float* lse,
+cudaError_t launch_vocab_merge(const VocabArgs& a, int parts, float* loss, float* lse,
                                cudaStream_t s);
 // rows x cols of the call's type as bf16 terms
 cudaError_t launch_vocab_pack(int dtype, const void* src, int64_t rows, int64_t cols, void* dst,

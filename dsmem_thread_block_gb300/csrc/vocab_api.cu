@@ -24,6 +24,11 @@ constexpr int64_t kPieceBytes = (int64_t)256 << 20;
 // Most parts of a sum over the vocabulary.
 constexpr int kMaxSplits = 64;
 
+// Widest tile: a piece of the vocabulary is whole tiles of any shape.
+constexpr int kTileN = vocab_tile_cols(kPair256);
+// Narrowest half tile: a part of the statistics.
+constexpr int kPartCols = vocab_tile_cols(kOne64) / 2;
+
 struct Shape {
     int64_t tokens, hidden, vocab;
     int dtype, es, terms;
@@ -37,8 +42,10 @@ credit_status_t shape_of(const void* h, const void* w, int64_t tokens, int64_t h
     // rows and columns are counted in 32 bits, tiles of 128 past them too
     const int64_t most = ((int64_t)1 << 31) - 1024;
     if (tokens > most || vocab > most || hidden > ((int64_t)1 << 24)) return CREDIT_ERR_INVALID_ARG;
-    const int64_t tiles = ceil_div(tokens, kTileM) * ceil_div(vocab, kTileN);
-    if (tiles > ((int64_t)1 << 30)) return CREDIT_ERR_INVALID_ARG;
+    // (tiles of a launch, too)
+    const int64_t tiles = ceil_div(tokens, kTileM) * ceil_div(vocab, kTileM);
+    const int64_t wide = ceil_div(std::max(tokens, vocab), kTileM) * ceil_div(hidden, kPartCols);
+    if (tiles > ((int64_t)1 << 28) || wide > ((int64_t)1 << 28)) return CREDIT_ERR_INVALID_ARG;
     s->tokens = tokens;
     s->hidden = hidden;
     s->vocab = vocab;
@@ -65,7 +72,7 @@ int64_t operand_bytes(const Shape& s, int64_t rows, bool pack) {
 struct Layout {
     int64_t h, w, parts, picked, grad, sums, bytes;  // offsets
     int64_t piece;      // vocabulary rows at a time
-    int32_t pieces, splits, per;
+    int32_t pieces;
     int64_t sums_pitch;
     void place(int64_t* at, int64_t n) {
         *at = bytes;
@@ -73,19 +80,80 @@ struct Layout {
     }
 };
 
-Layout forward_layout(const Shape& s) {
+// A tile's time in a launch, in stages of k of a 128 x 256 tile: its products, and
+// what a tile costs besides them.
+double tile_cost(VocabTile t, double stages) {
+    return stages * vocab_tile_cols(t) / 256 + 2.0;
+}
+// The shape whose tiles end first.
+VocabTile tile_for(int64_t rows, int64_t cols, int64_t stages, int sms) {
+    VocabTile best = kPair256;
+    double least = 0;
+    for (const VocabTile t : {kPair256, kOne128, kOne64}) {
+        const int64_t tiles = ceil_div(rows, vocab_tile_rows(t)) * ceil_div(cols, vocab_tile_cols(t));
+        const double time = (double)ceil_div(tiles, sms / vocab_tile_ctas(t)) * tile_cost(t, (double)stages);
+        if (t == kPair256 || time < 0.9 * least) {
+            best = t;
+            least = time;
+        }
+    }
+    return best;
+}
+
+VocabTile logits_tile(const Shape& s, int64_t cols, int sms) {
+    return tile_for(s.tokens, cols, ceil_div(s.hidden, kTileK) * (s.terms == 1 ? 1 : 6), sms);
+}
+
+Layout forward_layout(const Shape& s, VocabTile t) {
     Layout l{};
     l.place(&l.h, operand_bytes(s, s.tokens, s.pack_h));
     l.place(&l.w, operand_bytes(s, s.vocab, s.pack_w));
-    l.place(&l.parts, ceil_div(s.vocab, kTileN) * s.tokens * 8);
+    l.place(&l.parts, 2 * ceil_div(s.vocab, vocab_tile_cols(t)) * s.tokens * 8);
     l.place(&l.picked, s.tokens * 4);
     return l;
 }
 
-// The vocabulary is walked in equal pieces whose logits' gradient fits
-// kPieceBytes; the sum over a piece that dhidden takes is split where its
-// tiles alone would not fill the SMs.
-Layout backward_layout(const Shape& s, bool dh, bool dw, int sms) {
+// The two products of a piece of the vocabulary in one launch: the tiles' shape and
+// the parts of the sum over the piece that dhidden takes.  Where its tiles alone
+// would keep SMs waiting, a part is at most half of what each SM has to do.
+struct Products {
+    VocabTile tile;
+    int32_t splits, per;
+};
+Products products_for(const Shape& s, int64_t piece, bool dh, bool dw, int sms) {
+    Products best{};
+    double least = 0;
+    const int64_t kb = ceil_div(piece, kTileK), kt = ceil_div(s.tokens, kTileK);
+    const int pairs = s.terms == 1 ? 1 : 6;
+    for (const VocabTile t : {kPair256, kOne128, kOne64}) {
+        const int rows = vocab_tile_rows(t), cols = vocab_tile_cols(t), units = sms / vocab_tile_ctas(t);
+        const int64_t nt = ceil_div(s.hidden, cols);
+        const int64_t th = dh ? ceil_div(s.tokens, rows) * nt : 0, tw = dw ? ceil_div(piece, rows) * nt : 0;
+        const double all = (double)th * tile_cost(t, (double)(kb * pairs)) +
+                           (double)tw * tile_cost(t, (double)(kt * pairs));
+        Products p{t, 1, (int32_t)kb};
+        double time = all / units;
+        if (dh) {
+            const double stage = (double)pairs * cols / 256;
+            const int64_t share = std::max<int64_t>(16, (int64_t)(all / units / 2 / stage));
+            const int64_t want = std::min<int64_t>(ceil_div(kb, share), kMaxSplits);
+            p.per = (int32_t)ceil_div(kb, want);
+            p.splits = (int32_t)ceil_div(kb, p.per);
+            const double part = tile_cost(t, (double)p.per * pairs);
+            time = dw ? std::max(time, part) : (double)ceil_div(th * p.splits, units) * part;
+        } else {
+            time = (double)ceil_div(tw, units) * tile_cost(t, (double)(kt * pairs));
+        }
+        if (t == kPair256 || time < 0.9 * least) {
+            best = p;
+            least = time;
+        }
+    }
+    return best;
+}
+
+// The vocabulary is walked in equal pieces whose logits' gradient fits kPieceBytes.
+Layout backward_layout(const Shape& s, bool dh, bool dw, int sms, Products* products) {
     Layout l{};
     l.place(&l.h, operand_bytes(s, s.tokens, s.pack_h));
     l.place(&l.w, operand_bytes(s, s.vocab, s.pack_w));
@@ -94,23 +162,10 @@ Layout backward_layout(const Shape& s, bool dh, bool dw, int sms) {
     l.piece = round_up(ceil_div(s.vocab, l.pieces), kTileN);
     l.pieces = (int32_t)ceil_div(s.vocab, l.piece);
     l.place(&l.grad, s.tokens * l.piece * 2 * s.terms);
-    l.splits = 1;
-    const int64_t kb = ceil_div(std::min(l.piece, s.vocab), kTileK);
-    l.per = (int32_t)kb;
-    if (dh) {
-        const int64_t nt = ceil_div(s.hidden, kTileN), tiles = ceil_div(s.tokens, kTileM) * nt;
-        // stages of all products over the SMs: a part of k is at most half of that
-        int64_t all = tiles * kb;
-        if (dw) all += ceil_div(l.piece, kTileM) * nt * ceil_div(s.tokens, kTileK);
-        const int64_t share = std::max<int64_t>(16, ceil_div(all, 2 * sms));
-        const int64_t want = std::min<int64_t>({ceil_div(kb, share), kMaxSplits, kb});
-        if (want > 1) {
-            l.per = (int32_t)ceil_div(kb, want);
-            l.splits = (int32_t)ceil_div(kb, l.per);
-        }
-        l.sums_pitch = round_up(s.hidden, 4);
-        if (l.splits > 1 || l.pieces > 1) l.place(&l.sums, l.splits * s.tokens * l.sums_pitch * 4);
-    }
+    *products = products_for(s, std::min(l.piece, s.vocab), dh, dw, sms);
+    l.sums_pitch = round_up(s.hidden, 4);
+    if (dh && (products->splits > 1 || l.pieces > 1))
+        l.place(&l.sums, products->splits * s.tokens * l.sums_pitch * 4);
     return l;
 }
 
@@ -142,20 +197,28 @@ bool disjoint(const Span* in, int nin, const Span* out, int nout) {
     return true;
 }
 
-// Tile rows walked together: their operand rows stay in L2 while the other
-// operand's pass by.
-int32_t group_of(int64_t mt) { return (int32_t)std::min<int64_t>(mt, 16); }
-
-TileWork work_of(int64_t m, int64_t n, int64_t k, bool a_mn, bool b_mn) {
+// Tiles of a product of rows x cols.  Tile rows are walked together in groups of
+// 2048 rows, which stay in L2 while the other operand's pass by.
+TileWork work_of(VocabTile t, int64_t rows, int64_t cols, int64_t k, bool a_mn, bool b_mn) {
     TileWork w{};
-    w.mt = (int32_t)ceil_div(m, kTileM);
-    w.nt = (int32_t)ceil_div(n, kTileN);
+    w.mt = (int32_t)ceil_div(rows, vocab_tile_rows(t));
+    w.nt = (int32_t)ceil_div(cols, vocab_tile_cols(t));
     w.splits = 1;
     w.kb = w.per = (int32_t)ceil_div(k, kTileK);
-    w.group = group_of(w.mt);
+    w.group = std::min(w.mt, 2048 / vocab_tile_rows(t));
     w.a_mn = a_mn;
     w.b_mn = b_mn;
+    w.a_bytes = kTileM * kTileK * 2;
     return w;
+}
+
+// The rows of a box of A with K innermost: of a single tile only those there are
+// (the others of a stage keep what they held, and their products go nowhere).
+int box_rows(VocabTile t, int64_t rows, TileWork* w) {
+    int box = kTileM;
+    if (vocab_tile_ctas(t) == 1 && rows < kTileM) box = (int)round_up(rows, 8);
+    w->a_bytes = box * kTileK * 2;
+    return box;
 }
 
 cudaError_t pack(const Shape& s, const void* src, const TermMatrix& m, int sms, cudaStream_t stream) {
@@ -176,15 +239,15 @@ credit_status_t credit_linear_ce_workspace(int backward, const void* hidden, con
     if (st != CREDIT_OK) return st;
     *bytes = 0;
     if (tokens == 0) return CREDIT_OK;
-    if (!backward) {
-        *bytes = (size_t)forward_layout(s).bytes;
-        return CREDIT_OK;
-    }
     const DevInfo* d = device_info(device);
     if (!d) return CREDIT_ERR_CUDA;
-    // (whichever gradients are asked for)
-    *bytes = (size_t)std::max(backward_layout(s, true, true, d->sms).bytes,
-                              backward_layout(s, true, false, d->sms).bytes);
+    if (!backward) {
+        *bytes = (size_t)forward_layout(s, logits_tile(s, s.vocab, d->sms)).bytes;
+        return CREDIT_OK;
+    }
+    Products p;  // (whichever gradients are asked for)
+    *bytes = (size_t)std::max(backward_layout(s, true, true, d->sms, &p).bytes,
+                              backward_layout(s, true, false, d->sms, &p).bytes);
     return CREDIT_OK;
 }
 
@@ -204,26 +267,29 @@ credit_status_t credit_linear_ce_forward(const void* hidden, const void* weight,
     const Span out[] = {{loss, (uint64_t)tokens * 4}, {lse, (uint64_t)tokens * 4},
                         {workspace, workspace ? workspace_bytes : 0}};
     if (!disjoint(in, 3, out, 3)) return CREDIT_ERR_INVALID_ARG;
-    const Layout l = forward_layout(s);
-    if (!workspace || workspace_bytes < (uint64_t)l.bytes || !aligned(workspace, 16))
-        return CREDIT_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 16)) return CREDIT_ERR_INVALID_ARG;
     const DevInfo* d;
     st = device(&d);
     if (st != CREDIT_OK) return st;
+    const VocabTile tile = logits_tile(s, vocab, d->sms);
+    const Layout l = forward_layout(s, tile);
+    if (workspace_bytes < (uint64_t)l.bytes) return CREDIT_ERR_INVALID_ARG;
     unsigned* err = device_error_word();
     if (!err) return CREDIT_ERR_CUDA;
     cudaStream_t q = (cudaStream_t)stream;
     char* const ws = static_cast<char*>(workspace);
     const TermMatrix h = operand(s, hidden, tokens, s.pack_h, ws + l.h);
     const TermMatrix w = operand(s, weight, vocab, s.pack_w, ws + l.w);
-    CUtensorMap maps[4] = {};
-    if (!term_map(h, kTileM, &maps[0]) || !term_map(w, kTileN, &maps[1])) return CREDIT_ERR_CUDA;
-    if (s.pack_h && (st = from_cuda(pack(s, hidden, h, d->sms, q))) != CREDIT_OK) return st;
-    if (s.pack_w && (st = from_cuda(pack(s, weight, w, d->sms, q))) != CREDIT_OK) return st;
     VocabArgs a{};
     a.jobs = 1;
     a.pairs = s.terms == 1 ? 1 : 6;
-    a.work[0] = work_of(tokens, vocab, hidden_size, false, false);
+    a.work[0] = work_of(tile, tokens, vocab, hidden_size, false, false);
+    CUtensorMap maps[4] = {};
+    if (!term_map(h, box_rows(tile, tokens, &a.work[0]), &maps[0]) ||
+        !term_map(w, vocab_tile_cols(tile) / vocab_tile_ctas(tile), &maps[1]))
+        return CREDIT_ERR_CUDA;
+    if (s.pack_h && (st = from_cuda(pack(s, hidden, h, d->sms, q))) != CREDIT_OK) return st;
+    if (s.pack_w && (st = from_cuda(pack(s, weight, w, d->sms, q))) != CREDIT_OK) return st;
     a.rows = (int32_t)tokens;
     a.cols = (int32_t)vocab;
     a.vocab = vocab;
@@ -232,8 +298,9 @@ credit_status_t credit_linear_ce_forward(const void* hidden, const void* weight,
     a.parts = reinterpret_cast<float2*>(ws + l.parts);
     a.picked = reinterpret_cast<float*>(ws + l.picked);
     a.err = err;
-    if ((st = from_cuda(launch_vocab(kVocabStats, s.dtype, maps, a, d->sms, q))) != CREDIT_OK) return st;
-    return from_cuda(launch_vocab_merge(a, a.work[0].nt, loss, lse, q));
+    if ((st = from_cuda(launch_vocab(kVocabStats, s.dtype, tile, maps, a, d->sms, q))) != CREDIT_OK)
+        return st;
+    return from_cuda(launch_vocab_merge(a, 2 * a.work[0].nt, loss, lse, q));
 }
 
 credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse, const void* hidden,
@@ -260,7 +327,8 @@ credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse,
     const DevInfo* d;
     st = device(&d);
     if (st != CREDIT_OK) return st;
-    const Layout l = backward_layout(s, dhidden != nullptr, dweight != nullptr, d->sms);
+    Products products;
+    const Layout l = backward_layout(s, dhidden != nullptr, dweight != nullptr, d->sms, &products);
     if (!workspace || workspace_bytes < (uint64_t)l.bytes || !aligned(workspace, 16))
         return CREDIT_ERR_INVALID_ARG;
     unsigned* err = device_error_word();
@@ -271,17 +339,21 @@ credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse,
     if (s.pack_h && (st = from_cuda(pack(s, hidden, h, d->sms, q))) != CREDIT_OK) return st;
     if (s.pack_w && (st = from_cuda(pack(s, weight, w, d->sms, q))) != CREDIT_OK) return st;
 
-    // the logits' products, and what their gradient is multiplied with
-    CUtensorMap logits[4] = {}, products[4] = {};
-    if (!term_map(h, kTileM, &logits[0]) || !term_map(w, kTileN, &logits[1])) return CREDIT_ERR_CUDA;
-    const bool sums = l.splits > 1 || l.pieces > 1;
+    const bool sums = products.splits > 1 || l.pieces > 1;
+    const VocabTile pt = products.tile, gt = logits_tile(s, l.piece, d->sms);
+    // what the logits' gradient is formed from, and what it is multiplied with
+    CUtensorMap logits[4] = {}, operands[4] = {};
     for (int p = 0; p < l.pieces; ++p) {
         const int64_t v0 = p * l.piece, pv = std::min(l.piece, vocab - v0);
         VocabArgs a{};
         a.jobs = 1;
         a.pairs = s.terms == 1 ? 1 : 6;
-        a.work[0] = work_of(tokens, pv, hidden_size, false, false);
+        a.work[0] = work_of(gt, tokens, pv, hidden_size, false, false);
         a.work[0].b_y0 = (int32_t)v0;
+        const int box = box_rows(gt, tokens, &a.work[0]);
+        if (p == 0 && (!term_map(h, box, &logits[0]) ||
+                       !term_map(w, vocab_tile_cols(gt) / vocab_tile_ctas(gt), &logits[1])))
+            return CREDIT_ERR_CUDA;
         a.rows = (int32_t)tokens;
         a.cols = (int32_t)pv;
         a.v0 = (int32_t)v0;
@@ -295,17 +367,16 @@ credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse,
         a.grad_pitch = l.piece;
         a.grad_plane = l.piece * tokens;
         a.err = err;
-        if ((st = from_cuda(launch_vocab(kVocabGrad, s.dtype, logits, a, d->sms, q))) != CREDIT_OK)
+        if ((st = from_cuda(launch_vocab(kVocabGrad, s.dtype, gt, logits, a, d->sms, q))) != CREDIT_OK)
             return st;
         const TermMatrix g{ws + l.grad, tokens, pv, l.piece * 2, l.piece * tokens * 2, s.terms};
         a.jobs = 0;
         if (dhidden) {
             // (a piece starts at a whole stage of k, and past its end g is zero)
-            TileWork& k = a.work[0] = work_of(tokens, hidden_size, pv, false, true);
+            TileWork& k = a.work[0] = work_of(pt, tokens, hidden_size, pv, false, true);
             k.b_y0 = (int32_t)v0;
-            k.per = std::min(l.per, k.kb);
-            k.splits = l.splits;
-            // a shorter last piece may leave parts without a stage: they add nothing
+            // (a shorter last piece may leave parts without a stage: they add nothing)
+            k.per = std::min(products.per, k.kb);
             k.splits = (int32_t)ceil_div(k.kb, k.per);
             ProductOut& o = a.out[0];
             o.out = dhidden;
@@ -315,13 +386,13 @@ credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse,
             o.cols = (int32_t)hidden_size;
             o.add = p > 0;
             o.vec = aligned(dhidden, 16) && hidden_size * s.es % 16 == 0;
-            if (!term_map(g, kTileM, &products[0]) || !term_map(w, kTileK, &products[1]))
+            if (!term_map(g, box_rows(pt, tokens, &k), &operands[0]) || !term_map(w, kTileK, &operands[1]))
                 return CREDIT_ERR_CUDA;
             a.jobs = 1;
         }
         if (dweight) {
             const int j = a.jobs++;
-            a.work[j] = work_of(pv, hidden_size, tokens, true, true);
+            a.work[j] = work_of(pt, pv, hidden_size, tokens, true, true);
             ProductOut& o = a.out[j];
             o = ProductOut{};
             o.out = static_cast<char*>(dweight) + v0 * hidden_size * s.es;
@@ -329,14 +400,15 @@ credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse,
             o.rows = (int32_t)pv;
             o.cols = (int32_t)hidden_size;
             o.vec = aligned(dweight, 16) && hidden_size * s.es % 16 == 0;
-            if (!term_map(g, kTileK, &products[2 * j]) || !term_map(h, kTileK, &products[2 * j + 1]))
+            if (!term_map(g, kTileK, &operands[2 * j]) || !term_map(h, kTileK, &operands[2 * j + 1]))
                 return CREDIT_ERR_CUDA;
         }
-        if ((st = from_cuda(launch_vocab(kVocabProduct, s.dtype, products, a, d->sms, q))) != CREDIT_OK)
+        if ((st = from_cuda(launch_vocab(kVocabProduct, s.dtype, pt, operands, a, d->sms, q))) !=
+            CREDIT_OK)
             return st;
     }
     if (dhidden && sums)
-        return from_cuda(launch_vocab_sum(s.dtype, reinterpret_cast<float*>(ws + l.sums), l.splits,
+        return from_cuda(launch_vocab_sum(s.dtype, reinterpret_cast<float*>(ws + l.sums), products.splits,
                                           tokens, hidden_size, l.sums_pitch, dhidden, d->sms, q));
     return CREDIT_OK;
 }

@@ -1,0 +1,565 @@
+// vocab_tiles.cuh -- the tiled matrix products of the linear head's cross entropy:
+// a persistent kernel whose CTAs, or pairs of CTAs, walk output tiles; a warp
+// fills a ring of stages by tensor-map copies, a thread issues tcgen05 products
+// into one of two accumulators in tensor memory, and eight warps read the other
+// one out.
+//
+// Precision.  The tensor cores add into an fp32 accumulator without rounding to
+// nearest: a sum over k drifts towards zero by some 2^-25 of itself an addition of
+// sixteen products, 7e-6 over 4096.  A bf16 result does not see that.  Where the
+// result is fp32 (the statistics, and every product of fp32 operands) the
+// accumulator holds kPromote stages at a time, and the epilogue warps add these
+// parts in registers, which rounds to nearest; they do it while the next part is
+// multiplied.
+#pragma once
+
+#include <algorithm>
+#include <type_traits>
+
+#include "planner.h"
+#include "rowops.cuh"
+#include "tensor.cuh"
+#include "vocab.h"
+
+namespace credit {
+
+constexpr int kVocabWarps = 8;                  // of the epilogue: two a quarter of the rows
+constexpr int kVocabThreads = 32 * (kVocabWarps + 4);  // whole warpgroups; two warps only wait
+constexpr int kBoxBytes = 64 * kTileK * 2;      // one box of an operand with M or N innermost
+constexpr int kBytesA = kTileM * kTileK * 2;
+constexpr int kVocabRing = 6 * 32768;           // bytes of all stages
+constexpr int kVocabStages = 16;                // most of them
+constexpr int kStageOut = 32 * 128;             // a warp's room to turn its output around
+constexpr int kVocabSmem = kVocabRing + kVocabWarps * kStageOut + 1024;  // aligned to 1024 by hand
+constexpr int kPromote = 4;                     // stages of a part
+
+// A tile is 128 rows a CTA by N columns (CG = 2: a pair shares the columns'
+// operand, half of it each).
+template <int N, int CG> struct TileShape {
+    static constexpr int kRowsB = N / CG;       // of B a CTA stages
+    static constexpr int kBytesB = kRowsB * kTileK * 2;
+    static constexpr int kCols = N / 2;         // of an epilogue warp
+    static constexpr uint32_t kTmem = 2 * N;    // two accumulators
+};
+
+struct VocabBars {
+    uint64_t full[kVocabStages], empty[kVocabStages], acc_full[2], acc_empty[2], drained;
+};
+
+// Wait for a phase; false once a wait of this CTA has given up.
+__device__ __forceinline__ bool hold(uint64_t& bar, uint32_t parity, unsigned* err,
+                                     volatile int* dead) {
+    const uint32_t b = smem_u32(&bar);
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(b, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(b, parity)) {
+        if (*dead) return false;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            atomicOr(err, kErrTimeout);
+            *dead = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+// A tile of a launch: its product, corner and range of k.
+struct Tile {
+    int job, m0, n0, split, k0, kn;
+};
+__device__ __forceinline__ int tiles_of(const TileWork& w) { return w.mt * w.nt * w.splits; }
+
+// Tile i of unit u (a CTA or a pair) of `units`.  The first product's tiles go
+// round by round; units that get one less of them start `lead` rounds of the
+// second product's before the others join.
+template <int N, int CG>
+__device__ __forceinline__ bool tile_at(const VocabArgs& a, int u, int units, int rank, int i, Tile* r) {
+    const int n0 = tiles_of(a.work[0]), mine = n0 > u ? (n0 - u - 1) / units + 1 : 0;
+    int t;
+    r->job = i >= mine;
+    if (!r->job) {
+        t = u + i * units;
+    } else {
+        if (a.jobs < 2) return false;
+        const int rest = n0 % units, j = i - mine, ahead = a.lead * (units - rest);
+        t = u < rest ? ahead + j * units + u
+                     : j < a.lead ? j * (units - rest) + u - rest : ahead + (j - a.lead) * units + u;
+        if (t >= tiles_of(a.work[1])) return false;
+    }
+    const TileWork& w = a.work[r->job];
+    const int per = w.mt * w.nt;
+    r->split = t / per;
+    t -= r->split * per;
+    const int g = t / (w.group * w.nt);         // whole groups of tile rows
+    t -= g * w.group * w.nt;
+    const int rows = min(w.group, w.mt - g * w.group);
+    const int n = t / rows;
+    r->m0 = ((g * w.group + t - n * rows) * CG + rank) * kTileM;
+    r->n0 = n * N;
+    r->k0 = r->split * w.per;
+    r->kn = min(w.per, w.kb - r->k0);
+    return true;
+}
+
+// Terms of A and B in the order of their products, the smallest first: with
+// x = x0 + x1 + x2 to 24 bits, x0 y0 + (x0 y1 + x1 y0) + (x1 y1 + x0 y2 + x2 y0)
+// leaves out what is below 2^-24 of x y.
+__device__ __forceinline__ int term_a(int pairs, int p) { return pairs == 1 ? 0 : (0x001102 >> (4 * p)) & 3; }
+__device__ __forceinline__ int term_b(int pairs, int p) { return pairs == 1 ? 0 : (0x010120 >> (4 * p)) & 3; }
+
+template <int CG>
+__device__ __forceinline__ void load_operand(const CUtensorMap* map, bool mn, int boxes, int at,
+                                             int y0, int k, int term, uint32_t dst, uint32_t bar) {
+    if (!mn) {
+        tma_load_3d<CG>(dst, map, k * kTileK, at + y0, term, bar);
+        return;
+    }
+    for (int j = 0; j < boxes; ++j)
+        tma_load_3d<CG>(dst + j * kBoxBytes, map, at + 64 * j, k * kTileK + y0, term, bar);
+}
+
+// The bf16 terms of a value x0 + x1 + x2: each is what is left of it rounded to
+// bf16 (towards zero where that would be infinite); of a value that is not finite
+// nothing is left.
+__device__ __forceinline__ float first_term(float x) {
+    const float hi = __bfloat162float(__float2bfloat16_rn(x));
+    return isinf(hi) ? __uint_as_float(__float_as_uint(x) & 0xFFFF0000u) : hi;
+}
+__device__ __forceinline__ float rest_of(float x, float term) {
+    return fabsf(x) <= 3.402823466e38f ? x - term : 0.f;
+}
+
+// ------------------------------------------------------------ the epilogues
+// Each takes 32 columns of a warp's 32 rows at a time, from column c of the tile
+// on: lane i holds those of row row0 + i.  What goes to memory is turned around in
+// shared memory, 16-byte vectors permuted within a row so that both ways are free
+// of bank conflicts, so that consecutive lanes write consecutive columns: a lane a
+// row wrote 1.07 GB of dweight in 745 us where this takes
+// PLACEHOLDER_DW.
+//
+// A warp's 32 rows of 32 elements of E bytes.
+template <int E> struct Turn {
+    static constexpr int kVecs = 32 * E / 16;   // of a row
+    unsigned char* room;
+    int lane;
+    __device__ __forceinline__ uint4* at(int row, int vec) const {
+        const int x = E == 4 ? row & 7 : (row >> 1) & 3;
+        return reinterpret_cast<uint4*>(room + row * (32 * E)) + (vec ^ x);
+    }
+    __device__ __forceinline__ void put(const uint32_t (&w)[8 * E]) const {
+        __syncwarp();   // the last block has been read
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k)
+            *at(lane, k) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        __syncwarp();
+    }
+    // f(row, first column, vector) for a lane's vectors
+    template <typename F> __device__ __forceinline__ void vectors(F f) const {
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) {
+            const int row = (lane + 32 * k) / kVecs, vec = lane % kVecs;
+            f(row, vec * (16 / E), *at(row, vec));
+        }
+    }
+    // element `lane` of a row
+    __device__ __forceinline__ uint32_t element(int row) const {
+        const unsigned char* const p = reinterpret_cast<const unsigned char*>(at(row, lane * E / 16)) +
+                                       lane * E % 16;
+        if constexpr (E == 4) return *reinterpret_cast<const uint32_t*>(p);
+        else return *reinterpret_cast<const uint16_t*>(p);
+    }
+};
+__device__ __forceinline__ void halves(const float (&g)[32], uint32_t (&w)[16]) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = Pairs<bf16>::two(F2{g[2 * j], g[2 * j + 1]});
+}
+
+// A token's maximum and sum of exponentials over a warp's columns.
+struct StatsOut {
+    const VocabArgs& a;
+    int64_t to;          // the target's column in the tile, if it lies there
+    int left, row;
+    bool live;
+    float m = -INFINITY, s = 0.f;
+    __device__ StatsOut(const VocabArgs& args, const Tile& t, int row0, unsigned char*) : a(args) {
+        row = row0 + (threadIdx.x & 31);
+        live = row < a.rows;
+        to = (live ? a.target[row] : -1) - a.v0 - t.n0;
+        left = a.cols - t.n0;
+    }
+    __device__ __forceinline__ void take(int c, uint32_t (&v)[32]) {
+        if (c >= left) return;
+        if (c + 32 > left) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (c + j >= left) v[j] = __float_as_uint(-INFINITY);
+        }
+        float t0 = m, t1 = __uint_as_float(v[1]);
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+            t0 = fmaxf(t0, __uint_as_float(v[j]));
+            t1 = fmaxf(t1, __uint_as_float(v[j + 1]));
+        }
+        const float top = fmaxf(t0, t1);
+        // nothing is above an infinite maximum: exponents are then taken from zero
+        const float base = isinf(top) ? 0.f : top;
+        if (top != m) {
+            s = s == 0.f ? 0.f : s * fast_ex2((m - base) * kLog2e);
+            m = top;
+        }
+        const float off = -base * kLog2e;
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+            s0 += fast_ex2(fmaf(__uint_as_float(v[j]), kLog2e, off));
+            s1 += fast_ex2(fmaf(__uint_as_float(v[j + 1]), kLog2e, off));
+        }
+        s += s0 + s1;
+        if (to >= c && to < c + 32) {
+            float z = 0.f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (to == c + j) z = __uint_as_float(v[j]);
+            a.picked[row] = z;
+        }
+    }
+    __device__ __forceinline__ void done(int part) {
+        if (live) a.parts[(int64_t)part * a.rows + row] = make_float2(m, s);
+    }
+};
+
+// The gradient of a token's logits, as bf16 terms.
+template <typename T> struct GradOut {
+    const VocabArgs& a;
+    int64_t to = -1;
+    float scale = 0.f, both = 0.f, lse = 0.f;
+    int rows;            // of the warp's that there are
+    bool none;
+    bf16* out;           // the warp's first row
+    const Turn<2> turn;
+    __device__ GradOut(const VocabArgs& args, const Tile& t, int row0, unsigned char* room)
+        : a(args), turn{room, (int)threadIdx.x & 31} {
+        const int row = row0 + turn.lane;
+        rows = a.rows - row0;
+        if (row < a.rows) {
+            const int64_t target = a.target[row];
+            const bool ignored = target == a.ignore;
+            scale = ignored ? 0.f : target < 0 || target >= a.vocab ? NAN : a.dloss[row];
+            both = scale + (a.dlse ? a.dlse[row] : 0.f);
+            lse = a.lse[row];
+            to = ignored ? -1 : target - a.v0 - t.n0;
+        }
+        none = both == 0.f;  // (its exponentials may be infinite)
+        out = static_cast<bf16*>(a.grad) + (int64_t)row0 * a.grad_pitch + t.n0;
+    }
+    __device__ __forceinline__ void write(bf16* p, const float (&g)[32]) {
+        uint32_t w[16];
+        halves(g, w);
+        turn.put(w);
+        turn.vectors([&](int row, int col, uint4 v) {
+            if (row < rows) *reinterpret_cast<uint4*>(p + (int64_t)row * a.grad_pitch + col) = v;
+        });
+    }
+    __device__ __forceinline__ void take(int c, const uint32_t (&v)[32]) {
+        float g[32];
+        const float off = -lse * kLog2e;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const float z = __uint_as_float(v[j]);
+            const float e = sizeof(T) == 2 ? fast_ex2(fmaf(z, kLog2e, off)) : expf(z - lse);
+            g[j] = none ? 0.f : both * e;
+        }
+        if (to >= c && to < c + 32) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (to == c + j) g[j] -= scale;
+        }
+        if constexpr (sizeof(T) == 2) {
+            write(out + c, g);
+        } else {
+#pragma unroll 1
+            for (int k = 0; k < 3; ++k) {  // what is left of g, a term at a time
+                float x[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    x[j] = first_term(g[j]);
+                    g[j] = rest_of(g[j], x[j]);
+                }
+                write(out + k * a.grad_plane + c, x);
+            }
+        }
+    }
+    __device__ __forceinline__ void done(int) {}
+};
+
+// A product's rows, of the call's type or as fp32 sums.
+template <typename T> struct ProductRow {
+    const ProductOut& o;
+    int left, rows;
+    float* sums;
+    T* out;
+    const Turn<4> wide;
+    const Turn<sizeof(T)> turn;
+    __device__ ProductRow(const VocabArgs& a, const Tile& t, int row0, unsigned char* room)
+        : o(a.out[t.job]), wide{room, (int)threadIdx.x & 31}, turn{room, (int)threadIdx.x & 31} {
+        rows = o.rows - row0;
+        left = o.cols - t.n0;
+        sums = o.sums ? o.sums + ((int64_t)t.split * o.rows + row0) * o.pitch + t.n0 : nullptr;
+        out = static_cast<T*>(o.out) + (int64_t)row0 * o.pitch + t.n0;
+    }
+    __device__ __forceinline__ void take(int c, const uint32_t (&v)[32]) {
+        if (c >= left || rows <= 0) return;
+        if (sums) {  // (rows of sums are whole vectors)
+            wide.put(v);
+            wide.vectors([&](int row, int col, uint4 w) {
+                if (row >= rows || c + col >= left) return;
+                float4 f = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z),
+                                       __uint_as_float(w.w));
+                float4* const p = reinterpret_cast<float4*>(sums + row * o.pitch + c + col);
+                if (o.add) {
+                    const float4 b = __ldcg(p);
+                    f = make_float4(b.x + f.x, b.y + f.y, b.z + f.z, b.w + f.w);
+                }
+                __stcg(p, f);
+            });
+            return;
+        }
+        if constexpr (sizeof(T) == 4) {
+            turn.put(v);
+        } else {
+            float f[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
+            uint32_t w[16];
+            halves(f, w);
+            turn.put(w);
+        }
+        if (o.vec) {  // (a row's columns are whole vectors)
+            turn.vectors([&](int row, int col, uint4 w) {
+                if (row < rows && c + col < left)
+                    __stcs(reinterpret_cast<uint4*>(out + row * o.pitch + c + col), w);
+            });
+        } else if (c + turn.lane < left) {
+            using Word = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
+#pragma unroll 4
+            for (int row = 0; row < 32; ++row)
+                if (row < rows)
+                    reinterpret_cast<Word*>(out + row * o.pitch + c)[turn.lane] = (Word)turn.element(row);
+        }
+    }
+    __device__ __forceinline__ void done(int) {}
+};
+
+// ---------------------------------------------------------------- the kernel
+template <typename OUT, bool PROMOTE, int N, int CG>
+__global__ void __launch_bounds__(kVocabThreads, 1)
+vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUtensorMap b0,
+            const __grid_constant__ CUtensorMap a1, const __grid_constant__ CUtensorMap b1,
+            const __grid_constant__ VocabArgs a) {
+    using S = TileShape<N, CG>;
+    extern __shared__ unsigned char raw[];
+    __shared__ __align__(8) VocabBars bars;
+    __shared__ uint32_t tmem_base;
+    __shared__ int dead_flag;
+    volatile int* const dead = &dead_flag;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rank = CG == 1 ? 0 : (int)cluster_ctarank();
+    const int unit = (int)blockIdx.x / CG, units = (int)gridDim.x / CG;
+    const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
+    const int stage = a.a_room + S::kBytesB, stages = min(kVocabRing / stage, kVocabStages);
+    if (threadIdx.x == 0) {
+        dead_flag = 0;
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(smem_u32(&bars.full[s]), 1);
+            mbar_init(smem_u32(&bars.empty[s]), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&bars.acc_full[s]), 1);
+            mbar_init(smem_u32(&bars.acc_empty[s]), CG * kVocabWarps);
+        }
+        mbar_init(smem_u32(&bars.drained), 1);
+        fence_mbar_init();
+        fence_proxy_async_smem();
+    }
+    if (warp == kVocabWarps + 1) tmem_alloc<CG>(smem_u32(&tmem_base), S::kTmem);
+    tmem_fence_before();
+    __syncthreads();
+    if constexpr (CG > 1) {  // the other CTA's barriers are there
+        cluster_arrive_release();
+        cluster_wait_acquire();
+    }
+    tmem_fence_after();
+    const uint32_t tmem = tmem_base;
+    Tile t;
+    // The sums of an epilogue thread take registers that the other warps do not
+    // need: of 384 x 168 at launch, 128 x 80 and 256 x 208.
+    if (warp >= kVocabWarps) {
+        if constexpr (PROMOTE) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (warp == kVocabWarps) {
+            if (lane == 0) {
+                int s = 0;
+                uint32_t phase = 0, filled = 0;  // fills in all
+                bool ok = true;
+                for (int i = 0; ok && tile_at<N, CG>(a, unit, units, rank, i, &t); ++i) {
+                    const TileWork& w = a.work[t.job];
+                    const CUtensorMap* const ma = t.job ? &a1 : &a0;
+                    const CUtensorMap* const mb = t.job ? &b1 : &b0;
+                    for (int p = 0; ok && p < a.pairs; ++p)
+                        for (int k = 0; k < t.kn; ++k) {
+                            ok = hold(bars.empty[s], phase ^ 1u, a.err, dead);
+                            if (!ok) break;
+                            // both CTAs' bytes count on the first one's barrier
+                            uint32_t bar = smem_u32(&bars.full[s]);
+                            const uint32_t at = ring + s * stage;
+                            if (rank == 0) mbar_arrive_expect_tx(bar, CG * (w.a_bytes + S::kBytesB));
+                            if constexpr (CG > 1) bar = mapa_shared(bar, 0);
+                            load_operand<CG>(ma, w.a_mn, kTileM / 64, t.m0, 0, t.k0 + k,
+                                             term_a(a.pairs, p), at, bar);
+                            load_operand<CG>(mb, w.b_mn, S::kRowsB / 64, t.n0 + rank * S::kRowsB, w.b_y0,
+                                             t.k0 + k, term_b(a.pairs, p), at + a.a_room, bar);
+                            ++filled;
+                            if (++s == stages) {
+                                s = 0;
+                                phase ^= 1u;
+                            }
+                        }
+                }
+                // a CTA that has given up leaves no copy in flight
+                if (!ok && rank == 0)
+                    for (uint32_t f = filled > (uint32_t)stages ? filled - stages : 0; f < filled; ++f)
+                        mbar_wait_bounded(smem_u32(&bars.full[f % stages]), (f / stages) & 1u, a.err);
+            }
+        } else if (warp == kVocabWarps + 1) {
+            if (lane == 0 && rank == 0) {
+                int s = 0, n = 0;  // n: parts so far
+                uint32_t phase = 0;
+                bool ok = true;
+                for (int i = 0; ok && tile_at<N, CG>(a, unit, units, rank, i, &t); ++i) {
+                    const TileWork& w = a.work[t.job];
+                    const uint32_t desc = mma_desc(CG * kTileM, N, w.a_mn, w.b_mn);
+                    // bytes from one sixteen k to the next
+                    const uint32_t step_a = w.a_mn ? 16 * 128 : 32, step_b = w.b_mn ? 16 * 128 : 32;
+                    const int steps = t.kn * a.pairs;
+                    for (int k0 = 0; ok && k0 < steps; ++n) {
+                        const int k1 = PROMOTE ? min(steps, k0 + kPromote) : steps;
+                        const uint32_t acc = tmem + (n & 1) * N;
+                        ok = hold(bars.acc_empty[n & 1], ((n >> 1) & 1) ^ 1u, a.err, dead);
+                        if (!ok) break;
+                        tmem_fence_after();
+                        for (int k = k0; k < k1; ++k) {
+                            ok = hold(bars.full[s], phase, a.err, dead);
+                            if (!ok) break;
+                            tmem_fence_after();
+                            const uint32_t at = ring + s * stage;
+                            const uint64_t da = smem_desc(at, kBoxBytes, 1024);
+                            const uint64_t db = smem_desc(at + a.a_room, kBoxBytes, 1024);
+    #pragma unroll
+                            for (int q = 0; q < kTileK / 16; ++q)
+                                mma_bf16<CG>(acc, da + (q * step_a >> 4), db + (q * step_b >> 4), desc,
+                                             k > k0 || q > 0);
+                            mma_commit<CG>(smem_u32(&bars.empty[s]));
+                            if (++s == stages) {
+                                s = 0;
+                                phase ^= 1u;
+                            }
+                        }
+                        if (ok) mma_commit<CG>(smem_u32(&bars.acc_full[n & 1]));
+                        k0 = k1;
+                    }
+                }
+                if (!ok) {  // nor a product
+                    mma_commit<CG>(smem_u32(&bars.drained));
+                    mbar_wait_bounded(smem_u32(&bars.drained), 0, a.err);
+                }
+            }
+        }
+    } else {
+        if constexpr (PROMOTE) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int quarter = warp & 3, half = warp >> 2;
+        unsigned char* const room = raw + (ring - smem_u32(raw)) + kVocabRing + warp * kStageOut;
+        int n = 0;
+        bool ok = true;
+        // the accumulators of part n, once they are there
+        auto ready = [&]() {
+            ok = __all_sync(0xffffffffu, hold(bars.acc_full[n & 1], (n >> 1) & 1, a.err, dead));
+            tmem_fence_after();
+            return tmem + (n & 1) * N + half * S::kCols + ((uint32_t)(32 * quarter) << 16);
+        };
+        auto release = [&]() {
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                const uint32_t bar = smem_u32(&bars.acc_empty[n & 1]);
+                if constexpr (CG > 1) mbar_arrive_cluster(mapa_shared(bar, 0));
+                else mbar_arrive(bar);
+            }
+            ++n;
+        };
+        for (int i = 0; ok && tile_at<N, CG>(a, unit, units, rank, i, &t); ++i) {
+            OUT out(a, t, t.m0 + 32 * quarter, room);
+            if constexpr (PROMOTE) {
+                F2 sum[S::kCols / 2];
+                const int steps = t.kn * a.pairs;
+                for (int k0 = 0; k0 < steps; k0 += kPromote) {
+                    const uint32_t acc = ready();
+                    if (!ok) break;
+#pragma unroll
+                    for (int c = 0; c < S::kCols; c += 32) {
+                        uint32_t v[32];
+                        tmem_load(acc + c, v);
+                        tmem_load_wait();
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            const F2 x{__uint_as_float(v[j]), __uint_as_float(v[j + 1])};
+                            F2& y = sum[(c + j) / 2];
+                            y = k0 ? add2(y, x) : x;
+                        }
+                    }
+                    release();
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int c = 0; c < S::kCols; c += 32) {
+                    uint32_t v[32];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        v[j] = __float_as_uint(sum[(c + j) / 2].x);
+                        v[j + 1] = __float_as_uint(sum[(c + j) / 2].y);
+                    }
+                    out.take(half * S::kCols + c, v);
+                }
+            } else {
+                const uint32_t acc = ready();
+                if (!ok) break;
+                for (int c = 0; c < S::kCols; c += 32) {
+                    uint32_t v[32];
+                    tmem_load(acc + c, v);
+                    tmem_load_wait();
+                    out.take(half * S::kCols + c, v);
+                }
+                release();
+            }
+            out.done(t.n0 / S::kCols + half);
+        }
+    }
+    __syncwarp();
+    tmem_fence_before();
+    __syncthreads();
+    if constexpr (CG > 1) {  // no CTA leaves while the other may signal it
+        cluster_arrive_release();
+        cluster_wait_acquire();
+    }
+    tmem_fence_after();
+    if (warp == kVocabWarps + 1) tmem_free<CG>(tmem, S::kTmem);
+}
+
+template <typename OUT, bool PROMOTE> const void* vocab_kernel_of(VocabTile t) {
+    switch (t) {
+        case kPair256: return (const void*)vocab_tiles<OUT, PROMOTE, 256, 2>;
+        case kOne128: return (const void*)vocab_tiles<OUT, PROMOTE, 128, 1>;
+        default: return (const void*)vocab_tiles<OUT, PROMOTE, 64, 1>;
+    }
+}
+
+}  // namespace credit
