@@ -5,6 +5,7 @@
 #include <vector>
 
 #include "credit.h"
+#include "early_launch.h"
 #include "internal.h"
 #include "planner.h"
 #include "rowops.cuh"
@@ -153,6 +154,8 @@ __device__ __forceinline__ void chunk_scale(const void* p, void* out, int64_t co
 template <int N>
 __global__ void __launch_bounds__(kThreads)
 grad_squares(const __grid_constant__ Table<N> t, double* parts) {
+    dependents_may_launch();
+    wait_for_launches();
     int lo, hi;
     run_of(t.first[t.n], lo, hi);
     double sum = 0.0;
@@ -175,6 +178,8 @@ __device__ __forceinline__ float norm_of(const double* parts, int n) {
 }
 
 __global__ void __launch_bounds__(kThreads) grad_norm(const double* parts, int n, float* norm) {
+    dependents_may_launch();
+    wait_for_launches();
     const float v = norm_of(parts, n);
     if (threadIdx.x == 0) *norm = v;
 }
@@ -184,6 +189,8 @@ template <int N>
 __global__ void __launch_bounds__(kThreads)
 grad_scale(const __grid_constant__ Table<N> t, const double* parts, int nparts, float max_norm,
            float eps, float* norm, bool in_place) {
+    dependents_may_launch();
+    wait_for_launches();
     const float v = norm_of(parts, nparts);
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
     float factor = max_norm / (v + eps);
@@ -276,6 +283,7 @@ credit_status_t check(const credit_tensor_t* t, int64_t n, bool outs, const Rang
     std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
     uintptr_t end_in = 0, end_out = 0;
     for (const Range& a : r) {
+        if (a.lo == a.hi) continue;
         if (a.lo < end_out || (a.out && a.lo < end_in)) return CREDIT_ERR_INVALID_ARG;
         uintptr_t& e = a.out ? end_out : end_in;
         e = std::max(e, a.hi);
@@ -291,11 +299,17 @@ cudaError_t launch_batch(const credit_tensor_t* t, const Batch& b, double* parts
                          cudaStream_t s) {
     Table<N> table;
     fill<N>(t, b, &table);
-    if (scale)
-        grad_scale<N><<<b.grid, kThreads, 0, s>>>(table, parts, nparts, max_norm, eps, norm, in_place);
-    else
-        grad_squares<N><<<b.grid, kThreads, 0, s>>>(table, parts);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr = early_launch();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)b.grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    void* sum_args[] = {&table, &parts};
+    void* scale_args[] = {&table, &parts, &nparts, &max_norm, &eps, &norm, &in_place};
+    return scale ? cudaLaunchKernelExC(&cfg, (const void*)grad_scale<N>, scale_args)
+                 : cudaLaunchKernelExC(&cfg, (const void*)grad_squares<N>, sum_args);
 }
 
 cudaError_t launch_any(const credit_tensor_t* t, const Batch& b, double* parts, int nparts, bool scale,
@@ -334,8 +348,8 @@ credit_status_t run(const credit_tensor_t* t, int64_t n, bool clip, float max_no
         at += b.grid;
     }
     if (!clip || batches.empty()) {
-        grad_norm<<<1, kThreads, 0, s>>>(parts, (int)nparts, norm);
-        return from_cuda(cudaGetLastError());
+        return from_cuda(launch_early(grad_norm, dim3(1), kThreads, s, (const double*)parts, (int)nparts,
+                                      norm));
     }
     for (size_t i = batches.size(); i-- > 0;) {
         st = from_cuda(launch_any(t, batches[i], parts, (int)nparts, true, max_norm, eps,

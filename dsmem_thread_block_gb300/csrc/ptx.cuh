@@ -178,6 +178,16 @@ template <int N> __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
 }
 
+// Programmatic dependent launch: the next kernel of the stream may be launched
+// from here on; and wait until the kernels before this one are done and their
+// writes are seen.
+__device__ __forceinline__ void dependents_may_launch() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_launches() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ------------------------------------------------------------- vector access
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
     uint4 v;

@@ -5,6 +5,7 @@
 //
 // The products are vocab_tiles.cuh's; here are what comes before and after them,
 // and the launches.
+#include "early_launch.h"
 #include "vocab_tiles.cuh"
 
 namespace credit {
@@ -19,6 +20,8 @@ constexpr int kMergeWarps = 16;
 __global__ void __launch_bounds__(32 * kMergeWarps)
 vocab_merge(VocabArgs a, int nparts, float* loss, float* lse) {
     __shared__ float tops[kMergeWarps][32], sums[kMergeWarps][32];
+    dependents_may_launch();
+    wait_for_launches();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row = (int64_t)blockIdx.x * 32 + lane;
     const bool live = row < a.rows;
@@ -52,11 +55,25 @@ vocab_merge(VocabArgs a, int nparts, float* loss, float* lse) {
 }
 
 // Rows as bf16 terms, eight columns a thread (rows of dst are whole 16-byte lines,
-// their last one padded with zeros).
+// their last one padded with zeros); grid row y packs matrix y.
+struct PackArgs {
+    const void* src[2];
+    bf16* dst[2];
+    int64_t rows[2];
+    int64_t pitch, plane[2];
+    int cols;
+};
 template <typename T>
-__global__ void __launch_bounds__(256)
-vocab_pack(const T* src, int64_t rows, int cols, bf16* dst, int64_t pitch, int64_t plane, bool vec) {
-    const int vecs = (cols + 7) / 8;
+__global__ void __launch_bounds__(256) vocab_pack(PackArgs a) {
+    dependents_may_launch();
+    wait_for_launches();
+    const bool second = blockIdx.y;
+    const T* const src = static_cast<const T*>(second ? a.src[1] : a.src[0]);
+    bf16* const dst = second ? a.dst[1] : a.dst[0];
+    const int64_t rows = second ? a.rows[1] : a.rows[0], plane = second ? a.plane[1] : a.plane[0];
+    const int64_t pitch = a.pitch;
+    const int cols = a.cols, vecs = (cols + 7) / 8;
+    const bool vec = (uintptr_t)src % 16 == 0 && cols % 4 == 0;
     const int64_t step = (int64_t)gridDim.x * 256, drow = step / vecs;
     const int dvec = (int)(step - drow * vecs);
     const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -98,6 +115,8 @@ vocab_pack(const T* src, int64_t rows, int cols, bf16* dst, int64_t pitch, int64
 template <typename T>
 __global__ void __launch_bounds__(256)
 vocab_sum(const float* sums, int splits, int64_t rows, int cols, int64_t pitch, T* out, bool vec) {
+    dependents_may_launch();
+    wait_for_launches();
     const int vecs = (cols + 3) / 4;
     const int64_t step = (int64_t)gridDim.x * 256, drow = step / vecs, plane = rows * pitch;
     const int dvec = (int)(step - drow * vecs);
@@ -201,12 +220,13 @@ cudaError_t launch_vocab(VocabOut out, int dtype, VocabTile tile, const CUtensor
     cfg.blockDim = dim3(kVocabThreads);
     cfg.dynamicSmemBytes = kVocabSmem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ctas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0] = early_launch();
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = ctas > 1 ? 1 : 0;
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
     void* p[] = {const_cast<CUtensorMap*>(&maps[0]), const_cast<CUtensorMap*>(&maps[1]),
                  const_cast<CUtensorMap*>(&maps[2]), const_cast<CUtensorMap*>(&maps[3]), &a};
     return cudaLaunchKernelExC(&cfg, fn, p);
@@ -214,34 +234,36 @@ cudaError_t launch_vocab(VocabOut out, int dtype, VocabTile tile, const CUtensor
 
 cudaError_t launch_vocab_merge(const VocabArgs& a, int nparts, float* loss, float* lse,
                                cudaStream_t s) {
-    vocab_merge<<<(unsigned)((a.rows + 31) / 32), 32 * kMergeWarps, 0, s>>>(a, nparts, loss, lse);
-    return cudaGetLastError();
+    return launch_early(vocab_merge, dim3((unsigned)((a.rows + 31) / 32)), 32 * kMergeWarps, s, a, nparts,
+                        loss, lse);
 }
 
-cudaError_t launch_vocab_pack(int dtype, const void* src, int64_t rows, int64_t cols, void* dst,
-                              int64_t pitch, int64_t plane, int sms, cudaStream_t s) {
-    const int blocks = blocks_for(rows * ((cols + 7) / 8), sms);
-    const bool vec = (uintptr_t)src % 16 == 0 && cols % 4 == 0;
-    if (dtype == 0)
-        vocab_pack<float><<<blocks, 256, 0, s>>>(static_cast<const float*>(src), rows, (int)cols,
-                                                 static_cast<bf16*>(dst), pitch, plane, vec);
-    else
-        vocab_pack<bf16><<<blocks, 256, 0, s>>>(static_cast<const bf16*>(src), rows, (int)cols,
-                                                static_cast<bf16*>(dst), pitch, plane, vec);
-    return cudaGetLastError();
+cudaError_t launch_vocab_pack(int dtype, const void* const (&src)[2], const TermMatrix (&dst)[2], int n,
+                              int sms, cudaStream_t s) {
+    PackArgs a{};
+    int64_t rows = 0;
+    for (int i = 0; i < n; ++i) {
+        a.src[i] = src[i];
+        a.dst[i] = static_cast<bf16*>(const_cast<void*>(dst[i].p));
+        a.rows[i] = dst[i].rows;
+        a.plane[i] = dst[i].plane / 2;
+        rows = std::max(rows, dst[i].rows);
+    }
+    a.pitch = dst[0].pitch / 2;
+    a.cols = (int)dst[0].cols;
+    const dim3 grid((unsigned)blocks_for(rows * ((a.cols + 7) / 8), sms), (unsigned)n);
+    return dtype == 0 ? launch_early(vocab_pack<float>, grid, 256, s, a)
+                      : launch_early(vocab_pack<bf16>, grid, 256, s, a);
 }
 
 cudaError_t launch_vocab_sum(int dtype, const float* sums, int splits, int64_t rows, int64_t cols,
                              int64_t pitch, void* out, int sms, cudaStream_t s) {
-    const int blocks = blocks_for(rows * ((cols + 3) / 4), sms);
+    const dim3 grid((unsigned)blocks_for(rows * ((cols + 3) / 4), sms));
     const bool vec = (uintptr_t)out % 16 == 0 && cols % 4 == 0;
-    if (dtype == 0)
-        vocab_sum<float><<<blocks, 256, 0, s>>>(sums, splits, rows, (int)cols, pitch,
-                                                static_cast<float*>(out), vec);
-    else
-        vocab_sum<bf16><<<blocks, 256, 0, s>>>(sums, splits, rows, (int)cols, pitch,
-                                               static_cast<bf16*>(out), vec);
-    return cudaGetLastError();
+    return dtype == 0 ? launch_early(vocab_sum<float>, grid, 256, s, sums, splits, rows, (int)cols, pitch,
+                                     static_cast<float*>(out), vec)
+                      : launch_early(vocab_sum<bf16>, grid, 256, s, sums, splits, rows, (int)cols, pitch,
+                                     static_cast<bf16*>(out), vec);
 }
 
 }  // namespace credit

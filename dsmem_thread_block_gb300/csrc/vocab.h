@@ -88,9 +88,9 @@ cudaError_t launch_vocab(VocabOut out, int dtype, VocabTile tile, const CUtensor
 // loss and lse from the tiles' parts
 cudaError_t launch_vocab_merge(const VocabArgs& a, int parts, float* loss, float* lse,
                                cudaStream_t s);
-// rows x cols of the call's type as bf16 terms
-cudaError_t launch_vocab_pack(int dtype, const void* src, int64_t rows, int64_t cols, void* dst,
-                              int64_t pitch, int64_t plane, int sms, cudaStream_t s);
+// n matrices of the call's type and of one width as bf16 terms
+cudaError_t launch_vocab_pack(int dtype, const void* const (&src)[2], const TermMatrix (&dst)[2], int n,
+                              int sms, cudaStream_t s);
 // out = the splits' sums added in order
 cudaError_t launch_vocab_sum(int dtype, const float* sums, int splits, int64_t rows, int64_t cols,
                              int64_t pitch, void* out, int sms, cudaStream_t s);

@@ -23,6 +23,8 @@ int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 constexpr int64_t kPieceBytes = (int64_t)256 << 20;
 // Most parts of a sum over the vocabulary.
 constexpr int kMaxSplits = 64;
+// Fewest stages of a part.
+constexpr int kMinPart = 8;
 
 // Widest tile: a piece of the vocabulary is whole tiles of any shape.
 constexpr int kTileN = vocab_tile_cols(kPair256);
@@ -135,7 +137,7 @@ Products products_for(const Shape& s, int64_t piece, bool dh, bool dw, int sms) 
         double time = all / units;
         if (dh) {
             const double stage = (double)pairs * cols / 256;
-            const int64_t share = std::max<int64_t>(16, (int64_t)(all / units / 2 / stage));
+            const int64_t share = std::max<int64_t>(kMinPart, (int64_t)(all / units / 2 / stage));
             const int64_t want = std::min<int64_t>(ceil_div(kb, share), kMaxSplits);
             p.per = (int32_t)ceil_div(kb, want);
             p.splits = (int32_t)ceil_div(kb, p.per);
@@ -221,9 +223,15 @@ int box_rows(VocabTile t, int64_t rows, TileWork* w) {
     return box;
 }
 
-cudaError_t pack(const Shape& s, const void* src, const TermMatrix& m, int sms, cudaStream_t stream) {
-    return launch_vocab_pack(s.dtype, src, m.rows, m.cols, const_cast<void*>(m.p), m.pitch / 2,
-                             m.plane / 2, sms, stream);
+// Copies the operands that the tensor maps cannot take as they are.
+cudaError_t pack(const Shape& s, const void* hidden, const TermMatrix& h, const void* weight,
+                 const TermMatrix& w, int sms, cudaStream_t stream) {
+    const void* src[2];
+    TermMatrix dst[2];
+    int n = 0;
+    if (s.pack_h) { src[n] = hidden; dst[n++] = h; }
+    if (s.pack_w) { src[n] = weight; dst[n++] = w; }
+    return n ? launch_vocab_pack(s.dtype, src, dst, n, sms, stream) : cudaSuccess;
 }
 
 }  // namespace
@@ -288,8 +296,7 @@ credit_status_t credit_linear_ce_forward(const void* hidden, const void* weight,
     if (!term_map(h, box_rows(tile, tokens, &a.work[0]), &maps[0]) ||
         !term_map(w, vocab_tile_cols(tile) / vocab_tile_ctas(tile), &maps[1]))
         return CREDIT_ERR_CUDA;
-    if (s.pack_h && (st = from_cuda(pack(s, hidden, h, d->sms, q))) != CREDIT_OK) return st;
-    if (s.pack_w && (st = from_cuda(pack(s, weight, w, d->sms, q))) != CREDIT_OK) return st;
+    if ((st = from_cuda(pack(s, hidden, h, weight, w, d->sms, q))) != CREDIT_OK) return st;
     a.rows = (int32_t)tokens;
     a.cols = (int32_t)vocab;
     a.vocab = vocab;
@@ -336,8 +343,7 @@ credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse,
     char* const ws = static_cast<char*>(workspace);
     const TermMatrix h = operand(s, hidden, tokens, s.pack_h, ws + l.h);
     const TermMatrix w = operand(s, weight, vocab, s.pack_w, ws + l.w);
-    if (s.pack_h && (st = from_cuda(pack(s, hidden, h, d->sms, q))) != CREDIT_OK) return st;
-    if (s.pack_w && (st = from_cuda(pack(s, weight, w, d->sms, q))) != CREDIT_OK) return st;
+    if ((st = from_cuda(pack(s, hidden, h, weight, w, d->sms, q))) != CREDIT_OK) return st;
 
     const bool sums = products.splits > 1 || l.pieces > 1;
     const VocabTile pt = products.tile, gt = logits_tile(s, l.piece, d->sms);

@@ -31,7 +31,7 @@ constexpr int kVocabRing = 6 * 32768;           // bytes of all stages
 constexpr int kVocabStages = 16;                // most of them
 constexpr int kStageOut = 32 * 128;             // a warp's room to turn its output around
 constexpr int kVocabSmem = kVocabRing + kVocabWarps * kStageOut + 1024;  // aligned to 1024 by hand
-constexpr int kPromote = 4;                     // stages of a part
+constexpr int kPromote = 8;                     // stages of a part
 
 // A tile is 128 rows a CTA by N columns (CG = 2: a pair shares the columns'
 // operand, half of it each).
@@ -47,13 +47,14 @@ struct VocabBars {
 };
 
 // Wait for a phase; false once a wait of this CTA has given up.
-__device__ __forceinline__ bool hold(uint64_t& bar, uint32_t parity, unsigned* err,
+__device__ __forceinline__ bool hold(uint32_t bar, uint32_t parity, unsigned* err,
                                      volatile int* dead) {
-    const uint32_t b = smem_u32(&bar);
+#pragma unroll 1
     for (int i = 0; i < 64; ++i)
-        if (mbar_try_wait(b, parity)) return true;
+        if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(b, parity)) {
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
         if (*dead) return false;
         if (globaltimer_ns() - t0 > kWaitLimitNs) {
             atomicOr(err, kErrTimeout);
@@ -108,16 +109,27 @@ __device__ __forceinline__ bool tile_at(const VocabArgs& a, int u, int units, in
 __device__ __forceinline__ int term_a(int pairs, int p) { return pairs == 1 ? 0 : (0x001102 >> (4 * p)) & 3; }
 __device__ __forceinline__ int term_b(int pairs, int p) { return pairs == 1 ? 0 : (0x010120 >> (4 * p)) & 3; }
 
-template <int CG>
-__device__ __forceinline__ void load_operand(const CUtensorMap* map, bool mn, int boxes, int at,
-                                             int y0, int k, int term, uint32_t dst, uint32_t bar) {
-    if (!mn) {
-        tma_load_3d<CG>(dst, map, k * kTileK, at + y0, term, bar);
-        return;
+// Where an operand's boxes of a stage lie: one box with K innermost, `boxes` of 64
+// with M or N innermost.
+template <int CG, int BOXES> struct Boxes {
+    const CUtensorMap* map;
+    int x, y, dx, dy;
+    bool mn;
+    __device__ Boxes(const CUtensorMap* m, bool mn_, int at, int y0, int k) : map(m), mn(mn_) {
+        x = mn ? at : k * kTileK;
+        y = mn ? k * kTileK + y0 : at + y0;
+        dx = mn ? 0 : kTileK;
+        dy = mn ? kTileK : 0;
     }
-    for (int j = 0; j < boxes; ++j)
-        tma_load_3d<CG>(dst + j * kBoxBytes, map, at + 64 * j, k * kTileK + y0, term, bar);
-}
+    __device__ __forceinline__ void load(int step, int term, uint32_t dst, uint32_t bar) const {
+        const int u = x + step * dx, v = y + step * dy;
+        tma_load_3d<CG>(dst, map, u, v, term, bar);
+        if (BOXES > 1 && mn) {
+#pragma unroll
+            for (int j = 1; j < BOXES; ++j) tma_load_3d<CG>(dst + j * kBoxBytes, map, u + 64 * j, v, term, bar);
+        }
+    }
+};
 
 // The bf16 terms of a value x0 + x1 + x2: each is what is left of it rounded to
 // bf16 (towards zero where that would be infinite); of a value that is not finite
@@ -391,87 +403,87 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
     }
     tmem_fence_after();
     const uint32_t tmem = tmem_base;
+    dependents_may_launch();
+    wait_for_launches();
     Tile t;
     // The sums of an epilogue thread take registers that the other warps do not
     // need: of 384 x 168 at launch, 128 x 80 and 256 x 208.
     if (warp >= kVocabWarps) {
         if constexpr (PROMOTE) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-        if (warp == kVocabWarps) {
-            if (lane == 0) {
-                int s = 0;
-                uint32_t phase = 0, filled = 0;  // fills in all
-                bool ok = true;
-                for (int i = 0; ok && tile_at<N, CG>(a, unit, units, rank, i, &t); ++i) {
-                    const TileWork& w = a.work[t.job];
-                    const CUtensorMap* const ma = t.job ? &a1 : &a0;
-                    const CUtensorMap* const mb = t.job ? &b1 : &b0;
-                    for (int p = 0; ok && p < a.pairs; ++p)
-                        for (int k = 0; k < t.kn; ++k) {
-                            ok = hold(bars.empty[s], phase ^ 1u, a.err, dead);
-                            if (!ok) break;
-                            // both CTAs' bytes count on the first one's barrier
-                            uint32_t bar = smem_u32(&bars.full[s]);
-                            const uint32_t at = ring + s * stage;
-                            if (rank == 0) mbar_arrive_expect_tx(bar, CG * (w.a_bytes + S::kBytesB));
-                            if constexpr (CG > 1) bar = mapa_shared(bar, 0);
-                            load_operand<CG>(ma, w.a_mn, kTileM / 64, t.m0, 0, t.k0 + k,
-                                             term_a(a.pairs, p), at, bar);
-                            load_operand<CG>(mb, w.b_mn, S::kRowsB / 64, t.n0 + rank * S::kRowsB, w.b_y0,
-                                             t.k0 + k, term_b(a.pairs, p), at + a.a_room, bar);
-                            ++filled;
-                            if (++s == stages) {
-                                s = 0;
-                                phase ^= 1u;
-                            }
-                        }
-                }
-                // a CTA that has given up leaves no copy in flight
-                if (!ok && rank == 0)
-                    for (uint32_t f = filled > (uint32_t)stages ? filled - stages : 0; f < filled; ++f)
-                        mbar_wait_bounded(smem_u32(&bars.full[f % stages]), (f / stages) & 1u, a.err);
+        const uint32_t full0 = smem_u32(&bars.full[0]), empty0 = smem_u32(&bars.empty[0]);
+        const uint32_t end = ring + (uint32_t)(stages * stage);
+        uint32_t at = ring, bar = 0, phase = 0;  // of the present stage; bar: 8 bytes each
+        auto advance = [&]() {
+            at += stage;
+            bar += 8;
+            if (at == end) {
+                at = ring;
+                bar = 0;
+                phase ^= 1u;
             }
-        } else if (warp == kVocabWarps + 1) {
-            if (lane == 0 && rank == 0) {
-                int s = 0, n = 0;  // n: parts so far
-                uint32_t phase = 0;
-                bool ok = true;
-                for (int i = 0; ok && tile_at<N, CG>(a, unit, units, rank, i, &t); ++i) {
-                    const TileWork& w = a.work[t.job];
-                    const uint32_t desc = mma_desc(CG * kTileM, N, w.a_mn, w.b_mn);
-                    // bytes from one sixteen k to the next
-                    const uint32_t step_a = w.a_mn ? 16 * 128 : 32, step_b = w.b_mn ? 16 * 128 : 32;
-                    const int steps = t.kn * a.pairs;
-                    for (int k0 = 0; ok && k0 < steps; ++n) {
-                        const int k1 = PROMOTE ? min(steps, k0 + kPromote) : steps;
-                        const uint32_t acc = tmem + (n & 1) * N;
-                        ok = hold(bars.acc_empty[n & 1], ((n >> 1) & 1) ^ 1u, a.err, dead);
+        };
+        if (warp == kVocabWarps && lane == 0) {
+            // both CTAs' bytes count on the first one's barriers
+            const uint32_t signal0 = CG > 1 ? mapa_shared(full0, 0) : full0;
+            uint32_t filled = 0;  // fills in all
+            bool ok = true;
+            for (int i = 0; ok && tile_at<N, CG>(a, unit, units, rank, i, &t); ++i) {
+                const TileWork& w = a.work[t.job];
+                const Boxes<CG, kTileM / 64> boxes_a(t.job ? &a1 : &a0, w.a_mn, t.m0, 0, t.k0);
+                const Boxes<CG, S::kRowsB / 64> boxes_b(t.job ? &b1 : &b0, w.b_mn, t.n0 + rank * S::kRowsB,
+                                                        w.b_y0, t.k0);
+                const uint32_t bytes = CG * (w.a_bytes + S::kBytesB);
+                for (int p = 0; ok && p < a.pairs; ++p) {
+                    const int ta = term_a(a.pairs, p), tb = term_b(a.pairs, p);
+                    for (int k = 0; k < t.kn; ++k) {
+                        ok = hold(empty0 + bar, phase ^ 1u, a.err, dead);
                         if (!ok) break;
-                        tmem_fence_after();
-                        for (int k = k0; k < k1; ++k) {
-                            ok = hold(bars.full[s], phase, a.err, dead);
-                            if (!ok) break;
-                            tmem_fence_after();
-                            const uint32_t at = ring + s * stage;
-                            const uint64_t da = smem_desc(at, kBoxBytes, 1024);
-                            const uint64_t db = smem_desc(at + a.a_room, kBoxBytes, 1024);
-    #pragma unroll
-                            for (int q = 0; q < kTileK / 16; ++q)
-                                mma_bf16<CG>(acc, da + (q * step_a >> 4), db + (q * step_b >> 4), desc,
-                                             k > k0 || q > 0);
-                            mma_commit<CG>(smem_u32(&bars.empty[s]));
-                            if (++s == stages) {
-                                s = 0;
-                                phase ^= 1u;
-                            }
-                        }
-                        if (ok) mma_commit<CG>(smem_u32(&bars.acc_full[n & 1]));
-                        k0 = k1;
+                        if (rank == 0) mbar_arrive_expect_tx(full0 + bar, bytes);
+                        boxes_a.load(k, ta, at, signal0 + bar);
+                        boxes_b.load(k, tb, at + a.a_room, signal0 + bar);
+                        ++filled;
+                        advance();
                     }
                 }
-                if (!ok) {  // nor a product
-                    mma_commit<CG>(smem_u32(&bars.drained));
-                    mbar_wait_bounded(smem_u32(&bars.drained), 0, a.err);
+            }
+            // a CTA that has given up leaves no copy in flight
+            if (!ok && rank == 0)
+                for (uint32_t f = filled > (uint32_t)stages ? filled - stages : 0; f < filled; ++f)
+                    mbar_wait_bounded(full0 + 8 * (f % stages), (f / stages) & 1u, a.err);
+        } else if (warp == kVocabWarps + 1 && lane == 0 && rank == 0) {
+            int n = 0;  // parts so far
+            bool ok = true;
+            for (int i = 0; ok && tile_at<N, CG>(a, unit, units, rank, i, &t); ++i) {
+                const TileWork& w = a.work[t.job];
+                const uint32_t desc = mma_desc(CG * kTileM, N, w.a_mn, w.b_mn);
+                // from one sixteen k to the next, in descriptors' units of 16 bytes
+                const uint32_t step_a = w.a_mn ? 16 * 8 : 2, step_b = w.b_mn ? 16 * 8 : 2;
+                const int steps = t.kn * a.pairs;
+                for (int k0 = 0; ok && k0 < steps; ++n) {
+                    const int k1 = PROMOTE ? min(steps, k0 + kPromote) : steps;
+                    const uint32_t acc = tmem + (n & 1) * N;
+                    ok = hold(smem_u32(&bars.acc_empty[n & 1]), ((n >> 1) & 1) ^ 1u, a.err, dead);
+                    if (!ok) break;
+                    tmem_fence_after();
+                    for (int k = k0; k < k1; ++k) {
+                        ok = hold(full0 + bar, phase, a.err, dead);
+                        if (!ok) break;
+                        tmem_fence_after();
+                        const uint64_t da = smem_desc(at, kBoxBytes, 1024);
+                        const uint64_t db = smem_desc(at + a.a_room, kBoxBytes, 1024);
+#pragma unroll
+                        for (int q = 0; q < kTileK / 16; ++q)
+                            mma_bf16<CG>(acc, da + q * step_a, db + q * step_b, desc, k > k0 || q > 0);
+                        mma_commit<CG>(empty0 + bar);
+                        advance();
+                    }
+                    if (ok) mma_commit<CG>(smem_u32(&bars.acc_full[n & 1]));
+                    k0 = k1;
                 }
+            }
+            if (!ok) {  // nor a product
+                mma_commit<CG>(smem_u32(&bars.drained));
+                mbar_wait_bounded(smem_u32(&bars.drained), 0, a.err);
             }
         }
     } else {
@@ -482,7 +494,7 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
         bool ok = true;
         // the accumulators of part n, once they are there
         auto ready = [&]() {
-            ok = __all_sync(0xffffffffu, hold(bars.acc_full[n & 1], (n >> 1) & 1, a.err, dead));
+            ok = __all_sync(0xffffffffu, hold(smem_u32(&bars.acc_full[n & 1]), (n >> 1) & 1, a.err, dead));
             tmem_fence_after();
             return tmem + (n & 1) * N + half * S::kCols + ((uint32_t)(32 * quarter) << 16);
         };
