@@ -124,9 +124,10 @@ template <int CG> __device__ __forceinline__ void mma_commit(uint32_t bar) {
             "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
             "[%0], %1;" :: "r"(bar), "h"((uint16_t)3) : "memory");
 }
-// Arrive on an mbarrier of the cluster.
+// Arrive on an mbarrier of the cluster.  (Released to this CTA alone: what the other
+// one waits for is in tensor memory; a cluster's release waits for global stores.)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
 }
 
 }  // namespace credit

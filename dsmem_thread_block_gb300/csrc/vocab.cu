@@ -217,7 +217,7 @@ cudaError_t launch_vocab(VocabOut out, int dtype, VocabTile tile, const CUtensor
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(units * ctas));
-    cfg.blockDim = dim3(kVocabThreads);
+    cfg.blockDim = dim3((unsigned)vocab_threads(vocab_promotes(out, dtype), vocab_tile_cols(tile)));
     cfg.dynamicSmemBytes = kVocabSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];

@@ -13,11 +13,11 @@ constexpr int kTileK = 64;    // k of a stage
 // The output tile of a CTA or pair of CTAs: rows x columns.
 enum VocabTile : int {
     kPair256,   // 256 x 256, a pair
+    kOne256,    // 128 x 256
     kOne128,    // 128 x 128
-    kOne64,     // 128 x 64
 };
 constexpr int vocab_tile_rows(VocabTile t) { return t == kPair256 ? 2 * kTileM : kTileM; }
-constexpr int vocab_tile_cols(VocabTile t) { return t == kPair256 ? 256 : t == kOne128 ? 128 : 64; }
+constexpr int vocab_tile_cols(VocabTile t) { return t == kOne128 ? 128 : 256; }
 constexpr int vocab_tile_ctas(VocabTile t) { return t == kPair256 ? 2 : 1; }
 
 // A matrix of bf16 terms: `terms` planes of rows x cols, rows `pitch` bytes and
@@ -60,7 +60,7 @@ struct VocabArgs {
     int64_t vocab;
     const int64_t* target;
     int64_t ignore;
-    // statistics: per (half a tile's columns, token) maximum and sum of exponentials, and
+    // statistics: per (half of a tile's columns, token) maximum and sum of exponentials, and
     // the target's logit per token
     float2* parts;
     float* picked;
@@ -75,6 +75,8 @@ struct VocabArgs {
 };
 
 enum VocabOut : int { kVocabStats, kVocabGrad, kVocabProduct };
+// Results that the tensor cores' sums alone are not good enough for.
+constexpr bool vocab_promotes(VocabOut out, int dtype) { return out == kVocabStats || dtype == 0; }
 
 // `boxed`: rows of a box (K innermost: the tile's rows; else the stage's k).
 bool term_map(const TermMatrix& m, int box_rows, CUtensorMap* map);

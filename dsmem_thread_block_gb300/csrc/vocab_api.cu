@@ -28,8 +28,6 @@ constexpr int kMinPart = 8;
 
 // Widest tile: a piece of the vocabulary is whole tiles of any shape.
 constexpr int kTileN = vocab_tile_cols(kPair256);
-// Narrowest half tile: a part of the statistics.
-constexpr int kPartCols = vocab_tile_cols(kOne64) / 2;
 
 struct Shape {
     int64_t tokens, hidden, vocab;
@@ -46,7 +44,7 @@ credit_status_t shape_of(const void* h, const void* w, int64_t tokens, int64_t h
     if (tokens > most || vocab > most || hidden > ((int64_t)1 << 24)) return CREDIT_ERR_INVALID_ARG;
     // (tiles of a launch, too)
     const int64_t tiles = ceil_div(tokens, kTileM) * ceil_div(vocab, kTileM);
-    const int64_t wide = ceil_div(std::max(tokens, vocab), kTileM) * ceil_div(hidden, kPartCols);
+    const int64_t wide = ceil_div(std::max(tokens, vocab), kTileM) * ceil_div(hidden, kTileM);
     if (tiles > ((int64_t)1 << 28) || wide > ((int64_t)1 << 28)) return CREDIT_ERR_INVALID_ARG;
     s->tokens = tokens;
     s->hidden = hidden;
@@ -82,19 +80,27 @@ struct Layout {
     }
 };
 
-// A tile's time in a launch, in stages of k of a 128 x 256 tile: its products, and
-// what a tile costs besides them.
+// A tile's time in a launch, in stages of a pair: four products of sixteen k take
+// 512 cycles whatever the tile's shape (a CTA alone with 256 columns, which stages
+// half as much again, takes a tenth longer: backward 4096 x 4096 x 65536 3.83 ms
+// instead of 3.49); the epilogue, which runs beside the next tile's products, some
+// eight of that for 256 columns a CTA.
 double tile_cost(VocabTile t, double stages) {
-    return stages * vocab_tile_cols(t) / 256 + 2.0;
+    return std::max(t == kOne256 ? 1.1 * stages : stages, vocab_tile_cols(t) / 32.0) + 1.0;
 }
+// What the first tile waits for besides: a pair's CTAs meet, and a wide tile's
+// epilogue stands alone at the end.
+double launch_cost(VocabTile t) { return t == kPair256 ? 10.0 : t == kOne256 ? 4.0 : 0.0; }
+constexpr VocabTile kTiles[] = {kPair256, kOne256, kOne128};
 // The shape whose tiles end first.
 VocabTile tile_for(int64_t rows, int64_t cols, int64_t stages, int sms) {
     VocabTile best = kPair256;
     double least = 0;
-    for (const VocabTile t : {kPair256, kOne128, kOne64}) {
+    for (const VocabTile t : kTiles) {
         const int64_t tiles = ceil_div(rows, vocab_tile_rows(t)) * ceil_div(cols, vocab_tile_cols(t));
-        const double time = (double)ceil_div(tiles, sms / vocab_tile_ctas(t)) * tile_cost(t, (double)stages);
-        if (t == kPair256 || time < 0.9 * least) {
+        const double time = (double)ceil_div(tiles, sms / vocab_tile_ctas(t)) *
+                                tile_cost(t, (double)stages) + launch_cost(t);
+        if (t == kPair256 || time < least) {
             best = t;
             least = time;
         }
@@ -127,7 +133,7 @@ Products products_for(const Shape& s, int64_t piece, bool dh, bool dw, int sms) 
     double least = 0;
     const int64_t kb = ceil_div(piece, kTileK), kt = ceil_div(s.tokens, kTileK);
     const int pairs = s.terms == 1 ? 1 : 6;
-    for (const VocabTile t : {kPair256, kOne128, kOne64}) {
+    for (const VocabTile t : kTiles) {
         const int rows = vocab_tile_rows(t), cols = vocab_tile_cols(t), units = sms / vocab_tile_ctas(t);
         const int64_t nt = ceil_div(s.hidden, cols);
         const int64_t th = dh ? ceil_div(s.tokens, rows) * nt : 0, tw = dw ? ceil_div(piece, rows) * nt : 0;
@@ -136,8 +142,7 @@ Products products_for(const Shape& s, int64_t piece, bool dh, bool dw, int sms) 
         Products p{t, 1, (int32_t)kb};
         double time = all / units;
         if (dh) {
-            const double stage = (double)pairs * cols / 256;
-            const int64_t share = std::max<int64_t>(kMinPart, (int64_t)(all / units / 2 / stage));
+            const int64_t share = std::max<int64_t>(kMinPart, (int64_t)(all / units / 2 / pairs));
             const int64_t want = std::min<int64_t>(ceil_div(kb, share), kMaxSplits);
             p.per = (int32_t)ceil_div(kb, want);
             p.splits = (int32_t)ceil_div(kb, p.per);
@@ -146,7 +151,8 @@ Products products_for(const Shape& s, int64_t piece, bool dh, bool dw, int sms) 
         } else {
             time = (double)ceil_div(tw, units) * tile_cost(t, (double)(kt * pairs));
         }
-        if (t == kPair256 || time < 0.9 * least) {
+        time += launch_cost(t);
+        if (t == kPair256 || time < least) {
             best = p;
             least = time;
         }

@@ -3,6 +3,8 @@
 
 namespace credit {
 const void* vocab_grad_kernel(int dtype, VocabTile t) {
-    return dtype ? vocab_kernel_of<GradOut<bf16>, false>(t) : vocab_kernel_of<GradOut<float>, true>(t);
+    return dtype
+               ? vocab_kernel_of<GradOut<bf16>, vocab_promotes(kVocabGrad, 1)>(t)
+               : vocab_kernel_of<GradOut<float>, vocab_promotes(kVocabGrad, 0)>(t);
 }
 }  // namespace credit

@@ -2,5 +2,5 @@
 #include "vocab_tiles.cuh"
 
 namespace credit {
-const void* vocab_stats_kernel(VocabTile t) { return vocab_kernel_of<StatsOut, true>(t); }
+const void* vocab_stats_kernel(VocabTile t) { return vocab_kernel_of<StatsOut, vocab_promotes(kVocabStats, 0)>(t); }
 }  // namespace credit

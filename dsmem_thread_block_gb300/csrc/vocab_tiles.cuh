@@ -23,14 +23,19 @@
 
 namespace credit {
 
-constexpr int kVocabWarps = 8;                  // of the epilogue: two a quarter of the rows
-constexpr int kVocabThreads = 32 * (kVocabWarps + 4);  // whole warpgroups; two warps only wait
+// Warps of the epilogue: a quarter of them for each 32 of a tile's 128 rows.  One
+// warp's chain of loads, exponentials and stores leaves two of three issue slots
+// empty, so there are sixteen, but where the parts' sums take their registers, and
+// for narrow tiles, of small calls, whose launch they would only make longer.
+constexpr int vocab_warps(bool promote, int columns) { return promote || columns < 256 ? 8 : 16; }
+// whole warpgroups; two of the other four warps only wait
+constexpr int vocab_threads(bool promote, int columns) { return 32 * (vocab_warps(promote, columns) + 4); }
 constexpr int kBoxBytes = 64 * kTileK * 2;      // one box of an operand with M or N innermost
 constexpr int kBytesA = kTileM * kTileK * 2;
 constexpr int kVocabRing = 6 * 32768;           // bytes of all stages
 constexpr int kVocabStages = 16;                // most of them
-constexpr int kStageOut = 32 * 128;             // a warp's room to turn its output around
-constexpr int kVocabSmem = kVocabRing + kVocabWarps * kStageOut + 1024;  // aligned to 1024 by hand
+constexpr int kTurnBytes = 32 * 64;             // a warp's room to turn its output around
+constexpr int kVocabSmem = kVocabRing + 16 * kTurnBytes + 1024;  // aligned to 1024 by hand
 constexpr int kPromote = 8;                     // stages of a part
 
 // A tile is 128 rows a CTA by N columns (CG = 2: a pair shares the columns'
@@ -38,7 +43,6 @@ constexpr int kPromote = 8;                     // stages of a part
 template <int N, int CG> struct TileShape {
     static constexpr int kRowsB = N / CG;       // of B a CTA stages
     static constexpr int kBytesB = kRowsB * kTileK * 2;
-    static constexpr int kCols = N / 2;         // of an epilogue warp
     static constexpr uint32_t kTmem = 2 * N;    // two accumulators
 };
 
@@ -145,41 +149,38 @@ __device__ __forceinline__ float rest_of(float x, float term) {
 // ------------------------------------------------------------ the epilogues
 // Each takes 32 columns of a warp's 32 rows at a time, from column c of the tile
 // on: lane i holds those of row row0 + i.  What goes to memory is turned around in
-// shared memory, 16-byte vectors permuted within a row so that both ways are free
-// of bank conflicts, so that consecutive lanes write consecutive columns: a lane a
-// row wrote 1.07 GB of dweight in 745 us where this takes
-// PLACEHOLDER_DW.
-//
-// A warp's 32 rows of 32 elements of E bytes.
-template <int E> struct Turn {
-    static constexpr int kVecs = 32 * E / 16;   // of a row
+// shared memory, so that consecutive lanes write consecutive columns.
+
+// 32 rows of 64 bytes (32 bf16 or 16 fp32 elements); 16-byte vectors are permuted
+// within a row so that both ways are free of bank conflicts.
+struct Turn {
     unsigned char* room;
     int lane;
     __device__ __forceinline__ uint4* at(int row, int vec) const {
-        const int x = E == 4 ? row & 7 : (row >> 1) & 3;
-        return reinterpret_cast<uint4*>(room + row * (32 * E)) + (vec ^ x);
+        return reinterpret_cast<uint4*>(room + row * 64) + (vec ^ ((row >> 1) & 3));
     }
-    __device__ __forceinline__ void put(const uint32_t (&w)[8 * E]) const {
+    __device__ __forceinline__ void put(const uint32_t (&w)[16]) const {
         __syncwarp();   // the last block has been read
 #pragma unroll
-        for (int k = 0; k < kVecs; ++k)
-            *at(lane, k) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        for (int k = 0; k < 4; ++k) *at(lane, k) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
         __syncwarp();
     }
-    // f(row, first column, vector) for a lane's vectors
+    // f(row, vector of the row, its value): a lane's four vectors
     template <typename F> __device__ __forceinline__ void vectors(F f) const {
 #pragma unroll
-        for (int k = 0; k < kVecs; ++k) {
-            const int row = (lane + 32 * k) / kVecs, vec = lane % kVecs;
-            f(row, vec * (16 / E), *at(row, vec));
+        for (int k = 0; k < 4; ++k) {
+            const int row = lane / 4 + 8 * k, vec = lane % 4;
+            f(row, vec, *at(row, vec));
         }
     }
-    // element `lane` of a row
-    __device__ __forceinline__ uint32_t element(int row) const {
-        const unsigned char* const p = reinterpret_cast<const unsigned char*>(at(row, lane * E / 16)) +
-                                       lane * E % 16;
-        if constexpr (E == 4) return *reinterpret_cast<const uint32_t*>(p);
-        else return *reinterpret_cast<const uint16_t*>(p);
+    // f(row, element of the row, its value): a lane's elements, of type W
+    template <typename W, typename F> __device__ __forceinline__ void elements(F f) const {
+        constexpr int kRow = 64 / sizeof(W), kRows = 32 / kRow;  // of a row; rows at a time
+#pragma unroll 4
+        for (int r = 0; r < 32; r += kRows) {
+            const int row = r + lane / kRow, e = lane % kRow;
+            f(row, e, *(reinterpret_cast<const W*>(at(row, e * sizeof(W) / 16)) + e % (16 / sizeof(W))));
+        }
     }
 };
 __device__ __forceinline__ void halves(const float (&g)[32], uint32_t (&w)[16]) {
@@ -207,13 +208,11 @@ struct StatsOut {
             for (int j = 0; j < 32; ++j)
                 if (c + j >= left) v[j] = __float_as_uint(-INFINITY);
         }
-        float t0 = m, t1 = __uint_as_float(v[1]);
+        float t[4] = {m, m, m, m};
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-            t0 = fmaxf(t0, __uint_as_float(v[j]));
-            t1 = fmaxf(t1, __uint_as_float(v[j + 1]));
-        }
-        const float top = fmaxf(t0, t1);
+        for (int j = 0; j < 32; j += 2)
+            t[j / 2 % 4] = fmaxf(t[j / 2 % 4], fmaxf(__uint_as_float(v[j]), __uint_as_float(v[j + 1])));
+        const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
         // nothing is above an infinite maximum: exponents are then taken from zero
         const float base = isinf(top) ? 0.f : top;
         if (top != m) {
@@ -221,13 +220,14 @@ struct StatsOut {
             m = top;
         }
         const float off = -base * kLog2e;
-        float s0 = 0.f, s1 = 0.f;
+        F2 sums[2] = {f2(0.f), f2(0.f)};
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
-            s0 += fast_ex2(fmaf(__uint_as_float(v[j]), kLog2e, off));
-            s1 += fast_ex2(fmaf(__uint_as_float(v[j + 1]), kLog2e, off));
+            const F2 x = fma2(F2{__uint_as_float(v[j]), __uint_as_float(v[j + 1])}, f2(kLog2e), f2(off));
+            sums[j / 2 % 2] = add2(sums[j / 2 % 2], F2{fast_ex2(x.x), fast_ex2(x.y)});
         }
-        s += s0 + s1;
+        const F2 both = add2(sums[0], sums[1]);
+        s += both.x + both.y;
         if (to >= c && to < c + 32) {
             float z = 0.f;
 #pragma unroll
@@ -249,7 +249,7 @@ template <typename T> struct GradOut {
     int rows;            // of the warp's that there are
     bool none;
     bf16* out;           // the warp's first row
-    const Turn<2> turn;
+    const Turn turn;
     __device__ GradOut(const VocabArgs& args, const Tile& t, int row0, unsigned char* room)
         : a(args), turn{room, (int)threadIdx.x & 31} {
         const int row = row0 + turn.lane;
@@ -269,8 +269,8 @@ template <typename T> struct GradOut {
         uint32_t w[16];
         halves(g, w);
         turn.put(w);
-        turn.vectors([&](int row, int col, uint4 v) {
-            if (row < rows) *reinterpret_cast<uint4*>(p + (int64_t)row * a.grad_pitch + col) = v;
+        turn.vectors([&](int row, int vec, uint4 v) {
+            if (row < rows) *reinterpret_cast<uint4*>(p + (int64_t)row * a.grad_pitch + 8 * vec) = v;
         });
     }
     __device__ __forceinline__ void take(int c, const uint32_t (&v)[32]) {
@@ -311,53 +311,61 @@ template <typename T> struct ProductRow {
     int left, rows;
     float* sums;
     T* out;
-    const Turn<4> wide;
-    const Turn<sizeof(T)> turn;
+    const Turn turn;
     __device__ ProductRow(const VocabArgs& a, const Tile& t, int row0, unsigned char* room)
-        : o(a.out[t.job]), wide{room, (int)threadIdx.x & 31}, turn{room, (int)threadIdx.x & 31} {
+        : o(a.out[t.job]), turn{room, (int)threadIdx.x & 31} {
         rows = o.rows - row0;
         left = o.cols - t.n0;
         sums = o.sums ? o.sums + ((int64_t)t.split * o.rows + row0) * o.pitch + t.n0 : nullptr;
         out = static_cast<T*>(o.out) + (int64_t)row0 * o.pitch + t.n0;
     }
+    // 64 bytes of each row, E a vector's elements, to memory from column c on
+    template <int E> __device__ __forceinline__ void write(int c) const {
+        if (o.vec) {  // (a row's columns are whole vectors)
+            turn.vectors([&](int row, int vec, uint4 w) {
+                if (row < rows && c + E * vec < left)
+                    __stcs(reinterpret_cast<uint4*>(out + row * o.pitch + c + E * vec), w);
+            });
+        } else {
+            using Word = std::conditional_t<E == 4, uint32_t, uint16_t>;
+            turn.template elements<Word>([&](int row, int e, Word w) {
+                if (row < rows && c + e < left) reinterpret_cast<Word*>(out + row * o.pitch + c)[e] = w;
+            });
+        }
+    }
     __device__ __forceinline__ void take(int c, const uint32_t (&v)[32]) {
         if (c >= left || rows <= 0) return;
-        if (sums) {  // (rows of sums are whole vectors)
-            wide.put(v);
-            wide.vectors([&](int row, int col, uint4 w) {
-                if (row >= rows || c + col >= left) return;
-                float4 f = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z),
-                                       __uint_as_float(w.w));
-                float4* const p = reinterpret_cast<float4*>(sums + row * o.pitch + c + col);
-                if (o.add) {
-                    const float4 b = __ldcg(p);
-                    f = make_float4(b.x + f.x, b.y + f.y, b.z + f.z, b.w + f.w);
+        uint32_t w[16];
+        if (sums || sizeof(T) == 4) {
+#pragma unroll
+            for (int half = 0; half < 32; half += 16) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) w[j] = v[half + j];
+                turn.put(w);
+                if (sums) {  // (rows of sums are whole vectors)
+                    turn.vectors([&](int row, int vec, uint4 x) {
+                        const int col = c + half + 4 * vec;
+                        if (row >= rows || col >= left) return;
+                        float4 f = make_float4(__uint_as_float(x.x), __uint_as_float(x.y),
+                                               __uint_as_float(x.z), __uint_as_float(x.w));
+                        float4* const p = reinterpret_cast<float4*>(sums + row * o.pitch + col);
+                        if (o.add) {
+                            const float4 b = __ldcg(p);
+                            f = make_float4(b.x + f.x, b.y + f.y, b.z + f.z, b.w + f.w);
+                        }
+                        __stcg(p, f);
+                    });
+                } else {
+                    write<4>(c + half);
                 }
-                __stcg(p, f);
-            });
-            return;
-        }
-        if constexpr (sizeof(T) == 4) {
-            turn.put(v);
+            }
         } else {
             float f[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
-            uint32_t w[16];
             halves(f, w);
             turn.put(w);
-        }
-        if (o.vec) {  // (a row's columns are whole vectors)
-            turn.vectors([&](int row, int col, uint4 w) {
-                if (row < rows && c + col < left)
-                    __stcs(reinterpret_cast<uint4*>(out + row * o.pitch + c + col), w);
-            });
-        } else if (c + turn.lane < left) {
-            using Word = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
-#pragma unroll 4
-            for (int row = 0; row < 32; ++row)
-                if (row < rows)
-                    reinterpret_cast<Word*>(out + row * o.pitch + c)[turn.lane] = (Word)turn.element(row);
+            write<8>(c);
         }
     }
     __device__ __forceinline__ void done(int) {}
@@ -365,11 +373,12 @@ template <typename T> struct ProductRow {
 
 // ---------------------------------------------------------------- the kernel
 template <typename OUT, bool PROMOTE, int N, int CG>
-__global__ void __launch_bounds__(kVocabThreads, 1)
+__global__ void __launch_bounds__(vocab_threads(PROMOTE, N), 1)
 vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUtensorMap b0,
             const __grid_constant__ CUtensorMap a1, const __grid_constant__ CUtensorMap b1,
             const __grid_constant__ VocabArgs a) {
     using S = TileShape<N, CG>;
+    constexpr int kWarps = vocab_warps(PROMOTE, N), kCols = N / (kWarps / 4);  // a warp's
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) VocabBars bars;
     __shared__ uint32_t tmem_base;
@@ -388,13 +397,13 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&bars.acc_full[s]), 1);
-            mbar_init(smem_u32(&bars.acc_empty[s]), CG * kVocabWarps);
+            mbar_init(smem_u32(&bars.acc_empty[s]), CG * kWarps);
         }
         mbar_init(smem_u32(&bars.drained), 1);
         fence_mbar_init();
         fence_proxy_async_smem();
     }
-    if (warp == kVocabWarps + 1) tmem_alloc<CG>(smem_u32(&tmem_base), S::kTmem);
+    if (warp == kWarps + 1) tmem_alloc<CG>(smem_u32(&tmem_base), S::kTmem);
     tmem_fence_before();
     __syncthreads();
     if constexpr (CG > 1) {  // the other CTA's barriers are there
@@ -408,7 +417,7 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
     Tile t;
     // The sums of an epilogue thread take registers that the other warps do not
     // need: of 384 x 168 at launch, 128 x 80 and 256 x 208.
-    if (warp >= kVocabWarps) {
+    if (warp >= kWarps) {
         if constexpr (PROMOTE) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         const uint32_t full0 = smem_u32(&bars.full[0]), empty0 = smem_u32(&bars.empty[0]);
         const uint32_t end = ring + (uint32_t)(stages * stage);
@@ -422,7 +431,7 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                 phase ^= 1u;
             }
         };
-        if (warp == kVocabWarps && lane == 0) {
+        if (warp == kWarps && lane == 0) {
             // both CTAs' bytes count on the first one's barriers
             const uint32_t signal0 = CG > 1 ? mapa_shared(full0, 0) : full0;
             uint32_t filled = 0;  // fills in all
@@ -450,7 +459,7 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
             if (!ok && rank == 0)
                 for (uint32_t f = filled > (uint32_t)stages ? filled - stages : 0; f < filled; ++f)
                     mbar_wait_bounded(full0 + 8 * (f % stages), (f / stages) & 1u, a.err);
-        } else if (warp == kVocabWarps + 1 && lane == 0 && rank == 0) {
+        } else if (warp == kWarps + 1 && lane == 0 && rank == 0) {
             int n = 0;  // parts so far
             bool ok = true;
             for (int i = 0; ok && tile_at<N, CG>(a, unit, units, rank, i, &t); ++i) {
@@ -473,7 +482,8 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                         const uint64_t db = smem_desc(at + a.a_room, kBoxBytes, 1024);
 #pragma unroll
                         for (int q = 0; q < kTileK / 16; ++q)
-                            mma_bf16<CG>(acc, da + q * step_a, db + q * step_b, desc, k > k0 || q > 0);
+                            mma_bf16<CG>(acc, da + q * step_a, db + q * step_b, desc,
+                                         k > k0 || q > 0);
                         mma_commit<CG>(empty0 + bar);
                         advance();
                     }
@@ -488,15 +498,15 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
         }
     } else {
         if constexpr (PROMOTE) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-        const int quarter = warp & 3, half = warp >> 2;
-        unsigned char* const room = raw + (ring - smem_u32(raw)) + kVocabRing + warp * kStageOut;
+        const int quarter = warp & 3, block = warp >> 2;  // of rows, of columns
+        unsigned char* const room = raw + (ring - smem_u32(raw)) + kVocabRing + warp * kTurnBytes;
         int n = 0;
         bool ok = true;
         // the accumulators of part n, once they are there
         auto ready = [&]() {
             ok = __all_sync(0xffffffffu, hold(smem_u32(&bars.acc_full[n & 1]), (n >> 1) & 1, a.err, dead));
             tmem_fence_after();
-            return tmem + (n & 1) * N + half * S::kCols + ((uint32_t)(32 * quarter) << 16);
+            return tmem + (n & 1) * N + block * kCols + ((uint32_t)(32 * quarter) << 16);
         };
         auto release = [&]() {
             tmem_fence_before();
@@ -511,48 +521,49 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
         for (int i = 0; ok && tile_at<N, CG>(a, unit, units, rank, i, &t); ++i) {
             OUT out(a, t, t.m0 + 32 * quarter, room);
             if constexpr (PROMOTE) {
-                F2 sum[S::kCols / 2];
+                F2 sum[kCols / 2];
+#pragma unroll
+                for (int j = 0; j < kCols / 2; ++j) sum[j] = f2(0.f);
                 const int steps = t.kn * a.pairs;
                 for (int k0 = 0; k0 < steps; k0 += kPromote) {
                     const uint32_t acc = ready();
                     if (!ok) break;
 #pragma unroll
-                    for (int c = 0; c < S::kCols; c += 32) {
+                    for (int c = 0; c < kCols; c += 32) {
                         uint32_t v[32];
                         tmem_load(acc + c, v);
-                        tmem_load_wait();
+                    tmem_load_wait();
 #pragma unroll
                         for (int j = 0; j < 32; j += 2) {
                             const F2 x{__uint_as_float(v[j]), __uint_as_float(v[j + 1])};
-                            F2& y = sum[(c + j) / 2];
-                            y = k0 ? add2(y, x) : x;
+                            sum[(c + j) / 2] = add2(sum[(c + j) / 2], x);
                         }
                     }
                     release();
                 }
                 if (!ok) break;
 #pragma unroll
-                for (int c = 0; c < S::kCols; c += 32) {
+                for (int c = 0; c < kCols; c += 32) {
                     uint32_t v[32];
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
                         v[j] = __float_as_uint(sum[(c + j) / 2].x);
                         v[j + 1] = __float_as_uint(sum[(c + j) / 2].y);
                     }
-                    out.take(half * S::kCols + c, v);
+                    out.take(block * kCols + c, v);
                 }
             } else {
                 const uint32_t acc = ready();
                 if (!ok) break;
-                for (int c = 0; c < S::kCols; c += 32) {
+                for (int c = 0; c < kCols; c += 32) {
                     uint32_t v[32];
                     tmem_load(acc + c, v);
                     tmem_load_wait();
-                    out.take(half * S::kCols + c, v);
+                    out.take(block * kCols + c, v);
                 }
                 release();
             }
-            out.done(t.n0 / S::kCols + half);
+            out.done(t.n0 / kCols + block);
         }
     }
     __syncwarp();
@@ -563,14 +574,14 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
         cluster_wait_acquire();
     }
     tmem_fence_after();
-    if (warp == kVocabWarps + 1) tmem_free<CG>(tmem, S::kTmem);
+    if (warp == kWarps + 1) tmem_free<CG>(tmem, S::kTmem);
 }
 
 template <typename OUT, bool PROMOTE> const void* vocab_kernel_of(VocabTile t) {
     switch (t) {
         case kPair256: return (const void*)vocab_tiles<OUT, PROMOTE, 256, 2>;
-        case kOne128: return (const void*)vocab_tiles<OUT, PROMOTE, 128, 1>;
-        default: return (const void*)vocab_tiles<OUT, PROMOTE, 64, 1>;
+        case kOne256: return (const void*)vocab_tiles<OUT, PROMOTE, 256, 1>;
+        default: return (const void*)vocab_tiles<OUT, PROMOTE, 128, 1>;
     }
 }
 
