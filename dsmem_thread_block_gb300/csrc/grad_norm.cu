@@ -18,6 +18,8 @@ constexpr int kThreads = 256;
 constexpr int kLoads = 8;                           // 16-byte vectors of a thread and chunk
 constexpr int kChunkBytes = kThreads * kLoads * 16;
 constexpr int kCtasPerSm = 4;
+// Of L2, what the sums leave there for the scaling: the last chunks of every CTA.
+constexpr int kKeepNum = 1, kKeepDen = 2;
 
 // The tensors of a launch, in its parameters: captured with it, nothing to copy
 // or keep.  Chunks are counted through all tensors; a tensor's start at its
@@ -93,14 +95,14 @@ template <typename T> struct Vectors {
     __device__ __forceinline__ bool whole(int k, int64_t count) const {
         return at(k) >= 0 && at(k) + kVec <= count;
     }
-    __device__ __forceinline__ void load(const T* p, int64_t count, int64_t chunk) {
+    __device__ __forceinline__ void load(const T* p, int64_t count, int64_t chunk, uint64_t policy) {
         const int shift = (int)(((uintptr_t)p & 15) / sizeof(T));
         e0 = chunk * (kChunkBytes / (int)sizeof(T)) + threadIdx.x * kVec - shift;
 #pragma unroll
         for (int k = 0; k < kLoads; ++k) {
             v[k] = make_uint4(0, 0, 0, 0);
             if (whole(k, count)) {
-                v[k] = *reinterpret_cast<const uint4*>(p + at(k));
+                v[k] = ld_global_l2hint_v4(p + at(k), policy);
             } else if (at(k) < count) {
                 T x[kVec];
 #pragma unroll
@@ -113,9 +115,10 @@ template <typename T> struct Vectors {
 };
 
 template <typename T>
-__device__ __forceinline__ double chunk_squares(const void* p, int64_t count, int64_t chunk) {
+__device__ __forceinline__ double chunk_squares(const void* p, int64_t count, int64_t chunk,
+                                                uint64_t policy) {
     Vectors<T> x;
-    x.load(static_cast<const T*>(p), count, chunk);
+    x.load(static_cast<const T*>(p), count, chunk, policy);
     Squares s;
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) {
@@ -131,7 +134,7 @@ template <typename T>
 __device__ __forceinline__ void chunk_scale(const void* p, void* out, int64_t count, int64_t chunk,
                                             float factor) {
     Vectors<T> x;
-    x.load(static_cast<const T*>(p), count, chunk);
+    x.load(static_cast<const T*>(p), count, chunk, l2_policy_evict_first());
     T* const y = static_cast<T*>(out);
     const bool lines = (((uintptr_t)p ^ (uintptr_t)out) & 15) == 0;
 #pragma unroll
@@ -153,7 +156,7 @@ __device__ __forceinline__ void chunk_scale(const void* p, void* out, int64_t co
 
 template <int N>
 __global__ void __launch_bounds__(kThreads)
-grad_squares(const __grid_constant__ Table<N> t, double* parts) {
+grad_squares(const __grid_constant__ Table<N> t, double* parts, int keep) {
     dependents_may_launch();
     wait_for_launches();
     int lo, hi;
@@ -163,8 +166,9 @@ grad_squares(const __grid_constant__ Table<N> t, double* parts) {
     for (int c = lo; c < hi; ++c) {
         while (c >= t.first[i + 1]) ++i;
         const int64_t chunk = c - t.first[i];
-        sum += t.half[i] ? chunk_squares<bf16>(t.p[i], t.count[i], chunk)
-                         : chunk_squares<float>(t.p[i], t.count[i], chunk);
+        const uint64_t policy = c < hi - keep ? l2_policy_evict_first() : l2_policy_evict_last();
+        sum += t.half[i] ? chunk_squares<bf16>(t.p[i], t.count[i], chunk, policy)
+                         : chunk_squares<float>(t.p[i], t.count[i], chunk, policy);
     }
     sum = cta_sum(sum);
     if (threadIdx.x == 0) parts[blockIdx.x] = sum;
@@ -295,7 +299,7 @@ credit_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? CREDIT_OK :
 
 template <int N>
 cudaError_t launch_batch(const credit_tensor_t* t, const Batch& b, double* parts, int nparts,
-                         bool scale, float max_norm, float eps, float* norm, bool in_place,
+                         bool scale, float max_norm, float eps, float* norm, bool in_place, int keep,
                          cudaStream_t s) {
     Table<N> table;
     fill<N>(t, b, &table);
@@ -306,16 +310,17 @@ cudaError_t launch_batch(const credit_tensor_t* t, const Batch& b, double* parts
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    void* sum_args[] = {&table, &parts};
+    void* sum_args[] = {&table, &parts, &keep};
     void* scale_args[] = {&table, &parts, &nparts, &max_norm, &eps, &norm, &in_place};
     return scale ? cudaLaunchKernelExC(&cfg, (const void*)grad_scale<N>, scale_args)
                  : cudaLaunchKernelExC(&cfg, (const void*)grad_squares<N>, sum_args);
 }
 
 cudaError_t launch_any(const credit_tensor_t* t, const Batch& b, double* parts, int nparts, bool scale,
-                       float max_norm, float eps, float* norm, bool in_place, cudaStream_t s) {
-    return b.n <= kSmall ? launch_batch<kSmall>(t, b, parts, nparts, scale, max_norm, eps, norm, in_place, s)
-                         : launch_batch<kLarge>(t, b, parts, nparts, scale, max_norm, eps, norm, in_place, s);
+                       float max_norm, float eps, float* norm, bool in_place, int keep, cudaStream_t s) {
+    return b.n <= kSmall
+               ? launch_batch<kSmall>(t, b, parts, nparts, scale, max_norm, eps, norm, in_place, keep, s)
+               : launch_batch<kLarge>(t, b, parts, nparts, scale, max_norm, eps, norm, in_place, keep, s);
 }
 
 credit_status_t run(const credit_tensor_t* t, int64_t n, bool clip, float max_norm, float eps,
@@ -341,9 +346,14 @@ credit_status_t run(const credit_tensor_t* t, int64_t n, bool clip, float max_no
         return CREDIT_ERR_INVALID_ARG;
     cudaStream_t s = (cudaStream_t)stream;
     double* const parts = static_cast<double*>(workspace);
+    // chunks of a CTA that stay in L2 until they are scaled
+    const int keep = clip ? (int)((int64_t)d->l2_bytes / kKeepDen * kKeepNum /
+                                  ((int64_t)kChunkBytes * d->sms * kCtasPerSm))
+                          : 0;
     int64_t at = 0;
     for (const Batch& b : batches) {
-        if ((st = from_cuda(launch_any(t, b, parts + at, 0, false, 0, 0, nullptr, false, s))) != CREDIT_OK)
+        if ((st = from_cuda(launch_any(t, b, parts + at, 0, false, 0, 0, nullptr, false, keep, s))) !=
+            CREDIT_OK)
             return st;
         at += b.grid;
     }
@@ -353,7 +363,7 @@ credit_status_t run(const credit_tensor_t* t, int64_t n, bool clip, float max_no
     }
     for (size_t i = batches.size(); i-- > 0;) {
         st = from_cuda(launch_any(t, batches[i], parts, (int)nparts, true, max_norm, eps,
-                                  i ? nullptr : norm, in_place, s));
+                                  i ? nullptr : norm, in_place, 0, s));
         if (st != CREDIT_OK) return st;
     }
     return CREDIT_OK;
