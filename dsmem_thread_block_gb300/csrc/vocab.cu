@@ -111,27 +111,41 @@ __global__ void __launch_bounds__(256) vocab_pack(PackArgs a) {
     }
 }
 
-// The splits' sums, four columns a thread.
-template <typename T>
+// The splits' sums, four columns a thread.  Where there are many splits of few
+// sums, G threads share a column's, each every Gth split, and the first adds theirs
+// in order.
+template <typename T, int G>
 __global__ void __launch_bounds__(256)
 vocab_sum(const float* sums, int splits, int64_t rows, int cols, int64_t pitch, T* out, bool vec) {
+    constexpr int kColumns = 256 / G;
+    __shared__ float4 parts[G > 1 ? G : 1][G > 1 ? kColumns : 1];
     dependents_may_launch();
     wait_for_launches();
-    const int vecs = (cols + 3) / 4;
-    const int64_t step = (int64_t)gridDim.x * 256, drow = step / vecs, plane = rows * pitch;
-    const int dvec = (int)(step - drow * vecs);
-    const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    int64_t r = first / vecs;
-    int v = (int)(first - r * vecs);
-    while (r < rows) {
-        const float* p = sums + r * pitch + 4 * v;
-        float4 f = __ldcs(reinterpret_cast<const float4*>(p));
+    const int vecs = (cols + 3) / 4, lane = (int)threadIdx.x % kColumns, group = (int)threadIdx.x / kColumns;
+    const int64_t plane = rows * pitch, n = rows * vecs;
+    for (int64_t i0 = (int64_t)blockIdx.x * kColumns; i0 < n; i0 += (int64_t)gridDim.x * kColumns) {
+        const int64_t i = i0 + lane, r = i / vecs;
+        const int v = (int)(i - r * vecs);
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < n) {
+            const float* p = sums + r * pitch + 4 * v + group * plane;
 #pragma unroll 4
-        for (int s = 1; s < splits; ++s) {
-            p += plane;
-            const float4 g = __ldcs(reinterpret_cast<const float4*>(p));
-            f = make_float4(f.x + g.x, f.y + g.y, f.z + g.z, f.w + g.w);
+            for (int s = group; s < splits; s += G, p += G * plane) {
+                const float4 g = __ldcs(reinterpret_cast<const float4*>(p));
+                f = make_float4(f.x + g.x, f.y + g.y, f.z + g.z, f.w + g.w);
+            }
         }
+        if constexpr (G > 1) {
+            __syncthreads();
+            parts[group][lane] = f;
+            __syncthreads();
+            if (group) continue;
+            for (int k = 1; k < G; ++k) {
+                const float4 g = parts[k][lane];
+                f = make_float4(f.x + g.x, f.y + g.y, f.z + g.z, f.w + g.w);
+            }
+        }
+        if (i >= n) continue;
         T* const q = out + r * cols + 4 * v;
         const float x[4] = {f.x, f.y, f.z, f.w};
         if (vec) {
@@ -142,12 +156,6 @@ vocab_sum(const float* sums, int splits, int64_t rows, int cols, int64_t pitch, 
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 if (4 * v + k < cols) q[k] = Elem<T>::from_f(x[k]);
-        }
-        r += drow;
-        v += dvec;
-        if (v >= vecs) {
-            v -= vecs;
-            ++r;
         }
     }
 }
@@ -192,7 +200,7 @@ bool term_map(const TermMatrix& m, int box_rows, CUtensorMap* map) {
 
 cudaError_t launch_vocab(VocabOut out, int dtype, VocabTile tile, const CUtensorMap (&maps)[4],
                          const VocabArgs& args, int sms, cudaStream_t s) {
-    const void* fn = out == kVocabStats ? vocab_stats_kernel(tile)
+    const void* fn = out == kVocabStats ? vocab_stats_kernel(dtype, tile)
                      : out == kVocabGrad ? vocab_grad_kernel(dtype, tile)
                                          : vocab_product_kernel(dtype, tile);
     int dev;
@@ -258,12 +266,15 @@ cudaError_t launch_vocab_pack(int dtype, const void* const (&src)[2], const Term
 
 cudaError_t launch_vocab_sum(int dtype, const float* sums, int splits, int64_t rows, int64_t cols,
                              int64_t pitch, void* out, int sms, cudaStream_t s) {
-    const dim3 grid((unsigned)blocks_for(rows * ((cols + 3) / 4), sms));
-    const bool vec = (uintptr_t)out % 16 == 0 && cols % 4 == 0;
-    return dtype == 0 ? launch_early(vocab_sum<float>, grid, 256, s, sums, splits, rows, (int)cols, pitch,
-                                     static_cast<float*>(out), vec)
-                      : launch_early(vocab_sum<bf16>, grid, 256, s, sums, splits, rows, (int)cols, pitch,
-                                     static_cast<bf16*>(out), vec);
+    const int64_t n = rows * ((cols + 3) / 4);
+    const bool vec = (uintptr_t)out % 16 == 0 && cols % 4 == 0, shared = splits >= 16;
+    const dim3 grid((unsigned)blocks_for(shared ? 16 * n : n, sms));
+    auto run = [&](auto* fn, auto* o) {
+        return launch_early(fn, grid, 256, s, sums, splits, rows, (int)cols, pitch, o, vec);
+    };
+    if (dtype == 0)
+        return run(shared ? vocab_sum<float, 16> : vocab_sum<float, 1>, static_cast<float*>(out));
+    return run(shared ? vocab_sum<bf16, 16> : vocab_sum<bf16, 1>, static_cast<bf16*>(out));
 }
 
 }  // namespace credit

@@ -52,7 +52,7 @@ struct ProductOut {
 
 struct VocabArgs {
     TileWork work[2];
-    int32_t jobs, pairs;   // products, and pairs of terms of each
+    int32_t jobs;          // products
     int32_t lead;          // rounds of the second product that some units start early
     int32_t a_room;        // of A in a stage: a_bytes at least, a multiple of 1024
     int32_t rows, cols;    // tokens, vocabulary rows of this piece
@@ -78,17 +78,45 @@ enum VocabOut : int { kVocabStats, kVocabGrad, kVocabProduct };
 // Results that the tensor cores' sums alone are not good enough for.
 constexpr bool vocab_promotes(VocabOut out, int dtype) { return out == kVocabStats || dtype == 0; }
 
-// `boxed`: rows of a box (K innermost: the tile's rows; else the stage's k).
+// A call of a few tokens (vocab_few.cu).
+struct FewArgs {
+    const void* h;
+    const void* w;
+    int32_t tokens, cols, pitch;   // pitch: floats of a token in shared memory
+    int64_t vocab;
+    const int64_t* target;
+    int64_t ignore;
+    float2* parts;                 // per (block, token)
+    float* picked;
+    // the logits' gradient, vocab x few_tokens(tokens), written and then read; null:
+    // the statistics are wanted
+    float* grad;
+    const float* lse;
+    const float* dloss;
+    const float* dlse;             // or null
+    float* sums;                   // of dhidden, per slice; null: not wanted
+    int64_t sums_pitch;
+    void* dw;                      // null: not wanted
+};
+constexpr int kFewTokens = 8;      // most of them
+// the tokens that a kernel counts with
+constexpr int few_tokens(int tokens) { return tokens == 1 ? 1 : tokens <= 4 ? 4 : 8; }
+int few_blocks(int tokens, int pitch, int64_t vocab, int sms);
+int few_slices(int64_t cols, int dtype, bool vec, int64_t vocab, int sms);
+cudaError_t launch_few_logits(int dtype, bool vec, const FewArgs& a, int blocks, cudaStream_t s);
+cudaError_t launch_few_products(int dtype, bool vec, const FewArgs& a, int slices, cudaStream_t s);
+
+// box_rows: of a box (K innermost: the tile's rows; else the stage's k).
 bool term_map(const TermMatrix& m, int box_rows, CUtensorMap* map);
 
-const void* vocab_stats_kernel(VocabTile t);
+const void* vocab_stats_kernel(int dtype, VocabTile t);
 const void* vocab_grad_kernel(int dtype, VocabTile t);
 const void* vocab_product_kernel(int dtype, VocabTile t);
 
 cudaError_t launch_vocab(VocabOut out, int dtype, VocabTile tile, const CUtensorMap (&maps)[4],
                          const VocabArgs& a, int sms, cudaStream_t s);
 // loss and lse from the tiles' parts
-cudaError_t launch_vocab_merge(const VocabArgs& a, int parts, float* loss, float* lse,
+cudaError_t launch_vocab_merge(const VocabArgs& a, int nparts, float* loss, float* lse,
                                cudaStream_t s);
 // n matrices of the call's type and of one width as bf16 terms
 cudaError_t launch_vocab_pack(int dtype, const void* const (&src)[2], const TermMatrix (&dst)[2], int n,

@@ -33,7 +33,14 @@ struct Shape {
     int64_t tokens, hidden, vocab;
     int dtype, es, terms;
     bool pack_h, pack_w;   // the operand is copied as bf16 terms first
+    bool few;              // takes the form for a few tokens
 };
+
+// Floats of a token in the shared memory of the form for a few tokens: whole steps
+// of a warp.
+int64_t few_pitch(int64_t hidden) { return round_up(hidden, 256); }
+// Shared memory it takes at most, two CTAs to an SM.
+constexpr int64_t kFewRoom = 100 << 10;
 
 credit_status_t shape_of(const void* h, const void* w, int64_t tokens, int64_t hidden, int64_t vocab,
                          credit_dtype_t dtype, Shape* s) {
@@ -56,6 +63,12 @@ credit_status_t shape_of(const void* h, const void* w, int64_t tokens, int64_t h
     const bool lines = hidden * s->es % 16 == 0;
     s->pack_h = s->terms > 1 || !lines || !aligned(h, 16);
     s->pack_w = s->terms > 1 || !lines || !aligned(w, 16);
+    // One token is bound by reading the weight (131072 x 4096 bf16: 162 us in the form
+    // for a few, 175 in tiles).  More take it where the tiles would copy the weight
+    // first (4 tokens of 50000 x 1001 bf16: 47 and 73 us; 8 of 131072 x 2048 fp32: 265
+    // and 900; 8 of bf16 223 and 99).
+    s->few = tokens <= kFewTokens && (tokens <= 1 || s->pack_w) &&
+             few_tokens((int)tokens) * few_pitch(hidden) * 4 <= kFewRoom;
     return CREDIT_OK;
 }
 
@@ -177,6 +190,41 @@ Layout backward_layout(const Shape& s, bool dh, bool dw, int sms, Products* prod
     return l;
 }
 
+// The same of a call of a few tokens.
+struct FewLayout {
+    int64_t parts, picked, grad, sums, bytes = 0;
+    int blocks, slices;
+    int64_t sums_pitch;
+};
+FewLayout few_layout(const Shape& s, bool backward, bool dh, bool vec, int sms) {
+    FewLayout l;
+    Layout place{};
+    l.blocks = few_blocks((int)s.tokens, (int)few_pitch(s.hidden), s.vocab, sms);
+    l.slices = few_slices(s.hidden, s.dtype, vec, s.vocab, sms);
+    l.sums_pitch = round_up(s.hidden, 4);
+    if (!backward) {
+        place.place(&l.parts, l.blocks * s.tokens * 8);
+        place.place(&l.picked, s.tokens * 4);
+    } else {
+        place.place(&l.grad, s.vocab * few_tokens((int)s.tokens) * 4);
+        if (dh) place.place(&l.sums, l.slices * s.tokens * l.sums_pitch * 4);
+    }
+    l.bytes = place.bytes;
+    return l;
+}
+FewArgs few_args(const Shape& s, const void* h, const void* w, const int64_t* target, int64_t ignore) {
+    FewArgs a{};
+    a.h = h;
+    a.w = w;
+    a.tokens = (int32_t)s.tokens;
+    a.cols = (int32_t)s.hidden;
+    a.pitch = (int32_t)few_pitch(s.hidden);
+    a.vocab = s.vocab;
+    a.target = target;
+    a.ignore = ignore;
+    return a;
+}
+
 credit_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? CREDIT_OK : CREDIT_ERR_CUDA; }
 
 credit_status_t device(const DevInfo** info) {
@@ -255,6 +303,11 @@ credit_status_t credit_linear_ce_workspace(int backward, const void* hidden, con
     if (tokens == 0) return CREDIT_OK;
     const DevInfo* d = device_info(device);
     if (!d) return CREDIT_ERR_CUDA;
+    if (s.few) {  // (either access)
+        *bytes = (size_t)std::max(few_layout(s, backward, true, true, d->sms).bytes,
+                                  few_layout(s, backward, true, false, d->sms).bytes);
+        return CREDIT_OK;
+    }
     if (!backward) {
         *bytes = (size_t)forward_layout(s, logits_tile(s, s.vocab, d->sms)).bytes;
         return CREDIT_OK;
@@ -285,6 +338,24 @@ credit_status_t credit_linear_ce_forward(const void* hidden, const void* weight,
     const DevInfo* d;
     st = device(&d);
     if (st != CREDIT_OK) return st;
+    if (s.few) {
+        const bool vec = aligned(weight, 16) && hidden_size * s.es % 16 == 0;
+        const FewLayout l = few_layout(s, false, false, vec, d->sms);
+        if (workspace_bytes < (uint64_t)l.bytes) return CREDIT_ERR_INVALID_ARG;
+        cudaStream_t q = (cudaStream_t)stream;
+        FewArgs f = few_args(s, hidden, weight, target, ignore_index);
+        f.parts = reinterpret_cast<float2*>(static_cast<char*>(workspace) + l.parts);
+        f.picked = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.picked);
+        if ((st = from_cuda(launch_few_logits(s.dtype, vec, f, l.blocks, q))) != CREDIT_OK) return st;
+        VocabArgs a{};
+        a.rows = (int32_t)tokens;
+        a.vocab = vocab;
+        a.target = target;
+        a.ignore = ignore_index;
+        a.parts = f.parts;
+        a.picked = f.picked;
+        return from_cuda(launch_vocab_merge(a, l.blocks, loss, lse, q));
+    }
     const VocabTile tile = logits_tile(s, vocab, d->sms);
     const Layout l = forward_layout(s, tile);
     if (workspace_bytes < (uint64_t)l.bytes) return CREDIT_ERR_INVALID_ARG;
@@ -296,7 +367,6 @@ credit_status_t credit_linear_ce_forward(const void* hidden, const void* weight,
     const TermMatrix w = operand(s, weight, vocab, s.pack_w, ws + l.w);
     VocabArgs a{};
     a.jobs = 1;
-    a.pairs = s.terms == 1 ? 1 : 6;
     a.work[0] = work_of(tile, tokens, vocab, hidden_size, false, false);
     CUtensorMap maps[4] = {};
     if (!term_map(h, box_rows(tile, tokens, &a.work[0]), &maps[0]) ||
@@ -340,6 +410,26 @@ credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse,
     const DevInfo* d;
     st = device(&d);
     if (st != CREDIT_OK) return st;
+    if (s.few) {
+        const bool vec = aligned(weight, 16) && aligned(dweight, 16) && hidden_size * s.es % 16 == 0;
+        const FewLayout l = few_layout(s, true, dhidden != nullptr, vec, d->sms);
+        if (!workspace || workspace_bytes < (uint64_t)l.bytes || !aligned(workspace, 16))
+            return CREDIT_ERR_INVALID_ARG;
+        FewArgs f = few_args(s, hidden, weight, target, ignore_index);
+        f.lse = lse;
+        f.dloss = dloss;
+        f.dlse = dlse;
+        f.grad = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.grad);
+        if (dhidden) f.sums = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.sums);
+        f.sums_pitch = l.sums_pitch;
+        f.dw = dweight;
+        const bool lines = aligned(weight, 16) && hidden_size * s.es % 16 == 0;
+        if ((st = from_cuda(launch_few_logits(s.dtype, lines, f, l.blocks, q))) != CREDIT_OK) return st;
+        if ((st = from_cuda(launch_few_products(s.dtype, vec, f, l.slices, q))) != CREDIT_OK) return st;
+        return dhidden ? from_cuda(launch_vocab_sum(s.dtype, f.sums, l.slices, tokens, hidden_size,
+                                                    l.sums_pitch, dhidden, d->sms, q))
+                       : CREDIT_OK;
+    }
     Products products;
     const Layout l = backward_layout(s, dhidden != nullptr, dweight != nullptr, d->sms, &products);
     if (!workspace || workspace_bytes < (uint64_t)l.bytes || !aligned(workspace, 16))
@@ -359,8 +449,7 @@ credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse,
         const int64_t v0 = p * l.piece, pv = std::min(l.piece, vocab - v0);
         VocabArgs a{};
         a.jobs = 1;
-        a.pairs = s.terms == 1 ? 1 : 6;
-        a.work[0] = work_of(gt, tokens, pv, hidden_size, false, false);
+            a.work[0] = work_of(gt, tokens, pv, hidden_size, false, false);
         a.work[0].b_y0 = (int32_t)v0;
         const int box = box_rows(gt, tokens, &a.work[0]);
         if (p == 0 && (!term_map(h, box, &logits[0]) ||

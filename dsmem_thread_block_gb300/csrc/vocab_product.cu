@@ -4,6 +4,6 @@
 namespace credit {
 const void* vocab_product_kernel(int dtype, VocabTile t) {
     return dtype
-               ? vocab_kernel_of<ProductRow<bf16>, vocab_promotes(kVocabProduct, 1)>(t) : vocab_kernel_of<ProductRow<float>, vocab_promotes(kVocabProduct, 0)>(t);
+               ? vocab_kernel_of<ProductRow<bf16>, vocab_promotes(kVocabProduct, 1), 1>(t) : vocab_kernel_of<ProductRow<float>, vocab_promotes(kVocabProduct, 0), 3>(t);
 }
 }  // namespace credit

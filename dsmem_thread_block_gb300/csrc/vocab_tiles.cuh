@@ -11,6 +11,15 @@
 // accumulator holds kPromote stages at a time, and the epilogue warps add these
 // parts in registers, which rounds to nearest; they do it while the next part is
 // multiplied.
+//
+// fp32 operands come as three bf16 terms, x = x0 + x1 + x2 to 24 bits.  Of their
+// nine products six are formed; the others are below 2^-24 of x y.  A stage holds
+// one term of both operands, so three stages in a row (terms 2, 1, 0) make a step of
+// k and each term is loaded once.  The products take the order
+//   x1 y1,  x2 y0, x0 y2 (term 2 is done),  x1 y0, x0 y1 (term 1),  x0 y0
+// which lets the next step's terms in early: with four stages only, term 2 of the
+// next step waits in the fourth, term 1 takes term 2's place half-way through, and
+// term 0 is needed again a sixth into the next step.
 #pragma once
 
 #include <algorithm>
@@ -106,12 +115,6 @@ __device__ __forceinline__ bool tile_at(const VocabArgs& a, int u, int units, in
     r->kn = min(w.per, w.kb - r->k0);
     return true;
 }
-
-// Terms of A and B in the order of their products, the smallest first: with
-// x = x0 + x1 + x2 to 24 bits, x0 y0 + (x0 y1 + x1 y0) + (x1 y1 + x0 y2 + x2 y0)
-// leaves out what is below 2^-24 of x y.
-__device__ __forceinline__ int term_a(int pairs, int p) { return pairs == 1 ? 0 : (0x001102 >> (4 * p)) & 3; }
-__device__ __forceinline__ int term_b(int pairs, int p) { return pairs == 1 ? 0 : (0x010120 >> (4 * p)) & 3; }
 
 // Where an operand's boxes of a stage lie: one box with K innermost, `boxes` of 64
 // with M or N innermost.
@@ -372,7 +375,7 @@ template <typename T> struct ProductRow {
 };
 
 // ---------------------------------------------------------------- the kernel
-template <typename OUT, bool PROMOTE, int N, int CG>
+template <typename OUT, bool PROMOTE, int TERMS, int N, int CG>
 __global__ void __launch_bounds__(vocab_threads(PROMOTE, N), 1)
 vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUtensorMap b0,
             const __grid_constant__ CUtensorMap a1, const __grid_constant__ CUtensorMap b1,
@@ -384,7 +387,7 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
     __shared__ uint32_t tmem_base;
     __shared__ int dead_flag;
     volatile int* const dead = &dead_flag;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
     const int rank = CG == 1 ? 0 : (int)cluster_ctarank();
     const int unit = (int)blockIdx.x / CG, units = (int)gridDim.x / CG;
     const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
@@ -392,7 +395,7 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
     if (threadIdx.x == 0) {
         dead_flag = 0;
         for (int s = 0; s < stages; ++s) {
-            mbar_init(smem_u32(&bars.full[s]), 1);
+            mbar_init(smem_u32(&bars.full[s]), 2);  // A and B
             mbar_init(smem_u32(&bars.empty[s]), 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -411,7 +414,9 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
         cluster_wait_acquire();
     }
     tmem_fence_after();
-    const uint32_t tmem = tmem_base;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
+    // steps of k that the accumulators hold at a time
+    auto parts_of = [](int kn) { return !PROMOTE ? kn : TERMS == 1 ? kPromote : 1; };
     dependents_may_launch();
     wait_for_launches();
     Tile t;
@@ -431,67 +436,111 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                 phase ^= 1u;
             }
         };
-        if (warp == kWarps && lane == 0) {
+        // Warps 0 and 2 of this group fill the stages with A and B, warp 1 multiplies.  A
+        // whole warp walks the stages and one elected lane issues: what the copies and
+        // products take from uniform registers then stays there.  The warps that fill set
+        // the pace of large calls: one thread for both operands in a loop over terms took
+        // 3.9 ms where this takes PLACEHOLDER (backward 4096 x 4096 x 65536 bf16).
+        auto arrived = [&](uint32_t b, uint32_t parity) {
+            return (bool)__all_sync(0xffffffffu, hold(b, parity, a.err, dead));
+        };
+        auto fill = [&](auto which) {
+            constexpr bool B = decltype(which)::value;
+            constexpr int kBoxes = B ? S::kRowsB / 64 : kTileM / 64;
+            const bool leader = elect_one();
             // both CTAs' bytes count on the first one's barriers
             const uint32_t signal0 = CG > 1 ? mapa_shared(full0, 0) : full0;
+            const uint32_t offset = B ? a.a_room : 0;
             uint32_t filled = 0;  // fills in all
             bool ok = true;
             for (int i = 0; ok && tile_at<N, CG>(a, unit, units, rank, i, &t); ++i) {
                 const TileWork& w = a.work[t.job];
-                const Boxes<CG, kTileM / 64> boxes_a(t.job ? &a1 : &a0, w.a_mn, t.m0, 0, t.k0);
-                const Boxes<CG, S::kRowsB / 64> boxes_b(t.job ? &b1 : &b0, w.b_mn, t.n0 + rank * S::kRowsB,
-                                                        w.b_y0, t.k0);
-                const uint32_t bytes = CG * (w.a_bytes + S::kBytesB);
-                for (int p = 0; ok && p < a.pairs; ++p) {
-                    const int ta = term_a(a.pairs, p), tb = term_b(a.pairs, p);
-                    for (int k = 0; k < t.kn; ++k) {
-                        ok = hold(empty0 + bar, phase ^ 1u, a.err, dead);
-                        if (!ok) break;
+                const CUtensorMap* const map = B ? (t.job ? &b1 : &b0) : (t.job ? &a1 : &a0);
+                const Boxes<CG, kBoxes> boxes(map, B ? w.b_mn : w.a_mn, B ? t.n0 + rank * S::kRowsB : t.m0,
+                                              B ? w.b_y0 : 0, t.k0);
+                const uint32_t bytes = CG * (B ? S::kBytesB : w.a_bytes);
+                auto one = [&](int k, int term) {
+                    ok = arrived(empty0 + bar, phase ^ 1u);
+                    if (!ok) return false;
+                    if (leader) {
                         if (rank == 0) mbar_arrive_expect_tx(full0 + bar, bytes);
-                        boxes_a.load(k, ta, at, signal0 + bar);
-                        boxes_b.load(k, tb, at + a.a_room, signal0 + bar);
-                        ++filled;
-                        advance();
+                        boxes.load(k, term, at + offset, signal0 + bar);
                     }
-                }
+                    ++filled;
+                    advance();
+                    return true;
+                };
+                for (int k = 0; k < t.kn; ++k)
+                    if (!(TERMS == 1 ? one(k, 0) : one(k, 2) && one(k, 1) && one(k, 0))) break;
             }
             // a CTA that has given up leaves no copy in flight
-            if (!ok && rank == 0)
+            if (!ok && leader && rank == 0)
                 for (uint32_t f = filled > (uint32_t)stages ? filled - stages : 0; f < filled; ++f)
-                    mbar_wait_bounded(full0 + 8 * (f % stages), (f / stages) & 1u, a.err);
-        } else if (warp == kWarps + 1 && lane == 0 && rank == 0) {
+                    if (!mbar_wait_bounded(full0 + 8 * (f % stages), (f / stages) & 1u, a.err)) break;
+        };
+        if (warp == kWarps) {
+            fill(std::false_type());
+        } else if (warp == kWarps + 2) {
+            fill(std::true_type());
+        } else if (warp == kWarps + 1 && rank == 0) {
+            const bool leader = elect_one();
             int n = 0;  // parts so far
             bool ok = true;
+            auto there = [&](uint32_t b, uint32_t parity) {
+                ok = arrived(b, parity);
+                tmem_fence_after();
+                return ok;
+            };
             for (int i = 0; ok && tile_at<N, CG>(a, unit, units, rank, i, &t); ++i) {
                 const TileWork& w = a.work[t.job];
                 const uint32_t desc = mma_desc(CG * kTileM, N, w.a_mn, w.b_mn);
                 // from one sixteen k to the next, in descriptors' units of 16 bytes
                 const uint32_t step_a = w.a_mn ? 16 * 8 : 2, step_b = w.b_mn ? 16 * 8 : 2;
-                const int steps = t.kn * a.pairs;
-                for (int k0 = 0; ok && k0 < steps; ++n) {
-                    const int k1 = PROMOTE ? min(steps, k0 + kPromote) : steps;
+                const int steps = parts_of(t.kn);
+                for (int k0 = 0; ok && k0 < t.kn; ++n) {
+                    const int k1 = PROMOTE ? min(t.kn, k0 + steps) : t.kn;
                     const uint32_t acc = tmem + (n & 1) * N;
-                    ok = hold(smem_u32(&bars.acc_empty[n & 1]), ((n >> 1) & 1) ^ 1u, a.err, dead);
-                    if (!ok) break;
-                    tmem_fence_after();
-                    for (int k = k0; k < k1; ++k) {
-                        ok = hold(full0 + bar, phase, a.err, dead);
-                        if (!ok) break;
-                        tmem_fence_after();
-                        const uint64_t da = smem_desc(at, kBoxBytes, 1024);
-                        const uint64_t db = smem_desc(at + a.a_room, kBoxBytes, 1024);
+                    if (!there(smem_u32(&bars.acc_empty[n & 1]), ((n >> 1) & 1) ^ 1u)) break;
+                    // the products of A in stage `sa` with B in stage `sb`
+                    auto multiply = [&](uint32_t sa, uint32_t sb, bool add) {
+                        const uint64_t da = smem_desc(sa, kBoxBytes, 1024);
+                        const uint64_t db = smem_desc(sb + a.a_room, kBoxBytes, 1024);
+                        if (leader)
 #pragma unroll
-                        for (int q = 0; q < kTileK / 16; ++q)
-                            mma_bf16<CG>(acc, da + q * step_a, db + q * step_b, desc,
-                                         k > k0 || q > 0);
-                        mma_commit<CG>(empty0 + bar);
-                        advance();
+                            for (int q = 0; q < kTileK / 16; ++q)
+                                mma_bf16<CG>(acc, da + q * step_a, db + q * step_b, desc, add || q > 0);
+                    };
+                    for (int k = k0; k < k1; ++k) {
+                        if constexpr (TERMS == 1) {
+                            if (!there(full0 + bar, phase)) break;
+                            multiply(at, at, k > k0);
+                            if (leader) mma_commit<CG>(empty0 + bar);
+                            advance();
+                        } else {
+                            const uint32_t at2 = at, bar2 = bar;
+                            if (!there(full0 + bar, phase)) break;
+                            advance();
+                            const uint32_t at1 = at, bar1 = bar;
+                            if (!there(full0 + bar, phase)) break;
+                            multiply(at1, at1, k > k0);
+                            advance();
+                            if (!there(full0 + bar, phase)) break;
+                            multiply(at2, at, true);
+                            multiply(at, at2, true);
+                            if (leader) mma_commit<CG>(empty0 + bar2);
+                            multiply(at1, at, true);
+                            multiply(at, at1, true);
+                            if (leader) mma_commit<CG>(empty0 + bar1);
+                            multiply(at, at, true);
+                            if (leader) mma_commit<CG>(empty0 + bar);
+                            advance();
+                        }
                     }
-                    if (ok) mma_commit<CG>(smem_u32(&bars.acc_full[n & 1]));
+                    if (ok && leader) mma_commit<CG>(smem_u32(&bars.acc_full[n & 1]));
                     k0 = k1;
                 }
             }
-            if (!ok) {  // nor a product
+            if (!ok && leader) {  // nor a product
                 mma_commit<CG>(smem_u32(&bars.drained));
                 mbar_wait_bounded(smem_u32(&bars.drained), 0, a.err);
             }
@@ -524,8 +573,8 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                 F2 sum[kCols / 2];
 #pragma unroll
                 for (int j = 0; j < kCols / 2; ++j) sum[j] = f2(0.f);
-                const int steps = t.kn * a.pairs;
-                for (int k0 = 0; k0 < steps; k0 += kPromote) {
+                const int steps = parts_of(t.kn);
+                for (int k0 = 0; k0 < t.kn; k0 += steps) {
                     const uint32_t acc = ready();
                     if (!ok) break;
 #pragma unroll
@@ -577,11 +626,11 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
     if (warp == kWarps + 1) tmem_free<CG>(tmem, S::kTmem);
 }
 
-template <typename OUT, bool PROMOTE> const void* vocab_kernel_of(VocabTile t) {
+template <typename OUT, bool PROMOTE, int TERMS> const void* vocab_kernel_of(VocabTile t) {
     switch (t) {
-        case kPair256: return (const void*)vocab_tiles<OUT, PROMOTE, 256, 2>;
-        case kOne256: return (const void*)vocab_tiles<OUT, PROMOTE, 256, 1>;
-        default: return (const void*)vocab_tiles<OUT, PROMOTE, 128, 1>;
+        case kPair256: return (const void*)vocab_tiles<OUT, PROMOTE, TERMS, 256, 2>;
+        case kOne256: return (const void*)vocab_tiles<OUT, PROMOTE, TERMS, 256, 1>;
+        default: return (const void*)vocab_tiles<OUT, PROMOTE, TERMS, 128, 1>;
     }
 }
 

@@ -88,7 +88,8 @@ def ref_backward(dloss, dlse, h, w, target, lse, ignore=IGNORE):
 
 SHAPES = [(1, 8, 1), (1, 64, 2), (2, 1, 3), (3, 7, 255), (31, 64, 256), (33, 100, 257), (128, 65, 1000),
           (129, 512, 513), (300, 1001, 5003), (64, 1024, 4096), (1, 4096, 20000), (1000, 16, 40),
-          (257, 192, 1), (5, 2056, 777)]
+          (257, 192, 1), (5, 2056, 777), (8, 264, 1000), (9, 264, 1000), (4, 1001, 3001), (8, 4096, 600),
+          (6, 33, 130), (1, 20000, 37)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -128,7 +129,7 @@ def whole_numbers(shape, top, dtype, seed):
 
 # (8192 tokens: the vocabulary in two pieces; few tokens: parts of a sum over it)
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("tokens,hidden,vocab", [(1, 8, 5), (7, 72, 300), (130, 264, 700), (300, 1001, 1000),
+@pytest.mark.parametrize("tokens,hidden,vocab", [(1, 8, 5), (7, 72, 300), (4, 1001, 2000), (11, 72, 300), (130, 264, 700), (300, 1001, 1000),
                                                  (200, 24, 20011), (8192, 40, 20000), (4099, 72, 33333)])
 def test_gradients_of_whole_numbers_are_exact(tokens, hidden, vocab, dtype):
     # with w = 0 (or h = 0) every logit is 0, and with lse = 0 every p is 1:
@@ -151,12 +152,13 @@ def test_gradients_of_whole_numbers_are_exact(tokens, hidden, vocab, dtype):
     assert torch.equal(dh, (g @ w.double()).float().to(dt))
 
 
+@pytest.mark.parametrize("tokens", [3, 70])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_large_logits_neither_overflow_nor_vanish(dtype):
-    h, w, target = make(70, 128, 900, DT[dtype], seed=3, spread=2000.0, ignored=0.0)
+def test_large_logits_neither_overflow_nor_vanish(dtype, tokens):
+    h, w, target = make(tokens, 128, 900, DT[dtype], seed=3, spread=2000.0, ignored=0.0)
     loss, lse = credit.linear_cross_entropy_forward(h, w, target)
     want, want_lse, bound, bound_lse = ref_forward(h, w, target)
-    assert bool(torch.isfinite(loss).all()) and float(want_lse.max()) > 1000
+    assert bool(torch.isfinite(loss).all()) and float(want_lse.max()) > 500
     assert_close(lse, want_lse, bound_lse, "lse")
     assert_close(loss, want, bound, "loss")
 
@@ -184,9 +186,10 @@ def test_targets_at_every_place_of_a_tile_and_outside():
     assert float(loss[17]) == 0 and bool((loss[:17] > 0).all())
 
 
-def test_every_target_ignored():
-    h, w, target = make(140, 64, 300, torch.bfloat16, ignored=2.0)
-    dloss = torch.full((140,), float("nan"), device="cuda")  # of ignored tokens: not looked at
+@pytest.mark.parametrize("tokens", [2, 140])
+def test_every_target_ignored(tokens):
+    h, w, target = make(tokens, 64, 300, torch.bfloat16, ignored=2.0)
+    dloss = torch.full((tokens,), float("nan"), device="cuda")  # of ignored tokens: not looked at
     loss, lse = credit.linear_cross_entropy_forward(h, w, target)
     assert bool((loss == 0).all())
     dh, dw = credit.linear_cross_entropy_backward(dloss, h, w, target, lse)
@@ -194,14 +197,15 @@ def test_every_target_ignored():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_one_token_that_is_not_finite_leaves_the_others(dtype):
-    h, w, target = make(40, 64, 500, DT[dtype], seed=4, ignored=0.0)
+@pytest.mark.parametrize("tokens", [5, 40])
+def test_one_token_that_is_not_finite_leaves_the_others(dtype, tokens):
+    h, w, target = make(tokens, 64, 500, DT[dtype], seed=4, ignored=0.0)
     loss, lse = credit.linear_cross_entropy_forward(h, w, target)
     for value in (float("nan"), float("inf")):
         hb = h.clone()
         hb[3, 5] = value
         lb, sb = credit.linear_cross_entropy_forward(hb, w, target)
-        rest = torch.arange(40, device="cuda") != 3
+        rest = torch.arange(tokens, device="cuda") != 3
         assert torch.equal(lb[rest], loss[rest]) and torch.equal(sb[rest], lse[rest])
         assert not bool(torch.isfinite(sb[3]))
     # a padded token's infinite exponentials give no gradient to the hidden states
@@ -209,7 +213,7 @@ def test_one_token_that_is_not_finite_leaves_the_others(dtype):
     tb[3] = IGNORE
     big = lse.clone()
     big[3] = -1e30
-    dh, _ = credit.linear_cross_entropy_backward(torch.ones(40, device="cuda"), h, w, tb, big)
+    dh, _ = credit.linear_cross_entropy_backward(torch.ones(tokens, device="cuda"), h, w, tb, big)
     assert bool((dh[3] == 0).all())
 
 
@@ -222,10 +226,11 @@ def guarded(shape, dtype):
     return whole[32:32 + n].view(shape), whole
 
 
+@pytest.mark.parametrize("tokens", [3, 150])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("shift", [0, 1, 3])
-def test_addresses_and_given_outputs(dtype, shift):
-    tokens, hidden, vocab = 150, 72, 410
+def test_addresses_and_given_outputs(dtype, shift, tokens):
+    hidden, vocab = 72, 410
     dt = DT[dtype]
     h, w, target = make(tokens, hidden, vocab, dt, seed=6)
     dloss = torch.rand(tokens, device="cuda")
@@ -239,22 +244,31 @@ def test_addresses_and_given_outputs(dtype, shift):
 
     hm, wm = moved(h), moved(w)
     loss2, lse2 = credit.linear_cross_entropy_forward(hm, wm, target)
-    assert torch.equal(loss, loss2) and torch.equal(lse, lse2)
+    if tokens > 8:  # (a few tokens' dot products are added in another order at other addresses)
+        assert torch.equal(loss, loss2) and torch.equal(lse, lse2)
+    want, want_lse, bound, bound_lse = ref_forward(h, w, target)
+    assert_close(lse2, want_lse, bound_lse, "lse")
+    assert_close(loss2, want, bound, "loss")
     oh, all_h = guarded(h.shape, dt)
     ow, all_w = guarded((vocab * hidden + 1,), dt)
     ow = ow[1:].view(vocab, hidden) if shift else guarded(w.shape, dt)[0]
     rh, rw = credit.linear_cross_entropy_backward(dloss, hm, wm, target, lse, dhidden=oh, dweight=ow)
     assert rh is oh or rh.data_ptr() == oh.data_ptr()
-    assert torch.equal(oh, dh) and torch.equal(ow, dw)
+    if tokens > 8:
+        assert torch.equal(oh, dh) and torch.equal(ow, dw)
+    want_h, want_w, bound_h, bound_w = ref_backward(dloss, None, h, w, target, lse)
+    assert_close(oh, want_h, bound_h, "dhidden")
+    assert_close(ow, want_w, bound_w, "dweight")
     assert bool((all_h[:32] == 7).all()) and bool((all_h[-32:] == 7).all())
     if shift:
         assert bool((all_w[:33] == 7).all()) and bool((all_w[-32:] == 7).all())
 
 
 @pytest.mark.parametrize("need_h,need_w", [(True, False), (False, True), (False, False)])
-def test_gradients_that_are_not_needed(need_h, need_w):
-    h, w, target = make(200, 136, 3000, torch.bfloat16, seed=8)
-    dloss = torch.rand(200, device="cuda")
+@pytest.mark.parametrize("tokens", [7, 200])
+def test_gradients_that_are_not_needed(need_h, need_w, tokens):
+    h, w, target = make(tokens, 136, 3000, torch.bfloat16, seed=8)
+    dloss = torch.rand(tokens, device="cuda")
     _, lse = credit.linear_cross_entropy_forward(h, w, target)
     want = ref_backward(dloss, None, h, w, target, lse)
     dh, dw = credit.linear_cross_entropy_backward(dloss, h, w, target, lse, need_dhidden=need_h,
@@ -289,9 +303,10 @@ def test_batches_of_sequences_keep_their_shape():
     assert dh.shape == h3.shape
 
 
-def test_results_repeat_bit_for_bit_on_any_stream():
-    h, w, target = make(500, 264, 9000, torch.bfloat16, seed=12)
-    dloss = torch.rand(500, device="cuda")
+@pytest.mark.parametrize("tokens", [4, 500])
+def test_results_repeat_bit_for_bit_on_any_stream(tokens):
+    h, w, target = make(tokens, 264, 9000, torch.bfloat16, seed=12)
+    dloss = torch.rand(tokens, device="cuda")
 
     def both():
         loss, lse = credit.linear_cross_entropy_forward(h, w, target)
@@ -309,10 +324,11 @@ def test_results_repeat_bit_for_bit_on_any_stream():
         assert all(torch.equal(a, b) for a, b in zip(first, r))
 
 
-def test_captured_calls_take_new_inputs():
-    h, w, target = make(200, 128, 2100, torch.bfloat16, seed=13)
-    dloss = torch.rand(200, device="cuda")
-    ws = [torch.empty(C.credit_linear_ce_workspace(b, h.data_ptr(), w.data_ptr(), 200, 128, 2100, C.BF16,
+@pytest.mark.parametrize("tokens", [2, 200])
+def test_captured_calls_take_new_inputs(tokens):
+    h, w, target = make(tokens, 128, 2100, torch.bfloat16, seed=13)
+    dloss = torch.rand(tokens, device="cuda")
+    ws = [torch.empty(C.credit_linear_ce_workspace(b, h.data_ptr(), w.data_ptr(), tokens, 128, 2100, C.BF16,
                                                    h.device.index), dtype=torch.uint8, device="cuda")
           for b in (0, 1)]
 
@@ -327,7 +343,7 @@ def test_captured_calls_take_new_inputs():
     with torch.cuda.graph(graph):
         out = both()
     for seed in (20, 21):
-        h2, w2, t2 = make(200, 128, 2100, torch.bfloat16, seed=seed)
+        h2, w2, t2 = make(tokens, 128, 2100, torch.bfloat16, seed=seed)
         h.copy_(h2), w.copy_(w2), target.copy_(t2)
         graph.replay()
         torch.cuda.synchronize()
