@@ -13,41 +13,56 @@ namespace credit {
 namespace {
 
 // --------------------------------------------------------- the small kernels
-constexpr int kMergeWarps = 16;
+constexpr int kMergeThreads = 256;
+constexpr int kMergeRows = 4;   // of a CTA: a sector of each part
 
-// The parts of 32 tokens, a token a lane: warp w takes parts w, w + 16, ...  The
-// maximum over all of them is known before any sum is scaled to it.
-__global__ void __launch_bounds__(32 * kMergeWarps)
+// (m, s) and another pair: the larger maximum, the sums scaled to it.
+__device__ __forceinline__ void merge_pair(float& m, float& s, float mo, float so) {
+    const float top = fmaxf(m, mo), base = isinf(top) ? 0.f : top;
+    s = (s == 0.f ? 0.f : s * expf(m - base)) + (so == 0.f ? 0.f : so * expf(mo - base));
+    m = top;
+}
+
+// The parts of four tokens: 64 threads a token, each every 64th part.  (A token a
+// lane, 16 warps over the parts, took 17 us for 64 tokens of 1024 parts: PLACEHOLDER here.)
+__global__ void __launch_bounds__(kMergeThreads)
 vocab_merge(VocabArgs a, int nparts, float* loss, float* lse) {
-    __shared__ float tops[kMergeWarps][32], sums[kMergeWarps][32];
+    constexpr int kGroups = kMergeThreads / kMergeRows;
+    __shared__ float2 sums[kMergeThreads / 32][kMergeRows];
     dependents_may_launch();
     wait_for_launches();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t row = (int64_t)blockIdx.x * 32 + lane;
+    const int mine = threadIdx.x % kMergeRows, group = threadIdx.x / kMergeRows;
+    const int64_t row = (int64_t)blockIdx.x * kMergeRows + mine;
     const bool live = row < a.rows;
     float m = -INFINITY, s = 0.f;
-    auto scaled = [](float v, float from, float to) { return v == 0.f ? 0.f : v * expf(from - to); };
     if (live)
-#pragma unroll 4
-        for (int t = warp; t < nparts; t += kMergeWarps) {
-            const float2 p = a.parts[(int64_t)t * a.rows + row];
-            const float top = fmaxf(m, p.x), base = isinf(top) ? 0.f : top;
-            s = scaled(s, m, base) + scaled(p.y, p.x, base);
+        for (int t0 = group; t0 < nparts; t0 += 4 * kGroups) {
+            float2 p[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int t = t0 + u * kGroups;
+                p[u] = t < nparts ? __ldcg(&a.parts[(int64_t)t * a.rows + row]) : make_float2(-INFINITY, 0.f);
+            }
+            float top = m;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) top = fmaxf(top, p[u].x);
+            const float base = isinf(top) ? 0.f : top;
+            s = s == 0.f ? 0.f : s * expf(m - base);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) s += p[u].y == 0.f ? 0.f : p[u].y * expf(p[u].x - base);
             m = top;
         }
-    tops[warp][lane] = m;
-    __syncthreads();
-    float top = tops[0][lane];
 #pragma unroll
-    for (int w = 1; w < kMergeWarps; ++w) top = fmaxf(top, tops[w][lane]);
-    const float base = isinf(top) ? 0.f : top;
-    sums[warp][lane] = scaled(s, m, base);
+    for (int o = kMergeRows; o < 32; o <<= 1) {
+        const float mo = __shfl_xor_sync(0xffffffffu, m, o), so = __shfl_xor_sync(0xffffffffu, s, o);
+        merge_pair(m, s, mo, so);
+    }
+    if (lane < kMergeRows) sums[warp][lane] = make_float2(m, s);
     __syncthreads();
-    if (warp || !live) return;
-    float total = 0.f;
-#pragma unroll
-    for (int w = 0; w < kMergeWarps; ++w) total += sums[w][lane];
-    const float l = base + logf(total);
+    if (threadIdx.x >= kMergeRows || !live) return;
+    for (int w = 1; w < kMergeThreads / 32; ++w) merge_pair(m, s, sums[w][mine].x, sums[w][mine].y);
+    const float l = (isinf(m) ? 0.f : m) + logf(s);
     const int64_t target = a.target[row];
     lse[row] = l;
     loss[row] = target == a.ignore ? 0.f
@@ -242,8 +257,8 @@ cudaError_t launch_vocab(VocabOut out, int dtype, VocabTile tile, const CUtensor
 
 cudaError_t launch_vocab_merge(const VocabArgs& a, int nparts, float* loss, float* lse,
                                cudaStream_t s) {
-    return launch_early(vocab_merge, dim3((unsigned)((a.rows + 31) / 32)), 32 * kMergeWarps, s, a, nparts,
-                        loss, lse);
+    return launch_early(vocab_merge, dim3((unsigned)((a.rows + kMergeRows - 1) / kMergeRows)), kMergeThreads, s,
+                        a, nparts, loss, lse);
 }
 
 cudaError_t launch_vocab_pack(int dtype, const void* const (&src)[2], const TermMatrix (&dst)[2], int n,
