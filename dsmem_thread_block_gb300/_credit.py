@@ -186,6 +186,7 @@ SIGNATURES = {
     "credit_get_device_error": (_i32, [_i32]),
     "credit_selftest_wait_timeout": (_i32, [_i32, _i64]),
     "credit_selftest_team_timeout": (_i32, [_i32]),
+    "credit_selftest_tile_timeout": (_i32, [_i32]),
     "credit_debug_build": (_i32, []),
     "credit_selftest_bounds": (_i32, [_i32]),
     "credit_debug_trace": (_i32, [_vp, _i64]),
@@ -580,6 +581,10 @@ def credit_debug_build() -> int:
 
 def credit_selftest_team_timeout(device: int = 0) -> int:
     return load().credit_selftest_team_timeout(device)
+
+
+def credit_selftest_tile_timeout(device: int = 0) -> int:
+    return load().credit_selftest_tile_timeout(device)
 
 
 def credit_selftest_bounds(device: int = 0) -> int:

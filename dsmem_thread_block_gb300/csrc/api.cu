@@ -13,6 +13,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "planner.h"
+#include "vocab.h"
 
 namespace credit {
 
@@ -613,6 +614,21 @@ credit_status_t credit_selftest_team_timeout(int device) {
         return CREDIT_ERR_CUDA;
     }
     return credit_get_device_error(device);
+}
+
+credit_status_t credit_selftest_tile_timeout(int device) {
+    DeviceGuard g(device);
+    const DevInfo* d = g.ok ? device_info(device) : nullptr;
+    if (!d) return CREDIT_ERR_INVALID_ARG;
+    for (const VocabTile t : {kPair256, kOne128}) {
+        if (run_tiles_alone(device, d->sms, t) != cudaSuccess) {
+            cudaGetLastError();
+            return CREDIT_ERR_CUDA;
+        }
+        const credit_status_t st = credit_get_device_error(device);
+        if (st != CREDIT_ERR_DEVICE_TIMEOUT || t == kOne128) return st;
+    }
+    return CREDIT_ERR_CUDA;
 }
 
 const char* credit_version(void) { return "0.5.0"; }

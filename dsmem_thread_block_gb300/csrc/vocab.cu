@@ -255,6 +255,39 @@ cudaError_t launch_vocab(VocabOut out, int dtype, VocabTile tile, const CUtensor
     return cudaLaunchKernelExC(&cfg, fn, p);
 }
 
+cudaError_t run_tiles_alone(int dev, int sms, VocabTile tile) {
+    // one tile, more steps of k than a ring has stages
+    constexpr int kDepth = 2 * kVocabStages * kTileK;
+    const int rows = vocab_tile_rows(tile), cols = vocab_tile_cols(tile), pitch = 2 * kDepth;
+    const size_t need = (size_t)(rows + cols) * pitch + (size_t)rows * (8 + 4 + 2 * 8);
+    char* buf = nullptr;
+    cudaError_t e = cudaMalloc(&buf, need);
+    if (e != cudaSuccess) return e;
+    e = cudaMemset(buf, 0, need);
+    const TermMatrix h{buf, rows, kDepth, pitch, (int64_t)pitch * rows, 1};
+    const TermMatrix w{buf + h.plane, cols, kDepth, pitch, (int64_t)pitch * cols, 1};
+    VocabArgs a{};
+    a.jobs = 1;
+    a.work[0] = {1, 1, 1, kDepth / kTileK, kDepth / kTileK, 1, 0, 0, 0, kBytesA};
+    a.rows = rows;
+    a.cols = cols;
+    a.vocab = cols;
+    char* const rest = buf + h.plane + w.plane;
+    a.parts = reinterpret_cast<float2*>(rest);
+    a.target = reinterpret_cast<int64_t*>(rest + (size_t)rows * 16);
+    a.picked = reinterpret_cast<float*>(rest + (size_t)rows * 24);
+    a.err = device_error_word();
+    a.alone = 1;
+    CUtensorMap maps[4] = {};
+    if (e == cudaSuccess && (!a.err || !term_map(h, kTileM, &maps[0]) ||
+                             !term_map(w, cols / vocab_tile_ctas(tile), &maps[1])))
+        e = cudaErrorInvalidValue;
+    if (e == cudaSuccess) e = launch_vocab(kVocabStats, 1, tile, maps, a, sms, nullptr);
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
+    const cudaError_t f = cudaFree(buf);
+    return e != cudaSuccess ? e : f;
+}
+
 cudaError_t launch_vocab_merge(const VocabArgs& a, int nparts, float* loss, float* lse,
                                cudaStream_t s) {
     return launch_early(vocab_merge, dim3((unsigned)((a.rows + kMergeRows - 1) / kMergeRows)), kMergeThreads, s,

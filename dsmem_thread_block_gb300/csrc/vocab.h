@@ -72,6 +72,7 @@ struct VocabArgs {
     int64_t grad_pitch, grad_plane;  // elements
     ProductOut out[2];
     unsigned* err;
+    int32_t alone;         // a self-test: nothing brings B, every wait runs out
 };
 
 enum VocabOut : int { kVocabStats, kVocabGrad, kVocabProduct };
@@ -115,6 +116,8 @@ const void* vocab_product_kernel(int dtype, VocabTile t);
 
 cudaError_t launch_vocab(VocabOut out, int dtype, VocabTile tile, const CUtensorMap (&maps)[4],
                          const VocabArgs& a, int sms, cudaStream_t s);
+// The tiles' kernel with nothing that brings B; allocates its scratch and waits for it.
+cudaError_t run_tiles_alone(int dev, int sms, VocabTile tile);
 // loss and lse from the tiles' parts
 cudaError_t launch_vocab_merge(const VocabArgs& a, int nparts, float* loss, float* lse,
                                cudaStream_t s);

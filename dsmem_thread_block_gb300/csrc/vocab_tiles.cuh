@@ -480,7 +480,7 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
         };
         if (warp == kWarps) {
             fill(std::false_type());
-        } else if (warp == kWarps + 2) {
+        } else if (warp == kWarps + 2 && !a.alone) {
             fill(std::true_type());
         } else if (warp == kWarps + 1 && rank == 0) {
             const bool leader = elect_one();

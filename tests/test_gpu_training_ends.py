@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import dsmem_thread_block_gb300 as credit
+from dsmem_thread_block_gb300 import _credit as C
 
 pytestmark = pytest.mark.gpu
 
@@ -61,6 +62,7 @@ def test_a_step(dtype):
     want = torch.cat([t.grad.reshape(-1) for t in (xd, gd, wd)]).norm()
     # bf16: y, dy and every gradient are rounded, 2^-8 each, and g once more
     tol = 2e-5 if dtype == torch.float32 else 4 * 2.0 ** -8
+    loss = loss.detach()
     assert abs(float(total) - float(loss)) <= tol * abs(float(loss))
     assert abs(float(norm) - float(want)) <= tol * float(want)
     factor = min(1.0, 0.05 / (float(want) + 1e-6))
@@ -102,3 +104,34 @@ def test_a_captured_step():
     torch.cuda.synchronize()
     assert torch.equal(out[0], eager[0]) and torch.equal(out[1], eager[1])
     assert all(torch.equal(a, b) for a, b in zip(out[2], eager[2]))
+
+
+def test_a_checked_build_runs_the_same_step():
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    x = torch.randn((300, 192), generator=g, device="cuda").bfloat16()
+    gamma = torch.ones(192, device="cuda").bfloat16()
+    w = (0.2 * torch.randn((1100, 192), generator=g, device="cuda")).bfloat16()
+    target = torch.randint(0, 1100, (300,), generator=g, device="cuda")
+    want = step(x, gamma, w, target, torch.bfloat16)
+    with C.use_checked_build():
+        assert C.credit_debug_build() == 1
+        got = step(x, gamma, w, target, torch.bfloat16)
+        assert C.credit_get_device_error(torch.cuda.current_device()) == C.OK
+    assert torch.equal(got[1], want[1]) and all(torch.equal(a, b) for a, b in zip(got[2], want[2]))
+
+
+def test_waits_that_run_out_end_the_tiles_and_leave_the_context():
+    dev = torch.cuda.current_device()
+    assert C.credit_get_device_error(dev) == C.OK
+    assert C.credit_selftest_tile_timeout(dev) == C.ERR_DEVICE_TIMEOUT
+    assert C.credit_get_device_error(dev) == C.OK  # read and cleared
+    # tensor memory is free and the kernels work
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    h = torch.randn((400, 128), generator=g, device="cuda").bfloat16()
+    w = (0.2 * torch.randn((1000, 128), generator=g, device="cuda")).bfloat16()
+    target = torch.randint(0, 1000, (400,), generator=g, device="cuda")
+    _, lse = credit.linear_cross_entropy_forward(h, w, target)
+    want = torch.logsumexp(h.double() @ w.double().t(), 1)
+    assert float((lse.double() - want).abs().max()) < 1e-4
