@@ -417,9 +417,10 @@ PyObject* py_gradients(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int clip = PyObject_IsTrue(a[2]);
         const double max_norm = PyFloat_AsDouble(a[3]), eps = PyFloat_AsDouble(a[4]);
         if (clip < 0 || PyErr_Occurred()) return nullptr;
-        const Items in(a[0]);
+        const Items in(a[0]);  // (an iterator is walked once)
         const bool apart = clip && a[1] != Py_None;
-        const Items out(apart ? a[1] : a[0]);
+        const Items others(apart ? a[1] : in.seq);
+        const Items& out = apart ? others : in;
         if (in.size() == 0) bad("credit: at least one gradient is required");
         if (in.size() != out.size()) bad("credit: one output per gradient is required");
         std::vector<credit_tensor_t> t((size_t)in.size());

@@ -24,7 +24,7 @@ __device__ __forceinline__ void merge_pair(float& m, float& s, float mo, float s
 }
 
 // The parts of four tokens: 64 threads a token, each every 64th part.  (A token a
-// lane, 16 warps over the parts, took 17 us for 64 tokens of 1024 parts: PLACEHOLDER here.)
+// lane, 16 warps over the parts, took 17 us for 64 tokens of 1024 parts.)
 __global__ void __launch_bounds__(kMergeThreads)
 vocab_merge(VocabArgs a, int nparts, float* loss, float* lse) {
     constexpr int kGroups = kMergeThreads / kMergeRows;
@@ -213,11 +213,11 @@ bool term_map(const TermMatrix& m, int box_rows, CUtensorMap* map) {
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t launch_vocab(VocabOut out, int dtype, VocabTile tile, const CUtensorMap (&maps)[4],
+cudaError_t launch_vocab(VocabOut out, VocabTerms terms, VocabTile tile, const CUtensorMap (&maps)[4],
                          const VocabArgs& args, int sms, cudaStream_t s) {
-    const void* fn = out == kVocabStats ? vocab_stats_kernel(dtype, tile)
-                     : out == kVocabGrad ? vocab_grad_kernel(dtype, tile)
-                                         : vocab_product_kernel(dtype, tile);
+    const void* fn = out == kVocabStats ? vocab_stats_kernel(terms, tile)
+                     : out == kVocabGrad ? vocab_grad_kernel(terms, tile)
+                                         : vocab_product_kernel(terms, tile);
     int dev;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -240,7 +240,7 @@ cudaError_t launch_vocab(VocabOut out, int dtype, VocabTile tile, const CUtensor
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(units * ctas));
-    cfg.blockDim = dim3((unsigned)vocab_threads(vocab_promotes(out, dtype), vocab_tile_cols(tile)));
+    cfg.blockDim = dim3((unsigned)vocab_threads(vocab_promotes(out, terms), vocab_tile_cols(tile)));
     cfg.dynamicSmemBytes = kVocabSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -268,7 +268,7 @@ cudaError_t run_tiles_alone(int dev, int sms, VocabTile tile) {
     const TermMatrix w{buf + h.plane, cols, kDepth, pitch, (int64_t)pitch * cols, 1};
     VocabArgs a{};
     a.jobs = 1;
-    a.work[0] = {1, 1, 1, kDepth / kTileK, kDepth / kTileK, 1, 0, 0, 0, kBytesA};
+    a.work[0] = {1, 1, 1, kDepth / kTileK, kDepth / kTileK, 1, 0, 0, 0, kBytesA, 0};
     a.rows = rows;
     a.cols = cols;
     a.vocab = cols;
@@ -282,7 +282,7 @@ cudaError_t run_tiles_alone(int dev, int sms, VocabTile tile) {
     if (e == cudaSuccess && (!a.err || !term_map(h, kTileM, &maps[0]) ||
                              !term_map(w, cols / vocab_tile_ctas(tile), &maps[1])))
         e = cudaErrorInvalidValue;
-    if (e == cudaSuccess) e = launch_vocab(kVocabStats, 1, tile, maps, a, sms, nullptr);
+    if (e == cudaSuccess) e = launch_vocab(kVocabStats, kTerms1, tile, maps, a, sms, nullptr);
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     const cudaError_t f = cudaFree(buf);
     return e != cudaSuccess ? e : f;

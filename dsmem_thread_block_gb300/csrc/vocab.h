@@ -37,6 +37,7 @@ struct TileWork {
     int32_t a_mn, b_mn;    // operand lies with M (N) innermost
     int32_t b_y0;          // first row of B's matrix
     int32_t a_bytes;       // of A that a CTA's stage receives
+    int32_t both;          // A in two terms, both in a stage
 };
 
 // Where a product goes: rows x cols at `out` (of the call's type), or the
@@ -76,8 +77,12 @@ struct VocabArgs {
 };
 
 enum VocabOut : int { kVocabStats, kVocabGrad, kVocabProduct };
-// Results that the tensor cores' sums alone are not good enough for.
-constexpr bool vocab_promotes(VocabOut out, int dtype) { return out == kVocabStats || dtype == 0; }
+// What a call's operands are: bf16, bf16 with the logits' gradient in two terms, or
+// fp32 in three.
+enum VocabTerms : int { kTerms1 = 1, kTerms2 = 2, kTerms3 = 3 };
+// Results that the tensor cores' sums alone are not good enough for: all but bf16
+// products.
+constexpr bool vocab_promotes(VocabOut out, VocabTerms t) { return out != kVocabProduct || t == kTerms3; }
 
 // A call of a few tokens (vocab_few.cu).
 struct FewArgs {
@@ -110,11 +115,11 @@ cudaError_t launch_few_products(int dtype, bool vec, const FewArgs& a, int slice
 // box_rows: of a box (K innermost: the tile's rows; else the stage's k).
 bool term_map(const TermMatrix& m, int box_rows, CUtensorMap* map);
 
-const void* vocab_stats_kernel(int dtype, VocabTile t);
-const void* vocab_grad_kernel(int dtype, VocabTile t);
-const void* vocab_product_kernel(int dtype, VocabTile t);
+const void* vocab_stats_kernel(VocabTerms terms, VocabTile t);
+const void* vocab_grad_kernel(VocabTerms terms, VocabTile t);
+const void* vocab_product_kernel(VocabTerms terms, VocabTile t);
 
-cudaError_t launch_vocab(VocabOut out, int dtype, VocabTile tile, const CUtensorMap (&maps)[4],
+cudaError_t launch_vocab(VocabOut out, VocabTerms terms, VocabTile tile, const CUtensorMap (&maps)[4],
                          const VocabArgs& a, int sms, cudaStream_t s);
 // The tiles' kernel with nothing that brings B; allocates its scratch and waits for it.
 cudaError_t run_tiles_alone(int dev, int sms, VocabTile tile);

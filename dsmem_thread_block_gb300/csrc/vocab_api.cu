@@ -23,6 +23,11 @@ int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 constexpr int64_t kPieceBytes = (int64_t)256 << 20;
 // Most parts of a sum over the vocabulary.
 constexpr int kMaxSplits = 64;
+// Most tokens whose logits' gradient takes two bf16 terms.  Rounded to one, a token's
+// target is off by up to 2^-8, uniformly: the root mean square over T tokens varies by
+// 0.45 / sqrt(T) of itself, 8 % for 32.  The second term costs 64 tokens of 4096 x
+// 1024 20.2 us instead of 17.3, and 10 of 6907 x 512 16.5 instead of 15.6.
+constexpr int kTwoTerms = 32;
 // Fewest stages of a part.
 constexpr int kMinPart = 8;
 
@@ -31,9 +36,12 @@ constexpr int kTileN = vocab_tile_cols(kPair256);
 
 struct Shape {
     int64_t tokens, hidden, vocab;
-    int dtype, es, terms;
+    int dtype, es, terms;  // terms of the operands
+    VocabTerms kind;       // and of the logits' gradient
     bool pack_h, pack_w;   // the operand is copied as bf16 terms first
     bool few;              // takes the form for a few tokens
+    // rows of A in dhidden's product: two terms lie one behind the other
+    int64_t grad_rows() const { return kind == kTerms2 ? 2 * tokens : tokens; }
 };
 
 // Floats of a token in the shared memory of the form for a few tokens: whole steps
@@ -59,6 +67,7 @@ credit_status_t shape_of(const void* h, const void* w, int64_t tokens, int64_t h
     s->dtype = (int)dtype;
     s->es = dtype == CREDIT_F32 ? 4 : 2;
     s->terms = dtype == CREDIT_F32 ? 3 : 1;
+    s->kind = dtype == CREDIT_F32 ? kTerms3 : tokens <= kTwoTerms ? kTerms2 : kTerms1;
     if (!aligned(h, s->es) || !aligned(w, s->es)) return CREDIT_ERR_INVALID_ARG;
     const bool lines = hidden * s->es % 16 == 0;
     s->pack_h = s->terms > 1 || !lines || !aligned(h, 16);
@@ -87,6 +96,7 @@ struct Layout {
     int64_t piece;      // vocabulary rows at a time
     int32_t pieces;
     int64_t sums_pitch;
+    bool add;           // dhidden is the sums' sum
     void place(int64_t* at, int64_t n) {
         *at = bytes;
         bytes += round_up(n, 256);
@@ -144,12 +154,13 @@ struct Products {
 Products products_for(const Shape& s, int64_t piece, bool dh, bool dw, int sms) {
     Products best{};
     double least = 0;
-    const int64_t kb = ceil_div(piece, kTileK), kt = ceil_div(s.tokens, kTileK);
-    const int pairs = s.terms == 1 ? 1 : 6;
+    const int64_t kb = ceil_div(piece, kTileK), kt = ceil_div(s.tokens, kTileK) * (s.kind == kTerms2 ? 2 : 1);
+    const int64_t rows_h = s.grad_rows();
+    const int pairs = s.kind == kTerms3 ? 6 : 1;  // products a stage of k
     for (const VocabTile t : kTiles) {
         const int rows = vocab_tile_rows(t), cols = vocab_tile_cols(t), units = sms / vocab_tile_ctas(t);
         const int64_t nt = ceil_div(s.hidden, cols);
-        const int64_t th = dh ? ceil_div(s.tokens, rows) * nt : 0, tw = dw ? ceil_div(piece, rows) * nt : 0;
+        const int64_t th = dh ? ceil_div(rows_h, rows) * nt : 0, tw = dw ? ceil_div(piece, rows) * nt : 0;
         const double all = (double)th * tile_cost(t, (double)(kb * pairs)) +
                            (double)tw * tile_cost(t, (double)(kt * pairs));
         Products p{t, 1, (int32_t)kb};
@@ -178,15 +189,15 @@ Layout backward_layout(const Shape& s, bool dh, bool dw, int sms, Products* prod
     Layout l{};
     l.place(&l.h, operand_bytes(s, s.tokens, s.pack_h));
     l.place(&l.w, operand_bytes(s, s.vocab, s.pack_w));
-    const int64_t most = std::max<int64_t>(kTileN, kPieceBytes / (s.tokens * 2 * s.terms) / kTileN * kTileN);
+    const int64_t most = std::max<int64_t>(kTileN, kPieceBytes / (s.tokens * 2 * s.kind) / kTileN * kTileN);
     l.pieces = (int32_t)ceil_div(s.vocab, most);
     l.piece = round_up(ceil_div(s.vocab, l.pieces), kTileN);
     l.pieces = (int32_t)ceil_div(s.vocab, l.piece);
-    l.place(&l.grad, s.tokens * l.piece * 2 * s.terms);
+    l.place(&l.grad, s.tokens * l.piece * 2 * s.kind);
     *products = products_for(s, std::min(l.piece, s.vocab), dh, dw, sms);
     l.sums_pitch = round_up(s.hidden, 4);
-    if (dh && (products->splits > 1 || l.pieces > 1))
-        l.place(&l.sums, products->splits * s.tokens * l.sums_pitch * 4);
+    l.add = dh && (products->splits > 1 || l.pieces > 1 || s.kind == kTerms2);
+    if (l.add) l.place(&l.sums, products->splits * s.grad_rows() * l.sums_pitch * 4);
     return l;
 }
 
@@ -381,7 +392,7 @@ credit_status_t credit_linear_ce_forward(const void* hidden, const void* weight,
     a.parts = reinterpret_cast<float2*>(ws + l.parts);
     a.picked = reinterpret_cast<float*>(ws + l.picked);
     a.err = err;
-    if ((st = from_cuda(launch_vocab(kVocabStats, s.dtype, tile, maps, a, d->sms, q))) != CREDIT_OK)
+    if ((st = from_cuda(launch_vocab(kVocabStats, s.kind, tile, maps, a, d->sms, q))) != CREDIT_OK)
         return st;
     return from_cuda(launch_vocab_merge(a, 2 * a.work[0].nt, loss, lse, q));
 }
@@ -441,7 +452,6 @@ credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse,
     const TermMatrix w = operand(s, weight, vocab, s.pack_w, ws + l.w);
     if ((st = from_cuda(pack(s, hidden, h, weight, w, d->sms, q))) != CREDIT_OK) return st;
 
-    const bool sums = products.splits > 1 || l.pieces > 1;
     const VocabTile pt = products.tile, gt = logits_tile(s, l.piece, d->sms);
     // what the logits' gradient is formed from, and what it is multiplied with
     CUtensorMap logits[4] = {}, operands[4] = {};
@@ -468,32 +478,42 @@ credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse,
         a.grad_pitch = l.piece;
         a.grad_plane = l.piece * tokens;
         a.err = err;
-        if ((st = from_cuda(launch_vocab(kVocabGrad, s.dtype, gt, logits, a, d->sms, q))) != CREDIT_OK)
+        if ((st = from_cuda(launch_vocab(kVocabGrad, s.kind, gt, logits, a, d->sms, q))) != CREDIT_OK)
             return st;
-        const TermMatrix g{ws + l.grad, tokens, pv, l.piece * 2, l.piece * tokens * 2, s.terms};
+        const TermMatrix g{ws + l.grad, tokens, pv, l.piece * 2, l.piece * tokens * 2, s.kind};
         a.jobs = 0;
         if (dhidden) {
             // (a piece starts at a whole stage of k, and past its end g is zero)
-            TileWork& k = a.work[0] = work_of(pt, tokens, hidden_size, pv, false, true);
+            TermMatrix rows = g;  // (terms as rows)
+            if (s.kind == kTerms2) {
+                rows.rows = s.grad_rows();
+                rows.terms = 1;
+                rows.plane *= 2;
+            }
+            TileWork& k = a.work[0] = work_of(pt, rows.rows, hidden_size, pv, false, true);
             k.b_y0 = (int32_t)v0;
             // (a shorter last piece may leave parts without a stage: they add nothing)
             k.per = std::min(products.per, k.kb);
             k.splits = (int32_t)ceil_div(k.kb, k.per);
             ProductOut& o = a.out[0];
             o.out = dhidden;
-            o.sums = sums ? reinterpret_cast<float*>(ws + l.sums) : nullptr;
-            o.pitch = sums ? l.sums_pitch : hidden_size;
-            o.rows = (int32_t)tokens;
+            o.sums = l.add ? reinterpret_cast<float*>(ws + l.sums) : nullptr;
+            o.pitch = l.add ? l.sums_pitch : hidden_size;
+            o.rows = (int32_t)rows.rows;
             o.cols = (int32_t)hidden_size;
             o.add = p > 0;
             o.vec = aligned(dhidden, 16) && hidden_size * s.es % 16 == 0;
-            if (!term_map(g, box_rows(pt, tokens, &k), &operands[0]) || !term_map(w, kTileK, &operands[1]))
+            if (!term_map(rows, box_rows(pt, rows.rows, &k), &operands[0]) || !term_map(w, kTileK, &operands[1]))
                 return CREDIT_ERR_CUDA;
             a.jobs = 1;
         }
         if (dweight) {
             const int j = a.jobs++;
             a.work[j] = work_of(pt, pv, hidden_size, tokens, true, true);
+            if (s.kind == kTerms2) {
+                a.work[j].both = 1;
+                a.work[j].a_bytes *= 2;
+            }
             ProductOut& o = a.out[j];
             o = ProductOut{};
             o.out = static_cast<char*>(dweight) + v0 * hidden_size * s.es;
@@ -504,13 +524,13 @@ credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse,
             if (!term_map(g, kTileK, &operands[2 * j]) || !term_map(h, kTileK, &operands[2 * j + 1]))
                 return CREDIT_ERR_CUDA;
         }
-        if ((st = from_cuda(launch_vocab(kVocabProduct, s.dtype, pt, operands, a, d->sms, q))) !=
+        if ((st = from_cuda(launch_vocab(kVocabProduct, s.kind, pt, operands, a, d->sms, q))) !=
             CREDIT_OK)
             return st;
     }
-    if (dhidden && sums)
-        return from_cuda(launch_vocab_sum(s.dtype, reinterpret_cast<float*>(ws + l.sums), products.splits,
-                                          tokens, hidden_size, l.sums_pitch, dhidden, d->sms, q));
+    if (dhidden && l.add)  // (a split's terms lie one behind the other, as splits do)
+        return from_cuda(launch_vocab_sum(s.dtype, reinterpret_cast<float*>(ws + l.sums),
+                                          products.splits * (s.kind == kTerms2 ? 2 : 1), tokens, hidden_size, l.sums_pitch, dhidden, d->sms, q));
     return CREDIT_OK;
 }
 

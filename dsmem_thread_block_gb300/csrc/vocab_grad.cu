@@ -2,9 +2,9 @@
 #include "vocab_tiles.cuh"
 
 namespace credit {
-const void* vocab_grad_kernel(int dtype, VocabTile t) {
-    return dtype
-               ? vocab_kernel_of<GradOut<bf16>, vocab_promotes(kVocabGrad, 1), 1>(t)
-               : vocab_kernel_of<GradOut<float>, vocab_promotes(kVocabGrad, 0), 3>(t);
+const void* vocab_grad_kernel(VocabTerms terms, VocabTile t) {
+    return terms == kTerms1   ? vocab_kernel_of<GradOut<kTerms1>, kVocabGrad, kTerms1>(t)
+           : terms == kTerms2 ? vocab_kernel_of<GradOut<kTerms2>, kVocabGrad, kTerms1>(t)
+                              : vocab_kernel_of<GradOut<kTerms3>, kVocabGrad, kTerms3>(t);
 }
 }  // namespace credit

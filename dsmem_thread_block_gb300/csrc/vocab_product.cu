@@ -2,8 +2,9 @@
 #include "vocab_tiles.cuh"
 
 namespace credit {
-const void* vocab_product_kernel(int dtype, VocabTile t) {
-    return dtype
-               ? vocab_kernel_of<ProductRow<bf16>, vocab_promotes(kVocabProduct, 1), 1>(t) : vocab_kernel_of<ProductRow<float>, vocab_promotes(kVocabProduct, 0), 3>(t);
+const void* vocab_product_kernel(VocabTerms terms, VocabTile t) {
+    return terms == kTerms1   ? vocab_kernel_of<ProductRow<bf16>, kVocabProduct, kTerms1>(t)
+           : terms == kTerms2 ? vocab_kernel_of<ProductRow<bf16>, kVocabProduct, kTerms2>(t)
+                              : vocab_kernel_of<ProductRow<float>, kVocabProduct, kTerms3>(t);
 }
 }  // namespace credit

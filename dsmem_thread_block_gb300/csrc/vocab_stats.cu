@@ -2,8 +2,8 @@
 #include "vocab_tiles.cuh"
 
 namespace credit {
-const void* vocab_stats_kernel(int dtype, VocabTile t) {
-    return dtype ? vocab_kernel_of<StatsOut, vocab_promotes(kVocabStats, 1), 1>(t)
-                 : vocab_kernel_of<StatsOut, vocab_promotes(kVocabStats, 0), 3>(t);
+const void* vocab_stats_kernel(VocabTerms terms, VocabTile t) {
+    return terms == kTerms3 ? vocab_kernel_of<StatsOut, kVocabStats, kTerms3>(t)
+                            : vocab_kernel_of<StatsOut, kVocabStats, kTerms1>(t);
 }
 }  // namespace credit

@@ -6,11 +6,18 @@
 //
 // Precision.  The tensor cores add into an fp32 accumulator without rounding to
 // nearest: a sum over k drifts towards zero by some 2^-25 of itself an addition of
-// sixteen products, 7e-6 over 4096.  A bf16 result does not see that.  Where the
-// result is fp32 (the statistics, and every product of fp32 operands) the
+// sixteen products, 7e-6 over 4096.  A product rounded to bf16 does not see that.
+// The logits do (one of 30 is off by 2e-4, and so is the gradient p - 1 of a token
+// whose target is almost certain), and so do products of fp32 operands: there the
 // accumulator holds kPromote stages at a time, and the epilogue warps add these
 // parts in registers, which rounds to nearest; they do it while the next part is
 // multiplied.
+//
+// The gradient of the logits is rounded to bf16 for the products of bf16 operands.
+// Each token's error is dominated by its target's, so of few tokens' some are large:
+// up to 32 tokens it takes two terms, which costs little there.  For dhidden they are
+// rows of one tile, whose sums are added behind; for dweight a stage holds both terms
+// of A beside one B.
 //
 // fp32 operands come as three bf16 terms, x = x0 + x1 + x2 to 24 bits.  Of their
 // nine products six are formed; the others are below 2^-24 of x y.  A stage holds
@@ -196,16 +203,17 @@ struct StatsOut {
     const VocabArgs& a;
     int64_t to;          // the target's column in the tile, if it lies there
     int left, row;
-    bool live;
+    bool live, any;      // the row, a row of the warp's
     float m = -INFINITY, s = 0.f;
     __device__ StatsOut(const VocabArgs& args, const Tile& t, int row0, unsigned char*) : a(args) {
         row = row0 + (threadIdx.x & 31);
         live = row < a.rows;
+        any = row0 < a.rows;
         to = (live ? a.target[row] : -1) - a.v0 - t.n0;
         left = a.cols - t.n0;
     }
     __device__ __forceinline__ void take(int c, uint32_t (&v)[32]) {
-        if (c >= left) return;
+        if (c >= left || !any) return;
         if (c + 32 > left) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
@@ -245,7 +253,7 @@ struct StatsOut {
 };
 
 // The gradient of a token's logits, as bf16 terms.
-template <typename T> struct GradOut {
+template <VocabTerms TERMS> struct GradOut {
     const VocabArgs& a;
     int64_t to = -1;
     float scale = 0.f, both = 0.f, lse = 0.f;
@@ -277,12 +285,13 @@ template <typename T> struct GradOut {
         });
     }
     __device__ __forceinline__ void take(int c, const uint32_t (&v)[32]) {
+        if (rows <= 0) return;
         float g[32];
         const float off = -lse * kLog2e;
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
             const float z = __uint_as_float(v[j]);
-            const float e = sizeof(T) == 2 ? fast_ex2(fmaf(z, kLog2e, off)) : expf(z - lse);
+            const float e = TERMS != kTerms3 ? fast_ex2(fmaf(z, kLog2e, off)) : expf(z - lse);
             g[j] = none ? 0.f : both * e;
         }
         if (to >= c && to < c + 32) {
@@ -290,11 +299,11 @@ template <typename T> struct GradOut {
             for (int j = 0; j < 32; ++j)
                 if (to == c + j) g[j] -= scale;
         }
-        if constexpr (sizeof(T) == 2) {
+        if constexpr (TERMS == kTerms1) {
             write(out + c, g);
         } else {
 #pragma unroll 1
-            for (int k = 0; k < 3; ++k) {  // what is left of g, a term at a time
+            for (int k = 0; k < TERMS; ++k) {  // what is left of g, a term at a time
                 float x[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
@@ -375,12 +384,13 @@ template <typename T> struct ProductRow {
 };
 
 // ---------------------------------------------------------------- the kernel
-template <typename OUT, bool PROMOTE, int TERMS, int N, int CG>
-__global__ void __launch_bounds__(vocab_threads(PROMOTE, N), 1)
+template <typename OUT, VocabOut KIND, VocabTerms TERMS, int N, int CG>
+__global__ void __launch_bounds__(vocab_threads(vocab_promotes(KIND, TERMS), N), 1)
 vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUtensorMap b0,
             const __grid_constant__ CUtensorMap a1, const __grid_constant__ CUtensorMap b1,
             const __grid_constant__ VocabArgs a) {
     using S = TileShape<N, CG>;
+    constexpr bool PROMOTE = vocab_promotes(KIND, TERMS);
     constexpr int kWarps = vocab_warps(PROMOTE, N), kCols = N / (kWarps / 4);  // a warp's
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) VocabBars bars;
@@ -416,9 +426,10 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
     tmem_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
     // steps of k that the accumulators hold at a time
-    auto parts_of = [](int kn) { return !PROMOTE ? kn : TERMS == 1 ? kPromote : 1; };
+    auto parts_of = [](int kn) { return !PROMOTE ? kn : TERMS == kTerms1 ? kPromote : 1; };
     dependents_may_launch();
     wait_for_launches();
+    fence_proxy_async();  // an operand may be an earlier launch's
     Tile t;
     // The sums of an epilogue thread take registers that the other warps do not
     // need: of 384 x 168 at launch, 128 x 80 and 256 x 208.
@@ -440,7 +451,7 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
         // whole warp walks the stages and one elected lane issues: what the copies and
         // products take from uniform registers then stays there.  The warps that fill set
         // the pace of large calls: one thread for both operands in a loop over terms took
-        // 3.9 ms where this takes PLACEHOLDER (backward 4096 x 4096 x 65536 bf16).
+        // 3.9 ms where this takes 3.35 (backward 4096 x 4096 x 65536 bf16).
         auto arrived = [&](uint32_t b, uint32_t parity) {
             return (bool)__all_sync(0xffffffffu, hold(b, parity, a.err, dead));
         };
@@ -465,13 +476,14 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                     if (leader) {
                         if (rank == 0) mbar_arrive_expect_tx(full0 + bar, bytes);
                         boxes.load(k, term, at + offset, signal0 + bar);
+                        if (TERMS == kTerms2 && !B && w.both) boxes.load(k, 1, at + kBytesA, signal0 + bar);
                     }
                     ++filled;
                     advance();
                     return true;
                 };
                 for (int k = 0; k < t.kn; ++k)
-                    if (!(TERMS == 1 ? one(k, 0) : one(k, 2) && one(k, 1) && one(k, 0))) break;
+                    if (!(TERMS != kTerms3 ? one(k, 0) : one(k, 2) && one(k, 1) && one(k, 0))) break;
             }
             // a CTA that has given up leaves no copy in flight
             if (!ok && leader && rank == 0)
@@ -511,9 +523,11 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                                 mma_bf16<CG>(acc, da + q * step_a, db + q * step_b, desc, add || q > 0);
                     };
                     for (int k = k0; k < k1; ++k) {
-                        if constexpr (TERMS == 1) {
+                        if constexpr (TERMS != kTerms3) {
                             if (!there(full0 + bar, phase)) break;
-                            multiply(at, at, k > k0);
+                            const bool both = TERMS == kTerms2 && w.both;
+                            if (both) multiply(at + kBytesA, at, k > k0);
+                            multiply(at, at, k > k0 || both);
                             if (leader) mma_commit<CG>(empty0 + bar);
                             advance();
                         } else {
@@ -626,11 +640,11 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
     if (warp == kWarps + 1) tmem_free<CG>(tmem, S::kTmem);
 }
 
-template <typename OUT, bool PROMOTE, int TERMS> const void* vocab_kernel_of(VocabTile t) {
+template <typename OUT, VocabOut KIND, VocabTerms TERMS> const void* vocab_kernel_of(VocabTile t) {
     switch (t) {
-        case kPair256: return (const void*)vocab_tiles<OUT, PROMOTE, TERMS, 256, 2>;
-        case kOne256: return (const void*)vocab_tiles<OUT, PROMOTE, TERMS, 256, 1>;
-        default: return (const void*)vocab_tiles<OUT, PROMOTE, TERMS, 128, 1>;
+        case kPair256: return (const void*)vocab_tiles<OUT, KIND, TERMS, 256, 2>;
+        case kOne256: return (const void*)vocab_tiles<OUT, KIND, TERMS, 256, 1>;
+        default: return (const void*)vocab_tiles<OUT, KIND, TERMS, 128, 1>;
     }
 }
 

@@ -187,6 +187,27 @@ def test_refusals(what):
             credit.gradient_norm([g], workspace=torch.empty(1, dtype=torch.uint8, device="cuda"))
 
 
+def test_iterators_and_tuples():
+    grads = make([100, 7, 3000], ("f32", "bf16"), seed=9)
+    want = float(credit.gradient_norm(grads))
+    assert float(credit.gradient_norm(tuple(grads))) == want
+    assert float(credit.gradient_norm(g for g in grads)) == want
+    out = [torch.empty_like(g) for g in grads]
+    assert float(credit.clip_gradients((g for g in grads), 0.5, out=(o for o in out))) == want
+    copy = [g.clone() for g in grads]
+    assert float(credit.clip_gradients((g for g in copy), 0.5)) == want
+    assert all(torch.equal(a, b) for a, b in zip(copy, out))
+
+
+def test_more_elements_than_32_bits_count():
+    n = (1 << 32) + 12345
+    g = torch.zeros(n, device="cuda", dtype=torch.bfloat16)
+    g[0], g[1 << 31], g[n - 1] = 3.0, 4.0, 12.0
+    assert float(credit.clip_gradients([g], 6.5, eps=0.0)) == 13.0
+    assert (float(g[0]), float(g[1 << 31]), float(g[n - 1])) == (1.5, 2.0, 6.0)
+    assert int(torch.count_nonzero(g[: 1 << 31])) + int(torch.count_nonzero(g[1 << 31:])) == 3
+
+
 def test_versions_of_what_is_written():
     g = torch.ones(10, device="cuda")
     o, v = torch.empty_like(g), g._version

@@ -9,7 +9,8 @@ and leave out 3 u sum |h w|.  lse moves by no more than the worst logit does; it
 exponentials err by their argument's roundings, 4 u (max - min), and by 4 u, its
 sum by 100 additions, the logarithm and the sum with the maximum by 4 u |lse|.
 g errs by its logit's and lse's argument, and is rounded to bf16 (2^-8) for the
-products; fp32 keeps three terms (u).  dhidden and dweight sum over V and D terms
+products of more than 32 tokens; fewer keep two terms, or fp32, fp32 operands three
+(u).  dhidden and dweight sum over V and D terms
 as the logits do over D, in fp32 parts that are added in order, and are rounded
 once.  Where operands are small whole numbers every product and sum is exact, and
 so is the comparison.
@@ -281,6 +282,67 @@ def test_gradients_that_are_not_needed(need_h, need_w, tokens):
         assert_close(dw, want[1], want[3], "dweight")
     else:
         assert dw is None
+
+
+@pytest.mark.parametrize("tokens", [1, 20])
+def test_a_weight_of_more_elements_than_31_bits_count(tokens):
+    hidden, vocab = 8192, 270000
+    h, _, target = make(tokens, hidden, 8, torch.bfloat16, seed=15, ignored=0.0)
+    w = torch.zeros((vocab, hidden), dtype=torch.bfloat16, device="cuda")
+    # a few words of all zeros' company, the last one among them
+    words = torch.tensor([0, 5, 131071, 262143, 262144, vocab - 1], device="cuda")
+    w[words] = make(1, hidden, 6, torch.bfloat16, seed=16)[1] * 4
+    target = words[torch.arange(tokens, device="cuda") % 6]
+    loss, lse = credit.linear_cross_entropy_forward(h, w, target)
+    z, ez = ref_logits(h, w[words])
+    want = torch.logsumexp(torch.cat([z, torch.full((tokens, 1), (vocab - 6.0), device="cuda").double().log()], 1), 1)
+    e = ez.amax(1) + U * (104 + 8 * z.abs().amax(1) + 4 * want)
+    picked = z[torch.arange(tokens, device="cuda"), torch.arange(tokens, device="cuda") % 6]
+    assert_close(lse, want, e, "lse")
+    assert_close(loss, want - picked, e + ez.amax(1), "loss")
+    dloss = torch.ones(tokens, device="cuda")
+    dh, dw = credit.linear_cross_entropy_backward(dloss, h, w, target, lse)
+    # Of the words: the others' logits are 0.  g = p - [target] errs as p does, whose
+    # argument errs by its logit's and lse's roundings, and by its own rounding to
+    # bf16; the products add their sums' and outputs' roundings (ref_backward's bounds).
+    x = z - lse.double()[:, None]
+    p = x.exp()
+    g, eg = p.clone(), p * (ez + U * (6 * x.abs() + 2 * z.abs() + 10))
+    g[torch.arange(tokens), torch.arange(tokens) % 6] -= 1
+    eg = eg + (2.0 ** -8 + 2 * U) * (g.abs() + eg)
+    hd, wd = h.double(), w[words].double()
+
+    def bound(e, a, b, n):
+        mag = a.abs() @ b.abs()
+        return (e @ b.abs() + sums_err(n, h.dtype, mag)) * 1.01 + 2.0 ** -8 * (a @ b).abs()
+
+    assert_close(dw[words], g.t() @ hd, bound(eg.t(), g.t(), hd, tokens), "dweight")
+    assert_close(dh, g @ wd, bound(eg, g, wd, vocab), "dhidden")
+    # a word that is all zeros, anywhere: its logit is exactly 0
+    rest = (-lse.double()).exp()[:, None]
+    er = rest * U * (6 * lse.double().abs()[:, None] + 10) + (2.0 ** -8 + 2 * U) * rest
+    for v in (1, 131072, 262145, vocab - 2):
+        assert_close(dw[v], (rest.t() @ hd)[0], bound(er.t(), rest.t(), hd, tokens)[0], "dweight")
+
+
+def test_more_logits_than_32_bits_count():
+    # the first 1000 tokens over and over: every copy gets the same bits
+    hidden, vocab, copies = 24, 61000, 72
+    h, w, target = make(1000, hidden, vocab, torch.bfloat16, seed=17)
+    dloss = torch.rand(1000, device="cuda")
+    many = [t.repeat((copies,) + (1,) * (t.dim() - 1)) for t in (h, target, dloss)]
+    loss, lse = credit.linear_cross_entropy_forward(many[0], w, many[1])
+    want, want_lse, bound, bound_lse = ref_forward(h, w, target)
+    assert_close(lse[:1000], want_lse, bound_lse, "lse")
+    assert_close(loss[:1000], want, bound, "loss")
+    for t in (loss, lse):
+        assert bool((t.view(copies, 1000) == t[:1000]).all())
+    dh, dw = credit.linear_cross_entropy_backward(many[2], many[0], w, many[1], lse)
+    want_h, want_w, bound_h, bound_w = ref_backward(dloss, None, h, w, target, lse[:1000])
+    assert_close(dh[:1000], want_h, bound_h, "dhidden")
+    assert bool((dh.view(copies, 1000, hidden) == dh[:1000]).all())
+    # (the sum over 72 times the tokens errs 72 times over 72 times the magnitude)
+    assert_close(dw, copies * want_w, copies * copies * bound_w, "dweight")
 
 
 def test_no_tokens():
