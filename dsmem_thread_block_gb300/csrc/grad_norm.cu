@@ -1,5 +1,19 @@
 // grad_norm.cu -- the 2-norm of many tensors together, and their clipping:
 //   norm = sqrt(sum_i sum_e g_ie^2),  out_ie = g_ie min(1, max_norm / (norm + eps))
+//
+// Two kernels: every CTA sums the squares of a run of 32 KB chunks, whatever tensors
+// they lie in; then every CTA adds the CTAs' sums in one order and scales the same run.
+// Sums are fp32 over a thread's 32 or 64 elements of a chunk and 64 bits from there on.
+//
+// Bound by HBM: elements are read, read again once the norm is known, and written.
+// Measured (device time, share of the 6787 GB/s copy rate over those three passes):
+//   805 MB of bf16, clipped      383 us  0.93
+//   1.2 GB of fp32, clipped      562 us  0.95
+//   360 MB of 456 tensors, norm   60 us  0.88 (one pass; a run in flight a CTA, and the
+//                                 second launch)
+//   2.7 MB of 12 tensors         10 us   the call's host side
+// Runs are walked backwards the second time, and their ends are read with an L2 policy
+// that keeps them (71 MB of 805 are not read again): 391 us without.
 #include <algorithm>
 #include <climits>
 #include <vector>
@@ -18,7 +32,8 @@ constexpr int kThreads = 256;
 constexpr int kLoads = 8;                           // 16-byte vectors of a thread and chunk
 constexpr int kChunkBytes = kThreads * kLoads * 16;
 constexpr int kCtasPerSm = 4;
-// Of L2, what the sums leave there for the scaling: the last chunks of every CTA.
+// Of L2, what the sums leave there for the scaling: the last chunks of every CTA
+// (805 MB: none 391 us, a quarter 390, half 383, three quarters 382).
 constexpr int kKeepNum = 1, kKeepDen = 2;
 
 // The tensors of a launch, in its parameters: captured with it, nothing to copy

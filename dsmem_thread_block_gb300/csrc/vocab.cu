@@ -3,8 +3,14 @@
 //   g_tv = (dloss_t + dlse_t) exp(z_tv - lse_t) - dloss_t [v = target_t]
 //   dh = g w,  dw = g^T h
 //
-// The products are vocab_tiles.cuh's; here are what comes before and after them,
-// and the launches.
+// The products are vocab_tiles.cuh's, those of a few tokens vocab_few.cu's; here are
+// what comes before and after them, and the launches.
+//   vocab_pack   operands that tensor maps cannot take (rows that are no whole 16-byte
+//                lines, fp32) as bf16 terms; bound by HBM: 16384 x 2048 fp32 54 us
+//   vocab_merge  the tiles' statistics of a token: 4096 tokens of 128 parts 10 us alone
+//   vocab_sum    parts of dhidden in order: 4096 x 4096 20 us
+// All kernels of a call are launched early (early_launch.h), which saves some 3 us of
+// a small call (32 x 1024 x 4096 forward 13.4 us called without, 9.6 with).
 #include "early_launch.h"
 #include "vocab_tiles.cuh"
 

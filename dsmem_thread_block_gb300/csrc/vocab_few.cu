@@ -8,6 +8,12 @@
 //   few_products  a thread holds columns of every token's dhidden, and of the tokens,
 //                 and walks a slice of the vocabulary: w is read and dweight written
 //                 on the way
+//
+// Measured (device time): one token of 131072 x 4096 forward 163 us bf16 (0.97 of the
+// copy rate), 302 fp32; backward 547 bf16 (0.87 of it for the three passes over the
+// weight's size).  Bound by HBM for one token; by the shared-memory reads of the tokens
+// for eight (131072 x 2048 bf16 225 us, fp32 264), so aligned bf16 takes tiles from two
+// tokens on.  A lane has 16 vectors in flight for one token (four took 220 us).
 #include <algorithm>
 
 #include "early_launch.h"
