@@ -613,7 +613,7 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                     for (int c = 0; c < kCols; c += 32) {
                         uint32_t v[32];
                         tmem_load(acc + c, v);
-                    tmem_load_wait();
+                        tmem_load_wait();
 #pragma unroll
                         for (int j = 0; j < 32; j += 2) {
                             const F2 x{__uint_as_float(v[j]), __uint_as_float(v[j + 1])};

@@ -199,8 +199,9 @@ def linear_cross_entropy_backward(dloss, hidden, weight, target, lse, dlse=None,
                                   need_dweight: bool = True, dhidden=None, dweight=None,
                                   workspace=None):
     """The gradient of linear_cross_entropy_forward: from dloss (of each token's
-    loss; of an ignored one it does not count) and dlse (of its lse, or None),
-    returns (dhidden, dweight).  One that is not needed is None, unless a tensor
+    loss; of an ignored one it does not count) and dlse (of its lse, or None), both
+    fp32 and contiguous (what autograd hands a mean's backward is expanded:
+    `.contiguous()`), returns (dhidden, dweight).  One that is not needed is None, unless a tensor
     for it is given in `dhidden` or `dweight`."""
     if C._lib is not _bound or _bound is None:
         _bind()
