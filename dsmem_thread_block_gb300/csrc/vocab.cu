@@ -19,7 +19,6 @@ namespace credit {
 namespace {
 
 // --------------------------------------------------------- the small kernels
-constexpr int kMergeThreads = 256;
 constexpr int kMergeRows = 4;   // of a CTA: a sector of each part
 
 // (m, s) and another pair: the larger maximum, the sums scaled to it.
@@ -29,12 +28,13 @@ __device__ __forceinline__ void merge_pair(float& m, float& s, float mo, float s
     m = top;
 }
 
-// The parts of four tokens: 64 threads a token, each every 64th part.  (A token a
-// lane, 16 warps over the parts, took 17 us for 64 tokens of 1024 parts.)
-__global__ void __launch_bounds__(kMergeThreads)
-vocab_merge(VocabArgs a, int nparts, float* loss, float* lse) {
-    constexpr int kGroups = kMergeThreads / kMergeRows;
-    __shared__ float2 sums[kMergeThreads / 32][kMergeRows];
+// The parts of four tokens: THREADS / 4 threads a token, each every THREADS / 4th
+// part, 1024 threads from 512 parts on.  (A token a lane, 16 warps over the parts,
+// took 17 us for 64 tokens of 1024 parts.)
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) vocab_merge(VocabArgs a, int nparts, float* loss, float* lse) {
+    constexpr int kGroups = THREADS / kMergeRows;
+    __shared__ float2 sums[THREADS / 32][kMergeRows];
     dependents_may_launch();
     wait_for_launches();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -67,7 +67,7 @@ vocab_merge(VocabArgs a, int nparts, float* loss, float* lse) {
     if (lane < kMergeRows) sums[warp][lane] = make_float2(m, s);
     __syncthreads();
     if (threadIdx.x >= kMergeRows || !live) return;
-    for (int w = 1; w < kMergeThreads / 32; ++w) merge_pair(m, s, sums[w][mine].x, sums[w][mine].y);
+    for (int w = 1; w < THREADS / 32; ++w) merge_pair(m, s, sums[w][mine].x, sums[w][mine].y);
     const float l = (isinf(m) ? 0.f : m) + logf(s);
     const int64_t target = a.target[row];
     lse[row] = l;
@@ -277,7 +277,7 @@ cudaError_t launch_vocab(VocabOut out, VocabTerms terms, VocabTile tile, const C
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(units * ctas));
-    cfg.blockDim = dim3((unsigned)vocab_threads(vocab_promotes(out, terms), vocab_tile_cols(tile)));
+    cfg.blockDim = dim3((unsigned)vocab_threads(vocab_tile_cols(tile)));
     cfg.dynamicSmemBytes = kVocabSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -296,7 +296,7 @@ cudaError_t run_tiles_alone(int dev, int sms, VocabTile tile) {
     // one tile, more steps of k than a ring has stages
     constexpr int kDepth = 2 * kVocabStages * kTileK;
     const int rows = vocab_tile_rows(tile), cols = vocab_tile_cols(tile), pitch = 2 * kDepth;
-    const size_t need = (size_t)(rows + cols) * pitch + (size_t)rows * (8 + 4 + 2 * 8);
+    const size_t need = (size_t)(rows + cols) * pitch + (size_t)rows * (8 + 4 + 8 * vocab_tile_parts(tile));
     char* buf = nullptr;
     cudaError_t e = cudaMalloc(&buf, need);
     if (e != cudaSuccess) return e;
@@ -310,9 +310,9 @@ cudaError_t run_tiles_alone(int dev, int sms, VocabTile tile) {
     a.cols = cols;
     a.vocab = cols;
     char* const rest = buf + h.plane + w.plane;
-    a.parts = reinterpret_cast<float2*>(rest);
-    a.target = reinterpret_cast<int64_t*>(rest + (size_t)rows * 16);
-    a.picked = reinterpret_cast<float*>(rest + (size_t)rows * 24);
+    a.target = reinterpret_cast<int64_t*>(rest);
+    a.picked = reinterpret_cast<float*>(rest + (size_t)rows * 8);
+    a.parts = reinterpret_cast<float2*>(rest + (size_t)rows * 12);
     a.err = device_error_word();
     a.alone = 1;
     CUtensorMap maps[4] = {};
@@ -327,8 +327,9 @@ cudaError_t run_tiles_alone(int dev, int sms, VocabTile tile) {
 
 cudaError_t launch_vocab_merge(const VocabArgs& a, int nparts, float* loss, float* lse,
                                cudaStream_t s) {
-    return launch_early(vocab_merge, dim3((unsigned)((a.rows + kMergeRows - 1) / kMergeRows)), kMergeThreads, s,
-                        a, nparts, loss, lse);
+    const dim3 grid((unsigned)((a.rows + kMergeRows - 1) / kMergeRows));
+    return nparts < 512 ? launch_early(vocab_merge<256>, grid, 256, s, a, nparts, loss, lse)
+                        : launch_early(vocab_merge<1024>, grid, 1024, s, a, nparts, loss, lse);
 }
 
 cudaError_t launch_vocab_pack(int dtype, const void* const (&src)[2], const TermMatrix (&dst)[2], int n,

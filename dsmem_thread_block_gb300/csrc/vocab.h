@@ -19,6 +19,9 @@ enum VocabTile : int {
 constexpr int vocab_tile_rows(VocabTile t) { return t == kPair256 ? 2 * kTileM : kTileM; }
 constexpr int vocab_tile_cols(VocabTile t) { return t == kOne128 ? 128 : 256; }
 constexpr int vocab_tile_ctas(VocabTile t) { return t == kPair256 ? 2 : 1; }
+// parts of the statistics: one for an epilogue warp's columns
+constexpr int kPartCols = 64;
+constexpr int vocab_tile_parts(VocabTile t) { return vocab_tile_cols(t) / kPartCols; }
 
 // A matrix of bf16 terms: `terms` planes of rows x cols, rows `pitch` bytes and
 // planes `plane` bytes apart, all 16-byte aligned.
@@ -61,7 +64,7 @@ struct VocabArgs {
     int64_t vocab;
     const int64_t* target;
     int64_t ignore;
-    // statistics: per (half of a tile's columns, token) maximum and sum of exponentials, and
+    // statistics: per (kPartCols columns, token) maximum and sum of exponentials, and
     // the target's logit per token
     float2* parts;
     float* picked;

@@ -139,7 +139,7 @@ Layout forward_layout(const Shape& s, VocabTile t) {
     Layout l{};
     l.place(&l.h, operand_bytes(s, s.tokens, s.pack_h));
     l.place(&l.w, operand_bytes(s, s.vocab, s.pack_w));
-    l.place(&l.parts, 2 * ceil_div(s.vocab, vocab_tile_cols(t)) * s.tokens * 8);
+    l.place(&l.parts, ceil_div(s.vocab, vocab_tile_cols(t)) * vocab_tile_parts(t) * s.tokens * 8);
     l.place(&l.picked, s.tokens * 4);
     return l;
 }
@@ -394,7 +394,7 @@ credit_status_t credit_linear_ce_forward(const void* hidden, const void* weight,
     a.err = err;
     if ((st = from_cuda(launch_vocab(kVocabStats, s.kind, tile, maps, a, d->sms, q))) != CREDIT_OK)
         return st;
-    return from_cuda(launch_vocab_merge(a, 2 * a.work[0].nt, loss, lse, q));
+    return from_cuda(launch_vocab_merge(a, a.work[0].nt * vocab_tile_parts(tile), loss, lse, q));
 }
 
 credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse, const void* hidden,

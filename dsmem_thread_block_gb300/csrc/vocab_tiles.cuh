@@ -57,13 +57,11 @@
 
 namespace credit {
 
-// Warps of the epilogue: a quarter of them for each 32 of a tile's 128 rows.  One
-// warp's chain of loads, exponentials and stores leaves two of three issue slots
-// empty, so there are sixteen, but where the parts' sums take their registers, and
-// for narrow tiles, of small calls, whose launch they would only make longer.
-constexpr int vocab_warps(bool promote, int columns) { return promote || columns < 256 ? 8 : 16; }
-// whole warpgroups; two of the other four warps only wait
-constexpr int vocab_threads(bool promote, int columns) { return 32 * (vocab_warps(promote, columns) + 4); }
+// Warps of the epilogue: a quarter of them for each 32 of a tile's 128 rows, 64
+// columns a warp.  (Eight for 256 columns left two of three issue slots empty.)
+constexpr int vocab_warps(int columns) { return columns / kPartCols * 4; }
+// whole warpgroups; one of the other four warps only waits
+constexpr int vocab_threads(int columns) { return 32 * (vocab_warps(columns) + 4); }
 constexpr int kBoxBytes = 64 * kTileK * 2;      // one box of an operand with M or N innermost
 constexpr int kBytesA = kTileM * kTileK * 2;
 constexpr int kVocabRing = 6 * 32768;           // bytes of all stages
@@ -403,13 +401,13 @@ template <typename T> struct ProductRow {
 
 // ---------------------------------------------------------------- the kernel
 template <typename OUT, VocabOut KIND, VocabTerms TERMS, int N, int CG>
-__global__ void __launch_bounds__(vocab_threads(vocab_promotes(KIND, TERMS), N), 1)
+__global__ void __launch_bounds__(vocab_threads(N), 1)
 vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUtensorMap b0,
             const __grid_constant__ CUtensorMap a1, const __grid_constant__ CUtensorMap b1,
             const __grid_constant__ VocabArgs a) {
     using S = TileShape<N, CG>;
     constexpr bool PROMOTE = vocab_promotes(KIND, TERMS);
-    constexpr int kWarps = vocab_warps(PROMOTE, N), kCols = N / (kWarps / 4);  // a warp's
+    constexpr int kWarps = vocab_warps(N), kCols = kPartCols;  // a warp's
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) VocabBars bars;
     __shared__ uint32_t tmem_base;
@@ -450,9 +448,13 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
     fence_proxy_async();  // an operand may be an earlier launch's
     Tile t;
     // The sums of an epilogue thread take registers that the other warps do not
-    // need: of 384 x 168 at launch, 128 x 80 and 256 x 208.
+    // need: of 640 x 96 at launch 128 x 64 and 512 x 104, of 384 x 168 128 x 80 and
+    // 256 x 208.
     if (warp >= kWarps) {
-        if constexpr (PROMOTE) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if constexpr (PROMOTE) {
+            if constexpr (kWarps == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+            else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        }
         const uint32_t full0 = smem_u32(&bars.full[0]), empty0 = smem_u32(&bars.empty[0]);
         const uint32_t end = ring + (uint32_t)(stages * stage);
         uint32_t at = ring, bar = 0, phase = 0;  // of the present stage; bar: 8 bytes each
@@ -578,7 +580,10 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
             }
         }
     } else {
-        if constexpr (PROMOTE) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        if constexpr (PROMOTE) {
+            if constexpr (kWarps == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+            else asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        }
         const int quarter = warp & 3, block = warp >> 2;  // of rows, of columns
         unsigned char* const room = raw + (ring - smem_u32(raw)) + kVocabRing + warp * kTurnBytes;
         int n = 0;
@@ -602,6 +607,7 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
         for (int i = 0; ok && tile_at<N, CG>(a, unit, units, rank, i, &t); ++i) {
             OUT out(a, t, t.m0 + 32 * quarter, room);
             if constexpr (PROMOTE) {
+                constexpr int kLoad = kWarps == 8 ? 32 : 16;  // as registers allow
                 F2 sum[kCols / 2];
 #pragma unroll
                 for (int j = 0; j < kCols / 2; ++j) sum[j] = f2(0.f);
@@ -610,12 +616,12 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                     const uint32_t acc = ready();
                     if (!ok) break;
 #pragma unroll
-                    for (int c = 0; c < kCols; c += 32) {
-                        uint32_t v[32];
+                    for (int c = 0; c < kCols; c += kLoad) {
+                        uint32_t v[kLoad];
                         tmem_load(acc + c, v);
                         tmem_load_wait();
 #pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
+                        for (int j = 0; j < kLoad; j += 2) {
                             const F2 x{__uint_as_float(v[j]), __uint_as_float(v[j + 1])};
                             sum[(c + j) / 2] = add2(sum[(c + j) / 2], x);
                         }

@@ -387,8 +387,7 @@ credit_status_t credit_norm_backward(credit_op_t op, const void *dy, const void 
  * tokens x hidden_size, weight vocab x hidden_size, both of `dtype` and
  * contiguous; tokens == 0 is a legal empty batch.  The tokens x vocab logits are
  * formed a tile at a time by the tensor cores and reduced there: the forward
- * pass keeps a maximum and a sum per token and half a tile (8 bytes for 64 or
- * 128 logits), the backward pass the gradient of one piece of the vocabulary at
+ * pass keeps a maximum and a sum per token and 64 columns (8 bytes), the backward pass the gradient of one piece of the vocabulary at
  * a time, 256 MiB of it (bf16 operands: rounded to bf16 for the two products,
  * to two bf16 terms up to 32 tokens).  fp32 operands are taken apart into three
  * bf16 terms each and multiplied in six products, which keeps 24 bits; a value
