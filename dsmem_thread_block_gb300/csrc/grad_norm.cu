@@ -7,8 +7,8 @@
 //
 // Bound by HBM: elements are read, read again once the norm is known, and written.
 // Measured (device time, share of the 6787 GB/s copy rate over those three passes):
-//   805 MB of bf16, clipped      383 us  0.93
-//   1.2 GB of fp32, clipped      562 us  0.95
+//   805 MB of bf16, clipped      379 us  0.94
+//   1.2 GB of fp32, clipped      552 us  0.97
 //   360 MB of 456 tensors, norm   60 us  0.88 (one pass; a run in flight a CTA, and the
 //                                 second launch)
 //   2.7 MB of 12 tensors         10 us   the call's host side

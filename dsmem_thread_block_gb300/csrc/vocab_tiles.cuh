@@ -11,15 +11,15 @@
 // cores' rate.
 //
 // Measured (GB300, device time; the tensor pipe's share of cycles from ncu):
-//   statistics 4096 x 4096 x 131072 bf16    2.16 ms  2036 TFLOP/s (cuBLAS burst 1901,
+//   statistics 4096 x 4096 x 131072 bf16    2.18 ms  2015 TFLOP/s (cuBLAS burst 1901,
 //                                            sustained 1695); pipe 90 % active
-//   gradient and products 4096 x 4096 x 65536  3.38 ms  1954 TFLOP/s; 89 % and 95 %
-//   the same called back to back            2.27 and 3.72 ms: the power limit
+//   gradient and products 4096 x 4096 x 65536  3.32 to 3.41 ms  1988 TFLOP/s; 89, 95 %
+//   the same called back to back            2.20 to 2.51 and 3.53 to 3.88 ms: power
 //   32 x 1024 x 4096                        9.4 us forward, 64 tokens backward 16.7
 //   512 x 2048 x 16384 fp32                 171 us, 54 of them packing; pipe 75 %
 // What bounds the others: up to some 256 tokens the weight's read (64 x 4096 x 131072
-// 183 us, 0.87 of the copy rate); short k the epilogue (2048 x 256 x 32768 49 us: some
-// 2 us a tile of 256 columns, in latency: 8 warps fill 38 % of the issue slots); small calls one tile's latency (k / 16 products of 128 cycles, then
+// 180 us, 0.88 of the copy rate); short k the epilogue (2048 x 256 x 32768 43 us, some
+// 2 us a tile of 256 columns); small calls one tile's latency (k / 16 products of 128 cycles, then
 // its epilogue).
 //
 // Precision.  The tensor cores add into an fp32 accumulator without rounding to
