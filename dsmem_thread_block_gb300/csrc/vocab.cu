@@ -8,7 +8,9 @@
 //   vocab_pack   operands that tensor maps cannot take (rows that are no whole 16-byte
 //                lines, fp32) as bf16 terms; bound by HBM: 16384 x 2048 fp32 54 us
 //   vocab_merge  the tiles' statistics of a token: 4096 tokens of 128 parts 10 us alone
-//   vocab_sum    parts of dhidden in order: 4096 x 4096 20 us
+//   vocab_rows   from logits that were summed in parts of k, where they have few tiles,
+//                the statistics or the gradient
+//   vocab_sum    parts of dhidden, or of dweight, in order: 4096 x 4096 20 us
 // All kernels of a call are launched early (early_launch.h), which saves some 3 us of
 // a small call (32 x 1024 x 4096 forward 13.4 us called without, 9.6 with).
 #include "early_launch.h"
@@ -73,6 +75,87 @@ __global__ void __launch_bounds__(THREADS) vocab_merge(VocabArgs a, int nparts, 
     lse[row] = l;
     loss[row] = target == a.ignore ? 0.f
                 : target < 0 || target >= a.vocab ? NAN : l - a.picked[row];
+}
+
+// A CTA a token, four columns a thread at a time.
+constexpr int kRowThreads = 256;
+template <int TERMS>   // 0: the statistics
+__global__ void __launch_bounds__(kRowThreads)
+vocab_rows(VocabArgs a, const float* sums, int splits, int64_t pitch, float* loss, float* lse) {
+    __shared__ float2 parts[kRowThreads / 32];
+    __shared__ float picked;
+    dependents_may_launch();
+    wait_for_launches();
+    const int64_t row = blockIdx.x, plane = a.rows * pitch;
+    const float* const first = sums + row * pitch;
+    const int64_t target = a.target[row];
+    const bool ignored = target == a.ignore, outside = target < 0 || target >= a.vocab;
+    float scale = 0.f, both = 0.f, known = 0.f;
+    if (TERMS > 0) {
+        scale = ignored ? 0.f : outside ? NAN : a.dloss[row];
+        both = scale + (a.dlse ? a.dlse[row] : 0.f);
+        known = a.lse[row];
+    }
+    float m = -INFINITY, s = 0.f;
+    for (int c = 4 * (int)threadIdx.x; c < a.cols; c += 4 * kRowThreads) {
+        const float* p = first + c;
+        float4 f = __ldcg(reinterpret_cast<const float4*>(p));
+#pragma unroll 8
+        for (int k = 1; k < splits; ++k) {
+            p += plane;
+            const float4 g = __ldcg(reinterpret_cast<const float4*>(p));
+            f = make_float4(f.x + g.x, f.y + g.y, f.z + g.z, f.w + g.w);
+        }
+        const float z[4] = {f.x, f.y, f.z, f.w};
+        if constexpr (TERMS == 0) {
+            float top = m;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c + j < a.cols) top = fmaxf(top, z[j]);
+            const float base = isinf(top) ? 0.f : top;
+            s = s == 0.f ? 0.f : s * expf(m - base);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c + j < a.cols) {
+                    s += expf(z[j] - base);
+                    if (target == c + j) picked = z[j];
+                }
+            m = top;
+        } else {
+            float g[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                g[j] = both == 0.f ? 0.f : both * expf(z[j] - known);
+                if (target == a.v0 + c + j && !ignored) g[j] -= scale;
+            }
+            bf16* const out = static_cast<bf16*>(a.grad) + row * a.grad_pitch + c;
+#pragma unroll
+            for (int k = 0; k < TERMS; ++k) {
+                float t[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    t[j] = first_term(g[j]);
+                    g[j] = rest_of(g[j], t[j]);
+                }
+                *reinterpret_cast<uint2*>(out + k * a.grad_plane) =
+                    make_uint2(Elem<bf16>::pack2(t[0], t[1]), Elem<bf16>::pack2(t[2], t[3]));
+            }
+        }
+    }
+    if constexpr (TERMS == 0) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float mo = __shfl_xor_sync(0xffffffffu, m, o), so = __shfl_xor_sync(0xffffffffu, s, o);
+            merge_pair(m, s, mo, so);
+        }
+        if ((threadIdx.x & 31) == 0) parts[threadIdx.x >> 5] = make_float2(m, s);
+        __syncthreads();
+        if (threadIdx.x) return;
+        for (int w = 1; w < kRowThreads / 32; ++w) merge_pair(m, s, parts[w].x, parts[w].y);
+        const float l = (isinf(m) ? 0.f : m) + logf(s);
+        lse[row] = l;
+        loss[row] = ignored ? 0.f : outside ? NAN : l - picked;
+    }
 }
 
 // The 16 bytes at `p`, at any even address, from the two lines that hold them.
@@ -254,6 +337,7 @@ cudaError_t launch_vocab(VocabOut out, VocabTerms terms, VocabTile tile, const C
                          const VocabArgs& args, int sms, cudaStream_t s) {
     const void* fn = out == kVocabStats ? vocab_stats_kernel(terms, tile)
                      : out == kVocabGrad ? vocab_grad_kernel(terms, tile)
+                     : out == kVocabSums ? vocab_sums_kernel(terms)
                                          : vocab_product_kernel(terms, tile);
     int dev;
     cudaError_t e = cudaGetDevice(&dev);
@@ -330,6 +414,13 @@ cudaError_t launch_vocab_merge(const VocabArgs& a, int nparts, float* loss, floa
     const dim3 grid((unsigned)((a.rows + kMergeRows - 1) / kMergeRows));
     return nparts < 512 ? launch_early(vocab_merge<256>, grid, 256, s, a, nparts, loss, lse)
                         : launch_early(vocab_merge<1024>, grid, 1024, s, a, nparts, loss, lse);
+}
+
+cudaError_t launch_vocab_rows(const VocabArgs& a, const float* sums, int splits, int64_t pitch,
+                              VocabTerms terms, float* loss, float* lse, cudaStream_t s) {
+    auto* fn = !a.grad ? vocab_rows<0>
+               : terms == kTerms1 ? vocab_rows<1> : terms == kTerms2 ? vocab_rows<2> : vocab_rows<3>;
+    return launch_early(fn, dim3((unsigned)a.rows), kRowThreads, s, a, sums, splits, pitch, loss, lse);
 }
 
 cudaError_t launch_vocab_pack(int dtype, const void* const (&src)[2], const TermMatrix (&dst)[2], int n,

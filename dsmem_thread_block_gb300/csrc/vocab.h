@@ -79,7 +79,8 @@ struct VocabArgs {
     int32_t alone;         // a self-test: nothing brings B, every wait runs out
 };
 
-enum VocabOut : int { kVocabStats, kVocabGrad, kVocabProduct };
+// kVocabSums: the logits themselves, as fp32 sums of their splits.
+enum VocabOut : int { kVocabStats, kVocabGrad, kVocabProduct, kVocabSums };
 // What a call's operands are: bf16, bf16 with the logits' gradient in two terms, or
 // fp32 in three.
 enum VocabTerms : int { kTerms1 = 1, kTerms2 = 2, kTerms3 = 3 };
@@ -122,6 +123,8 @@ const void* vocab_stats_kernel(VocabTerms terms, VocabTile t);
 const void* vocab_grad_kernel(VocabTerms terms, VocabTile t);
 const void* vocab_product_kernel(VocabTerms terms, VocabTile t);
 
+const void* vocab_sums_kernel(VocabTerms terms);   // kOne128 alone
+
 cudaError_t launch_vocab(VocabOut out, VocabTerms terms, VocabTile tile, const CUtensorMap (&maps)[4],
                          const VocabArgs& a, int sms, cudaStream_t s);
 // The tiles' kernel with nothing that brings B; allocates its scratch and waits for it.
@@ -129,6 +132,10 @@ cudaError_t run_tiles_alone(int dev, int sms, VocabTile tile);
 // loss and lse from the tiles' parts
 cudaError_t launch_vocab_merge(const VocabArgs& a, int nparts, float* loss, float* lse,
                                cudaStream_t s);
+// From the splits' sums of the logits, splits x tokens x pitch: loss and lse, or with
+// a.grad the logits' gradient in `terms` terms.
+cudaError_t launch_vocab_rows(const VocabArgs& a, const float* sums, int splits, int64_t pitch,
+                              VocabTerms terms, float* loss, float* lse, cudaStream_t s);
 // n matrices of the call's type and of one width as bf16 terms
 cudaError_t launch_vocab_pack(int dtype, const void* const (&src)[2], const TermMatrix (&dst)[2], int n,
                               int sms, cudaStream_t s);

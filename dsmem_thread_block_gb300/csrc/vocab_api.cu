@@ -92,7 +92,7 @@ int64_t operand_bytes(const Shape& s, int64_t rows, bool pack) {
 
 // The workspace of a call, in the order of its parts.
 struct Layout {
-    int64_t h, w, parts, picked, grad, sums, bytes;  // offsets
+    int64_t h, w, parts, picked, logits, grad, sums, dw, bytes;  // offsets
     int64_t piece;      // vocabulary rows at a time
     int32_t pieces;
     int64_t sums_pitch;
@@ -135,10 +135,37 @@ VocabTile logits_tile(const Shape& s, int64_t cols, int sms) {
     return tile_for(s.tokens, cols, ceil_div(s.hidden, kTileK) * (s.terms == 1 ? 1 : 6), sms);
 }
 
-Layout forward_layout(const Shape& s, VocabTile t) {
+// Parts of k of a product whose tiles of 128 x 128 would leave half of the SMs idle
+// (1: it is not split); `pairs` products a stage, a part of four stages' at least.
+// The parts' sums go through memory and another kernel, some 6 us: what a tile saves
+// has to be worth them, 32 stages of 0.27 us (bf16 loss of 32, 1024 x 4096, 12 stages
+// less: 11.5 us split, 9.8 whole; of 200, 2048 x 2048, 24 less: 13.1 and 12.6; of 64,
+// 4096 x 4096, 48 less: 14.4 and 18.7; fp32 of 38, 4864 x 246: 19 and 90; dweight of
+// 8192, 64 x 128 with its call: 14 and 31).
+struct Split {
+    int32_t splits, per;
+    int64_t pitch;      // of a row's sums
+};
+Split split_for(int64_t rows, int64_t cols, int64_t k, int pairs, int sms) {
+    const int64_t kb = ceil_div(k, kTileK), least = pairs > 1 ? 2 : 4;
+    const int64_t tiles = ceil_div(rows, vocab_tile_rows(kOne128)) * ceil_div(cols, vocab_tile_cols(kOne128));
+    const int64_t want = std::min<int64_t>({sms / tiles, kb / least, kMaxSplits});
+    const int64_t per = want > 1 ? ceil_div(kb, want) : kb;
+    const bool worth = (kb - per) * pairs >= 32;
+    return {worth ? (int32_t)ceil_div(kb, per) : 1, (int32_t)(worth ? per : kb), round_up(cols, 4)};
+}
+Split logits_split(const Shape& s, int64_t cols, int sms) {
+    return split_for(s.tokens, cols, s.hidden, s.terms == 1 ? 1 : 6, sms);
+}
+
+Layout forward_layout(const Shape& s, VocabTile t, const Split& k) {
     Layout l{};
     l.place(&l.h, operand_bytes(s, s.tokens, s.pack_h));
     l.place(&l.w, operand_bytes(s, s.vocab, s.pack_w));
+    if (k.splits > 1) {
+        l.place(&l.logits, k.splits * s.tokens * k.pitch * 4);
+        return l;
+    }
     l.place(&l.parts, ceil_div(s.vocab, vocab_tile_cols(t)) * vocab_tile_parts(t) * s.tokens * 8);
     l.place(&l.picked, s.tokens * 4);
     return l;
@@ -150,6 +177,7 @@ Layout forward_layout(const Shape& s, VocabTile t) {
 struct Products {
     VocabTile tile;
     int32_t splits, per;
+    Split dw;            // of dweight's sum over the tokens
 };
 Products products_for(const Shape& s, int64_t piece, bool dh, bool dw, int sms) {
     Products best{};
@@ -163,7 +191,7 @@ Products products_for(const Shape& s, int64_t piece, bool dh, bool dw, int sms) 
         const int64_t th = dh ? ceil_div(rows_h, rows) * nt : 0, tw = dw ? ceil_div(piece, rows) * nt : 0;
         const double all = (double)th * tile_cost(t, (double)(kb * pairs)) +
                            (double)tw * tile_cost(t, (double)(kt * pairs));
-        Products p{t, 1, (int32_t)kb};
+        Products p{t, 1, (int32_t)kb, {}};
         double time = all / units;
         if (dh) {
             const int64_t share = std::max<int64_t>(kMinPart, (int64_t)(all / units / 2 / pairs));
@@ -195,6 +223,14 @@ Layout backward_layout(const Shape& s, bool dh, bool dw, int sms, Products* prod
     l.pieces = (int32_t)ceil_div(s.vocab, l.piece);
     l.place(&l.grad, s.tokens * l.piece * 2 * s.kind);
     *products = products_for(s, std::min(l.piece, s.vocab), dh, dw, sms);
+    const Split k = logits_split(s, l.piece, sms);
+    if (k.splits > 1) l.place(&l.logits, k.splits * s.tokens * k.pitch * 4);
+    Split& d = products->dw;
+    d = split_for(l.piece, s.hidden, s.tokens, s.terms == 1 ? 1 : 6, sms);
+    if (dw && d.splits > 1) {
+        products->tile = kOne128;
+        l.place(&l.dw, d.splits * std::min(l.piece, s.vocab) * d.pitch * 4);
+    }
     l.sums_pitch = round_up(s.hidden, 4);
     l.add = dh && (products->splits > 1 || l.pieces > 1 || s.kind == kTerms2);
     if (l.add) l.place(&l.sums, products->splits * s.grad_rows() * l.sums_pitch * 4);
@@ -288,6 +324,13 @@ int box_rows(VocabTile t, int64_t rows, TileWork* w) {
     return box;
 }
 
+// The logits of a.rows tokens and a.cols columns as the sums of their splits.
+void logits_out(const Split& k, float* sums, VocabArgs* a) {
+    a->work[0].per = k.per;
+    a->work[0].splits = k.splits;
+    a->out[0] = ProductOut{nullptr, sums, k.pitch, a->rows, a->cols, 0, 1};
+}
+
 // Copies the operands that the tensor maps cannot take as they are.
 cudaError_t pack(const Shape& s, const void* hidden, const TermMatrix& h, const void* weight,
                  const TermMatrix& w, int sms, cudaStream_t stream) {
@@ -320,7 +363,7 @@ credit_status_t credit_linear_ce_workspace(int backward, const void* hidden, con
         return CREDIT_OK;
     }
     if (!backward) {
-        *bytes = (size_t)forward_layout(s, logits_tile(s, s.vocab, d->sms)).bytes;
+        *bytes = (size_t)forward_layout(s, logits_tile(s, s.vocab, d->sms), logits_split(s, s.vocab, d->sms)).bytes;
         return CREDIT_OK;
     }
     Products p;  // (whichever gradients are asked for)
@@ -367,8 +410,9 @@ credit_status_t credit_linear_ce_forward(const void* hidden, const void* weight,
         a.picked = f.picked;
         return from_cuda(launch_vocab_merge(a, l.blocks, loss, lse, q));
     }
-    const VocabTile tile = logits_tile(s, vocab, d->sms);
-    const Layout l = forward_layout(s, tile);
+    const Split split = logits_split(s, vocab, d->sms);
+    const VocabTile tile = split.splits > 1 ? kOne128 : logits_tile(s, vocab, d->sms);
+    const Layout l = forward_layout(s, tile, split);
     if (workspace_bytes < (uint64_t)l.bytes) return CREDIT_ERR_INVALID_ARG;
     unsigned* err = device_error_word();
     if (!err) return CREDIT_ERR_CUDA;
@@ -389,9 +433,16 @@ credit_status_t credit_linear_ce_forward(const void* hidden, const void* weight,
     a.vocab = vocab;
     a.target = target;
     a.ignore = ignore_index;
+    a.err = err;
+    if (split.splits > 1) {
+        float* const sums = reinterpret_cast<float*>(ws + l.logits);
+        logits_out(split, sums, &a);
+        if ((st = from_cuda(launch_vocab(kVocabSums, s.kind, tile, maps, a, d->sms, q))) != CREDIT_OK)
+            return st;
+        return from_cuda(launch_vocab_rows(a, sums, split.splits, split.pitch, s.kind, loss, lse, q));
+    }
     a.parts = reinterpret_cast<float2*>(ws + l.parts);
     a.picked = reinterpret_cast<float*>(ws + l.picked);
-    a.err = err;
     if ((st = from_cuda(launch_vocab(kVocabStats, s.kind, tile, maps, a, d->sms, q))) != CREDIT_OK)
         return st;
     return from_cuda(launch_vocab_merge(a, a.work[0].nt * vocab_tile_parts(tile), loss, lse, q));
@@ -452,7 +503,8 @@ credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse,
     const TermMatrix w = operand(s, weight, vocab, s.pack_w, ws + l.w);
     if ((st = from_cuda(pack(s, hidden, h, weight, w, d->sms, q))) != CREDIT_OK) return st;
 
-    const VocabTile pt = products.tile, gt = logits_tile(s, l.piece, d->sms);
+    const Split split = logits_split(s, l.piece, d->sms);
+    const VocabTile pt = products.tile, gt = split.splits > 1 ? kOne128 : logits_tile(s, l.piece, d->sms);
     // what the logits' gradient is formed from, and what it is multiplied with
     CUtensorMap logits[4] = {}, operands[4] = {};
     for (int p = 0; p < l.pieces; ++p) {
@@ -478,8 +530,16 @@ credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse,
         a.grad_pitch = l.piece;
         a.grad_plane = l.piece * tokens;
         a.err = err;
-        if ((st = from_cuda(launch_vocab(kVocabGrad, s.kind, gt, logits, a, d->sms, q))) != CREDIT_OK)
+        if (split.splits > 1) {
+            float* const sums = reinterpret_cast<float*>(ws + l.logits);
+            logits_out(split, sums, &a);
+            if ((st = from_cuda(launch_vocab(kVocabSums, s.kind, gt, logits, a, d->sms, q))) != CREDIT_OK)
+                return st;
+            st = from_cuda(launch_vocab_rows(a, sums, split.splits, split.pitch, s.kind, nullptr, nullptr, q));
+            if (st != CREDIT_OK) return st;
+        } else if ((st = from_cuda(launch_vocab(kVocabGrad, s.kind, gt, logits, a, d->sms, q))) != CREDIT_OK) {
             return st;
+        }
         const TermMatrix g{ws + l.grad, tokens, pv, l.piece * 2, l.piece * tokens * 2, s.kind};
         a.jobs = 0;
         if (dhidden) {
@@ -521,12 +581,25 @@ credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse,
             o.rows = (int32_t)pv;
             o.cols = (int32_t)hidden_size;
             o.vec = aligned(dweight, 16) && hidden_size * s.es % 16 == 0;
+            if (products.dw.splits > 1) {
+                TileWork& k = a.work[j];
+                k.per = std::min(products.dw.per, k.kb);
+                k.splits = (int32_t)ceil_div(k.kb, k.per);
+                o.sums = reinterpret_cast<float*>(ws + l.dw);
+                o.pitch = products.dw.pitch;
+            }
             if (!term_map(g, kTileK, &operands[2 * j]) || !term_map(h, kTileK, &operands[2 * j + 1]))
                 return CREDIT_ERR_CUDA;
         }
         if ((st = from_cuda(launch_vocab(kVocabProduct, s.kind, pt, operands, a, d->sms, q))) !=
             CREDIT_OK)
             return st;
+        if (dweight && products.dw.splits > 1) {
+            st = from_cuda(launch_vocab_sum(s.dtype, reinterpret_cast<float*>(ws + l.dw), products.dw.splits, pv,
+                                            hidden_size, products.dw.pitch,
+                                            static_cast<char*>(dweight) + v0 * hidden_size * s.es, d->sms, q));
+            if (st != CREDIT_OK) return st;
+        }
     }
     if (dhidden && l.add)  // (a split's terms lie one behind the other, as splits do)
         return from_cuda(launch_vocab_sum(s.dtype, reinterpret_cast<float*>(ws + l.sums),

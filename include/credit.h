@@ -389,7 +389,8 @@ credit_status_t credit_norm_backward(credit_op_t op, const void *dy, const void 
  * formed a tile at a time by the tensor cores and reduced there: the forward
  * pass keeps a maximum and a sum per token and 64 columns (8 bytes), the backward pass the gradient of one piece of the vocabulary at
  * a time, 256 MiB of it (bf16 operands: rounded to bf16 for the two products,
- * to two bf16 terms up to 32 tokens).  fp32 operands are taken apart into three
+ * to two bf16 terms up to 32 tokens); only products of few tiles and a long k
+ * leave theirs, 10 MB at most, in the workspace.  fp32 operands are taken apart into three
  * bf16 terms each and multiplied in six products, which keeps 24 bits; a value
  * that is infinite there may give NaN where the formula gives infinity.  Sums
  * are fp32, every output is rounded once, and results repeat bit for bit.

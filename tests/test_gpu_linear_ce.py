@@ -90,7 +90,8 @@ def ref_backward(dloss, dlse, h, w, target, lse, ignore=IGNORE):
 SHAPES = [(1, 8, 1), (1, 64, 2), (2, 1, 3), (3, 7, 255), (31, 64, 256), (33, 100, 257), (128, 65, 1000),
           (129, 512, 513), (300, 1001, 5003), (64, 1024, 4096), (1, 4096, 20000), (1000, 16, 40),
           (257, 192, 1), (5, 2056, 777), (8, 264, 1000), (9, 264, 1000), (4, 1001, 3001), (8, 4096, 600),
-          (6, 33, 130), (1, 20000, 37), (1, 30000, 40)]
+          (6, 33, 130), (1, 20000, 37), (1, 30000, 40), (38, 4864, 246), (124, 2415, 128),
+          (3000, 40, 100), (40, 8192, 1), (2100, 136, 300)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -131,7 +132,7 @@ def whole_numbers(shape, top, dtype, seed):
 # (8192 tokens: the vocabulary in two pieces; few tokens: parts of a sum over it)
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("tokens,hidden,vocab", [(1, 8, 5), (7, 72, 300), (4, 1001, 2000), (11, 72, 300), (130, 264, 700), (300, 1001, 1000),
-                                                 (200, 24, 20011), (8192, 40, 20000), (4099, 72, 33333)])
+                                                 (200, 24, 20011), (5000, 72, 130), (130, 3000, 200), (20, 5000, 333), (8192, 40, 20000), (4099, 72, 33333)])
 def test_gradients_of_whole_numbers_are_exact(tokens, hidden, vocab, dtype):
     # with w = 0 (or h = 0) every logit is 0, and with lse = 0 every p is 1:
     # g = dloss (1 - [target]) + dlse, whole numbers
@@ -176,9 +177,10 @@ def test_what_a_forward_pass_leaves_makes_a_gradient_without_a_sum(tokens, hidde
     assert float(dh[:, 0].abs().max()) <= 2 * 2.0 ** -8 + 1e-4
 
 
-def test_targets_at_every_place_of_a_tile_and_outside():
+@pytest.mark.parametrize("hidden", [72, 4104])
+def test_targets_at_every_place_of_a_tile_and_outside(hidden):
     vocab, tokens = 600, 600
-    h, w, _ = make(tokens, 72, vocab, torch.bfloat16, seed=9)
+    h, w, _ = make(tokens, hidden, vocab, torch.bfloat16, seed=9)
     target = torch.arange(tokens, device="cuda")
     loss, _ = credit.linear_cross_entropy_forward(h, w, target)
     want, _, bound, _ = ref_forward(h, w, target)
@@ -216,9 +218,9 @@ def test_every_target_ignored(tokens, hidden):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("tokens", [5, 40])
-def test_one_token_that_is_not_finite_leaves_the_others(dtype, tokens):
-    h, w, target = make(tokens, 64, 500, DT[dtype], seed=4, ignored=0.0)
+@pytest.mark.parametrize("tokens,hidden", [(5, 64), (40, 64), (40, 4096)])
+def test_one_token_that_is_not_finite_leaves_the_others(dtype, tokens, hidden):
+    h, w, target = make(tokens, hidden, 500, DT[dtype], seed=4, ignored=0.0)
     loss, lse = credit.linear_cross_entropy_forward(h, w, target)
     for value in (float("nan"), float("inf")):
         hb = h.clone()
