@@ -93,10 +93,12 @@ struct FewArgs {
     const void* h;
     const void* w;
     int32_t tokens, cols, pitch;   // pitch: floats of a token in shared memory
+    int32_t shaped;                // the kernel is that of so many tokens
     int64_t vocab;
     const int64_t* target;
     int64_t ignore;
-    float2* parts;                 // per (block, token)
+    float2* parts;                 // per (block, token), blocks parts_pitch apart
+    int64_t parts_pitch;
     float* picked;
     // the logits' gradient, vocab x few_tokens(tokens), written and then read; null:
     // the statistics are wanted

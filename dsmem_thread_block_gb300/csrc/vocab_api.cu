@@ -47,16 +47,23 @@ struct Shape {
 // Floats of a token in the shared memory of the form for a few tokens: whole steps
 // of a warp.
 int64_t few_pitch(int64_t hidden) { return round_up(hidden, 256); }
-// Shared memory it takes at most, two CTAs to an SM.
-constexpr int64_t kFewRoom = 100 << 10;
+// Columns that it takes at most: two CTAs to an SM, of eight tokens one of twice the
+// threads.
+constexpr int64_t few_columns(int tokens) { return (tokens == 8 ? 200 << 10 : 100 << 10) / (4 * tokens); }
+// fp32 tokens and elements of the weight of a forward pass that takes it eight tokens at
+// a time: up to 16 read the weight twice, where the tiles read it, write its three bf16
+// terms and read those (16 tokens of 32768 x 4096: 235 and 387 us, of 16384 x 1024 46 and
+// 52, 12 of 131072 x 256 77 and 110; of 4096 x 1024 24 and 22, of 10000 x 256 23 and 16;
+// 24 of 32768 x 4096 361 and 384, of 10000 x 6000 254 and 205, of 8192 x 4096 110 and 102).
+constexpr int64_t kFewForward = 16, kFewForwardWeight = 1 << 24;
 
-credit_status_t shape_of(const void* h, const void* w, int64_t tokens, int64_t hidden, int64_t vocab,
-                         credit_dtype_t dtype, Shape* s) {
+credit_status_t shape_of(bool backward, const void* h, const void* w, int64_t tokens, int64_t hidden,
+                         int64_t vocab, credit_dtype_t dtype, Shape* s) {
     if (tokens < 0 || hidden < 1 || vocab < 1) return CREDIT_ERR_INVALID_ARG;
     if (dtype != CREDIT_F32 && dtype != CREDIT_BF16) return CREDIT_ERR_UNSUPPORTED;
     // rows and columns are counted in 32 bits, tiles of 128 past them too
-    const int64_t most = ((int64_t)1 << 31) - 1024;
-    if (tokens > most || vocab > most || hidden > ((int64_t)1 << 24)) return CREDIT_ERR_INVALID_ARG;
+    const int64_t limit = ((int64_t)1 << 31) - 1024;
+    if (tokens > limit || vocab > limit || hidden > ((int64_t)1 << 24)) return CREDIT_ERR_INVALID_ARG;
     // (tiles of a launch, too)
     const int64_t tiles = ceil_div(tokens, kTileM) * ceil_div(vocab, kTileM);
     const int64_t wide = ceil_div(std::max(tokens, vocab), kTileM) * ceil_div(hidden, kTileM);
@@ -74,10 +81,12 @@ credit_status_t shape_of(const void* h, const void* w, int64_t tokens, int64_t h
     s->pack_w = s->terms > 1 || !lines || !aligned(w, 16);
     // One token is bound by reading the weight (131072 x 4096 bf16: 162 us in the form
     // for a few, 175 in tiles).  More take it where the tiles would copy the weight
-    // first (4 tokens of 50000 x 1001 bf16: 47 and 73 us; 8 of 131072 x 2048 fp32: 265
+    // first (4 tokens of 50000 x 1001 bf16: 47 and 73 us; 8 of 131072 x 2048 fp32: 212
     // and 900; 8 of bf16 223 and 99).
-    s->few = tokens <= kFewTokens && (tokens <= 1 || s->pack_w) &&
-             few_tokens((int)tokens) * few_pitch(hidden) * 4 <= kFewRoom;
+    const int64_t most =
+        !backward && dtype == CREDIT_F32 && vocab * hidden >= kFewForwardWeight ? kFewForward : kFewTokens;
+    s->few = tokens <= most && (tokens <= 1 || s->pack_w) &&
+             few_pitch(hidden) <= few_columns(few_tokens((int)std::min<int64_t>(tokens, kFewTokens)));
     return CREDIT_OK;
 }
 
@@ -246,14 +255,15 @@ struct FewLayout {
 FewLayout few_layout(const Shape& s, bool backward, bool dh, bool vec, int sms) {
     FewLayout l;
     Layout place{};
-    l.blocks = few_blocks((int)s.tokens, (int)few_pitch(s.hidden), s.vocab, sms);
+    const int shaped = (int)std::min<int64_t>(s.tokens, kFewTokens);
+    l.blocks = few_blocks(shaped, (int)few_pitch(s.hidden), s.vocab, sms);
     l.slices = few_slices(s.hidden, s.dtype, vec, s.vocab, sms);
     l.sums_pitch = round_up(s.hidden, 4);
     if (!backward) {
         place.place(&l.parts, l.blocks * s.tokens * 8);
         place.place(&l.picked, s.tokens * 4);
     } else {
-        place.place(&l.grad, s.vocab * few_tokens((int)s.tokens) * 4);
+        place.place(&l.grad, s.vocab * few_tokens(shaped) * 4);
         if (dh) place.place(&l.sums, l.slices * s.tokens * l.sums_pitch * 4);
     }
     l.bytes = place.bytes;
@@ -263,7 +273,7 @@ FewArgs few_args(const Shape& s, const void* h, const void* w, const int64_t* ta
     FewArgs a{};
     a.h = h;
     a.w = w;
-    a.tokens = (int32_t)s.tokens;
+    a.tokens = a.shaped = (int32_t)s.tokens;
     a.cols = (int32_t)s.hidden;
     a.pitch = (int32_t)few_pitch(s.hidden);
     a.vocab = s.vocab;
@@ -351,7 +361,7 @@ credit_status_t credit_linear_ce_workspace(int backward, const void* hidden, con
                                            credit_dtype_t dtype, int device, size_t* bytes) {
     if (!bytes) return CREDIT_ERR_INVALID_ARG;
     Shape s;
-    const credit_status_t st = shape_of(hidden, weight, tokens, hidden_size, vocab, dtype, &s);
+    const credit_status_t st = shape_of(backward, hidden, weight, tokens, hidden_size, vocab, dtype, &s);
     if (st != CREDIT_OK) return st;
     *bytes = 0;
     if (tokens == 0) return CREDIT_OK;
@@ -378,7 +388,7 @@ credit_status_t credit_linear_ce_forward(const void* hidden, const void* weight,
                                          int64_t vocab, credit_dtype_t dtype, void* workspace,
                                          size_t workspace_bytes, void* stream) {
     Shape s;
-    credit_status_t st = shape_of(hidden, weight, tokens, hidden_size, vocab, dtype, &s);
+    credit_status_t st = shape_of(false, hidden, weight, tokens, hidden_size, vocab, dtype, &s);
     if (st != CREDIT_OK) return st;
     if (tokens == 0) return CREDIT_OK;
     if (!hidden || !weight || !target || !loss || !lse) return CREDIT_ERR_INVALID_ARG;
@@ -399,8 +409,22 @@ credit_status_t credit_linear_ce_forward(const void* hidden, const void* weight,
         cudaStream_t q = (cudaStream_t)stream;
         FewArgs f = few_args(s, hidden, weight, target, ignore_index);
         f.parts = reinterpret_cast<float2*>(static_cast<char*>(workspace) + l.parts);
+        f.parts_pitch = tokens;
         f.picked = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.picked);
-        if ((st = from_cuda(launch_few_logits(s.dtype, vec, f, l.blocks, q))) != CREDIT_OK) return st;
+        float2* const parts = f.parts;
+        float* const picked = f.picked;
+        // (as many at a time as the first, so that each leaves as many parts)
+        for (int64_t t = 0; t < tokens; t += kFewTokens) {
+            f.h = static_cast<const char*>(hidden) + t * hidden_size * s.es;
+            f.tokens = (int32_t)std::min<int64_t>(kFewTokens, tokens - t);
+            f.shaped = (int32_t)std::min<int64_t>(kFewTokens, tokens);
+            f.target = target + t;
+            f.parts = parts + t;
+            f.picked = picked + t;
+            if ((st = from_cuda(launch_few_logits(s.dtype, vec, f, l.blocks, q))) != CREDIT_OK) return st;
+        }
+        f.parts = parts;
+        f.picked = picked;
         VocabArgs a{};
         a.rows = (int32_t)tokens;
         a.vocab = vocab;
@@ -455,7 +479,7 @@ credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse,
                                           int64_t vocab, credit_dtype_t dtype, void* workspace,
                                           size_t workspace_bytes, void* stream) {
     Shape s;
-    credit_status_t st = shape_of(hidden, weight, tokens, hidden_size, vocab, dtype, &s);
+    credit_status_t st = shape_of(true, hidden, weight, tokens, hidden_size, vocab, dtype, &s);
     if (st != CREDIT_OK) return st;
     cudaStream_t q = (cudaStream_t)stream;
     const uint64_t hb = (uint64_t)(tokens * hidden_size) * s.es, wb = (uint64_t)(vocab * hidden_size) * s.es;
@@ -603,7 +627,8 @@ credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse,
     }
     if (dhidden && l.add)  // (a split's terms lie one behind the other, as splits do)
         return from_cuda(launch_vocab_sum(s.dtype, reinterpret_cast<float*>(ws + l.sums),
-                                          products.splits * (s.kind == kTerms2 ? 2 : 1), tokens, hidden_size, l.sums_pitch, dhidden, d->sms, q));
+                                          products.splits * (s.kind == kTerms2 ? 2 : 1), tokens,
+                                          hidden_size, l.sums_pitch, dhidden, d->sms, q));
     return CREDIT_OK;
 }
 

@@ -10,10 +10,13 @@
 //                 on the way
 //
 // Measured (device time): one token of 131072 x 4096 forward 163 us bf16 (0.97 of the
-// copy rate), 302 fp32; backward 547 bf16 (0.87 of it for the three passes over the
+// copy rate), 301 fp32; backward 519 bf16 (0.91 of it for the three passes over the
 // weight's size).  Bound by HBM for one token; by the shared-memory reads of the tokens
-// for eight (131072 x 2048 bf16 225 us, fp32 264), so aligned bf16 takes tiles from two
-// tokens on.  A lane has 16 vectors in flight for one token (four took 220 us).
+// for eight (131072 x 2048 fp32 212 us, x 2047 bf16 216), so aligned bf16 takes tiles
+// from two tokens on.  A lane has 16 vectors in flight for one token (four took 220 us);
+// of eight tokens the next step's loads are issued before a step is used, by sixteen
+// warps that share one copy of the tokens (263 and 260 us without, in CTAs of eight
+// warps); four tokens lose by the same (97 to 115 us at 32768 x 4096 fp32).
 #include <algorithm>
 
 #include "early_launch.h"
@@ -27,7 +30,8 @@ namespace credit {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+// few_logits: sixteen warps an SM, in one CTA where eight tokens fill its shared memory
+constexpr int few_threads(int tokens) { return tokens == 8 ? 512 : 256; }
 constexpr int kRows = 4;         // vocabulary rows of a warp
 constexpr int kGrads = 1024;     // gradients of logits that few_products stages at a time
 
@@ -67,9 +71,9 @@ template <typename T, bool VEC> struct FewIO {
 };
 
 template <typename T, bool VEC, int TOKENS>
-__global__ void __launch_bounds__(kThreads) few_logits(FewArgs a) {
+__global__ void __launch_bounds__(few_threads(TOKENS)) few_logits(FewArgs a) {
     using IO = FewIO<T, VEC>;
-    constexpr int N = IO::N, kSums = kRows * TOKENS;
+    constexpr int N = IO::N, kSums = kRows * TOKENS, kThreads = few_threads(TOKENS), kWarps = kThreads / 32;
     extern __shared__ __align__(16) float hidden[];     // TOKENS x pitch
     __shared__ float2 parts[kWarps][TOKENS];
     dependents_may_launch();
@@ -104,21 +108,33 @@ __global__ void __launch_bounds__(kThreads) few_logits(FewArgs a) {
         for (int k = 0; k < kRows; ++k)
 #pragma unroll
             for (int j = 0; j < TOKENS; ++j) sum[k][j] = f2(0.f);
-        // kUnroll steps' loads at once
+        // kUnroll steps' loads at once, of eight tokens the next step's before these
+        // are used
         constexpr int kUnroll = TOKENS == 1 ? 4 : TOKENS == 4 ? 2 : 1;
-        for (int c0 = IO::first(lane); c0 < a.cols; c0 += kUnroll * IO::kStep) {
-            typename IO::Raw raw[kUnroll][kRows];
+        constexpr bool kAhead = TOKENS == 8;
+        typename IO::Raw raw[kUnroll][kRows];
+        auto fetch = [&](int c0) {
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
                 for (int k = 0; k < kRows; ++k) raw[u][k] = IO::load(row[k], c0 + u * IO::kStep, a.cols);
+        };
+        if (kAhead) fetch(IO::first(lane));
+        for (int c0 = IO::first(lane); c0 < a.cols; c0 += kUnroll * IO::kStep) {
+            if (!kAhead) fetch(c0);
+            typename IO::Raw now[kUnroll][kRows];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+                for (int k = 0; k < kRows; ++k) now[u][k] = raw[u][k];
+            if (kAhead) fetch(c0 + kUnroll * IO::kStep);
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
                 const int c = c0 + u * IO::kStep;
                 if (u > 0 && c >= a.cols) break;
                 float x[kRows][N];
 #pragma unroll
-                for (int k = 0; k < kRows; ++k) IO::unpack(raw[u][k], x[k]);
+                for (int k = 0; k < kRows; ++k) IO::unpack(now[u][k], x[k]);
 #pragma unroll
                 for (int j = 0; j < TOKENS; ++j) {
                     const float* const h = hidden + j * pitch + c;
@@ -179,7 +195,7 @@ __global__ void __launch_bounds__(kThreads) few_logits(FewArgs a) {
     __syncthreads();
     if (warp || !writes || r) return;
     for (int w = 1; w < kWarps; ++w) merge(parts[w][t].x, parts[w][t].y);
-    a.parts[(int64_t)blockIdx.x * a.tokens + t] = make_float2(m, s);
+    a.parts[(int64_t)blockIdx.x * a.parts_pitch + t] = make_float2(m, s);
 }
 
 // Grid: x the column blocks, y the slices of the vocabulary.
@@ -276,14 +292,17 @@ template <typename F> cudaError_t with_constants(int dtype, bool vec, int tokens
     return vec ? typed(bf16(), std::true_type()) : typed(bf16(), std::false_type());
 }
 
-int room_of(const FewArgs& a) { return few_tokens(a.tokens) * a.pitch * 4; }
+int room_of(const FewArgs& a) { return few_tokens(a.shaped) * a.pitch * 4; }
 
 }  // namespace
 
 int few_blocks(int tokens, int pitch, int64_t vocab, int sms) {
     const int room = few_tokens(tokens) * pitch * 4;
+    const int warps = few_threads(few_tokens(tokens)) / 32;
     const int64_t groups = (vocab + kRows - 1) / kRows;
-    return (int)std::min<int64_t>((groups + kWarps - 1) / kWarps, (int64_t)sms * std::max(1, std::min(4, 200000 / (room + 1024))));
+    // CTAs of an SM, as shared memory and registers allow
+    const int most = std::max(1, std::min(32 / warps, 220000 / (room + 5120)));
+    return (int)std::min<int64_t>((groups + warps - 1) / warps, (int64_t)sms * most);
 }
 
 int few_slices(int64_t cols, int dtype, bool vec, int64_t vocab, int sms) {
@@ -293,7 +312,7 @@ int few_slices(int64_t cols, int dtype, bool vec, int64_t vocab, int sms) {
 }
 
 cudaError_t launch_few_logits(int dtype, bool vec, const FewArgs& a, int blocks, cudaStream_t s) {
-    return with_constants(dtype, vec, a.tokens, [&](auto type, auto v, auto tokens) -> cudaError_t {
+    return with_constants(dtype, vec, a.shaped, [&](auto type, auto v, auto tokens) -> cudaError_t {
         auto* fn = &few_logits<decltype(type), decltype(v)::value, decltype(tokens)::value>;
         int dev;
         cudaError_t e = cudaGetDevice(&dev);
@@ -302,7 +321,7 @@ cudaError_t launch_few_logits(int dtype, bool vec, const FewArgs& a, int blocks,
         cudaLaunchAttribute attr = early_launch();
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3((unsigned)blocks);
-        cfg.blockDim = dim3(kThreads);
+        cfg.blockDim = dim3((unsigned)few_threads(few_tokens(a.shaped)));
         cfg.dynamicSmemBytes = (size_t)room_of(a);
         cfg.stream = s;
         cfg.attrs = &attr;
@@ -312,7 +331,7 @@ cudaError_t launch_few_logits(int dtype, bool vec, const FewArgs& a, int blocks,
 }
 
 cudaError_t launch_few_products(int dtype, bool vec, const FewArgs& a, int slices, cudaStream_t s) {
-    return with_constants(dtype, vec, a.tokens, [&](auto type, auto v, auto tokens) -> cudaError_t {
+    return with_constants(dtype, vec, a.shaped, [&](auto type, auto v, auto tokens) -> cudaError_t {
         using IO = FewIO<decltype(type), decltype(v)::value>;
         const dim3 grid((unsigned)((a.cols + kThreads * IO::N - 1) / (kThreads * IO::N)), (unsigned)slices);
         return launch_early(few_products<decltype(type), decltype(v)::value, decltype(tokens)::value>, grid,

@@ -387,23 +387,24 @@ credit_status_t credit_norm_backward(credit_op_t op, const void *dy, const void 
  * tokens x hidden_size, weight vocab x hidden_size, both of `dtype` and
  * contiguous; tokens == 0 is a legal empty batch.  The tokens x vocab logits are
  * formed a tile at a time by the tensor cores and reduced there: the forward
- * pass keeps a maximum and a sum per token and 64 columns (8 bytes), the backward pass the gradient of one piece of the vocabulary at
- * a time, 256 MiB of it (bf16 operands: rounded to bf16 for the two products,
- * to two bf16 terms up to 32 tokens); only products of few tiles and a long k
- * leave theirs, 10 MB at most, in the workspace.  fp32 operands are taken apart into three
- * bf16 terms each and multiplied in six products, which keeps 24 bits; a value
- * that is infinite there may give NaN where the formula gives infinity.  Sums
- * are fp32, every output is rounded once, and results repeat bit for bit.
+ * pass keeps a maximum and a sum per token and 64 columns (8 bytes), the
+ * backward pass the gradient of one piece of the vocabulary at a time, 256 MiB
+ * of it (bf16 operands: rounded to bf16 for the two products, to two bf16 terms
+ * up to 32 tokens); only products of few tiles and a long k leave theirs, 10 MB
+ * at most, in the workspace.  fp32 operands are taken apart into three bf16
+ * terms each and multiplied in six products, which keeps 24 bits; a value that
+ * is infinite there may give NaN where the formula gives infinity.  Sums are
+ * fp32, every output is rounded once, and results repeat bit for bit.
  *
  * Operands whose rows are not whole 16-byte lines at 16-byte addresses, and fp32
  * ones, are copied into the workspace first (fp32: 6 bytes an element).  One
- * token, and up to eight where that copy would be made, take a form without
- * tensor cores that reads the weight as it is; up to 100 KiB of fp32 tokens.
+ * token, and up to eight where that copy would be made (forward, of fp32 with a
+ * weight of 2^24 elements, up to 16), take a form without tensor cores that reads
+ * the weight as it is: of one token up to 25600 columns, of more up to 6400.
  * dweight of a token counts its hidden states even where its gradient is 0: they
- * must be finite.  A target outside [0, vocab) that
- * is not ignore_index gives its token a NaN loss and gradient.  Each call works
- * entirely on `stream` and may be captured; a workspace is used by one call at a
- * time.
+ * must be finite.  A target outside [0, vocab) that is not ignore_index gives its
+ * token a NaN loss and gradient.  Each call works entirely on `stream` and may be
+ * captured; a workspace is used by one call at a time.
  */
 
 /*

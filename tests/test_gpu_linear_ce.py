@@ -91,7 +91,8 @@ SHAPES = [(1, 8, 1), (1, 64, 2), (2, 1, 3), (3, 7, 255), (31, 64, 256), (33, 100
           (129, 512, 513), (300, 1001, 5003), (64, 1024, 4096), (1, 4096, 20000), (1000, 16, 40),
           (257, 192, 1), (5, 2056, 777), (8, 264, 1000), (9, 264, 1000), (4, 1001, 3001), (8, 4096, 600),
           (6, 33, 130), (1, 20000, 37), (1, 30000, 40), (38, 4864, 246), (124, 2415, 128),
-          (3000, 40, 100), (40, 8192, 1), (2100, 136, 300)]
+          (3000, 40, 100), (40, 8192, 1), (2100, 136, 300), (9, 256, 65536), (13, 1001, 17000),
+          (16, 264, 63551), (17, 260, 65003), (16, 256, 65535), (8, 6400, 300), (8, 6401, 300)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
