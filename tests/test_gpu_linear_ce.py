@@ -407,6 +407,45 @@ def test_results_repeat_bit_for_bit_on_any_stream(tokens, hidden):
         assert all(torch.equal(a, b) for a, b in zip(first, r))
 
 
+@pytest.mark.parametrize("hidden", [264, 263])
+@pytest.mark.parametrize("tokens", [9, 13, 16])
+def test_fp32_tokens_eight_at_a_time(tokens, hidden):
+    """A weight that takes that form: targets outside, ignored and at the ends in each
+    eight, a token that is not finite, streams side by side and a graph."""
+    vocab = 64007  # (x 263: 2^24 and some)
+    h, w, target = make(tokens, hidden, vocab, torch.float32, seed=15, ignored=0.0)
+    target[1], target[2], target[3], target[8] = IGNORE, vocab - 1, 0, vocab - 1
+    want, want_lse, bound, bound_lse = ref_forward(h, w, target)
+    loss, lse = credit.linear_cross_entropy_forward(h, w, target)
+    assert_close(lse, want_lse, bound_lse, "lse")
+    assert_close(loss, want, bound, "loss")
+    rest = torch.ones(tokens, dtype=torch.bool, device="cuda")
+    rest[[0, tokens - 1]] = False
+    bad, hb = target.clone(), h.clone()
+    bad[0], bad[tokens - 1] = vocab, -1
+    hb[0, 7] = float("inf")
+    lb, sb = credit.linear_cross_entropy_forward(hb, w, bad)
+    assert torch.equal(lb[rest], loss[rest]) and torch.equal(sb[rest], lse[rest])
+    assert bool(torch.isnan(lb[~rest]).all()) and torch.equal(sb[-1], lse[-1])
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    results = []
+    for s in streams:
+        with torch.cuda.stream(s):
+            results.append(credit.linear_cross_entropy_forward(h, w, target))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, loss) and torch.equal(b, lse) for a, b in results)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cl, cs = credit.linear_cross_entropy_forward(h, w, target)
+    h.copy_(h.roll(1, 0))
+    target.copy_(target.roll(1, 0))
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(cl, loss.roll(1, 0)) and torch.equal(cs, lse.roll(1, 0))
+
+
 @pytest.mark.parametrize("tokens", [1, 2, 200])
 def test_captured_calls_take_new_inputs(tokens):
     h, w, target = make(tokens, 128, 2100, torch.bfloat16, seed=13)
