@@ -535,7 +535,7 @@ credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse,
         const int64_t v0 = p * l.piece, pv = std::min(l.piece, vocab - v0);
         VocabArgs a{};
         a.jobs = 1;
-            a.work[0] = work_of(gt, tokens, pv, hidden_size, false, false);
+        a.work[0] = work_of(gt, tokens, pv, hidden_size, false, false);
         a.work[0].b_y0 = (int32_t)v0;
         const int box = box_rows(gt, tokens, &a.work[0]);
         if (p == 0 && (!term_map(h, box, &logits[0]) ||
