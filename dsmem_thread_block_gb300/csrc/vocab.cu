@@ -11,6 +11,7 @@
 //   vocab_rows   from logits that were summed in parts of k, where they have few tiles,
 //                the statistics or the gradient
 //   vocab_sum    parts of dhidden, or of dweight, in order: 4096 x 4096 20 us
+//   vocab_unit   what a logits' gradient of one bf16 term is divided by: some 2 us of a call
 // All kernels of a call are launched early (early_launch.h), which saves some 3 us of
 // a small call (32 x 1024 x 4096 forward 13.4 us called without, 9.6 with).
 #include "early_launch.h"
@@ -95,6 +96,11 @@ vocab_rows(VocabArgs a, const float* sums, int splits, int64_t pitch, float* los
         scale = ignored ? 0.f : outside ? NAN : a.dloss[row];
         both = scale + (a.dlse ? a.dlse[row] : 0.f);
         known = a.lse[row];
+        if (TERMS == 1) {
+            const float unit = *a.unit;
+            scale /= unit;
+            both /= unit;
+        }
     }
     float m = -INFINITY, s = 0.f;
     for (int c = 4 * (int)threadIdx.x; c < a.cols; c += 4 * kRowThreads) {
@@ -156,6 +162,33 @@ vocab_rows(VocabArgs a, const float* sums, int splits, int64_t pitch, float* los
         lse[row] = l;
         loss[row] = ignored ? 0.f : outside ? NAN : l - picked;
     }
+}
+
+// The logits' gradient is divided by this number before it is rounded to one bf16 term,
+// and what its products give is multiplied by it: the significand, 1 to 2, of the
+// largest dloss.  That one becomes a power of two: the dloss of a mean, the same for
+// every token, is not rounded at all (g = -dloss of an unlikely target: before, one
+// relative error for all tokens, up to 2^-8 and 1.8e-3 of the gradient for 777 tokens),
+// and others that are a little smaller lie where a rounding is least of a number.
+__global__ void __launch_bounds__(1024)
+vocab_unit(const float* dloss, const int64_t* target, int64_t ignore, int64_t tokens, float* unit) {
+    __shared__ float tops[32];
+    dependents_may_launch();
+    wait_for_launches();
+    float top = 0.f;
+#pragma unroll 4
+    for (int64_t t = threadIdx.x; t < tokens; t += 1024) {
+        const float d = fabsf(dloss[t]);
+        // (an infinite or subnormal one has no significand; a NaN is never larger)
+        if (target[t] != ignore && d <= 3.402823466e38f && d >= 1.175494351e-38f) top = fmaxf(top, d);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+    __syncthreads();
+    if (threadIdx.x) return;
+    for (int w = 1; w < 32; ++w) top = fmaxf(top, tops[w]);
+    *unit = top == 0.f ? 1.f : __uint_as_float((__float_as_uint(top) & 0x007FFFFFu) | 0x3F800000u);
 }
 
 // The 16 bytes at `p`, at any even address, from the two lines that hold them.
@@ -251,13 +284,15 @@ __global__ void __launch_bounds__(256) vocab_pack(PackArgs a) {
 // in order.
 template <typename T, int G>
 __global__ void __launch_bounds__(256)
-vocab_sum(const float* sums, int splits, int64_t rows, int cols, int64_t pitch, T* out, bool vec) {
+vocab_sum(const float* sums, int splits, int64_t rows, int cols, int64_t pitch, const float* unit, T* out,
+          bool vec) {
     constexpr int kColumns = 256 / G;
     __shared__ float4 parts[G > 1 ? G : 1][G > 1 ? kColumns : 1];
     dependents_may_launch();
     wait_for_launches();
     const int vecs = (cols + 3) / 4, lane = (int)threadIdx.x % kColumns, group = (int)threadIdx.x / kColumns;
     const int64_t plane = rows * pitch, n = rows * vecs;
+    const float by = unit ? *unit : 1.f;
     for (int64_t i0 = (int64_t)blockIdx.x * kColumns; i0 < n; i0 += (int64_t)gridDim.x * kColumns) {
         const int64_t i = i0 + lane, r = i / vecs;
         const int v = (int)(i - r * vecs);
@@ -282,9 +317,9 @@ vocab_sum(const float* sums, int splits, int64_t rows, int cols, int64_t pitch, 
         }
         if (i >= n) continue;
         T* const q = out + r * cols + 4 * v;
-        const float x[4] = {f.x, f.y, f.z, f.w};
+        const float x[4] = {by * f.x, by * f.y, by * f.z, by * f.w};
         if (vec) {
-            if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(q) = f;
+            if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(q) = make_float4(x[0], x[1], x[2], x[3]);
             else *reinterpret_cast<uint2*>(q) = make_uint2(Elem<bf16>::pack2(x[0], x[1]),
                                                            Elem<bf16>::pack2(x[2], x[3]));
         } else {
@@ -423,6 +458,11 @@ cudaError_t launch_vocab_rows(const VocabArgs& a, const float* sums, int splits,
     return launch_early(fn, dim3((unsigned)a.rows), kRowThreads, s, a, sums, splits, pitch, loss, lse);
 }
 
+cudaError_t launch_vocab_unit(const float* dloss, const int64_t* target, int64_t ignore, int64_t tokens,
+                              float* unit, cudaStream_t s) {
+    return launch_early(vocab_unit, dim3(1), 1024, s, dloss, target, ignore, tokens, unit);
+}
+
 cudaError_t launch_vocab_pack(int dtype, const void* const (&src)[2], const TermMatrix (&dst)[2], int n,
                               int sms, cudaStream_t s) {
     PackArgs a{};
@@ -442,12 +482,12 @@ cudaError_t launch_vocab_pack(int dtype, const void* const (&src)[2], const Term
 }
 
 cudaError_t launch_vocab_sum(int dtype, const float* sums, int splits, int64_t rows, int64_t cols,
-                             int64_t pitch, void* out, int sms, cudaStream_t s) {
+                             int64_t pitch, const float* unit, void* out, int sms, cudaStream_t s) {
     const int64_t n = rows * ((cols + 3) / 4);
     const bool vec = (uintptr_t)out % 16 == 0 && cols % 4 == 0, shared = splits >= 16;
     const dim3 grid((unsigned)blocks_for(shared ? 16 * n : n, sms));
     auto run = [&](auto* fn, auto* o) {
-        return launch_early(fn, grid, 256, s, sums, splits, rows, (int)cols, pitch, o, vec);
+        return launch_early(fn, grid, 256, s, sums, splits, rows, (int)cols, pitch, unit, o, vec);
     };
     if (dtype == 0)
         return run(shared ? vocab_sum<float, 16> : vocab_sum<float, 1>, static_cast<float*>(out));

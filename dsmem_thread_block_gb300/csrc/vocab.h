@@ -52,6 +52,7 @@ struct ProductOut {
     int32_t rows, cols;
     int32_t add;           // to what the sums hold
     int32_t vec;           // rows of `out` are whole 16-byte lines
+    const float* unit;     // what the logits' gradient was divided by (null: 1; not for sums)
 };
 
 struct VocabArgs {
@@ -74,6 +75,7 @@ struct VocabArgs {
     const float* dlse;     // or null
     void* grad;            // terms planes, tokens x grad_pitch
     int64_t grad_pitch, grad_plane;  // elements
+    const float* unit;     // of one term: what it is divided by (vocab_unit)
     ProductOut out[2];
     unsigned* err;
     int32_t alone;         // a self-test: nothing brings B, every wait runs out
@@ -141,8 +143,11 @@ cudaError_t launch_vocab_rows(const VocabArgs& a, const float* sums, int splits,
 // n matrices of the call's type and of one width as bf16 terms
 cudaError_t launch_vocab_pack(int dtype, const void* const (&src)[2], const TermMatrix (&dst)[2], int n,
                               int sms, cudaStream_t s);
-// out = the splits' sums added in order
+// out = the splits' sums added in order, times *unit (null: 1)
 cudaError_t launch_vocab_sum(int dtype, const float* sums, int splits, int64_t rows, int64_t cols,
-                             int64_t pitch, void* out, int sms, cudaStream_t s);
+                             int64_t pitch, const float* unit, void* out, int sms, cudaStream_t s);
+// What a logits' gradient of one term is divided by.
+cudaError_t launch_vocab_unit(const float* dloss, const int64_t* target, int64_t ignore, int64_t tokens,
+                              float* unit, cudaStream_t s);
 
 }  // namespace credit

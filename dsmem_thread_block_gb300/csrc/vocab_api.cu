@@ -101,7 +101,7 @@ int64_t operand_bytes(const Shape& s, int64_t rows, bool pack) {
 
 // The workspace of a call, in the order of its parts.
 struct Layout {
-    int64_t h, w, parts, picked, logits, grad, sums, dw, bytes;  // offsets
+    int64_t h, w, parts, picked, unit, logits, grad, sums, dw, bytes;  // offsets
     int64_t piece;      // vocabulary rows at a time
     int32_t pieces;
     int64_t sums_pitch;
@@ -231,6 +231,7 @@ Layout backward_layout(const Shape& s, bool dh, bool dw, int sms, Products* prod
     l.piece = round_up(ceil_div(s.vocab, l.pieces), kTileN);
     l.pieces = (int32_t)ceil_div(s.vocab, l.piece);
     l.place(&l.grad, s.tokens * l.piece * 2 * s.kind);
+    if (s.kind == kTerms1) l.place(&l.unit, 4);
     *products = products_for(s, std::min(l.piece, s.vocab), dh, dw, sms);
     const Split k = logits_split(s, l.piece, sms);
     if (k.splits > 1) l.place(&l.logits, k.splits * s.tokens * k.pitch * 4);
@@ -513,7 +514,7 @@ credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse,
         if ((st = from_cuda(launch_few_logits(s.dtype, lines, f, l.blocks, q))) != CREDIT_OK) return st;
         if ((st = from_cuda(launch_few_products(s.dtype, vec, f, l.slices, q))) != CREDIT_OK) return st;
         return dhidden ? from_cuda(launch_vocab_sum(s.dtype, f.sums, l.slices, tokens, hidden_size,
-                                                    l.sums_pitch, dhidden, d->sms, q))
+                                                    l.sums_pitch, nullptr, dhidden, d->sms, q))
                        : CREDIT_OK;
     }
     Products products;
@@ -525,6 +526,9 @@ credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse,
     char* const ws = static_cast<char*>(workspace);
     const TermMatrix h = operand(s, hidden, tokens, s.pack_h, ws + l.h);
     const TermMatrix w = operand(s, weight, vocab, s.pack_w, ws + l.w);
+    float* const unit = s.kind == kTerms1 ? reinterpret_cast<float*>(ws + l.unit) : nullptr;
+    if (unit && (st = from_cuda(launch_vocab_unit(dloss, target, ignore_index, tokens, unit, q))) != CREDIT_OK)
+        return st;
     if ((st = from_cuda(pack(s, hidden, h, weight, w, d->sms, q))) != CREDIT_OK) return st;
 
     const Split split = logits_split(s, l.piece, d->sms);
@@ -553,6 +557,7 @@ credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse,
         a.grad = ws + l.grad;
         a.grad_pitch = l.piece;
         a.grad_plane = l.piece * tokens;
+        a.unit = unit;
         a.err = err;
         if (split.splits > 1) {
             float* const sums = reinterpret_cast<float*>(ws + l.logits);
@@ -587,6 +592,7 @@ credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse,
             o.cols = (int32_t)hidden_size;
             o.add = p > 0;
             o.vec = aligned(dhidden, 16) && hidden_size * s.es % 16 == 0;
+            o.unit = unit;
             if (!term_map(rows, box_rows(pt, rows.rows, &k), &operands[0]) || !term_map(w, kTileK, &operands[1]))
                 return CREDIT_ERR_CUDA;
             a.jobs = 1;
@@ -605,6 +611,7 @@ credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse,
             o.rows = (int32_t)pv;
             o.cols = (int32_t)hidden_size;
             o.vec = aligned(dweight, 16) && hidden_size * s.es % 16 == 0;
+            o.unit = unit;
             if (products.dw.splits > 1) {
                 TileWork& k = a.work[j];
                 k.per = std::min(products.dw.per, k.kb);
@@ -620,7 +627,7 @@ credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse,
             return st;
         if (dweight && products.dw.splits > 1) {
             st = from_cuda(launch_vocab_sum(s.dtype, reinterpret_cast<float*>(ws + l.dw), products.dw.splits, pv,
-                                            hidden_size, products.dw.pitch,
+                                            hidden_size, products.dw.pitch, unit,
                                             static_cast<char*>(dweight) + v0 * hidden_size * s.es, d->sms, q));
             if (st != CREDIT_OK) return st;
         }
@@ -628,7 +635,7 @@ credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse,
     if (dhidden && l.add)  // (a split's terms lie one behind the other, as splits do)
         return from_cuda(launch_vocab_sum(s.dtype, reinterpret_cast<float*>(ws + l.sums),
                                           products.splits * (s.kind == kTerms2 ? 2 : 1), tokens,
-                                          hidden_size, l.sums_pitch, dhidden, d->sms, q));
+                                          hidden_size, l.sums_pitch, unit, dhidden, d->sms, q));
     return CREDIT_OK;
 }
 

@@ -31,7 +31,8 @@
 // parts in registers, which rounds to nearest; they do it while the next part is
 // multiplied.
 //
-// The gradient of the logits is rounded to bf16 for the products of bf16 operands.
+// The gradient of the logits is rounded to bf16 for the products of bf16 operands,
+// divided by the significand of the largest dloss (vocab_unit).
 // Each token's error is dominated by its target's, so of few tokens' some are large:
 // up to 32 tokens it takes two terms, which costs little there.  For dhidden they are
 // rows of one tile, whose sums are added behind; for dweight a stage holds both terms
@@ -287,6 +288,11 @@ template <VocabTerms TERMS> struct GradOut {
             scale = ignored ? 0.f : target < 0 || target >= a.vocab ? NAN : a.dloss[row];
             both = scale + (a.dlse ? a.dlse[row] : 0.f);
             lse = a.lse[row];
+            if (TERMS == kTerms1) {
+                const float unit = *a.unit;
+                scale /= unit;
+                both /= unit;
+            }
             to = ignored ? -1 : target - a.v0 - t.n0;
         }
         none = both == 0.f;  // (its exponentials may be infinite)
@@ -339,6 +345,7 @@ template <typename T> struct ProductRow {
     int left, rows;
     float* sums;
     T* out;
+    float unit;
     const Turn turn;
     __device__ ProductRow(const VocabArgs& a, const Tile& t, int row0, unsigned char* room)
         : o(a.out[t.job]), turn{room, (int)threadIdx.x & 31} {
@@ -346,6 +353,7 @@ template <typename T> struct ProductRow {
         left = o.cols - t.n0;
         sums = o.sums ? o.sums + ((int64_t)t.split * o.rows + row0) * o.pitch + t.n0 : nullptr;
         out = static_cast<T*>(o.out) + (int64_t)row0 * o.pitch + t.n0;
+        unit = o.unit ? *o.unit : 1.f;
     }
     // 64 bytes of each row, E a vector's elements, to memory from column c on
     template <int E> __device__ __forceinline__ void write(int c) const {
@@ -390,7 +398,7 @@ template <typename T> struct ProductRow {
         } else {
             float f[32];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
+            for (int j = 0; j < 32; ++j) f[j] = unit * __uint_as_float(v[j]);
             halves(f, w);
             turn.put(w);
             write<8>(c);
