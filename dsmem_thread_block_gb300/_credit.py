@@ -158,6 +158,8 @@ SIGNATURES = {
                                         _vp, _sz, _vp]),
     "credit_linear_ce_backward": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64,
                                          _i64, _i64, _i32, _vp, _sz, _vp]),
+    "credit_linear_ce_backward_precise": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64,
+                                                 _i64, _i64, _i32, _vp, _sz, _vp]),
     "credit_grad_workspace": (_i32, [ctypes.POINTER(Tensor), _i64, _i32,
                                      ctypes.POINTER(ctypes.c_size_t)]),
     "credit_grad_norm": (_i32, [ctypes.POINTER(Tensor), _i64, _vp, _vp, _sz, _vp]),
@@ -387,7 +389,7 @@ def credit_norm_backward(op: int, dy: int, dh: int, h: int, mean: int, rstd: int
                                        dtype, workspace, workspace_bytes, stream)
 
 
-def credit_linear_ce_workspace(backward: bool, hidden: int, weight: int, tokens: int,
+def credit_linear_ce_workspace(backward: int, hidden: int, weight: int, tokens: int,
                                hidden_size: int, vocab: int, dtype: int, device: int = 0) -> int:
     n = ctypes.c_size_t()
     _check(load().credit_linear_ce_workspace(int(backward), hidden, weight, tokens, hidden_size,
@@ -411,6 +413,17 @@ def credit_linear_ce_backward(dloss: int, dlse: int, hidden: int, weight: int, t
     return load().credit_linear_ce_backward(dloss, dlse, hidden, weight, target, ignore_index, lse,
                                             dhidden, dweight, tokens, hidden_size, vocab, dtype,
                                             workspace, workspace_bytes, stream)
+
+
+def credit_linear_ce_backward_precise(dloss: int, dlse: int, hidden: int, weight: int, target: int,
+                                      ignore_index: int, lse: int, dhidden: int, dweight: int,
+                                      tokens: int, hidden_size: int, vocab: int, dtype: int,
+                                      workspace: int = 0, workspace_bytes: int = 0,
+                                      stream: int = 0) -> int:
+    return load().credit_linear_ce_backward_precise(dloss, dlse, hidden, weight, target,
+                                                    ignore_index, lse, dhidden, dweight, tokens,
+                                                    hidden_size, vocab, dtype, workspace,
+                                                    workspace_bytes, stream)
 
 
 def tensors(entries):

@@ -31,7 +31,7 @@ decltype(&credit_norm_forward) g_forward;
 decltype(&credit_norm_backward) g_backward;
 decltype(&credit_linear_ce_workspace) g_ce_workspace;
 decltype(&credit_linear_ce_forward) g_ce_forward;
-decltype(&credit_linear_ce_backward) g_ce_backward;
+decltype(&credit_linear_ce_backward) g_ce_backward, g_ce_backward_precise;
 decltype(&credit_grad_workspace) g_grad_workspace;
 decltype(&credit_grad_norm) g_grad_norm;
 decltype(&credit_grad_clip) g_grad_clip;
@@ -362,9 +362,9 @@ PyObject* py_ce_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // linear_ce_backward(dloss, hidden, weight, target, lse, dlse, ignore index, need dhidden,
-//                    need dweight, dhidden, dweight, workspace)
+//                    need dweight, dhidden, dweight, workspace, precise)
 PyObject* py_ce_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded(n, 12, [&]() -> PyObject* {
+    return guarded(n, 13, [&]() -> PyObject* {
         no_graph(a, {0, 1, 2, 4, 5, 9, 10});
         const Head head(a[1], a[2], a[3], a[6]);
         if (PyErr_Occurred()) return nullptr;
@@ -375,7 +375,8 @@ PyObject* py_ce_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const float *dp = head.per_token(dloss), *lp = head.per_token(lse);
         const float* ep = dlse.defined() ? head.per_token(dlse) : nullptr;
         const int want_h = PyObject_IsTrue(a[7]), want_w = PyObject_IsTrue(a[8]);
-        if (want_h < 0 || want_w < 0) return nullptr;
+        const int precise = PyObject_IsTrue(a[12]);
+        if (want_h < 0 || want_w < 0 || precise < 0) return nullptr;
         h.matrix(dh_given);
         if (dw_given.defined() &&
             (dw_given.sizes() != head.w.sizes() || dw_given.scalar_type() != head.w.scalar_type() ||
@@ -384,13 +385,14 @@ PyObject* py_ce_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const c10::cuda::CUDAGuard guard(h.t.device());
         size_t wb = 0;
         credit_status_t st;
-        const at::Tensor ws = head.workspace(1, tensor(a[11]), &wb, &st);
+        const at::Tensor ws = head.workspace(precise ? 2 : 1, tensor(a[11]), &wb, &st);
         if (st != CREDIT_OK) return result(st);
         at::Tensor dh = dh_given, dw = dw_given;
         if (!dh.defined() && want_h) dh = h.like();
         if (!dw.defined() && want_w) dw = h.empty(head.w.sizes(), head.w.scalar_type());
-        st = g_ce_backward(dp, ep, ptr(h.t), ptr(head.w), head.targets(), head.ignore, lp, ptr(dh),
-                           ptr(dw), h.rows, h.cols, head.vocab, h.code, ptr(ws), wb, stream(h));
+        const auto call = precise ? g_ce_backward_precise : g_ce_backward;
+        st = call(dp, ep, ptr(h.t), ptr(head.w), head.targets(), head.ignore, lp, ptr(dh), ptr(dw), h.rows,
+                  h.cols, head.vocab, h.code, ptr(ws), wb, stream(h));
         if (st == CREDIT_OK) written({&dh_given, &dw_given});
         return result(st, dh, dw);
     });
@@ -471,10 +473,11 @@ PyObject* py_gradients(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // bind(addresses of credit_dropout, credit_norm_workspace, credit_norm_forward,
 //      credit_norm_backward, credit_linear_ce_workspace, credit_linear_ce_forward,
-//      credit_linear_ce_backward, credit_grad_workspace, credit_grad_norm, credit_grad_clip)
+//      credit_linear_ce_backward, credit_grad_workspace, credit_grad_norm, credit_grad_clip,
+//      credit_linear_ce_backward_precise)
 PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (n != 10) {
-        PyErr_SetString(PyExc_TypeError, "bind takes ten addresses");
+    if (n != 11) {
+        PyErr_SetString(PyExc_TypeError, "bind takes eleven addresses");
         return nullptr;
     }
     g_dropout = reinterpret_cast<decltype(g_dropout)>(PyLong_AsVoidPtr(a[0]));
@@ -487,6 +490,7 @@ PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     g_grad_workspace = reinterpret_cast<decltype(g_grad_workspace)>(PyLong_AsVoidPtr(a[7]));
     g_grad_norm = reinterpret_cast<decltype(g_grad_norm)>(PyLong_AsVoidPtr(a[8]));
     g_grad_clip = reinterpret_cast<decltype(g_grad_clip)>(PyLong_AsVoidPtr(a[9]));
+    g_ce_backward_precise = reinterpret_cast<decltype(g_ce_backward)>(PyLong_AsVoidPtr(a[10]));
     if (PyErr_Occurred()) return nullptr;
     Py_RETURN_NONE;
 }

@@ -23,11 +23,11 @@ int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 constexpr int64_t kPieceBytes = (int64_t)256 << 20;
 // Most parts of a sum over the vocabulary.
 constexpr int kMaxSplits = 64;
-// Most tokens whose logits' gradient takes two bf16 terms.  Rounded to one, a token's
-// target is off by up to 2^-8, uniformly: the root mean square over T tokens varies by
-// 0.45 / sqrt(T) of itself, 8 % for 32.  The second term costs 64 tokens of 4096 x
-// 1024 20.2 us instead of 17.3, and 10 of 6907 x 512 16.5 instead of 15.6.
-constexpr int kTwoTerms = 32;
+// Most tokens whose logits' gradient takes two bf16 terms unasked: those whose two terms
+// are rows of one tile, so that dhidden's products cost no more for the second.  Rounded
+// to one, a token's target is off by up to 2^-8, uniformly: the root mean square over T
+// tokens varies by 0.45 / sqrt(T) of itself, 6 % for 64.
+constexpr int kTwoTerms = kTileM / 2;
 // Fewest stages of a part.
 constexpr int kMinPart = 8;
 
@@ -57,9 +57,10 @@ constexpr int64_t few_columns(int tokens) { return (tokens == 8 ? 200 << 10 : 10
 // 24 of 32768 x 4096 361 and 384, of 10000 x 6000 254 and 205, of 8192 x 4096 110 and 102).
 constexpr int64_t kFewForward = 16, kFewForwardWeight = 1 << 24;
 
-credit_status_t shape_of(bool backward, const void* h, const void* w, int64_t tokens, int64_t hidden,
+// backward: 0 the loss, 1 its gradient, 2 its precise gradient.
+credit_status_t shape_of(int backward, const void* h, const void* w, int64_t tokens, int64_t hidden,
                          int64_t vocab, credit_dtype_t dtype, Shape* s) {
-    if (tokens < 0 || hidden < 1 || vocab < 1) return CREDIT_ERR_INVALID_ARG;
+    if (tokens < 0 || hidden < 1 || vocab < 1 || backward < 0 || backward > 2) return CREDIT_ERR_INVALID_ARG;
     if (dtype != CREDIT_F32 && dtype != CREDIT_BF16) return CREDIT_ERR_UNSUPPORTED;
     // rows and columns are counted in 32 bits, tiles of 128 past them too
     const int64_t limit = ((int64_t)1 << 31) - 1024;
@@ -74,7 +75,9 @@ credit_status_t shape_of(bool backward, const void* h, const void* w, int64_t to
     s->dtype = (int)dtype;
     s->es = dtype == CREDIT_F32 ? 4 : 2;
     s->terms = dtype == CREDIT_F32 ? 3 : 1;
-    s->kind = dtype == CREDIT_F32 ? kTerms3 : tokens <= kTwoTerms ? kTerms2 : kTerms1;
+    s->kind = dtype == CREDIT_F32 ? kTerms3 : tokens <= kTwoTerms || backward == 2 ? kTerms2 : kTerms1;
+    // (two terms of a token are two rows)
+    if (s->kind == kTerms2 && tokens > limit / 2) return CREDIT_ERR_INVALID_ARG;
     if (!aligned(h, s->es) || !aligned(w, s->es)) return CREDIT_ERR_INVALID_ARG;
     const bool lines = hidden * s->es % 16 == 0;
     s->pack_h = s->terms > 1 || !lines || !aligned(h, 16);
@@ -389,7 +392,7 @@ credit_status_t credit_linear_ce_forward(const void* hidden, const void* weight,
                                          int64_t vocab, credit_dtype_t dtype, void* workspace,
                                          size_t workspace_bytes, void* stream) {
     Shape s;
-    credit_status_t st = shape_of(false, hidden, weight, tokens, hidden_size, vocab, dtype, &s);
+    credit_status_t st = shape_of(0, hidden, weight, tokens, hidden_size, vocab, dtype, &s);
     if (st != CREDIT_OK) return st;
     if (tokens == 0) return CREDIT_OK;
     if (!hidden || !weight || !target || !loss || !lse) return CREDIT_ERR_INVALID_ARG;
@@ -473,14 +476,17 @@ credit_status_t credit_linear_ce_forward(const void* hidden, const void* weight,
     return from_cuda(launch_vocab_merge(a, a.work[0].nt * vocab_tile_parts(tile), loss, lse, q));
 }
 
-credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse, const void* hidden,
-                                          const void* weight, const int64_t* target,
-                                          int64_t ignore_index, const float* lse, void* dhidden,
-                                          void* dweight, int64_t tokens, int64_t hidden_size,
-                                          int64_t vocab, credit_dtype_t dtype, void* workspace,
-                                          size_t workspace_bytes, void* stream) {
+}  // extern "C"
+
+namespace {
+
+credit_status_t gradient(int backward, const float* dloss, const float* dlse, const void* hidden,
+                         const void* weight, const int64_t* target, int64_t ignore_index,
+                         const float* lse, void* dhidden, void* dweight, int64_t tokens,
+                         int64_t hidden_size, int64_t vocab, credit_dtype_t dtype, void* workspace,
+                         size_t workspace_bytes, void* stream) {
     Shape s;
-    credit_status_t st = shape_of(true, hidden, weight, tokens, hidden_size, vocab, dtype, &s);
+    credit_status_t st = shape_of(backward, hidden, weight, tokens, hidden_size, vocab, dtype, &s);
     if (st != CREDIT_OK) return st;
     cudaStream_t q = (cudaStream_t)stream;
     const uint64_t hb = (uint64_t)(tokens * hidden_size) * s.es, wb = (uint64_t)(vocab * hidden_size) * s.es;
@@ -637,6 +643,31 @@ credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse,
                                           products.splits * (s.kind == kTerms2 ? 2 : 1), tokens,
                                           hidden_size, l.sums_pitch, unit, dhidden, d->sms, q));
     return CREDIT_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+credit_status_t credit_linear_ce_backward(const float* dloss, const float* dlse, const void* hidden,
+                                          const void* weight, const int64_t* target,
+                                          int64_t ignore_index, const float* lse, void* dhidden,
+                                          void* dweight, int64_t tokens, int64_t hidden_size,
+                                          int64_t vocab, credit_dtype_t dtype, void* workspace,
+                                          size_t workspace_bytes, void* stream) {
+    return gradient(1, dloss, dlse, hidden, weight, target, ignore_index, lse, dhidden, dweight, tokens,
+                    hidden_size, vocab, dtype, workspace, workspace_bytes, stream);
+}
+
+credit_status_t credit_linear_ce_backward_precise(const float* dloss, const float* dlse,
+                                                  const void* hidden, const void* weight,
+                                                  const int64_t* target, int64_t ignore_index,
+                                                  const float* lse, void* dhidden, void* dweight,
+                                                  int64_t tokens, int64_t hidden_size, int64_t vocab,
+                                                  credit_dtype_t dtype, void* workspace,
+                                                  size_t workspace_bytes, void* stream) {
+    return gradient(2, dloss, dlse, hidden, weight, target, ignore_index, lse, dhidden, dweight, tokens,
+                    hidden_size, vocab, dtype, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

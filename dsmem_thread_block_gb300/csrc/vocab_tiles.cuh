@@ -34,9 +34,9 @@
 // The gradient of the logits is rounded to bf16 for the products of bf16 operands,
 // divided by the significand of the largest dloss (vocab_unit).
 // Each token's error is dominated by its target's, so of few tokens' some are large:
-// up to 32 tokens it takes two terms, which costs little there.  For dhidden they are
-// rows of one tile, whose sums are added behind; for dweight a stage holds both terms
-// of A beside one B.
+// up to 64 tokens, and where the caller asks for it, it takes two terms.  For dhidden
+// they are rows of one product, whose sums are added behind (of 64 tokens the rows of
+// one tile); for dweight a stage holds both terms of A beside one B.
 //
 // fp32 operands come as three bf16 terms, x = x0 + x1 + x2 to 24 bits.  Of their
 // nine products six are formed; the others are below 2^-24 of x y.  A stage holds

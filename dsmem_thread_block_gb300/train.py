@@ -53,7 +53,8 @@ def _bind():
                 for f in ("credit_dropout", "credit_norm_workspace", "credit_norm_forward",
                           "credit_norm_backward", "credit_linear_ce_workspace",
                           "credit_linear_ce_forward", "credit_linear_ce_backward",
-                          "credit_grad_workspace", "credit_grad_norm", "credit_grad_clip")))
+                          "credit_grad_workspace", "credit_grad_norm", "credit_grad_clip",
+                          "credit_linear_ce_backward_precise")))
     _bound = lib
 
 
@@ -197,16 +198,21 @@ def linear_cross_entropy_forward(hidden, weight, target, ignore_index: int = -10
 def linear_cross_entropy_backward(dloss, hidden, weight, target, lse, dlse=None,
                                   ignore_index: int = -100, need_dhidden: bool = True,
                                   need_dweight: bool = True, dhidden=None, dweight=None,
-                                  workspace=None):
+                                  workspace=None, precise: bool = False):
     """The gradient of linear_cross_entropy_forward: from dloss (of each token's
     loss; of an ignored one it does not count) and dlse (of its lse, or None), both
     fp32 and contiguous (what autograd hands a mean's backward is expanded:
     `.contiguous()`), returns (dhidden, dweight).  One that is not needed is None, unless a tensor
-    for it is given in `dhidden` or `dweight`."""
+    for it is given in `dhidden` or `dweight`.
+
+    Of more than 64 bf16 tokens the logits' gradient is rounded to bf16 for the two
+    products, which takes 2.2e-3 of the 2-norm where dloss differs from token to token
+    (1.7e-3, the outputs' own rounding, where it is a mean's).  `precise` keeps it in two
+    bf16 terms, for about twice the time of the products; other calls do not change."""
     if C._lib is not _bound or _bound is None:
         _bind()
     r = _ext.linear_ce_backward(dloss, hidden, weight, target, lse, dlse, ignore_index,
-                                need_dhidden, need_dweight, dhidden, dweight, workspace)
+                                need_dhidden, need_dweight, dhidden, dweight, workspace, precise)
     if type(r) is int:
         raise CreditError(r, "credit_linear_ce_backward")
     return r

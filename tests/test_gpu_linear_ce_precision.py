@@ -63,3 +63,111 @@ def test_dloss_of_every_size_and_none():
     rest = torch.ones(200, dtype=torch.bool, device="cuda")
     rest[[7, 9]] = False
     assert torch.equal(dh[rest], base[0][rest]) and not bool(torch.isfinite(dh[~rest]).any())
+
+
+def exact_ones(tokens, vocab, seed):
+    """With w = 0 (or h = 0) every logit is 0, and with lse = 0 every p is 1: g = dloss (1 -
+    [target]) + dlse, of whole numbers, 0, 1, 256 or 257 in magnitude: the last takes two
+    bf16 terms."""
+    _, _, target = make(tokens, 1, vocab, torch.bfloat16, seed=seed, ignored=0.1)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    dloss = torch.randint(0, 2, (tokens,), generator=g, device="cuda").float()
+    dlse = (256 * (2 * torch.randint(0, 2, (tokens,), generator=g, device="cuda") - 1)).float()
+    counted = torch.where(target == IGNORE, torch.zeros_like(dloss), dloss)
+    grad = (counted + dlse)[:, None].double().expand(tokens, vocab).clone()
+    rows = (target != IGNORE).nonzero()[:, 0]
+    grad[rows, target[rows]] -= dloss[rows].double()
+    return target, dloss, dlse, grad
+
+
+# few tokens' form (fp32 g), whole and split products, several pieces, splits of both sums
+@pytest.mark.parametrize("tokens,hidden,vocab,precise", [
+    (1, 72, 300, False), (4, 65, 300, False), (9, 72, 300, False), (20, 5000, 333, False),
+    (32, 64, 4000, False), (33, 64, 4000, False), (64, 136, 1000, False), (64, 4104, 300, False),
+    (64, 72, 1100000, False), (65, 72, 700, True), (300, 136, 1000, True), (300, 1001, 2000, True),
+    (4099, 72, 33333, True), (200, 4104, 200, True), (3000, 40, 100, True)])
+def test_a_gradient_of_two_terms_keeps_them(tokens, hidden, vocab, precise):
+    target, dloss, dlse, g = exact_ones(tokens, vocab, tokens)
+    lse = torch.zeros(tokens, device="cuda")
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(3)
+
+    def ones(shape):
+        return (2 * torch.randint(0, 2, shape, generator=gen, device="cuda") - 1).bfloat16()
+
+    h, w = ones((tokens, hidden)), torch.zeros((vocab, hidden), device="cuda", dtype=torch.bfloat16)
+    dh, dw = credit.linear_cross_entropy_backward(dloss, h, w, target, lse, dlse=dlse, precise=precise)
+    assert bool((dh == 0).all())
+    # (sums below 2^24: exact in fp32, and rounded once)
+    assert torch.equal(dw, (g.t() @ h.double()).float().bfloat16())
+    # pairs of rows that cancel but for the small term: what one term would drop is all there is
+    w = ones((vocab // 2, hidden)).repeat_interleave(2, 0)
+    w[1::2] *= -1
+    w = torch.cat([w, torch.zeros((vocab - len(w), hidden), device="cuda").bfloat16()])
+    dh, dw = credit.linear_cross_entropy_backward(dloss, 0 * h, w, target, lse, dlse=dlse, precise=precise)
+    assert bool((dw == 0).all())
+    assert torch.equal(dh, (g @ w.double()).float().bfloat16())
+    assert tokens < 9 or float(dh.abs().max()) == 1
+
+
+@pytest.mark.parametrize("tokens,hidden,vocab,precise", [
+    (20, 64, 700, False), (64, 264, 1003, False), (50, 4104, 300, False), (40, 33, 700, False),
+    (65, 264, 1003, True), (333, 128, 5000, True), (2100, 136, 300, True)])
+def test_two_terms_leave_the_outputs_rounding(tokens, hidden, vocab, precise):
+    # ones in a column of w: dhidden there is dloss (sum p - 1) = 0 but for g's roundings,
+    # 2^-16 of each |g| for two terms, which add up to 2, and p's and lse's, 2^-24 of
+    # their arguments (logits up to some 20, 1000 of k at most)
+    h, w, target = make(tokens, hidden, vocab, torch.bfloat16, seed=21, ignored=0.0)
+    w[:, 0] = 1
+    _, lse = credit.linear_cross_entropy_forward(h, w, target)
+    one = torch.ones(tokens, device="cuda")
+    dh, dw = credit.linear_cross_entropy_backward(one, h, w, target, lse, precise=precise)
+    assert float(dh[:, 0].abs().max()) <= 2 * 2.0 ** -16 + 1e-4
+    g = (h.double() @ w.double().t() - lse.double()[:, None]).exp()
+    g[torch.arange(tokens), target] -= 1
+    for got, want in ((dh[:, 1:], (g @ w.double())[:, 1:]), (dw, g.t() @ h.double())):
+        own = (want.bfloat16().double() - want).norm() / want.norm()
+        off = (got.double() - want).norm() / want.norm()
+        # (sums of two terms err by 2^-16 of |g| against 2^-9 of the output's own rounding)
+        assert float(off) <= float(own) * 1.02 + 2.0 ** -16
+
+
+def test_precise_changes_nothing_else():
+    for tokens, dtype in ((5, torch.bfloat16), (30, torch.bfloat16), (300, torch.float32)):
+        h, w, target = make(tokens, 64, 500, dtype, seed=4)
+        loss, lse = credit.linear_cross_entropy_forward(h, w, target)
+        a = credit.linear_cross_entropy_backward(loss, h, w, target, lse)
+        b = credit.linear_cross_entropy_backward(loss, h, w, target, lse, precise=True)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_precise_with_given_outputs_a_workspace_and_a_graph():
+    h, w, target = make(300, 128, 2100, torch.bfloat16, seed=13)
+    _, lse = credit.linear_cross_entropy_forward(h, w, target)
+    dloss = torch.rand(300, device="cuda")
+    want = credit.linear_cross_entropy_backward(dloss, h, w, target, lse, precise=True)
+    ws = torch.empty(C.credit_linear_ce_workspace(2, h.data_ptr(), w.data_ptr(), 300, 128, 2100, C.BF16,
+                                                  h.device.index), dtype=torch.uint8, device="cuda")
+    dh, dw = torch.empty_like(h), torch.empty_like(w)
+
+    def call():
+        return credit.linear_cross_entropy_backward(dloss, h, w, target, lse, dhidden=dh, dweight=dw,
+                                                    workspace=ws, precise=True)
+
+    call()
+    assert torch.equal(dh, want[0]) and torch.equal(dw, want[1])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    h.copy_(h.roll(1, 0)), target.copy_(target.roll(1, 0))
+    lse.copy_(lse.roll(1, 0)), dloss.copy_(dloss.roll(1, 0))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(dh, want[0].roll(1, 0))
+    only = credit.linear_cross_entropy_backward(dloss, h, w, target, lse, need_dweight=False, precise=True)
+    # (its sums may be split at other places: another rounding of some elements)
+    assert only[1] is None and float((only[0] - dh).float().norm()) <= 2.0 ** -8 * float(dh.float().norm())
+    with pytest.raises(credit.CreditError):
+        credit.linear_cross_entropy_backward(dloss, h, w, target, lse, workspace=ws[:256], precise=True)

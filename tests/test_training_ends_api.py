@@ -106,3 +106,17 @@ int main(void) {
     got = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True,
                                           check=True).stdout.split()]
     assert got == [ctypes.sizeof(C.Tensor), C.Tensor.count.offset, C.Tensor.dtype.offset]
+
+
+def test_the_precise_gradient_refuses_as_the_other():
+    def precise(dloss=D, h=H, w=W, tokens=100, vocab=1000, dtype=C.BF16, dh=7 << 32):
+        return C.credit_linear_ce_backward_precise(dloss, 0, h, w, T, -100, S, dh, 8 << 32, tokens, 64, vocab,
+                                                   dtype, WS, 1 << 30)
+
+    for bad in (dict(dloss=0), dict(h=H + 1), dict(w=0), dict(vocab=0), dict(dh=W + 64), dict(tokens=-1),
+                dict(tokens=1 << 30, vocab=64)):  # (the last: two rows a token pass 31 bits)
+        assert precise(**bad) == C.ERR_INVALID_ARG
+    assert precise(dtype=7) == C.ERR_UNSUPPORTED
+    for backward in (-1, 3):
+        with pytest.raises(C.CreditError):
+            C.credit_linear_ce_workspace(backward, H, W, 100, 64, 1000, C.BF16)
