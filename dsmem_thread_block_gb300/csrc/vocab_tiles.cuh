@@ -247,11 +247,12 @@ struct StatsOut {
             s = s == 0.f ? 0.f : s * fast_ex2((m - base) * kLog2e);
             m = top;
         }
-        const float off = -base * kLog2e;
+        // (base goes first: base log2(e), rounded, would be off by more than the maximum's
+        // own term where logits are large, and leave that term below 1 where they are not)
         F2 sums[2] = {f2(0.f), f2(0.f)};
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
-            const F2 x = fma2(F2{__uint_as_float(v[j]), __uint_as_float(v[j + 1])}, f2(kLog2e), f2(off));
+            const F2 x = mul2(add2(F2{__uint_as_float(v[j]), __uint_as_float(v[j + 1])}, f2(-base)), f2(kLog2e));
             sums[j / 2 % 2] = add2(sums[j / 2 % 2], F2{fast_ex2(x.x), fast_ex2(x.y)});
         }
         const F2 both = add2(sums[0], sums[1]);
@@ -309,11 +310,10 @@ template <VocabTerms TERMS> struct GradOut {
     __device__ __forceinline__ void take(int c, const uint32_t (&v)[32]) {
         if (rows <= 0) return;
         float g[32];
-        const float off = -lse * kLog2e;
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-            const float z = __uint_as_float(v[j]);
-            const float e = TERMS != kTerms3 ? fast_ex2(fmaf(z, kLog2e, off)) : expf(z - lse);
+            const float x = __uint_as_float(v[j]) - lse;
+            const float e = TERMS != kTerms3 ? fast_ex2(x * kLog2e) : expf(x);
             g[j] = none ? 0.f : both * e;
         }
         if (to >= c && to < c + 32) {

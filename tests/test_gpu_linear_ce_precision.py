@@ -171,3 +171,46 @@ def test_precise_with_given_outputs_a_workspace_and_a_graph():
     assert only[1] is None and float((only[0] - dh).float().norm()) <= 2.0 ** -8 * float(dh.float().norm())
     with pytest.raises(credit.CreditError):
         credit.linear_cross_entropy_backward(dloss, h, w, target, lse, workspace=ws[:256], precise=True)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("spread", [20.0, 100.0, 1000.0])
+@pytest.mark.parametrize("tokens,hidden,vocab", [(1, 128, 1000), (40, 128, 1000), (300, 1001, 777), (130, 128, 70000),
+                                                 (4096, 128, 1000), (40, 4096, 500)])
+def test_no_loss_is_below_zero(tokens, hidden, vocab, spread, dtype):
+    # the target's logit is among those whose exponentials are summed: the sum is 1 or
+    # more times the largest's, which is the target's or above it
+    h, w, _ = make(tokens, hidden, vocab, dtype, seed=7, spread=spread)
+    z = h.double() @ w.double().t()
+    loss, _ = credit.linear_cross_entropy_forward(h, w, z.argmax(1))
+    assert bool((loss >= 0).all())
+
+
+@pytest.mark.parametrize("tokens", [1, 8, 40, 300])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("scale", [1e4, 1e6, 1e8, 1e10, 1e20, 1e30, 1e38, 2e38])
+def test_logits_of_any_finite_size(scale, dtype, tokens):
+    # one product a logit, so every logit is exact; the largest stands far above the others
+    vocab = 500
+    h = torch.zeros((tokens, 64), device="cuda", dtype=dtype)
+    w = torch.zeros((vocab, 64), device="cuda", dtype=dtype)
+    h[:, 0] = 1
+    for sign in (1, -1):
+        w[:, 0] = (torch.linspace(0.2, 1, vocab, device="cuda") * scale * sign).to(dtype)
+        w[13, 0] = 1.5 * scale if sign > 0 else 0.1 * scale * -1
+        z = w[:, 0].double()
+        target = torch.full((tokens,), 13, device="cuda")
+        loss, lse = credit.linear_cross_entropy_forward(h, w, target)
+        assert bool((lse.double() == z[13]).all()) and bool((loss == 0).all())
+        loss, _ = credit.linear_cross_entropy_forward(h, w, target + 1)
+        assert_close(loss, (z[13] - z[14]).expand(tokens), (2 * U * (z[13] - z[14]).abs()).expand(tokens), "loss")
+        # p is 1 for the largest and 0 for the others
+        one = torch.ones(tokens, device="cuda")
+        dh, dw = credit.linear_cross_entropy_backward(one, h, w, target + 1, lse)
+        assert bool((dw[13, 0] == tokens).all()) and bool((dw[14, 0] == -tokens).all())
+        dw[13:15, 0] = 0
+        assert bool((dw == 0).all())
+        want = (z[13] - z[14]).expand(tokens)
+        assert_close(dh[:, 0], want, (2.0 ** -8 if dtype == torch.bfloat16 else 8 * U) * want.abs() + 8 * U * 1.5 * scale,
+                     "dhidden")
+        assert bool((dh[:, 1:] == 0).all())
