@@ -30,6 +30,11 @@ constexpr int kMaxSplits = 64;
 constexpr int kTwoTerms = kTileM / 2;
 // Fewest stages of a part.
 constexpr int kMinPart = 8;
+// Most stages of a part of a product that is summed in the tensor cores' accumulators
+// alone.  Every addition of sixteen k drops up to 2^-25 of the sum, always towards zero:
+// four a stage, 2^-12 in all, where the rounding to bf16 behind it is up to 2^-8 (in one
+// part 4194304 tokens of one sign lost 0.8 %).
+constexpr int kLongPart = 2048;
 
 // Widest tile: a piece of the vocabulary is whole tiles of any shape.
 constexpr int kTileN = vocab_tile_cols(kPair256);
@@ -207,7 +212,8 @@ Products products_for(const Shape& s, int64_t piece, bool dh, bool dw, int sms) 
         double time = all / units;
         if (dh) {
             const int64_t share = std::max<int64_t>(kMinPart, (int64_t)(all / units / 2 / pairs));
-            const int64_t want = std::min<int64_t>(ceil_div(kb, share), kMaxSplits);
+            int64_t want = std::min<int64_t>(ceil_div(kb, share), kMaxSplits);
+            if (s.kind != kTerms3) want = std::max<int64_t>(want, ceil_div(kb, kLongPart));
             p.per = (int32_t)ceil_div(kb, want);
             p.splits = (int32_t)ceil_div(kb, p.per);
             const double part = tile_cost(t, (double)p.per * pairs);
@@ -240,10 +246,14 @@ Layout backward_layout(const Shape& s, bool dh, bool dw, int sms, Products* prod
     if (k.splits > 1) l.place(&l.logits, k.splits * s.tokens * k.pitch * 4);
     Split& d = products->dw;
     d = split_for(l.piece, s.hidden, s.tokens, s.terms == 1 ? 1 : 6, sms);
-    if (dw && d.splits > 1) {
-        products->tile = kOne128;
-        l.place(&l.dw, d.splits * std::min(l.piece, s.vocab) * d.pitch * 4);
+    if (dw && d.splits > 1) products->tile = kOne128;
+    // (a stage adds both terms' products)
+    const int64_t kt = ceil_div(s.tokens, kTileK), longest = s.kind == kTerms2 ? kLongPart / 2 : kLongPart;
+    if (s.kind != kTerms3 && d.per > longest) {
+        d.splits = (int32_t)ceil_div(kt, longest);
+        d.per = (int32_t)ceil_div(kt, d.splits);
     }
+    if (dw && d.splits > 1) l.place(&l.dw, d.splits * std::min(l.piece, s.vocab) * d.pitch * 4);
     l.sums_pitch = round_up(s.hidden, 4);
     l.add = dh && (products->splits > 1 || l.pieces > 1 || s.kind == kTerms2);
     if (l.add) l.place(&l.sums, products->splits * s.grad_rows() * l.sums_pitch * 4);

@@ -24,7 +24,9 @@
 //
 // Precision.  The tensor cores add into an fp32 accumulator without rounding to
 // nearest: a sum over k drifts towards zero by some 2^-25 of itself an addition of
-// sixteen products, 7e-6 over 4096.  A product rounded to bf16 does not see that.
+// sixteen products, 7e-6 over 4096.  A product rounded to bf16 does not see that up to a
+// k of 131072 (2^-12 of the terms' magnitude), and longer ones are summed in parts of that
+// (kLongPart).
 // The logits do (one of 30 is off by 2e-4, and so is the gradient p - 1 of a token
 // whose target is almost certain), and so do products of fp32 operands: there the
 // accumulator holds kPromote stages at a time, and the epilogue warps add these

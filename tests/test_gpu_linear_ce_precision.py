@@ -214,3 +214,46 @@ def test_logits_of_any_finite_size(scale, dtype, tokens):
         assert_close(dh[:, 0], want, (2.0 ** -8 if dtype == torch.bfloat16 else 8 * U) * want.abs() + 8 * U * 1.5 * scale,
                      "dhidden")
         assert bool((dh[:, 1:] == 0).all())
+
+
+def bias(got, want):
+    return float(((got.double() - want) / want).mean())
+
+
+@pytest.mark.parametrize("precise", [False, True])
+def test_a_long_sum_of_one_sign_does_not_sink(precise):
+    # Sums over a million tokens, or words, of products in 1 to 4.  The accumulator drops
+    # less than its last digit, 2^-23 of the sum so far, at each addition of sixteen
+    # products; 8192 additions to a part whose sum grows evenly make 2^-11.  The sums of a
+    # million numbers are nearly alike, so the outputs' own rounding is too: the rounded
+    # sums are compared.  Those that lie within 2^-11 of a rounding's border may fall on
+    # either side: of dweight's, 2346614 to 2347710 beside a border at 2334720, none; of
+    # dhidden's, a hundred different ones, an eighth, which is another 2^-11 of the mean.
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+
+    def ones_to_twos(shape):
+        return (1 + torch.randint(0, 128, shape, generator=g, device="cuda") / 128).bfloat16()
+
+    tokens, hidden, vocab = 1 << 20, 5120, 256
+    h = torch.empty((tokens, hidden), dtype=torch.bfloat16, device="cuda")
+    for i in range(0, tokens, 1 << 16):
+        h[i:i + (1 << 16)] = ones_to_twos((1 << 16, hidden))
+    w = torch.zeros((vocab, hidden), dtype=torch.bfloat16, device="cuda")
+    none, zero = torch.full((tokens,), IGNORE, device="cuda"), torch.zeros(tokens, device="cuda")
+    dlse = ones_to_twos((tokens,)).float()  # (with w = 0 and lse = 0 every p is 1: g = dlse)
+    _, dw = credit.linear_cross_entropy_backward(zero, h, w, none, zero, dlse=dlse, need_dhidden=False,
+                                                 precise=precise)
+    want = torch.zeros(hidden, dtype=torch.float64, device="cuda")
+    for i in range(0, tokens, 1 << 14):
+        want += dlse[i:i + (1 << 14)].double() @ h[i:i + (1 << 14)].double()
+    assert abs(bias(dw, want.bfloat16().double().expand(vocab, hidden))) <= 2.0 ** -11
+    del h, dw
+    tokens, hidden, vocab = 100, 136, 1300000
+    h = torch.zeros((tokens, hidden), dtype=torch.bfloat16, device="cuda")
+    w, dlse = ones_to_twos((vocab, hidden)), ones_to_twos((tokens,)).float()
+    for need_w in (True, False):
+        dh, _ = credit.linear_cross_entropy_backward(zero[:tokens], h, w, none[:tokens], zero[:tokens], dlse=dlse,
+                                                     need_dweight=need_w, precise=precise)
+        want = dlse.double()[:, None] * w.double().sum(0)
+        assert abs(bias(dh, want.bfloat16().double())) <= 2 * 2.0 ** -11
