@@ -85,7 +85,8 @@ struct VocabBars {
     uint64_t full[kVocabStages], empty[kVocabStages], acc_full[2], acc_empty[2], drained;
 };
 
-// Wait for a phase; false once a wait of this CTA has given up.
+// Wait for a phase; false once a wait of this CTA (or of its pair's, at the end) has
+// given up.
 __device__ __forceinline__ bool hold(uint32_t bar, uint32_t parity, unsigned* err,
                                      volatile int* dead) {
 #pragma unroll 1
@@ -422,6 +423,7 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
     __shared__ __align__(8) VocabBars bars;
     __shared__ uint32_t tmem_base;
     __shared__ int dead_flag;
+    __shared__ uint32_t fills[2];  // of A and B in all
     volatile int* const dead = &dead_flag;
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
     const int rank = CG == 1 ? 0 : (int)cluster_ctarank();
@@ -430,6 +432,7 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
     const int stage = a.a_room + S::kBytesB, stages = min(kVocabRing / stage, kVocabStages);
     if (threadIdx.x == 0) {
         dead_flag = 0;
+        fills[0] = fills[1] = 0;
         for (int s = 0; s < stages; ++s) {
             mbar_init(smem_u32(&bars.full[s]), 2);  // A and B
             mbar_init(smem_u32(&bars.empty[s]), 1);
@@ -515,10 +518,7 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                 for (int k = 0; k < t.kn; ++k)
                     if (!(TERMS != kTerms3 ? one(k, 0) : one(k, 2) && one(k, 1) && one(k, 0))) break;
             }
-            // a CTA that has given up leaves no copy in flight
-            if (!ok && leader && rank == 0)
-                for (uint32_t f = filled > (uint32_t)stages ? filled - stages : 0; f < filled; ++f)
-                    if (!mbar_wait_bounded(full0 + 8 * (f % stages), (f / stages) & 1u, a.err)) break;
+            if (leader) fills[B] = filled;
         };
         if (warp == kWarps) {
             fill(std::false_type());
@@ -583,10 +583,6 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                     if (ok && leader) mma_commit<CG>(smem_u32(&bars.acc_full[n & 1]));
                     k0 = k1;
                 }
-            }
-            if (!ok && leader) {  // nor a product
-                mma_commit<CG>(smem_u32(&bars.drained));
-                mbar_wait_bounded(smem_u32(&bars.drained), 0, a.err);
             }
         }
     } else {
@@ -667,10 +663,41 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
     tmem_fence_before();
     __syncthreads();
     if constexpr (CG > 1) {  // no CTA leaves while the other may signal it
+        if (threadIdx.x == 0 && *dead) st_cluster_u32(mapa_shared(smem_u32(&dead_flag), rank ^ 1), 1u);
         cluster_arrive_release();
         cluster_wait_acquire();
     }
     tmem_fence_after();
+    if (*dead) {  // A wait has given up: nothing is issued any more, and nothing is left in flight.
+        const bool leader = elect_one();     // (the same lane as before)
+        if (warp == kWarps + 1 && leader) {  // products
+            if (rank == 0) mma_commit<CG>(smem_u32(&bars.drained));
+            mbar_wait_bounded(smem_u32(&bars.drained), 0, a.err);
+        }
+        if (warp == kWarps && leader && rank == 0) {  // copies: both CTAs' count on the first one's stages
+            const uint32_t full0 = smem_u32(&bars.full[0]), most = max(fills[0], fills[1]);
+            const uint32_t least = most > (uint32_t)stages ? most - stages : 0;
+            bool ok = true;
+            for (uint32_t f = least; f < most; ++f)  // (the other operand of a stage does not come)
+                if (f >= min(fills[0], fills[1])) mbar_arrive(full0 + 8 * (f % stages));
+            for (uint32_t f = least; ok && f < most; ++f)
+                ok = mbar_wait_bounded(full0 + 8 * (f % stages), (f / stages) & 1u, a.err);
+            if constexpr (CG > 1) {
+                // A CTA that filled other stages than the first: their bytes complete no
+                // phase, and one time limit is what its copies are given.
+                const uint32_t there = mapa_shared(smem_u32(&fills[0]), 1);
+                if (ld_cluster_u32(there) != fills[0] || ld_cluster_u32(there + 4) != fills[1]) {
+                    const uint64_t t0 = globaltimer_ns();
+                    while (globaltimer_ns() - t0 < kWaitLimitNs) __nanosleep(1000);
+                }
+            }
+        }
+        __syncthreads();
+        if constexpr (CG > 1) {
+            cluster_arrive_release();
+            cluster_wait_acquire();
+        }
+    }
     if (warp == kWarps + 1) tmem_free<CG>(tmem, S::kTmem);
 }
 

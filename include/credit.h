@@ -920,9 +920,10 @@ credit_status_t credit_selftest_team_timeout(int device);
 /*
  * The same for the matrix products of the head's cross entropy: a tile of a pair
  * of CTAs, then one of a CTA alone, whose second operand nothing brings.  Every
- * wait gives up or sees that another has, copies in flight are waited for, the
- * tensor memory is freed, and CREDIT_ERR_DEVICE_TIMEOUT is returned.  Takes some
- * seconds; allocates scratch and synchronises the device.
+ * wait gives up or sees that another has, copies and products in flight are
+ * waited for, the tensor memory is freed, and CREDIT_ERR_DEVICE_TIMEOUT is
+ * returned.  Takes a second, the limit of a wait, for each; allocates scratch
+ * and synchronises the device.
  */
 credit_status_t credit_selftest_tile_timeout(int device);
 
