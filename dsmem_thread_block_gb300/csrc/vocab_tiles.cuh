@@ -518,6 +518,11 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
                 for (int k = 0; k < t.kn; ++k)
                     if (!(TERMS != kTerms3 ? one(k, 0) : one(k, 2) && one(k, 1) && one(k, 0))) break;
             }
+            // The products signal the last stages too: no CTA leaves before it has seen that
+            // (of a pair the signals come from the first CTA).
+            if (!B)
+                for (uint32_t f = filled > (uint32_t)stages ? filled - stages : 0; ok && f < filled; ++f)
+                    ok = arrived(empty0 + 8 * (f % stages), (f / stages) & 1u);
             if (leader) fills[B] = filled;
         };
         if (warp == kWarps) {
