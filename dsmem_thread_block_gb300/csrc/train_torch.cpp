@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -58,15 +59,27 @@ const at::Tensor& tensor(PyObject* o) {
 }
 
 // The calls record no graph: under grad mode a tensor that requires a gradient
-// would lose it without a word.
-void no_graph(PyObject* const* a, std::initializer_list<int> tensors) {
-    if (!c10::GradMode::is_enabled()) return;
-    for (const int i : tensors)
-        if (THPVariable_Check(a[i]) && THPVariable_Unpack(a[i]).requires_grad())
+// would lose it without a word, and one with a forward-mode tangent that.
+struct NoGraph {
+    const bool grad = c10::GradMode::is_enabled();
+    const bool tangents = c10::AutogradState::get_tls_state().get_fw_grad_mode();
+    void check(const at::Tensor& t, const char* message) const {
+        if (!t.defined()) return;
+        if (grad && t.requires_grad()) throw Refused{PyExc_RuntimeError, message};
+        if (tangents && t._fw_grad(0).defined())
             throw Refused{PyExc_RuntimeError,
-                          "credit: the training operators record no autograd graph, and a tensor "
-                          "that requires a gradient was given: call the forward and backward pair "
-                          "under torch.no_grad(), or inside a torch.autograd.Function"};
+                          "credit: the training operators have no forward-mode derivative, and a "
+                          "tensor with a tangent was given"};
+    }
+};
+void no_graph(PyObject* const* a, std::initializer_list<int> tensors) {
+    const NoGraph none;
+    for (const int i : tensors)
+        if (THPVariable_Check(a[i]))
+            none.check(THPVariable_Unpack(a[i]),
+                       "credit: the training operators record no autograd graph, and a tensor "
+                       "that requires a gradient was given: call the forward and backward pair "
+                       "under torch.no_grad(), or inside a torch.autograd.Function");
 }
 
 // A caller's output has been written: autograd refuses to use what it saved of it.
@@ -426,7 +439,12 @@ PyObject* py_gradients(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (in.size() == 0) bad("credit: at least one gradient is required");
         if (in.size() != out.size()) bad("credit: one output per gradient is required");
         std::vector<credit_tensor_t> t((size_t)in.size());
-        const bool graph = c10::GradMode::is_enabled();
+        const NoGraph none;
+        for (const Items* const list : {&in, &out})
+            for (Py_ssize_t i = 0; i < list->size(); ++i)
+                none.check(tensor((*list)[i]),
+                           "credit: the training operators record no autograd graph, and a tensor "
+                           "that requires a gradient was given: call under torch.no_grad()");
         at::Device device(at::kCPU);
         for (Py_ssize_t i = 0; i < in.size(); ++i) {
             const at::Tensor &g = tensor(in[i]), &o = tensor(out[i]);
@@ -437,10 +455,6 @@ PyObject* py_gradients(PyObject*, PyObject* const* a, Py_ssize_t n) {
             if (apart && (!o.defined() || o.sizes() != g.sizes() || o.strides() != g.strides() ||
                           o.scalar_type() != g.scalar_type() || o.device() != device))
                 bad("credit: outputs must be tensors like the gradients, of their strides");
-            if (graph && (g.requires_grad() || (apart && o.requires_grad())))
-                throw Refused{PyExc_RuntimeError,
-                              "credit: the training operators record no autograd graph, and a tensor "
-                              "that requires a gradient was given: call under torch.no_grad()"};
             t[i].data = ptr(g);
             t[i].out = clip ? ptr(o) : nullptr;
             t[i].count = g.numel();
