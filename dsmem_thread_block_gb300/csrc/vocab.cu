@@ -377,7 +377,11 @@ cudaError_t launch_vocab(VocabOut out, VocabTerms terms, VocabTile tile, const C
     int dev;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (!kernel_info(dev, fn, false)) return cudaErrorInvalidDeviceFunction;  // its shared memory is opted in
+    const KernelInfo* const info = kernel_info(dev, fn, false);  // its shared memory is opted in
+    if (!info) return cudaErrorInvalidDeviceFunction;
+    // (another compiler, or its flags)
+    if (vocab_promotes(out, terms) && info->regs < vocab_launch_regs(vocab_tile_cols(tile)))
+        return cudaErrorLaunchOutOfResources;
     const int ctas = vocab_tile_ctas(tile), most = sms / ctas;
     int64_t total = 0;
     for (int j = 0; j < args.jobs; ++j)

@@ -65,6 +65,16 @@ namespace credit {
 constexpr int vocab_warps(int columns) { return columns / kPartCols * 4; }
 // whole warpgroups; one of the other four warps only waits
 constexpr int vocab_threads(int columns) { return 32 * (vocab_warps(columns) + 4); }
+// The sums of an epilogue thread (where they are kept in registers) take registers that
+// the other four warps do not need: a thread of the epilogue's, one of the others', and
+// what a thread has to have at launch for both to be there (a block that has fewer would
+// wait for them forever): 96 of 640 threads, 166 of 384.
+constexpr int vocab_regs(int columns) { return vocab_warps(columns) == 8 ? 208 : 104; }
+constexpr int vocab_other_regs(int columns) { return vocab_warps(columns) == 8 ? 80 : 64; }
+constexpr int vocab_launch_regs(int columns) {
+    return (vocab_warps(columns) * vocab_regs(columns) + 4 * vocab_other_regs(columns) + vocab_warps(columns) + 3) /
+           (vocab_warps(columns) + 4);
+}
 constexpr int kBoxBytes = 64 * kTileK * 2;      // one box of an operand with M or N innermost
 constexpr int kBytesA = kTileM * kTileK * 2;
 constexpr int kVocabRing = 6 * 32768;           // bytes of all stages
@@ -460,14 +470,8 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
     wait_for_launches();
     fence_proxy_async();  // an operand may be an earlier launch's
     Tile t;
-    // The sums of an epilogue thread take registers that the other warps do not
-    // need: of 640 x 96 at launch 128 x 64 and 512 x 104, of 384 x 168 128 x 80 and
-    // 256 x 208.
     if (warp >= kWarps) {
-        if constexpr (PROMOTE) {
-            if constexpr (kWarps == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-            else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        }
+        if constexpr (PROMOTE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(vocab_other_regs(N)));
         const uint32_t full0 = smem_u32(&bars.full[0]), empty0 = smem_u32(&bars.empty[0]);
         const uint32_t end = ring + (uint32_t)(stages * stage);
         uint32_t at = ring, bar = 0, phase = 0;  // of the present stage; bar: 8 bytes each
@@ -591,10 +595,7 @@ vocab_tiles(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUte
             }
         }
     } else {
-        if constexpr (PROMOTE) {
-            if constexpr (kWarps == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-            else asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-        }
+        if constexpr (PROMOTE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(vocab_regs(N)));
         const int quarter = warp & 3, block = warp >> 2;  // of rows, of columns
         unsigned char* const room = raw + (ring - smem_u32(raw)) + kVocabRing + warp * kTurnBytes;
         int n = 0;
