@@ -131,6 +131,14 @@ unsigned* device_error_word() {
     return static_cast<unsigned*>(p);
 }
 
+unsigned* checked_error_word() {
+#ifdef CREDIT_DEBUG
+    return device_error_word();
+#else
+    return nullptr;
+#endif
+}
+
 int occupancy_clusters(int dev, const void* fn, int P, int threads, size_t smem, int64_t rows) {
     const DevInfo* d = device_info(dev);
     if (!d) return 0;

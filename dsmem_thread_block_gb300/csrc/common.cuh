@@ -314,6 +314,14 @@ __device__ __forceinline__ bool in_bounds(bool ok, unsigned* err) {
 #endif
 }
 
+// Do `bytes` at p lie inside the `room` bytes at base?
+__device__ __forceinline__ bool inside(const void* p, size_t bytes, const void* base, size_t room,
+                                       unsigned* err) {
+    const char* const q = static_cast<const char*>(p);
+    const char* const b = static_cast<const char*>(base);
+    return in_bounds(q >= b && q + bytes <= b + room, err);
+}
+
 // Checked build: the combined statistics every CTA rebuilt for a row, so a
 // test can see that all P CTAs of a cluster hold bit-identical values (the
 // premise of the replicated push: "C. Cluster Reduction and Reuse Protocol",

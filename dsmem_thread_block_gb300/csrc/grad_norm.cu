@@ -46,6 +46,7 @@ template <int N> struct Table {
     int32_t first[N + 1];   // chunk
     uint8_t half[N];        // bf16
     int32_t n;
+    unsigned* err;          // (looked at by the checked build)
 };
 constexpr int kSmall = 64, kLarge = 960;
 static_assert(sizeof(Table<kLarge>) + 64 <= 32764, "kernel parameters");
@@ -82,6 +83,12 @@ __device__ __forceinline__ double cta_sum(double v) {
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) t += parts[w];
     return t;
+}
+
+// Is this chunk one of tensor i's?
+template <int N>
+__device__ __forceinline__ bool chunk_of(const Table<N>& t, int i, int c) {
+    return in_bounds(i >= 0 && i < t.n && c >= t.first[i] && c < t.first[i + 1], t.err);
 }
 
 // The chunks of a CTA: a run of the launch's.
@@ -180,6 +187,7 @@ grad_squares(const __grid_constant__ Table<N> t, double* parts, int keep) {
     int i = tensor_of(t, lo);
     for (int c = lo; c < hi; ++c) {
         while (c >= t.first[i + 1]) ++i;
+        if (!chunk_of(t, i, c)) break;
         const int64_t chunk = c - t.first[i];
         const uint64_t policy = c < hi - keep ? l2_policy_evict_first() : l2_policy_evict_last();
         sum += t.half[i] ? chunk_squares<bf16>(t.p[i], t.count[i], chunk, policy)
@@ -221,6 +229,7 @@ grad_scale(const __grid_constant__ Table<N> t, const double* parts, int nparts, 
     int i = tensor_of(t, hi - 1);
     for (int c = hi - 1; c >= lo; --c) {
         while (c < t.first[i]) --i;
+        if (!chunk_of(t, i, c)) break;
         const int64_t chunk = c - t.first[i];
         if (t.half[i]) chunk_scale<bf16>(t.p[i], t.out[i], t.count[i], chunk, factor);
         else chunk_scale<float>(t.p[i], t.out[i], t.count[i], chunk, factor);
@@ -276,11 +285,11 @@ template <int N> void fill(const credit_tensor_t* t, const Batch& b, Table<N>* t
     }
     table->first[k] = c;
     table->n = k;
+    table->err = checked_error_word();
 }
 
 struct Range {
     uintptr_t lo, hi;
-    int64_t owner;
     bool out;
 };
 
@@ -295,8 +304,8 @@ credit_status_t check(const credit_tensor_t* t, int64_t n, bool outs, const Rang
         const uintptr_t bytes = (uintptr_t)(t[i].count * es);
         const uintptr_t p = (uintptr_t)t[i].data, q = (uintptr_t)t[i].out;
         if (outs && (!q || q % es)) return CREDIT_ERR_INVALID_ARG;
-        if (!outs || p != q) r.push_back({p, p + bytes, i, false});
-        if (outs) r.push_back({q, q + bytes, i, true});
+        if (!outs || p != q) r.push_back({p, p + bytes, false});
+        if (outs) r.push_back({q, q + bytes, true});
     }
     // no output meets another buffer: sorted, each range against the furthest end before it
     std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
@@ -342,7 +351,7 @@ credit_status_t run(const credit_tensor_t* t, int64_t n, bool clip, float max_no
                     float* norm, void* workspace, size_t workspace_bytes, void* stream) try {
     if (n < 0 || (n && !t) || !norm || (uintptr_t)norm % 4) return CREDIT_ERR_INVALID_ARG;
     const uintptr_t w = (uintptr_t)workspace, o = (uintptr_t)norm;
-    const Range more[] = {{o, o + 4, -1, true}, {w, w + (workspace ? workspace_bytes : 0), -1, true}};
+    const Range more[] = {{o, o + 4, true}, {w, w + (workspace ? workspace_bytes : 0), true}};
     credit_status_t st = check(t, n, clip, more, 2);
     if (st != CREDIT_OK) return st;
     int dev;

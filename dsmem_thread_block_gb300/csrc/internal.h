@@ -225,6 +225,7 @@ cudaError_t launch_two_pass(KernelKey k, const TwoPassArgs& a, int64_t rows,
 cudaError_t launch_warp_rows(KernelKey k, const WarpRowsArgs& a, int blocks, cudaStream_t s);
 
 unsigned* device_error_word();  // address of this device's error word
+unsigned* checked_error_word();  // the same in the checked build, else null
 // checked build: this device's per-(row, rank) statistics record (null in the
 // regular build)
 float* debug_stats_buffer();

@@ -51,7 +51,9 @@ __global__ void __launch_bounds__(THREADS) vocab_merge(VocabArgs a, int nparts, 
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int t = t0 + u * kGroups;
-                p[u] = t < nparts ? __ldcg(&a.parts[(int64_t)t * a.rows + row]) : make_float2(-INFINITY, 0.f);
+                const float2* const q = &a.parts[(int64_t)t * a.rows + row];
+                p[u] = t < nparts && inside(q, sizeof(*q), a.parts, a.parts_room, a.err)
+                           ? __ldcg(q) : make_float2(-INFINITY, 0.f);
             }
             float top = m;
 #pragma unroll
@@ -105,6 +107,7 @@ vocab_rows(VocabArgs a, const float* sums, int splits, int64_t pitch, float* los
     float m = -INFINITY, s = 0.f;
     for (int c = 4 * (int)threadIdx.x; c < a.cols; c += 4 * kRowThreads) {
         const float* p = first + c;
+        if (!inside(p + (splits - 1) * plane, 16, sums, a.out[0].room, a.err)) continue;
         float4 f = __ldcg(reinterpret_cast<const float4*>(p));
 #pragma unroll 8
         for (int k = 1; k < splits; ++k) {
@@ -143,8 +146,9 @@ vocab_rows(VocabArgs a, const float* sums, int splits, int64_t pitch, float* los
                     t[j] = first_term(g[j]);
                     g[j] = rest_of(g[j], t[j]);
                 }
-                *reinterpret_cast<uint2*>(out + k * a.grad_plane) =
-                    make_uint2(Elem<bf16>::pack2(t[0], t[1]), Elem<bf16>::pack2(t[2], t[3]));
+                if (inside(out + k * a.grad_plane, 8, a.grad, a.grad_room, a.err))
+                    *reinterpret_cast<uint2*>(out + k * a.grad_plane) =
+                        make_uint2(Elem<bf16>::pack2(t[0], t[1]), Elem<bf16>::pack2(t[2], t[3]));
             }
         }
     }
@@ -217,6 +221,8 @@ struct PackArgs {
     int64_t rows[2];
     int64_t pitch, plane[2];
     int cols;
+    int64_t room[2];        // bytes at dst, and the error word (looked at by the checked build)
+    unsigned* err;
 };
 template <typename T>
 __global__ void __launch_bounds__(256) vocab_pack(PackArgs a) {
@@ -238,6 +244,7 @@ __global__ void __launch_bounds__(256) vocab_pack(PackArgs a) {
         const int c = 8 * v;
         const T* const p = src + r * cols + c;
         bf16* const q = dst + r * pitch + c;
+        if (!inside(q + (sizeof(T) == 4 ? 2 : 0) * plane, 16, dst, second ? a.room[1] : a.room[0], a.err)) return;
         bool done = false;
         if constexpr (sizeof(T) == 2) {
             // (both lines lie inside the matrix; element by element 10778 rows of 1001
@@ -285,7 +292,7 @@ __global__ void __launch_bounds__(256) vocab_pack(PackArgs a) {
 template <typename T, int G>
 __global__ void __launch_bounds__(256)
 vocab_sum(const float* sums, int splits, int64_t rows, int cols, int64_t pitch, const float* unit, T* out,
-          bool vec) {
+          bool vec, int64_t room, unsigned* err) {
     constexpr int kColumns = 256 / G;
     __shared__ float4 parts[G > 1 ? G : 1][G > 1 ? kColumns : 1];
     dependents_may_launch();
@@ -301,6 +308,7 @@ vocab_sum(const float* sums, int splits, int64_t rows, int cols, int64_t pitch, 
             const float* p = sums + r * pitch + 4 * v + group * plane;
 #pragma unroll 4
             for (int s = group; s < splits; s += G, p += G * plane) {
+                if (!inside(p, 16, sums, room, err)) break;
                 const float4 g = __ldcs(reinterpret_cast<const float4*>(p));
                 f = make_float4(f.x + g.x, f.y + g.y, f.z + g.z, f.w + g.w);
             }
@@ -433,6 +441,7 @@ cudaError_t run_tiles_alone(int dev, int sms, VocabTile tile) {
     a.cols = cols;
     a.vocab = cols;
     char* const rest = buf + h.plane + w.plane;
+    a.parts_room = (int64_t)rows * 8 * vocab_tile_parts(tile);
     a.target = reinterpret_cast<int64_t*>(rest);
     a.picked = reinterpret_cast<float*>(rest + (size_t)rows * 8);
     a.parts = reinterpret_cast<float2*>(rest + (size_t)rows * 12);
@@ -468,14 +477,16 @@ cudaError_t launch_vocab_unit(const float* dloss, const int64_t* target, int64_t
 }
 
 cudaError_t launch_vocab_pack(int dtype, const void* const (&src)[2], const TermMatrix (&dst)[2], int n,
-                              int sms, cudaStream_t s) {
+                              unsigned* err, int sms, cudaStream_t s) {
     PackArgs a{};
+    a.err = err;
     int64_t rows = 0;
     for (int i = 0; i < n; ++i) {
         a.src[i] = src[i];
         a.dst[i] = static_cast<bf16*>(const_cast<void*>(dst[i].p));
         a.rows[i] = dst[i].rows;
         a.plane[i] = dst[i].plane / 2;
+        a.room[i] = dst[i].plane * dst[i].terms;
         rows = std::max(rows, dst[i].rows);
     }
     a.pitch = dst[0].pitch / 2;
@@ -486,12 +497,14 @@ cudaError_t launch_vocab_pack(int dtype, const void* const (&src)[2], const Term
 }
 
 cudaError_t launch_vocab_sum(int dtype, const float* sums, int splits, int64_t rows, int64_t cols,
-                             int64_t pitch, const float* unit, void* out, int sms, cudaStream_t s) {
+                             int64_t pitch, const float* unit, void* out, int64_t room, unsigned* err, int sms,
+                             cudaStream_t s) {
     const int64_t n = rows * ((cols + 3) / 4);
     const bool vec = (uintptr_t)out % 16 == 0 && cols % 4 == 0, shared = splits >= 16;
     const dim3 grid((unsigned)blocks_for(shared ? 16 * n : n, sms));
     auto run = [&](auto* fn, auto* o) {
-        return launch_early(fn, grid, 256, s, sums, splits, rows, (int)cols, pitch, unit, o, vec);
+        return launch_early(fn, grid, 256, s, sums, splits, rows, (int)cols, pitch, unit, o, vec, room,
+                            err);
     };
     if (dtype == 0)
         return run(shared ? vocab_sum<float, 16> : vocab_sum<float, 1>, static_cast<float*>(out));

@@ -53,6 +53,7 @@ struct ProductOut {
     int32_t add;           // to what the sums hold
     int32_t vec;           // rows of `out` are whole 16-byte lines
     const float* unit;     // what the logits' gradient was divided by (null: 1; not for sums)
+    int64_t room;          // bytes at `sums`, or else at `out` (looked at by the checked build)
 };
 
 struct VocabArgs {
@@ -69,6 +70,7 @@ struct VocabArgs {
     // the target's logit per token
     float2* parts;
     float* picked;
+    int64_t parts_room;    // bytes of it, as grad_room (looked at by the checked build)
     // gradient of the logits
     const float* lse;
     const float* dloss;
@@ -76,6 +78,7 @@ struct VocabArgs {
     void* grad;            // terms planes, tokens x grad_pitch
     int64_t grad_pitch, grad_plane;  // elements
     const float* unit;     // of one term: what it is divided by (vocab_unit)
+    int64_t grad_room;
     ProductOut out[2];
     unsigned* err;
     int32_t alone;         // a self-test: nothing brings B, every wait runs out
@@ -111,6 +114,9 @@ struct FewArgs {
     float* sums;                   // of dhidden, per slice; null: not wanted
     int64_t sums_pitch;
     void* dw;                      // null: not wanted
+    // bytes of parts, grad and sums, and the error word (looked at by the checked build)
+    int64_t parts_room, grad_room, sums_room;
+    unsigned* err;
 };
 constexpr int kFewTokens = 8;      // most of them
 // the tokens that a kernel counts with
@@ -136,16 +142,17 @@ cudaError_t run_tiles_alone(int dev, int sms, VocabTile tile);
 // loss and lse from the tiles' parts
 cudaError_t launch_vocab_merge(const VocabArgs& a, int nparts, float* loss, float* lse,
                                cudaStream_t s);
-// From the splits' sums of the logits, splits x tokens x pitch: loss and lse, or with
+// From the splits' sums of the logits, splits x tokens x pitch (a.out[0].room bytes): loss and lse, or with
 // a.grad the logits' gradient in `terms` terms.
 cudaError_t launch_vocab_rows(const VocabArgs& a, const float* sums, int splits, int64_t pitch,
                               VocabTerms terms, float* loss, float* lse, cudaStream_t s);
 // n matrices of the call's type and of one width as bf16 terms
 cudaError_t launch_vocab_pack(int dtype, const void* const (&src)[2], const TermMatrix (&dst)[2], int n,
-                              int sms, cudaStream_t s);
-// out = the splits' sums added in order, times *unit (null: 1)
+                              unsigned* err, int sms, cudaStream_t s);
+// out = the splits' sums (`room` bytes) added in order, times *unit (null: 1)
 cudaError_t launch_vocab_sum(int dtype, const float* sums, int splits, int64_t rows, int64_t cols,
-                             int64_t pitch, const float* unit, void* out, int sms, cudaStream_t s);
+                             int64_t pitch, const float* unit, void* out, int64_t room, unsigned* err, int sms,
+                             cudaStream_t s);
 // What a logits' gradient of one term is divided by.
 cudaError_t launch_vocab_unit(const float* dloss, const int64_t* target, int64_t ignore, int64_t tokens,
                               float* unit, cudaStream_t s);

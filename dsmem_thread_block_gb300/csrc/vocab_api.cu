@@ -114,9 +114,11 @@ struct Layout {
     int32_t pieces;
     int64_t sums_pitch;
     bool add;           // dhidden is the sums' sum
-    void place(int64_t* at, int64_t n) {
+    int64_t parts_room, logits_room, grad_room, dw_room, sums_room;  // bytes
+    int64_t place(int64_t* at, int64_t n) {
         *at = bytes;
         bytes += round_up(n, 256);
+        return n;
     }
 };
 
@@ -180,10 +182,10 @@ Layout forward_layout(const Shape& s, VocabTile t, const Split& k) {
     l.place(&l.h, operand_bytes(s, s.tokens, s.pack_h));
     l.place(&l.w, operand_bytes(s, s.vocab, s.pack_w));
     if (k.splits > 1) {
-        l.place(&l.logits, k.splits * s.tokens * k.pitch * 4);
+        l.logits_room = l.place(&l.logits, k.splits * s.tokens * k.pitch * 4);
         return l;
     }
-    l.place(&l.parts, ceil_div(s.vocab, vocab_tile_cols(t)) * vocab_tile_parts(t) * s.tokens * 8);
+    l.parts_room = l.place(&l.parts, ceil_div(s.vocab, vocab_tile_cols(t)) * vocab_tile_parts(t) * s.tokens * 8);
     l.place(&l.picked, s.tokens * 4);
     return l;
 }
@@ -239,11 +241,11 @@ Layout backward_layout(const Shape& s, bool dh, bool dw, int sms, Products* prod
     l.pieces = (int32_t)ceil_div(s.vocab, most);
     l.piece = round_up(ceil_div(s.vocab, l.pieces), kTileN);
     l.pieces = (int32_t)ceil_div(s.vocab, l.piece);
-    l.place(&l.grad, s.tokens * l.piece * 2 * s.kind);
+    l.grad_room = l.place(&l.grad, s.tokens * l.piece * 2 * s.kind);
     if (s.kind == kTerms1) l.place(&l.unit, 4);
     *products = products_for(s, std::min(l.piece, s.vocab), dh, dw, sms);
     const Split k = logits_split(s, l.piece, sms);
-    if (k.splits > 1) l.place(&l.logits, k.splits * s.tokens * k.pitch * 4);
+    if (k.splits > 1) l.logits_room = l.place(&l.logits, k.splits * s.tokens * k.pitch * 4);
     Split& d = products->dw;
     d = split_for(l.piece, s.hidden, s.tokens, s.terms == 1 ? 1 : 6, sms);
     if (dw && d.splits > 1) products->tile = kOne128;
@@ -253,16 +255,17 @@ Layout backward_layout(const Shape& s, bool dh, bool dw, int sms, Products* prod
         d.splits = (int32_t)ceil_div(kt, longest);
         d.per = (int32_t)ceil_div(kt, d.splits);
     }
-    if (dw && d.splits > 1) l.place(&l.dw, d.splits * std::min(l.piece, s.vocab) * d.pitch * 4);
+    if (dw && d.splits > 1) l.dw_room = l.place(&l.dw, d.splits * std::min(l.piece, s.vocab) * d.pitch * 4);
     l.sums_pitch = round_up(s.hidden, 4);
     l.add = dh && (products->splits > 1 || l.pieces > 1 || s.kind == kTerms2);
-    if (l.add) l.place(&l.sums, products->splits * s.grad_rows() * l.sums_pitch * 4);
+    if (l.add) l.sums_room = l.place(&l.sums, products->splits * s.grad_rows() * l.sums_pitch * 4);
     return l;
 }
 
 // The same of a call of a few tokens.
 struct FewLayout {
     int64_t parts, picked, grad, sums, bytes = 0;
+    int64_t parts_room = 0, grad_room = 0, sums_room = 0;
     int blocks, slices;
     int64_t sums_pitch;
 };
@@ -274,11 +277,11 @@ FewLayout few_layout(const Shape& s, bool backward, bool dh, bool vec, int sms) 
     l.slices = few_slices(s.hidden, s.dtype, vec, s.vocab, sms);
     l.sums_pitch = round_up(s.hidden, 4);
     if (!backward) {
-        place.place(&l.parts, l.blocks * s.tokens * 8);
+        l.parts_room = place.place(&l.parts, l.blocks * s.tokens * 8);
         place.place(&l.picked, s.tokens * 4);
     } else {
-        place.place(&l.grad, s.vocab * few_tokens(shaped) * 4);
-        if (dh) place.place(&l.sums, l.slices * s.tokens * l.sums_pitch * 4);
+        l.grad_room = place.place(&l.grad, s.vocab * few_tokens(shaped) * 4);
+        if (dh) l.sums_room = place.place(&l.sums, l.slices * s.tokens * l.sums_pitch * 4);
     }
     l.bytes = place.bytes;
     return l;
@@ -349,21 +352,21 @@ int box_rows(VocabTile t, int64_t rows, TileWork* w) {
 }
 
 // The logits of a.rows tokens and a.cols columns as the sums of their splits.
-void logits_out(const Split& k, float* sums, VocabArgs* a) {
+void logits_out(const Split& k, float* sums, int64_t room, VocabArgs* a) {
     a->work[0].per = k.per;
     a->work[0].splits = k.splits;
-    a->out[0] = ProductOut{nullptr, sums, k.pitch, a->rows, a->cols, 0, 1};
+    a->out[0] = ProductOut{nullptr, sums, k.pitch, a->rows, a->cols, 0, 1, nullptr, room};
 }
 
 // Copies the operands that the tensor maps cannot take as they are.
 cudaError_t pack(const Shape& s, const void* hidden, const TermMatrix& h, const void* weight,
-                 const TermMatrix& w, int sms, cudaStream_t stream) {
+                 const TermMatrix& w, unsigned* err, int sms, cudaStream_t stream) {
     const void* src[2];
     TermMatrix dst[2];
     int n = 0;
     if (s.pack_h) { src[n] = hidden; dst[n++] = h; }
     if (s.pack_w) { src[n] = weight; dst[n++] = w; }
-    return n ? launch_vocab_pack(s.dtype, src, dst, n, sms, stream) : cudaSuccess;
+    return n ? launch_vocab_pack(s.dtype, src, dst, n, err, sms, stream) : cudaSuccess;
 }
 
 }  // namespace
@@ -424,6 +427,8 @@ credit_status_t credit_linear_ce_forward(const void* hidden, const void* weight,
         FewArgs f = few_args(s, hidden, weight, target, ignore_index);
         f.parts = reinterpret_cast<float2*>(static_cast<char*>(workspace) + l.parts);
         f.parts_pitch = tokens;
+        f.parts_room = l.parts_room;
+        f.err = checked_error_word();
         f.picked = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.picked);
         float2* const parts = f.parts;
         float* const picked = f.picked;
@@ -434,6 +439,7 @@ credit_status_t credit_linear_ce_forward(const void* hidden, const void* weight,
             f.shaped = (int32_t)std::min<int64_t>(kFewTokens, tokens);
             f.target = target + t;
             f.parts = parts + t;
+            f.parts_room = l.parts_room - t * (int64_t)sizeof(*parts);
             f.picked = picked + t;
             if ((st = from_cuda(launch_few_logits(s.dtype, vec, f, l.blocks, q))) != CREDIT_OK) return st;
         }
@@ -446,6 +452,8 @@ credit_status_t credit_linear_ce_forward(const void* hidden, const void* weight,
         a.ignore = ignore_index;
         a.parts = f.parts;
         a.picked = f.picked;
+        a.parts_room = l.parts_room;
+        a.err = f.err;
         return from_cuda(launch_vocab_merge(a, l.blocks, loss, lse, q));
     }
     const Split split = logits_split(s, vocab, d->sms);
@@ -465,7 +473,7 @@ credit_status_t credit_linear_ce_forward(const void* hidden, const void* weight,
     if (!term_map(h, box_rows(tile, tokens, &a.work[0]), &maps[0]) ||
         !term_map(w, vocab_tile_cols(tile) / vocab_tile_ctas(tile), &maps[1]))
         return CREDIT_ERR_CUDA;
-    if ((st = from_cuda(pack(s, hidden, h, weight, w, d->sms, q))) != CREDIT_OK) return st;
+    if ((st = from_cuda(pack(s, hidden, h, weight, w, err, d->sms, q))) != CREDIT_OK) return st;
     a.rows = (int32_t)tokens;
     a.cols = (int32_t)vocab;
     a.vocab = vocab;
@@ -474,13 +482,14 @@ credit_status_t credit_linear_ce_forward(const void* hidden, const void* weight,
     a.err = err;
     if (split.splits > 1) {
         float* const sums = reinterpret_cast<float*>(ws + l.logits);
-        logits_out(split, sums, &a);
+        logits_out(split, sums, l.logits_room, &a);
         if ((st = from_cuda(launch_vocab(kVocabSums, s.kind, tile, maps, a, d->sms, q))) != CREDIT_OK)
             return st;
         return from_cuda(launch_vocab_rows(a, sums, split.splits, split.pitch, s.kind, loss, lse, q));
     }
     a.parts = reinterpret_cast<float2*>(ws + l.parts);
     a.picked = reinterpret_cast<float*>(ws + l.picked);
+    a.parts_room = l.parts_room;
     if ((st = from_cuda(launch_vocab(kVocabStats, s.kind, tile, maps, a, d->sms, q))) != CREDIT_OK)
         return st;
     return from_cuda(launch_vocab_merge(a, a.work[0].nt * vocab_tile_parts(tile), loss, lse, q));
@@ -525,12 +534,16 @@ credit_status_t gradient(int backward, const float* dloss, const float* dlse, co
         f.grad = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.grad);
         if (dhidden) f.sums = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.sums);
         f.sums_pitch = l.sums_pitch;
+        f.grad_room = l.grad_room;
+        f.sums_room = l.sums_room;
+        f.err = checked_error_word();
         f.dw = dweight;
         const bool lines = aligned(weight, 16) && hidden_size * s.es % 16 == 0;
         if ((st = from_cuda(launch_few_logits(s.dtype, lines, f, l.blocks, q))) != CREDIT_OK) return st;
         if ((st = from_cuda(launch_few_products(s.dtype, vec, f, l.slices, q))) != CREDIT_OK) return st;
         return dhidden ? from_cuda(launch_vocab_sum(s.dtype, f.sums, l.slices, tokens, hidden_size,
-                                                    l.sums_pitch, nullptr, dhidden, d->sms, q))
+                                                    l.sums_pitch, nullptr, dhidden, l.sums_room, f.err, d->sms,
+                                                    q))
                        : CREDIT_OK;
     }
     Products products;
@@ -545,7 +558,7 @@ credit_status_t gradient(int backward, const float* dloss, const float* dlse, co
     float* const unit = s.kind == kTerms1 ? reinterpret_cast<float*>(ws + l.unit) : nullptr;
     if (unit && (st = from_cuda(launch_vocab_unit(dloss, target, ignore_index, tokens, unit, q))) != CREDIT_OK)
         return st;
-    if ((st = from_cuda(pack(s, hidden, h, weight, w, d->sms, q))) != CREDIT_OK) return st;
+    if ((st = from_cuda(pack(s, hidden, h, weight, w, err, d->sms, q))) != CREDIT_OK) return st;
 
     const Split split = logits_split(s, l.piece, d->sms);
     const VocabTile pt = products.tile, gt = split.splits > 1 ? kOne128 : logits_tile(s, l.piece, d->sms);
@@ -573,11 +586,12 @@ credit_status_t gradient(int backward, const float* dloss, const float* dlse, co
         a.grad = ws + l.grad;
         a.grad_pitch = l.piece;
         a.grad_plane = l.piece * tokens;
+        a.grad_room = l.grad_room;
         a.unit = unit;
         a.err = err;
         if (split.splits > 1) {
             float* const sums = reinterpret_cast<float*>(ws + l.logits);
-            logits_out(split, sums, &a);
+            logits_out(split, sums, l.logits_room, &a);
             if ((st = from_cuda(launch_vocab(kVocabSums, s.kind, gt, logits, a, d->sms, q))) != CREDIT_OK)
                 return st;
             st = from_cuda(launch_vocab_rows(a, sums, split.splits, split.pitch, s.kind, nullptr, nullptr, q));
@@ -604,6 +618,7 @@ credit_status_t gradient(int backward, const float* dloss, const float* dlse, co
             o.out = dhidden;
             o.sums = l.add ? reinterpret_cast<float*>(ws + l.sums) : nullptr;
             o.pitch = l.add ? l.sums_pitch : hidden_size;
+            o.room = l.add ? l.sums_room : (int64_t)hb;
             o.rows = (int32_t)rows.rows;
             o.cols = (int32_t)hidden_size;
             o.add = p > 0;
@@ -624,6 +639,7 @@ credit_status_t gradient(int backward, const float* dloss, const float* dlse, co
             o = ProductOut{};
             o.out = static_cast<char*>(dweight) + v0 * hidden_size * s.es;
             o.pitch = hidden_size;
+            o.room = pv * hidden_size * s.es;
             o.rows = (int32_t)pv;
             o.cols = (int32_t)hidden_size;
             o.vec = aligned(dweight, 16) && hidden_size * s.es % 16 == 0;
@@ -634,6 +650,7 @@ credit_status_t gradient(int backward, const float* dloss, const float* dlse, co
                 k.splits = (int32_t)ceil_div(k.kb, k.per);
                 o.sums = reinterpret_cast<float*>(ws + l.dw);
                 o.pitch = products.dw.pitch;
+                o.room = l.dw_room;
             }
             if (!term_map(g, kTileK, &operands[2 * j]) || !term_map(h, kTileK, &operands[2 * j + 1]))
                 return CREDIT_ERR_CUDA;
@@ -644,14 +661,15 @@ credit_status_t gradient(int backward, const float* dloss, const float* dlse, co
         if (dweight && products.dw.splits > 1) {
             st = from_cuda(launch_vocab_sum(s.dtype, reinterpret_cast<float*>(ws + l.dw), products.dw.splits, pv,
                                             hidden_size, products.dw.pitch, unit,
-                                            static_cast<char*>(dweight) + v0 * hidden_size * s.es, d->sms, q));
+                                            static_cast<char*>(dweight) + v0 * hidden_size * s.es, l.dw_room, err,
+                                            d->sms, q));
             if (st != CREDIT_OK) return st;
         }
     }
     if (dhidden && l.add)  // (a split's terms lie one behind the other, as splits do)
         return from_cuda(launch_vocab_sum(s.dtype, reinterpret_cast<float*>(ws + l.sums),
                                           products.splits * (s.kind == kTerms2 ? 2 : 1), tokens,
-                                          hidden_size, l.sums_pitch, unit, dhidden, d->sms, q));
+                                          hidden_size, l.sums_pitch, unit, dhidden, l.sums_room, err, d->sms, q));
     return CREDIT_OK;
 }
 

@@ -79,6 +79,10 @@ __global__ void __launch_bounds__(few_threads(TOKENS)) few_logits(FewArgs a) {
     dependents_may_launch();
     wait_for_launches();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pitch = a.pitch;
+    // (the tokens' room, which every step of a row stays in: zeros up to the pitch)
+    if (!layout_fits((uint64_t)TOKENS * pitch * 4, 0, 0, a.err) ||
+        !in_bounds((a.cols + IO::kStep - 1) / IO::kStep * IO::kStep <= pitch, a.err))
+        return;
     for (int i = threadIdx.x; i < TOKENS * pitch; i += kThreads) {
         const int t = i / pitch, c = i - t * pitch;
         hidden[i] = t < a.tokens && c < a.cols ? Elem<T>::to_f(static_cast<const T*>(a.h)[(int64_t)t * a.cols + c])
@@ -169,14 +173,15 @@ __global__ void __launch_bounds__(few_threads(TOKENS)) few_logits(FewArgs a) {
         if (v >= a.vocab) continue;
         if (a.grad) {
             const float e = both == 0.f ? 0.f : both * expf(logit - lse);
-            if (lane % (32 / kSums) == 0)
-                a.grad[v * TOKENS + t] = live ? (v == target && target != a.ignore ? e - scale : e) : 0.f;
+            float* const p = a.grad + v * TOKENS + t;
+            if (lane % (32 / kSums) == 0 && inside(p, 4, a.grad, a.grad_room, a.err))
+                *p = live ? (v == target && target != a.ignore ? e - scale : e) : 0.f;
             continue;
         }
         const float top = fmaxf(m, logit), base = isinf(top) ? 0.f : top;
         s = (s == 0.f ? 0.f : s * expf(m - base)) + expf(logit - base);
         m = top;
-        if (writes && v == target) a.picked[t] = logit;
+        if (writes && v == target && in_bounds(t < a.tokens, a.err)) a.picked[t] = logit;
     }
     if (a.grad) return;
     // the rows of a token, then the warps
@@ -195,7 +200,8 @@ __global__ void __launch_bounds__(few_threads(TOKENS)) few_logits(FewArgs a) {
     __syncthreads();
     if (warp || !writes || r) return;
     for (int w = 1; w < kWarps; ++w) merge(parts[w][t].x, parts[w][t].y);
-    a.parts[(int64_t)blockIdx.x * a.parts_pitch + t] = make_float2(m, s);
+    float2* const p = a.parts + (int64_t)blockIdx.x * a.parts_pitch + t;
+    if (inside(p, sizeof(*p), a.parts, a.parts_room, a.err)) *p = make_float2(m, s);
 }
 
 // Grid: x the column blocks, y the slices of the vocabulary.
@@ -219,13 +225,16 @@ __global__ void __launch_bounds__(kThreads) few_products(FewArgs a) {
             h[t][k] = dw && t < a.tokens && col(k) < a.cols
                           ? Elem<T>::to_f(static_cast<const T*>(a.h)[(int64_t)t * a.cols + col(k)]) : 0.f;
         }
-    const bool inside = c0 < a.cols;  // (VEC: the whole vector)
+    const bool there = c0 < a.cols;  // (VEC: the whole vector)
     for (int64_t v0 = lo; v0 < hi; v0 += kGrads / TOKENS) {
         const int n = (int)min(hi - v0, (int64_t)(kGrads / TOKENS));
         __syncthreads();
-        for (int i = threadIdx.x; i < n * TOKENS; i += kThreads) grads[i] = a.grad[v0 * TOKENS + i];
+        for (int i = threadIdx.x; i < n * TOKENS; i += kThreads)
+            grads[i] = in_bounds(i < kGrads, a.err) &&
+                               inside(a.grad + v0 * TOKENS + i, 4, a.grad, a.grad_room, a.err)
+                           ? a.grad[v0 * TOKENS + i] : 0.f;
         __syncthreads();
-        if (!inside) continue;
+        if (!there) continue;
         for (int i0 = 0; i0 < n; i0 += kUnroll) {
             float x[kUnroll][N];
             if (a.sums)
@@ -258,24 +267,26 @@ __global__ void __launch_bounds__(kThreads) few_products(FewArgs a) {
                     for (int t = 1; t < TOKENS; ++t) y[k] = fmaf(g[t], h[t][k], y[k]);
                 }
                 T* const row = dw + (v0 + i0 + u) * a.cols;
+                const size_t room = (size_t)(a.vocab * a.cols) * sizeof(T);
                 if constexpr (VEC) {
-                    st_global_cs_v4(row + c0, Elem<T>::pack(y));
+                    if (inside(row + c0, 16, dw, room, a.err)) st_global_cs_v4(row + c0, Elem<T>::pack(y));
                 } else {
 #pragma unroll
                     for (int k = 0; k < N; ++k)
-                        if (col(k) < a.cols) row[col(k)] = Elem<T>::from_f(y[k]);
+                        if (col(k) < a.cols && inside(row + col(k), sizeof(T), dw, room, a.err))
+                            row[col(k)] = Elem<T>::from_f(y[k]);
                 }
             }
         }
     }
-    if (!a.sums || !inside) return;
+    if (!a.sums || !there) return;
 #pragma unroll
     for (int t = 0; t < TOKENS; ++t) {
         if (t >= a.tokens) break;
         float* const p = a.sums + ((int64_t)blockIdx.y * a.tokens + t) * a.sums_pitch;
 #pragma unroll
         for (int k = 0; k < N; ++k)
-            if (col(k) < a.cols) p[col(k)] = sum[t][k];
+            if (col(k) < a.cols && inside(p + col(k), 4, a.sums, a.sums_room, a.err)) p[col(k)] = sum[t][k];
     }
 }
 

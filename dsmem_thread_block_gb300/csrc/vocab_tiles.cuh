@@ -275,11 +275,12 @@ struct StatsOut {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
                 if (to == c + j) z = __uint_as_float(v[j]);
-            a.picked[row] = z;
+            if (in_bounds(live, a.err)) a.picked[row] = z;
         }
     }
     __device__ __forceinline__ void done(int part) {
-        if (live) a.parts[(int64_t)part * a.rows + row] = make_float2(m, s);
+        float2* const p = a.parts + (int64_t)part * a.rows + row;
+        if (live && inside(p, sizeof(*p), a.parts, a.parts_room, a.err)) *p = make_float2(m, s);
     }
 };
 
@@ -317,7 +318,8 @@ template <VocabTerms TERMS> struct GradOut {
         halves(g, w);
         turn.put(w);
         turn.vectors([&](int row, int vec, uint4 v) {
-            if (row < rows) *reinterpret_cast<uint4*>(p + (int64_t)row * a.grad_pitch + 8 * vec) = v;
+            bf16* const q = p + (int64_t)row * a.grad_pitch + 8 * vec;
+            if (row < rows && inside(q, 16, a.grad, a.grad_room, a.err)) *reinterpret_cast<uint4*>(q) = v;
         });
     }
     __device__ __forceinline__ void take(int c, const uint32_t (&v)[32]) {
@@ -355,13 +357,14 @@ template <VocabTerms TERMS> struct GradOut {
 // A product's rows, of the call's type or as fp32 sums.
 template <typename T> struct ProductRow {
     const ProductOut& o;
+    unsigned* const err;
     int left, rows;
     float* sums;
     T* out;
     float unit;
     const Turn turn;
     __device__ ProductRow(const VocabArgs& a, const Tile& t, int row0, unsigned char* room)
-        : o(a.out[t.job]), turn{room, (int)threadIdx.x & 31} {
+        : o(a.out[t.job]), err(a.err), turn{room, (int)threadIdx.x & 31} {
         rows = o.rows - row0;
         left = o.cols - t.n0;
         sums = o.sums ? o.sums + ((int64_t)t.split * o.rows + row0) * o.pitch + t.n0 : nullptr;
@@ -372,13 +375,16 @@ template <typename T> struct ProductRow {
     template <int E> __device__ __forceinline__ void write(int c) const {
         if (o.vec) {  // (a row's columns are whole vectors)
             turn.vectors([&](int row, int vec, uint4 w) {
-                if (row < rows && c + E * vec < left)
-                    __stcs(reinterpret_cast<uint4*>(out + row * o.pitch + c + E * vec), w);
+                T* const q = out + row * o.pitch + c + E * vec;
+                if (row < rows && c + E * vec < left && inside(q, 16, o.out, o.room, err))
+                    __stcs(reinterpret_cast<uint4*>(q), w);
             });
         } else {
             using Word = std::conditional_t<E == 4, uint32_t, uint16_t>;
             turn.template elements<Word>([&](int row, int e, Word w) {
-                if (row < rows && c + e < left) reinterpret_cast<Word*>(out + row * o.pitch + c)[e] = w;
+                T* const q = out + row * o.pitch + c + e;
+                if (row < rows && c + e < left && inside(q, sizeof(T), o.out, o.room, err))
+                    *reinterpret_cast<Word*>(q) = w;
             });
         }
     }
@@ -398,6 +404,7 @@ template <typename T> struct ProductRow {
                         float4 f = make_float4(__uint_as_float(x.x), __uint_as_float(x.y),
                                                __uint_as_float(x.z), __uint_as_float(x.w));
                         float4* const p = reinterpret_cast<float4*>(sums + row * o.pitch + col);
+                        if (!inside(p, 16, o.sums, o.room, err)) return;
                         if (o.add) {
                             const float4 b = __ldcg(p);
                             f = make_float4(b.x + f.x, b.y + f.y, b.z + f.z, b.w + f.w);
