@@ -28,9 +28,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
             ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
             :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
 }
-__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
-    asm volatile("prefetch.tensormap [%0];" :: "l"(map) : "memory");
-}
 
 // ------------------------------------------------------------ tensor memory
 // `columns` (a power of two, 32 at least) for this CTA, or for both CTAs of a
