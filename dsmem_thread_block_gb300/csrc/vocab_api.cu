@@ -19,7 +19,8 @@ bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
-// Bytes of the logits' gradient that a piece of the vocabulary may take.
+// Bytes of the logits' gradient that a piece of the vocabulary may take, and of the
+// statistics' parts that a piece of the tokens may.
 constexpr int64_t kPieceBytes = (int64_t)256 << 20;
 // Most parts of a sum over the vocabulary.
 constexpr int kMaxSplits = 64;
@@ -36,7 +37,7 @@ constexpr int kMinPart = 8;
 // part 4194304 tokens of one sign lost 0.8 %).
 constexpr int kLongPart = 2048;
 
-// Widest tile: a piece of the vocabulary is whole tiles of any shape.
+// Widest tile: a piece of the vocabulary, or of the tokens, is whole tiles of any shape.
 constexpr int kTileN = vocab_tile_cols(kPair256);
 
 struct Shape {
@@ -110,7 +111,7 @@ int64_t operand_bytes(const Shape& s, int64_t rows, bool pack) {
 // The workspace of a call, in the order of its parts.
 struct Layout {
     int64_t h, w, parts, picked, unit, logits, grad, sums, dw, bytes;  // offsets
-    int64_t piece;      // vocabulary rows at a time
+    int64_t piece;      // vocabulary rows (backward) or tokens (forward) at a time
     int32_t pieces;
     int64_t sums_pitch;
     bool add;           // dhidden is the sums' sum
@@ -150,8 +151,8 @@ VocabTile tile_for(int64_t rows, int64_t cols, int64_t stages, int sms) {
     return best;
 }
 
-VocabTile logits_tile(const Shape& s, int64_t cols, int sms) {
-    return tile_for(s.tokens, cols, ceil_div(s.hidden, kTileK) * (s.terms == 1 ? 1 : 6), sms);
+VocabTile logits_tile(const Shape& s, int64_t rows, int64_t cols, int sms) {
+    return tile_for(rows, cols, ceil_div(s.hidden, kTileK) * (s.terms == 1 ? 1 : 6), sms);
 }
 
 // Parts of k of a product whose tiles of 128 x 128 would leave half of the SMs idle
@@ -177,16 +178,25 @@ Split logits_split(const Shape& s, int64_t cols, int sms) {
     return split_for(s.tokens, cols, s.hidden, s.terms == 1 ? 1 : 6, sms);
 }
 
-Layout forward_layout(const Shape& s, VocabTile t, const Split& k) {
+// The tokens are walked in equal pieces whose parts fit kPieceBytes, however wide the
+// tiles (16384 tokens of 131072 words: one piece).
+Layout forward_layout(const Shape& s, int sms, VocabTile* t, Split* split) {
     Layout l{};
+    const Split k = *split = logits_split(s, s.vocab, sms);
+    const int64_t token = ceil_div(s.vocab, kTileN) * vocab_tile_parts(kPair256) * 8;
+    const int64_t most = std::max<int64_t>(kTileN, kPieceBytes / token / kTileN * kTileN);
+    l.pieces = k.splits > 1 ? 1 : (int32_t)ceil_div(s.tokens, most);
+    l.piece = l.pieces > 1 ? round_up(ceil_div(s.tokens, l.pieces), kTileN) : s.tokens;
+    l.pieces = (int32_t)ceil_div(s.tokens, l.piece);
+    *t = k.splits > 1 ? kOne128 : logits_tile(s, l.piece, s.vocab, sms);
     l.place(&l.h, operand_bytes(s, s.tokens, s.pack_h));
     l.place(&l.w, operand_bytes(s, s.vocab, s.pack_w));
     if (k.splits > 1) {
         l.logits_room = l.place(&l.logits, k.splits * s.tokens * k.pitch * 4);
         return l;
     }
-    l.parts_room = l.place(&l.parts, ceil_div(s.vocab, vocab_tile_cols(t)) * vocab_tile_parts(t) * s.tokens * 8);
-    l.place(&l.picked, s.tokens * 4);
+    l.parts_room = l.place(&l.parts, ceil_div(s.vocab, vocab_tile_cols(*t)) * vocab_tile_parts(*t) * l.piece * 8);
+    l.place(&l.picked, l.piece * 4);
     return l;
 }
 
@@ -390,7 +400,9 @@ credit_status_t credit_linear_ce_workspace(int backward, const void* hidden, con
         return CREDIT_OK;
     }
     if (!backward) {
-        *bytes = (size_t)forward_layout(s, logits_tile(s, s.vocab, d->sms), logits_split(s, s.vocab, d->sms)).bytes;
+        VocabTile t;
+        Split k;
+        *bytes = (size_t)forward_layout(s, d->sms, &t, &k).bytes;
         return CREDIT_OK;
     }
     Products p;  // (whichever gradients are asked for)
@@ -456,9 +468,9 @@ credit_status_t credit_linear_ce_forward(const void* hidden, const void* weight,
         a.err = f.err;
         return from_cuda(launch_vocab_merge(a, l.blocks, loss, lse, q));
     }
-    const Split split = logits_split(s, vocab, d->sms);
-    const VocabTile tile = split.splits > 1 ? kOne128 : logits_tile(s, vocab, d->sms);
-    const Layout l = forward_layout(s, tile, split);
+    Split split;
+    VocabTile tile;
+    const Layout l = forward_layout(s, d->sms, &tile, &split);
     if (workspace_bytes < (uint64_t)l.bytes) return CREDIT_ERR_INVALID_ARG;
     unsigned* err = device_error_word();
     if (!err) return CREDIT_ERR_CUDA;
@@ -466,21 +478,21 @@ credit_status_t credit_linear_ce_forward(const void* hidden, const void* weight,
     char* const ws = static_cast<char*>(workspace);
     const TermMatrix h = operand(s, hidden, tokens, s.pack_h, ws + l.h);
     const TermMatrix w = operand(s, weight, vocab, s.pack_w, ws + l.w);
+    CUtensorMap maps[4] = {};
+    if (!term_map(w, vocab_tile_cols(tile) / vocab_tile_ctas(tile), &maps[1])) return CREDIT_ERR_CUDA;
+    if ((st = from_cuda(pack(s, hidden, h, weight, w, err, d->sms, q))) != CREDIT_OK) return st;
     VocabArgs a{};
     a.jobs = 1;
-    a.work[0] = work_of(tile, tokens, vocab, hidden_size, false, false);
-    CUtensorMap maps[4] = {};
-    if (!term_map(h, box_rows(tile, tokens, &a.work[0]), &maps[0]) ||
-        !term_map(w, vocab_tile_cols(tile) / vocab_tile_ctas(tile), &maps[1]))
-        return CREDIT_ERR_CUDA;
-    if ((st = from_cuda(pack(s, hidden, h, weight, w, err, d->sms, q))) != CREDIT_OK) return st;
-    a.rows = (int32_t)tokens;
     a.cols = (int32_t)vocab;
     a.vocab = vocab;
-    a.target = target;
     a.ignore = ignore_index;
     a.err = err;
     if (split.splits > 1) {
+        a.work[0] = work_of(tile, tokens, vocab, hidden_size, false, false);
+        if (!term_map(h, box_rows(tile, tokens, &a.work[0]), &maps[0])) return CREDIT_ERR_CUDA;
+        a.rows = (int32_t)tokens;
+        a.target = target;
+
         float* const sums = reinterpret_cast<float*>(ws + l.logits);
         logits_out(split, sums, l.logits_room, &a);
         if ((st = from_cuda(launch_vocab(kVocabSums, s.kind, tile, maps, a, d->sms, q))) != CREDIT_OK)
@@ -490,9 +502,21 @@ credit_status_t credit_linear_ce_forward(const void* hidden, const void* weight,
     a.parts = reinterpret_cast<float2*>(ws + l.parts);
     a.picked = reinterpret_cast<float*>(ws + l.picked);
     a.parts_room = l.parts_room;
-    if ((st = from_cuda(launch_vocab(kVocabStats, s.kind, tile, maps, a, d->sms, q))) != CREDIT_OK)
-        return st;
-    return from_cuda(launch_vocab_merge(a, a.work[0].nt * vocab_tile_parts(tile), loss, lse, q));
+    for (int64_t t = 0; t < tokens; t += l.piece) {
+        const int64_t n = std::min(l.piece, tokens - t);
+        TermMatrix rows = h;
+        rows.p = static_cast<const char*>(h.p) + t * h.pitch;
+        rows.rows = n;
+        a.work[0] = work_of(tile, n, vocab, hidden_size, false, false);
+        if (!term_map(rows, box_rows(tile, n, &a.work[0]), &maps[0])) return CREDIT_ERR_CUDA;
+        a.rows = (int32_t)n;
+        a.target = target + t;
+        if ((st = from_cuda(launch_vocab(kVocabStats, s.kind, tile, maps, a, d->sms, q))) != CREDIT_OK)
+            return st;
+        st = from_cuda(launch_vocab_merge(a, a.work[0].nt * vocab_tile_parts(tile), loss + t, lse + t, q));
+        if (st != CREDIT_OK) return st;
+    }
+    return CREDIT_OK;
 }
 
 }  // extern "C"
@@ -561,7 +585,7 @@ credit_status_t gradient(int backward, const float* dloss, const float* dlse, co
     if ((st = from_cuda(pack(s, hidden, h, weight, w, err, d->sms, q))) != CREDIT_OK) return st;
 
     const Split split = logits_split(s, l.piece, d->sms);
-    const VocabTile pt = products.tile, gt = split.splits > 1 ? kOne128 : logits_tile(s, l.piece, d->sms);
+    const VocabTile pt = products.tile, gt = split.splits > 1 ? kOne128 : logits_tile(s, tokens, l.piece, d->sms);
     // what the logits' gradient is formed from, and what it is multiplied with
     CUtensorMap logits[4] = {}, operands[4] = {};
     for (int p = 0; p < l.pieces; ++p) {

@@ -387,9 +387,11 @@ credit_status_t credit_norm_backward(credit_op_t op, const void *dy, const void 
  * tokens x hidden_size, weight vocab x hidden_size, both of `dtype` and
  * contiguous; tokens == 0 is a legal empty batch.  The tokens x vocab logits are
  * formed a tile at a time by the tensor cores and reduced there: the forward
- * pass keeps a maximum and a sum per token and 64 columns (8 bytes), the
+ * pass keeps a maximum and a sum per token and 64 columns (8 bytes) for a piece
+ * of the tokens at a time, 256 MiB of them (of 256 tokens, if that is more), the
  * backward pass the gradient of one piece of the vocabulary at a time, 256 MiB
- * of it (bf16 operands: rounded to bf16 for the two products, to two bf16 terms
+ * of it (256 columns of all tokens, if that is more: from 524288 bf16 tokens,
+ * 174763 fp32 ones; bf16 operands: rounded to bf16 for the two products, to two bf16 terms
  * up to 64 tokens and in credit_linear_ce_backward_precise); only products of few tiles and a long k leave theirs, 10 MB
  * at most, in the workspace.  fp32 operands are taken apart into three bf16
  * terms each and multiplied in six products, which keeps 24 bits; a value that

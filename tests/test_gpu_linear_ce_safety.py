@@ -142,3 +142,42 @@ def test_clipping_writes_nothing_beside_its_tensors():
             c()
         for t, o in zip(grads, outs):
             assert float((o.double() - t.double() * factor).abs().max() if t.numel() else 0) <= 2.0 ** -8 * 6 * factor
+
+
+def forward_workspace(tokens, hidden, vocab, code):
+    return C.credit_linear_ce_workspace(0, 1 << 32, 2 << 32, tokens, hidden, vocab, code,
+                                        torch.cuda.current_device())
+
+
+def test_a_losss_workspace_is_bounded():
+    mib = 1 << 20
+    for tokens in (4096, 16384, 65536, 1 << 20, 10 ** 7):
+        for vocab in (4096, 32000, 131072, 262144):
+            if tokens * vocab > 1 << 40:
+                continue
+            # (bf16 at whole lines: nothing is packed; 4 bytes a token for its target's logit)
+            assert forward_workspace(tokens, 64, vocab, C.BF16) <= 256 * mib + 4 * min(tokens, 1 << 19) + 512
+            # fp32: and both operands in three terms
+            packed = 6 * 64 * (tokens + vocab)
+            assert forward_workspace(tokens, 64, vocab, C.F32) <= 256 * mib + packed + 4 * min(tokens, 1 << 19) + 1024
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("hidden", [24, 65])
+def test_a_loss_of_several_pieces_of_tokens(hidden, dtype):
+    # 131072 words leave 16 KiB a token: pieces of 16384 tokens at most, here 13824 and less
+    tokens, vocab = 41001, 131072
+    h, w, target = make(tokens, hidden, vocab, dtype, seed=5)
+    loss, lse = credit.linear_cross_entropy_forward(h, w, target)
+    for lo, hi in ((0, 13824), (13824, 27648), (27648, tokens)):
+        part = credit.linear_cross_entropy_forward(h[lo:hi].clone(), w, target[lo:hi])
+        assert torch.equal(loss[lo:hi], part[0]) and torch.equal(lse[lo:hi], part[1])
+    with C.use_checked_build():
+        again = credit.linear_cross_entropy_forward(h, w, target)
+        assert C.credit_get_device_error(torch.cuda.current_device()) == C.OK
+    assert torch.equal(again[0], loss) and torch.equal(again[1], lse)
+    n = forward_workspace(tokens, hidden, vocab, C.BF16 if dtype == torch.bfloat16 else C.F32)
+    ws, check = guarded(n)
+    again = credit.linear_cross_entropy_forward(h, w, target, workspace=ws)
+    check()
+    assert torch.equal(again[0], loss) and torch.equal(again[1], lse)
