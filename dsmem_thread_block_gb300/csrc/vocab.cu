@@ -7,11 +7,13 @@
 // what comes before and after them, and the launches.
 //   vocab_pack   operands that tensor maps cannot take (rows that are no whole 16-byte
 //                lines, fp32) as bf16 terms; bound by HBM: 16384 x 2048 fp32 54 us
-//   vocab_merge  the tiles' statistics of a token: 4096 tokens of 128 parts 10 us alone
+//   vocab_merge  the tiles' statistics of a token: alone, 4096 tokens of 256 parts 11 us, of
+//                2048 34
 //   vocab_rows   from logits that were summed in parts of k, where they have few tiles,
 //                the statistics or the gradient
 //   vocab_sum    parts of dhidden, or of dweight, in order: 4096 x 4096 20 us
-//   vocab_unit   what a logits' gradient of one bf16 term is divided by: some 2 us of a call
+//   vocab_unit   what a logits' gradient of one bf16 term is divided by: some 2 us of a call,
+//                4096 tokens alone 3.6 to 4.9
 // All kernels of a call are launched early (early_launch.h), which saves some 3 us of
 // a small call (32 x 1024 x 4096 forward 13.4 us called without, 9.6 with).
 #include "early_launch.h"

@@ -1,8 +1,8 @@
 // vocab_tiles.cuh -- the tiled matrix products of the linear head's cross entropy:
 // a persistent kernel whose CTAs, or pairs of CTAs, walk output tiles; a warp
 // fills a ring of stages by tensor-map copies, a thread issues tcgen05 products
-// into one of two accumulators in tensor memory, and eight warps read the other
-// one out.
+// into one of two accumulators in tensor memory, and eight warps (of a tile 256
+// columns wide sixteen) read the other one out.
 //
 // Shapes.  A product of sixteen k takes 128 cycles whatever the tile's rows (64, 128)
 // and columns (64 to 256) of a CTA alone, and 128 for 256 x 256 of a pair: narrow
@@ -11,23 +11,23 @@
 // cores' rate.
 //
 // Measured (GB300, device time; the tensor pipe's share of cycles from ncu):
-//   statistics 4096 x 4096 x 131072 bf16    2.18 ms  2015 TFLOP/s (cuBLAS burst 1901,
-//                                            sustained 1695); pipe 90 % active
-//   gradient and products 4096 x 4096 x 65536  3.32 to 3.41 ms  1988 TFLOP/s; 89, 95 %
-//   the same called back to back            2.20 to 2.51 and 3.53 to 3.88 ms: power
-//   32 x 1024 x 4096                        9.4 us forward, 64 tokens backward 16.7
-//   512 x 2048 x 16384 fp32                 171 us, 54 of them packing; pipe 75 %
+//   statistics 4096 x 4096 x 131072 bf16    2.14 to 2.45 ms  2050 to 1800 TFLOP/s (cuBLAS
+//                                            burst 1901, sustained 1695); pipe 89 % active
+//   gradient and products 4096 x 4096 x 65536  3.30 to 3.76 ms; pipe 88 and 94 %
+//   the same called back to back            2.16 to 2.59 and 3.67 to 3.99 ms: power
+//   the gradient in two terms               6.19 to 6.61 ms; pipe 73 and 86 %
+//   32 x 1024 x 4096                        9.5 us forward, 64 tokens backward 20.7
+//   512 x 2048 x 16384 fp32                 171 us, 55 of them packing; pipe 75 %
 // What bounds the others: up to some 256 tokens the weight's read (64 x 4096 x 131072
-// 180 us, 0.88 of the copy rate); short k the epilogue (2048 x 256 x 32768 43 us, some
-// 2 us a tile of 256 columns); small calls one tile's latency (k / 16 products of 128 cycles, then
-// its epilogue).
+// 180 us, 0.88 of the copy rate); short k the epilogue (2048 x 256 x 32768 43 to 51 us,
+// some 2 us a tile of 256 columns); small calls one tile's latency (k / 16 products of 128
+// cycles, then its epilogue).
 //
 // Precision.  The tensor cores add into an fp32 accumulator without rounding to
 // nearest: a sum over k drifts towards zero by some 2^-25 of itself an addition of
 // sixteen products, 7e-6 over 4096.  A product rounded to bf16 does not see that up to a
 // k of 131072 (2^-12 of the terms' magnitude), and longer ones are summed in parts of that
-// (kLongPart).
-// The logits do (one of 30 is off by 2e-4, and so is the gradient p - 1 of a token
+// (kLongPart).  The logits do (one of 30 is off by 2e-4, and so is the gradient p - 1 of a token
 // whose target is almost certain), and so do products of fp32 operands: there the
 // accumulator holds kPromote stages at a time, and the epilogue warps add these
 // parts in registers, which rounds to nearest; they do it while the next part is
