@@ -11,12 +11,12 @@
 // cores' rate.
 //
 // Measured (GB300, device time; the tensor pipe's share of cycles from ncu):
-//   statistics 4096 x 4096 x 131072 bf16    2.14 to 2.45 ms  2050 to 1800 TFLOP/s (cuBLAS
-//                                            burst 1901, sustained 1695); pipe 89 % active
-//   gradient and products 4096 x 4096 x 65536  3.30 to 3.76 ms; pipe 88 and 94 %
-//   the same called back to back            2.16 to 2.59 and 3.67 to 3.99 ms: power
-//   the gradient in two terms               6.19 to 6.61 ms; pipe 73 and 86 %
-//   32 x 1024 x 4096                        9.5 us forward, 64 tokens backward 20.7
+//   statistics 4096 x 4096 x 131072 bf16    2.23 to 2.42 ms  1970 to 1820 TFLOP/s (cuBLAS
+//                                            burst 1901, sustained 1695)
+//   gradient and products 4096 x 4096 x 65536  3.35 to 3.86 ms
+//   the same called back to back            2.37 to 2.50 and 3.71 to 3.89 ms: power
+//   the gradient in two terms               6.2 to 6.7 ms
+//   32 x 1024 x 4096                        9.8 us forward, 64 tokens backward 20.9
 //   512 x 2048 x 16384 fp32                 171 us, 55 of them packing; pipe 75 %
 // What bounds the others: up to some 256 tokens the weight's read (64 x 4096 x 131072
 // 180 us, 0.88 of the copy rate); short k the epilogue (2048 x 256 x 32768 43 to 51 us,
@@ -81,7 +81,10 @@ constexpr int kVocabRing = 6 * 32768;           // bytes of all stages
 constexpr int kVocabStages = 16;                // most of them
 constexpr int kTurnBytes = 32 * 64;             // a warp's room to turn its output around
 constexpr int kVocabSmem = kVocabRing + 16 * kTurnBytes + 1024;  // aligned to 1024 by hand
-constexpr int kPromote = 8;                     // stages of a part
+// Stages of a part that is summed in registers.  Of 8, 4 and 2 a loss is off by 2.3e-7,
+// 1.1e-7 and 0.7e-7 (plain fp32 products: 0.7e-7 to 2.4e-7), one of 4096 x 4096 x 131072
+// takes 2155, 2230 and 2325 us, the gradient of 1000 x 1024 x 50000 192, 205 and 212.
+constexpr int kPromote = 4;
 
 // A tile is 128 rows a CTA by N columns (CG = 2: a pair shares the columns'
 // operand, half of it each).

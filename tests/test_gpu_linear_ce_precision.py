@@ -257,3 +257,20 @@ def test_a_long_sum_of_one_sign_does_not_sink(precise):
                                                      need_dweight=need_w, precise=precise)
         want = dlse.double()[:, None] * w.double().sum(0)
         assert abs(bias(dh, want.bfloat16().double())) <= 2 * 2.0 ** -11
+
+
+@pytest.mark.parametrize("tokens", [4096, 20000])  # (few tiles: k is split)
+def test_a_logits_sum_sinks_no_more_than_its_parts_do(tokens):
+    # One word: lse is its logit, a sum of 4096 products in 1 to 4, multiples of 2^-14.  The
+    # accumulator holds 256 of k, below 1024, so 24 bits and exact; of more it would drop
+    # digits towards zero.  The sixteen parts are added to nearest, u of the sum each at most
+    # in either direction: 16 u / sqrt(3) / sqrt(4096) = 0.14 u on average over the tokens.
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    h = (1 + torch.randint(0, 128, (tokens, 4096), generator=g, device="cuda") / 128).bfloat16()
+    w = (1 + torch.randint(0, 128, (1, 4096), generator=g, device="cuda") / 128).bfloat16()
+    target = torch.zeros(tokens, dtype=torch.int64, device="cuda")
+    loss, lse = credit.linear_cross_entropy_forward(h, w, target)
+    assert bool((loss == 0).all())
+    want = torch.cat([h[i:i + 4096].double() @ w[0].double() for i in range(0, tokens, 4096)])
+    assert abs(bias(lse, want)) <= 0.5 * U
